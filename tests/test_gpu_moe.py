@@ -1,0 +1,230 @@
+"""GPU parity of the mixture-of-experts operators with the fp64 oracle (oracle/moe.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import tile_level_sync_gb300 as cs
+from oracle import moe as ref
+from moe_helpers import assert_within, f64, layer, mlp_inputs, run_mlp, run_mlp_grad
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ plan
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (3, 2, 2), (33, 7, 3), (500, 60, 8), (513, 1024, 8),
+                                   (2000, 5, 2), (2049, 37, 2), (9000, 256, 3), (70000, 33, 9)])
+@pytest.mark.parametrize("how", ["random", "one", "invalid"])
+def test_plan(T, E, k, how):
+    rng = np.random.default_rng(T + E + k)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    if how == "one":
+        ids[:] = E - 1
+    if how == "invalid":
+        ids[rng.random((T, k)) < 0.3] = -1
+        ids[rng.random((T, k)) < 0.1] = E + 3
+        ids[rng.random((T, k)) < 0.05] = -(1 << 31)
+    m = cs.Moe(cs.make_moe_desc(T=T, experts=E, top_k=min(k, E)) if k <= E else
+               cs.make_moe_desc(T=T * k, experts=E, top_k=1))
+    if k > E:
+        ids = ids.reshape(T * k, 1)
+    buf = torch.full((m.info.plan_bytes // 4 + 64,), 12345, dtype=torch.int32, device="cuda")
+    plan = buf[:-64]
+    m.plan(torch.from_numpy(ids).cuda(), plan)
+    want = ref.plan(ids, E)
+    for name, got in m.plan_views(plan).items():
+        assert np.array_equal(got.cpu().numpy(), want[name]), name
+    assert bool((buf[-64:] == 12345).all())
+    assert m.check(plan) == (cs.OK, 0)
+
+
+# ------------------------------------------------------------------ route
+
+ROUTES = [
+    dict(T=1, E=64, k=8, score="softmax", renorm=True),
+    dict(T=3, E=1, k=1, score="sigmoid"),
+    dict(T=77, E=60, k=4, score="softmax"),
+    dict(T=77, E=33, k=4, score="softmax", bias=True, renorm=True, scale=2.5),
+    dict(T=50, E=256, k=8, score="sigmoid", bias=True, groups=8, group_limit=4, group_top=2, renorm=True, scale=2.5),
+    dict(T=50, E=160, k=6, score="softmax", groups=8, group_limit=3, group_top=1, scale=16.0),
+    dict(T=40, E=96, k=6, score="softmax", groups=32, group_limit=5, group_top=2, bias=True),
+    dict(T=9, E=1024, k=32, score="sigmoid", renorm=True),
+    dict(T=9, E=1000, k=32, score="softmax", bias=True, groups=4, group_limit=1, group_top=2),
+    dict(T=20, E=8, k=8, score="softmax", renorm=True),
+    dict(T=20, E=8, k=4, score="sigmoid", groups=8, group_limit=4, group_top=2),
+]
+
+
+def _route_case(c, f32, mask, seed=0):
+    rng = np.random.default_rng(seed + c["T"] * 1000 + c["E"])
+    logits = torch.from_numpy(rng.normal(0, 1.5, (c["T"], c["E"])).astype(np.float32))
+    if mask == "some":
+        logits[torch.from_numpy(rng.random((c["T"], c["E"])) < 0.5)] = float("-inf")
+        logits[torch.from_numpy(rng.random((c["T"], c["E"])) < 0.05)] = float("nan")
+        logits[0] = float("-inf")
+    elif mask == "lowest":
+        logits[torch.from_numpy(rng.random((c["T"], c["E"])) < 0.9)] = torch.finfo(torch.bfloat16).min
+    elif mask == "equal":
+        logits[:] = logits[:, :1]
+    logits = logits if f32 else logits.to(torch.bfloat16)
+    bias = torch.from_numpy(rng.normal(0, 0.1, c["E"]).astype(np.float32)) if c.get("bias") else None
+    if mask == "equal" and bias is not None:
+        bias[:] = 0.25
+    return logits, bias
+
+
+def _layer(c, f32):
+    return cs.Moe(cs.make_moe_desc(T=c["T"], experts=c["E"], top_k=c["k"], score=c["score"], groups=c.get("groups", 1),
+                                   group_limit=c.get("group_limit", 0), group_top=c.get("group_top", 1),
+                                   renorm=c.get("renorm", False), scale=c.get("scale", 1.0), logits_f32=f32))
+
+
+def _oracle_route(c, logits, bias):
+    return ref.route(f64(logits), None if bias is None else f64(bias), c["k"], c["score"], c.get("groups", 1),
+                     c.get("group_limit", 0), c.get("group_top", 1), c.get("renorm", False), c.get("scale", 1.0))
+
+
+def _run_route(c, logits, bias, f32):
+    m = _layer(c, f32)
+    ids = torch.full((c["T"], c["k"]), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((c["T"], c["k"]), float("nan"), device="cuda")
+    m.route(logits.cuda(), None if bias is None else bias.cuda(), ids, w)
+    return ids.cpu().numpy(), f64(w)
+
+
+# An fp32 weight: the exponential (2 ulp), its argument's rounding (|l - max| <= 200 where the
+# weight is not negligible: below, 200 steps), sums of at most 1024 terms in 37 additions,
+# a division and a product: 2^-24 * (2 * 2 + 200 + 37 + 2) < 2^-16 of the value.
+ROUTE_TOL = 2.0 ** -16
+
+
+@pytest.mark.parametrize("c", ROUTES, ids=lambda c: f"T{c['T']}E{c['E']}k{c['k']}{c['score']}")
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("mask", ["none", "some", "lowest", "equal"])
+def test_route(c, f32, mask):
+    logits, bias = _route_case(c, f32, mask)
+    want_ids, want_w = _oracle_route(c, logits, bias)
+    ids, w = _run_route(c, logits, bias, f32)
+    assert np.array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want_w) <= ROUTE_TOL * np.abs(want_w) + 1e-37)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_near_ties(score, groups):
+    """Keys that differ in the tenth digit: biases that undo the scores' differences but for
+    1e-10, which 32-bit keys cannot see."""
+    T, E, k = 64, 64, 8
+    rng = np.random.default_rng(3)
+    bias = np.float32(rng.choice([0.5, 0.25, 0.125], E))
+    logits = np.zeros((T, E), np.float32)
+    for t in range(T):
+        # one value in an expert's logit, a neighbour 2^-24 away in relative terms
+        base = np.float32(rng.normal())
+        logits[t] = base * (1 + np.float32(2.0 ** -23) * rng.integers(0, 4, E)).astype(np.float32)
+    c = dict(T=T, E=E, k=k, score=score, bias=True, groups=groups, group_limit=min(2, groups), group_top=2)
+    want_ids, _ = _oracle_route(c, torch.from_numpy(logits), torch.from_numpy(bias))
+    ids, _ = _run_route(c, torch.from_numpy(logits), torch.from_numpy(bias), True)
+    assert np.array_equal(ids, want_ids)
+
+
+@pytest.mark.parametrize("c", [c for c in ROUTES if c["T"] > 1], ids=lambda c: f"T{c['T']}E{c['E']}k{c['k']}{c['score']}")
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("mask", ["none", "some"])
+def test_route_grad(c, f32, mask):
+    logits, bias = _route_case(c, f32, mask)
+    ids, _ = _oracle_route(c, logits, bias)
+    dw = np.random.default_rng(1).normal(size=ids.shape).astype(np.float32)
+    m = _layer(c, f32)
+    dl = torch.full_like(logits, 77).cuda()
+    m.route_grad(logits.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), dl)
+    renorm, scale = c.get("renorm", False), c.get("scale", 1.0)
+    want = ref.route_grad(f64(logits), ids, dw.astype(np.float64), c["score"], renorm, scale)
+    # the gradient is a difference of terms of size scale * |dw|_max * s / (1 or sum s)
+    size = scale * np.abs(dw).max(axis=1, keepdims=True)
+    s = ref.scores(f64(logits), c["score"])
+    if renorm:
+        total = np.where(ids >= 0, np.take_along_axis(s, np.maximum(ids, 0), 1), 0).sum(axis=1, keepdims=True)
+        s = np.divide(s, total, out=np.zeros_like(s), where=total > 0)
+    half = 0.0 if f32 else ref.BF16
+    assert np.all(np.abs(f64(dl) - want) <= 2 * ROUTE_TOL * size * s + half * np.abs(want) + 1e-37)
+
+
+def test_route_grad_against_differences():
+    c = dict(T=6, E=40, k=5, score="softmax")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            c = dict(T=6, E=40, k=5, score=score, renorm=renorm, scale=1.5)
+            logits, _ = _route_case(c, True, "none", seed=5)
+            ids, _ = _run_route(c, logits, None, True)
+            dw = np.random.default_rng(2).normal(size=ids.shape).astype(np.float32)
+            dl = torch.empty_like(logits, device="cuda")
+            _layer(c, True).route_grad(logits.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), dl)
+            l, h = f64(logits), 1e-5
+            for e in range(c["E"]):
+                up, down = l.copy(), l.copy()
+                up[:, e] += h
+                down[:, e] -= h
+                f = [(ref.route_weights(x, ids, score, renorm, 1.5) * dw).sum(axis=1) for x in (up, down)]
+                # central differences: h^2 times a third derivative below 10, and 1e-16 / h
+                assert np.all(np.abs(f64(dl)[:, e] - (f[0] - f[1]) / (2 * h)) <= 2e-5)
+
+
+# ------------------------------------------------------------------ mlp and its gradient
+
+MLPS = [
+    dict(T=1, E=8, k=2, D=64, N1=64),
+    dict(T=1, E=3, k=3, D=8, N1=8),
+    dict(T=4, E=16, k=8, D=264, N1=136),
+    dict(T=33, E=4, k=1, D=64, N1=64),
+    dict(T=40, E=4, k=2, D=72, N1=40),
+    dict(T=37, E=9, k=3, D=328, N1=200),
+    dict(T=300, E=5, k=2, D=200, N1=264),
+    dict(T=130, E=1, k=1, D=128, N1=128),
+    dict(T=700, E=3, k=1, D=136, N1=520),
+    dict(T=64, E=64, k=8, D=512, N1=256),
+]
+_name = lambda c: "T{T}E{E}k{k}D{D}N{N1}".format(**c)  # noqa: E731
+
+
+def _check_mlp(s, act, grad, **more):
+    host = {n: f64(v) for n, v in s.items()}
+    host["ids"] = s["ids"].numpy()
+    m = layer(s, act, **more)
+    if not grad:
+        Y, bound = ref.mlp(host["X"], host["W1t"], host["W2t"], host["ids"], host["weights"], act)
+        assert_within(run_mlp(m, s), Y, bound, "Y")
+        return
+    want = ref.mlp_grad(host["X"], host["W1t"], host["W2t"], host["ids"], host["weights"], host["dY"], act)
+    got = run_mlp_grad(m, s)
+    for name, (value, bound) in want.items():
+        assert_within(got[name], value, bound, name)
+
+
+@pytest.mark.parametrize("c", MLPS, ids=_name)
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_mlp(c, act, grad):
+    _check_mlp(mlp_inputs(act=act, seed=7, **c), act, grad)
+
+
+@pytest.mark.parametrize("T", [3, 90])
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("how", ["dropped", "twice", "none", "one"])
+def test_mlp_ids(T, act, grad, how):
+    """Assignments to no expert, the same expert twice, tokens without any, one expert for all."""
+    E, k = 6, 3
+    rng = np.random.default_rng(T)
+    ids = rng.integers(0, E - 1, (T, k)).astype(np.int32)  # the last expert gets none
+    if how == "dropped":
+        ids[rng.random((T, k)) < 0.4] = -1
+        ids[0], ids[-1, 0] = -1, E
+    elif how == "twice":
+        ids[:, 1] = ids[:, 0]
+    elif how == "none":
+        ids[:] = -1
+    else:
+        ids[:] = 2
+    _check_mlp(mlp_inputs(T, E, k, 96, 80, act, seed=1, ids=torch.from_numpy(ids)), act, grad)

@@ -1,4 +1,5 @@
-"""Python binding of the tile-level synchronisation library (include/cusync.h).
+"""Python binding of the tile-level synchronisation library (include/cusync.h,
+include/cusync_moe.h).
 
 Argument marshalling only: every function forwards to the C ABI function of the same
 name in the in-tree ``libcusync.so``; all computation runs in the library's CUDA
@@ -27,6 +28,10 @@ DEBUG_SKIP_POST = 1 << 8
 DEBUG_SKIP_INIT = 1 << 9
 DEBUG_SKIP_SPLIT = 1 << 10
 NOALLOC_MAX_SEMAPHORES = 16336
+# cusync_moe.h
+MOE_SOFTMAX, MOE_SIGMOID = range(2)
+MOE_GELU, MOE_SWIGLU = range(2)
+MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_MAX_GROUPS, MOE_MAX_ASSIGNMENTS, MOE_TILE_ROWS = 1024, 32, 32, 16777216, 128
 
 POLICY_NAMES = {"STREAM": POLICY_STREAM, "ROW": POLICY_ROW, "TILE": POLICY_TILE,
                 "STRIDED": POLICY_STRIDED_TILE, "SENTINEL": POLICY_SENTINEL, "AUTO": POLICY_AUTO}
@@ -83,7 +88,19 @@ class cusync_policy_prediction_t(ctypes.Structure):
     _fields_ = [("us", c_dbl * 5), ("best_sync", c_i32), ("best", c_i32), ("num_sms", c_i32)]
 
 
+class cusync_moe_desc_t(ctypes.Structure):
+    _fields_ = [("T", c_i64), ("D", c_i64), ("N1", c_i64), ("experts", c_i32), ("top_k", c_i32), ("act", c_i32),
+                ("score", c_i32), ("groups", c_i32), ("group_limit", c_i32), ("group_top", c_i32), ("renorm", c_i32),
+                ("scale", ctypes.c_float), ("logits_f32", c_i32), ("num_sms", c_i32), ("_pad0", c_i32)]
+
+
+class cusync_moe_info_t(ctypes.Structure):
+    _fields_ = [("plan_bytes", c_i64), ("work_bytes", c_i64), ("grad_work_bytes", c_i64), ("slots", c_i64),
+                ("counts", c_i64), ("offsets", c_i64), ("slot_of", c_i64), ("row_of", c_i64)]
+
+
 _VP = ctypes.c_void_p
+_MOE = ctypes.POINTER(cusync_moe_desc_t)
 _SIGNATURES = {
     "cusync_status_string": (ctypes.c_char_p, [c_i32]),
     "cusync_wave_stats": (c_i32, [c_i64, c_i64, c_i32, c_i32, ctypes.POINTER(cusync_wave_report_t)]),
@@ -118,6 +135,13 @@ _SIGNATURES = {
     "cusync_band_rows": (c_i32, [ctypes.POINTER(cusync_chain_desc_t), c_i32, ctypes.POINTER(c_i64),
                                  ctypes.POINTER(c_i64)]),
     "cusync_destroy_chain": (c_i32, [_VP]),
+    "cusync_moe_info": (c_i32, [_MOE, ctypes.POINTER(cusync_moe_info_t)]),
+    "cusync_moe_route": (c_i32, [_MOE] + [_VP] * 5),
+    "cusync_moe_route_grad": (c_i32, [_MOE] + [_VP] * 5),
+    "cusync_moe_plan": (c_i32, [_MOE] + [_VP] * 3),
+    "cusync_moe_mlp": (c_i32, [_MOE] + [_VP] * 8),
+    "cusync_moe_mlp_grad": (c_i32, [_MOE] + [_VP] * 12),
+    "cusync_moe_check": (c_i32, [_VP, _VP, ctypes.POINTER(c_u32)]),
 }
 
 _lib = None
@@ -399,3 +423,122 @@ class Chain:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- mixture of experts
+
+
+def make_moe_desc(T=0, D=0, N1=0, experts=0, top_k=0, act=MOE_SWIGLU, score=MOE_SOFTMAX, groups=0, group_limit=0,
+                  group_top=0, renorm=False, scale=1.0, logits_f32=True, num_sms=0):
+    """Descriptor of an expert layer (cusync_moe_desc_t); act and score also by name:
+    "gelu" / "swiglu", "softmax" / "sigmoid"."""
+    if isinstance(act, str):
+        act = {"gelu": MOE_GELU, "swiglu": MOE_SWIGLU}[act.lower()]
+    if isinstance(score, str):
+        score = {"softmax": MOE_SOFTMAX, "sigmoid": MOE_SIGMOID}[score.lower()]
+    return cusync_moe_desc_t(T=T, D=D, N1=N1, experts=experts, top_k=top_k, act=act, score=score, groups=groups,
+                             group_limit=group_limit, group_top=group_top, renorm=int(renorm), scale=scale,
+                             logits_f32=int(logits_f32), num_sms=num_sms)
+
+
+def cusync_moe_info(desc):
+    r = cusync_moe_info_t()
+    _check(load().cusync_moe_info(ctypes.byref(desc), ctypes.byref(r)), "cusync_moe_info")
+    return r
+
+
+class Moe:
+    """An expert layer of one descriptor: its calls, on tensors and buffers of the caller.
+
+    Torch tensors are checked for type, size, contiguity and device (the current one);
+    raw device addresses are passed on as they are.  ``plan`` takes an int32 buffer of
+    ``info.plan_bytes``, ``mlp`` and ``run`` a buffer of ``info.work_bytes``, ``mlp_grad``
+    one of ``info.grad_work_bytes``."""
+
+    def __init__(self, desc):
+        self.desc = desc
+        self.info = cusync_moe_info(desc)
+        self._d = ctypes.byref(desc)
+        self._lib = load()
+        d, gated = desc, 2 if desc.act == MOE_SWIGLU else 1
+        rows, logits = d.T * d.top_k, "float32" if d.logits_f32 else "bfloat16"
+        self._want = {
+            "logits": (logits, d.T * d.experts), "dlogits": (logits, d.T * d.experts), "bias": ("float32", d.experts),
+            "ids": ("int32", rows), "weights": ("float32", rows), "dweights": ("float32", rows),
+            "plan": (None, self.info.plan_bytes), "work": (None, self.info.work_bytes),
+            "grad_work": (None, self.info.grad_work_bytes),
+            "W1t": ("bfloat16", d.experts * gated * d.N1 * d.D), "W2t": ("bfloat16", d.experts * d.N1 * d.D),
+            "dW1t": ("bfloat16", d.experts * gated * d.N1 * d.D), "dW2t": ("bfloat16", d.experts * d.N1 * d.D),
+        }
+        for name in ("X", "Y", "dX", "dY"):
+            self._want[name] = ("bfloat16", d.T * d.D)
+
+    def _ptrs(self, **tensors):
+        """Device addresses of the named arguments, the tensors among them checked."""
+        import torch
+        out = []
+        for name, t in tensors.items():
+            if t is None or isinstance(t, int):
+                out.append(t)
+                continue
+            dtype, n = self._want[name]
+            if dtype is None:  # a buffer of bytes, in elements of any type
+                if t.numel() * t.element_size() < n:
+                    raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes: {n} are needed")
+            elif t.dtype is not getattr(torch, dtype):
+                raise ValueError(f"{name} is {t.dtype}: torch.{dtype} is needed")
+            elif t.numel() != n:
+                raise ValueError(f"{name} has {t.numel()} elements: {n} are needed")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} is not contiguous")
+            if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+                raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
+            out.append(t.data_ptr())
+        return out
+
+    def route(self, logits, bias, ids, weights, stream=None):
+        p = self._ptrs(logits=logits, bias=bias, ids=ids, weights=weights)
+        _check(self._lib.cusync_moe_route(self._d, *p, _stream(stream)), "cusync_moe_route")
+
+    def route_grad(self, logits, ids, dweights, dlogits, stream=None):
+        p = self._ptrs(logits=logits, ids=ids, dweights=dweights, dlogits=dlogits)
+        _check(self._lib.cusync_moe_route_grad(self._d, *p, _stream(stream)), "cusync_moe_route_grad")
+
+    def plan(self, ids, plan, stream=None):
+        p = self._ptrs(ids=ids, plan=plan)
+        _check(self._lib.cusync_moe_plan(self._d, *p, _stream(stream)), "cusync_moe_plan")
+
+    def plan_views(self, plan):
+        """The arrays of an int32 plan buffer: counts, offsets, slot_of and row_of."""
+        i, d = self.info, self.desc
+        return {"counts": plan[i.counts:i.counts + d.experts], "offsets": plan[i.offsets:i.offsets + d.experts + 1],
+                "slot_of": plan[i.slot_of:i.slot_of + d.T * d.top_k].view(d.T, d.top_k),
+                "row_of": plan[i.row_of:i.row_of + i.slots]}
+
+    def mlp(self, X, W1t, W2t, ids, weights, work, Y, stream=None):
+        p = self._ptrs(X=X, W1t=W1t, W2t=W2t, ids=ids, weights=weights, work=work, Y=Y)
+        _check(self._lib.cusync_moe_mlp(self._d, *p, _stream(stream)), "cusync_moe_mlp")
+
+    def mlp_grad(self, X, W1t, W2t, ids, weights, dY, work, dX, dW1t, dW2t, dweights, stream=None):
+        p = self._ptrs(X=X, W1t=W1t, W2t=W2t, ids=ids, weights=weights, dY=dY, grad_work=work, dX=dX, dW1t=dW1t,
+                       dW2t=dW2t, dweights=dweights)
+        _check(self._lib.cusync_moe_mlp_grad(self._d, *p, _stream(stream)), "cusync_moe_mlp_grad")
+
+    def run(self, X, logits, bias, W1t, W2t, ids, weights, work, Y, stream=None):
+        """The layer's forward pass: route, then mlp with what it chose."""
+        self.route(logits, bias, ids, weights, stream)
+        self.mlp(X, W1t, W2t, ids, weights, work, Y, stream)
+
+    def run_grad(self, X, logits, W1t, W2t, ids, weights, dY, work, dX, dW1t, dW2t, dweights, dlogits, stream=None):
+        """The layer's backward pass: mlp_grad, then the router's gradient from dweights.
+        dX lacks the part that flows through the logits: that is the caller's product."""
+        self.mlp_grad(X, W1t, W2t, ids, weights, dY, work, dX, dW1t, dW2t, dweights, stream)
+        self.route_grad(logits, ids, dweights, dlogits, stream)
+
+    def check(self, buffer, stream=None):
+        """(status, code) of the last call that used a plan or work buffer: OK or ERR_DEVICE."""
+        code = c_u32()
+        st = self._lib.cusync_moe_check(_ptr(buffer), _stream(stream), ctypes.byref(code))
+        if st not in (OK, ERR_DEVICE):
+            raise CusyncError(st, "cusync_moe_check")
+        return st, code.value

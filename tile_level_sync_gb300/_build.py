@@ -1,7 +1,8 @@
 """In-tree build of the CUDA library (libcusync.so) for sm_103a with nvcc.
 
-One translation unit, one -gencode; the shared object is written next to this file.
-Rebuilds when any source or the public header is newer than the library.
+One -gencode; the translation units are compiled side by side and linked into a shared
+object next to this file.  Rebuilds when any source or public header is newer than the
+library.
 """
 
 import os
@@ -14,15 +15,15 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libcusync.so")
 
-SOURCES = [os.path.join(CSRC, "cusync.cu")]
+SOURCES = [os.path.join(CSRC, "cusync.cu"), os.path.join(CSRC, "moe.cu")]
 DEPS = SOURCES + [
     os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".h", ".cuh"))
-] + [os.path.join(INCLUDE, "cusync.h")]
+] + [os.path.join(INCLUDE, f) for f in ("cusync.h", "cusync_moe.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC",
     "-I" + INCLUDE,
 ]
 
@@ -45,13 +46,24 @@ def build(force=False, verbose=False, extra_flags=()):
     """Compile libcusync.so if it is missing or stale; return its path."""
     if not force and not needs_build():
         return LIB_PATH
+    nvcc = _nvcc()
+    objs = [os.path.splitext(src)[0] + ".o" for src in SOURCES]
+    running = []
+    for src, obj in zip(SOURCES, objs):
+        cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-c", "-o", obj, src]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        running.append(subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
+    outputs = [(p.communicate()[0], p.returncode) for p in running]
     tmp = LIB_PATH + ".tmp"
-    cmd = [_nvcc(), *NVCC_FLAGS, *extra_flags, "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
+    if all(rc == 0 for _, rc in outputs):
+        cmd = [nvcc, *NVCC_FLAGS, "-shared", "-o", tmp, *objs]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        outputs.append((res.stdout + res.stderr, res.returncode))
+    if any(rc != 0 for _, rc in outputs):
+        raise RuntimeError("nvcc failed:\n" + "".join(text for text, _ in outputs))
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -1,0 +1,524 @@
+// Host side of include/cusync_moe.h: argument checks, buffer layouts, TMA descriptors and
+// kernel launches of the expert layer.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "../../include/cusync_moe.h"
+#include "moe_gemm.cuh"
+#include "moe_plan.cuh"
+#include "moe_route.cuh"
+#include "moe_small.cuh"
+
+using namespace cusync;
+using namespace cusync::moe;
+
+namespace {
+
+static_assert(kTileRows == CUSYNC_MOE_TILE_ROWS, "the plan's alignment");
+static_assert(CUSYNC_MOE_MAX_EXPERTS <= kPlanThreads, "the plan scans the experts in one step");
+
+constexpr int64_t kPlanChunk = 4096;   // assignments of a plan block
+constexpr int64_t kPlanBlocks = 128;   // plan blocks at most
+// Assignments up to which the MLP runs without tiles.
+constexpr int64_t kSmallAssignments = 32;
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
+bool aligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// What a descriptor means, its defaults filled in.
+struct Layer {
+  int64_t T, D, N1, A, S;
+  int32_t E, k, G, groups, group_limit, group_top;
+  int64_t chunk, blocks;                                          // plan
+  int64_t counts, offsets, tile_expert, slot_of, row_of, hist;    // plan, 32-bit words
+  int64_t plan_bytes;
+  int64_t h, rows, work_bytes;                                    // forward work, bytes
+  int64_t gh, gz, grows, gpart, grad_bytes;                       // gradient work, bytes
+  int32_t parts;
+};
+
+cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
+  if (!d) return CUSYNC_ERR_INVALID_ARG;
+  if (d->T < 0 || d->experts < 1 || d->top_k < 1 || d->groups < 0 || d->group_limit < 0 || d->num_sms < 0 ||
+      d->D < 0 || d->N1 < 0)
+    return CUSYNC_ERR_INVALID_ARG;
+  if ((d->act != CUSYNC_MOE_GELU && d->act != CUSYNC_MOE_SWIGLU) ||
+      (d->score != CUSYNC_MOE_SOFTMAX && d->score != CUSYNC_MOE_SIGMOID) || d->group_top < 0 || d->group_top > 2 ||
+      !std::isfinite(d->scale))
+    return CUSYNC_ERR_INVALID_ARG;
+  L->groups = d->groups ? d->groups : 1;
+  L->group_limit = d->group_limit ? d->group_limit : L->groups;
+  L->group_top = d->group_top ? d->group_top : 1;
+  if (d->experts > CUSYNC_MOE_MAX_EXPERTS || d->top_k > CUSYNC_MOE_MAX_TOP_K || L->groups > CUSYNC_MOE_MAX_GROUPS)
+    return CUSYNC_ERR_UNSUPPORTED;
+  if (d->experts % L->groups || L->group_limit > L->groups ||
+      d->top_k > L->group_limit * (d->experts / L->groups))
+    return CUSYNC_ERR_INVALID_ARG;
+  if (d->T > CUSYNC_MOE_MAX_ASSIGNMENTS / d->top_k) return CUSYNC_ERR_UNSUPPORTED;
+  if (mlp) {
+    if (d->D < 1 || d->N1 < 1) return CUSYNC_ERR_INVALID_ARG;
+    if (d->D % 8 || d->N1 % 8 || d->D > (1 << 20) || d->N1 > (1 << 20)) return CUSYNC_ERR_UNSUPPORTED;
+  }
+  L->T = d->T;
+  L->D = d->D;
+  L->N1 = d->N1;
+  L->E = d->experts;
+  L->k = d->top_k;
+  L->G = d->act == CUSYNC_MOE_SWIGLU ? 2 : 1;
+  L->A = L->T * L->k;
+  L->S = round_up(L->A + (kTileRows - 1) * std::min<int64_t>(L->E, L->A), kTileRows);
+  L->chunk = std::max(kPlanChunk, round_up(div_up(L->A, kPlanBlocks), kPlanThreads));
+  L->blocks = std::max<int64_t>(1, div_up(L->A, L->chunk));
+  int64_t w = PLAN_HEADER;
+  auto take = [&w](int64_t n) {
+    const int64_t at = w;
+    w += round_up(n, 4);
+    return at;
+  };
+  L->counts = take(L->E);
+  L->offsets = take(L->E + 1);
+  L->tile_expert = take(L->S / kTileRows);
+  L->slot_of = take(L->A);
+  L->row_of = take(L->S);
+  L->hist = take(L->blocks > 1 ? L->blocks * L->E : 0);
+  L->plan_bytes = round_up(w * 4, 256);
+  L->h = L->rows = L->work_bytes = L->gh = L->gz = L->grows = L->gpart = L->grad_bytes = 0;
+  L->parts = 0;
+  if (d->D >= 1 && d->N1 >= 1) {
+    int64_t b = L->plan_bytes;
+    auto bytes = [&b](int64_t n) {
+      const int64_t at = b;
+      b += round_up(n, 256);
+      return at;
+    };
+    L->h = bytes(L->S * L->N1 * 2);
+    L->rows = bytes(L->S * L->D * 4);
+    L->work_bytes = b;
+    b = L->plan_bytes;
+    L->parts = (int32_t)(2 * div_up(L->N1, 128));
+    L->gh = bytes(L->S * L->N1 * 2);
+    L->gz = bytes(L->S * L->G * L->N1 * 2);
+    L->grows = bytes(L->S * L->D * 4);
+    L->gpart = bytes(L->S * L->parts * 4);
+    L->grad_bytes = b;
+  }
+  return CUSYNC_OK;
+}
+
+// ----------------------------------------------------------------------------- devices
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::mutex g_mu;
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];  // SMs of a prepared device, 0 = not prepared
+
+template <int MODE, int ACT, int BN>
+cudaError_t prepare_gemm() {
+  const void* f = reinterpret_cast<const void*>(&moe_gemm_kernel<MODE, ACT, BN>);
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmCfg<MODE, ACT, BN>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;  // loads the kernel now, not at a launch inside a capture
+  return cudaFuncGetAttributes(&fa, f);
+}
+
+template <int ACT>
+cudaError_t prepare_act() {
+  cudaError_t e = prepare_gemm<FWD1, ACT, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 128>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 64>();
+  if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128>();
+  return e;
+}
+
+// The current device: its kernels' attributes set, the descriptor encoder found.  The first
+// call on a device does the work.
+cusync_status_t prepare_device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return CUSYNC_ERR_CUDA;
+  if (int n = g_sms[dev].load(std::memory_order_acquire)) {
+    *sms = n;
+    return CUSYNC_OK;
+  }
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return CUSYNC_ERR_CUDA;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  int n = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = prepare_act<0>();
+  if (e == cudaSuccess) e = prepare_act<1>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 128>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 64>();
+  if (e == cudaSuccess) e = prepare_gemm<DX, 0, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<DW1, 0, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<DW2, 0, 256>();
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)plan_smem(CUSYNC_MOE_MAX_EXPERTS));
+  if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
+  g_sms[dev].store(n, std::memory_order_release);
+  *sms = n;
+  return CUSYNC_OK;
+}
+
+// bf16 boxes of 64 elements x box_rows rows (x one matrix), 128-byte swizzle; elements
+// outside read as zero.
+bool map_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, uint32_t box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t one[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_3d(CUtensorMap* m, const void* p, int64_t depth, int64_t rows, int64_t cols, uint32_t box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(rows * cols) * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t one[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ----------------------------------------------------------------------------- launches
+
+// Every launch is a programmatic dependent of the kernel before it in the stream: it may be
+// set up while that one ends, and each kernel waits for that end before it touches memory.
+template <typename... P, typename... Q>
+cudaError_t launch(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, Q... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+template <typename L, int SCORE, bool GRAD>
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
+  const dim3 grid((unsigned)div_up(a.T, 8));
+  const int v = (int)div_up(a.E, 32);
+#define CUSYNC_ROUTE(V)                                                                     \
+  if (v <= V)                                                                               \
+    return GRAD ? launch(route_grad_kernel<L, V, SCORE>, grid, 256, 0, s, a)                \
+                : launch(route_kernel<L, V, SCORE>, grid, 256, 0, s, a);
+  CUSYNC_ROUTE(1)
+  CUSYNC_ROUTE(2)
+  CUSYNC_ROUTE(4)
+  CUSYNC_ROUTE(8)
+  CUSYNC_ROUTE(16)
+  CUSYNC_ROUTE(32)
+#undef CUSYNC_ROUTE
+  return cudaErrorInvalidValue;
+}
+
+template <bool GRAD>
+cusync_status_t route_any(const cusync_moe_desc_t* d, const Layer& L, RouteArgs a, cudaStream_t s) {
+  a.T = L.T;
+  a.E = L.E;
+  a.k = L.k;
+  a.groups = L.groups;
+  a.group_size = L.E / L.groups;
+  a.group_limit = L.group_limit;
+  a.group_top = L.group_top;
+  a.renorm = d->renorm ? 1 : 0;
+  a.scale = d->scale;
+  if (L.T == 0) return CUSYNC_OK;
+  const bool soft = d->score == CUSYNC_MOE_SOFTMAX;
+  const cudaError_t e =
+      d->logits_f32 ? (soft ? launch_route<float, 0, GRAD>(a, s) : launch_route<float, 1, GRAD>(a, s))
+                    : (soft ? launch_route<__nv_bfloat16, 0, GRAD>(a, s) : launch_route<__nv_bfloat16, 1, GRAD>(a, s));
+  return e == cudaSuccess ? CUSYNC_OK : CUSYNC_ERR_CUDA;
+}
+
+cudaError_t launch_plan(const Layer& L, const int32_t* ids, void* plan, cudaStream_t s) {
+  PlanArgs p = {};
+  p.ids = ids;
+  p.plan = static_cast<int32_t*>(plan);
+  p.A = L.A;
+  p.S = L.S;
+  p.E = L.E;
+  p.blocks = (int32_t)L.blocks;
+  p.chunk = L.chunk;
+  p.counts = L.counts;
+  p.offsets = L.offsets;
+  p.tile_expert = L.tile_expert;
+  p.slot_of = L.slot_of;
+  p.row_of = L.row_of;
+  p.hist = L.hist;
+  if (L.blocks > 1) {
+    const cudaError_t e = launch(plan_hist_kernel, dim3((unsigned)L.blocks), kPlanThreads, (size_t)L.E * 4, s, p);
+    if (e != cudaSuccess) return e;
+  }
+  return launch(plan_kernel, dim3((unsigned)L.blocks), kPlanThreads, plan_smem(L.E), s, p);
+}
+
+GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
+  GemmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.plan = static_cast<int32_t*>(work);
+  a.weights = weights;
+  a.counts = L.counts;
+  a.offsets = L.offsets;
+  a.tile_expert = L.tile_expert;
+  a.row_of = L.row_of;
+  a.T = (int32_t)L.T;
+  a.k = L.k;
+  a.E = L.E;
+  return a;
+}
+
+template <int MODE, int ACT, int BN>
+cudaError_t launch_gemm(GemmArgs a, int64_t row_tiles, int sms, cudaStream_t s) {
+  using C = GemmCfg<MODE, ACT, BN>;
+  a.col_tiles = (int32_t)div_up(a.N, C::kOutCols);
+  a.m_tiles = (int32_t)div_up(a.M, 128);
+  const int64_t tiles = C::kDw ? (int64_t)a.E * a.m_tiles * a.col_tiles : row_tiles * a.col_tiles;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms));
+  return launch(moe_gemm_kernel<MODE, ACT, BN>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
+}
+
+// Tile width of a forward product: the widest whose tiles fill the SMs twice over, counting
+// one row tile for every expert that can be active and one for every 128 assignments.
+int tile_width(int64_t row_tiles, int64_t cols256, int sms) {
+  if (row_tiles * cols256 >= 2 * sms) return 256;
+  if (row_tiles * cols256 * 2 >= 2 * sms) return 128;
+  return 64;
+}
+
+template <int MODE, int ACT>
+cudaError_t launch_fwd(const GemmArgs& a, int bn, int64_t row_tiles, int sms, cudaStream_t s) {
+  if (bn == 256) return launch_gemm<MODE, ACT, 256>(a, row_tiles, sms, s);
+  if (bn == 128) return launch_gemm<MODE, ACT, 128>(a, row_tiles, sms, s);
+  return launch_gemm<MODE, ACT, 64>(a, row_tiles, sms, s);
+}
+
+cudaError_t launch_combine(const Layer& L, void* work, const float* rows, const float* weights, void* out,
+                           const float* part, float* dweights, cudaStream_t s) {
+  CombineArgs c = {};
+  c.plan = static_cast<int32_t*>(work);
+  c.rows = rows;
+  c.weights = weights;
+  c.out = out;
+  c.part = part;
+  c.dweights = dweights;
+  c.slot_of = L.slot_of;
+  c.T = (int32_t)L.T;
+  c.k = L.k;
+  c.D = (int32_t)L.D;
+  c.parts = L.parts;
+  return launch(combine_kernel, dim3((unsigned)L.T, (unsigned)div_up(L.D, 4 * kCombineThreads)), kCombineThreads, 0, s,
+                c);
+}
+
+cusync_status_t status_of(cudaError_t e) { return e == cudaSuccess ? CUSYNC_OK : CUSYNC_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+cusync_status_t cusync_moe_info(const cusync_moe_desc_t* d, cusync_moe_info_t* out) {
+  Layer L;
+  if (!out) return CUSYNC_ERR_INVALID_ARG;
+  const bool mlp = d && (d->D != 0 || d->N1 != 0);
+  const cusync_status_t st = read_desc(d, &L, mlp);
+  if (st != CUSYNC_OK) return st;
+  out->plan_bytes = L.plan_bytes;
+  out->work_bytes = L.work_bytes;
+  out->grad_work_bytes = L.grad_bytes;
+  out->slots = L.S;
+  out->counts = L.counts;
+  out->offsets = L.offsets;
+  out->slot_of = L.slot_of;
+  out->row_of = L.row_of;
+  return CUSYNC_OK;
+}
+
+cusync_status_t cusync_moe_route(const cusync_moe_desc_t* d, const void* logits, const float* bias, int32_t* ids,
+                                 float* weights, cusync_stream_t stream) {
+  Layer L;
+  const cusync_status_t st = read_desc(d, &L, false);
+  if (st != CUSYNC_OK) return st;
+  if (L.T && (!aligned(logits) || !aligned(ids) || !aligned(weights) || (bias && !aligned(bias))))
+    return CUSYNC_ERR_INVALID_ARG;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.ids = ids;
+  a.weights = weights;
+  return route_any<false>(d, L, a, (cudaStream_t)stream);
+}
+
+cusync_status_t cusync_moe_route_grad(const cusync_moe_desc_t* d, const void* logits, const int32_t* ids,
+                                      const float* dweights, void* dlogits, cusync_stream_t stream) {
+  Layer L;
+  const cusync_status_t st = read_desc(d, &L, false);
+  if (st != CUSYNC_OK) return st;
+  if (L.T && (!aligned(logits) || !aligned(ids) || !aligned(dweights) || !aligned(dlogits)))
+    return CUSYNC_ERR_INVALID_ARG;
+  RouteArgs a = {};
+  a.logits = logits;
+  a.ids = const_cast<int32_t*>(ids);
+  a.weights = const_cast<float*>(dweights);
+  a.dlogits = dlogits;
+  return route_any<true>(d, L, a, (cudaStream_t)stream);
+}
+
+cusync_status_t cusync_moe_plan(const cusync_moe_desc_t* d, const int32_t* ids, void* plan, cusync_stream_t stream) {
+  Layer L;
+  cusync_status_t st = read_desc(d, &L, false);
+  if (st != CUSYNC_OK) return st;
+  if ((L.A && !aligned(ids)) || !aligned(plan)) return CUSYNC_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = prepare_device(&sms)) != CUSYNC_OK) return st;
+  return status_of(launch_plan(L, ids, plan, (cudaStream_t)stream));
+}
+
+cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const void* W1t, const void* W2t,
+                               const int32_t* ids, const float* weights, void* work, void* Y,
+                               cusync_stream_t stream) {
+  Layer L;
+  cusync_status_t st = read_desc(d, &L, true);
+  if (st != CUSYNC_OK) return st;
+  if (L.T == 0) return CUSYNC_OK;
+  if (!aligned(X) || !aligned(W1t) || !aligned(W2t) || !aligned(ids) || !aligned(weights) || !aligned(work) ||
+      !aligned(Y))
+    return CUSYNC_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = prepare_device(&sms)) != CUSYNC_OK) return st;
+  if (d->num_sms) sms = std::min(sms, d->num_sms);
+  cudaStream_t s = (cudaStream_t)stream;
+  char* w = static_cast<char*>(work);
+  if (L.A <= kSmallAssignments) {
+    SmallArgs a = {};
+    a.X = static_cast<const uint16_t*>(X);
+    a.W1t = static_cast<const uint16_t*>(W1t);
+    a.W2t = static_cast<const uint16_t*>(W2t);
+    a.ids = ids;
+    a.weights = weights;
+    a.h = reinterpret_cast<float*>(w + L.h);
+    a.Y = static_cast<uint16_t*>(Y);
+    a.err = static_cast<int32_t*>(work);
+    a.T = (int32_t)L.T;
+    a.k = L.k;
+    a.E = L.E;
+    a.D = (int32_t)L.D;
+    a.N1 = (int32_t)L.N1;
+    const dim3 up((unsigned)div_up(L.A * L.N1, kSmallThreads / 32)), down((unsigned)div_up(L.T * L.D, kSmallThreads / 32));
+    cudaError_t e = L.G == 2 ? launch(small_up_kernel<1>, up, kSmallThreads, 0, s, a)
+                             : launch(small_up_kernel<0>, up, kSmallThreads, 0, s, a);
+    if (e == cudaSuccess) e = launch(small_down_kernel, down, kSmallThreads, 0, s, a);
+    return status_of(e);
+  }
+  cudaError_t e = launch_plan(L, ids, work, s);
+  if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
+  const int64_t row_tiles = std::min<int64_t>(L.S / kTileRows, std::min<int64_t>(L.E, L.A) + L.A / kTileRows);
+  const int bn1 = tile_width(row_tiles, div_up(L.N1, 256 / L.G), sms), bn2 = tile_width(row_tiles, div_up(L.D, 256), sms);
+  GemmArgs a = gemm_args(L, work, weights);
+  a.N = (int32_t)L.N1;
+  a.K = (int32_t)L.D;
+  a.out = w + L.h;
+  GemmArgs b = gemm_args(L, work, weights);
+  b.N = (int32_t)L.D;
+  b.K = (int32_t)L.N1;
+  b.out = w + L.rows;
+  if (!map_2d(&a.mA, X, L.T, L.D, 1) || !map_3d(&a.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, bn1 / L.G) ||
+      !map_2d(&b.mA, w + L.h, L.S, L.N1, 32) || !map_3d(&b.mB, W2t, L.E, L.D, L.N1, bn2))
+    return CUSYNC_ERR_CUDA;
+  e = L.G == 2 ? launch_fwd<FWD1, 1>(a, bn1, row_tiles, sms, s) : launch_fwd<FWD1, 0>(a, bn1, row_tiles, sms, s);
+  if (e == cudaSuccess) e = launch_fwd<FWD2, 0>(b, bn2, row_tiles, sms, s);
+  if (e == cudaSuccess)
+    e = launch_combine(L, work, reinterpret_cast<float*>(w + L.rows), weights, Y, nullptr, nullptr, s);
+  return status_of(e);
+}
+
+cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, const void* W1t, const void* W2t,
+                                    const int32_t* ids, const float* weights, const void* dY, void* work, void* dX,
+                                    void* dW1t, void* dW2t, float* dweights, cusync_stream_t stream) {
+  Layer L;
+  cusync_status_t st = read_desc(d, &L, true);
+  if (st != CUSYNC_OK) return st;
+  if (!aligned(dW1t) || !aligned(dW2t)) return CUSYNC_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (L.T == 0) {  // no token: every weight gradient is zero
+    cudaError_t e = cudaMemsetAsync(dW1t, 0, (size_t)L.E * L.G * L.N1 * L.D * 2, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dW2t, 0, (size_t)L.E * L.N1 * L.D * 2, s);
+    return status_of(e);
+  }
+  if (!aligned(X) || !aligned(W1t) || !aligned(W2t) || !aligned(ids) || !aligned(weights) || !aligned(dY) ||
+      !aligned(work) || !aligned(dX) || !aligned(dweights))
+    return CUSYNC_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = prepare_device(&sms)) != CUSYNC_OK) return st;
+  if (d->num_sms) sms = std::min(sms, d->num_sms);
+  char* w = static_cast<char*>(work);
+  const int64_t H = L.G * L.N1, row_tiles = L.S / kTileRows;
+  void *gh = w + L.gh, *gz = w + L.gz;
+  float *rows = reinterpret_cast<float*>(w + L.grows), *part = reinterpret_cast<float*>(w + L.gpart);
+
+  GemmArgs p = gemm_args(L, work, weights);  // hidden layer and its gradient
+  p.N = (int32_t)L.N1;
+  p.K = (int32_t)L.D;
+  p.out = gz;
+  p.out2 = gh;
+  p.part = part;
+  GemmArgs x = gemm_args(L, work, weights);  // dX per slot
+  x.N = (int32_t)L.D;
+  x.K = (int32_t)H;
+  x.out = rows;
+  GemmArgs w1 = gemm_args(L, work, weights);
+  w1.M = (int32_t)H;
+  w1.N = (int32_t)L.D;
+  w1.out = dW1t;
+  GemmArgs w2 = gemm_args(L, work, weights);
+  w2.M = (int32_t)L.D;
+  w2.N = (int32_t)L.N1;
+  w2.out = dW2t;
+  if (!map_2d(&p.mA, X, L.T, L.D, 1) || !map_2d(&p.mA2, dY, L.T, L.D, 1) ||
+      !map_3d(&p.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, 128) || !map_3d(&p.mB2, W2t, L.E, L.D, L.N1, 64) ||
+      !map_2d(&x.mA, gz, L.S, H, 32) || !map_3d(&x.mB, W1t, L.E, H, L.D, 64) ||
+      !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB, X, L.T, L.D, 1) ||
+      !map_2d(&w2.mA, dY, L.T, L.D, 1) || !map_2d(&w2.mB, gh, L.S, L.N1, 64))
+    return CUSYNC_ERR_CUDA;
+  cudaError_t e = launch_plan(L, ids, work, s);
+  if (e == cudaSuccess)
+    e = L.G == 2 ? launch_gemm<BWD1, 1, 256>(p, row_tiles, sms, s) : launch_gemm<BWD1, 0, 128>(p, row_tiles, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DX, 0, 256>(x, row_tiles, sms, s);
+  if (e == cudaSuccess) e = launch_combine(L, work, rows, nullptr, dX, part, dweights, s);
+  if (e == cudaSuccess) e = launch_gemm<DW1, 0, 256>(w1, row_tiles, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DW2, 0, 256>(w2, row_tiles, sms, s);
+  return status_of(e);
+}
+
+cusync_status_t cusync_moe_check(const void* buffer, cusync_stream_t stream, uint32_t* code) {
+  if (!aligned(buffer)) return CUSYNC_ERR_INVALID_ARG;
+  uint32_t err = 0;
+  cudaError_t e = cudaMemcpyAsync(&err, buffer, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
+  if (code) *code = err;
+  return err ? CUSYNC_ERR_DEVICE : CUSYNC_OK;
+}
+
+}  // extern "C"

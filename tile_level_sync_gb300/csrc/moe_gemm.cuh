@@ -1,0 +1,486 @@
+// The products of an expert layer: one persistent tcgen05 kernel per product.
+//
+// A tile is 128 rows of one expert (the plan aligns an expert's rows to 128) x BN columns,
+// or, for a weight gradient, 128 x BN of one expert's matrix.  One CTA per SM walks its
+// tiles with a fixed stride:
+//   warp 0     copies: TMA boxes of the weights and of the slot-ordered intermediates;
+//              rows of X and dY are fetched through the plan's row indices four at a time
+//              (tile::gather4), so the tokens are never copied into expert order.
+//   warp 1     TMEM owner; lane 0 issues tcgen05.mma (128 x BN x 16, fp32 accumulators).
+//   warps 2-9  epilogue: two warps per TMEM lane quarter, a thread per row.
+// Accumulators are double-buffered where two fit in TMEM's 512 columns.
+//
+//   mode   rows x columns          A            B                       epilogue
+//   FWD1   slots x N1              X (gather)   W1t[e]                  h = act(z), bf16
+//   FWD2   slots x D               H            W2t[e]                  O, fp32
+//   BWD1   slots x N1              X, dY        W1t[e]; W2t[e] along N  z and dH = dY W2 side by
+//                                                                       side: dZ and w h (bf16),
+//                                                                       partial sums of dH h
+//   DX     slots x D               dZ           W1t[e] along N          dX per slot, fp32
+//   DW1    G*N1 x D (per expert)   dZ along M   X (gather) along N      bf16
+//   DW2    D x N1 (per expert)     dY (gather)  w H along N             bf16
+//
+// "along M/N": the operand is stored with that index contiguous rather than K, and the MMA
+// reads it that way (instruction and shared-memory descriptors), so no operand is ever
+// transposed in memory.
+//
+// A row behind an expert's last one gets no store in the forward pass; its accumulator
+// rows hold whatever the ring held, and rows do not mix.  In the weight gradients K runs
+// over slots: there the gather reads zeros for such rows (an index outside the tensor) and
+// BWD1 stored zeros, so they add nothing.
+//
+// Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "moe_plan.cuh"
+#include "ptx.cuh"
+
+namespace cusync {
+namespace moe {
+
+enum : int { FWD1 = 0, FWD2 = 1, BWD1 = 2, DX = 3, DW1 = 4, DW2 = 5 };
+
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr int kGemmThreads = 320;
+constexpr uint32_t kErrWait = 3u << 24;  // the pipeline-wait class of the chain kernel's error words
+
+struct GemmArgs {
+  CUtensorMap mA;    // X, H, dZ or dY
+  CUtensorMap mA2;   // BWD1: dY
+  CUtensorMap mB;    // W1t, W2t, X or w H
+  CUtensorMap mB2;   // BWD1: W2t
+  int32_t* plan;
+  const float* weights;
+  void* out;         // H, O, dZ, dX per slot, dW1t or dW2t
+  void* out2;        // BWD1: w H
+  float* part;       // BWD1: partial sums of dH h, [slot][2 * column tiles]
+  int64_t counts, offsets, tile_expert, row_of;
+  int32_t T, k, E;
+  int32_t M;         // DW: rows of an expert's matrix
+  int32_t N;         // output columns (FWD1, BWD1: N1)
+  int32_t K;         // reduction length (DW: the expert's rows)
+  int32_t col_tiles, m_tiles;
+};
+
+template <int MODE, int ACT, int BN>
+struct GemmCfg {
+  static constexpr bool kDw = MODE == DW1 || MODE == DW2;
+  static constexpr bool kBwd1 = MODE == BWD1;
+  static constexpr bool kGatherA = MODE == FWD1 || MODE == BWD1 || MODE == DW2;
+  static constexpr bool kGatherB = MODE == DW1;
+  static constexpr bool kPairB = ACT == 1 && (MODE == FWD1 || MODE == BWD1);  // gate and up columns in one tile
+  static constexpr bool kMnA = kDw;
+  static constexpr bool kMnB = kDw || MODE == DX;
+  static constexpr int kOutCols = kPairB ? BN / 2 : BN;  // output columns of a tile
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = BN * 128;
+  static constexpr int kD2 = kBwd1 ? kOutCols : 0;       // columns of BWD1's second accumulator
+  static constexpr int kStageBytes = kABytes + kBBytes + (kBwd1 ? kABytes + kD2 * 128 : 0);
+  static constexpr int kRing = 208 * 1024;
+  static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
+  static constexpr int kAccCols = BN + kD2;
+  static constexpr int kAccs = 2 * kAccCols <= 512 ? 2 : 1;
+  static constexpr int kTmemCols = kAccs * kAccCols <= 128 ? 128 : kAccs * kAccCols <= 256 ? 256 : 512;
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// 1 / (1 + e^-x); the fast exponential and division are within a few 1e-7 of it
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+// The factor of z in GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3))
+__device__ __forceinline__ float gelu_gate(float z) {
+  return sigmoid_fast(2.0f * kGeluC * (z + 0.044715f * z * z * z));
+}
+
+// The tile t of a launch.
+struct Tile {
+  int32_t e, slot0, rows, m0, n0, nkb;
+};
+
+template <int MODE, int ACT, int BN>
+__device__ __forceinline__ int32_t tile_total(const GemmArgs& a) {
+  if (GemmCfg<MODE, ACT, BN>::kDw) return a.E * a.m_tiles * a.col_tiles;
+  return a.plan[PLAN_TILES] * a.col_tiles;
+}
+
+template <int MODE, int ACT, int BN>
+__device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
+  using C = GemmCfg<MODE, ACT, BN>;
+  Tile r;
+  if (C::kDw) {
+    const int32_t per = a.m_tiles * a.col_tiles;
+    r.e = t / per;
+    const int32_t q = t - r.e * per;
+    r.m0 = (q % a.m_tiles) * 128;
+    r.n0 = (q / a.m_tiles) * BN;
+    r.slot0 = a.plan[a.offsets + r.e];
+    r.rows = a.plan[a.counts + r.e];
+    r.nkb = (r.rows + 63) / 64;
+  } else {
+    const int32_t rt = t / a.col_tiles;
+    r.e = a.plan[a.tile_expert + rt];
+    r.m0 = 0;
+    r.n0 = (t - rt * a.col_tiles) * C::kOutCols;
+    r.slot0 = rt * kTileRows;
+    r.rows = min(kTileRows, a.plan[a.offsets + r.e] + a.plan[a.counts + r.e] - r.slot0);
+    r.nkb = (a.K + 63) / 64;
+  }
+  return r;
+}
+
+template <int MODE, int ACT, int BN>
+__global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_constant__ GemmArgs a) {
+  using C = GemmCfg<MODE, ACT, BN>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int32_t abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&tfull[i], 1);
+      ptx::mbar_init(&tempty[i], 8);
+    }
+    ptx::mbar_init(&drain, 1);
+    ptx::mbar_init_fence();
+    abort_flag = 0;
+    ptx::prefetch_tmap(&a.mA);
+    ptx::prefetch_tmap(&a.mB);
+    if (C::kBwd1) {
+      ptx::prefetch_tmap(&a.mA2);
+      ptx::prefetch_tmap(&a.mB2);
+    }
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&tmem_slot, C::kTmemCols);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int32_t total = tile_total<MODE, ACT, BN>(a);
+  const int32_t step = gridDim.x;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    const uint64_t keep = ptx::l2_policy_evict_last(), stream = ptx::l2_policy_evict_normal();
+    uint32_t it = 0;
+    for (int32_t t = blockIdx.x; t < total && !abort_flag; t += step) {
+      const Tile q = tile_at<MODE, ACT, BN>(a, t);
+      // a lane's four gathered rows, as token indices: of the tile (FWD1, BWD1) or of one
+      // k-block; -1 (a slot behind the last row) becomes T, outside the tensor, read as zero
+      const int gl = C::kDw ? (lane & 15) : lane;  // DW: 16 lanes cover a k-block's 64 rows
+      auto tokens = [&](int32_t r0) {
+        int4 r = make_int4(-1, -1, -1, -1);
+        if (r0 + 4 * gl < q.rows) r = *reinterpret_cast<const int4*>(a.plan + a.row_of + q.slot0 + r0 + 4 * gl);
+        return r;
+      };
+      auto token = [&](int32_t r) { return r < 0 ? a.T : r / a.k; };
+      int4 next = make_int4(-1, -1, -1, -1), tok = next;
+      if (C::kGatherA || C::kGatherB) next = tokens(0);
+      if (!C::kDw) tok = make_int4(token(next.x), token(next.y), token(next.z), token(next.w));
+      const int live = (q.rows + 3) / 4;           // lanes whose rows a tile of slots needs
+      const int boxes = (q.rows + 31) / 32;        // 32-row boxes of a slot-ordered A
+      bool ok = true;
+      for (int kb = 0; kb < q.nkb; ++kb, ++it) {
+        const uint32_t st = it % C::kStages, par = ((it / C::kStages) & 1) ^ 1;
+        if (C::kDw) {
+          tok = make_int4(token(next.x), token(next.y), token(next.z), token(next.w));
+          next = tokens(kb * 64 + 64);
+        }
+        ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs) && !abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint8_t* sA = ring + st * C::kStageBytes;
+        uint8_t* sB = sA + C::kABytes;
+        uint8_t* sA2 = sB + C::kBBytes;
+        uint8_t* sB2 = sA2 + C::kABytes;
+        uint64_t* bar = &full[st];
+        if (lane == 0) {
+          uint32_t bytes = C::kBBytes;
+          if (C::kDw) bytes += C::kABytes;
+          else if (C::kGatherA) bytes += live * 512;
+          else bytes += boxes * 4096;
+          if (C::kBwd1) bytes += live * 512 + C::kD2 * 128;
+          ptx::mbar_arrive_expect_tx(bar, bytes);
+        }
+        __syncwarp();
+        const int32_t kc = kb * 64;
+        if (MODE == FWD1 || MODE == BWD1) {
+          if (lane < live) {
+            ptx::tma_gather4(sA + lane * 512, &a.mA, bar, kc, tok, keep);
+            if (C::kBwd1) ptx::tma_gather4(sA2 + lane * 512, &a.mA2, bar, kc, tok, keep);
+          }
+          if (lane == 0) {
+            if (C::kPairB) {
+              ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, 2 * q.e, stream);
+              ptx::tma_load_3d(sB + C::kBBytes / 2, &a.mB, bar, kc, q.n0, 2 * q.e + 1, stream);
+            } else {
+              ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, q.e, stream);
+            }
+            if (C::kBwd1)
+#pragma unroll
+              for (int c = 0; c < C::kD2 / 64; ++c)
+                ptx::tma_load_3d(sB2 + c * 8192, &a.mB2, bar, q.n0 + 64 * c, kc, q.e, stream);
+          }
+        } else if (MODE == FWD2 || MODE == DX) {
+          if (lane < boxes) ptx::tma_load_2d(sA + lane * 4096, &a.mA, bar, kc, q.slot0 + 32 * lane, keep);
+          if (MODE == FWD2) {
+            if (lane == 0) ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, q.e, stream);
+          } else if (lane < BN / 64) {
+            ptx::tma_load_3d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, kc, q.e, stream);
+          }
+        } else if (MODE == DW1) {
+          if (lane < 2) ptx::tma_load_2d(sA + lane * 8192, &a.mA, bar, q.m0 + 64 * lane, q.slot0 + kc, keep);
+#pragma unroll
+          for (int c = 0; c < BN / 128; ++c) {
+            const int ch = 2 * c + (lane >> 4);
+            ptx::tma_gather4(sB + ch * 8192 + gl * 512, &a.mB, bar, q.n0 + 64 * ch, tok, keep);
+          }
+        } else {
+          const int ch = lane >> 4;
+          ptx::tma_gather4(sA + ch * 8192 + gl * 512, &a.mA, bar, q.m0 + 64 * ch, tok, keep);
+          if (lane < BN / 64)
+            ptx::tma_load_2d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, q.slot0 + kc, keep);
+        }
+      }
+      if (!ok) {
+        if (lane == 0) {
+          abort_flag = 1;
+          a.plan[PLAN_ERR] = (int32_t)kErrWait;
+        }
+        break;
+      }
+    }
+    __syncwarp();
+    // after an abort: wait, bounded, for the copies still in flight
+    if (abort_flag && lane == 0)
+      for (uint32_t i = it > (uint32_t)C::kStages ? it - C::kStages : 0; i < it; ++i)
+        ptx::mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t majors = (C::kMnA ? ptx::kIdescAMn : 0) | (C::kMnB ? ptx::kIdescBMn : 0);
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, BN) | majors;
+      constexpr uint32_t idesc2 = ptx::idesc_bf16_f32(128, C::kBwd1 ? C::kD2 : BN) | ptx::kIdescBMn;
+      uint32_t it = 0, acc = 0;
+      bool ok = true;
+      for (int32_t t = blockIdx.x; t < total && ok && !abort_flag; t += step) {
+        const Tile q = tile_at<MODE, ACT, BN>(a, t);
+        if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
+        ++acc;
+        ok = ptx::mbar_wait_bounded(&tempty[buf], (use & 1) ^ 1, kWaitNs) && !abort_flag;
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + buf * C::kAccCols;
+        for (int kb = 0; kb < q.nkb; ++kb, ++it) {
+          const uint32_t st = it % C::kStages;
+          ok = ptx::mbar_wait_bounded(&full[st], (it / C::kStages) & 1, kWaitNs) && !abort_flag;
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t sA = ptx::smem_u32(ring + st * C::kStageBytes);
+          const uint32_t sB = sA + C::kABytes, sA2 = sB + C::kBBytes, sB2 = sA2 + C::kABytes;
+          // 16 k: 32 bytes of a K-contiguous row, or 16 rows of 128 bytes
+          constexpr uint64_t stepA = C::kMnA ? 2048 >> 4 : 32 >> 4, stepB = C::kMnB ? 2048 >> 4 : 32 >> 4;
+          const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
+          const uint64_t dB = C::kMnB ? ptx::smem_desc_mn128(sB) : ptx::smem_desc_k128(sB);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) ptx::umma_bf16(d, dA + s * stepA, dB + s * stepB, idesc, kb || s);
+          if (C::kBwd1) {
+            const uint64_t dA2 = ptx::smem_desc_k128(sA2), dB2 = ptx::smem_desc_mn128(sB2);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              ptx::umma_bf16(d + BN, dA2 + s * (32 >> 4), dB2 + s * (2048 >> 4), idesc2, kb || s);
+          }
+          ptx::umma_commit(&empty[st]);
+        }
+        if (!ok) break;
+        ptx::umma_commit(&tfull[buf]);
+      }
+      if (!ok || abort_flag) {
+        abort_flag = 1;
+        a.plan[PLAN_ERR] = (int32_t)kErrWait;
+        ptx::umma_commit(&drain);  // MMAs still in flight
+        ptx::mbar_wait_bounded(&drain, 0, kWaitNs);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint32_t acc = 0;
+    for (int32_t t = blockIdx.x; t < total; t += step) {
+      const Tile q = tile_at<MODE, ACT, BN>(a, t);
+      const bool empty_tile = q.nkb == 0;
+      const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
+      if (!empty_tile) {
+        ++acc;
+        const bool ok = ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag;
+        if (!__all_sync(0xffffffffu, ok)) {
+          abort_flag = 1;
+          if (lane == 0) a.plan[PLAN_ERR] = (int32_t)kErrWait;
+          break;
+        }
+        ptx::tc_fence_after();
+      }
+      const uint32_t d = tmem + buf * C::kAccCols + lanes;
+      const int64_t slot = (int64_t)q.slot0 + row;
+      const bool live = row < q.rows;
+      if (MODE == FWD1) {
+#pragma unroll 1
+        for (int c = half * 32; c < C::kOutCols; c += 64) {
+          uint32_t z[32], u[32];
+          ptx::tmem_ld_32x32b_x32(d + c, z);
+          if (C::kPairB) ptx::tmem_ld_32x32b_x32(d + C::kOutCols + c, u);
+          ptx::tmem_ld_wait();
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + slot * a.N + q.n0 + c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float h[2];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const float x = __uint_as_float(z[i + 2 * j + b]);
+                h[b] = C::kPairB ? x * sigmoid_fast(x) * __uint_as_float(u[i + 2 * j + b]) : x * gelu_gate(x);
+              }
+              p[j] = pack2(h[0], h[1]);
+            }
+            if (live && q.n0 + c + i < a.N) *reinterpret_cast<uint4*>(out + i) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+        }
+      } else if (MODE == FWD2 || MODE == DX) {
+#pragma unroll 1
+        for (int c = half * 32; c < BN; c += 64) {
+          uint32_t z[32];
+          ptx::tmem_ld_32x32b_x32(d + c, z);
+          ptx::tmem_ld_wait();
+          float* out = reinterpret_cast<float*>(a.out) + slot * a.N + q.n0 + c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            if (live && q.n0 + c + i < a.N)
+              *reinterpret_cast<uint4*>(out + i) = make_uint4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+        }
+      } else if (MODE == BWD1) {
+        float w = 0.0f, dot = 0.0f;
+        if (live) {
+          const int r = a.plan[a.row_of + slot];
+          w = r >= 0 ? a.weights[r] : 0.0f;
+        }
+        constexpr int G = C::kPairB ? 2 : 1;
+#pragma unroll 1
+        for (int c = half * 32; c < C::kOutCols; c += 64) {
+          uint16_t* dz = reinterpret_cast<uint16_t*>(a.out) + slot * ((int64_t)G * a.N) + q.n0 + c;
+          uint16_t* wh = reinterpret_cast<uint16_t*>(a.out2) + slot * a.N + q.n0 + c;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32; i0 += 16) {
+            uint32_t z[16], u[16], g[16];
+            ptx::tmem_ld_32x32b_x16(d + c + i0, z);
+            if (C::kPairB) ptx::tmem_ld_32x32b_x16(d + C::kOutCols + c + i0, u);
+            ptx::tmem_ld_32x32b_x16(d + BN + c + i0, g);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; i += 8) {
+              const bool in = q.n0 + c + i0 + i < a.N;
+              uint32_t pz[4], pu[4], ph[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float vz[2], vu[2], vh[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  const int x = i + 2 * j + b;
+                  const float zz = __uint_as_float(z[x]), dh = __uint_as_float(g[x]);
+                  const float dhw = w * dh;
+                  float h;
+                  if (C::kPairB) {
+                    const float uu = __uint_as_float(u[x]);
+                    const float sg = sigmoid_fast(zz);
+                    h = zz * sg * uu;
+                    vz[b] = dhw * uu * sg * (1.0f + zz * (1.0f - sg));
+                    vu[b] = dhw * zz * sg;
+                  } else {
+                    const float sg = gelu_gate(zz);
+                    h = zz * sg;
+                    vz[b] = dhw * (sg + zz * sg * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
+                    vu[b] = 0.0f;
+                  }
+                  vh[b] = w * h;
+                  if (in) dot += dh * h;
+                  if (!live) vz[b] = vu[b] = vh[b] = 0.0f;
+                }
+                pz[j] = pack2(vz[0], vz[1]);
+                pu[j] = pack2(vu[0], vu[1]);
+                ph[j] = pack2(vh[0], vh[1]);
+              }
+              if (in) {
+                *reinterpret_cast<uint4*>(dz + i0 + i) = make_uint4(pz[0], pz[1], pz[2], pz[3]);
+                if (C::kPairB) *reinterpret_cast<uint4*>(dz + a.N + i0 + i) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
+                *reinterpret_cast<uint4*>(wh + i0 + i) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+              }
+            }
+          }
+        }
+        if (live) a.part[slot * (2 * a.col_tiles) + 2 * (q.n0 / C::kOutCols) + half] = dot;
+      } else {
+        const int64_t m = (int64_t)q.m0 + row;
+        uint16_t* base = reinterpret_cast<uint16_t*>(a.out) + ((int64_t)q.e * a.M + m) * a.N;
+#pragma unroll 1
+        for (int c = half * 32; c < BN; c += 64) {
+          uint32_t z[32];
+          if (empty_tile) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0;
+          } else {
+            ptx::tmem_ld_32x32b_x32(d + c, z);
+            ptx::tmem_ld_wait();
+          }
+          uint16_t* out = base + q.n0 + c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            if (m < a.M && q.n0 + c + i < a.N) {
+              uint32_t p[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                p[j] = pack2(__uint_as_float(z[i + 2 * j]), __uint_as_float(z[i + 2 * j + 1]));
+              *reinterpret_cast<uint4*>(out + i) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+        }
+      }
+      if (!empty_tile) {
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+}  // namespace moe
+}  // namespace cusync

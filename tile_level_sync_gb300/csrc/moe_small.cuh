@@ -1,0 +1,161 @@
+// The parts of an expert layer outside the tiled products: the sums over a token's
+// experts, and the MLP of a few tokens without tiles.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "moe_gemm.cuh"
+#include "ptx.cuh"
+
+namespace cusync {
+namespace moe {
+
+struct CombineArgs {
+  int32_t* plan;
+  const float* rows;     // [slots, D] fp32
+  const float* weights;  // [T, k], or null: plain sums
+  void* out;             // [T, D] bf16
+  const float* part;     // gradient: [slots][parts]; null otherwise
+  float* dweights;       // [T, k]
+  int64_t slot_of;
+  int32_t T, k, D, parts;
+};
+
+constexpr int kCombineThreads = 256;
+
+// out[t] = sum_j weights[t,j] rows[slot_of[t,j]], in the order of j, in fp32; one rounding.
+// A block takes one token's next 4 * kCombineThreads columns.  With `part`, the first
+// block of a token also adds up dweights from the column tiles' partial sums, in order.
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int64_t t = blockIdx.x;
+  const int32_t* slots = a.plan + a.slot_of + t * a.k;
+  const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * 4;
+  if (c < a.D) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t slot = slots[j];
+      if (slot < 0) continue;
+      const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(a.rows + (int64_t)slot * a.D + c));
+      s.x += w * v.x;
+      s.y += w * v.y;
+      s.z += w * v.z;
+      s.w += w * v.w;
+    }
+    uint2 p = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + t * a.D + c) = p;
+  }
+  if (a.part && blockIdx.y == 0 && threadIdx.x < a.k) {
+    const int32_t slot = slots[threadIdx.x];
+    float s = 0.0f;
+    if (slot >= 0)
+      for (int i = 0; i < a.parts; ++i) s += a.part[(int64_t)slot * a.parts + i];
+    a.dweights[t * a.k + threadIdx.x] = s;
+  }
+}
+
+struct SmallArgs {
+  const uint16_t *X, *W1t, *W2t;
+  const int32_t* ids;
+  const float* weights;
+  float* h;              // [A, N1] fp32
+  uint16_t* Y;
+  int32_t* err;          // the work buffer's error word
+  int32_t T, k, E, D, N1;
+};
+
+__device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ float dot8(const uint4& w, const uint4& x, float s) {
+  s += lo16(w.x) * lo16(x.x);
+  s += hi16(w.x) * hi16(x.x);
+  s += lo16(w.y) * lo16(x.y);
+  s += hi16(w.y) * hi16(x.y);
+  s += lo16(w.z) * lo16(x.z);
+  s += hi16(w.z) * hi16(x.z);
+  s += lo16(w.w) * lo16(x.w);
+  s += hi16(w.w) * hi16(x.w);
+  return s;
+}
+__device__ __forceinline__ float dot8f(const uint4& w, const float4& x, const float4& y, float s) {
+  s += lo16(w.x) * x.x;
+  s += hi16(w.x) * x.y;
+  s += lo16(w.y) * x.z;
+  s += hi16(w.y) * x.w;
+  s += lo16(w.z) * y.x;
+  s += hi16(w.z) * y.y;
+  s += lo16(w.w) * y.z;
+  s += hi16(w.w) * y.w;
+  return s;
+}
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint4 ld_stream(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+
+constexpr int kSmallThreads = 256;
+
+// h[a][n] = act(X[t] . W1 rows of the chosen expert): a warp per (assignment, n).
+template <int ACT>
+__global__ void __launch_bounds__(kSmallThreads) small_up_kernel(SmallArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
+  if (u == 0 && lane == 0) *a.err = 0;
+  const int as = (int)(u / a.N1), n = (int)(u - (int64_t)as * a.N1);
+  if (as >= a.T * a.k) return;
+  const int e = a.ids[as];
+  if ((unsigned)e >= (unsigned)a.E) return;
+  const uint16_t* x = a.X + (int64_t)(as / a.k) * a.D;
+  const uint16_t* w = a.W1t + ((int64_t)e * (ACT == 1 ? 2 : 1) * a.N1 + n) * a.D;
+  const uint16_t* v = w + (int64_t)a.N1 * a.D;
+  float z = 0.0f, g = 0.0f;
+#pragma unroll 8
+  for (int c = lane * 8; c < a.D; c += 256) {
+    const uint4 xx = *reinterpret_cast<const uint4*>(x + c);
+    z = dot8(ld_stream(w + c), xx, z);
+    if (ACT == 1) g = dot8(ld_stream(v + c), xx, g);
+  }
+  z = warp_add(z);
+  if (ACT == 1) g = warp_add(g);
+  if (lane == 0) a.h[(int64_t)as * a.N1 + n] = ACT == 1 ? z * sigmoid_fast(z) * g : z * gelu_gate(z);
+}
+
+// Y[t][d] = sum_j weights[t,j] W2[e_j][d] . h[t,j]: a warp per (t, d), in the order of j.
+__global__ void __launch_bounds__(kSmallThreads) small_down_kernel(SmallArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
+  const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
+  if (t >= a.T) return;
+  float y = 0.0f;
+#pragma unroll 2
+  for (int j = 0; j < a.k; ++j) {
+    const int as = t * a.k + j;
+    const int e = a.ids[as];
+    if ((unsigned)e >= (unsigned)a.E) continue;
+    const uint16_t* w = a.W2t + ((int64_t)e * a.D + d) * a.N1;
+    const float* h = a.h + (int64_t)as * a.N1;
+    float s = 0.0f;
+#pragma unroll 4
+    for (int c = lane * 8; c < a.N1; c += 256) {
+      const float4 p = *reinterpret_cast<const float4*>(h + c), q = *reinterpret_cast<const float4*>(h + c + 4);
+      s = dot8f(ld_stream(w + c), p, q, s);
+    }
+    y += a.weights[as] * s;
+  }
+  y = warp_add(y);
+  if (lane == 0) a.Y[(int64_t)t * a.D + d] = (uint16_t)(pack2(y, 0.0f) & 0xffffu);
+}
+
+}  // namespace moe
+}  // namespace cusync
