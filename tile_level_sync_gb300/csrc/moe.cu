@@ -28,6 +28,8 @@ constexpr int64_t kPlanChunk = 4096;   // assignments of a plan block
 constexpr int64_t kPlanBlocks = 128;   // plan blocks at most
 // Assignments up to which the MLP runs without tiles.
 constexpr int64_t kSmallAssignments = 32;
+// Assignments per expert up to which the first product gathers the tokens' rows itself.
+constexpr int64_t kGatherRows = 16;
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
@@ -38,10 +40,10 @@ struct Layer {
   int64_t T, D, N1, A, S;
   int32_t E, k, G, groups, group_limit, group_top;
   int64_t chunk, blocks;                                          // plan
-  int64_t counts, offsets, tile_expert, slot_of, row_of, hist;    // plan, 32-bit words
+  int64_t counts, offsets, tiles, slot_of, row_of, hist;          // plan, 32-bit words
   int64_t plan_bytes;
-  int64_t h, rows, work_bytes;                                    // forward work, bytes
-  int64_t gh, gz, grows, gpart, grad_bytes;                       // gradient work, bytes
+  int64_t x, h, rows, work_bytes;                                 // forward work, bytes
+  int64_t gx, gy, gh, gz, grows, gpart, grad_bytes;                      // gradient work, bytes
   int32_t parts;
 };
 
@@ -85,12 +87,12 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
   };
   L->counts = take(L->E);
   L->offsets = take(L->E + 1);
-  L->tile_expert = take(L->S / kTileRows);
+  L->tiles = take(2 * (L->S / kTileRows));
   L->slot_of = take(L->A);
   L->row_of = take(L->S);
   L->hist = take(L->blocks > 1 ? L->blocks * L->E : 0);
   L->plan_bytes = round_up(w * 4, 256);
-  L->h = L->rows = L->work_bytes = L->gh = L->gz = L->grows = L->gpart = L->grad_bytes = 0;
+  L->x = L->h = L->rows = L->work_bytes = L->gx = L->gy = L->gh = L->gz = L->grows = L->gpart = L->grad_bytes = 0;
   L->parts = 0;
   if (d->D >= 1 && d->N1 >= 1) {
     int64_t b = L->plan_bytes;
@@ -99,11 +101,14 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
       b += round_up(n, 256);
       return at;
     };
+    L->x = bytes(L->S * L->D * 2);
     L->h = bytes(L->S * L->N1 * 2);
     L->rows = bytes(L->S * L->D * 4);
     L->work_bytes = b;
     b = L->plan_bytes;
     L->parts = (int32_t)(2 * div_up(L->N1, 128));
+    L->gx = bytes(L->S * L->D * 2);
+    L->gy = bytes(L->S * L->D * 2);
     L->gh = bytes(L->S * L->N1 * 2);
     L->gz = bytes(L->S * L->G * L->N1 * 2);
     L->grows = bytes(L->S * L->D * 4);
@@ -134,6 +139,9 @@ cudaError_t prepare_act() {
   cudaError_t e = prepare_gemm<FWD1, ACT, 256>();
   if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 128>();
   if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 64>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1G, ACT, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1G, ACT, 128>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1G, ACT, 64>();
   if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128>();
   return e;
 }
@@ -263,7 +271,7 @@ cudaError_t launch_plan(const Layer& L, const int32_t* ids, void* plan, cudaStre
   p.chunk = L.chunk;
   p.counts = L.counts;
   p.offsets = L.offsets;
-  p.tile_expert = L.tile_expert;
+  p.tiles = L.tiles;
   p.slot_of = L.slot_of;
   p.row_of = L.row_of;
   p.hist = L.hist;
@@ -281,7 +289,7 @@ GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
   a.weights = weights;
   a.counts = L.counts;
   a.offsets = L.offsets;
-  a.tile_expert = L.tile_expert;
+  a.tiles = L.tiles;
   a.row_of = L.row_of;
   a.T = (int32_t)L.T;
   a.k = L.k;
@@ -312,6 +320,21 @@ cudaError_t launch_fwd(const GemmArgs& a, int bn, int64_t row_tiles, int sms, cu
   if (bn == 256) return launch_gemm<MODE, ACT, 256>(a, row_tiles, sms, s);
   if (bn == 128) return launch_gemm<MODE, ACT, 128>(a, row_tiles, sms, s);
   return launch_gemm<MODE, ACT, 64>(a, row_tiles, sms, s);
+}
+
+cudaError_t launch_dispatch(const Layer& L, void* work, const void* x, void* xs, const void* y, void* ys, int sms,
+                            cudaStream_t s) {
+  DispatchArgs d = {};
+  d.plan = static_cast<int32_t*>(work);
+  d.x = static_cast<const uint4*>(x);
+  d.xs = static_cast<uint4*>(xs);
+  d.y = static_cast<const uint4*>(y);
+  d.ys = static_cast<uint4*>(ys);
+  d.row_of = L.row_of;
+  d.k = L.k;
+  d.chunks = (int32_t)(L.D / 8);
+  const int64_t blocks = std::min<int64_t>(div_up(L.S, kDispatchThreads / 32), (int64_t)sms * 8);
+  return launch(dispatch_kernel, dim3((unsigned)blocks), kDispatchThreads, 0, s, d);
 }
 
 cudaError_t launch_combine(const Layer& L, void* work, const float* rows, const float* weights, void* out,
@@ -443,10 +466,18 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   b.N = (int32_t)L.D;
   b.K = (int32_t)L.N1;
   b.out = w + L.rows;
-  if (!map_2d(&a.mA, X, L.T, L.D, 1) || !map_3d(&a.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, bn1 / L.G) ||
+  const bool gather = L.A <= kGatherRows * L.E;
+  if (!(gather ? map_2d(&a.mA, X, L.T, L.D, 1) : map_2d(&a.mA, w + L.x, L.S, L.D, 32)) ||
+      !map_3d(&a.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, bn1 / L.G) ||
       !map_2d(&b.mA, w + L.h, L.S, L.N1, 32) || !map_3d(&b.mB, W2t, L.E, L.D, L.N1, bn2))
     return CUSYNC_ERR_CUDA;
-  e = L.G == 2 ? launch_fwd<FWD1, 1>(a, bn1, row_tiles, sms, s) : launch_fwd<FWD1, 0>(a, bn1, row_tiles, sms, s);
+  if (gather) {
+    e = L.G == 2 ? launch_fwd<FWD1G, 1>(a, bn1, row_tiles, sms, s) : launch_fwd<FWD1G, 0>(a, bn1, row_tiles, sms, s);
+  } else {
+    e = launch_dispatch(L, work, X, w + L.x, nullptr, nullptr, sms, s);
+    if (e == cudaSuccess)
+      e = L.G == 2 ? launch_fwd<FWD1, 1>(a, bn1, row_tiles, sms, s) : launch_fwd<FWD1, 0>(a, bn1, row_tiles, sms, s);
+  }
   if (e == cudaSuccess) e = launch_fwd<FWD2, 0>(b, bn2, row_tiles, sms, s);
   if (e == cudaSuccess)
     e = launch_combine(L, work, reinterpret_cast<float*>(w + L.rows), weights, Y, nullptr, nullptr, s);
@@ -474,7 +505,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if (d->num_sms) sms = std::min(sms, d->num_sms);
   char* w = static_cast<char*>(work);
   const int64_t H = L.G * L.N1, row_tiles = L.S / kTileRows;
-  void *gh = w + L.gh, *gz = w + L.gz;
+  void *gx = w + L.gx, *gy = w + L.gy, *gh = w + L.gh, *gz = w + L.gz;
   float *rows = reinterpret_cast<float*>(w + L.grows), *part = reinterpret_cast<float*>(w + L.gpart);
 
   GemmArgs p = gemm_args(L, work, weights);  // hidden layer and its gradient
@@ -495,13 +526,14 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   w2.M = (int32_t)L.D;
   w2.N = (int32_t)L.N1;
   w2.out = dW2t;
-  if (!map_2d(&p.mA, X, L.T, L.D, 1) || !map_2d(&p.mA2, dY, L.T, L.D, 1) ||
+  if (!map_2d(&p.mA, gx, L.S, L.D, 128) || !map_2d(&p.mA2, gy, L.S, L.D, 128) ||
       !map_3d(&p.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, 128) || !map_3d(&p.mB2, W2t, L.E, L.D, L.N1, 64) ||
       !map_2d(&x.mA, gz, L.S, H, 32) || !map_3d(&x.mB, W1t, L.E, H, L.D, 64) ||
-      !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB, X, L.T, L.D, 1) ||
-      !map_2d(&w2.mA, dY, L.T, L.D, 1) || !map_2d(&w2.mB, gh, L.S, L.N1, 64))
+      !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB, gx, L.S, L.D, 64) ||
+      !map_2d(&w2.mA, gy, L.S, L.D, 64) || !map_2d(&w2.mB, gh, L.S, L.N1, 64))
     return CUSYNC_ERR_CUDA;
   cudaError_t e = launch_plan(L, ids, work, s);
+  if (e == cudaSuccess) e = launch_dispatch(L, work, X, gx, dY, gy, sms, s);
   if (e == cudaSuccess)
     e = L.G == 2 ? launch_gemm<BWD1, 1, 256>(p, row_tiles, sms, s) : launch_gemm<BWD1, 0, 128>(p, row_tiles, sms, s);
   if (e == cudaSuccess) e = launch_gemm<DX, 0, 256>(x, row_tiles, sms, s);

@@ -3,31 +3,34 @@
 // A tile is 128 rows of one expert (the plan aligns an expert's rows to 128) x BN columns,
 // or, for a weight gradient, 128 x BN of one expert's matrix.  One CTA per SM walks its
 // tiles with a fixed stride:
-//   warp 0     copies: TMA boxes of the weights and of the slot-ordered intermediates;
-//              rows of X and dY are fetched through the plan's row indices four at a time
-//              (tile::gather4), so the tokens are never copied into expert order.
+//   warp 0     copies: TMA boxes of the weights and of the slot-ordered rows.
 //   warp 1     TMEM owner; lane 0 issues tcgen05.mma (128 x BN x 16, fp32 accumulators).
 //   warps 2-9  epilogue: two warps per TMEM lane quarter, a thread per row.
 // Accumulators are double-buffered where two fit in TMEM's 512 columns.
 //
 //   mode   rows x columns          A            B                       epilogue
-//   FWD1   slots x N1              X (gather)   W1t[e]                  h = act(z), bf16
+//   FWD1   slots x N1              X by slot    W1t[e]                  h = act(z), bf16
+//   FWD1G  the same                X (gather)
 //   FWD2   slots x D               H            W2t[e]                  O, fp32
 //   BWD1   slots x N1              X, dY        W1t[e]; W2t[e] along N  z and dH = dY W2 side by
 //                                                                       side: dZ and w h (bf16),
 //                                                                       partial sums of dH h
 //   DX     slots x D               dZ           W1t[e] along N          dX per slot, fp32
-//   DW1    G*N1 x D (per expert)   dZ along M   X (gather) along N      bf16
-//   DW2    D x N1 (per expert)     dY (gather)  w H along N             bf16
+//   DW1    G*N1 x D (per expert)   dZ along M   X along N               bf16
+//   DW2    D x N1 (per expert)     dY along M   w H along N             bf16
 //
 // "along M/N": the operand is stored with that index contiguous rather than K, and the MMA
 // reads it that way (instruction and shared-memory descriptors), so no operand is ever
 // transposed in memory.
 //
+// X by slot: a copy in slot order (dispatch_kernel).  The gather (tile::gather4, four rows a
+// copy through the plan's row indices) needs no such copy, but brings 128 rows x 64 columns
+// in 1.25 us, three times what the MMAs of a 128 x 256 x 64 block take (first product of
+// 4096 tokens x 8 of 64 experts, D = 2048, N1 = 1024: 609 us): it is for tiles of few rows.
+//
 // A row behind an expert's last one gets no store in the forward pass; its accumulator
 // rows hold whatever the ring held, and rows do not mix.  In the weight gradients K runs
-// over slots: there the gather reads zeros for such rows (an index outside the tensor) and
-// BWD1 stored zeros, so they add nothing.
+// over slots: there dispatch_kernel and BWD1 stored zeros for such rows.
 //
 // Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
 #pragma once
@@ -42,7 +45,7 @@
 namespace cusync {
 namespace moe {
 
-enum : int { FWD1 = 0, FWD2 = 1, BWD1 = 2, DX = 3, DW1 = 4, DW2 = 5 };
+enum : int { FWD1 = 0, FWD2 = 1, BWD1 = 2, DX = 3, DW1 = 4, DW2 = 5, FWD1G = 6 };
 
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kGemmThreads = 320;
@@ -58,7 +61,7 @@ struct GemmArgs {
   void* out;         // H, O, dZ, dX per slot, dW1t or dW2t
   void* out2;        // BWD1: w H
   float* part;       // BWD1: partial sums of dH h, [slot][2 * column tiles]
-  int64_t counts, offsets, tile_expert, row_of;
+  int64_t counts, offsets, tiles, row_of;
   int32_t T, k, E;
   int32_t M;         // DW: rows of an expert's matrix
   int32_t N;         // output columns (FWD1, BWD1: N1)
@@ -70,9 +73,9 @@ template <int MODE, int ACT, int BN>
 struct GemmCfg {
   static constexpr bool kDw = MODE == DW1 || MODE == DW2;
   static constexpr bool kBwd1 = MODE == BWD1;
-  static constexpr bool kGatherA = MODE == FWD1 || MODE == BWD1 || MODE == DW2;
-  static constexpr bool kGatherB = MODE == DW1;
-  static constexpr bool kPairB = ACT == 1 && (MODE == FWD1 || MODE == BWD1);  // gate and up columns in one tile
+  static constexpr bool kFwd1 = MODE == FWD1 || MODE == FWD1G;
+  static constexpr bool kGather = MODE == FWD1G;
+  static constexpr bool kPairB = ACT == 1 && (kFwd1 || kBwd1);  // gate and up columns in one tile
   static constexpr bool kMnA = kDw;
   static constexpr bool kMnB = kDw || MODE == DX;
   static constexpr int kOutCols = kPairB ? BN / 2 : BN;  // output columns of a tile
@@ -80,12 +83,13 @@ struct GemmCfg {
   static constexpr int kBBytes = BN * 128;
   static constexpr int kD2 = kBwd1 ? kOutCols : 0;       // columns of BWD1's second accumulator
   static constexpr int kStageBytes = kABytes + kBBytes + (kBwd1 ? kABytes + kD2 * 128 : 0);
-  static constexpr int kRing = 208 * 1024;
+  static constexpr int kRing = 192 * 1024;
+  static constexpr int kStageOut = 8 * 4096;              // epilogue: 32 rows of 128 bytes for each warp
   static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
   static constexpr int kAccCols = BN + kD2;
   static constexpr int kAccs = 2 * kAccCols <= 512 ? 2 : 1;
   static constexpr int kTmemCols = kAccs * kAccCols <= 128 ? 128 : kAccs * kAccCols <= 256 ? 256 : 512;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kStageOut + 1024;
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -101,7 +105,7 @@ __device__ __forceinline__ float gelu_gate(float z) {
   return sigmoid_fast(2.0f * kGeluC * (z + 0.044715f * z * z * z));
 }
 
-// The tile t of a launch.
+// One tile of a launch.
 struct Tile {
   int32_t e, slot0, rows, m0, n0, nkb;
 };
@@ -127,14 +131,59 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
     r.nkb = (r.rows + 63) / 64;
   } else {
     const int32_t rt = t / a.col_tiles;
-    r.e = a.plan[a.tile_expert + rt];
+    const int2 er = *reinterpret_cast<const int2*>(a.plan + a.tiles + 2 * rt);
+    r.e = er.x;
+    r.rows = er.y;
     r.m0 = 0;
     r.n0 = (t - rt * a.col_tiles) * C::kOutCols;
     r.slot0 = rt * kTileRows;
-    r.rows = min(kTileRows, a.plan[a.offsets + r.e] + a.plan[a.counts + r.e] - r.slot0);
     r.nkb = (a.K + 63) / 64;
   }
   return r;
+}
+
+// A CTA's tiles, read one ahead: the plan's entry of a tile is a trip to L2 that no role
+// should wait for between two tiles.
+template <int MODE, int ACT, int BN>
+struct Walk {
+  const GemmArgs& a;
+  const int32_t total;
+  int32_t t;
+  Tile next;
+  __device__ __forceinline__ Walk(const GemmArgs& args, int32_t n) : a(args), total(n), t(blockIdx.x) {
+    if (t < total) next = tile_at<MODE, ACT, BN>(a, t);
+  }
+  __device__ __forceinline__ bool take(Tile& q) {
+    if (t >= total) return false;
+    q = next;
+    t += gridDim.x;
+    if (t < total) next = tile_at<MODE, ACT, BN>(a, t);
+    return true;
+  }
+};
+
+// 32 rows x 128 bytes, staged in shared memory (16-byte pieces, swizzled so that neither
+// side conflicts) and stored as whole 128-byte rows, four to an instruction.  `mine` is this
+// lane's row; row r of the warp goes to out + r * pitch when r < rows, its 16-byte pieces
+// below `pieces`.
+template <int PIECES>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine)[4 * PIECES], uint8_t* out,
+                                           int64_t pitch, int rows, int pieces, int lane) {
+  constexpr int kRowsEach = 32 / PIECES;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i)
+    *reinterpret_cast<uint4*>(stage + lane * (16 * PIECES) + ((i ^ (lane * PIECES / 8)) & (PIECES - 1)) * 16) =
+        make_uint4(mine[4 * i], mine[4 * i + 1], mine[4 * i + 2], mine[4 * i + 3]);
+  __syncwarp();
+  const int piece = lane % PIECES;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    const int r = i * kRowsEach + lane / PIECES;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (16 * PIECES) +
+                                                    ((piece ^ (r * PIECES / 8)) & (PIECES - 1)) * 16);
+    if (r < rows && piece < pieces) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = v;
+  }
 }
 
 template <int MODE, int ACT, int BN>
@@ -176,36 +225,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   const uint32_t tmem = tmem_slot;
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int32_t total = tile_total<MODE, ACT, BN>(a);
-  const int32_t step = gridDim.x;
+  Walk<MODE, ACT, BN> walk(a, tile_total<MODE, ACT, BN>(a));
+  Tile q;
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     const uint64_t keep = ptx::l2_policy_evict_last(), stream = ptx::l2_policy_evict_normal();
     uint32_t it = 0;
-    for (int32_t t = blockIdx.x; t < total && !abort_flag; t += step) {
-      const Tile q = tile_at<MODE, ACT, BN>(a, t);
-      // a lane's four gathered rows, as token indices: of the tile (FWD1, BWD1) or of one
-      // k-block; -1 (a slot behind the last row) becomes T, outside the tensor, read as zero
-      const int gl = C::kDw ? (lane & 15) : lane;  // DW: 16 lanes cover a k-block's 64 rows
-      auto tokens = [&](int32_t r0) {
-        int4 r = make_int4(-1, -1, -1, -1);
-        if (r0 + 4 * gl < q.rows) r = *reinterpret_cast<const int4*>(a.plan + a.row_of + q.slot0 + r0 + 4 * gl);
-        return r;
-      };
-      auto token = [&](int32_t r) { return r < 0 ? a.T : r / a.k; };
-      int4 next = make_int4(-1, -1, -1, -1), tok = next;
-      if (C::kGatherA || C::kGatherB) next = tokens(0);
-      if (!C::kDw) tok = make_int4(token(next.x), token(next.y), token(next.z), token(next.w));
-      const int live = (q.rows + 3) / 4;           // lanes whose rows a tile of slots needs
+    while (!abort_flag && walk.take(q)) {
+      // a lane's four gathered rows, as token indices; -1 (a slot behind the last row)
+      // becomes T, outside the tensor, read as zero
+      int4 tok = make_int4(a.T, a.T, a.T, a.T);
+      if (C::kGather && 4 * lane < q.rows) {
+        const int4 r = *reinterpret_cast<const int4*>(a.plan + a.row_of + q.slot0 + 4 * lane);
+        auto token = [&](int32_t x) { return x < 0 ? a.T : x / a.k; };
+        tok = make_int4(token(r.x), token(r.y), token(r.z), token(r.w));
+      }
+      const int live = (q.rows + 3) / 4;           // lanes whose rows a gathered tile needs
       const int boxes = (q.rows + 31) / 32;        // 32-row boxes of a slot-ordered A
       bool ok = true;
       for (int kb = 0; kb < q.nkb; ++kb, ++it) {
         const uint32_t st = it % C::kStages, par = ((it / C::kStages) & 1) ^ 1;
-        if (C::kDw) {
-          tok = make_int4(token(next.x), token(next.y), token(next.z), token(next.w));
-          next = tokens(kb * 64 + 64);
-        }
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs) && !abort_flag;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -216,18 +256,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         uint64_t* bar = &full[st];
         if (lane == 0) {
           uint32_t bytes = C::kBBytes;
-          if (C::kDw) bytes += C::kABytes;
-          else if (C::kGatherA) bytes += live * 512;
+          if (C::kGather) bytes += live * 512;
+          else if (C::kDw || C::kBwd1) bytes += C::kABytes;
           else bytes += boxes * 4096;
-          if (C::kBwd1) bytes += live * 512 + C::kD2 * 128;
+          if (C::kBwd1) bytes += C::kABytes + C::kD2 * 128;
           ptx::mbar_arrive_expect_tx(bar, bytes);
         }
         __syncwarp();
         const int32_t kc = kb * 64;
-        if (MODE == FWD1 || MODE == BWD1) {
-          if (lane < live) {
-            ptx::tma_gather4(sA + lane * 512, &a.mA, bar, kc, tok, keep);
-            if (C::kBwd1) ptx::tma_gather4(sA2 + lane * 512, &a.mA2, bar, kc, tok, keep);
+        if (C::kFwd1 || C::kBwd1) {
+          if (C::kGather) {
+            if (lane < live) ptx::tma_gather4(sA + lane * 512, &a.mA, bar, kc, tok, keep);
+          } else if (C::kBwd1) {
+            if (lane == 1) ptx::tma_load_2d(sA, &a.mA, bar, kc, q.slot0, keep);
+            if (lane == 2) ptx::tma_load_2d(sA2, &a.mA2, bar, kc, q.slot0, keep);
+          } else {
+            if (lane < boxes) ptx::tma_load_2d(sA + lane * 4096, &a.mA, bar, kc, q.slot0 + 32 * lane, keep);
           }
           if (lane == 0) {
             if (C::kPairB) {
@@ -236,11 +280,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
             } else {
               ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, q.e, stream);
             }
-            if (C::kBwd1)
-#pragma unroll
-              for (int c = 0; c < C::kD2 / 64; ++c)
-                ptx::tma_load_3d(sB2 + c * 8192, &a.mB2, bar, q.n0 + 64 * c, kc, q.e, stream);
           }
+          if (C::kBwd1 && lane < C::kD2 / 64)
+            ptx::tma_load_3d(sB2 + lane * 8192, &a.mB2, bar, q.n0 + 64 * lane, kc, q.e, stream);
         } else if (MODE == FWD2 || MODE == DX) {
           if (lane < boxes) ptx::tma_load_2d(sA + lane * 4096, &a.mA, bar, kc, q.slot0 + 32 * lane, keep);
           if (MODE == FWD2) {
@@ -248,18 +290,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           } else if (lane < BN / 64) {
             ptx::tma_load_3d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, kc, q.e, stream);
           }
-        } else if (MODE == DW1) {
-          if (lane < 2) ptx::tma_load_2d(sA + lane * 8192, &a.mA, bar, q.m0 + 64 * lane, q.slot0 + kc, keep);
-#pragma unroll
-          for (int c = 0; c < BN / 128; ++c) {
-            const int ch = 2 * c + (lane >> 4);
-            ptx::tma_gather4(sB + ch * 8192 + gl * 512, &a.mB, bar, q.n0 + 64 * ch, tok, keep);
-          }
         } else {
-          const int ch = lane >> 4;
-          ptx::tma_gather4(sA + ch * 8192 + gl * 512, &a.mA, bar, q.m0 + 64 * ch, tok, keep);
-          if (lane < BN / 64)
-            ptx::tma_load_2d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, q.slot0 + kc, keep);
+          if (lane < 2) ptx::tma_load_2d(sA + lane * 8192, &a.mA, bar, q.m0 + 64 * lane, q.slot0 + kc, keep);
+          if (lane < BN / 64) ptx::tma_load_2d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, q.slot0 + kc, keep);
         }
       }
       if (!ok) {
@@ -283,8 +316,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       constexpr uint32_t idesc2 = ptx::idesc_bf16_f32(128, C::kBwd1 ? C::kD2 : BN) | ptx::kIdescBMn;
       uint32_t it = 0, acc = 0;
       bool ok = true;
-      for (int32_t t = blockIdx.x; t < total && ok && !abort_flag; t += step) {
-        const Tile q = tile_at<MODE, ACT, BN>(a, t);
+      while (ok && !abort_flag && walk.take(q)) {
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
         const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
         ++acc;
@@ -327,11 +359,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
-    const int row = quarter * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
+    const int row0 = quarter * 32;
     uint32_t acc = 0;
-    for (int32_t t = blockIdx.x; t < total; t += step) {
-      const Tile q = tile_at<MODE, ACT, BN>(a, t);
+    while (walk.take(q)) {
       const bool empty_tile = q.nkb == 0;
       const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
       if (!empty_tile) {
@@ -345,31 +377,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         ptx::tc_fence_after();
       }
       const uint32_t d = tmem + buf * C::kAccCols + lanes;
-      const int64_t slot = (int64_t)q.slot0 + row;
-      const bool live = row < q.rows;
-      if (MODE == FWD1) {
+      const int64_t slot0 = (int64_t)q.slot0 + row0, slot = slot0 + lane;
+      const bool live = row0 + lane < q.rows;
+      if (C::kFwd1) {
 #pragma unroll 1
         for (int c = half * 32; c < C::kOutCols; c += 64) {
-          uint32_t z[32], u[32];
+          uint32_t z[32], u[32], p[16];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           if (C::kPairB) ptx::tmem_ld_32x32b_x32(d + C::kOutCols + c, u);
           ptx::tmem_ld_wait();
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + slot * a.N + q.n0 + c;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t p[4];
+          for (int i = 0; i < 16; ++i) {
+            float h[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float h[2];
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float x = __uint_as_float(z[i + 2 * j + b]);
-                h[b] = C::kPairB ? x * sigmoid_fast(x) * __uint_as_float(u[i + 2 * j + b]) : x * gelu_gate(x);
-              }
-              p[j] = pack2(h[0], h[1]);
+            for (int b = 0; b < 2; ++b) {
+              const float x = __uint_as_float(z[2 * i + b]);
+              h[b] = C::kPairB ? x * sigmoid_fast(x) * __uint_as_float(u[2 * i + b]) : x * gelu_gate(x);
             }
-            if (live && q.n0 + c + i < a.N) *reinterpret_cast<uint4*>(out + i) = make_uint4(p[0], p[1], p[2], p[3]);
+            p[i] = pack2(h[0], h[1]);
           }
+          const int n = q.n0 + c;
+          store_rows<4>(stage, p, reinterpret_cast<uint8_t*>(a.out) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2,
+                        q.rows - row0, (a.N - n) / 8, lane);
         }
       } else if (MODE == FWD2 || MODE == DX) {
 #pragma unroll 1
@@ -377,11 +406,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
-          float* out = reinterpret_cast<float*>(a.out) + slot * a.N + q.n0 + c;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            if (live && q.n0 + c + i < a.N)
-              *reinterpret_cast<uint4*>(out + i) = make_uint4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+          const int n = q.n0 + c;
+          store_rows<8>(stage, z, reinterpret_cast<uint8_t*>(a.out) + (slot0 * a.N + n) * 4, (int64_t)a.N * 4,
+                        q.rows - row0, (a.N - n) / 4, lane);
         }
       } else if (MODE == BWD1) {
         float w = 0.0f, dot = 0.0f;
@@ -390,11 +417,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           w = r >= 0 ? a.weights[r] : 0.0f;
         }
         constexpr int G = C::kPairB ? 2 : 1;
+        const int64_t pitch = (int64_t)G * a.N * 2;
 #pragma unroll 1
         for (int c = half * 32; c < C::kOutCols; c += 64) {
-          uint16_t* dz = reinterpret_cast<uint16_t*>(a.out) + slot * ((int64_t)G * a.N) + q.n0 + c;
-          uint16_t* wh = reinterpret_cast<uint16_t*>(a.out2) + slot * a.N + q.n0 + c;
-#pragma unroll 1
+          const int n = q.n0 + c;
+          uint32_t pz[16], pu[16], ph[16];
+#pragma unroll
           for (int i0 = 0; i0 < 32; i0 += 16) {
             uint32_t z[16], u[16], g[16];
             ptx::tmem_ld_32x32b_x16(d + c + i0, z);
@@ -402,53 +430,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
             ptx::tmem_ld_32x32b_x16(d + BN + c + i0, g);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; i += 8) {
-              const bool in = q.n0 + c + i0 + i < a.N;
-              uint32_t pz[4], pu[4], ph[4];
+            for (int j = 0; j < 8; ++j) {
+              float vz[2], vu[2], vh[2];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float vz[2], vu[2], vh[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                  const int x = i + 2 * j + b;
-                  const float zz = __uint_as_float(z[x]), dh = __uint_as_float(g[x]);
-                  const float dhw = w * dh;
-                  float h;
-                  if (C::kPairB) {
-                    const float uu = __uint_as_float(u[x]);
-                    const float sg = sigmoid_fast(zz);
-                    h = zz * sg * uu;
-                    vz[b] = dhw * uu * sg * (1.0f + zz * (1.0f - sg));
-                    vu[b] = dhw * zz * sg;
-                  } else {
-                    const float sg = gelu_gate(zz);
-                    h = zz * sg;
-                    vz[b] = dhw * (sg + zz * sg * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
-                    vu[b] = 0.0f;
-                  }
-                  vh[b] = w * h;
-                  if (in) dot += dh * h;
-                  if (!live) vz[b] = vu[b] = vh[b] = 0.0f;
+              for (int b = 0; b < 2; ++b) {
+                const float zz = __uint_as_float(z[2 * j + b]), dh = __uint_as_float(g[2 * j + b]);
+                const float dhw = w * dh;
+                float h;
+                if (C::kPairB) {
+                  const float uu = __uint_as_float(u[2 * j + b]);
+                  const float sg = sigmoid_fast(zz);
+                  h = zz * sg * uu;
+                  vz[b] = dhw * uu * sg * (1.0f + zz * (1.0f - sg));
+                  vu[b] = dhw * zz * sg;
+                } else {
+                  const float sg = gelu_gate(zz);
+                  h = zz * sg;
+                  vz[b] = dhw * (sg + zz * sg * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
+                  vu[b] = 0.0f;
                 }
-                pz[j] = pack2(vz[0], vz[1]);
-                pu[j] = pack2(vu[0], vu[1]);
-                ph[j] = pack2(vh[0], vh[1]);
+                vh[b] = w * h;
+                dot += dh * h;  // columns behind N1 hold zeros
+                if (!live) vz[b] = vu[b] = vh[b] = 0.0f;
               }
-              if (in) {
-                *reinterpret_cast<uint4*>(dz + i0 + i) = make_uint4(pz[0], pz[1], pz[2], pz[3]);
-                if (C::kPairB) *reinterpret_cast<uint4*>(dz + a.N + i0 + i) = make_uint4(pu[0], pu[1], pu[2], pu[3]);
-                *reinterpret_cast<uint4*>(wh + i0 + i) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-              }
+              pz[i0 / 2 + j] = pack2(vz[0], vz[1]);
+              pu[i0 / 2 + j] = pack2(vu[0], vu[1]);
+              ph[i0 / 2 + j] = pack2(vh[0], vh[1]);
             }
           }
+          // all 128 rows of the tile: the weight gradients read zeros behind the last one
+          uint8_t* dz = reinterpret_cast<uint8_t*>(a.out) + slot0 * pitch + (int64_t)n * 2;
+          store_rows<4>(stage, pz, dz, pitch, 32, (a.N - n) / 8, lane);
+          if (C::kPairB) store_rows<4>(stage, pu, dz + (int64_t)a.N * 2, pitch, 32, (a.N - n) / 8, lane);
+          store_rows<4>(stage, ph, reinterpret_cast<uint8_t*>(a.out2) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2, 32,
+                        (a.N - n) / 8, lane);
         }
         if (live) a.part[slot * (2 * a.col_tiles) + 2 * (q.n0 / C::kOutCols) + half] = dot;
       } else {
-        const int64_t m = (int64_t)q.m0 + row;
-        uint16_t* base = reinterpret_cast<uint16_t*>(a.out) + ((int64_t)q.e * a.M + m) * a.N;
+        const int64_t m = (int64_t)q.m0 + row0;
+        uint8_t* base = reinterpret_cast<uint8_t*>(a.out) + (((int64_t)q.e * a.M + m) * a.N + q.n0) * 2;
 #pragma unroll 1
         for (int c = half * 32; c < BN; c += 64) {
-          uint32_t z[32];
+          uint32_t z[32], p[16];
           if (empty_tile) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0;
@@ -456,16 +479,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
             ptx::tmem_ld_32x32b_x32(d + c, z);
             ptx::tmem_ld_wait();
           }
-          uint16_t* out = base + q.n0 + c;
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            if (m < a.M && q.n0 + c + i < a.N) {
-              uint32_t p[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                p[j] = pack2(__uint_as_float(z[i + 2 * j]), __uint_as_float(z[i + 2 * j + 1]));
-              *reinterpret_cast<uint4*>(out + i) = make_uint4(p[0], p[1], p[2], p[3]);
-            }
+          for (int i = 0; i < 16; ++i) p[i] = pack2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
+          store_rows<4>(stage, p, base + c * 2, (int64_t)a.N * 2, (int)(a.M - m), (a.N - q.n0 - c) / 8, lane);
         }
       }
       if (!empty_tile) {

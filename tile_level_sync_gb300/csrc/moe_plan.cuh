@@ -2,8 +2,8 @@
 //
 // A plan is an array of 32-bit words: a header, the experts' counts, the offsets of their
 // first slots (multiples of kTileRows, so that a 128-row tile of a product belongs to one
-// expert), the expert of each row tile, slot_of (assignment -> slot) and row_of (slot ->
-// assignment).
+// expert), each row tile's expert and rows, slot_of (assignment -> slot) and row_of (slot
+// -> assignment).
 //
 // Blocks take consecutive chunks of the ids, a block's warps consecutive parts of its
 // chunk.  Within 32 ids, equal ones find each other with one match instruction; the rank
@@ -32,7 +32,7 @@ struct PlanArgs {
   int32_t E;
   int32_t blocks;       // 1: no histogram kernel ran
   int64_t chunk;        // assignments of a block (a multiple of kPlanThreads)
-  int64_t counts, offsets, tile_expert, slot_of, row_of, hist;  // word offsets
+  int64_t counts, offsets, tiles, slot_of, row_of, hist;  // word offsets
 };
 
 __device__ __forceinline__ int plan_id(const PlanArgs& a, int64_t i, int64_t end) {
@@ -162,7 +162,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   int32_t* row_of = a.plan + a.row_of;
   for (int e = blockIdx.x * kPlanWarps + warp; e < E; e += gridDim.x * kPlanWarps) {
     const int64_t o = offset[e], n = offset[e + 1];
-    for (int64_t i = o / kTileRows + lane; i < n / kTileRows; i += 32) a.plan[a.tile_expert + i] = e;
+    int2* tiles = reinterpret_cast<int2*>(a.plan + a.tiles);
+    for (int64_t i = o / kTileRows + lane; i < n / kTileRows; i += 32)
+      tiles[i] = make_int2(e, (int)min((int64_t)kTileRows, o + count[e] - i * kTileRows));
     for (int64_t i = o + count[e] + lane; i < n; i += 32) row_of[i] = -1;
   }
   for (int64_t i = used + (int64_t)blockIdx.x * kPlanThreads + tid; i < a.S; i += (int64_t)gridDim.x * kPlanThreads)

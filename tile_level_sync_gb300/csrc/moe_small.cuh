@@ -23,6 +23,36 @@ struct CombineArgs {
   int32_t T, k, D, parts;
 };
 
+struct DispatchArgs {
+  int32_t* plan;
+  const uint4 *x, *y;    // [T, chunks] of 16 bytes
+  uint4 *xs, *ys;        // [slots, chunks]; y and ys may be null
+  int64_t row_of;
+  int32_t k, chunks;
+};
+
+constexpr int kDispatchThreads = 256;
+
+// Rows of X (and dY) into slot order, a warp per slot; zeros behind an expert's last row
+// (the weight gradients sum over them).
+__global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(DispatchArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t used = (int64_t)a.plan[PLAN_TILES] * kTileRows;
+  const int64_t warps = (int64_t)gridDim.x * (kDispatchThreads / 32);
+  for (int64_t s = (int64_t)blockIdx.x * (kDispatchThreads / 32) + (threadIdx.x >> 5); s < used; s += warps) {
+    const int32_t r = a.plan[a.row_of + s];
+    const int64_t from = r < 0 ? 0 : (int64_t)(r / a.k) * a.chunks, to = s * a.chunks;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+    for (int c = lane; c < a.chunks; c += 32) a.xs[to + c] = r < 0 ? zero : a.x[from + c];
+    if (a.y)
+#pragma unroll 4
+      for (int c = lane; c < a.chunks; c += 32) a.ys[to + c] = r < 0 ? zero : a.y[from + c];
+  }
+}
+
 constexpr int kCombineThreads = 256;
 
 // out[t] = sum_j weights[t,j] rows[slot_of[t,j]], in the order of j, in fp32; one rounding.
