@@ -184,6 +184,8 @@ MLPS = [
     dict(T=130, E=1, k=1, D=128, N1=128),
     dict(T=700, E=3, k=1, D=136, N1=520),
     dict(T=64, E=64, k=8, D=512, N1=256),
+    dict(T=900, E=4, k=2, D=264, N1=264),
+    dict(T=257, E=1, k=1, D=72, N1=136),
 ]
 _name = lambda c: "T{T}E{E}k{k}D{D}N{N1}".format(**c)  # noqa: E731
 

@@ -28,6 +28,8 @@ constexpr int64_t kPlanChunk = 4096;   // assignments of a plan block
 constexpr int64_t kPlanBlocks = 128;   // plan blocks at most
 // Assignments up to which the MLP runs without tiles.
 constexpr int64_t kSmallAssignments = 32;
+// Assignments per expert from which products take tiles of 256 rows on pairs of CTAs.
+constexpr int64_t kPairRows = 128;
 // Assignments per expert up to which the first product gathers the tokens' rows itself.
 constexpr int64_t kGatherRows = 16;
 
@@ -37,10 +39,10 @@ bool aligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u)
 
 // What a descriptor means, its defaults filled in.
 struct Layer {
-  int64_t T, D, N1, A, S;
+  int64_t T, D, N1, A, S, max_pairs;
   int32_t E, k, G, groups, group_limit, group_top;
   int64_t chunk, blocks;                                          // plan
-  int64_t counts, offsets, tiles, slot_of, row_of, hist;          // plan, 32-bit words
+  int64_t counts, offsets, tiles, pairs, slot_of, row_of, hist;   // plan, 32-bit words
   int64_t plan_bytes;
   int64_t x, h, rows, work_bytes;                                 // forward work, bytes
   int64_t gx, gy, gh, gz, grows, gpart, grad_bytes;                      // gradient work, bytes
@@ -87,7 +89,9 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
   };
   L->counts = take(L->E);
   L->offsets = take(L->E + 1);
-  L->tiles = take(2 * (L->S / kTileRows));
+  L->tiles = take(4 * (L->S / kTileRows));
+  L->max_pairs = L->A / (2 * kTileRows) + std::min<int64_t>(L->E, L->A);
+  L->pairs = take(4 * L->max_pairs);
   L->slot_of = take(L->A);
   L->row_of = take(L->S);
   L->hist = take(L->blocks > 1 ? L->blocks * L->E : 0);
@@ -125,24 +129,39 @@ std::mutex g_mu;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];  // SMs of a prepared device, 0 = not prepared
 
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT, int BN, int PAIR>
 cudaError_t prepare_gemm() {
-  const void* f = reinterpret_cast<const void*>(&moe_gemm_kernel<MODE, ACT, BN>);
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmCfg<MODE, ACT, BN>::kSmemBytes);
+  const void* f = reinterpret_cast<const void*>(&moe_gemm_kernel<MODE, ACT, BN, PAIR>);
+  cudaError_t e =
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmCfg<MODE, ACT, BN, PAIR>::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;  // loads the kernel now, not at a launch inside a capture
   return cudaFuncGetAttributes(&fa, f);
 }
 
+template <int MODE, int ACT>
+cudaError_t prepare_widths() {
+  cudaError_t e = prepare_gemm<MODE, ACT, 256, 1>();
+  if (e == cudaSuccess) e = prepare_gemm<MODE, ACT, 128, 1>();
+  if (e == cudaSuccess) e = prepare_gemm<MODE, ACT, 64, 1>();
+  return e;
+}
+
 template <int ACT>
 cudaError_t prepare_act() {
-  cudaError_t e = prepare_gemm<FWD1, ACT, 256>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 128>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 64>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD1G, ACT, 256>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD1G, ACT, 128>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD1G, ACT, 64>();
-  if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128>();
+  cudaError_t e = prepare_widths<FWD1, ACT>();
+  if (e == cudaSuccess) e = prepare_widths<FWD1G, ACT>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 256, 2>();
+  if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128, 1>();
+  if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128, 2>();
+  return e;
+}
+
+template <int PAIR>
+cudaError_t prepare_pair() {
+  cudaError_t e = prepare_gemm<DX, 0, 256, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<DW1, 0, 256, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<DW2, 0, 256, PAIR>();
   return e;
 }
 
@@ -168,12 +187,10 @@ cusync_status_t prepare_device(int* sms) {
   cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = prepare_act<0>();
   if (e == cudaSuccess) e = prepare_act<1>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 256>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 128>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 64>();
-  if (e == cudaSuccess) e = prepare_gemm<DX, 0, 256>();
-  if (e == cudaSuccess) e = prepare_gemm<DW1, 0, 256>();
-  if (e == cudaSuccess) e = prepare_gemm<DW2, 0, 256>();
+  if (e == cudaSuccess) e = prepare_widths<FWD2, 0>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 256, 2>();
+  if (e == cudaSuccess) e = prepare_pair<1>();
+  if (e == cudaSuccess) e = prepare_pair<2>();
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)plan_smem(CUSYNC_MOE_MAX_EXPERTS));
@@ -209,18 +226,26 @@ bool map_3d(CUtensorMap* m, const void* p, int64_t depth, int64_t rows, int64_t 
 // Every launch is a programmatic dependent of the kernel before it in the stream: it may be
 // set up while that one ends, and each kernel waits for that end before it touches memory.
 template <typename... P, typename... Q>
-cudaError_t launch(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, Q... args) {
+cudaError_t launch_cluster(int cluster, void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, Q... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, f, args...);
+}
+template <typename... P, typename... Q>
+cudaError_t launch(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, Q... args) {
+  return launch_cluster(1, f, grid, threads, smem, s, args...);
 }
 
 template <typename L, int SCORE, bool GRAD>
@@ -272,6 +297,7 @@ cudaError_t launch_plan(const Layer& L, const int32_t* ids, void* plan, cudaStre
   p.counts = L.counts;
   p.offsets = L.offsets;
   p.tiles = L.tiles;
+  p.pairs = L.pairs;
   p.slot_of = L.slot_of;
   p.row_of = L.row_of;
   p.hist = L.hist;
@@ -297,14 +323,21 @@ GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
   return a;
 }
 
-template <int MODE, int ACT, int BN>
-cudaError_t launch_gemm(GemmArgs a, int64_t row_tiles, int sms, cudaStream_t s) {
-  using C = GemmCfg<MODE, ACT, BN>;
+// row_tiles: an upper bound of the launch's tiles of 128 (PAIR = 2: 256) rows.
+template <int MODE, int ACT, int BN, int PAIR>
+cudaError_t launch_gemm(GemmArgs a, const Layer& L, int64_t row_tiles, int sms, cudaStream_t s) {
+  using C = GemmCfg<MODE, ACT, BN, PAIR>;
+  a.tiles = PAIR == 2 ? L.pairs : L.tiles;
   a.col_tiles = (int32_t)div_up(a.N, C::kOutCols);
-  a.m_tiles = (int32_t)div_up(a.M, 128);
+  a.m_tiles = (int32_t)div_up(a.M, 128 * PAIR);
   const int64_t tiles = C::kDw ? (int64_t)a.E * a.m_tiles * a.col_tiles : row_tiles * a.col_tiles;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms));
-  return launch(moe_gemm_kernel<MODE, ACT, BN>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
+  const int grid = PAIR * (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / PAIR));
+  return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, BN, PAIR>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
+}
+template <int MODE, int ACT, int BN>
+cudaError_t launch_gemm(bool pair, const GemmArgs& a, const Layer& L, int sms, cudaStream_t s) {
+  return pair ? launch_gemm<MODE, ACT, BN, 2>(a, L, L.max_pairs, sms, s)
+              : launch_gemm<MODE, ACT, BN, 1>(a, L, L.S / kTileRows, sms, s);
 }
 
 // Tile width of a forward product: the widest whose tiles fill the SMs twice over, counting
@@ -315,11 +348,13 @@ int tile_width(int64_t row_tiles, int64_t cols256, int sms) {
   return 64;
 }
 
+bool use_pairs(const Layer& L, int sms) { return L.A >= kPairRows * L.E && sms >= 2; }
+
 template <int MODE, int ACT>
-cudaError_t launch_fwd(const GemmArgs& a, int bn, int64_t row_tiles, int sms, cudaStream_t s) {
-  if (bn == 256) return launch_gemm<MODE, ACT, 256>(a, row_tiles, sms, s);
-  if (bn == 128) return launch_gemm<MODE, ACT, 128>(a, row_tiles, sms, s);
-  return launch_gemm<MODE, ACT, 64>(a, row_tiles, sms, s);
+cudaError_t launch_fwd(const GemmArgs& a, const Layer& L, int bn, int64_t row_tiles, int sms, cudaStream_t s) {
+  if (bn == 256) return launch_gemm<MODE, ACT, 256, 1>(a, L, row_tiles, sms, s);
+  if (bn == 128) return launch_gemm<MODE, ACT, 128, 1>(a, L, row_tiles, sms, s);
+  return launch_gemm<MODE, ACT, 64, 1>(a, L, row_tiles, sms, s);
 }
 
 cudaError_t launch_dispatch(const Layer& L, void* work, const void* x, void* xs, const void* y, void* ys, int sms,
@@ -457,7 +492,9 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   cudaError_t e = launch_plan(L, ids, work, s);
   if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
   const int64_t row_tiles = std::min<int64_t>(L.S / kTileRows, std::min<int64_t>(L.E, L.A) + L.A / kTileRows);
-  const int bn1 = tile_width(row_tiles, div_up(L.N1, 256 / L.G), sms), bn2 = tile_width(row_tiles, div_up(L.D, 256), sms);
+  const bool gather = L.A <= kGatherRows * L.E, pair = use_pairs(L, sms);
+  const int bn1 = pair ? 256 : tile_width(row_tiles, div_up(L.N1, 256 / L.G), sms);
+  const int bn2 = pair ? 256 : tile_width(row_tiles, div_up(L.D, 256), sms);
   GemmArgs a = gemm_args(L, work, weights);
   a.N = (int32_t)L.N1;
   a.K = (int32_t)L.D;
@@ -466,19 +503,23 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   b.N = (int32_t)L.D;
   b.K = (int32_t)L.N1;
   b.out = w + L.rows;
-  const bool gather = L.A <= kGatherRows * L.E;
-  if (!(gather ? map_2d(&a.mA, X, L.T, L.D, 1) : map_2d(&a.mA, w + L.x, L.S, L.D, 32)) ||
-      !map_3d(&a.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, bn1 / L.G) ||
-      !map_2d(&b.mA, w + L.h, L.S, L.N1, 32) || !map_3d(&b.mB, W2t, L.E, L.D, L.N1, bn2))
+  const int box_a = pair ? 128 : 32;
+  if (!(gather ? map_2d(&a.mA, X, L.T, L.D, 1) : map_2d(&a.mA, w + L.x, L.S, L.D, box_a)) ||
+      !map_3d(&a.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, pair ? 128 : bn1 / L.G) ||
+      !map_2d(&b.mA, w + L.h, L.S, L.N1, box_a) || !map_3d(&b.mB, W2t, L.E, L.D, L.N1, pair ? 128 : bn2))
     return CUSYNC_ERR_CUDA;
   if (gather) {
-    e = L.G == 2 ? launch_fwd<FWD1G, 1>(a, bn1, row_tiles, sms, s) : launch_fwd<FWD1G, 0>(a, bn1, row_tiles, sms, s);
+    e = L.G == 2 ? launch_fwd<FWD1G, 1>(a, L, bn1, row_tiles, sms, s) : launch_fwd<FWD1G, 0>(a, L, bn1, row_tiles, sms, s);
   } else {
     e = launch_dispatch(L, work, X, w + L.x, nullptr, nullptr, sms, s);
-    if (e == cudaSuccess)
-      e = L.G == 2 ? launch_fwd<FWD1, 1>(a, bn1, row_tiles, sms, s) : launch_fwd<FWD1, 0>(a, bn1, row_tiles, sms, s);
+    if (e == cudaSuccess && pair)
+      e = L.G == 2 ? launch_gemm<FWD1, 1, 256, 2>(a, L, L.max_pairs, sms, s)
+                   : launch_gemm<FWD1, 0, 256, 2>(a, L, L.max_pairs, sms, s);
+    else if (e == cudaSuccess)
+      e = L.G == 2 ? launch_fwd<FWD1, 1>(a, L, bn1, row_tiles, sms, s) : launch_fwd<FWD1, 0>(a, L, bn1, row_tiles, sms, s);
   }
-  if (e == cudaSuccess) e = launch_fwd<FWD2, 0>(b, bn2, row_tiles, sms, s);
+  if (e == cudaSuccess)
+    e = pair ? launch_gemm<FWD2, 0, 256, 2>(b, L, L.max_pairs, sms, s) : launch_fwd<FWD2, 0>(b, L, bn2, row_tiles, sms, s);
   if (e == cudaSuccess)
     e = launch_combine(L, work, reinterpret_cast<float*>(w + L.rows), weights, Y, nullptr, nullptr, s);
   return status_of(e);
@@ -504,7 +545,8 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if ((st = prepare_device(&sms)) != CUSYNC_OK) return st;
   if (d->num_sms) sms = std::min(sms, d->num_sms);
   char* w = static_cast<char*>(work);
-  const int64_t H = L.G * L.N1, row_tiles = L.S / kTileRows;
+  const int64_t H = L.G * L.N1;
+  const bool pair = use_pairs(L, sms), pair1 = H > 128 && sms >= 2, pair2 = L.D > 128 && sms >= 2;  // rows: slots; the weights' gradients'
   void *gx = w + L.gx, *gy = w + L.gy, *gh = w + L.gh, *gz = w + L.gz;
   float *rows = reinterpret_cast<float*>(w + L.grows), *part = reinterpret_cast<float*>(w + L.gpart);
 
@@ -527,19 +569,19 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   w2.N = (int32_t)L.N1;
   w2.out = dW2t;
   if (!map_2d(&p.mA, gx, L.S, L.D, 128) || !map_2d(&p.mA2, gy, L.S, L.D, 128) ||
-      !map_3d(&p.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, 128) || !map_3d(&p.mB2, W2t, L.E, L.D, L.N1, 64) ||
-      !map_2d(&x.mA, gz, L.S, H, 32) || !map_3d(&x.mB, W1t, L.E, H, L.D, 64) ||
+      !map_3d(&p.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, pair && L.G == 1 ? 64 : 128) || !map_3d(&p.mB2, W2t, L.E, L.D, L.N1, 64) ||
+      !map_2d(&x.mA, gz, L.S, H, pair ? 128 : 32) || !map_3d(&x.mB, W1t, L.E, H, L.D, 64) ||
       !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB, gx, L.S, L.D, 64) ||
       !map_2d(&w2.mA, gy, L.S, L.D, 64) || !map_2d(&w2.mB, gh, L.S, L.N1, 64))
     return CUSYNC_ERR_CUDA;
   cudaError_t e = launch_plan(L, ids, work, s);
   if (e == cudaSuccess) e = launch_dispatch(L, work, X, gx, dY, gy, sms, s);
   if (e == cudaSuccess)
-    e = L.G == 2 ? launch_gemm<BWD1, 1, 256>(p, row_tiles, sms, s) : launch_gemm<BWD1, 0, 128>(p, row_tiles, sms, s);
-  if (e == cudaSuccess) e = launch_gemm<DX, 0, 256>(x, row_tiles, sms, s);
+    e = L.G == 2 ? launch_gemm<BWD1, 1, 256>(pair, p, L, sms, s) : launch_gemm<BWD1, 0, 128>(pair, p, L, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DX, 0, 256>(pair, x, L, sms, s);
   if (e == cudaSuccess) e = launch_combine(L, work, rows, nullptr, dX, part, dweights, s);
-  if (e == cudaSuccess) e = launch_gemm<DW1, 0, 256>(w1, row_tiles, sms, s);
-  if (e == cudaSuccess) e = launch_gemm<DW2, 0, 256>(w2, row_tiles, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DW1, 0, 256>(pair1, w1, L, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DW2, 0, 256>(pair2, w2, L, sms, s);
   return status_of(e);
 }
 

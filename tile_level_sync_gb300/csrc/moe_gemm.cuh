@@ -1,10 +1,13 @@
 // The products of an expert layer: one persistent tcgen05 kernel per product.
 //
 // A tile is 128 rows of one expert (the plan aligns an expert's rows to 128) x BN columns,
-// or, for a weight gradient, 128 x BN of one expert's matrix.  One CTA per SM walks its
-// tiles with a fixed stride:
+// or, for a weight gradient, 128 x BN of one expert's matrix.  With PAIR = 2 a pair of CTAs
+// (cta_group::2) computes 256 rows: each holds its 128 rows of A and half of B's columns,
+// so that a 128 x 256 x 64 block costs an SM 32 KB of loads, not 48 KB.  One CTA per SM
+// walks its tiles with a fixed stride:
 //   warp 0     copies: TMA boxes of the weights and of the slot-ordered rows.
-//   warp 1     TMEM owner; lane 0 issues tcgen05.mma (128 x BN x 16, fp32 accumulators).
+//   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma (fp32
+//              accumulators).
 //   warps 2-9  epilogue: two warps per TMEM lane quarter, a thread per row.
 // Accumulators are double-buffered where two fit in TMEM's 512 columns.
 //
@@ -61,7 +64,7 @@ struct GemmArgs {
   void* out;         // H, O, dZ, dX per slot, dW1t or dW2t
   void* out2;        // BWD1: w H
   float* part;       // BWD1: partial sums of dH h, [slot][2 * column tiles]
-  int64_t counts, offsets, tiles, row_of;
+  int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
   int32_t T, k, E;
   int32_t M;         // DW: rows of an expert's matrix
   int32_t N;         // output columns (FWD1, BWD1: N1)
@@ -69,7 +72,7 @@ struct GemmArgs {
   int32_t col_tiles, m_tiles;
 };
 
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT, int BN, int PAIR>
 struct GemmCfg {
   static constexpr bool kDw = MODE == DW1 || MODE == DW2;
   static constexpr bool kBwd1 = MODE == BWD1;
@@ -80,9 +83,9 @@ struct GemmCfg {
   static constexpr bool kMnB = kDw || MODE == DX;
   static constexpr int kOutCols = kPairB ? BN / 2 : BN;  // output columns of a tile
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = BN * 128;
+  static constexpr int kBBytes = BN / PAIR * 128;
   static constexpr int kD2 = kBwd1 ? kOutCols : 0;       // columns of BWD1's second accumulator
-  static constexpr int kStageBytes = kABytes + kBBytes + (kBwd1 ? kABytes + kD2 * 128 : 0);
+  static constexpr int kStageBytes = kABytes + kBBytes + (kBwd1 ? kABytes + kD2 / PAIR * 128 : 0);
   static constexpr int kRing = 192 * 1024;
   static constexpr int kStageOut = 8 * 4096;              // epilogue: 32 rows of 128 bytes for each warp
   static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
@@ -110,33 +113,33 @@ struct Tile {
   int32_t e, slot0, rows, m0, n0, nkb;
 };
 
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT, int BN, int PAIR>
 __device__ __forceinline__ int32_t tile_total(const GemmArgs& a) {
-  if (GemmCfg<MODE, ACT, BN>::kDw) return a.E * a.m_tiles * a.col_tiles;
-  return a.plan[PLAN_TILES] * a.col_tiles;
+  if (GemmCfg<MODE, ACT, BN, PAIR>::kDw) return a.E * a.m_tiles * a.col_tiles;
+  return a.plan[PAIR == 2 ? PLAN_PAIRS : PLAN_TILES] * a.col_tiles;
 }
 
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT, int BN, int PAIR>
 __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
-  using C = GemmCfg<MODE, ACT, BN>;
+  using C = GemmCfg<MODE, ACT, BN, PAIR>;
   Tile r;
   if (C::kDw) {
     const int32_t per = a.m_tiles * a.col_tiles;
     r.e = t / per;
     const int32_t q = t - r.e * per;
-    r.m0 = (q % a.m_tiles) * 128;
+    r.m0 = (q % a.m_tiles) * (128 * PAIR);
     r.n0 = (q / a.m_tiles) * BN;
     r.slot0 = a.plan[a.offsets + r.e];
     r.rows = a.plan[a.counts + r.e];
     r.nkb = (r.rows + 63) / 64;
   } else {
     const int32_t rt = t / a.col_tiles;
-    const int2 er = *reinterpret_cast<const int2*>(a.plan + a.tiles + 2 * rt);
+    const int4 er = *reinterpret_cast<const int4*>(a.plan + a.tiles + 4 * rt);
     r.e = er.x;
-    r.rows = er.y;
+    r.slot0 = er.y;
+    r.rows = er.z;
     r.m0 = 0;
     r.n0 = (t - rt * a.col_tiles) * C::kOutCols;
-    r.slot0 = rt * kTileRows;
     r.nkb = (a.K + 63) / 64;
   }
   return r;
@@ -144,20 +147,20 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
 
 // A CTA's tiles, read one ahead: the plan's entry of a tile is a trip to L2 that no role
 // should wait for between two tiles.
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT, int BN, int PAIR>
 struct Walk {
   const GemmArgs& a;
   const int32_t total;
   int32_t t;
   Tile next;
-  __device__ __forceinline__ Walk(const GemmArgs& args, int32_t n) : a(args), total(n), t(blockIdx.x) {
-    if (t < total) next = tile_at<MODE, ACT, BN>(a, t);
+  __device__ __forceinline__ Walk(const GemmArgs& args, int32_t n) : a(args), total(n), t(blockIdx.x / PAIR) {
+    if (t < total) next = tile_at<MODE, ACT, BN, PAIR>(a, t);
   }
   __device__ __forceinline__ bool take(Tile& q) {
     if (t >= total) return false;
     q = next;
-    t += gridDim.x;
-    if (t < total) next = tile_at<MODE, ACT, BN>(a, t);
+    t += gridDim.x / PAIR;
+    if (t < total) next = tile_at<MODE, ACT, BN, PAIR>(a, t);
     return true;
   }
 };
@@ -186,15 +189,16 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine
   }
 }
 
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT, int BN, int PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_constant__ GemmArgs a) {
-  using C = GemmCfg<MODE, ACT, BN>;
+  using C = GemmCfg<MODE, ACT, BN, PAIR>;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int32_t abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR == 2 ? (int)ptx::cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&tfull[i], 1);
-      ptx::mbar_init(&tempty[i], 8);
+      ptx::mbar_init(&tempty[i], 8 * PAIR);
     }
     ptx::mbar_init(&drain, 1);
     ptx::mbar_init_fence();
@@ -216,16 +220,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     }
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&tmem_slot, C::kTmemCols);
-    ptx::tmem_relinquish();
+    if (PAIR == 2) {
+      ptx::tmem_alloc_pair(&tmem_slot, C::kTmemCols);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(&tmem_slot, C::kTmemCols);
+      ptx::tmem_relinquish();
+    }
     ptx::tc_fence_before();
   }
   __syncthreads();
+  if (PAIR == 2) ptx::cluster_sync();  // the other CTA's barriers exist
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  Walk<MODE, ACT, BN> walk(a, tile_total<MODE, ACT, BN>(a));
+  Walk<MODE, ACT, BN, PAIR> walk(a, tile_total<MODE, ACT, BN, PAIR>(a));
   Tile q;
 
   if (warp == 0) {
@@ -242,7 +252,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         tok = make_int4(token(r.x), token(r.y), token(r.z), token(r.w));
       }
       const int live = (q.rows + 3) / 4;           // lanes whose rows a gathered tile needs
-      const int boxes = (q.rows + 31) / 32;        // 32-row boxes of a slot-ordered A
+      // this CTA's rows and columns of the tile
+      const int32_t slot = q.slot0 + (C::kDw ? 0 : 128 * rank), m0 = q.m0 + 128 * rank;
+      const int boxes = C::kDw ? 0 : (q.rows - 128 * rank + 31) / 32;  // 32-row boxes of A
+      const int32_t nb = q.n0 + (C::kPairB ? 0 : rank * (BN / 2)), n2 = q.n0 + rank * (C::kD2 / 2);
       bool ok = true;
       for (int kb = 0; kb < q.nkb; ++kb, ++it) {
         const uint32_t st = it % C::kStages, par = ((it / C::kStages) & 1) ^ 1;
@@ -254,46 +267,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         uint8_t* sA2 = sB + C::kBBytes;
         uint8_t* sB2 = sA2 + C::kABytes;
         uint64_t* bar = &full[st];
-        if (lane == 0) {
-          uint32_t bytes = C::kBBytes;
+        // in a pair both CTAs' copies complete on the first one's barrier
+        const uint32_t bar0 = PAIR == 2 ? ptx::mapa(bar, 0) : 0;
+        auto load2 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1, uint64_t pol) {
+          if (PAIR == 2) ptx::tma_load_2d_to_leader(dst, m, bar0, c0, c1, pol);
+          else ptx::tma_load_2d(dst, m, bar, c0, c1, pol);
+        };
+        auto load3 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2, uint64_t pol) {
+          if (PAIR == 2) ptx::tma_load_3d_to_leader(dst, m, bar0, c0, c1, c2, pol);
+          else ptx::tma_load_3d(dst, m, bar, c0, c1, c2, pol);
+        };
+        if (lane == 0 && rank == 0) {
+          uint32_t bytes = PAIR * (C::kBBytes + (C::kBwd1 ? C::kD2 / PAIR * 128 : 0));
           if (C::kGather) bytes += live * 512;
-          else if (C::kDw || C::kBwd1) bytes += C::kABytes;
+          else if (C::kDw) bytes += PAIR * C::kABytes;
+          else if (PAIR == 2 || C::kBwd1) bytes += (C::kBwd1 ? 2 : 1) * (q.rows > 128 ? 2 : 1) * C::kABytes;
           else bytes += boxes * 4096;
-          if (C::kBwd1) bytes += C::kABytes + C::kD2 * 128;
           ptx::mbar_arrive_expect_tx(bar, bytes);
         }
         __syncwarp();
         const int32_t kc = kb * 64;
-        if (C::kFwd1 || C::kBwd1) {
-          if (C::kGather) {
-            if (lane < live) ptx::tma_gather4(sA + lane * 512, &a.mA, bar, kc, tok, keep);
-          } else if (C::kBwd1) {
-            if (lane == 1) ptx::tma_load_2d(sA, &a.mA, bar, kc, q.slot0, keep);
-            if (lane == 2) ptx::tma_load_2d(sA2, &a.mA2, bar, kc, q.slot0, keep);
-          } else {
-            if (lane < boxes) ptx::tma_load_2d(sA + lane * 4096, &a.mA, bar, kc, q.slot0 + 32 * lane, keep);
-          }
-          if (lane == 0) {
-            if (C::kPairB) {
-              ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, 2 * q.e, stream);
-              ptx::tma_load_3d(sB + C::kBBytes / 2, &a.mB, bar, kc, q.n0, 2 * q.e + 1, stream);
-            } else {
-              ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, q.e, stream);
-            }
-          }
-          if (C::kBwd1 && lane < C::kD2 / 64)
-            ptx::tma_load_3d(sB2 + lane * 8192, &a.mB2, bar, q.n0 + 64 * lane, kc, q.e, stream);
-        } else if (MODE == FWD2 || MODE == DX) {
-          if (lane < boxes) ptx::tma_load_2d(sA + lane * 4096, &a.mA, bar, kc, q.slot0 + 32 * lane, keep);
-          if (MODE == FWD2) {
-            if (lane == 0) ptx::tma_load_3d(sB, &a.mB, bar, kc, q.n0, q.e, stream);
-          } else if (lane < BN / 64) {
-            ptx::tma_load_3d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, kc, q.e, stream);
-          }
+        // A
+        if (C::kGather) {
+          if (lane < live) ptx::tma_gather4(sA + lane * 512, &a.mA, bar, kc, tok, keep);
+        } else if (C::kDw) {
+          if (lane < 2) load2(sA + lane * 8192, &a.mA, m0 + 64 * lane, slot + kc, keep);
+        } else if (PAIR == 2 || C::kBwd1) {
+          if (lane == 1 && boxes > 0) load2(sA, &a.mA, kc, slot, keep);
+          if (C::kBwd1 && lane == 2 && boxes > 0) load2(sA2, &a.mA2, kc, slot, keep);
         } else {
-          if (lane < 2) ptx::tma_load_2d(sA + lane * 8192, &a.mA, bar, q.m0 + 64 * lane, q.slot0 + kc, keep);
-          if (lane < BN / 64) ptx::tma_load_2d(sB + lane * 8192, &a.mB, bar, q.n0 + 64 * lane, q.slot0 + kc, keep);
+          if (lane < boxes) load2(sA + lane * 4096, &a.mA, kc, slot + 32 * lane, keep);
         }
+        // B: this CTA's columns
+        if (C::kDw) {
+          if (lane < BN / PAIR / 64) load2(sB + lane * 8192, &a.mB, nb + 64 * lane, slot + kc, keep);
+        } else if (MODE == DX) {
+          if (lane < BN / PAIR / 64) load3(sB + lane * 8192, &a.mB, nb + 64 * lane, kc, q.e, stream);
+        } else if (lane == 0) {
+          if (!C::kPairB) {
+            load3(sB, &a.mB, kc, nb, q.e, stream);
+          } else if (PAIR == 2) {
+            load3(sB, &a.mB, kc, nb, 2 * q.e + rank, stream);  // gate columns; up columns
+          } else {
+            load3(sB, &a.mB, kc, nb, 2 * q.e, stream);
+            load3(sB + C::kBBytes / 2, &a.mB, kc, nb, 2 * q.e + 1, stream);
+          }
+        }
+        if (C::kBwd1 && lane < C::kD2 / PAIR / 64) load3(sB2 + lane * 8192, &a.mB2, n2 + 64 * lane, kc, q.e, stream);
       }
       if (!ok) {
         if (lane == 0) {
@@ -305,22 +325,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     }
     __syncwarp();
     // after an abort: wait, bounded, for the copies still in flight
-    if (abort_flag && lane == 0)
+    if (abort_flag && lane == 0 && rank == 0)
       for (uint32_t i = it > (uint32_t)C::kStages ? it - C::kStages : 0; i < it; ++i)
         ptx::mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       constexpr uint32_t majors = (C::kMnA ? ptx::kIdescAMn : 0) | (C::kMnB ? ptx::kIdescBMn : 0);
-      constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, BN) | majors;
-      constexpr uint32_t idesc2 = ptx::idesc_bf16_f32(128, C::kBwd1 ? C::kD2 : BN) | ptx::kIdescBMn;
+      constexpr uint32_t idesc = ptx::idesc_bf16_f32(128 * PAIR, BN) | majors;
+      constexpr uint32_t idesc2 = ptx::idesc_bf16_f32(128 * PAIR, C::kBwd1 ? C::kD2 : BN) | ptx::kIdescBMn;
+      auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t more) {
+        if (PAIR == 2) ptx::umma_bf16_pair(d, da, db, id, more);
+        else ptx::umma_bf16(d, da, db, id, more);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (PAIR == 2) ptx::umma_commit_pair_multicast(bar, 0x3);
+        else ptx::umma_commit(bar);
+      };
       uint32_t it = 0, acc = 0;
       bool ok = true;
       while (ok && !abort_flag && walk.take(q)) {
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
         const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
         ++acc;
-        ok = ptx::mbar_wait_bounded(&tempty[buf], (use & 1) ^ 1, kWaitNs) && !abort_flag;
+        ok = (PAIR == 2 ? ptx::mbar_wait_bounded_cluster(&tempty[buf], (use & 1) ^ 1, kWaitNs)
+                        : ptx::mbar_wait_bounded(&tempty[buf], (use & 1) ^ 1, kWaitNs)) &&
+             !abort_flag;
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * C::kAccCols;
@@ -336,22 +366,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
           const uint64_t dB = C::kMnB ? ptx::smem_desc_mn128(sB) : ptx::smem_desc_k128(sB);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) ptx::umma_bf16(d, dA + s * stepA, dB + s * stepB, idesc, kb || s);
+          for (int s = 0; s < 4; ++s) mma(d, dA + s * stepA, dB + s * stepB, idesc, kb || s);
           if (C::kBwd1) {
             const uint64_t dA2 = ptx::smem_desc_k128(sA2), dB2 = ptx::smem_desc_mn128(sB2);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              ptx::umma_bf16(d + BN, dA2 + s * (32 >> 4), dB2 + s * (2048 >> 4), idesc2, kb || s);
+              mma(d + BN, dA2 + s * (32 >> 4), dB2 + s * (2048 >> 4), idesc2, kb || s);
           }
-          ptx::umma_commit(&empty[st]);
+          commit(&empty[st]);
         }
         if (!ok) break;
-        ptx::umma_commit(&tfull[buf]);
+        commit(&tfull[buf]);
       }
       if (!ok || abort_flag) {
         abort_flag = 1;
         a.plan[PLAN_ERR] = (int32_t)kErrWait;
-        ptx::umma_commit(&drain);  // MMAs still in flight
+        commit(&drain);  // MMAs still in flight
         ptx::mbar_wait_bounded(&drain, 0, kWaitNs);
       }
     }
@@ -377,8 +407,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         ptx::tc_fence_after();
       }
       const uint32_t d = tmem + buf * C::kAccCols + lanes;
-      const int64_t slot0 = (int64_t)q.slot0 + row0, slot = slot0 + lane;
-      const bool live = row0 + lane < q.rows;
+      // this warp's 32 rows: of the matrix (weight gradients) or of the slots, `rows` of them real
+      const int r0 = 128 * rank + row0, rows = q.rows - r0;
+      const int64_t slot0 = (int64_t)q.slot0 + r0, slot = slot0 + lane;
+      const bool live = lane < rows;
       if (C::kFwd1) {
 #pragma unroll 1
         for (int c = half * 32; c < C::kOutCols; c += 64) {
@@ -398,7 +430,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           }
           const int n = q.n0 + c;
           store_rows<4>(stage, p, reinterpret_cast<uint8_t*>(a.out) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2,
-                        q.rows - row0, (a.N - n) / 8, lane);
+                        rows, (a.N - n) / 8, lane);
         }
       } else if (MODE == FWD2 || MODE == DX) {
 #pragma unroll 1
@@ -408,7 +440,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           ptx::tmem_ld_wait();
           const int n = q.n0 + c;
           store_rows<8>(stage, z, reinterpret_cast<uint8_t*>(a.out) + (slot0 * a.N + n) * 4, (int64_t)a.N * 4,
-                        q.rows - row0, (a.N - n) / 4, lane);
+                        rows, (a.N - n) / 4, lane);
         }
       } else if (MODE == BWD1) {
         float w = 0.0f, dot = 0.0f;
@@ -458,16 +490,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
               ph[i0 / 2 + j] = pack2(vh[0], vh[1]);
             }
           }
-          // all 128 rows of the tile: the weight gradients read zeros behind the last one
+          // all 128 rows of the CTA's tile: the weight gradients read zeros behind the last one
+          const int all = q.rows > 128 * rank ? 32 : 0;
           uint8_t* dz = reinterpret_cast<uint8_t*>(a.out) + slot0 * pitch + (int64_t)n * 2;
-          store_rows<4>(stage, pz, dz, pitch, 32, (a.N - n) / 8, lane);
-          if (C::kPairB) store_rows<4>(stage, pu, dz + (int64_t)a.N * 2, pitch, 32, (a.N - n) / 8, lane);
-          store_rows<4>(stage, ph, reinterpret_cast<uint8_t*>(a.out2) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2, 32,
+          store_rows<4>(stage, pz, dz, pitch, all, (a.N - n) / 8, lane);
+          if (C::kPairB) store_rows<4>(stage, pu, dz + (int64_t)a.N * 2, pitch, all, (a.N - n) / 8, lane);
+          store_rows<4>(stage, ph, reinterpret_cast<uint8_t*>(a.out2) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2, all,
                         (a.N - n) / 8, lane);
         }
         if (live) a.part[slot * (2 * a.col_tiles) + 2 * (q.n0 / C::kOutCols) + half] = dot;
       } else {
-        const int64_t m = (int64_t)q.m0 + row0;
+        const int64_t m = (int64_t)q.m0 + r0;
         uint8_t* base = reinterpret_cast<uint8_t*>(a.out) + (((int64_t)q.e * a.M + m) * a.N + q.n0) * 2;
 #pragma unroll 1
         for (int c = half * 32; c < BN; c += 64) {
@@ -487,14 +520,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       if (!empty_tile) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
+        if (lane == 0) {
+          if (rank == 0) ptx::mbar_arrive(&tempty[buf]);
+          else ptx::mbar_arrive_cluster(ptx::mapa(&tempty[buf], 0));
+        }
       }
     }
   }
+  ptx::tc_fence_before();
   __syncthreads();
+  if (PAIR == 2) ptx::cluster_sync();  // both CTAs are done with the pair's TMEM and barriers
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, C::kTmemCols);
+    if (PAIR == 2) ptx::tmem_dealloc_pair(tmem, C::kTmemCols);
+    else ptx::tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 

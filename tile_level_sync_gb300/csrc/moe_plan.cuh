@@ -2,7 +2,7 @@
 //
 // A plan is an array of 32-bit words: a header, the experts' counts, the offsets of their
 // first slots (multiples of kTileRows, so that a 128-row tile of a product belongs to one
-// expert), each row tile's expert and rows, slot_of (assignment -> slot) and row_of (slot
+// expert), the row tiles {expert, first slot, rows} and the same for tiles of 256 rows, slot_of (assignment -> slot) and row_of (slot
 // -> assignment).
 //
 // Blocks take consecutive chunks of the ids, a block's warps consecutive parts of its
@@ -22,7 +22,7 @@ namespace moe {
 constexpr int kTileRows = 128;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_HEADER = 16 };
+enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_PAIRS = 3, PLAN_HEADER = 16 };
 
 struct PlanArgs {
   const int32_t* ids;
@@ -32,7 +32,7 @@ struct PlanArgs {
   int32_t E;
   int32_t blocks;       // 1: no histogram kernel ran
   int64_t chunk;        // assignments of a block (a multiple of kPlanThreads)
-  int64_t counts, offsets, tiles, slot_of, row_of, hist;  // word offsets
+  int64_t counts, offsets, tiles, pairs, slot_of, row_of, hist;  // word offsets
 };
 
 __device__ __forceinline__ int plan_id(const PlanArgs& a, int64_t i, int64_t end) {
@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(PlanArgs a) {
 }
 
 // Shared memory of plan_kernel: per-warp histograms [kPlanWarps][E], then before[E],
-// count[E], offset[E + 1], and the scan's 32 partial sums.
-__host__ __device__ inline size_t plan_smem(int E) { return ((size_t)kPlanWarps * E + 3 * (size_t)E + 1 + 32) * 4; }
+// count[E], offset[E + 1], pair[E + 1], and the scan's 32 partial sums of 64 bits.
+__host__ __device__ inline int plan_scan_at(int E) { return (kPlanWarps * E + 4 * E + 2 + 1) & ~1; }
+__host__ __device__ inline size_t plan_smem(int E) { return (size_t)plan_scan_at(E) * 4 + 32 * 8; }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   extern __shared__ uint32_t sh[];
@@ -69,7 +70,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   uint32_t* before = whist + kPlanWarps * E;
   uint32_t* count = before + E;
   uint32_t* offset = count + E;
-  uint32_t* part = offset + E + 1;
+  uint32_t* pair = offset + E + 1;
+  uint64_t* part = reinterpret_cast<uint64_t*>(sh + plan_scan_at(E));
   for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) whist[i] = 0;
   for (int e = tid; e < E; e += kPlanThreads) before[e] = count[e] = 0;
   ptx::pdl_wait();
@@ -121,31 +123,39 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
     if (a.blocks == 1) count[e] = c;
   }
   __syncthreads();
-  // offsets: exclusive scan of the counts rounded up to whole tiles (E <= kPlanThreads)
+  // offsets: exclusive scans of the counts in whole tiles and in whole pairs of tiles
+  // (E <= kPlanThreads)
   {
-    const uint32_t v = tid < E ? (count[tid] + kTileRows - 1) / kTileRows * kTileRows : 0;
-    uint32_t s = v;
+    const uint32_t n = tid < E ? count[tid] : 0;
+    // tiles in the low 32 bits, pairs in the high ones
+    const uint64_t v = (n + kTileRows - 1) / kTileRows + ((uint64_t)((n + 2 * kTileRows - 1) / (2 * kTileRows)) << 32);
+    uint64_t s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, s, o);
+      const uint64_t u = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += u;
     }
     if (lane == 31) part[warp] = s;
     __syncthreads();
     if (warp == 0) {
-      const uint32_t p = part[lane];
-      uint32_t q = p;
+      const uint64_t p = part[lane];
+      uint64_t q = p;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, q, o);
+        const uint64_t u = __shfl_up_sync(0xffffffffu, q, o);
         if (lane >= o) q += u;
       }
       part[lane] = q - p;
     }
     __syncthreads();
     if (tid < E) {
-      offset[tid] = part[warp] + s - v;
-      if (tid == E - 1) offset[E] = part[warp] + s;
+      s += part[warp];
+      offset[tid] = (uint32_t)(s - v) * kTileRows;
+      pair[tid] = (uint32_t)((s - v) >> 32);
+      if (tid == E - 1) {
+        offset[E] = (uint32_t)s * kTileRows;
+        pair[E] = (uint32_t)(s >> 32);
+      }
     }
   }
   __syncthreads();
@@ -154,6 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
     if (tid == 0) {
       a.plan[PLAN_ERR] = 0;
       a.plan[PLAN_TILES] = (int32_t)(used / kTileRows);
+      a.plan[PLAN_PAIRS] = (int32_t)pair[E];
     }
     for (int e = tid; e < E; e += kPlanThreads) a.plan[a.counts + e] = (int32_t)count[e];
     for (int e = tid; e <= E; e += kPlanThreads) a.plan[a.offsets + e] = (int32_t)offset[e];
@@ -162,9 +173,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   int32_t* row_of = a.plan + a.row_of;
   for (int e = blockIdx.x * kPlanWarps + warp; e < E; e += gridDim.x * kPlanWarps) {
     const int64_t o = offset[e], n = offset[e + 1];
-    int2* tiles = reinterpret_cast<int2*>(a.plan + a.tiles);
-    for (int64_t i = o / kTileRows + lane; i < n / kTileRows; i += 32)
-      tiles[i] = make_int2(e, (int)min((int64_t)kTileRows, o + count[e] - i * kTileRows));
+    const int c = (int)count[e];
+    int4* tiles = reinterpret_cast<int4*>(a.plan + a.tiles) + o / kTileRows;
+    for (int i = lane; i * kTileRows < c; i += 32)
+      tiles[i] = make_int4(e, (int)o + i * kTileRows, min(kTileRows, c - i * kTileRows), 0);
+    int4* pairs = reinterpret_cast<int4*>(a.plan + a.pairs) + pair[e];
+    for (int i = lane; i * 2 * kTileRows < c; i += 32)
+      pairs[i] = make_int4(e, (int)o + i * 2 * kTileRows, min(2 * kTileRows, c - i * 2 * kTileRows), 0);
     for (int64_t i = o + count[e] + lane; i < n; i += 32) row_of[i] = -1;
   }
   for (int64_t i = used + (int64_t)blockIdx.x * kPlanThreads + tid; i < a.S; i += (int64_t)gridDim.x * kPlanThreads)
