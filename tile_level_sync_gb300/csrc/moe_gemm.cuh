@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     const uint64_t keep = ptx::l2_policy_evict_last(), stream = ptx::l2_policy_evict_normal();
-    uint32_t it = 0;
+    uint32_t it = 0, st = 0, par = 1;
+    const uint32_t full0 = PAIR == 2 ? ptx::mapa(&full[0], 0) : 0;
     while (!abort_flag && walk.take(q)) {
       // a lane's four gathered rows, as token indices; -1 (a slot behind the last row)
       // becomes T, outside the tensor, read as zero
@@ -256,11 +257,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       const int32_t slot = q.slot0 + (C::kDw ? 0 : 128 * rank), m0 = q.m0 + 128 * rank;
       const int boxes = C::kDw ? 0 : (q.rows - 128 * rank + 31) / 32;  // 32-row boxes of A
       const int32_t nb = q.n0 + (C::kPairB ? 0 : rank * (BN / 2)), n2 = q.n0 + rank * (C::kD2 / 2);
+      uint32_t bytes = PAIR * (C::kBBytes + (C::kBwd1 ? C::kD2 / PAIR * 128 : 0));
+      if (C::kGather) bytes += live * 512;
+      else if (C::kDw) bytes += PAIR * C::kABytes;
+      else if (PAIR == 2 || C::kBwd1) bytes += (C::kBwd1 ? 2 : 1) * (q.rows > 128 ? 2 : 1) * C::kABytes;
+      else bytes += boxes * 4096;
       bool ok = true;
+      // Every lane waits for the slot and issues its own copies: nothing orders the lanes,
+      // since the barrier's phase cannot end before lane 0's arrival.
       for (int kb = 0; kb < q.nkb; ++kb, ++it) {
-        const uint32_t st = it % C::kStages, par = ((it / C::kStages) & 1) ^ 1;
-        ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs) && !abort_flag;
-        ok = __all_sync(0xffffffffu, ok);
+        ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
         uint8_t* sA = ring + st * C::kStageBytes;
         uint8_t* sB = sA + C::kABytes;
@@ -268,7 +274,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         uint8_t* sB2 = sA2 + C::kABytes;
         uint64_t* bar = &full[st];
         // in a pair both CTAs' copies complete on the first one's barrier
-        const uint32_t bar0 = PAIR == 2 ? ptx::mapa(bar, 0) : 0;
+        const uint32_t bar0 = full0 + 8 * st;
         auto load2 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1, uint64_t pol) {
           if (PAIR == 2) ptx::tma_load_2d_to_leader(dst, m, bar0, c0, c1, pol);
           else ptx::tma_load_2d(dst, m, bar, c0, c1, pol);
@@ -277,15 +283,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           if (PAIR == 2) ptx::tma_load_3d_to_leader(dst, m, bar0, c0, c1, c2, pol);
           else ptx::tma_load_3d(dst, m, bar, c0, c1, c2, pol);
         };
-        if (lane == 0 && rank == 0) {
-          uint32_t bytes = PAIR * (C::kBBytes + (C::kBwd1 ? C::kD2 / PAIR * 128 : 0));
-          if (C::kGather) bytes += live * 512;
-          else if (C::kDw) bytes += PAIR * C::kABytes;
-          else if (PAIR == 2 || C::kBwd1) bytes += (C::kBwd1 ? 2 : 1) * (q.rows > 128 ? 2 : 1) * C::kABytes;
-          else bytes += boxes * 4096;
-          ptx::mbar_arrive_expect_tx(bar, bytes);
+        if (lane == 0 && rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+        if (++st == C::kStages) {
+          st = 0;
+          par ^= 1;
         }
-        __syncwarp();
         const int32_t kc = kb * 64;
         // A
         if (C::kGather) {
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         }
         if (C::kBwd1 && lane < C::kD2 / PAIR / 64) load3(sB2 + lane * 8192, &a.mB2, n2 + 64 * lane, kc, q.e, stream);
       }
-      if (!ok) {
+      if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) {
           abort_flag = 1;
           a.plan[PLAN_ERR] = (int32_t)kErrWait;
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         if (PAIR == 2) ptx::umma_commit_pair_multicast(bar, 0x3);
         else ptx::umma_commit(bar);
       };
-      uint32_t it = 0, acc = 0;
+      uint32_t st = 0, par = 0, acc = 0;
       bool ok = true;
       while (ok && !abort_flag && walk.take(q)) {
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
@@ -354,9 +356,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * C::kAccCols;
-        for (int kb = 0; kb < q.nkb; ++kb, ++it) {
-          const uint32_t st = it % C::kStages;
-          ok = ptx::mbar_wait_bounded(&full[st], (it / C::kStages) & 1, kWaitNs) && !abort_flag;
+        for (int kb = 0; kb < q.nkb; ++kb) {
+          ok = ptx::mbar_wait_bounded(&full[st], par, kWaitNs);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t sA = ptx::smem_u32(ring + st * C::kStageBytes);
@@ -374,6 +375,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
               mma(d + BN, dA2 + s * (32 >> 4), dB2 + s * (2048 >> 4), idesc2, kb || s);
           }
           commit(&empty[st]);
+          if (++st == C::kStages) {
+            st = 0;
+            par ^= 1;
+          }
         }
         if (!ok) break;
         commit(&tfull[buf]);
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
-      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
     const int row0 = quarter * 32;
     uint32_t acc = 0;
