@@ -110,7 +110,7 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     L->rows = bytes(L->S * L->D * 4);
     L->work_bytes = b;
     b = L->plan_bytes;
-    L->parts = (int32_t)(2 * div_up(L->N1, 128));
+    L->parts = (int32_t)(8 * div_up(L->N1, 256));  // one for 32 columns
     L->gx = bytes(L->S * L->D * 2);
     L->gy = bytes(L->S * L->D * 2);
     L->gh = bytes(L->S * L->N1 * 2);
@@ -129,39 +129,26 @@ std::mutex g_mu;
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];  // SMs of a prepared device, 0 = not prepared
 
-template <int MODE, int ACT, int BN, int PAIR>
+template <int MODE, int ACT, int PAIR>
 cudaError_t prepare_gemm() {
-  const void* f = reinterpret_cast<const void*>(&moe_gemm_kernel<MODE, ACT, BN, PAIR>);
+  const void* f = reinterpret_cast<const void*>(&moe_gemm_kernel<MODE, ACT, PAIR>);
   cudaError_t e =
-      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmCfg<MODE, ACT, BN, PAIR>::kSmemBytes);
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, GemmCfg<MODE, ACT, PAIR>::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;  // loads the kernel now, not at a launch inside a capture
   return cudaFuncGetAttributes(&fa, f);
 }
 
-template <int MODE, int ACT>
-cudaError_t prepare_widths() {
-  cudaError_t e = prepare_gemm<MODE, ACT, 256, 1>();
-  if (e == cudaSuccess) e = prepare_gemm<MODE, ACT, 128, 1>();
-  if (e == cudaSuccess) e = prepare_gemm<MODE, ACT, 64, 1>();
-  return e;
-}
-
-template <int ACT>
-cudaError_t prepare_act() {
-  cudaError_t e = prepare_widths<FWD1, ACT>();
-  if (e == cudaSuccess) e = prepare_widths<FWD1G, ACT>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD1, ACT, 256, 2>();
-  if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128, 1>();
-  if (e == cudaSuccess) e = prepare_gemm<BWD1, ACT, ACT == 1 ? 256 : 128, 2>();
-  return e;
-}
-
 template <int PAIR>
 cudaError_t prepare_pair() {
-  cudaError_t e = prepare_gemm<DX, 0, 256, PAIR>();
-  if (e == cudaSuccess) e = prepare_gemm<DW1, 0, 256, PAIR>();
-  if (e == cudaSuccess) e = prepare_gemm<DW2, 0, 256, PAIR>();
+  cudaError_t e = prepare_gemm<FWD1, 0, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1, 1, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<BWD1, 0, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<BWD1, 1, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<DX, 0, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<DW1, 0, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<DW2, 0, PAIR>();
   return e;
 }
 
@@ -185,12 +172,10 @@ cusync_status_t prepare_device(int* sms) {
   }
   int n = 0;
   cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = prepare_act<0>();
-  if (e == cudaSuccess) e = prepare_act<1>();
-  if (e == cudaSuccess) e = prepare_widths<FWD2, 0>();
-  if (e == cudaSuccess) e = prepare_gemm<FWD2, 0, 256, 2>();
   if (e == cudaSuccess) e = prepare_pair<1>();
   if (e == cudaSuccess) e = prepare_pair<2>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1G, 0, 1>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD1G, 1, 1>();
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)plan_smem(CUSYNC_MOE_MAX_EXPERTS));
@@ -219,6 +204,25 @@ bool map_3d(CUtensorMap* m, const void* p, int64_t depth, int64_t rows, int64_t 
   return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// W1t of a gated layer with gate and up rows eight by eight: [E][N1/8][2][8][D], 64 of these
+// rows for each CTA's 64 columns of H.
+bool map_gated(CUtensorMap* m, const void* p, int64_t experts, int64_t n1, int64_t d) {
+  cuuint64_t dims[5] = {(cuuint64_t)d, 8, 2, (cuuint64_t)n1 / 8, (cuuint64_t)experts};
+  cuuint64_t strides[4] = {(cuuint64_t)d * 2, (cuuint64_t)(n1 * d) * 2, (cuuint64_t)(8 * d) * 2,
+                           (cuuint64_t)(2 * n1 * d) * 2};
+  cuuint32_t box[5] = {64, 8, 2, 8, 1};
+  cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(p), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Token rows by slot, in the four box heights.
+bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols) {
+  bool ok = true;
+  for (int i = 0; i < 4; ++i) ok = ok && map_2d(&m[i], p, rows, cols, 16u << i);
+  return ok;
 }
 
 // ----------------------------------------------------------------------------- launches
@@ -323,39 +327,24 @@ GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
   return a;
 }
 
-// row_tiles: an upper bound of the launch's tiles of 128 (PAIR = 2: 256) rows.
-template <int MODE, int ACT, int BN, int PAIR>
-cudaError_t launch_gemm(GemmArgs a, const Layer& L, int64_t row_tiles, int sms, cudaStream_t s) {
-  using C = GemmCfg<MODE, ACT, BN, PAIR>;
-  a.tiles = PAIR == 2 ? L.pairs : L.tiles;
-  a.col_tiles = (int32_t)div_up(a.N, C::kOutCols);
-  a.m_tiles = (int32_t)div_up(a.M, 128 * PAIR);
-  const int64_t tiles = C::kDw ? (int64_t)a.E * a.m_tiles * a.col_tiles : row_tiles * a.col_tiles;
+template <int MODE, int ACT, int PAIR>
+cudaError_t launch_gemm(GemmArgs a, const Layer& L, int sms, cudaStream_t s) {
+  using C = GemmCfg<MODE, ACT, PAIR>;
+  const bool wide = C::kCols == 256;
+  a.tiles = wide ? L.pairs : L.tiles;
+  a.m_tiles = (int32_t)div_up(a.M, C::kFeatures);
+  a.n_tiles = C::kDw ? (int32_t)div_up(a.N, C::kCols) : 1;
+  // an upper bound: how many tiles of rows there are is only known on the device
+  const int64_t tiles = (C::kDw ? (int64_t)a.E * a.n_tiles : wide ? L.max_pairs : L.S / kTileRows) * a.m_tiles;
   const int grid = PAIR * (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / PAIR));
-  return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, BN, PAIR>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
+  return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, PAIR>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
 }
-template <int MODE, int ACT, int BN>
+template <int MODE, int ACT>
 cudaError_t launch_gemm(bool pair, const GemmArgs& a, const Layer& L, int sms, cudaStream_t s) {
-  return pair ? launch_gemm<MODE, ACT, BN, 2>(a, L, L.max_pairs, sms, s)
-              : launch_gemm<MODE, ACT, BN, 1>(a, L, L.S / kTileRows, sms, s);
-}
-
-// Tile width of a forward product: the widest whose tiles fill the SMs twice over, counting
-// one row tile for every expert that can be active and one for every 128 assignments.
-int tile_width(int64_t row_tiles, int64_t cols256, int sms) {
-  if (row_tiles * cols256 >= 2 * sms) return 256;
-  if (row_tiles * cols256 * 2 >= 2 * sms) return 128;
-  return 64;
+  return pair ? launch_gemm<MODE, ACT, 2>(a, L, sms, s) : launch_gemm<MODE, ACT, 1>(a, L, sms, s);
 }
 
 bool use_pairs(const Layer& L, int sms) { return L.A >= kPairRows * L.E && sms >= 2; }
-
-template <int MODE, int ACT>
-cudaError_t launch_fwd(const GemmArgs& a, const Layer& L, int bn, int64_t row_tiles, int sms, cudaStream_t s) {
-  if (bn == 256) return launch_gemm<MODE, ACT, 256, 1>(a, L, row_tiles, sms, s);
-  if (bn == 128) return launch_gemm<MODE, ACT, 128, 1>(a, L, row_tiles, sms, s);
-  return launch_gemm<MODE, ACT, 64, 1>(a, L, row_tiles, sms, s);
-}
 
 cudaError_t launch_dispatch(const Layer& L, void* work, const void* x, void* xs, const void* y, void* ys, int sms,
                             cudaStream_t s) {
@@ -386,6 +375,7 @@ cudaError_t launch_combine(const Layer& L, void* work, const float* rows, const 
   c.k = L.k;
   c.D = (int32_t)L.D;
   c.parts = L.parts;
+  c.used = (int32_t)div_up(L.N1, 32);
   return launch(combine_kernel, dim3((unsigned)L.T, (unsigned)div_up(L.D, 4 * kCombineThreads)), kCombineThreads, 0, s,
                 c);
 }
@@ -491,35 +481,28 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   }
   cudaError_t e = launch_plan(L, ids, work, s);
   if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
-  const int64_t row_tiles = std::min<int64_t>(L.S / kTileRows, std::min<int64_t>(L.E, L.A) + L.A / kTileRows);
   const bool gather = L.A <= kGatherRows * L.E, pair = use_pairs(L, sms);
-  const int bn1 = pair ? 256 : tile_width(row_tiles, div_up(L.N1, 256 / L.G), sms);
-  const int bn2 = pair ? 256 : tile_width(row_tiles, div_up(L.D, 256), sms);
   GemmArgs a = gemm_args(L, work, weights);
-  a.N = (int32_t)L.N1;
+  a.M = (int32_t)L.N1;
   a.K = (int32_t)L.D;
   a.out = w + L.h;
   GemmArgs b = gemm_args(L, work, weights);
-  b.N = (int32_t)L.D;
+  b.M = (int32_t)L.D;
   b.K = (int32_t)L.N1;
   b.out = w + L.rows;
-  const int box_a = pair ? 128 : 32;
-  if (!(gather ? map_2d(&a.mA, X, L.T, L.D, 1) : map_2d(&a.mA, w + L.x, L.S, L.D, box_a)) ||
-      !map_3d(&a.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, pair ? 128 : bn1 / L.G) ||
-      !map_2d(&b.mA, w + L.h, L.S, L.N1, box_a) || !map_3d(&b.mB, W2t, L.E, L.D, L.N1, pair ? 128 : bn2))
+  if (!(L.G == 2 ? map_gated(&a.mA, W1t, L.E, L.N1, L.D) : map_3d(&a.mA, W1t, L.E, L.N1, L.D, 128)) ||
+      !(gather ? map_2d(&a.mB[0], X, L.T, L.D, 1) : map_tokens(a.mB, w + L.x, L.S, L.D)) ||
+      !map_3d(&b.mA, W2t, L.E, L.D, L.N1, 128) || !map_tokens(b.mB, w + L.h, L.S, L.N1))
     return CUSYNC_ERR_CUDA;
   if (gather) {
-    e = L.G == 2 ? launch_fwd<FWD1G, 1>(a, L, bn1, row_tiles, sms, s) : launch_fwd<FWD1G, 0>(a, L, bn1, row_tiles, sms, s);
+    for (int i = 1; i < 4; ++i) a.mB[i] = a.mB[0];
+    e = L.G == 2 ? launch_gemm<FWD1G, 1, 1>(a, L, sms, s) : launch_gemm<FWD1G, 0, 1>(a, L, sms, s);
   } else {
     e = launch_dispatch(L, work, X, w + L.x, nullptr, nullptr, sms, s);
-    if (e == cudaSuccess && pair)
-      e = L.G == 2 ? launch_gemm<FWD1, 1, 256, 2>(a, L, L.max_pairs, sms, s)
-                   : launch_gemm<FWD1, 0, 256, 2>(a, L, L.max_pairs, sms, s);
-    else if (e == cudaSuccess)
-      e = L.G == 2 ? launch_fwd<FWD1, 1>(a, L, bn1, row_tiles, sms, s) : launch_fwd<FWD1, 0>(a, L, bn1, row_tiles, sms, s);
+    if (e == cudaSuccess)
+      e = L.G == 2 ? launch_gemm<FWD1, 1>(pair, a, L, sms, s) : launch_gemm<FWD1, 0>(pair, a, L, sms, s);
   }
-  if (e == cudaSuccess)
-    e = pair ? launch_gemm<FWD2, 0, 256, 2>(b, L, L.max_pairs, sms, s) : launch_fwd<FWD2, 0>(b, L, bn2, row_tiles, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<FWD2, 0>(pair, b, L, sms, s);
   if (e == cudaSuccess)
     e = launch_combine(L, work, reinterpret_cast<float*>(w + L.rows), weights, Y, nullptr, nullptr, s);
   return status_of(e);
@@ -551,13 +534,14 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   float *rows = reinterpret_cast<float*>(w + L.grows), *part = reinterpret_cast<float*>(w + L.gpart);
 
   GemmArgs p = gemm_args(L, work, weights);  // hidden layer and its gradient
-  p.N = (int32_t)L.N1;
+  p.M = (int32_t)L.N1;
   p.K = (int32_t)L.D;
   p.out = gz;
   p.out2 = gh;
   p.part = part;
+  p.parts = L.parts;
   GemmArgs x = gemm_args(L, work, weights);  // dX per slot
-  x.N = (int32_t)L.D;
+  x.M = (int32_t)L.D;
   x.K = (int32_t)H;
   x.out = rows;
   GemmArgs w1 = gemm_args(L, work, weights);
@@ -568,20 +552,24 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   w2.M = (int32_t)L.D;
   w2.N = (int32_t)L.N1;
   w2.out = dW2t;
-  if (!map_2d(&p.mA, gx, L.S, L.D, 128) || !map_2d(&p.mA2, gy, L.S, L.D, 128) ||
-      !map_3d(&p.mB, W1t, (int64_t)L.E * L.G, L.N1, L.D, pair && L.G == 1 ? 64 : 128) || !map_3d(&p.mB2, W2t, L.E, L.D, L.N1, 64) ||
-      !map_2d(&x.mA, gz, L.S, H, pair ? 128 : 32) || !map_3d(&x.mB, W1t, L.E, H, L.D, 64) ||
-      !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB, gx, L.S, L.D, 64) ||
-      !map_2d(&w2.mA, gy, L.S, L.D, 64) || !map_2d(&w2.mB, gh, L.S, L.N1, 64))
+  if (!map_3d(&p.mA, W1t, (int64_t)L.E * L.G, L.N1, L.D, 128) || !map_3d(&p.mA2, W2t, L.E, L.D, L.N1, 64) ||
+      !map_tokens(p.mB, gx, L.S, L.D) || !map_tokens(p.mB2, gy, L.S, L.D) ||
+      !map_3d(&x.mA, W1t, L.E, H, L.D, 64) || !map_tokens(x.mB, gz, L.S, H) ||
+      !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB[0], gx, L.S, L.D, 64) ||
+      !map_2d(&w2.mA, gy, L.S, L.D, 64) || !map_2d(&w2.mB[0], gh, L.S, L.N1, 64))
     return CUSYNC_ERR_CUDA;
+  for (int i = 1; i < 4; ++i) {
+    w1.mB[i] = w1.mB[0];
+    w2.mB[i] = w2.mB[0];
+  }
   cudaError_t e = launch_plan(L, ids, work, s);
   if (e == cudaSuccess) e = launch_dispatch(L, work, X, gx, dY, gy, sms, s);
   if (e == cudaSuccess)
-    e = L.G == 2 ? launch_gemm<BWD1, 1, 256>(pair, p, L, sms, s) : launch_gemm<BWD1, 0, 128>(pair, p, L, sms, s);
-  if (e == cudaSuccess) e = launch_gemm<DX, 0, 256>(pair, x, L, sms, s);
+    e = L.G == 2 ? launch_gemm<BWD1, 1>(pair, p, L, sms, s) : launch_gemm<BWD1, 0>(pair, p, L, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DX, 0>(pair, x, L, sms, s);
   if (e == cudaSuccess) e = launch_combine(L, work, rows, nullptr, dX, part, dweights, s);
-  if (e == cudaSuccess) e = launch_gemm<DW1, 0, 256>(pair1, w1, L, sms, s);
-  if (e == cudaSuccess) e = launch_gemm<DW2, 0, 256>(pair2, w2, L, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DW1, 0>(pair1, w1, L, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DW2, 0>(pair2, w2, L, sms, s);
   return status_of(e);
 }
 

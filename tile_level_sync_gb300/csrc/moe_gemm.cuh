@@ -1,39 +1,41 @@
 // The products of an expert layer: one persistent tcgen05 kernel per product.
 //
-// A tile is 128 rows of one expert (the plan aligns an expert's rows to 128) x BN columns,
-// or, for a weight gradient, 128 x BN of one expert's matrix.  With PAIR = 2 a pair of CTAs
-// (cta_group::2) computes 256 rows: each holds its 128 rows of A and half of B's columns,
-// so that a 128 x 256 x 64 block costs an SM 32 KB of loads, not 48 KB.  One CTA per SM
-// walks its tiles with a fixed stride:
-//   warp 0     copies: TMA boxes of the weights and of the slot-ordered rows.
-//   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma (fp32
-//              accumulators).
-//   warps 2-9  epilogue: two warps per TMEM lane quarter, a thread per row.
+// Products over slots (tokens in dispatch order) are computed transposed: the MMA's 128
+// rows (256 across a pair of CTAs, cta_group::2) are columns of the expert's weights, its
+// columns are the tile's tokens.  The width then follows the expert's rows in steps of 16 (32),
+// where tiles of 128 or 256 token rows would be filled up with rows that count for nothing
+// (4096 tokens x 8 of 64 experts: a quarter of the work), and a lane of the accumulator is
+// an output column, so that a warp stores 32 neighbours of a token's row at once.
+//
+//   mode   A (M)                      B (N)                  epilogue
+//   FWD1   W1t[e] rows (G * N1)       X by slot              h = act(z), bf16
+//   FWD1G  the same                   X (gather)
+//   FWD2   W2t[e] rows (D)            H                      O, fp32
+//   BWD1   W1t[e] gate, up;           X; dY by slot          dZ and w h, bf16; sums of dH h
+//          W2t[e] along N1
+//   DX     W1t[e] along D             dZ                     dX per slot, fp32
+//   DW1    dZ along G * N1            X along D              dW1t[e], bf16   (K = slots)
+//   DW2    dY along D                 w h along N1           dW2t[e], bf16   (K = slots)
+//
+// "along": the operand is stored with its M (or N) index contiguous rather than K, and the
+// MMA reads it that way, so nothing is ever transposed in memory.  FWD1's SwiGLU tile
+// takes gate and up rows of W1t eight by eight (one 5-D box): a gate lane and the lane
+// eight further hold the two factors of one h.  BWD1 has them in accumulators of their own.
+//
+// One CTA per SM walks its tiles with a fixed stride:
+//   warp 0     copies of A, warp 10 copies of B (TMA boxes; FWD1G: tile::gather4, four
+//              rows a copy, through the plan's row indices).
+//   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma.
+//   warps 2-9  epilogue: two warps per TMEM lane quarter, every other 32 columns each.
 // Accumulators are double-buffered where two fit in TMEM's 512 columns.
 //
-//   mode   rows x columns          A            B                       epilogue
-//   FWD1   slots x N1              X by slot    W1t[e]                  h = act(z), bf16
-//   FWD1G  the same                X (gather)
-//   FWD2   slots x D               H            W2t[e]                  O, fp32
-//   BWD1   slots x N1              X, dY        W1t[e]; W2t[e] along N  z and dH = dY W2 side by
-//                                                                       side: dZ and w h (bf16),
-//                                                                       partial sums of dH h
-//   DX     slots x D               dZ           W1t[e] along N          dX per slot, fp32
-//   DW1    G*N1 x D (per expert)   dZ along M   X along N               bf16
-//   DW2    D x N1 (per expert)     dY along M   w H along N             bf16
+// X by slot is a copy in dispatch order (dispatch_kernel).  The gather needs none, but
+// brings 128 rows x 64 columns in 1.25 us, more than twice what their MMAs take: it is for
+// tiles of few rows.
 //
-// "along M/N": the operand is stored with that index contiguous rather than K, and the MMA
-// reads it that way (instruction and shared-memory descriptors), so no operand is ever
-// transposed in memory.
-//
-// X by slot: a copy in slot order (dispatch_kernel).  The gather (tile::gather4, four rows a
-// copy through the plan's row indices) needs no such copy, but brings 128 rows x 64 columns
-// in 1.25 us, three times what the MMAs of a 128 x 256 x 64 block take (first product of
-// 4096 tokens x 8 of 64 experts, D = 2048, N1 = 1024: 609 us): it is for tiles of few rows.
-//
-// A row behind an expert's last one gets no store in the forward pass; its accumulator
-// rows hold whatever the ring held, and rows do not mix.  In the weight gradients K runs
-// over slots: there dispatch_kernel and BWD1 stored zeros for such rows.
+// Token rows behind an expert's last one are columns of their own and are not stored.  In
+// the weight gradients K runs over slots in steps of 16: dispatch_kernel and BWD1 store
+// zeros up to the step's end.
 //
 // Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
 #pragma once
@@ -51,53 +53,62 @@ namespace moe {
 enum : int { FWD1 = 0, FWD2 = 1, BWD1 = 2, DX = 3, DW1 = 4, DW2 = 5, FWD1G = 6 };
 
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kGemmThreads = 320;
-constexpr uint32_t kErrWait = 3u << 24;  // the pipeline-wait class of the chain kernel's error words
+constexpr int kGemmThreads = 352;
+constexpr int kRowStep = 16;                 // slots up to a multiple of which a row's zeros are stored
+constexpr uint32_t kErrWait = 3u << 24;      // the pipeline-wait class of the chain kernel's error words
 
 struct GemmArgs {
-  CUtensorMap mA;    // X, H, dZ or dY
-  CUtensorMap mA2;   // BWD1: dY
-  CUtensorMap mB;    // W1t, W2t, X or w H
-  CUtensorMap mB2;   // BWD1: W2t
+  CUtensorMap mA;      // weights; DW: dZ or dY
+  CUtensorMap mA2;     // BWD1: W2t
+  CUtensorMap mB[4];   // tokens, boxes of 16, 32, 64 and 128 rows (gather: [0], one row); DW: [0], 64 rows
+  CUtensorMap mB2[4];  // BWD1: dY
   int32_t* plan;
   const float* weights;
-  void* out;         // H, O, dZ, dX per slot, dW1t or dW2t
-  void* out2;        // BWD1: w H
-  float* part;       // BWD1: partial sums of dH h, [slot][2 * column tiles]
+  void* out;           // H, O, dZ, dX per slot, dW1t or dW2t
+  void* out2;          // BWD1: w H
+  float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
   int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
   int32_t T, k, E;
-  int32_t M;         // DW: rows of an expert's matrix
-  int32_t N;         // output columns (FWD1, BWD1: N1)
-  int32_t K;         // reduction length (DW: the expert's rows)
-  int32_t col_tiles, m_tiles;
+  int32_t M;           // output columns (DW: rows of an expert's matrix)
+  int32_t N;           // DW: output columns
+  int32_t K;           // reduction length (not DW)
+  int32_t m_tiles, n_tiles, parts;
 };
 
-template <int MODE, int ACT, int BN, int PAIR>
+template <int MODE, int ACT, int PAIR>
 struct GemmCfg {
   static constexpr bool kDw = MODE == DW1 || MODE == DW2;
   static constexpr bool kBwd1 = MODE == BWD1;
   static constexpr bool kFwd1 = MODE == FWD1 || MODE == FWD1G;
   static constexpr bool kGather = MODE == FWD1G;
-  static constexpr bool kPairB = ACT == 1 && (kFwd1 || kBwd1);  // gate and up columns in one tile
-  static constexpr bool kMnA = kDw;
-  static constexpr bool kMnB = kDw || MODE == DX;
-  static constexpr int kOutCols = kPairB ? BN / 2 : BN;  // output columns of a tile
+  static constexpr bool kGated = ACT == 1 && kFwd1;        // gate and up rows eight by eight
+  static constexpr bool kMnA = kDw || MODE == DX;
+  static constexpr int kG = ACT == 1 ? 2 : 1;
+  static constexpr int kAParts = kBwd1 ? kG + 1 : 1;       // 128 x 64 blocks of A in a stage
+  static constexpr int kBParts = kBwd1 ? 2 : 1;
+  static constexpr int kCols = kDw ? 256 : (PAIR == 2 && !kBwd1) ? 256 : 128;  // widest tile
+  static constexpr int kColStep = 16 * PAIR;               // of the MMA's width
+  static constexpr int kBBytes = kCols / PAIR * 128;       // a CTA's share of B
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = BN / PAIR * 128;
-  static constexpr int kD2 = kBwd1 ? kOutCols : 0;       // columns of BWD1's second accumulator
-  static constexpr int kStageBytes = kABytes + kBBytes + (kBwd1 ? kABytes + kD2 / PAIR * 128 : 0);
-  static constexpr int kRing = 192 * 1024;
-  static constexpr int kStageOut = 8 * 4096;              // epilogue: 32 rows of 128 bytes for each warp
+  static constexpr int kBlockBytes = kAParts * kABytes + kBParts * kBBytes;  // 64 k
+  static constexpr int kKps = kBlockBytes <= 32 * 1024 ? 2 : 1;              // blocks of 64 k in a stage
+  static constexpr int kStageBytes = kKps * kBlockBytes;
+  static constexpr int kRing = (kDw ? 192 : 224) * 1024;
   static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
-  static constexpr int kAccCols = BN + kD2;
+  static constexpr int kStageOut = kDw ? 8 * 4096 : 0;     // DW epilogue: 32 rows of 128 bytes a warp
+  static constexpr int kAccCols = kAParts * kCols;
   static constexpr int kAccs = 2 * kAccCols <= 512 ? 2 : 1;
-  static constexpr int kTmemCols = kAccs * kAccCols <= 128 ? 128 : kAccs * kAccCols <= 256 ? 256 : 512;
+  static constexpr int kTmemCols = kAccs * kAccCols <= 256 ? 256 : 512;
+  static constexpr int kFeatures = (kGated ? 64 : 128) * PAIR;  // output columns of a tile (DW: rows)
   static constexpr int kSmemBytes = kStages * kStageBytes + kStageOut + 1024;
 };
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void store_bf16(uint16_t* p, float v) {
+  *p = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 // 1 / (1 + e^-x); the fast exponential and division are within a few 1e-7 of it
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
@@ -108,38 +119,39 @@ __device__ __forceinline__ float gelu_gate(float z) {
   return sigmoid_fast(2.0f * kGeluC * (z + 0.044715f * z * z * z));
 }
 
-// One tile of a launch.
+// One tile of a launch: `rows` tokens of expert e from slot0 on (DW: all of the expert's),
+// output columns (DW: matrix rows) from m0 on, DW: columns from n0 on; nkb blocks of 64 k.
 struct Tile {
   int32_t e, slot0, rows, m0, n0, nkb;
 };
 
-template <int MODE, int ACT, int BN, int PAIR>
+template <int MODE, int ACT, int PAIR>
 __device__ __forceinline__ int32_t tile_total(const GemmArgs& a) {
-  if (GemmCfg<MODE, ACT, BN, PAIR>::kDw) return a.E * a.m_tiles * a.col_tiles;
-  return a.plan[PAIR == 2 ? PLAN_PAIRS : PLAN_TILES] * a.col_tiles;
+  if (GemmCfg<MODE, ACT, PAIR>::kDw) return a.E * a.m_tiles * a.n_tiles;
+  return a.plan[GemmCfg<MODE, ACT, PAIR>::kCols == 256 ? PLAN_PAIRS : PLAN_TILES] * a.m_tiles;
 }
 
-template <int MODE, int ACT, int BN, int PAIR>
+template <int MODE, int ACT, int PAIR>
 __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
-  using C = GemmCfg<MODE, ACT, BN, PAIR>;
+  using C = GemmCfg<MODE, ACT, PAIR>;
   Tile r;
   if (C::kDw) {
-    const int32_t per = a.m_tiles * a.col_tiles;
+    const int32_t per = a.m_tiles * a.n_tiles;
     r.e = t / per;
     const int32_t q = t - r.e * per;
-    r.m0 = (q % a.m_tiles) * (128 * PAIR);
-    r.n0 = (q / a.m_tiles) * BN;
+    r.m0 = (q % a.m_tiles) * C::kFeatures;
+    r.n0 = (q / a.m_tiles) * C::kCols;
     r.slot0 = a.plan[a.offsets + r.e];
     r.rows = a.plan[a.counts + r.e];
     r.nkb = (r.rows + 63) / 64;
   } else {
-    const int32_t rt = t / a.col_tiles;
+    const int32_t rt = t / a.m_tiles;
     const int4 er = *reinterpret_cast<const int4*>(a.plan + a.tiles + 4 * rt);
     r.e = er.x;
     r.slot0 = er.y;
     r.rows = er.z;
-    r.m0 = 0;
-    r.n0 = (t - rt * a.col_tiles) * C::kOutCols;
+    r.m0 = (t - rt * a.m_tiles) * C::kFeatures;
+    r.n0 = 0;
     r.nkb = (a.K + 63) / 64;
   }
   return r;
@@ -147,51 +159,61 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
 
 // A CTA's tiles, read one ahead: the plan's entry of a tile is a trip to L2 that no role
 // should wait for between two tiles.
-template <int MODE, int ACT, int BN, int PAIR>
+template <int MODE, int ACT, int PAIR>
 struct Walk {
   const GemmArgs& a;
   const int32_t total;
   int32_t t;
   Tile next;
   __device__ __forceinline__ Walk(const GemmArgs& args, int32_t n) : a(args), total(n), t(blockIdx.x / PAIR) {
-    if (t < total) next = tile_at<MODE, ACT, BN, PAIR>(a, t);
+    if (t < total) next = tile_at<MODE, ACT, PAIR>(a, t);
   }
   __device__ __forceinline__ bool take(Tile& q) {
     if (t >= total) return false;
     q = next;
     t += gridDim.x / PAIR;
-    if (t < total) next = tile_at<MODE, ACT, BN, PAIR>(a, t);
+    if (t < total) next = tile_at<MODE, ACT, PAIR>(a, t);
     return true;
   }
 };
 
-// 32 rows x 128 bytes, staged in shared memory (16-byte pieces, swizzled so that neither
-// side conflicts) and stored as whole 128-byte rows, four to an instruction.  `mine` is this
-// lane's row; row r of the warp goes to out + r * pitch when r < rows, its 16-byte pieces
-// below `pieces`.
-template <int PIECES>
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine)[4 * PIECES], uint8_t* out,
-                                           int64_t pitch, int rows, int pieces, int lane) {
-  constexpr int kRowsEach = 32 / PIECES;
+// 32 rows x 64 bytes, staged in shared memory (16-byte pieces, swizzled so that neither
+// side conflicts) and stored eight rows to an instruction.  `mine` is this lane's row; row
+// r of the warp goes to out + r * pitch when r < rows, its 16-byte pieces below `pieces`.
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine)[16], uint8_t* out, int64_t pitch,
+                                           int rows, int pieces, int lane) {
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i)
-    *reinterpret_cast<uint4*>(stage + lane * (16 * PIECES) + ((i ^ (lane * PIECES / 8)) & (PIECES - 1)) * 16) =
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane / 2)) & 3) * 16) =
         make_uint4(mine[4 * i], mine[4 * i + 1], mine[4 * i + 2], mine[4 * i + 3]);
   __syncwarp();
-  const int piece = lane % PIECES;
+  const int piece = lane % 4;
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) {
-    const int r = i * kRowsEach + lane / PIECES;
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * (16 * PIECES) +
-                                                    ((piece ^ (r * PIECES / 8)) & (PIECES - 1)) * 16);
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + lane / 4;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ (r / 2)) & 3) * 16);
     if (r < rows && piece < pieces) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = v;
   }
 }
 
-template <int MODE, int ACT, int BN, int PAIR>
+// Sums over the warp's lanes of 32 values: lane i ends with the sum of v[i].
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+template <int MODE, int ACT, int PAIR>
 __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_constant__ GemmArgs a) {
-  using C = GemmCfg<MODE, ACT, BN, PAIR>;
+  using C = GemmCfg<MODE, ACT, PAIR>;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
@@ -213,11 +235,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     ptx::mbar_init_fence();
     abort_flag = 0;
     ptx::prefetch_tmap(&a.mA);
-    ptx::prefetch_tmap(&a.mB);
-    if (C::kBwd1) {
-      ptx::prefetch_tmap(&a.mA2);
-      ptx::prefetch_tmap(&a.mB2);
-    }
   }
   if (warp == 1) {
     if (PAIR == 2) {
@@ -235,87 +252,91 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   const uint32_t tmem = tmem_slot;
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  Walk<MODE, ACT, BN, PAIR> walk(a, tile_total<MODE, ACT, BN, PAIR>(a));
+  Walk<MODE, ACT, PAIR> walk(a, tile_total<MODE, ACT, PAIR>(a));
   Tile q;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 10) {
     // ------------------------------------------------------------ copies
-    const uint64_t keep = ptx::l2_policy_evict_last(), stream = ptx::l2_policy_evict_normal();
+    const bool copies_a = warp == 0;
+    const uint64_t pol = ptx::l2_policy_evict_normal();
     uint32_t it = 0, st = 0, par = 1;
     const uint32_t full0 = PAIR == 2 ? ptx::mapa(&full[0], 0) : 0;
     while (!abort_flag && walk.take(q)) {
+      // this CTA's share of the tile's tokens, and the box that covers it
+      const int cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
+      const int share = cols / PAIR;
+      const int pick = share <= 16 ? 0 : share <= 32 ? 1 : share <= 64 ? 2 : 3;
+      const CUtensorMap *mb = &a.mB[pick], *mb2 = &a.mB2[pick];
+      const int32_t slot = q.slot0 + rank * share;
+      const int32_t m0 = q.m0 + rank * (C::kFeatures / PAIR), n0 = q.n0 + rank * (C::kCols / PAIR);
       // a lane's four gathered rows, as token indices; -1 (a slot behind the last row)
       // becomes T, outside the tensor, read as zero
+      const int live = C::kGather ? (q.rows + 3) / 4 : 0;
       int4 tok = make_int4(a.T, a.T, a.T, a.T);
-      if (C::kGather && 4 * lane < q.rows) {
+      if (C::kGather && !copies_a && lane < live) {
         const int4 r = *reinterpret_cast<const int4*>(a.plan + a.row_of + q.slot0 + 4 * lane);
         auto token = [&](int32_t x) { return x < 0 ? a.T : x / a.k; };
         tok = make_int4(token(r.x), token(r.y), token(r.z), token(r.w));
       }
-      const int live = (q.rows + 3) / 4;           // lanes whose rows a gathered tile needs
-      // this CTA's rows and columns of the tile
-      const int32_t slot = q.slot0 + (C::kDw ? 0 : 128 * rank), m0 = q.m0 + 128 * rank;
-      const int boxes = C::kDw ? 0 : (q.rows - 128 * rank + 31) / 32;  // 32-row boxes of A
-      const int32_t nb = q.n0 + (C::kPairB ? 0 : rank * (BN / 2)), n2 = q.n0 + rank * (C::kD2 / 2);
-      uint32_t bytes = PAIR * (C::kBBytes + (C::kBwd1 ? C::kD2 / PAIR * 128 : 0));
-      if (C::kGather) bytes += live * 512;
-      else if (C::kDw) bytes += PAIR * C::kABytes;
-      else if (PAIR == 2 || C::kBwd1) bytes += (C::kBwd1 ? 2 : 1) * (q.rows > 128 ? 2 : 1) * C::kABytes;
-      else bytes += boxes * 4096;
+      const uint32_t block_bytes =
+          PAIR * (C::kAParts * C::kABytes +
+                  C::kBParts * (C::kGather ? live * 512 : C::kDw ? C::kBBytes : (16 << pick) * 128));
       bool ok = true;
-      // Every lane waits for the slot and issues its own copies: nothing orders the lanes,
-      // since the barrier's phase cannot end before lane 0's arrival.
-      for (int kb = 0; kb < q.nkb; ++kb, ++it) {
+      // Every lane waits for the slot and issues its own copies: nothing orders the lanes or
+      // the two warps, since the barrier's phase cannot end before warp 0's arrival.
+      for (int kb0 = 0; kb0 < q.nkb; kb0 += C::kKps, ++it) {
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
-        uint8_t* sA = ring + st * C::kStageBytes;
-        uint8_t* sB = sA + C::kABytes;
-        uint8_t* sA2 = sB + C::kBBytes;
-        uint8_t* sB2 = sA2 + C::kABytes;
+        uint8_t* stage = ring + st * C::kStageBytes;
         uint64_t* bar = &full[st];
         // in a pair both CTAs' copies complete on the first one's barrier
         const uint32_t bar0 = full0 + 8 * st;
-        auto load2 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1, uint64_t pol) {
+        auto load2 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1) {
           if (PAIR == 2) ptx::tma_load_2d_to_leader(dst, m, bar0, c0, c1, pol);
           else ptx::tma_load_2d(dst, m, bar, c0, c1, pol);
         };
-        auto load3 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2, uint64_t pol) {
+        auto load3 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2) {
           if (PAIR == 2) ptx::tma_load_3d_to_leader(dst, m, bar0, c0, c1, c2, pol);
           else ptx::tma_load_3d(dst, m, bar, c0, c1, c2, pol);
         };
-        if (lane == 0 && rank == 0) ptx::mbar_arrive_expect_tx(bar, bytes);
+        auto load5 = [&](void* dst, const CUtensorMap* m, int32_t c0, int32_t c3, int32_t c4) {
+          if (PAIR == 2) ptx::tma_load_5d_to_leader(dst, m, bar0, c0, 0, 0, c3, c4, pol);
+          else ptx::tma_load_5d(dst, m, bar, c0, 0, 0, c3, c4, pol);
+        };
         if (++st == C::kStages) {
           st = 0;
           par ^= 1;
         }
-        const int32_t kc = kb * 64;
-        // A
-        if (C::kGather) {
-          if (lane < live) ptx::tma_gather4(sA + lane * 512, &a.mA, bar, kc, tok, keep);
-        } else if (C::kDw) {
-          if (lane < 2) load2(sA + lane * 8192, &a.mA, m0 + 64 * lane, slot + kc, keep);
-        } else if (PAIR == 2 || C::kBwd1) {
-          if (lane == 1 && boxes > 0) load2(sA, &a.mA, kc, slot, keep);
-          if (C::kBwd1 && lane == 2 && boxes > 0) load2(sA2, &a.mA2, kc, slot, keep);
-        } else {
-          if (lane < boxes) load2(sA + lane * 4096, &a.mA, kc, slot + 32 * lane, keep);
-        }
-        // B: this CTA's columns
-        if (C::kDw) {
-          if (lane < BN / PAIR / 64) load2(sB + lane * 8192, &a.mB, nb + 64 * lane, slot + kc, keep);
-        } else if (MODE == DX) {
-          if (lane < BN / PAIR / 64) load3(sB + lane * 8192, &a.mB, nb + 64 * lane, kc, q.e, stream);
-        } else if (lane == 0) {
-          if (!C::kPairB) {
-            load3(sB, &a.mB, kc, nb, q.e, stream);
-          } else if (PAIR == 2) {
-            load3(sB, &a.mB, kc, nb, 2 * q.e + rank, stream);  // gate columns; up columns
-          } else {
-            load3(sB, &a.mB, kc, nb, 2 * q.e, stream);
-            load3(sB + C::kBBytes / 2, &a.mB, kc, nb, 2 * q.e + 1, stream);
+        const int blocks = min(C::kKps, q.nkb - kb0);
+        if (copies_a && lane == 0 && rank == 0) ptx::mbar_arrive_expect_tx(bar, blocks * block_bytes);
+#pragma unroll
+        for (int b = 0; b < C::kKps; ++b) {
+        if (b >= blocks) break;
+        uint8_t* sA = stage + b * C::kBlockBytes;
+        uint8_t* sB = sA + C::kAParts * C::kABytes;
+        const int32_t kc = (kb0 + b) * 64;
+        if (copies_a) {
+          if (C::kDw) {
+            if (lane < 2) load2(sA + lane * 8192, &a.mA, m0 + 64 * lane, q.slot0 + kc);
+          } else if (C::kGated) {
+            if (lane == 0) load5(sA, &a.mA, kc, m0 / 8, q.e);
+          } else if (C::kBwd1) {
+            if (lane < C::kG) load3(sA + lane * C::kABytes, &a.mA, kc, m0, C::kG * q.e + lane);
+            else if (lane < C::kG + 2)
+              load3(sA + C::kG * C::kABytes + (lane - C::kG) * 8192, &a.mA2, m0 + 64 * (lane - C::kG), kc, q.e);
+          } else if (MODE == DX) {
+            if (lane < 2) load3(sA + lane * 8192, &a.mA, m0 + 64 * lane, kc, q.e);
+          } else if (lane == 0) {
+            load3(sA, &a.mA, kc, m0, q.e);
           }
+        } else if (C::kDw) {
+          if (lane < C::kCols / PAIR / 64) load2(sB + lane * 8192, mb, n0 + 64 * lane, q.slot0 + kc);
+        } else if (C::kGather) {
+          if (lane < live) ptx::tma_gather4(sB + lane * 512, mb, bar, kc, tok, pol);
+        } else if (lane < C::kBParts) {
+          load2(sB + lane * C::kBBytes, lane ? mb2 : mb, kc, slot);
         }
-        if (C::kBwd1 && lane < C::kD2 / PAIR / 64) load3(sB2 + lane * 8192, &a.mB2, n2 + 64 * lane, kc, q.e, stream);
+        }
       }
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) {
@@ -326,16 +347,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       }
     }
     __syncwarp();
-    // after an abort: wait, bounded, for the copies still in flight
-    if (abort_flag && lane == 0 && rank == 0)
+    // after an abort: wait, bounded, for the copies still in flight (both warps' complete on `full`)
+    if (abort_flag && copies_a && lane == 0 && rank == 0)
       for (uint32_t i = it > (uint32_t)C::kStages ? it - C::kStages : 0; i < it; ++i)
         ptx::mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     if (lane == 0 && rank == 0) {
-      constexpr uint32_t majors = (C::kMnA ? ptx::kIdescAMn : 0) | (C::kMnB ? ptx::kIdescBMn : 0);
-      constexpr uint32_t idesc = ptx::idesc_bf16_f32(128 * PAIR, BN) | majors;
-      constexpr uint32_t idesc2 = ptx::idesc_bf16_f32(128 * PAIR, C::kBwd1 ? C::kD2 : BN) | ptx::kIdescBMn;
       auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t more) {
         if (PAIR == 2) ptx::umma_bf16_pair(d, da, db, id, more);
         else ptx::umma_bf16(d, da, db, id, more);
@@ -348,6 +366,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       bool ok = true;
       while (ok && !abort_flag && walk.take(q)) {
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
+        const uint32_t cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
+        const uint32_t idesc = ptx::idesc_bf16_f32(128 * PAIR, cols) | (C::kMnA ? ptx::kIdescAMn : 0) |
+                               (C::kDw ? ptx::kIdescBMn : 0);
         const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
         ++acc;
         ok = (PAIR == 2 ? ptx::mbar_wait_bounded_cluster(&tempty[buf], (use & 1) ^ 1, kWaitNs)
@@ -356,23 +377,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * C::kAccCols;
-        for (int kb = 0; kb < q.nkb; ++kb) {
+        for (int kb0 = 0; kb0 < q.nkb; kb0 += C::kKps) {
           ok = ptx::mbar_wait_bounded(&full[st], par, kWaitNs);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t sA = ptx::smem_u32(ring + st * C::kStageBytes);
-          const uint32_t sB = sA + C::kABytes, sA2 = sB + C::kBBytes, sB2 = sA2 + C::kABytes;
-          // 16 k: 32 bytes of a K-contiguous row, or 16 rows of 128 bytes
-          constexpr uint64_t stepA = C::kMnA ? 2048 >> 4 : 32 >> 4, stepB = C::kMnB ? 2048 >> 4 : 32 >> 4;
-          const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
-          const uint64_t dB = C::kMnB ? ptx::smem_desc_mn128(sB) : ptx::smem_desc_k128(sB);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) mma(d, dA + s * stepA, dB + s * stepB, idesc, kb || s);
-          if (C::kBwd1) {
-            const uint64_t dA2 = ptx::smem_desc_k128(sA2), dB2 = ptx::smem_desc_mn128(sB2);
+          for (int b = 0; b < C::kKps; ++b) {
+            const int kb = kb0 + b;
+            const uint32_t sA = ptx::smem_u32(ring + st * C::kStageBytes + b * C::kBlockBytes);
+            const uint32_t sB = sA + C::kAParts * C::kABytes;
+            // 16 k: 32 bytes of a K-contiguous row, or 16 rows of 128 bytes
+            constexpr uint64_t mn = 2048 >> 4, kk = 32 >> 4;
+            const uint64_t dB = C::kDw ? ptx::smem_desc_mn128(sB) : ptx::smem_desc_k128(sB);
+            // the last block's steps of 16: only those that hold k (DW: rows; elsewhere columns)
+            const int left = (C::kDw ? q.rows : a.K) - kb * 64;
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma(d + BN, dA2 + s * (32 >> 4), dB2 + s * (2048 >> 4), idesc2, kb || s);
+            for (int s = 0; s < 4; ++s) {
+              if (16 * s >= left) break;
+              if (C::kBwd1) {
+#pragma unroll
+                for (int p = 0; p < C::kG; ++p)
+                  mma(d + p * C::kCols, ptx::smem_desc_k128(sA + p * C::kABytes) + s * kk, dB + s * kk, idesc, kb || s);
+                mma(d + C::kG * C::kCols, ptx::smem_desc_mn128(sA + C::kG * C::kABytes) + s * mn,
+                    ptx::smem_desc_k128(sB + C::kBBytes) + s * kk, idesc | ptx::kIdescAMn, kb || s);
+              } else {
+                const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
+                mma(d, dA + s * (C::kMnA ? mn : kk), dB + s * (C::kDw ? mn : kk), idesc, kb || s);
+              }
+            }
           }
           commit(&empty[st]);
           if (++st == C::kStages) {
@@ -395,8 +427,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
-    const int row0 = quarter * 32;
     uint32_t acc = 0;
     while (walk.take(q)) {
       const bool empty_tile = q.nkb == 0;
@@ -412,103 +442,99 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         ptx::tc_fence_after();
       }
       const uint32_t d = tmem + buf * C::kAccCols + lanes;
-      // this warp's 32 rows: of the matrix (weight gradients) or of the slots, `rows` of them real
-      const int r0 = 128 * rank + row0, rows = q.rows - r0;
-      const int64_t slot0 = (int64_t)q.slot0 + r0, slot = slot0 + lane;
-      const bool live = lane < rows;
-      if (C::kFwd1) {
+      const int lane0 = 128 * rank + quarter * 32;  // this warp's first accumulator lane in the tile
+      if (C::kGated) {
+        // lanes 0-7 and 16-23 hold gate values, the lanes eight further the up values of the
+        // same column of H; of two tokens each of the two lanes computes one
+        const int up = (lane >> 3) & 1;
+        const int f = q.m0 + lane0 / 2 + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll 1
-        for (int c = half * 32; c < C::kOutCols; c += 64) {
-          uint32_t z[32], u[32], p[16];
-          ptx::tmem_ld_32x32b_x32(d + c, z);
-          if (C::kPairB) ptx::tmem_ld_32x32b_x32(d + C::kOutCols + c, u);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float h[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float x = __uint_as_float(z[2 * i + b]);
-              h[b] = C::kPairB ? x * sigmoid_fast(x) * __uint_as_float(u[2 * i + b]) : x * gelu_gate(x);
-            }
-            p[i] = pack2(h[0], h[1]);
-          }
-          const int n = q.n0 + c;
-          store_rows<4>(stage, p, reinterpret_cast<uint8_t*>(a.out) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2,
-                        rows, (a.N - n) / 8, lane);
-        }
-      } else if (MODE == FWD2 || MODE == DX) {
-#pragma unroll 1
-        for (int c = half * 32; c < BN; c += 64) {
+        for (int c = half * 32; c < q.rows; c += 64) {
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
-          const int n = q.n0 + c;
-          store_rows<8>(stage, z, reinterpret_cast<uint8_t*>(a.out) + (slot0 * a.N + n) * 4, (int64_t)a.N * 4,
-                        rows, (a.N - n) / 4, lane);
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c + up) * a.M + f;
+          const int left = f < a.M ? q.rows - c - up : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float z0 = __uint_as_float(z[2 * i]), z1 = __uint_as_float(z[2 * i + 1]);
+            const float other = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 8);
+            const float g = up ? other : z0, u = up ? z1 : other;
+            if (2 * i < left) store_bf16(out + (int64_t)(2 * i) * a.M, g * sigmoid_fast(g) * u);
+          }
         }
-      } else if (MODE == BWD1) {
-        float w = 0.0f, dot = 0.0f;
-        if (live) {
-          const int r = a.plan[a.row_of + slot];
-          w = r >= 0 ? a.weights[r] : 0.0f;
-        }
-        constexpr int G = C::kPairB ? 2 : 1;
-        const int64_t pitch = (int64_t)G * a.N * 2;
+      } else if (C::kFwd1 || MODE == FWD2 || MODE == DX) {
+        const int f = q.m0 + lane0 + lane;
 #pragma unroll 1
-        for (int c = half * 32; c < C::kOutCols; c += 64) {
-          const int n = q.n0 + c;
-          uint32_t pz[16], pu[16], ph[16];
+        for (int c = half * 32; c < q.rows; c += 64) {
+          uint32_t z[32];
+          ptx::tmem_ld_32x32b_x32(d + c, z);
+          ptx::tmem_ld_wait();
+          const int left = f < a.M ? q.rows - c : 0;
+          const int64_t at = (int64_t)(q.slot0 + c) * a.M + f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = __uint_as_float(z[i]);
+            if (i < left) {
+              if (C::kFwd1) store_bf16(reinterpret_cast<uint16_t*>(a.out) + at + (int64_t)i * a.M, v * gelu_gate(v));
+              else reinterpret_cast<float*>(a.out)[at + (int64_t)i * a.M] = v;
+            }
+          }
+        }
+      } else if (C::kBwd1) {
+        const int f = q.m0 + lane0 + lane;
+        const bool in = f < a.M;
+        const int stored = (q.rows + kRowStep - 1) / kRowStep * kRowStep;  // zeros behind the last row
+#pragma unroll 1
+        for (int c = half * 32; c < q.rows; c += 64) {
+          const int mine = q.slot0 + c + lane;
+          const bool live = c + lane < q.rows;
+          const int r = live ? a.plan[a.row_of + mine] : -1;
+          const float w_lane = r >= 0 ? a.weights[r] : 0.0f;
+          float dots[32];
+          uint16_t* dz = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * (C::kG * (int64_t)a.M) + f;
+          uint16_t* wh = reinterpret_cast<uint16_t*>(a.out2) + (int64_t)(q.slot0 + c) * a.M + f;
 #pragma unroll
           for (int i0 = 0; i0 < 32; i0 += 16) {
             uint32_t z[16], u[16], g[16];
             ptx::tmem_ld_32x32b_x16(d + c + i0, z);
-            if (C::kPairB) ptx::tmem_ld_32x32b_x16(d + C::kOutCols + c + i0, u);
-            ptx::tmem_ld_32x32b_x16(d + BN + c + i0, g);
+            if (C::kG == 2) ptx::tmem_ld_32x32b_x16(d + C::kCols + c + i0, u);
+            ptx::tmem_ld_32x32b_x16(d + C::kG * C::kCols + c + i0, g);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float vz[2], vu[2], vh[2];
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float zz = __uint_as_float(z[2 * j + b]), dh = __uint_as_float(g[2 * j + b]);
-                const float dhw = w * dh;
-                float h;
-                if (C::kPairB) {
-                  const float uu = __uint_as_float(u[2 * j + b]);
-                  const float sg = sigmoid_fast(zz);
-                  h = zz * sg * uu;
-                  vz[b] = dhw * uu * sg * (1.0f + zz * (1.0f - sg));
-                  vu[b] = dhw * zz * sg;
-                } else {
-                  const float sg = gelu_gate(zz);
-                  h = zz * sg;
-                  vz[b] = dhw * (sg + zz * sg * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
-                  vu[b] = 0.0f;
-                }
-                vh[b] = w * h;
-                dot += dh * h;  // columns behind N1 hold zeros
-                if (!live) vz[b] = vu[b] = vh[b] = 0.0f;
+            for (int j = 0; j < 16; ++j) {
+              const int i = i0 + j;
+              const float w = __shfl_sync(0xffffffffu, w_lane, i);
+              const bool on = c + i < q.rows;
+              const float zz = __uint_as_float(z[j]), dh = __uint_as_float(g[j]), dhw = w * dh;
+              float h, vz, vu = 0.0f;
+              if (C::kG == 2) {
+                const float uu = __uint_as_float(u[j]), sg = sigmoid_fast(zz), zs = zz * sg;
+                h = zs * uu;
+                vz = dhw * uu * (sg + zs * (1.0f - sg));
+                vu = dhw * zs;
+              } else {
+                const float sg = gelu_gate(zz);
+                h = zz * sg;
+                vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
               }
-              pz[i0 / 2 + j] = pack2(vz[0], vz[1]);
-              pu[i0 / 2 + j] = pack2(vu[0], vu[1]);
-              ph[i0 / 2 + j] = pack2(vh[0], vh[1]);
+              dots[i] = in ? dh * h : 0.0f;
+              if (in && c + i < stored) {
+                store_bf16(dz + (int64_t)i * (C::kG * (int64_t)a.M), on ? vz : 0.0f);
+                if (C::kG == 2) store_bf16(dz + (int64_t)i * (2 * (int64_t)a.M) + a.M, on ? vu : 0.0f);
+                store_bf16(wh + (int64_t)i * a.M, on ? w * h : 0.0f);
+              }
             }
           }
-          // all 128 rows of the CTA's tile: the weight gradients read zeros behind the last one
-          const int all = q.rows > 128 * rank ? 32 : 0;
-          uint8_t* dz = reinterpret_cast<uint8_t*>(a.out) + slot0 * pitch + (int64_t)n * 2;
-          store_rows<4>(stage, pz, dz, pitch, all, (a.N - n) / 8, lane);
-          if (C::kPairB) store_rows<4>(stage, pu, dz + (int64_t)a.N * 2, pitch, all, (a.N - n) / 8, lane);
-          store_rows<4>(stage, ph, reinterpret_cast<uint8_t*>(a.out2) + (slot0 * a.N + n) * 2, (int64_t)a.N * 2, all,
-                        (a.N - n) / 8, lane);
+          const float s = transpose_sum(dots, lane);
+          if (live) a.part[(int64_t)mine * a.parts + (q.m0 + lane0) / 32] = s;
         }
-        if (live) a.part[slot * (2 * a.col_tiles) + 2 * (q.n0 / C::kOutCols) + half] = dot;
       } else {
-        const int64_t m = (int64_t)q.m0 + r0;
+        uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
+        const int64_t m = (int64_t)q.m0 + lane0;
         uint8_t* base = reinterpret_cast<uint8_t*>(a.out) + (((int64_t)q.e * a.M + m) * a.N + q.n0) * 2;
 #pragma unroll 1
-        for (int c = half * 32; c < BN; c += 64) {
+        for (int c = half * 32; c < C::kCols; c += 64) {
           uint32_t z[32], p[16];
           if (empty_tile) {
 #pragma unroll
@@ -519,7 +545,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) p[i] = pack2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
-          store_rows<4>(stage, p, base + c * 2, (int64_t)a.N * 2, (int)(a.M - m), (a.N - q.n0 - c) / 8, lane);
+          store_rows(stage, p, base + c * 2, (int64_t)a.N * 2, (int)(a.M - m), (a.N - q.n0 - c) / 8, lane);
         }
       }
       if (!empty_tile) {

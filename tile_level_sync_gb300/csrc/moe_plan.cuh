@@ -2,7 +2,7 @@
 //
 // A plan is an array of 32-bit words: a header, the experts' counts, the offsets of their
 // first slots (multiples of kTileRows, so that a 128-row tile of a product belongs to one
-// expert), the row tiles {expert, first slot, rows} and the same for tiles of 256 rows, slot_of (assignment -> slot) and row_of (slot
+// expert), the row tiles {expert, first slot, rows} of up to 128 rows and those of up to 256, slot_of (assignment -> slot) and row_of (slot
 // -> assignment).
 //
 // Blocks take consecutive chunks of the ids, a block's warps consecutive parts of its
@@ -56,6 +56,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(PlanArgs a) {
   __syncthreads();
   uint32_t* h = reinterpret_cast<uint32_t*>(a.plan + a.hist) + (int64_t)blockIdx.x * a.E;
   for (int e = threadIdx.x; e < a.E; e += kPlanThreads) h[e] = sh[e];
+}
+
+// An expert's c rows from slot o on, as ceil(c / most) tiles {expert, first slot, rows} of
+// as equal lengths as whole multiples of 32 (the step in columns of a pair's MMA) allow.
+__device__ __forceinline__ void cut_tiles(int4* out, int e, int o, int c, int most, int lane) {
+  const int n = (c + most - 1) / most;
+  const int each = n ? ((c + n - 1) / n + 31) / 32 * 32 : 0;
+  for (int i = lane; i < n; i += 32) out[i] = make_int4(e, o + i * each, max(0, min(each, c - i * each)), 0);
 }
 
 // Shared memory of plan_kernel: per-warp histograms [kPlanWarps][E], then before[E],
@@ -174,12 +182,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   for (int e = blockIdx.x * kPlanWarps + warp; e < E; e += gridDim.x * kPlanWarps) {
     const int64_t o = offset[e], n = offset[e + 1];
     const int c = (int)count[e];
-    int4* tiles = reinterpret_cast<int4*>(a.plan + a.tiles) + o / kTileRows;
-    for (int i = lane; i * kTileRows < c; i += 32)
-      tiles[i] = make_int4(e, (int)o + i * kTileRows, min(kTileRows, c - i * kTileRows), 0);
-    int4* pairs = reinterpret_cast<int4*>(a.plan + a.pairs) + pair[e];
-    for (int i = lane; i * 2 * kTileRows < c; i += 32)
-      pairs[i] = make_int4(e, (int)o + i * 2 * kTileRows, min(2 * kTileRows, c - i * 2 * kTileRows), 0);
+    cut_tiles(reinterpret_cast<int4*>(a.plan + a.tiles) + o / kTileRows, e, (int)o, c, kTileRows, lane);
+    cut_tiles(reinterpret_cast<int4*>(a.plan + a.pairs) + pair[e], e, (int)o, c, 2 * kTileRows, lane);
     for (int64_t i = o + count[e] + lane; i < n; i += 32) row_of[i] = -1;
   }
   for (int64_t i = used + (int64_t)blockIdx.x * kPlanThreads + tid; i < a.S; i += (int64_t)gridDim.x * kPlanThreads)

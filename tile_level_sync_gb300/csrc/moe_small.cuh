@@ -17,10 +17,10 @@ struct CombineArgs {
   const float* rows;     // [slots, D] fp32
   const float* weights;  // [T, k], or null: plain sums
   void* out;             // [T, D] bf16
-  const float* part;     // gradient: [slots][parts]; null otherwise
+  const float* part;     // gradient: sums of dH h, [slots][parts]; null otherwise
   float* dweights;       // [T, k]
   int64_t slot_of;
-  int32_t T, k, D, parts;
+  int32_t T, k, D, parts, used;  // used: sums of a slot, of parts
 };
 
 struct DispatchArgs {
@@ -33,8 +33,8 @@ struct DispatchArgs {
 
 constexpr int kDispatchThreads = 256;
 
-// Rows of X (and dY) into slot order, a warp per slot; zeros behind an expert's last row
-// (the weight gradients sum over them).
+// Rows of X (and dY) into slot order, a warp per slot; zeros behind an expert's last row up
+// to the next multiple of kRowStep (the weight gradients sum over them).
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(DispatchArgs a) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(DispatchArgs
   const int64_t warps = (int64_t)gridDim.x * (kDispatchThreads / 32);
   for (int64_t s = (int64_t)blockIdx.x * (kDispatchThreads / 32) + (threadIdx.x >> 5); s < used; s += warps) {
     const int32_t r = a.plan[a.row_of + s];
+    if (r < 0 && a.plan[a.row_of + s / kRowStep * kRowStep] < 0) continue;
     const int64_t from = r < 0 ? 0 : (int64_t)(r / a.k) * a.chunks, to = s * a.chunks;
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a)
     const int32_t slot = slots[threadIdx.x];
     float s = 0.0f;
     if (slot >= 0)
-      for (int i = 0; i < a.parts; ++i) s += a.part[(int64_t)slot * a.parts + i];
+      for (int i = 0; i < a.used; ++i) s += a.part[(int64_t)slot * a.parts + i];
     a.dweights[t * a.k + threadIdx.x] = s;
   }
 }
