@@ -168,6 +168,16 @@ struct Walk {
   __device__ __forceinline__ Walk(const GemmArgs& args, int32_t n) : a(args), total(n), t(blockIdx.x / PAIR) {
     if (t < total) next = tile_at<MODE, ACT, PAIR>(a, t);
   }
+  // The same for a whole warp, whose lanes all hold one tile: broadcast, so that what is
+  // computed from it is known to be uniform.
+  __device__ __forceinline__ bool take_warp(Tile& q) {
+    if (!take(q)) return false;
+    q.e = __shfl_sync(0xffffffffu, q.e, 0);
+    q.slot0 = __shfl_sync(0xffffffffu, q.slot0, 0);
+    q.rows = __shfl_sync(0xffffffffu, q.rows, 0);
+    q.nkb = __shfl_sync(0xffffffffu, q.nkb, 0);
+    return true;
+  }
   __device__ __forceinline__ bool take(Tile& q) {
     if (t >= total) return false;
     q = next;
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int32_t abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = PAIR == 2 ? (int)ptx::cluster_ctarank() : 0;
 
   if (threadIdx.x == 0) {
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   __syncthreads();
   if (PAIR == 2) ptx::cluster_sync();  // the other CTA's barriers exist
   ptx::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   Walk<MODE, ACT, PAIR> walk(a, tile_total<MODE, ACT, PAIR>(a));
@@ -259,9 +269,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     // ------------------------------------------------------------ copies
     const bool copies_a = warp == 0;
     const uint64_t pol = ptx::l2_policy_evict_normal();
+    const bool one = ptx::elect_one();
     uint32_t it = 0, st = 0, par = 1;
     const uint32_t full0 = PAIR == 2 ? ptx::mapa(&full[0], 0) : 0;
-    while (!abort_flag && walk.take(q)) {
+    while (!abort_flag && walk.take_warp(q)) {
       // this CTA's share of the tile's tokens, and the box that covers it
       const int cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
       const int share = cols / PAIR;
@@ -282,8 +293,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           PAIR * (C::kAParts * C::kABytes +
                   C::kBParts * (C::kGather ? live * 512 : C::kDw ? C::kBBytes : (16 << pick) * 128));
       bool ok = true;
-      // Every lane waits for the slot and issues its own copies: nothing orders the lanes or
-      // the two warps, since the barrier's phase cannot end before warp 0's arrival.
+      // Nothing orders the two warps' copies: the barrier's phase cannot end before warp 0's
+      // arrival.
       for (int kb0 = 0; kb0 < q.nkb; kb0 += C::kKps, ++it) {
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
@@ -308,34 +319,43 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           par ^= 1;
         }
         const int blocks = min(C::kKps, q.nkb - kb0);
-        if (copies_a && lane == 0 && rank == 0) ptx::mbar_arrive_expect_tx(bar, blocks * block_bytes);
+        if (copies_a && rank == 0 && one) ptx::mbar_arrive_expect_tx(bar, blocks * block_bytes);
 #pragma unroll
         for (int b = 0; b < C::kKps; ++b) {
-        if (b >= blocks) break;
-        uint8_t* sA = stage + b * C::kBlockBytes;
-        uint8_t* sB = sA + C::kAParts * C::kABytes;
-        const int32_t kc = (kb0 + b) * 64;
-        if (copies_a) {
-          if (C::kDw) {
-            if (lane < 2) load2(sA + lane * 8192, &a.mA, m0 + 64 * lane, q.slot0 + kc);
-          } else if (C::kGated) {
-            if (lane == 0) load5(sA, &a.mA, kc, m0 / 8, q.e);
-          } else if (C::kBwd1) {
-            if (lane < C::kG) load3(sA + lane * C::kABytes, &a.mA, kc, m0, C::kG * q.e + lane);
-            else if (lane < C::kG + 2)
-              load3(sA + C::kG * C::kABytes + (lane - C::kG) * 8192, &a.mA2, m0 + 64 * (lane - C::kG), kc, q.e);
-          } else if (MODE == DX) {
-            if (lane < 2) load3(sA + lane * 8192, &a.mA, m0 + 64 * lane, kc, q.e);
-          } else if (lane == 0) {
-            load3(sA, &a.mA, kc, m0, q.e);
+          if (b >= blocks) break;
+          uint8_t* sA = stage + b * C::kBlockBytes;
+          uint8_t* sB = sA + C::kAParts * C::kABytes;
+          const int32_t kc = (kb0 + b) * 64;
+          if (copies_a) {
+            if (one) {
+              if (C::kDw) {
+                load2(sA, &a.mA, m0, q.slot0 + kc);
+                load2(sA + 8192, &a.mA, m0 + 64, q.slot0 + kc);
+              } else if (C::kGated) {
+                load5(sA, &a.mA, kc, m0 / 8, q.e);
+              } else if (C::kBwd1) {
+                load3(sA, &a.mA, kc, m0, C::kG * q.e);
+                if (C::kG == 2) load3(sA + C::kABytes, &a.mA, kc, m0, 2 * q.e + 1);
+                load3(sA + C::kG * C::kABytes, &a.mA2, m0, kc, q.e);
+                load3(sA + C::kG * C::kABytes + 8192, &a.mA2, m0 + 64, kc, q.e);
+              } else if (MODE == DX) {
+                load3(sA, &a.mA, m0, kc, q.e);
+                load3(sA + 8192, &a.mA, m0 + 64, kc, q.e);
+              } else {
+                load3(sA, &a.mA, kc, m0, q.e);
+              }
+            }
+          } else if (C::kGather) {
+            if (lane < live) ptx::tma_gather4(sB + lane * 512, mb, bar, kc, tok, pol);
+          } else if (one) {
+            if (C::kDw) {
+#pragma unroll
+              for (int c = 0; c < C::kCols / PAIR / 64; ++c) load2(sB + c * 8192, mb, n0 + 64 * c, q.slot0 + kc);
+            } else {
+              load2(sB, mb, kc, slot);
+              if (C::kBwd1) load2(sB + C::kBBytes, mb2, kc, slot);
+            }
           }
-        } else if (C::kDw) {
-          if (lane < C::kCols / PAIR / 64) load2(sB + lane * 8192, mb, n0 + 64 * lane, q.slot0 + kc);
-        } else if (C::kGather) {
-          if (lane < live) ptx::tma_gather4(sB + lane * 512, mb, bar, kc, tok, pol);
-        } else if (lane < C::kBParts) {
-          load2(sB + lane * C::kBBytes, lane ? mb2 : mb, kc, slot);
-        }
         }
       }
       if (!__all_sync(0xffffffffu, ok)) {
@@ -353,7 +373,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         ptx::mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, kWaitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       auto mma = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t id, uint32_t more) {
         if (PAIR == 2) ptx::umma_bf16_pair(d, da, db, id, more);
         else ptx::umma_bf16(d, da, db, id, more);
@@ -362,9 +382,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         if (PAIR == 2) ptx::umma_commit_pair_multicast(bar, 0x3);
         else ptx::umma_commit(bar);
       };
+      const uint32_t ring0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
+      const bool one = ptx::elect_one();  // the lane whose MMAs its commits cover
       uint32_t st = 0, par = 0, acc = 0;
       bool ok = true;
-      while (ok && !abort_flag && walk.take(q)) {
+      while (ok && !abort_flag && walk.take_warp(q)) {
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
         const uint32_t cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
         const uint32_t idesc = ptx::idesc_bf16_f32(128 * PAIR, cols) | (C::kMnA ? ptx::kIdescAMn : 0) |
@@ -374,51 +396,56 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         ok = (PAIR == 2 ? ptx::mbar_wait_bounded_cluster(&tempty[buf], (use & 1) ^ 1, kWaitNs)
                         : ptx::mbar_wait_bounded(&tempty[buf], (use & 1) ^ 1, kWaitNs)) &&
              !abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * C::kAccCols;
         for (int kb0 = 0; kb0 < q.nkb; kb0 += C::kKps) {
-          ok = ptx::mbar_wait_bounded(&full[st], par, kWaitNs);
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full[st], par, kWaitNs));
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll
           for (int b = 0; b < C::kKps; ++b) {
             const int kb = kb0 + b;
-            const uint32_t sA = ptx::smem_u32(ring + st * C::kStageBytes + b * C::kBlockBytes);
+            const uint32_t sA = ring0 + st * C::kStageBytes + b * C::kBlockBytes;
             const uint32_t sB = sA + C::kAParts * C::kABytes;
             // 16 k: 32 bytes of a K-contiguous row, or 16 rows of 128 bytes
             constexpr uint64_t mn = 2048 >> 4, kk = 32 >> 4;
+            const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
             const uint64_t dB = C::kDw ? ptx::smem_desc_mn128(sB) : ptx::smem_desc_k128(sB);
+            const uint64_t dA2 = ptx::smem_desc_mn128(sA + C::kG * C::kABytes);
+            const uint64_t dB2 = ptx::smem_desc_k128(sB + C::kBBytes);
             // the last block's steps of 16: only those that hold k (DW: rows; elsewhere columns)
             const int left = (C::kDw ? q.rows : a.K) - kb * 64;
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               if (16 * s >= left) break;
+              if (!one) continue;
               if (C::kBwd1) {
 #pragma unroll
                 for (int p = 0; p < C::kG; ++p)
-                  mma(d + p * C::kCols, ptx::smem_desc_k128(sA + p * C::kABytes) + s * kk, dB + s * kk, idesc, kb || s);
-                mma(d + C::kG * C::kCols, ptx::smem_desc_mn128(sA + C::kG * C::kABytes) + s * mn,
-                    ptx::smem_desc_k128(sB + C::kBBytes) + s * kk, idesc | ptx::kIdescAMn, kb || s);
+                  mma(d + p * C::kCols, dA + p * (C::kABytes >> 4) + s * kk, dB + s * kk, idesc, kb || s);
+                mma(d + C::kG * C::kCols, dA2 + s * mn, dB2 + s * kk, idesc | ptx::kIdescAMn, kb || s);
               } else {
-                const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
                 mma(d, dA + s * (C::kMnA ? mn : kk), dB + s * (C::kDw ? mn : kk), idesc, kb || s);
               }
             }
           }
-          commit(&empty[st]);
+          if (one) commit(&empty[st]);
+          __syncwarp();
           if (++st == C::kStages) {
             st = 0;
             par ^= 1;
           }
         }
         if (!ok) break;
-        commit(&tfull[buf]);
+        if (one) commit(&tfull[buf]);
+        __syncwarp();
       }
       if (!ok || abort_flag) {
         abort_flag = 1;
         a.plan[PLAN_ERR] = (int32_t)kErrWait;
-        commit(&drain);  // MMAs still in flight
+        if (one) commit(&drain);  // MMAs still in flight
         ptx::mbar_wait_bounded(&drain, 0, kWaitNs);
       }
     }

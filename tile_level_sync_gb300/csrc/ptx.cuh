@@ -33,6 +33,19 @@ __device__ __forceinline__ uint32_t lane_id() {
   return l;
 }
 
+// True in one lane of a converged warp.  Code that a whole warp runs, with only the
+// instruction itself under this predicate, keeps operands such as descriptors in uniform
+// registers; in a branch of one lane each has to be moved there first.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
