@@ -186,6 +186,9 @@ MLPS = [
     dict(T=64, E=64, k=8, D=512, N1=256),
     dict(T=900, E=4, k=2, D=264, N1=264),
     dict(T=257, E=1, k=1, D=72, N1=136),
+    dict(T=900, E=4, k=2, D=320, N1=192),
+    dict(T=70, E=5, k=2, D=192, N1=320),
+    dict(T=300, E=2, k=2, D=640, N1=64),
 ]
 _name = lambda c: "T{T}E{E}k{k}D{D}N{N1}".format(**c)  # noqa: E731
 

@@ -185,43 +185,54 @@ cusync_status_t prepare_device(int* sms) {
   return CUSYNC_OK;
 }
 
-// bf16 boxes of 64 elements x box_rows rows (x one matrix), 128-byte swizzle; elements
-// outside read as zero.
-bool map_2d(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, uint32_t box_rows) {
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t one[2] = {1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool map_3d(CUtensorMap* m, const void* p, int64_t depth, int64_t rows, int64_t cols, uint32_t box_rows) {
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(rows * cols) * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
-  cuuint32_t one[3] = {1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+// A map of bf16 elements: sizes and strides (in elements, from the second dimension on) and
+// the box, innermost first; 128-byte swizzle; elements outside read as zero.
+template <int N>
+bool map_nd(CUtensorMap* m, const void* p, const int64_t (&size)[N], const int64_t (&stride)[N - 1],
+            const int (&box_size)[N]) {
+  cuuint64_t dims[N], strides[N - 1];
+  cuuint32_t box[N], one[N];
+  for (int i = 0; i < N; ++i) {
+    dims[i] = (cuuint64_t)size[i];
+    box[i] = (cuuint32_t)box_size[i];
+    one[i] = 1;
+    if (i) strides[i - 1] = (cuuint64_t)stride[i - 1] * 2;
+  }
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, const_cast<void*>(p), dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// W1t of a gated layer with gate and up rows eight by eight: [E][N1/8][2][8][D], 64 of these
-// rows for each CTA's 64 columns of H.
-bool map_gated(CUtensorMap* m, const void* p, int64_t experts, int64_t n1, int64_t d) {
-  cuuint64_t dims[5] = {(cuuint64_t)d, 8, 2, (cuuint64_t)n1 / 8, (cuuint64_t)experts};
-  cuuint64_t strides[4] = {(cuuint64_t)d * 2, (cuuint64_t)(n1 * d) * 2, (cuuint64_t)(8 * d) * 2,
-                           (cuuint64_t)(2 * n1 * d) * 2};
-  cuuint32_t box[5] = {64, 8, 2, 8, 1};
-  cuuint32_t one[5] = {1, 1, 1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(p), dims, strides, box, one,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// Rows [rows, cols]: boxes of 64 columns x box_rows; wide: [cols / 64][rows][64], boxes of
+// `chunks` times that.
+bool map_rows(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows, bool wide, int chunks) {
+  return wide ? map_nd<3>(m, p, {64, rows, cols / 64}, {cols, 64}, {64, box_rows, chunks})
+              : map_nd<2>(m, p, {cols, rows}, {cols}, {64, box_rows});
+}
+// Matrices [depth][rows, cols], the depth a dimension of its own (rows outside a matrix read
+// as zero); wide: their rows one after the other, as above.
+bool map_weights(CUtensorMap* m, const void* p, int64_t depth, int64_t rows, int64_t cols, int box_rows, bool wide,
+                 int chunks) {
+  return wide ? map_rows(m, p, depth * rows, cols, box_rows, true, chunks)
+              : map_nd<3>(m, p, {cols, rows, depth}, {cols, rows * cols}, {64, box_rows, 1});
+}
+// W1t of a gated layer with gate and up rows eight by eight, 64 of each at a time: the rows
+// as [N1/8 of every expert][2][8].  wide: all experts' rows as one run of eights, which ends
+// N1 early so that the up rows of the last one stay inside.
+bool map_gated(CUtensorMap* m, const void* p, int64_t experts, int64_t n1, int64_t d, bool wide, int blocks) {
+  return wide ? map_nd<5>(m, p, {64, 8, 2, (2 * experts - 1) * n1 / 8, d / 64}, {d, n1 * d, 8 * d, 64},
+                          {64, 8, 2, 8, blocks})
+              : map_nd<5>(m, p, {d, 8, 2, n1 / 8, experts}, {d, n1 * d, 8 * d, 2 * n1 * d}, {64, 8, 2, 8, 1});
+}
+// W1t's rows for BWD1: 128 gate and the 128 up rows N1 further (GeLU: 128 rows).
+bool map_gate_up(CUtensorMap* m, const void* p, int64_t experts, int g, int64_t n1, int64_t d, bool wide) {
+  if (!wide) return map_weights(m, p, experts * g, n1, d, 128, false, 1);
+  return map_nd<3>(m, p, {d, (g * experts - (g - 1)) * n1, g}, {d, n1 * d}, {64, 128, g});
 }
 // Token rows by slot, in the four box heights.
-bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols) {
+bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, bool wide, int blocks) {
   bool ok = true;
-  for (int i = 0; i < 4; ++i) ok = ok && map_2d(&m[i], p, rows, cols, 16u << i);
+  for (int i = 0; i < 4; ++i) ok = ok && map_rows(&m[i], p, rows, cols, 16 << i, wide, blocks);
   return ok;
 }
 
@@ -329,6 +340,8 @@ GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
 
 template <int MODE, int ACT, int PAIR>
 cudaError_t launch_gemm(GemmArgs a, const Layer& L, int sms, cudaStream_t s) {
+  static_assert(MODE <= DW2 || MODE == FWD1G, "one counter for each product of a call");
+  a.counter = PLAN_COUNTERS + (MODE == FWD1G ? FWD1 : MODE);
   using C = GemmCfg<MODE, ACT, PAIR>;
   const bool wide = C::kCols == 256;
   a.tiles = wide ? L.pairs : L.tiles;
@@ -490,9 +503,12 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   b.M = (int32_t)L.D;
   b.K = (int32_t)L.N1;
   b.out = w + L.rows;
-  if (!(L.G == 2 ? map_gated(&a.mA, W1t, L.E, L.N1, L.D) : map_3d(&a.mA, W1t, L.E, L.N1, L.D, 128)) ||
-      !(gather ? map_2d(&a.mB[0], X, L.T, L.D, 1) : map_tokens(a.mB, w + L.x, L.S, L.D)) ||
-      !map_3d(&b.mA, W2t, L.E, L.D, L.N1, 128) || !map_tokens(b.mB, w + L.h, L.S, L.N1))
+  const bool wide = L.D % 64 == 0 && L.N1 % 64 == 0;
+  a.wide = b.wide = wide;
+  if (!(L.G == 2 ? map_gated(&a.mA, W1t, L.E, L.N1, L.D, wide, 2)
+                 : map_weights(&a.mA, W1t, L.E, L.N1, L.D, 128, wide, 2)) ||
+      !(gather ? map_rows(&a.mB[0], X, L.T, L.D, 1, false, 1) : map_tokens(a.mB, w + L.x, L.S, L.D, wide, 2)) ||
+      !map_weights(&b.mA, W2t, L.E, L.D, L.N1, 128, wide, 2) || !map_tokens(b.mB, w + L.h, L.S, L.N1, wide, 2))
     return CUSYNC_ERR_CUDA;
   if (gather) {
     for (int i = 1; i < 4; ++i) a.mB[i] = a.mB[0];
@@ -552,11 +568,16 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   w2.M = (int32_t)L.D;
   w2.N = (int32_t)L.N1;
   w2.out = dW2t;
-  if (!map_3d(&p.mA, W1t, (int64_t)L.E * L.G, L.N1, L.D, 128) || !map_3d(&p.mA2, W2t, L.E, L.D, L.N1, 64) ||
-      !map_tokens(p.mB, gx, L.S, L.D) || !map_tokens(p.mB2, gy, L.S, L.D) ||
-      !map_3d(&x.mA, W1t, L.E, H, L.D, 64) || !map_tokens(x.mB, gz, L.S, H) ||
-      !map_2d(&w1.mA, gz, L.S, H, 64) || !map_2d(&w1.mB[0], gx, L.S, L.D, 64) ||
-      !map_2d(&w2.mA, gy, L.S, L.D, 64) || !map_2d(&w2.mB[0], gh, L.S, L.N1, 64))
+  const bool wide = L.D % 64 == 0 && L.N1 % 64 == 0;
+  p.wide = x.wide = w1.wide = w2.wide = wide;
+  // a weight gradient's stage holds two blocks of 64 rows on pairs, one on single CTAs
+  const int kr1 = wide && pair1 ? 128 : 64, kr2 = wide && pair2 ? 128 : 64;
+  // BWD1's stage holds one block, DX's two
+  if (!map_gate_up(&p.mA, W1t, L.E, L.G, L.N1, L.D, wide) || !map_weights(&p.mA2, W2t, L.E, L.D, L.N1, 64, wide, 2) ||
+      !map_tokens(p.mB, gx, L.S, L.D, wide, 1) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1) ||
+      !map_weights(&x.mA, W1t, L.E, H, L.D, wide ? 128 : 64, wide, 2) || !map_tokens(x.mB, gz, L.S, H, wide, 2) ||
+      !map_rows(&w1.mA, gz, L.S, H, kr1, wide, 2) || !map_rows(&w1.mB[0], gx, L.S, L.D, kr1, wide, 2) ||
+      !map_rows(&w2.mA, gy, L.S, L.D, kr2, wide, 2) || !map_rows(&w2.mB[0], gh, L.S, L.N1, kr2, wide, 2))
     return CUSYNC_ERR_CUDA;
   for (int i = 1; i < 4; ++i) {
     w1.mB[i] = w1.mB[0];

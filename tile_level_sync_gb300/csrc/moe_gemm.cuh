@@ -22,9 +22,14 @@
 // takes gate and up rows of W1t eight by eight (one 5-D box): a gate lane and the lane
 // eight further hold the two factors of one h.  BWD1 has them in accumulators of their own.
 //
-// One CTA per SM walks its tiles with a fixed stride:
+// One CTA (or pair) per SM.  Tiles differ in length, so they are claimed one by one from a
+// counter that the plan cleared; the claim of a tile is made when the one before it starts:
+//   warp 11    (of a pair's first CTA) claims tiles, reads their plan entries and hands them
+//              to the other warps of both CTAs through a ring in shared memory.
 //   warp 0     copies of A, warp 10 copies of B (TMA boxes; FWD1G: tile::gather4, four
-//              rows a copy, through the plan's row indices).
+//              rows a copy, through the plan's row indices).  A copy has a fixed cost
+//              besides its bytes, so a stage holds two blocks of 64 k where three such
+//              stages fit, and where widths allow one box brings all of an operand.
 //   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma.
 //   warps 2-9  epilogue: two warps per TMEM lane quarter, every other 32 columns each.
 // Accumulators are double-buffered where two fit in TMEM's 512 columns.
@@ -53,7 +58,8 @@ namespace moe {
 enum : int { FWD1 = 0, FWD2 = 1, BWD1 = 2, DX = 3, DW1 = 4, DW2 = 5, FWD1G = 6 };
 
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kGemmThreads = 352;
+constexpr int kGemmThreads = 384;
+constexpr int kTileSlots = 4;
 constexpr int kRowStep = 16;                 // slots up to a multiple of which a row's zeros are stored
 constexpr uint32_t kErrWait = 3u << 24;      // the pipeline-wait class of the chain kernel's error words
 
@@ -73,6 +79,10 @@ struct GemmArgs {
   int32_t N;           // DW: output columns
   int32_t K;           // reduction length (not DW)
   int32_t m_tiles, n_tiles, parts;
+  int32_t counter;     // plan word that counts this launch's claimed tiles
+  // Every width is a multiple of 64: the maps see rows as [width / 64][rows][64], and one
+  // copy brings an operand's two blocks of 64 k, or its two chunks of 64 columns, at once.
+  int32_t wide;
 };
 
 template <int MODE, int ACT, int PAIR>
@@ -157,33 +167,48 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
   return r;
 }
 
-// A CTA's tiles, read one ahead: the plan's entry of a tile is a trip to L2 that no role
-// should wait for between two tiles.
-template <int MODE, int ACT, int PAIR>
+// The ring of claimed tiles.  full: one arrival by the claiming warp (each CTA has its
+// own); empty, taken (the first CTA's): arrivals by every warp that read a slot, and by the
+// first copying warp alone.
+struct TileRing {
+  int32_t slot[kTileSlots][8];  // a Tile; rows < 0: no more
+  uint64_t full[kTileSlots], empty[kTileSlots], taken;
+};
+
+// One warp's way through the ring.
+template <int PAIR>
 struct Walk {
-  const GemmArgs& a;
-  const int32_t total;
-  int32_t t;
-  Tile next;
-  __device__ __forceinline__ Walk(const GemmArgs& args, int32_t n) : a(args), total(n), t(blockIdx.x / PAIR) {
-    if (t < total) next = tile_at<MODE, ACT, PAIR>(a, t);
-  }
-  // The same for a whole warp, whose lanes all hold one tile: broadcast, so that what is
-  // computed from it is known to be uniform.
-  __device__ __forceinline__ bool take_warp(Tile& q) {
-    if (!take(q)) return false;
-    q.e = __shfl_sync(0xffffffffu, q.e, 0);
-    q.slot0 = __shfl_sync(0xffffffffu, q.slot0, 0);
-    q.rows = __shfl_sync(0xffffffffu, q.rows, 0);
-    q.nkb = __shfl_sync(0xffffffffu, q.nkb, 0);
-    return true;
-  }
-  __device__ __forceinline__ bool take(Tile& q) {
-    if (t >= total) return false;
-    q = next;
-    t += gridDim.x / PAIR;
-    if (t < total) next = tile_at<MODE, ACT, PAIR>(a, t);
-    return true;
+  TileRing& ring;
+  const int rank;
+  uint32_t n;
+  __device__ __forceinline__ Walk(TileRing& r, int rank_) : ring(r), rank(rank_), n(0) {}
+  // The next tile, in every lane.  False at the end, and (with *ok cleared) if a wait expired.
+  __device__ __forceinline__ bool take(Tile& q, bool* ok, bool first_copier = false) {
+    const uint32_t s = n % kTileSlots, par = (n / kTileSlots) & 1;
+    const bool got = PAIR == 2 ? ptx::mbar_wait_bounded_cluster(&ring.full[s], par, kWaitNs)
+                               : ptx::mbar_wait_bounded(&ring.full[s], par, kWaitNs);
+    if (!__all_sync(0xffffffffu, got)) {
+      *ok = false;
+      return false;
+    }
+    const volatile int32_t* v = ring.slot[s];
+    const int lane = threadIdx.x & 31;
+    const int32_t mine = v[lane & 7];
+    // broadcast, so that what is computed from the tile is known to be uniform
+    q.e = __shfl_sync(0xffffffffu, mine, 0);
+    q.slot0 = __shfl_sync(0xffffffffu, mine, 1);
+    q.rows = __shfl_sync(0xffffffffu, mine, 2);
+    q.m0 = __shfl_sync(0xffffffffu, mine, 3);
+    q.n0 = __shfl_sync(0xffffffffu, mine, 4);
+    q.nkb = __shfl_sync(0xffffffffu, mine, 5);
+    if (lane == 0) {
+      if (rank == 0) ptx::mbar_arrive(&ring.empty[s]);
+      else ptx::mbar_arrive_cluster(ptx::mapa(&ring.empty[s], 0));
+      if (first_copier) ptx::mbar_arrive(&ring.taken);
+    }
+    __syncwarp();
+    ++n;
+    return q.rows >= 0;
   }
 };
 
@@ -229,6 +254,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int32_t abort_flag;
+  __shared__ TileRing tiles;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = PAIR == 2 ? (int)ptx::cluster_ctarank() : 0;
 
@@ -242,6 +268,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       ptx::mbar_init(&tempty[i], 8 * PAIR);
     }
     ptx::mbar_init(&drain, 1);
+    for (int i = 0; i < kTileSlots; ++i) {
+      ptx::mbar_init(&tiles.full[i], 1);
+      ptx::mbar_init(&tiles.empty[i], PAIR == 2 ? 21 : 11);  // copies, MMA (first CTA), epilogue
+    }
+    ptx::mbar_init(&tiles.taken, 1);
     ptx::mbar_init_fence();
     abort_flag = 0;
     ptx::prefetch_tmap(&a.mA);
@@ -262,7 +293,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  Walk<MODE, ACT, PAIR> walk(a, tile_total<MODE, ACT, PAIR>(a));
+  Walk<PAIR> walk(tiles, rank);
   Tile q;
 
   if (warp == 0 || warp == 10) {
@@ -272,7 +303,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     const bool one = ptx::elect_one();
     uint32_t it = 0, st = 0, par = 1;
     const uint32_t full0 = PAIR == 2 ? ptx::mapa(&full[0], 0) : 0;
-    while (!abort_flag && walk.take_warp(q)) {
+    bool ok = true;
+    while (!abort_flag && walk.take(q, &ok, copies_a && rank == 0)) {
       // this CTA's share of the tile's tokens, and the box that covers it
       const int cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
       const int share = cols / PAIR;
@@ -289,16 +321,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         auto token = [&](int32_t x) { return x < 0 ? a.T : x / a.k; };
         tok = make_int4(token(r.x), token(r.y), token(r.z), token(r.w));
       }
-      const uint32_t block_bytes =
-          PAIR * (C::kAParts * C::kABytes +
-                  C::kBParts * (C::kGather ? live * 512 : C::kDw ? C::kBBytes : (16 << pick) * 128));
-      bool ok = true;
+      const uint32_t b_bytes = C::kGather ? live * 512 : C::kDw ? C::kBBytes : (16 << pick) * 128;
+      const uint32_t block_bytes = PAIR * (C::kAParts * C::kABytes + C::kBParts * b_bytes);
       // Nothing orders the two warps' copies: the barrier's phase cannot end before warp 0's
       // arrival.
       for (int kb0 = 0; kb0 < q.nkb; kb0 += C::kKps, ++it) {
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
-        uint8_t* stage = ring + st * C::kStageBytes;
+        uint8_t* sA = ring + st * C::kStageBytes;
+        uint8_t* sB = sA + C::kKps * C::kAParts * C::kABytes;
         uint64_t* bar = &full[st];
         // in a pair both CTAs' copies complete on the first one's barrier
         const uint32_t bar0 = full0 + 8 * st;
@@ -318,53 +349,87 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           st = 0;
           par ^= 1;
         }
+        const bool wide = a.wide;
         const int blocks = min(C::kKps, q.nkb - kb0);
-        if (copies_a && rank == 0 && one) ptx::mbar_arrive_expect_tx(bar, blocks * block_bytes);
-#pragma unroll
-        for (int b = 0; b < C::kKps; ++b) {
-          if (b >= blocks) break;
-          uint8_t* sA = stage + b * C::kBlockBytes;
-          uint8_t* sB = sA + C::kAParts * C::kABytes;
-          const int32_t kc = (kb0 + b) * 64;
-          if (copies_a) {
-            if (one) {
-              if (C::kDw) {
-                load2(sA, &a.mA, m0, q.slot0 + kc);
-                load2(sA + 8192, &a.mA, m0 + 64, q.slot0 + kc);
-              } else if (C::kGated) {
-                load5(sA, &a.mA, kc, m0 / 8, q.e);
-              } else if (C::kBwd1) {
-                load3(sA, &a.mA, kc, m0, C::kG * q.e);
-                if (C::kG == 2) load3(sA + C::kABytes, &a.mA, kc, m0, 2 * q.e + 1);
-                load3(sA + C::kG * C::kABytes, &a.mA2, m0, kc, q.e);
-                load3(sA + C::kG * C::kABytes + 8192, &a.mA2, m0 + 64, kc, q.e);
-              } else if (MODE == DX) {
-                load3(sA, &a.mA, m0, kc, q.e);
-                load3(sA + 8192, &a.mA, m0 + 64, kc, q.e);
-              } else {
-                load3(sA, &a.mA, kc, m0, q.e);
-              }
-            }
-          } else if (C::kGather) {
-            if (lane < live) ptx::tma_gather4(sB + lane * 512, mb, bar, kc, tok, pol);
-          } else if (one) {
+        if (copies_a && rank == 0 && one) {
+          // a box of two blocks counts whole where the second lies outside
+          const int counted = wide && !C::kGather ? C::kKps : blocks;
+          ptx::mbar_arrive_expect_tx(bar, C::kGather && wide ? C::kKps * C::kABytes + blocks * b_bytes
+                                                             : counted * block_bytes);
+        }
+        if (wide && copies_a) {
+          const int32_t kc = kb0 * 64;
+          if (one) {
             if (C::kDw) {
-#pragma unroll
-              for (int c = 0; c < C::kCols / PAIR / 64; ++c) load2(sB + c * 8192, mb, n0 + 64 * c, q.slot0 + kc);
+              load3(sA, &a.mA, 0, q.slot0 + kc, m0 / 64);
+            } else if (C::kGated) {
+              load5(sA, &a.mA, 0, q.e * (2 * a.M / 8) + m0 / 8, kb0);
+            } else if (C::kBwd1) {
+              load3(sA, &a.mA, kc, q.e * C::kG * a.M + m0, 0);
+              load3(sA + C::kG * C::kABytes, &a.mA2, 0, q.e * a.K + kc, m0 / 64);
+            } else if (MODE == DX) {
+              load3(sA, &a.mA, 0, q.e * a.K + kc, m0 / 64);
             } else {
-              load2(sB, mb, kc, slot);
-              if (C::kBwd1) load2(sB + C::kBBytes, mb2, kc, slot);
+              load3(sA, &a.mA, 0, q.e * a.M + m0, kb0);
+            }
+          }
+        } else if (wide && !C::kGather) {
+          const int32_t kc = kb0 * 64;
+          if (one) {
+            if (C::kDw) {
+              load3(sB, mb, 0, q.slot0 + kc, n0 / 64);
+              if (PAIR == 1) load3(sB + 2 * C::kKps * 8192, mb, 0, q.slot0 + kc, n0 / 64 + 2);
+            } else {
+              load3(sB, mb, 0, slot, kb0);
+              if (C::kBwd1) load3(sB + C::kBBytes, mb2, 0, slot, kb0);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < C::kKps; ++b) {
+            if (b >= blocks) break;
+            uint8_t* pA = sA + b * C::kABytes;
+            uint8_t* pB = sB + b * C::kBBytes;
+            const int32_t kc = (kb0 + b) * 64;
+            if (copies_a) {
+              if (one) {
+                if (C::kDw) {
+                  load2(pA, &a.mA, m0, q.slot0 + kc);
+                  load2(pA + 8192, &a.mA, m0 + 64, q.slot0 + kc);
+                } else if (C::kGated) {
+                  load5(pA, &a.mA, kc, m0 / 8, q.e);
+                } else if (C::kBwd1) {
+                  load3(pA, &a.mA, kc, m0, C::kG * q.e);
+                  if (C::kG == 2) load3(pA + C::kABytes, &a.mA, kc, m0, 2 * q.e + 1);
+                  load3(pA + C::kG * C::kABytes, &a.mA2, m0, kc, q.e);
+                  load3(pA + C::kG * C::kABytes + 8192, &a.mA2, m0 + 64, kc, q.e);
+                } else if (MODE == DX) {
+                  load3(pA, &a.mA, m0, kc, q.e);
+                  load3(pA + 8192, &a.mA, m0 + 64, kc, q.e);
+                } else {
+                  load3(pA, &a.mA, kc, m0, q.e);
+                }
+              }
+            } else if (C::kGather) {
+              if (lane < live) ptx::tma_gather4(pB + lane * 512, mb, bar, kc, tok, pol);
+            } else if (one) {
+              if (C::kDw) {
+#pragma unroll
+                for (int c = 0; c < C::kCols / PAIR / 64; ++c) load2(pB + c * 8192, mb, n0 + 64 * c, q.slot0 + kc);
+              } else {
+                load2(pB, mb, kc, slot);
+                if (C::kBwd1) load2(pB + C::kBBytes, mb2, kc, slot);
+              }
             }
           }
         }
       }
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) {
-          abort_flag = 1;
-          a.plan[PLAN_ERR] = (int32_t)kErrWait;
-        }
-        break;
-      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      a.plan[PLAN_ERR] = (int32_t)kErrWait;
     }
     __syncwarp();
     // after an abort: wait, bounded, for the copies still in flight (both warps' complete on `full`)
@@ -384,11 +449,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       };
       const uint32_t ring0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
       const bool one = ptx::elect_one();  // the lane whose MMAs its commits cover
+      const bool wide = a.wide;
+      const uint32_t chunk = wide ? C::kKps * 8192 : 8192;  // 64 columns of an operand that lies along M or N
       uint32_t st = 0, par = 0, acc = 0;
       bool ok = true;
-      while (ok && !abort_flag && walk.take_warp(q)) {
+      while (ok && !abort_flag && walk.take(q, &ok)) {
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
         const uint32_t cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
+        const uint32_t share = cols / PAIR;
+        const uint32_t box_bytes = (share <= 16 ? 16 : share <= 32 ? 32 : share <= 64 ? 64 : 128) * 128;
         const uint32_t idesc = ptx::idesc_bf16_f32(128 * PAIR, cols) | (C::kMnA ? ptx::kIdescAMn : 0) |
                                (C::kDw ? ptx::kIdescBMn : 0);
         const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
@@ -407,13 +476,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
 #pragma unroll
           for (int b = 0; b < C::kKps; ++b) {
             const int kb = kb0 + b;
-            const uint32_t sA = ring0 + st * C::kStageBytes + b * C::kBlockBytes;
-            const uint32_t sB = sA + C::kAParts * C::kABytes;
+            // block b of the stage: wide boxes put a chunk's blocks, and a token box's, back to back
+            const uint32_t st0 = ring0 + st * C::kStageBytes;
+            const uint32_t sA = st0 + b * (C::kMnA && wide ? 8192 : C::kABytes);
+            const uint32_t sB = st0 + C::kKps * C::kAParts * C::kABytes +
+                                b * (C::kDw && wide ? 8192 : wide && !C::kGather ? box_bytes : C::kBBytes);
             // 16 k: 32 bytes of a K-contiguous row, or 16 rows of 128 bytes
             constexpr uint64_t mn = 2048 >> 4, kk = 32 >> 4;
-            const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA) : ptx::smem_desc_k128(sA);
-            const uint64_t dB = C::kDw ? ptx::smem_desc_mn128(sB) : ptx::smem_desc_k128(sB);
-            const uint64_t dA2 = ptx::smem_desc_mn128(sA + C::kG * C::kABytes);
+            const uint64_t dA = C::kMnA ? ptx::smem_desc_mn128(sA, chunk) : ptx::smem_desc_k128(sA);
+            const uint64_t dB = C::kDw ? ptx::smem_desc_mn128(sB, chunk) : ptx::smem_desc_k128(sB);
+            const uint64_t dA2 = ptx::smem_desc_mn128(sA + C::kG * C::kABytes, 8192);
             const uint64_t dB2 = ptx::smem_desc_k128(sB + C::kBBytes);
             // the last block's steps of 16: only those that hold k (DW: rows; elsewhere columns)
             const int left = (C::kDw ? q.rows : a.K) - kb * 64;
@@ -450,22 +522,51 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       }
     }
     __syncwarp();
+  } else if (warp == 11) {
+    // ------------------------------------------------------------ claims
+    if (rank == 0 && lane == 0) {
+      const int32_t total = tile_total<MODE, ACT, PAIR>(a);
+      bool ok = true;
+      for (uint32_t n = 0; !abort_flag; ++n) {
+        const uint32_t s = n % kTileSlots;
+        if (n >= kTileSlots)
+          ok = PAIR == 2 ? ptx::mbar_wait_bounded_cluster(&tiles.empty[s], ((n / kTileSlots) & 1) ^ 1, kWaitNs)
+                         : ptx::mbar_wait_sleepy(&tiles.empty[s], ((n / kTileSlots) & 1) ^ 1, kWaitNs);
+        if (ok && n) ok = ptx::mbar_wait_sleepy(&tiles.taken, (n - 1) & 1, kWaitNs);
+        if (!ok) break;
+        int32_t t = blockIdx.x / PAIR;  // the first tile needs no claim
+        if (n) t = gridDim.x / PAIR + atomicAdd(a.plan + a.counter, 1);
+        Tile q = {0, 0, -1, 0, 0, 0};
+        if (t < total) q = tile_at<MODE, ACT, PAIR>(a, t);
+        const int32_t v[6] = {q.e, q.slot0, q.rows, q.m0, q.n0, q.nkb};
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+          *const_cast<volatile int32_t*>(&tiles.slot[s][i]) = v[i];
+          if (PAIR == 2) ptx::st_cluster_u32(ptx::mapa(&tiles.slot[s][i], 1), (uint32_t)v[i]);
+        }
+        ptx::mbar_arrive(&tiles.full[s]);
+        if (PAIR == 2) ptx::mbar_arrive_cluster(ptx::mapa(&tiles.full[s], 1));
+        if (t >= total) break;
+      }
+      if (!ok) {
+        abort_flag = 1;
+        a.plan[PLAN_ERR] = (int32_t)kErrWait;
+      }
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     uint32_t acc = 0;
-    while (walk.take(q)) {
+    bool ok = true;
+    while (walk.take(q, &ok)) {
       const bool empty_tile = q.nkb == 0;
       const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
       if (!empty_tile) {
         ++acc;
-        const bool ok = ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag;
-        if (!__all_sync(0xffffffffu, ok)) {
-          abort_flag = 1;
-          if (lane == 0) a.plan[PLAN_ERR] = (int32_t)kErrWait;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
+        if (!ok) break;
         ptx::tc_fence_after();
       }
       const uint32_t d = tmem + buf * C::kAccCols + lanes;
@@ -583,6 +684,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           else ptx::mbar_arrive_cluster(ptx::mapa(&tempty[buf], 0));
         }
       }
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      a.plan[PLAN_ERR] = (int32_t)kErrWait;
     }
   }
   ptx::tc_fence_before();

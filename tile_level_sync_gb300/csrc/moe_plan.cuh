@@ -22,7 +22,7 @@ namespace moe {
 constexpr int kTileRows = 128;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_PAIRS = 3, PLAN_HEADER = 16 };
+enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_PAIRS = 3, PLAN_COUNTERS = 8, PLAN_HEADER = 16 };
 
 struct PlanArgs {
   const int32_t* ids;
@@ -58,12 +58,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_hist_kernel(PlanArgs a) {
   for (int e = threadIdx.x; e < a.E; e += kPlanThreads) h[e] = sh[e];
 }
 
-// An expert's c rows from slot o on, as ceil(c / most) tiles {expert, first slot, rows} of
-// as equal lengths as whole multiples of 32 (the step in columns of a pair's MMA) allow.
+// An expert's c rows from slot o on, as tiles {expert, first slot, rows} of `most` rows and
+// one of the rest: a product's time goes by the bytes it loads, which a full tile uses best.
 __device__ __forceinline__ void cut_tiles(int4* out, int e, int o, int c, int most, int lane) {
-  const int n = (c + most - 1) / most;
-  const int each = n ? ((c + n - 1) / n + 31) / 32 * 32 : 0;
-  for (int i = lane; i < n; i += 32) out[i] = make_int4(e, o + i * each, max(0, min(each, c - i * each)), 0);
+  for (int i = lane; i * most < c; i += 32) out[i] = make_int4(e, o + i * most, min(most, c - i * most), 0);
 }
 
 // Shared memory of plan_kernel: per-warp histograms [kPlanWarps][E], then before[E],
@@ -169,6 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   __syncthreads();
   const int64_t used = offset[E];
   if (blockIdx.x == 0) {
+    if (tid < PLAN_HEADER - PLAN_COUNTERS) a.plan[PLAN_COUNTERS + tid] = 0;  // tiles claimed by each product
     if (tid == 0) {
       a.plan[PLAN_ERR] = 0;
       a.plan[PLAN_TILES] = (int32_t)(used / kTileRows);

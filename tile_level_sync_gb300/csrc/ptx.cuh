@@ -346,12 +346,12 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr) {
 }
 
 // Shared-memory matrix descriptor for an operand whose M (or N) index is contiguous, in the
-// 128-byte-swizzle layout of TMA boxes of 64 such elements x 64 k rows: 64-element chunks
-// 8192 bytes apart (leading-dimension offset), groups of 8 k rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr) {
+// 128-byte-swizzle layout of TMA boxes of 64 such elements x some k rows: 64-element chunks
+// `chunk` bytes apart (leading-dimension offset), groups of 8 k rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t chunk) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(8192 >> 4) << 16;
+  d |= (uint64_t)(chunk >> 4) << 16;
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
