@@ -52,6 +52,10 @@ ROUTES = [
     dict(T=9, E=1024, k=32, score="sigmoid", renorm=True),
     dict(T=9, E=1000, k=32, score="softmax", bias=True, groups=4, group_limit=1, group_top=2),
     dict(T=20, E=8, k=8, score="softmax", renorm=True),
+    dict(T=30, E=64, k=6, score="sigmoid", groups=8, group_limit=2, group_top=1, renorm=True),
+    dict(T=30, E=128, k=4, score="softmax", groups=4, group_limit=2, group_top=2),
+    dict(T=30, E=255, k=20, score="sigmoid", bias=True),
+    dict(T=5000, E=32, k=2, score="sigmoid", bias=True, groups=4, group_limit=1, group_top=2, renorm=True),
     dict(T=20, E=8, k=4, score="sigmoid", groups=8, group_limit=4, group_top=2),
 ]
 

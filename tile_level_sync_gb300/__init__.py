@@ -184,10 +184,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None  # raw handle of torch's current stream on a device
+
+
 def _stream(s):
     if s is None:
+        global _current_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            # the accessor behind torch.cuda.current_stream(), without building a Stream object
+            _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+                (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _current_stream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -460,38 +468,44 @@ class Moe:
         self.info = cusync_moe_info(desc)
         self._d = ctypes.byref(desc)
         self._lib = load()
+        import torch
         d, gated = desc, 2 if desc.act == MOE_SWIGLU else 1
-        rows, logits = d.T * d.top_k, "float32" if d.logits_f32 else "bfloat16"
+        bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+        logits, rows = f32 if d.logits_f32 else bf16, d.T * d.top_k
+        tokens, w1, w2 = d.T * d.D, d.experts * gated * d.N1 * d.D, d.experts * d.N1 * d.D
+        # type and elements of every argument; buffers: bytes, in elements of any type
         self._want = {
-            "logits": (logits, d.T * d.experts), "dlogits": (logits, d.T * d.experts), "bias": ("float32", d.experts),
-            "ids": ("int32", rows), "weights": ("float32", rows), "dweights": ("float32", rows),
+            "logits": (logits, d.T * d.experts), "dlogits": (logits, d.T * d.experts), "bias": (f32, d.experts),
+            "ids": (i32, rows), "weights": (f32, rows), "dweights": (f32, rows),
+            "X": (bf16, tokens), "Y": (bf16, tokens), "dX": (bf16, tokens), "dY": (bf16, tokens),
+            "W1t": (bf16, w1), "W2t": (bf16, w2), "dW1t": (bf16, w1), "dW2t": (bf16, w2),
             "plan": (None, self.info.plan_bytes), "work": (None, self.info.work_bytes),
             "grad_work": (None, self.info.grad_work_bytes),
-            "W1t": ("bfloat16", d.experts * gated * d.N1 * d.D), "W2t": ("bfloat16", d.experts * d.N1 * d.D),
-            "dW1t": ("bfloat16", d.experts * gated * d.N1 * d.D), "dW2t": ("bfloat16", d.experts * d.N1 * d.D),
         }
-        for name in ("X", "Y", "dX", "dY"):
-            self._want[name] = ("bfloat16", d.T * d.D)
+        self._device = torch.cuda.current_device
 
     def _ptrs(self, **tensors):
         """Device addresses of the named arguments, the tensors among them checked."""
-        import torch
-        out = []
+        out, device = [], None
         for name, t in tensors.items():
             if t is None or isinstance(t, int):
                 out.append(t)
                 continue
             dtype, n = self._want[name]
-            if dtype is None:  # a buffer of bytes, in elements of any type
+            if dtype is None:
                 if t.numel() * t.element_size() < n:
                     raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes: {n} are needed")
-            elif t.dtype is not getattr(torch, dtype):
-                raise ValueError(f"{name} is {t.dtype}: torch.{dtype} is needed")
+            elif t.dtype is not dtype:
+                raise ValueError(f"{name} is {t.dtype}: {dtype} is needed")
             elif t.numel() != n:
                 raise ValueError(f"{name} has {t.numel()} elements: {n} are needed")
             if not t.is_contiguous():
                 raise ValueError(f"{name} is not contiguous")
-            if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            if not t.is_cuda:
+                raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
+            if device is None:
+                device = self._device()
+            if t.get_device() != device:
                 raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
             out.append(t.data_ptr())
         return out

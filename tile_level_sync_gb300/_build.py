@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libcusync.so")
 
-SOURCES = [os.path.join(CSRC, "cusync.cu"), os.path.join(CSRC, "moe.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("cusync.cu", "moe.cu", "moe_route_f32.cu", "moe_route_bf16.cu")]
 DEPS = SOURCES + [
     os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".h", ".cuh"))
 ] + [os.path.join(INCLUDE, f) for f in ("cusync.h", "cusync_moe.h")]

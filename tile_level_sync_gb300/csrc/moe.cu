@@ -12,8 +12,8 @@
 
 #include "../../include/cusync_moe.h"
 #include "moe_gemm.cuh"
+#include "moe_launch.h"
 #include "moe_plan.cuh"
-#include "moe_route.cuh"
 #include "moe_small.cuh"
 
 using namespace cusync;
@@ -238,49 +238,6 @@ bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, 
 
 // ----------------------------------------------------------------------------- launches
 
-// Every launch is a programmatic dependent of the kernel before it in the stream: it may be
-// set up while that one ends, and each kernel waits for that end before it touches memory.
-template <typename... P, typename... Q>
-cudaError_t launch_cluster(int cluster, void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, Q... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, f, args...);
-}
-template <typename... P, typename... Q>
-cudaError_t launch(void (*f)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, Q... args) {
-  return launch_cluster(1, f, grid, threads, smem, s, args...);
-}
-
-template <typename L, int SCORE, bool GRAD>
-cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)div_up(a.T, 8));
-  const int v = (int)div_up(a.E, 32);
-#define CUSYNC_ROUTE(V)                                                                     \
-  if (v <= V)                                                                               \
-    return GRAD ? launch(route_grad_kernel<L, V, SCORE>, grid, 256, 0, s, a)                \
-                : launch(route_kernel<L, V, SCORE>, grid, 256, 0, s, a);
-  CUSYNC_ROUTE(1)
-  CUSYNC_ROUTE(2)
-  CUSYNC_ROUTE(4)
-  CUSYNC_ROUTE(8)
-  CUSYNC_ROUTE(16)
-  CUSYNC_ROUTE(32)
-#undef CUSYNC_ROUTE
-  return cudaErrorInvalidValue;
-}
-
 template <bool GRAD>
 cusync_status_t route_any(const cusync_moe_desc_t* d, const Layer& L, RouteArgs a, cudaStream_t s) {
   a.T = L.T;
@@ -293,10 +250,11 @@ cusync_status_t route_any(const cusync_moe_desc_t* d, const Layer& L, RouteArgs 
   a.renorm = d->renorm ? 1 : 0;
   a.scale = d->scale;
   if (L.T == 0) return CUSYNC_OK;
+  int sms = 0;
+  const cusync_status_t st = prepare_device(&sms);
+  if (st != CUSYNC_OK) return st;
   const bool soft = d->score == CUSYNC_MOE_SOFTMAX;
-  const cudaError_t e =
-      d->logits_f32 ? (soft ? launch_route<float, 0, GRAD>(a, s) : launch_route<float, 1, GRAD>(a, s))
-                    : (soft ? launch_route<__nv_bfloat16, 0, GRAD>(a, s) : launch_route<__nv_bfloat16, 1, GRAD>(a, s));
+  const cudaError_t e = d->logits_f32 ? route_f32(a, soft, GRAD, sms, s) : route_bf16(a, soft, GRAD, sms, s);
   return e == cudaSuccess ? CUSYNC_OK : CUSYNC_ERR_CUDA;
 }
 

@@ -1,41 +1,33 @@
 // The router of a mixture-of-experts layer and its gradient: one warp per token.
 //
-// A lane holds experts lane, lane + 32, ... (V of them) in registers, so a row of logits is
-// read once, coalesced, at any expert count.  Scores are s = softmax(l) or sigmoid(l); the
-// choice goes by key = s + bias.  The largest key is found by one pass over a lane's
-// registers and two warp reductions (of the key's ordered bits, then of the index among
-// equal keys), so equal keys go to the lowest index.
+// Scores are s = softmax(l) or sigmoid(l); the choice goes by key = s + bias.  Without a bias
+// the keys are the logits themselves (both scores grow with the logit): the comparison is
+// exact.  With one, 32-bit keys carry the rounding of the exponential, the division, the sum
+// and the addition; where two neighbours in the chosen order (or the last chosen and the
+// first left out, or two groups' ranks) are closer than a bound on that error, the token's
+// selection is done again with 64-bit scores, of the experts that come into question only.
 //
-// Without a bias the keys are the logits themselves (both scores grow with the logit): the
-// comparison is exact.  With one, 32-bit keys carry the rounding of the exponential, the
-// sum and the addition; where two neighbours in the chosen order (or the last chosen and
-// the first left out, or two groups' ranks) are closer than a bound on that error, the
-// token's selection is done again with 64-bit scores.
+// route_kernel (up to 256 experts, groups of whole lanes): a lane holds V neighbouring
+// experts as unsigned keys whose low bits are the place in the lane, sorted by a network of
+// min/max; a step of the selection is then one reduction of the lanes' heads, one vote and a
+// shift in the winning lane.  route_any_kernel takes any count and grouping: experts lane,
+// lane + 32, ..., and a pass over the lane's registers at every step.  32768 tokens x 256
+// experts, 8 chosen out of 4 of 8 groups: ROUTE_FAST us against ROUTE_ANY us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
+#include "moe_launch.h"
 #include "ptx.cuh"
 
 namespace cusync {
 namespace moe {
 
 constexpr unsigned kFull = 0xffffffffu;
-
-struct RouteArgs {
-  const void* logits;
-  const float* bias;
-  int32_t* ids;
-  float* weights;        // route: out; gradient: dweights (in)
-  void* dlogits;
-  int64_t T;
-  int32_t E, k, groups, group_size, group_limit, group_top;
-  int32_t renorm;
-  float scale;
-};
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -60,8 +52,8 @@ __device__ __forceinline__ double warp_sum(double v) {
 
 // Bits that compare as unsigned integers as the floats do; both zeros alike.
 __device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const int32_t u = __float_as_int(f + 0.0f);
+  return (uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u);
 }
 
 // The warp's largest (key, lowest index); index INT_MAX where every key is -inf.
@@ -199,38 +191,422 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane
   }
 }
 
-template <int V, int SCORE>
-__device__ __forceinline__ void keys_64(const RouteArgs& a, const float (&l)[V], int lane, float m, double (&key)[V]) {
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    key[i] = SCORE == 0 ? exp((double)l[i] - (double)m) : 1.0 / (1.0 + exp(-(double)l[i]));
-    sum += key[i];
-  }
-  if (SCORE == 0) sum = warp_sum(sum);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    if (SCORE == 0) key[i] /= sum;
-    if (a.bias && e < a.E) key[i] += (double)a.bias[e];
-    if (l[i] == -INFINITY || key[i] != key[i]) key[i] = -INFINITY;
-  }
-}
-
-// The selection again, in 64 bits; kept out of line so that its registers do not count
-// against the usual path.
-template <int V, int SCORE>
-__device__ __noinline__ int pick_64(const RouteArgs& a, const float (&l)[V], int lane, float m) {
-  double key[V];
-  keys_64<V, SCORE>(a, l, lane, m, key);
-  if (a.groups > 1) keep_groups<double, V>(a, key, lane, -1.0);
+// The whole selection of a token again, in 64 bits where keys are scores, else of the 32-bit
+// logits in full.  It reads the row itself and is kept out of line, so that its registers do
+// not count against the usual path.
+template <typename L, int V, int SCORE>
+__device__ __noinline__ int select_again(const RouteArgs& a, int64_t t, int lane) {
+  float l[V];
+  load_row<L, V>(a, t, lane, l);
   int id;
+  if (!a.bias && !(a.groups > 1 && a.group_top == 2)) {
+    if (a.groups > 1) keep_groups<float, V>(a, l, lane, -1.0f);
+    pick<float, V>(a, l, lane, -1.0f, id);
+    return id;
+  }
+  float m = 0.0f;
+  double sum = 1.0;
+  if (SCORE == 0) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (l[i] > -INFINITY) sum += exp((double)l[i] - (double)m);
+    sum = warp_sum(sum);
+  }
+  double key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = -INFINITY;
+    if (l[i] > -INFINITY) {
+      double k = SCORE == 0 ? exp((double)l[i] - (double)m) / sum : 1.0 / (1.0 + exp(-(double)l[i]));
+      if (a.bias) k += (double)a.bias[lane + 32 * i];
+      if (k == k) key[i] = k;
+    }
+  }
+  if (a.groups > 1) keep_groups<double, V>(a, key, lane, -1.0);
   pick<double, V>(a, key, lane, -1.0, id);
   return id;
 }
 
+// Lane j < k holds the j-th chosen expert (-1: none): its weight, and both stored.  m and
+// inv: the row's largest logit and the inverse of its sum of exponentials (softmax weights
+// that are not renormalised).
+template <typename L, int SCORE>
+__device__ __forceinline__ void store_choice(const RouteArgs& a, int64_t t, int lane, int id, float m, float inv) {
+  const bool on = lane < a.k && id >= 0;
+  const float mine = on ? one_logit<L>(a, t, id) : -INFINITY;  // read again, from L1
+  float w;
+  if (a.renorm) {
+    // s_j / sum s_i: softmax's as exponentials relative to the largest chosen logit; sigmoids
+    // as they are, unless one is so small (below e^-60) that only its logarithm is safe
+    float ex;
+    if (SCORE == 0 || __any_sync(kFull, on && mine < -60.0f)) {
+      const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
+      const float mx = warp_max(ls);
+      ex = on ? expf(ls - mx) : 0.0f;
+    } else {
+      ex = on ? sigmoid_f(mine) : 0.0f;
+    }
+    w = ex / warp_sum(ex);
+  } else {
+    w = SCORE == 0 ? expf(mine - m) * inv : sigmoid_f(mine);
+  }
+  if (lane < a.k) {
+    a.ids[t * a.k + lane] = id;
+    a.weights[t * a.k + lane] = on ? a.scale * w : 0.0f;
+  }
+}
+
+// ------------------------------------------------------------------ V neighbours a lane
+
+__device__ __forceinline__ void order_two(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+// Largest first.
+__device__ __forceinline__ void sort_lane(uint32_t (&)[1]) {}
+__device__ __forceinline__ void sort_lane(uint32_t (&v)[2]) { order_two(v[0], v[1]); }
+__device__ __forceinline__ void sort_lane(uint32_t (&v)[4]) {
+  order_two(v[0], v[1]);
+  order_two(v[2], v[3]);
+  order_two(v[0], v[2]);
+  order_two(v[1], v[3]);
+  order_two(v[1], v[2]);
+}
+__device__ __forceinline__ void sort_lane(uint32_t (&v)[8]) {  // odd-even merge of two sorted fours
+#pragma unroll
+  for (int h = 0; h < 8; h += 4) {
+    order_two(v[h], v[h + 1]);
+    order_two(v[h + 2], v[h + 3]);
+    order_two(v[h], v[h + 2]);
+    order_two(v[h + 1], v[h + 3]);
+    order_two(v[h + 1], v[h + 2]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) order_two(v[i], v[i + 4]);
+  order_two(v[2], v[4]);
+  order_two(v[3], v[5]);
+  order_two(v[1], v[2]);
+  order_two(v[3], v[4]);
+  order_two(v[5], v[6]);
+}
+
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+
+template <int V>
+__device__ __forceinline__ void load_lane(const float* row, int e0, int E, bool vec, float (&l)[V]) {
+  if (vec && e0 + V <= E) {
+    if constexpr (V == 8 || V == 4) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(row + e0 + i);
+        l[i] = v.x;
+        l[i + 1] = v.y;
+        l[i + 2] = v.z;
+        l[i + 3] = v.w;
+      }
+      return;
+    } else if constexpr (V == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(row + e0);
+      l[0] = v.x;
+      l[1] = v.y;
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? row[e0 + i] : -INFINITY;
+}
+template <int V>
+__device__ __forceinline__ void load_lane(const __nv_bfloat16* row, int e0, int E, bool vec, float (&l)[V]) {
+  if constexpr (V > 1) {
+    if (vec && e0 + V <= E) {
+      uint32_t w[V / 2];
+      if constexpr (V == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + e0);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else if constexpr (V == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(row + e0);
+        w[0] = v.x, w[1] = v.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(row + e0);
+      }
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        l[2 * i] = __uint_as_float(w[i] << 16);
+        l[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? __bfloat162float(row[e0 + i]) : -INFINITY;
+}
+
+// Bits of a double that compare as integers as the doubles do.
+__device__ __forceinline__ int64_t ordered_64(double d) {
+  const int64_t u = __double_as_longlong(d + 0.0);
+  return u ^ ((u >> 63) & 0x7fffffffffffffffll);
+}
+
+// Keys in 64 bits (logits: in full), one to a lane, of the experts whose approximate key is at
+// least this lane's `floor`: the c-th such expert e goes to lane c.  Returns how many there
+// are; more than 32 do not fit.
+template <typename L, int V, int SCORE, bool scored>
+__device__ __forceinline__ int candidates(const RouteArgs& a, int64_t t, int lane, float floor, int& e, double& key) {
+  float l[V];
+  load_lane<V>(reinterpret_cast<const L*>(a.logits) + t * a.E, lane * V, a.E, false, l);
+  float m = 0.0f;
+  double sum = 1.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = l[i] == l[i] ? l[i] : -INFINITY;
+  if (scored && SCORE == 0) {
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += l[i] > -INFINITY ? exp((double)l[i] - (double)m) : 0.0;
+    sum = warp_sum(sum);
+  }
+  int total = 0, src = -1, part = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float k = l[i];
+    if (scored && l[i] > -INFINITY) {
+      k = SCORE == 0 ? __expf(l[i] - m) / (float)sum : sigmoid_f(l[i]);
+      if (a.bias) k += a.bias[lane * V + i];
+    }
+    for (unsigned mask = __ballot_sync(kFull, k > -INFINITY && k >= floor); mask; mask &= mask - 1, ++total)
+      if (lane == total) {
+        src = __ffs(mask) - 1;
+        part = i;
+      }
+  }
+  float mine = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float x = __shfl_sync(kFull, l[i], src < 0 ? 0 : src);
+    if (part == i) mine = x;
+  }
+  e = src < 0 ? 0x7fffffff : src * V + part;
+  key = -INFINITY;
+  if (src >= 0) {
+    key = mine;
+    if (scored) {
+      key = SCORE == 0 ? exp((double)mine - (double)m) / sum : 1.0 / (1.0 + exp(-(double)mine));
+      if (a.bias) key += (double)a.bias[e];
+    }
+  }
+  return total;
+}
+
+// The kept groups, a bit each, where 32-bit ranks could not decide: ranks again from every
+// group's candidates.  0 if they do not fit.
+template <typename L, int V, int SCORE, bool scored>
+__device__ __noinline__ unsigned groups_again(const RouteArgs& a, int64_t t, int lane, float floor) {
+  int e;
+  double key;
+  const int total = candidates<L, V, SCORE, scored>(a, t, lane, floor, e, key);
+  if (total > 32) return 0;
+  const int64_t none = ordered_64(-INFINITY);
+  const int64_t o = ordered_64(key);
+  int64_t b1 = none, b2 = none;
+  double d1 = -INFINITY, d2 = -INFINITY;
+  for (int c = 0; c < total; ++c) {
+    const int64_t k = __shfl_sync(kFull, o, c);
+    const double d = __shfl_sync(kFull, key, c);
+    if (__shfl_sync(kFull, e, c) / a.group_size != lane) continue;
+    if (k > b1) {
+      b2 = b1, d2 = d1;
+      b1 = k, d1 = d;
+    } else if (k > b2) {
+      b2 = k, d2 = d;
+    }
+  }
+  const int64_t rank = ordered_64(a.group_top == 2 && a.group_size > 1 ? d1 + d2 : d1);
+  int better = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const int64_t r = __shfl_sync(kFull, rank, g);
+    better += r > rank || (r == rank && g < lane);
+  }
+  return __ballot_sync(kFull, lane < a.groups && better < a.group_limit);
+}
+
+// The chosen experts (lane j: the j-th), where 32-bit keys could not decide: the candidates
+// from `least` on, the k-th key's approximation less its error, in the kept groups (this
+// lane's among them or not).  -2 in every lane if they do not fit.
+template <typename L, int V, int SCORE, bool scored>
+__device__ __noinline__ int order_again(const RouteArgs& a, int64_t t, int lane, bool keep, float least) {
+  int e;
+  double key;
+  const int total = candidates<L, V, SCORE, scored>(a, t, lane, keep ? least : INFINITY, e, key);
+  if (total > 32) return -2;
+  const int64_t o = ordered_64(key);
+  int better = 0;
+  for (int c = 0; c < total; ++c) {
+    const int64_t k = __shfl_sync(kFull, o, c);
+    const int x = __shfl_sync(kFull, e, c);
+    better += k > o || (k == o && x < e);
+  }
+  int id = -1;
+  for (int c = 0; c < total; ++c) {
+    const int place = __shfl_sync(kFull, better, c), x = __shfl_sync(kFull, e, c);
+    if (place == lane) id = x;
+  }
+  return lane < a.k ? id : -1;
+}
+
+constexpr int kRouteBlocks = 4;  // resident blocks of route_kernel on an SM
+
+// scored: keys are scores, or sums of two (a bias, or group_top = 2 with groups); else logits.
+// `vec`: rows start at multiples of V elements.  A group is group_size / V neighbouring lanes,
+// a power of two of them (one group: any size).
+template <typename L, int V, int SCORE, bool scored, bool grouped>
+__global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_constant__ RouteArgs a, int vec) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, e0 = lane * V;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  constexpr uint32_t kLow = V - 1;
+  float bias[V], next[V];
+  float bias_most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bias[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
+    if (bias[i] > -INFINITY) bias_most = fmaxf(bias_most, fabsf(bias[i]));
+  }
+  // a group's lanes, this lane's group and the group's first lane
+  const int lanes = a.group_size / V > 0 ? a.group_size / V : 1, mine = lane / lanes, leader = mine * lanes;
+  bias_most = warp_max(bias_most);
+  load_lane<V>(reinterpret_cast<const L*>(a.logits) + t * a.E, e0, a.E, vec, next);
+  for (; t < a.T; t += warps) {
+    float l[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = SCORE == 0 && !(next[i] == next[i]) ? -INFINITY : next[i];
+    if (t + warps < a.T) load_lane<V>(reinterpret_cast<const L*>(a.logits) + (t + warps) * a.E, e0, a.E, vec, next);
+    // softmax's largest logit and sum, where a score of its own is needed
+    float m = 0.0f, inv = 0.0f;
+    if (SCORE == 0 && (scored || !a.renorm)) {
+      m = l[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+      m = warp_max(m);
+      float sum = 0.0f;
+      if (m > -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += expf(l[i] - m);
+      }
+      inv = 1.0f / warp_sum(sum);
+    }
+    // Keys.  A bound on how far the difference of two may be off (tol), besides the low bits:
+    // sigmoid: the fast exponential (2 + 1.2 |l| ulp, times s (1 - s)) and division (2 ulp), the
+    // addition: 3.7e-7 a key.  softmax: the same exponential of l - m, at most 37 additions in
+    // the sum, a product: 3e-6 of a score of at most inv.  The bias adds half an ulp, the low
+    // bits 7 ulp of the larger key.
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float k = l[i];
+      if (scored) {
+        k = SCORE == 0 ? __expf(l[i] - m) * inv : __fdividef(1.0f, 1.0f + __expf(-l[i]));
+        k += bias[i];
+      }
+      // -inf and NaN logits (or biases) are off
+      key[i] = l[i] > -INFINITY && k > -INFINITY ? ((ordered(k) & ~kLow) | (kLow - i)) : 0u;
+    }
+    sort_lane(key);
+    const float most = SCORE == 0 ? inv : 1.0f;  // a score is at most
+    const float tol = scored ? (SCORE == 0 ? 6.5e-6f * inv : 8e-7f) + 1.1e-6f * (most + bias_most) : 0.0f;
+    bool keep = true;   // this lane's group is among the kept ones
+    bool lost = false;  // nothing here can decide: the whole selection again
+    if (grouped) {
+      uint32_t b1 = key[0], b2 = V > 1 ? key[V > 1 ? 1 : 0] : 0u;
+      for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
+        b2 = max(min(b1, c1), max(b2, c2));
+        b1 = max(b1, c1);
+      }
+      auto value = [](uint32_t k) { return k ? unordered(k & ~kLow) : -INFINITY; };
+      float rank = value(b1);
+      if (a.group_top == 2 && a.group_size > 1) rank += value(b2);
+      if (mine >= a.groups) rank = -INFINITY;  // lanes behind the last group
+      // the other groups' ranks, by whole groups of lanes up the warp and round; of equal
+      // ranks the lower group is the better one
+      int better = 0;
+      for (int o = lanes; o < 32; o += lanes) {
+        const int from = (lane + o) & 31;
+        const float r = __shfl_sync(kFull, rank, from);
+        better += r > rank || (r == rank && from < leader);
+      }
+      const bool real = mine < a.groups;
+      keep = real && better < a.group_limit;
+      // the closest pair across the border: scores, by the bound; 32-bit logits, by equality but
+      // for the low bits
+      const float low = unordered(__reduce_min_sync(kFull, keep ? ordered(rank) : 0xffffffffu));
+      const float high = unordered(__reduce_max_sync(kFull, real && !keep ? ordered(rank) : ordered(-INFINITY)));
+      if ((scored || sizeof(L) == 4) && high > -INFINITY && !(scored ? low - high > 2.0f * tol : low != high)) {
+        const float floor = value(a.group_top == 2 && a.group_size > 1 ? b2 : b1) - 4.0f * tol;
+        const unsigned bits = groups_again<L, V, SCORE, scored>(a, t, lane, real ? floor : INFINITY);
+        lost = bits == 0;
+        keep = real && ((bits >> mine) & 1u);
+      }
+      if (!keep) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = 0u;
+      }
+    }
+    int id = -1;
+    uint32_t last = 0u;       // 32-bit logits: the key before, for equality but for the low bits
+    float before = INFINITY;  // scores: the value before
+    float gap = INFINITY;     // the closest pair
+    float least = -INFINITY;  // the last chosen
+    for (int j = 0; j <= a.k; ++j) {
+      const uint32_t head = key[0] | kLow;
+      const uint32_t best = __reduce_max_sync(kFull, head);
+      if (best == kLow) break;  // none left
+      if (scored) {
+        const float value = unordered(best);
+        gap = fminf(gap, before - value);
+        before = value;
+      } else if (sizeof(L) == 4) {
+        if (last == best) gap = -1.0f;
+        last = best;
+        before = unordered(best & ~kLow);
+      }
+      if (j == a.k) break;
+      least = before;
+      const int who = __ffs(__ballot_sync(kFull, head == best)) - 1;  // equal keys: the lowest expert
+      const uint32_t won = __shfl_sync(kFull, key[0], who);
+      if (lane == j) id = who * V + (int)(~won & kLow);
+      if (lane == who) {
+#pragma unroll
+        for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
+        key[V - 1] = 0u;
+      }
+    }
+    if ((scored || sizeof(L) == 4) && !(gap > tol) && !lost) {
+      id = order_again<L, V, SCORE, scored>(a, t, lane, keep, least - 4.0f * tol);
+      lost = id == -2;
+    }
+    if (__any_sync(kFull, lost)) id = select_again<L, V, SCORE>(a, t, lane);
+    store_choice<L, SCORE>(a, t, lane, id, m, inv);
+  }
+}
+
+// ------------------------------------------------------------------ any count and grouping
+
 template <typename L, int V, int SCORE>
-__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(256) route_any_kernel(const __grid_constant__ RouteArgs a) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -280,25 +656,8 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   if (a.groups > 1) sure = keep_groups<float, V>(a, key, lane, scored ? 2.0f * tol : -1.0f);
   int id;
   sure = pick<float, V>(a, key, lane, tol, id) && sure;
-  if (scored && !sure) id = pick_64<V, SCORE>(a, l, lane, m);
-  // weights: lane j holds the j-th chosen expert (its logit read again, from L1)
-  const bool on = lane < a.k && id >= 0;
-  const float mine = on ? one_logit<L>(a, t, id) : -INFINITY;
-  float w;
-  if (a.renorm) {
-    // s_j / sum s_i = exp(log s_j) / sum exp(log s_i), taken relative to the largest chosen
-    // score: no underflow, whatever the others are
-    const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
-    const float mx = warp_max(ls);
-    const float ex = on ? expf(ls - mx) : 0.0f;
-    w = ex / warp_sum(ex);
-  } else {
-    w = SCORE == 0 ? expf(mine - m) / sum : sigmoid_f(mine);
-  }
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = id;
-    a.weights[t * a.k + lane] = on ? a.scale * w : 0.0f;
-  }
+  if (scored && !sure) id = select_again<L, V, SCORE>(a, t, lane);
+  store_choice<L, SCORE>(a, t, lane, id, m, 1.0f / sum);
 }
 
 // With q_j = s_j / sum of chosen s (renorm) the chosen experts' gradients need nothing of
@@ -308,7 +667,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 // Without: softmax dl_e = p_e (scale dw_e [e chosen] - scale sum_j p_j dw_j), sigmoid
 // dl_j = scale dw_j s_j (1 - s_j).  All other gradients are zero.
 template <typename L, int V, int SCORE>
-__global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__ RouteArgs a) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -374,6 +733,55 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs a) {
     const int e = lane + 32 * i;
     if (e < a.E) store_logit(row + e, d[i]);
   }
+}
+
+// ------------------------------------------------------------------ launches
+
+template <typename L, int V, int SCORE>
+cudaError_t launch_lanes(bool scored, bool grouped, dim3 g, cudaStream_t s, const RouteArgs& a, int vec) {
+  if (scored)
+    return grouped ? launch(route_kernel<L, V, SCORE, true, true>, g, 256, 0, s, a, vec)
+                   : launch(route_kernel<L, V, SCORE, true, false>, g, 256, 0, s, a, vec);
+  return grouped ? launch(route_kernel<L, V, SCORE, false, true>, g, 256, 0, s, a, vec)
+                 : launch(route_kernel<L, V, SCORE, false, false>, g, 256, 0, s, a, vec);
+}
+
+template <typename L, int SCORE, bool GRAD>
+cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
+  const dim3 grid((unsigned)((a.T + 7) / 8));
+  const int v = (a.E + 31) / 32;
+  // Up to 256 experts in groups of whole lanes, a power of two of them: neighbours in a lane;
+  // warps go on to further tokens, so that the biases are read once.
+  if (!GRAD && v <= 8) {
+    const int V = v <= 1 ? 1 : v <= 2 ? 2 : v <= 4 ? 4 : 8, lanes = a.group_size / V;
+    if (a.groups == 1 || (a.group_size % V == 0 && (lanes & (lanes - 1)) == 0)) {
+      const dim3 g((unsigned)std::min<int64_t>(((a.T + 7) / 8), (int64_t)sms * kRouteBlocks));
+      const int vec = a.E % V == 0;
+      const bool grouped = a.groups > 1, scored = a.bias || (grouped && a.group_top == 2);
+      if (V == 1) return launch_lanes<L, 1, SCORE>(scored, grouped, g, s, a, vec);
+      if (V == 2) return launch_lanes<L, 2, SCORE>(scored, grouped, g, s, a, vec);
+      if (V == 4) return launch_lanes<L, 4, SCORE>(scored, grouped, g, s, a, vec);
+      return launch_lanes<L, 8, SCORE>(scored, grouped, g, s, a, vec);
+    }
+  }
+#define CUSYNC_ROUTE(V)                                                                     \
+  if (v <= V)                                                                               \
+    return GRAD ? launch(route_grad_kernel<L, V, SCORE>, grid, 256, 0, s, a)                \
+                : launch(route_any_kernel<L, V, SCORE>, grid, 256, 0, s, a);
+  CUSYNC_ROUTE(1)
+  CUSYNC_ROUTE(2)
+  CUSYNC_ROUTE(4)
+  CUSYNC_ROUTE(8)
+  CUSYNC_ROUTE(16)
+  CUSYNC_ROUTE(32)
+#undef CUSYNC_ROUTE
+  return cudaErrorInvalidValue;
+}
+
+template <typename L>
+cudaError_t route_logits(const RouteArgs& a, bool softmax, bool grad, int sms, cudaStream_t s) {
+  if (grad) return softmax ? launch_route<L, 0, true>(a, sms, s) : launch_route<L, 1, true>(a, sms, s);
+  return softmax ? launch_route<L, 0, false>(a, sms, s) : launch_route<L, 1, false>(a, sms, s);
 }
 
 }  // namespace moe
