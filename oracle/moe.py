@@ -3,7 +3,8 @@ dispatch order, the experts' MLP and its gradients, token by token and assignmen
 assignment, with a bound on what 16-bit stores and fp32 sums may change in each result.
 
 The bounds count, for every value: half a bf16 step (2^-8 of the value) where the device
-stores it in bf16, one fp32 step (2^-23) of the sum of magnitudes for every term of an fp32
+stores it in bf16, half an fp16 step (2^-11 of the largest of its 32 neighbours at most)
+where it stores a slot's row of the output before the sum over a token's experts, one fp32 step (2^-23) of the sum of magnitudes for every term of an fp32
 sum, and 2^-20 of the value for the device's exponential and division; each error is
 carried through the formula that uses the value by that formula's largest slope.
 """
@@ -11,6 +12,7 @@ carried through the formula that uses the value by that formula's largest slope.
 import numpy as np
 
 BF16 = 2.0 ** -8
+HALF = 2.0 ** -11  # an fp16 step of a value of the largest size in its block of 32, at most
 STEP = 2.0 ** -23
 FAST = 2.0 ** -20
 TILE_ROWS = 128
@@ -117,6 +119,14 @@ def plan(ids, E):
             "slot_of": slot_of.reshape(T, k), "row_of": row_of}
 
 
+def _blocks_of_32(o):
+    """The largest magnitude of each row's block of 32 columns, at every column."""
+    n, d = o.shape
+    pad = np.zeros((n, -(-d // 32) * 32))
+    pad[:, :d] = np.abs(o)
+    return np.repeat(pad.reshape(n, -1, 32).max(axis=2), 32, axis=1)[:, :d]
+
+
 _C = np.sqrt(2.0 / np.pi)
 
 
@@ -159,8 +169,10 @@ def mlp(X, W1t, W2t, ids, weights, act):
         h, dh, _ = _hidden(x, W1t[e], act, dz)
         dh = dh + BF16 * (np.abs(h) + dh)
         w = weights[t, j][:, None]
-        np.add.at(Y, t, w * (h @ W2t[e].T))
+        o = h @ W2t[e].T
+        np.add.at(Y, t, w * o)
         a2 = np.abs(W2t[e]).T
+        np.add.at(bound, t, np.abs(w) * HALF * (_blocks_of_32(o) * (1 + BF16)))
         np.add.at(bound, t, np.abs(w) * (dh @ a2 + (N1 + ids.shape[1] + 4) * STEP * (np.abs(h) @ a2)))
     return Y, bound + BF16 * (np.abs(Y) + bound)
 
@@ -191,6 +203,7 @@ def mlp_grad(X, W1t, W2t, ids, weights, dY, act):
                              for s, es in slopes], axis=1)
         ez = ez + BF16 * (np.abs(dz) + ez)
         np.add.at(dX, t, dz @ a)
+        np.add.at(bX, t, HALF * _blocks_of_32(dz @ a) * (1 + BF16))
         np.add.at(bX, t, ez @ np.abs(a) + (a.shape[0] + ids.shape[1]) * STEP * (np.abs(dz) @ np.abs(a)))
         dW1[e] = dz.T @ x
         b1[e] = ez.T @ np.abs(x) + (n + 64) * STEP * (np.abs(dz).T @ np.abs(x))

@@ -1,6 +1,7 @@
 // Host side of include/cusync_moe.h: argument checks, buffer layouts, TMA descriptors and
 // kernel launches of the expert layer.
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -24,8 +25,9 @@ namespace {
 static_assert(kTileRows == CUSYNC_MOE_TILE_ROWS, "the plan's alignment");
 static_assert(CUSYNC_MOE_MAX_EXPERTS <= kPlanThreads, "the plan scans the experts in one step");
 
-constexpr int64_t kPlanChunk = 4096;   // assignments of a plan block
-constexpr int64_t kPlanBlocks = 128;   // plan blocks at most
+constexpr int64_t kPlanAlone = 2048;   // assignments that one plan block takes
+constexpr int64_t kPlanChunk = 1024;   // assignments of a plan block, where there are more
+constexpr int64_t kPlanBlocks = 64;    // plan blocks at most
 // Assignments up to which the MLP runs without tiles.
 constexpr int64_t kSmallAssignments = 32;
 // Assignments per expert from which products take tiles of 256 rows on pairs of CTAs.
@@ -39,13 +41,13 @@ bool aligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u)
 
 // What a descriptor means, its defaults filled in.
 struct Layer {
-  int64_t T, D, N1, A, S, max_pairs;
+  int64_t T, D, N1, A, S, max_pairs, max_mids;
   int32_t E, k, G, groups, group_limit, group_top;
   int64_t chunk, blocks;                                          // plan
-  int64_t counts, offsets, tiles, pairs, slot_of, row_of, hist;   // plan, 32-bit words
+  int64_t counts, offsets, tiles, pairs, mids, slot_of, row_of, hist;  // plan, 32-bit words
   int64_t plan_bytes;
-  int64_t x, h, rows, work_bytes;                                 // forward work, bytes
-  int64_t gx, gy, gh, gz, grows, gpart, grad_bytes;                      // gradient work, bytes
+  int64_t x, h, rows, scales, work_bytes;                                // forward work, bytes
+  int64_t gx, gy, gh, gz, grows, gscales, gpart, grad_bytes;                      // gradient work, bytes
   int32_t parts;
 };
 
@@ -79,7 +81,7 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
   L->G = d->act == CUSYNC_MOE_SWIGLU ? 2 : 1;
   L->A = L->T * L->k;
   L->S = round_up(L->A + (kTileRows - 1) * std::min<int64_t>(L->E, L->A), kTileRows);
-  L->chunk = std::max(kPlanChunk, round_up(div_up(L->A, kPlanBlocks), kPlanThreads));
+  L->chunk = L->A <= kPlanAlone ? kPlanAlone : std::max(kPlanChunk, round_up(div_up(L->A, kPlanBlocks), kPlanThreads));
   L->blocks = std::max<int64_t>(1, div_up(L->A, L->chunk));
   int64_t w = PLAN_HEADER;
   auto take = [&w](int64_t n) {
@@ -92,11 +94,13 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
   L->tiles = take(4 * (L->S / kTileRows));
   L->max_pairs = L->A / (2 * kTileRows) + std::min<int64_t>(L->E, L->A);
   L->pairs = take(4 * L->max_pairs);
+  L->max_mids = L->A / kMidRows + std::min<int64_t>(L->E, L->A);
+  L->mids = take(4 * L->max_mids);
   L->slot_of = take(L->A);
   L->row_of = take(L->S);
   L->hist = take(L->blocks > 1 ? L->blocks * L->E : 0);
   L->plan_bytes = round_up(w * 4, 256);
-  L->x = L->h = L->rows = L->work_bytes = L->gx = L->gy = L->gh = L->gz = L->grows = L->gpart = L->grad_bytes = 0;
+  L->x = L->h = L->rows = L->scales = L->gscales = L->work_bytes = L->gx = L->gy = L->gh = L->gz = L->grows = L->gpart = L->grad_bytes = 0;
   L->parts = 0;
   if (d->D >= 1 && d->N1 >= 1) {
     int64_t b = L->plan_bytes;
@@ -107,7 +111,8 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     };
     L->x = bytes(L->S * L->D * 2);
     L->h = bytes(L->S * L->N1 * 2);
-    L->rows = bytes(L->S * L->D * 4);
+    L->rows = bytes(L->S * L->D * 2);
+    L->scales = bytes(L->S * div_up(L->D, 32) * 2);
     L->work_bytes = b;
     b = L->plan_bytes;
     L->parts = (int32_t)(8 * div_up(L->N1, 256));  // one for 32 columns
@@ -115,7 +120,8 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     L->gy = bytes(L->S * L->D * 2);
     L->gh = bytes(L->S * L->N1 * 2);
     L->gz = bytes(L->S * L->G * L->N1 * 2);
-    L->grows = bytes(L->S * L->D * 4);
+    L->grows = bytes(L->S * L->D * 2);
+    L->gscales = bytes(L->S * div_up(L->D, 32) * 2);
     L->gpart = bytes(L->S * L->parts * 4);
     L->grad_bytes = b;
   }
@@ -230,9 +236,9 @@ bool map_gate_up(CUtensorMap* m, const void* p, int64_t experts, int g, int64_t 
   return map_nd<3>(m, p, {d, (g * experts - (g - 1)) * n1, g}, {d, n1 * d}, {64, 128, g});
 }
 // Token rows by slot, in the four box heights.
-bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, bool wide, int blocks) {
+bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, bool wide, int blocks, int last = 128) {
   bool ok = true;
-  for (int i = 0; i < 4; ++i) ok = ok && map_rows(&m[i], p, rows, cols, 16 << i, wide, blocks);
+  for (int i = 0; i < 4; ++i) ok = ok && map_rows(&m[i], p, rows, cols, i < 3 ? 16 << i : last, wide, blocks);
   return ok;
 }
 
@@ -271,6 +277,7 @@ cudaError_t launch_plan(const Layer& L, const int32_t* ids, void* plan, cudaStre
   p.offsets = L.offsets;
   p.tiles = L.tiles;
   p.pairs = L.pairs;
+  p.mids = L.mids;
   p.slot_of = L.slot_of;
   p.row_of = L.row_of;
   p.hist = L.hist;
@@ -301,12 +308,13 @@ cudaError_t launch_gemm(GemmArgs a, const Layer& L, int sms, cudaStream_t s) {
   static_assert(MODE <= DW2 || MODE == FWD1G, "one counter for each product of a call");
   a.counter = PLAN_COUNTERS + (MODE == FWD1G ? FWD1 : MODE);
   using C = GemmCfg<MODE, ACT, PAIR>;
-  const bool wide = C::kCols == 256;
-  a.tiles = wide ? L.pairs : L.tiles;
+  constexpr int count = C::kTileCount;
+  a.tiles = count == PLAN_PAIRS ? L.pairs : count == PLAN_MIDS ? L.mids : L.tiles;
+  const int64_t row_tiles = count == PLAN_PAIRS ? L.max_pairs : count == PLAN_MIDS ? L.max_mids : L.S / kTileRows;
   a.m_tiles = (int32_t)div_up(a.M, C::kFeatures);
   a.n_tiles = C::kDw ? (int32_t)div_up(a.N, C::kCols) : 1;
   // an upper bound: how many tiles of rows there are is only known on the device
-  const int64_t tiles = (C::kDw ? (int64_t)a.E * a.n_tiles : wide ? L.max_pairs : L.S / kTileRows) * a.m_tiles;
+  const int64_t tiles = (C::kDw ? (int64_t)a.E * a.n_tiles : row_tiles) * a.m_tiles;
   const int grid = PAIR * (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / PAIR));
   return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, PAIR>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
 }
@@ -332,11 +340,13 @@ cudaError_t launch_dispatch(const Layer& L, void* work, const void* x, void* xs,
   return launch(dispatch_kernel, dim3((unsigned)blocks), kDispatchThreads, 0, s, d);
 }
 
-cudaError_t launch_combine(const Layer& L, void* work, const float* rows, const float* weights, void* out,
-                           const float* part, float* dweights, cudaStream_t s) {
+cudaError_t launch_combine(const Layer& L, void* work, const void* rows, const void* scale, const float* weights,
+                           void* out, const float* part, float* dweights, cudaStream_t s) {
   CombineArgs c = {};
   c.plan = static_cast<int32_t*>(work);
-  c.rows = rows;
+  c.rows = static_cast<const __half*>(rows);
+  c.scale = static_cast<const uint16_t*>(scale);
+  c.scales = (int32_t)div_up(L.D, 32);
   c.weights = weights;
   c.out = out;
   c.part = part;
@@ -347,7 +357,7 @@ cudaError_t launch_combine(const Layer& L, void* work, const float* rows, const 
   c.D = (int32_t)L.D;
   c.parts = L.parts;
   c.used = (int32_t)div_up(L.N1, 32);
-  return launch(combine_kernel, dim3((unsigned)L.T, (unsigned)div_up(L.D, 4 * kCombineThreads)), kCombineThreads, 0, s,
+  return launch(combine_kernel, dim3((unsigned)L.T, (unsigned)div_up(L.D, 8 * kCombineThreads)), kCombineThreads, 0, s,
                 c);
 }
 
@@ -444,7 +454,9 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
     a.E = L.E;
     a.D = (int32_t)L.D;
     a.N1 = (int32_t)L.N1;
-    const dim3 up((unsigned)div_up(L.A * L.N1, kSmallThreads / 32)), down((unsigned)div_up(L.T * L.D, kSmallThreads / 32));
+    const int64_t most = (int64_t)sms * kSmallBlocks;
+    const dim3 up((unsigned)std::min(most, div_up(L.A * L.N1, kSmallThreads / 32)));
+    const dim3 down((unsigned)std::min(most, div_up(L.T * L.D, kSmallThreads / 32)));
     cudaError_t e = L.G == 2 ? launch(small_up_kernel<1>, up, kSmallThreads, 0, s, a)
                              : launch(small_up_kernel<0>, up, kSmallThreads, 0, s, a);
     if (e == cudaSuccess) e = launch(small_down_kernel, down, kSmallThreads, 0, s, a);
@@ -461,6 +473,8 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   b.M = (int32_t)L.D;
   b.K = (int32_t)L.N1;
   b.out = w + L.rows;
+  b.out2 = w + L.scales;
+  b.scales = (int32_t)div_up(L.D, 32);
   const bool wide = L.D % 64 == 0 && L.N1 % 64 == 0;
   a.wide = b.wide = wide;
   if (!(L.G == 2 ? map_gated(&a.mA, W1t, L.E, L.N1, L.D, wide, 2)
@@ -478,7 +492,7 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   }
   if (e == cudaSuccess) e = launch_gemm<FWD2, 0>(pair, b, L, sms, s);
   if (e == cudaSuccess)
-    e = launch_combine(L, work, reinterpret_cast<float*>(w + L.rows), weights, Y, nullptr, nullptr, s);
+    e = launch_combine(L, work, w + L.rows, w + L.scales, weights, Y, nullptr, nullptr, s);
   return status_of(e);
 }
 
@@ -505,7 +519,8 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   const int64_t H = L.G * L.N1;
   const bool pair = use_pairs(L, sms), pair1 = H > 128 && sms >= 2, pair2 = L.D > 128 && sms >= 2;  // rows: slots; the weights' gradients'
   void *gx = w + L.gx, *gy = w + L.gy, *gh = w + L.gh, *gz = w + L.gz;
-  float *rows = reinterpret_cast<float*>(w + L.grows), *part = reinterpret_cast<float*>(w + L.gpart);
+  void* rows = w + L.grows;
+  float* part = reinterpret_cast<float*>(w + L.gpart);
 
   GemmArgs p = gemm_args(L, work, weights);  // hidden layer and its gradient
   p.M = (int32_t)L.N1;
@@ -518,6 +533,8 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   x.M = (int32_t)L.D;
   x.K = (int32_t)H;
   x.out = rows;
+  x.out2 = w + L.gscales;
+  x.scales = (int32_t)div_up(L.D, 32);
   GemmArgs w1 = gemm_args(L, work, weights);
   w1.M = (int32_t)H;
   w1.N = (int32_t)L.D;
@@ -530,9 +547,10 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   p.wide = x.wide = w1.wide = w2.wide = wide;
   // a weight gradient's stage holds two blocks of 64 rows on pairs, one on single CTAs
   const int kr1 = wide && pair1 ? 128 : 64, kr2 = wide && pair2 ? 128 : 64;
+  const int last = pair ? kMidRows / 2 : 128;  // BWD1's highest token box
   // BWD1's stage holds one block, DX's two
   if (!map_gate_up(&p.mA, W1t, L.E, L.G, L.N1, L.D, wide) || !map_weights(&p.mA2, W2t, L.E, L.D, L.N1, 64, wide, 2) ||
-      !map_tokens(p.mB, gx, L.S, L.D, wide, 1) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1) ||
+      !map_tokens(p.mB, gx, L.S, L.D, wide, 1, last) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1, last) ||
       !map_weights(&x.mA, W1t, L.E, H, L.D, wide ? 128 : 64, wide, 2) || !map_tokens(x.mB, gz, L.S, H, wide, 2) ||
       !map_rows(&w1.mA, gz, L.S, H, kr1, wide, 2) || !map_rows(&w1.mB[0], gx, L.S, L.D, kr1, wide, 2) ||
       !map_rows(&w2.mA, gy, L.S, L.D, kr2, wide, 2) || !map_rows(&w2.mB[0], gh, L.S, L.N1, kr2, wide, 2))
@@ -546,7 +564,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if (e == cudaSuccess)
     e = L.G == 2 ? launch_gemm<BWD1, 1>(pair, p, L, sms, s) : launch_gemm<BWD1, 0>(pair, p, L, sms, s);
   if (e == cudaSuccess) e = launch_gemm<DX, 0>(pair, x, L, sms, s);
-  if (e == cudaSuccess) e = launch_combine(L, work, rows, nullptr, dX, part, dweights, s);
+  if (e == cudaSuccess) e = launch_combine(L, work, rows, w + L.gscales, nullptr, dX, part, dweights, s);
   if (e == cudaSuccess) e = launch_gemm<DW1, 0>(pair1, w1, L, sms, s);
   if (e == cudaSuccess) e = launch_gemm<DW2, 0>(pair2, w2, L, sms, s);
   return status_of(e);

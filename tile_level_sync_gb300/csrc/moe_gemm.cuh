@@ -10,10 +10,10 @@
 //   mode   A (M)                      B (N)                  epilogue
 //   FWD1   W1t[e] rows (G * N1)       X by slot              h = act(z), bf16
 //   FWD1G  the same                   X (gather)
-//   FWD2   W2t[e] rows (D)            H                      O, fp32
+//   FWD2   W2t[e] rows (D)            H                      O, fp16 scaled by 32 columns
 //   BWD1   W1t[e] gate, up;           X; dY by slot          dZ and w h, bf16; sums of dH h
 //          W2t[e] along N1
-//   DX     W1t[e] along D             dZ                     dX per slot, fp32
+//   DX     W1t[e] along D             dZ                     dX per slot, as O
 //   DW1    dZ along G * N1            X along D              dW1t[e], bf16   (K = slots)
 //   DW2    dY along D                 w h along N1           dW2t[e], bf16   (K = slots)
 //
@@ -38,6 +38,10 @@
 // brings 128 rows x 64 columns in 1.25 us, more than twice what their MMAs take: it is for
 // tiles of few rows.
 //
+// O and dX per slot are sums over a token's experts in fp32 still to be made: their 16 bits
+// are fp16 with a power of two for 32 columns of 32 rows (kept for each row), an error of
+// 2^-12 beside the 2^-9 of the bf16 result, at half the bytes of fp32.
+//
 // Token rows behind an expert's last one are columns of their own and are not stored.  In
 // the weight gradients K runs over slots in steps of 16: dispatch_kernel and BWD1 store
 // zeros up to the step's end.
@@ -45,6 +49,7 @@
 // Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -66,19 +71,20 @@ constexpr uint32_t kErrWait = 3u << 24;      // the pipeline-wait class of the c
 struct GemmArgs {
   CUtensorMap mA;      // weights; DW: dZ or dY
   CUtensorMap mA2;     // BWD1: W2t
-  CUtensorMap mB[4];   // tokens, boxes of 16, 32, 64 and 128 rows (gather: [0], one row); DW: [0], 64 rows
+  CUtensorMap mB[4];   // tokens, boxes of 16, 32, 64 and 128 (BWD1 on pairs: 80) rows (gather: [0],
+                       // one row); DW: [0], 64 rows
   CUtensorMap mB2[4];  // BWD1: dY
   int32_t* plan;
   const float* weights;
   void* out;           // H, O, dZ, dX per slot, dW1t or dW2t
-  void* out2;          // BWD1: w H
+  void* out2;          // BWD1: w H; FWD2, DX: scales, bf16 [slot][scales]
   float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
   int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
   int32_t T, k, E;
   int32_t M;           // output columns (DW: rows of an expert's matrix)
   int32_t N;           // DW: output columns
   int32_t K;           // reduction length (not DW)
-  int32_t m_tiles, n_tiles, parts;
+  int32_t m_tiles, n_tiles, parts, scales;
   int32_t counter;     // plan word that counts this launch's claimed tiles
   // Every width is a multiple of 64: the maps see rows as [width / 64][rows][64], and one
   // copy brings an operand's two blocks of 64 k, or its two chunks of 64 columns, at once.
@@ -96,7 +102,10 @@ struct GemmCfg {
   static constexpr int kG = ACT == 1 ? 2 : 1;
   static constexpr int kAParts = kBwd1 ? kG + 1 : 1;       // 128 x 64 blocks of A in a stage
   static constexpr int kBParts = kBwd1 ? 2 : 1;
-  static constexpr int kCols = kDw ? 256 : (PAIR == 2 && !kBwd1) ? 256 : 128;  // widest tile
+  // widest tile: BWD1's three accumulators leave room for 160 columns
+  static constexpr int kCols = kDw ? 256 : PAIR == 1 ? 128 : kBwd1 ? 160 : 256;
+  static constexpr int kTileCount = kCols == 256 ? PLAN_PAIRS : kCols == 160 ? PLAN_MIDS : PLAN_TILES;
+  static constexpr int kLastBox = kCols / PAIR;            // rows of the highest token box
   static constexpr int kColStep = 16 * PAIR;               // of the MMA's width
   static constexpr int kBBytes = kCols / PAIR * 128;       // a CTA's share of B
   static constexpr int kABytes = 128 * 128;
@@ -109,6 +118,7 @@ struct GemmCfg {
   static constexpr int kAccCols = kAParts * kCols;
   static constexpr int kAccs = 2 * kAccCols <= 512 ? 2 : 1;
   static constexpr int kTmemCols = kAccs * kAccCols <= 256 ? 256 : 512;
+  static_assert(kAccs * kAccCols <= 512, "TMEM columns");
   static constexpr int kFeatures = (kGated ? 64 : 128) * PAIR;  // output columns of a tile (DW: rows)
   static constexpr int kSmemBytes = kStages * kStageBytes + kStageOut + 1024;
 };
@@ -138,7 +148,7 @@ struct Tile {
 template <int MODE, int ACT, int PAIR>
 __device__ __forceinline__ int32_t tile_total(const GemmArgs& a) {
   if (GemmCfg<MODE, ACT, PAIR>::kDw) return a.E * a.m_tiles * a.n_tiles;
-  return a.plan[GemmCfg<MODE, ACT, PAIR>::kCols == 256 ? PLAN_PAIRS : PLAN_TILES] * a.m_tiles;
+  return a.plan[GemmCfg<MODE, ACT, PAIR>::kTileCount] * a.m_tiles;
 }
 
 template <int MODE, int ACT, int PAIR>
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         auto token = [&](int32_t x) { return x < 0 ? a.T : x / a.k; };
         tok = make_int4(token(r.x), token(r.y), token(r.z), token(r.w));
       }
-      const uint32_t b_bytes = C::kGather ? live * 512 : C::kDw ? C::kBBytes : (16 << pick) * 128;
+      const uint32_t b_bytes = C::kGather ? live * 512 : C::kDw ? C::kBBytes : (pick == 3 ? C::kLastBox : 16 << pick) * 128;
       const uint32_t block_bytes = PAIR * (C::kAParts * C::kABytes + C::kBParts * b_bytes);
       // Nothing orders the two warps' copies: the barrier's phase cannot end before warp 0's
       // arrival.
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         if (q.nkb == 0) continue;  // an expert without rows: the epilogue writes zeros
         const uint32_t cols = C::kDw ? C::kCols : (q.rows + C::kColStep - 1) / C::kColStep * C::kColStep;
         const uint32_t share = cols / PAIR;
-        const uint32_t box_bytes = (share <= 16 ? 16 : share <= 32 ? 32 : share <= 64 ? 64 : 128) * 128;
+        const uint32_t box_bytes = (share <= 16 ? 16 : share <= 32 ? 32 : share <= 64 ? 64 : C::kLastBox) * 128;
         const uint32_t idesc = ptx::idesc_bf16_f32(128 * PAIR, cols) | (C::kMnA ? ptx::kIdescAMn : 0) |
                                (C::kDw ? ptx::kIdescBMn : 0);
         const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
@@ -591,7 +601,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
             if (2 * i < left) store_bf16(out + (int64_t)(2 * i) * a.M, g * sigmoid_fast(g) * u);
           }
         }
-      } else if (C::kFwd1 || MODE == FWD2 || MODE == DX) {
+      } else if (C::kFwd1) {
         const int f = q.m0 + lane0 + lane;
 #pragma unroll 1
         for (int c = half * 32; c < q.rows; c += 64) {
@@ -599,15 +609,44 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
           const int left = f < a.M ? q.rows - c : 0;
-          const int64_t at = (int64_t)(q.slot0 + c) * a.M + f;
+          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float v = __uint_as_float(z[i]);
-            if (i < left) {
-              if (C::kFwd1) store_bf16(reinterpret_cast<uint16_t*>(a.out) + at + (int64_t)i * a.M, v * gelu_gate(v));
-              else reinterpret_cast<float*>(a.out)[at + (int64_t)i * a.M] = v;
-            }
+            if (i < left) store_bf16(out + (int64_t)i * a.M, v * gelu_gate(v));
           }
+        }
+      } else if (MODE == FWD2 || MODE == DX) {
+        const int f = q.m0 + lane0 + lane;
+#pragma unroll 1
+        for (int c = half * 32; c < q.rows; c += 64) {
+          uint32_t z[32];
+          ptx::tmem_ld_32x32b_x32(d + c, z);
+          ptx::tmem_ld_wait();
+          const int left = f < a.M ? q.rows - c : 0;
+          __half* out = reinterpret_cast<__half*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
+          // the largest finite value of 32 tokens x 32 columns is put into [2^14, 2^15); what is
+          // above 2^-29 of it keeps fp16's precision
+          float most = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < left) most = fmaxf(most, fabsf(__uint_as_float(z[i])));
+          uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+          if (top >= 0x7f800000u) {  // an infinity among them: without those
+            most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < left && (z[i] & 0x7fffffffu) < 0x7f800000u) most = fmaxf(most, fabsf(__uint_as_float(z[i])));
+            top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+          }
+          const uint32_t e = max(top >> 23, 15u);
+          const float by = __uint_as_float((268u - e) << 23);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < left) out[(int64_t)i * a.M] = __float2half_rn(__uint_as_float(z[i]) * by);
+          if (c + lane < q.rows && q.m0 + lane0 < a.M)
+            reinterpret_cast<uint16_t*>(a.out2)[(int64_t)(q.slot0 + c + lane) * a.scales + (q.m0 + lane0) / 32] =
+                (uint16_t)((e - 14u) << 7);
         }
       } else if (C::kBwd1) {
         const int f = q.m0 + lane0 + lane;

@@ -2,7 +2,7 @@
 //
 // A plan is an array of 32-bit words: a header, the experts' counts, the offsets of their
 // first slots (multiples of kTileRows, so that a 128-row tile of a product belongs to one
-// expert), the row tiles {expert, first slot, rows} of up to 128 rows and those of up to 256, slot_of (assignment -> slot) and row_of (slot
+// expert), the row tiles {expert, first slot, rows} of up to 128, 160 and 256 rows, slot_of (assignment -> slot) and row_of (slot
 // -> assignment).
 //
 // Blocks take consecutive chunks of the ids, a block's warps consecutive parts of its
@@ -20,9 +20,10 @@ namespace cusync {
 namespace moe {
 
 constexpr int kTileRows = 128;
+constexpr int kMidRows = 160;  // rows of BWD1's tiles on pairs
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
-enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_PAIRS = 3, PLAN_COUNTERS = 8, PLAN_HEADER = 16 };
+enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_PAIRS = 3, PLAN_MIDS = 4, PLAN_COUNTERS = 8, PLAN_HEADER = 16 };
 
 struct PlanArgs {
   const int32_t* ids;
@@ -32,7 +33,7 @@ struct PlanArgs {
   int32_t E;
   int32_t blocks;       // 1: no histogram kernel ran
   int64_t chunk;        // assignments of a block (a multiple of kPlanThreads)
-  int64_t counts, offsets, tiles, pairs, slot_of, row_of, hist;  // word offsets
+  int64_t counts, offsets, tiles, pairs, mids, slot_of, row_of, hist;  // word offsets
 };
 
 __device__ __forceinline__ int plan_id(const PlanArgs& a, int64_t i, int64_t end) {
@@ -65,8 +66,8 @@ __device__ __forceinline__ void cut_tiles(int4* out, int e, int o, int c, int mo
 }
 
 // Shared memory of plan_kernel: per-warp histograms [kPlanWarps][E], then before[E],
-// count[E], offset[E + 1], pair[E + 1], and the scan's 32 partial sums of 64 bits.
-__host__ __device__ inline int plan_scan_at(int E) { return (kPlanWarps * E + 4 * E + 2 + 1) & ~1; }
+// count[E], offset[E + 1], pair[E + 1], mid[E + 1], and the scan's 32 partial sums of 64 bits.
+__host__ __device__ inline int plan_scan_at(int E) { return (kPlanWarps * E + 5 * E + 3 + 1) & ~1; }
 __host__ __device__ inline size_t plan_smem(int E) { return (size_t)plan_scan_at(E) * 4 + 32 * 8; }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   uint32_t* count = before + E;
   uint32_t* offset = count + E;
   uint32_t* pair = offset + E + 1;
+  uint32_t* mid = pair + E + 1;
   uint64_t* part = reinterpret_cast<uint64_t*>(sh + plan_scan_at(E));
   for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) whist[i] = 0;
   for (int e = tid; e < E; e += kPlanThreads) before[e] = count[e] = 0;
@@ -129,12 +131,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
     if (a.blocks == 1) count[e] = c;
   }
   __syncthreads();
-  // offsets: exclusive scans of the counts in whole tiles and in whole pairs of tiles
-  // (E <= kPlanThreads)
+  // offsets: exclusive scans of the counts in whole tiles of each kind (E <= kPlanThreads)
   {
     const uint32_t n = tid < E ? count[tid] : 0;
-    // tiles in the low 32 bits, pairs in the high ones
-    const uint64_t v = (n + kTileRows - 1) / kTileRows + ((uint64_t)((n + 2 * kTileRows - 1) / (2 * kTileRows)) << 32);
+    // 21 bits each (at most 2^17 + 2^10 tiles): of 128 rows, of 256, of 160
+    const uint64_t v = (n + kTileRows - 1) / kTileRows + ((uint64_t)((n + 2 * kTileRows - 1) / (2 * kTileRows)) << 21) +
+                       ((uint64_t)((n + kMidRows - 1) / kMidRows) << 42);
     uint64_t s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -156,11 +158,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
     __syncthreads();
     if (tid < E) {
       s += part[warp];
-      offset[tid] = (uint32_t)(s - v) * kTileRows;
-      pair[tid] = (uint32_t)((s - v) >> 32);
+      const uint64_t from = s - v;
+      offset[tid] = (uint32_t)(from & 0x1fffff) * kTileRows;
+      pair[tid] = (uint32_t)(from >> 21) & 0x1fffff;
+      mid[tid] = (uint32_t)(from >> 42);
       if (tid == E - 1) {
-        offset[E] = (uint32_t)s * kTileRows;
-        pair[E] = (uint32_t)(s >> 32);
+        offset[E] = (uint32_t)(s & 0x1fffff) * kTileRows;
+        pair[E] = (uint32_t)(s >> 21) & 0x1fffff;
+        mid[E] = (uint32_t)(s >> 42);
       }
     }
   }
@@ -172,6 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
       a.plan[PLAN_ERR] = 0;
       a.plan[PLAN_TILES] = (int32_t)(used / kTileRows);
       a.plan[PLAN_PAIRS] = (int32_t)pair[E];
+      a.plan[PLAN_MIDS] = (int32_t)mid[E];
     }
     for (int e = tid; e < E; e += kPlanThreads) a.plan[a.counts + e] = (int32_t)count[e];
     for (int e = tid; e <= E; e += kPlanThreads) a.plan[a.offsets + e] = (int32_t)offset[e];
@@ -183,6 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
     const int c = (int)count[e];
     cut_tiles(reinterpret_cast<int4*>(a.plan + a.tiles) + o / kTileRows, e, (int)o, c, kTileRows, lane);
     cut_tiles(reinterpret_cast<int4*>(a.plan + a.pairs) + pair[e], e, (int)o, c, 2 * kTileRows, lane);
+    cut_tiles(reinterpret_cast<int4*>(a.plan + a.mids) + mid[e], e, (int)o, c, kMidRows, lane);
     for (int64_t i = o + count[e] + lane; i < n; i += 32) row_of[i] = -1;
   }
   for (int64_t i = used + (int64_t)blockIdx.x * kPlanThreads + tid; i < a.S; i += (int64_t)gridDim.x * kPlanThreads)

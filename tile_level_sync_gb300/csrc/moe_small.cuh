@@ -2,6 +2,7 @@
 // experts, and the MLP of a few tokens without tiles.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -14,13 +15,14 @@ namespace moe {
 
 struct CombineArgs {
   int32_t* plan;
-  const float* rows;     // [slots, D] fp32
+  const __half* rows;    // [slots, D], scaled by 32 columns
+  const uint16_t* scale; // bf16 [slots, ceil(D / 32)]
   const float* weights;  // [T, k], or null: plain sums
   void* out;             // [T, D] bf16
   const float* part;     // gradient: sums of dH h, [slots][parts]; null otherwise
   float* dweights;       // [T, k]
   int64_t slot_of;
-  int32_t T, k, D, parts, used;  // used: sums of a slot, of parts
+  int32_t T, k, D, scales, parts, used;  // used: sums of a slot, of parts
 };
 
 struct DispatchArgs {
@@ -57,29 +59,35 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(DispatchArgs
 constexpr int kCombineThreads = 256;
 
 // out[t] = sum_j weights[t,j] rows[slot_of[t,j]], in the order of j, in fp32; one rounding.
-// A block takes one token's next 4 * kCombineThreads columns.  With `part`, the first
-// block of a token also adds up dweights from the column tiles' partial sums, in order.
+// A block takes one token's next 8 * kCombineThreads columns.  With `part`, the first block
+// of a token also adds up dweights from the column tiles' partial sums, in order.
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int64_t t = blockIdx.x;
   const int32_t* slots = a.plan + a.slot_of + t * a.k;
-  const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * 4;
+  const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * 8;
   if (c < a.D) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.0f;
 #pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
       const int32_t slot = slots[j];
       if (slot < 0) continue;
+      const uint4 v = __ldcs(reinterpret_cast<const uint4*>(a.rows + (int64_t)slot * a.D + c));
+      const float unit = __uint_as_float((uint32_t)a.scale[(int64_t)slot * a.scales + c / 32] << 16);
       const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(a.rows + (int64_t)slot * a.D + c));
-      s.x += w * v.x;
-      s.y += w * v.y;
-      s.z += w * v.z;
-      s.w += w * v.w;
+      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&words[i]));
+        s[2 * i] += w * (f.x * unit);
+        s[2 * i + 1] += w * (f.y * unit);
+      }
     }
-    uint2 p = make_uint2(pack2(s.x, s.y), pack2(s.z, s.w));
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + t * a.D + c) = p;
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + t * a.D + c) =
+        make_uint4(pack2(s[0], s[1]), pack2(s[2], s[3]), pack2(s[4], s[5]), pack2(s[6], s[7]));
   }
   if (a.part && blockIdx.y == 0 && threadIdx.x < a.k) {
     const int32_t slot = slots[threadIdx.x];
@@ -132,60 +140,96 @@ __device__ __forceinline__ float warp_add(float v) {
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
 constexpr int kSmallThreads = 256;
+constexpr int kSmallBlocks = 4;  // of each kernel on an SM: both fit at once
 
-// h[a][n] = act(X[t] . W1 rows of the chosen expert): a warp per (assignment, n).
+// h[a][n] = act(X[t] . W1 rows of the chosen expert): a warp per (assignment, n) at a time.
+// All blocks are resident from the start, so that those of small_down_kernel, which fit
+// beside them, can begin to bring their weights to L2.
 template <int ACT>
-__global__ void __launch_bounds__(kSmallThreads) small_up_kernel(SmallArgs a) {
+__global__ void __launch_bounds__(kSmallThreads, kSmallBlocks) small_up_kernel(SmallArgs a) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
+  const int64_t units = (int64_t)a.T * a.k * a.N1, warps = (int64_t)gridDim.x * (kSmallThreads / 32);
+  int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
   if (u == 0 && lane == 0) *a.err = 0;
-  const int as = (int)(u / a.N1), n = (int)(u - (int64_t)as * a.N1);
-  if (as >= a.T * a.k) return;
-  const int e = a.ids[as];
-  if ((unsigned)e >= (unsigned)a.E) return;
-  const uint16_t* x = a.X + (int64_t)(as / a.k) * a.D;
-  const uint16_t* w = a.W1t + ((int64_t)e * (ACT == 1 ? 2 : 1) * a.N1 + n) * a.D;
-  const uint16_t* v = w + (int64_t)a.N1 * a.D;
-  float z = 0.0f, g = 0.0f;
-#pragma unroll 8
-  for (int c = lane * 8; c < a.D; c += 256) {
-    const uint4 xx = *reinterpret_cast<const uint4*>(x + c);
-    z = dot8(ld_stream(w + c), xx, z);
-    if (ACT == 1) g = dot8(ld_stream(v + c), xx, g);
-  }
-  z = warp_add(z);
-  if (ACT == 1) g = warp_add(g);
-  if (lane == 0) a.h[(int64_t)as * a.N1 + n] = ACT == 1 ? z * sigmoid_fast(z) * g : z * gelu_gate(z);
-}
-
-// Y[t][d] = sum_j weights[t,j] W2[e_j][d] . h[t,j]: a warp per (t, d), in the order of j.
-__global__ void __launch_bounds__(kSmallThreads) small_down_kernel(SmallArgs a) {
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
-  const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
-  if (t >= a.T) return;
-  float y = 0.0f;
-#pragma unroll 2
-  for (int j = 0; j < a.k; ++j) {
-    const int as = t * a.k + j;
+  for (; u < units; u += warps) {
+    const int as = (int)(u / a.N1), n = (int)(u - (int64_t)as * a.N1);
     const int e = a.ids[as];
     if ((unsigned)e >= (unsigned)a.E) continue;
-    const uint16_t* w = a.W2t + ((int64_t)e * a.D + d) * a.N1;
-    const float* h = a.h + (int64_t)as * a.N1;
-    float s = 0.0f;
+    const uint16_t* x = a.X + (int64_t)(as / a.k) * a.D;
+    const uint16_t* w = a.W1t + ((int64_t)e * (ACT == 1 ? 2 : 1) * a.N1 + n) * a.D;
+    const uint16_t* v = w + (int64_t)a.N1 * a.D;
+    float z = 0.0f, g = 0.0f;
 #pragma unroll 4
-    for (int c = lane * 8; c < a.N1; c += 256) {
-      const float4 p = *reinterpret_cast<const float4*>(h + c), q = *reinterpret_cast<const float4*>(h + c + 4);
-      s = dot8f(ld_stream(w + c), p, q, s);
+    for (int c = lane * 8; c < a.D; c += 256) {
+      const uint4 ww = ld_stream(w + c);
+      uint4 vv;
+      if (ACT == 1) vv = ld_stream(v + c);
+      const uint4 xx = *reinterpret_cast<const uint4*>(x + c);
+      z = dot8(ww, xx, z);
+      if (ACT == 1) g = dot8(vv, xx, g);
     }
-    y += a.weights[as] * s;
+    z = warp_add(z);
+    if (ACT == 1) g = warp_add(g);
+    if (lane == 0) a.h[(int64_t)as * a.N1 + n] = ACT == 1 ? z * sigmoid_fast(z) * g : z * gelu_gate(z);
   }
-  y = warp_add(y);
-  if (lane == 0) a.Y[(int64_t)t * a.D + d] = (uint16_t)(pack2(y, 0.0f) & 0xffffu);
+}
+
+// Y[t][d] = sum_j weights[t,j] W2[e_j][d] . h[t,j]: a warp per (t, d) at a time, in the order
+// of j.  It starts while small_up_kernel still runs (whose own start waited for the kernel
+// before it, so the ids are there) and brings its first rows of W2t to L2 before it waits.
+__global__ void __launch_bounds__(kSmallThreads, kSmallBlocks) small_down_kernel(SmallArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t units = (int64_t)a.T * a.D, warps = (int64_t)gridDim.x * (kSmallThreads / 32);
+  int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
+  if (u < units) {
+    const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
+    for (int j = 0; j < a.k; ++j) {
+      const int e = __ldcg(a.ids + t * a.k + j);
+      if ((unsigned)e >= (unsigned)a.E) continue;
+      const uint16_t* w = a.W2t + ((int64_t)e * a.D + d) * a.N1;
+      for (int c = lane * 64; c < a.N1; c += 32 * 64)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + c));
+    }
+  }
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  for (; u < units; u += warps) {
+    const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
+    float y = 0.0f;
+    for (int j0 = 0; j0 < a.k; j0 += 4) {  // four experts' rows at a time, all loads in flight together
+      const uint16_t* w[4];
+      const float* h = a.h + (int64_t)(t * a.k + j0) * a.N1;
+      float s[4], f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = j0 + i < a.k ? a.ids[t * a.k + j0 + i] : -1;
+        const bool on = (unsigned)e < (unsigned)a.E;
+        w[i] = on ? a.W2t + ((int64_t)e * a.D + d) * a.N1 : nullptr;
+        f[i] = on ? a.weights[t * a.k + j0 + i] : 0.0f;
+        s[i] = 0.0f;
+      }
+#pragma unroll 2
+      for (int c = lane * 8; c < a.N1; c += 256) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (w[i]) v[i] = ld_stream(w[i] + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (w[i]) {
+            const float4* p = reinterpret_cast<const float4*>(h + (int64_t)i * a.N1 + c);
+            s[i] = dot8f(v[i], p[0], p[1], s[i]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (w[i]) y += f[i] * s[i];
+    }
+    y = warp_add(y);
+    if (lane == 0) a.Y[(int64_t)t * a.D + d] = (uint16_t)(pack2(y, 0.0f) & 0xffffu);
+  }
 }
 
 }  // namespace moe
