@@ -456,7 +456,7 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
     a.N1 = (int32_t)L.N1;
     const int64_t most = (int64_t)sms * kSmallBlocks;
     const dim3 up((unsigned)std::min(most, div_up(L.A * L.N1, kSmallThreads / 32)));
-    const dim3 down((unsigned)std::min(most, div_up(L.T * L.D, kSmallThreads / 32)));
+    const dim3 down((unsigned)std::min(most, div_up(L.T * L.D, kDownUnits)));
     cudaError_t e = L.G == 2 ? launch(small_up_kernel<1>, up, kSmallThreads, 0, s, a)
                              : launch(small_up_kernel<0>, up, kSmallThreads, 0, s, a);
     if (e == cudaSuccess) e = launch(small_down_kernel, down, kSmallThreads, 0, s, a);

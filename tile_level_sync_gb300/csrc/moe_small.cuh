@@ -176,59 +176,70 @@ __global__ void __launch_bounds__(kSmallThreads, kSmallBlocks) small_up_kernel(S
   }
 }
 
-// Y[t][d] = sum_j weights[t,j] W2[e_j][d] . h[t,j]: a warp per (t, d) at a time, in the order
-// of j.  It starts while small_up_kernel still runs (whose own start waited for the kernel
-// before it, so the ids are there) and brings its first rows of W2t to L2 before it waits.
+// Y[t][d] = sum_j weights[t,j] W2[e_j][d] . h[t,j]: four warps per (t, d) at a time, each with
+// a quarter of the token's experts, their sums added in the order of j.  It starts while
+// small_up_kernel still runs (whose own start waited for the kernel before it, so the ids are
+// there) and brings its first rows of W2t to L2 before it waits.
+constexpr int kDownSplit = 4;
+constexpr int kDownUnits = kSmallThreads / 32 / kDownSplit;  // (t, d) of a block at a time
 __global__ void __launch_bounds__(kSmallThreads, kSmallBlocks) small_down_kernel(SmallArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t units = (int64_t)a.T * a.D, warps = (int64_t)gridDim.x * (kSmallThreads / 32);
-  int64_t u = (int64_t)blockIdx.x * (kSmallThreads / 32) + (threadIdx.x >> 5);
+  __shared__ float sums[2][kDownUnits][kDownSplit];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = warp % kDownSplit, mine = warp / kDownSplit;
+  const int j0 = part * a.k / kDownSplit, j1 = (part + 1) * a.k / kDownSplit;
+  const int64_t units = (int64_t)a.T * a.D;
+  int64_t u = (int64_t)blockIdx.x * kDownUnits + mine;
   if (u < units) {
     const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
-    for (int j = 0; j < a.k; ++j) {
+    for (int j = j0; j < j1; ++j) {
       const int e = __ldcg(a.ids + t * a.k + j);
       if ((unsigned)e >= (unsigned)a.E) continue;
       const uint16_t* w = a.W2t + ((int64_t)e * a.D + d) * a.N1;
-      for (int c = lane * 64; c < a.N1; c += 32 * 64)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + c));
+      for (int c = lane * 64; c < a.N1; c += 32 * 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + c));
     }
   }
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  for (; u < units; u += warps) {
-    const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
+  for (int64_t base = (int64_t)blockIdx.x * kDownUnits, n = 0; base < units;
+       base += (int64_t)gridDim.x * kDownUnits, ++n) {
+    u = base + mine;
     float y = 0.0f;
-    for (int j0 = 0; j0 < a.k; j0 += 4) {  // four experts' rows at a time, all loads in flight together
-      const uint16_t* w[4];
-      const float* h = a.h + (int64_t)(t * a.k + j0) * a.N1;
-      float s[4], f[4];
+    const int t = (int)(u / a.D), d = (int)(u - (int64_t)t * a.D);
+    if (u < units)
+      for (int j = j0; j < j1; j += 2) {  // two experts' rows at a time, their loads in flight together
+        const uint16_t* w[2];
+        const float* h = a.h + (int64_t)(t * a.k + j) * a.N1;
+        float s[2] = {0.0f, 0.0f}, f[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = j0 + i < a.k ? a.ids[t * a.k + j0 + i] : -1;
-        const bool on = (unsigned)e < (unsigned)a.E;
-        w[i] = on ? a.W2t + ((int64_t)e * a.D + d) * a.N1 : nullptr;
-        f[i] = on ? a.weights[t * a.k + j0 + i] : 0.0f;
-        s[i] = 0.0f;
+        for (int i = 0; i < 2; ++i) {
+          const int e = j + i < j1 ? a.ids[t * a.k + j + i] : -1;
+          const bool on = (unsigned)e < (unsigned)a.E;
+          w[i] = on ? a.W2t + ((int64_t)e * a.D + d) * a.N1 : nullptr;
+          f[i] = on ? a.weights[t * a.k + j + i] : 0.0f;
+        }
+#pragma unroll 4
+        for (int c = lane * 8; c < a.N1; c += 256) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (w[i]) {
+              const uint4 v = ld_stream(w[i] + c);
+              const float4* p = reinterpret_cast<const float4*>(h + (int64_t)i * a.N1 + c);
+              s[i] = dot8f(v, p[0], p[1], s[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (w[i]) y += f[i] * s[i];
       }
-#pragma unroll 2
-      for (int c = lane * 8; c < a.N1; c += 256) {
-        uint4 v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (w[i]) v[i] = ld_stream(w[i] + c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (w[i]) {
-            const float4* p = reinterpret_cast<const float4*>(h + (int64_t)i * a.N1 + c);
-            s[i] = dot8f(v[i], p[0], p[1], s[i]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (w[i]) y += f[i] * s[i];
-    }
     y = warp_add(y);
-    if (lane == 0) a.Y[(int64_t)t * a.D + d] = (uint16_t)(pack2(y, 0.0f) & 0xffffu);
+    if (lane == 0) sums[n & 1][mine][part] = y;
+    __syncthreads();  // the other half of `sums` is free again: its readers passed this barrier
+    if (part == 0 && lane == 0 && u < units) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kDownSplit; ++i) s += sums[n & 1][mine][i];
+      a.Y[(int64_t)t * a.D + d] = (uint16_t)(pack2(s, 0.0f) & 0xffffu);
+    }
   }
 }
 
