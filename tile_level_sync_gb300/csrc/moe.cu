@@ -235,6 +235,14 @@ bool map_gate_up(CUtensorMap* m, const void* p, int64_t experts, int g, int64_t 
   if (!wide) return map_weights(m, p, experts * g, n1, d, 128, false, 1);
   return map_nd<3>(m, p, {d, (g * experts - (g - 1)) * n1, g}, {d, n1 * d}, {64, 128, g});
 }
+// An output by slot: boxes of `cols` columns (a warp's) x 32 rows as they lie in shared memory.
+bool map_output(CUtensorMap* m, const void* p, int64_t rows, int64_t width, int cols) {
+  cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)width * 2};
+  cuuint32_t box[2] = {(cuuint32_t)cols, 32}, one[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // Token rows by slot, in the four box heights.
 bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, bool wide, int blocks, int last = 128) {
   bool ok = true;
@@ -480,7 +488,8 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   if (!(L.G == 2 ? map_gated(&a.mA, W1t, L.E, L.N1, L.D, wide, 2)
                  : map_weights(&a.mA, W1t, L.E, L.N1, L.D, 128, wide, 2)) ||
       !(gather ? map_rows(&a.mB[0], X, L.T, L.D, 1, false, 1) : map_tokens(a.mB, w + L.x, L.S, L.D, wide, 2)) ||
-      !map_weights(&b.mA, W2t, L.E, L.D, L.N1, 128, wide, 2) || !map_tokens(b.mB, w + L.h, L.S, L.N1, wide, 2))
+      !map_weights(&b.mA, W2t, L.E, L.D, L.N1, 128, wide, 2) || !map_tokens(b.mB, w + L.h, L.S, L.N1, wide, 2) ||
+      !map_output(&a.mO, w + L.h, L.S, L.N1, 32 / L.G) || !map_output(&b.mO, w + L.rows, L.S, L.D, 32))
     return CUSYNC_ERR_CUDA;
   if (gather) {
     for (int i = 1; i < 4; ++i) a.mB[i] = a.mB[0];
@@ -552,6 +561,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if (!map_gate_up(&p.mA, W1t, L.E, L.G, L.N1, L.D, wide) || !map_weights(&p.mA2, W2t, L.E, L.D, L.N1, 64, wide, 2) ||
       !map_tokens(p.mB, gx, L.S, L.D, wide, 1, last) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1, last) ||
       !map_weights(&x.mA, W1t, L.E, H, L.D, wide ? 128 : 64, wide, 2) || !map_tokens(x.mB, gz, L.S, H, wide, 2) ||
+      !map_output(&x.mO, rows, L.S, L.D, 32) ||
       !map_rows(&w1.mA, gz, L.S, H, kr1, wide, 2) || !map_rows(&w1.mB[0], gx, L.S, L.D, kr1, wide, 2) ||
       !map_rows(&w2.mA, gy, L.S, L.D, kr2, wide, 2) || !map_rows(&w2.mB[0], gh, L.S, L.N1, kr2, wide, 2))
     return CUSYNC_ERR_CUDA;

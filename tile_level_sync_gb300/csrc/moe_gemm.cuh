@@ -74,6 +74,7 @@ struct GemmArgs {
   CUtensorMap mB[4];   // tokens, boxes of 16, 32, 64 and 128 (BWD1 on pairs: 80) rows (gather: [0],
                        // one row); DW: [0], 64 rows
   CUtensorMap mB2[4];  // BWD1: dY
+  CUtensorMap mO;      // FWD1, FWD2, DX: the output by slot, boxes of a warp's columns x 32 rows
   int32_t* plan;
   const float* weights;
   void* out;           // H, O, dZ, dX per slot, dW1t or dW2t
@@ -112,9 +113,10 @@ struct GemmCfg {
   static constexpr int kBlockBytes = kAParts * kABytes + kBParts * kBBytes;  // 64 k
   static constexpr int kKps = kBlockBytes <= 32 * 1024 ? 2 : 1;              // blocks of 64 k in a stage
   static constexpr int kStageBytes = kKps * kBlockBytes;
-  static constexpr int kRing = (kDw ? 192 : 224) * 1024;
+  static constexpr bool kStaged = kFwd1 || MODE == FWD2 || MODE == DX;
+  static constexpr int kRing = (kDw || kStaged ? 192 : 224) * 1024;
   static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
-  static constexpr int kStageOut = kDw ? 8 * 4096 : 0;     // DW epilogue: 32 rows of 128 bytes a warp
+  static constexpr int kStageOut = kDw || kStaged ? 8 * 4096 : 0;  // epilogue: two blocks of 2 KB a warp
   static constexpr int kAccCols = kAParts * kCols;
   static constexpr int kAccs = 2 * kAccCols <= 512 ? 2 : 1;
   static constexpr int kTmemCols = kAccs * kAccCols <= 256 ? 256 : 512;
@@ -240,6 +242,28 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine
     const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ (r / 2)) & 3) * 16);
     if (r < rows && piece < pieces) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = v;
   }
+}
+
+// A warp's two blocks of 2 KB in turn for TMA stores of 32 tokens: the block to fill, once the
+// store before the last has read it ...
+template <int N>
+__device__ __forceinline__ uint16_t* stage_block(uint8_t* stage, uint32_t blocks) {
+  if ((threadIdx.x & 31) == 0) ptx::bulk_wait_group_read<N - 1>();
+  __syncwarp();
+  return reinterpret_cast<uint16_t*>(stage + (blocks % N) * 2048);
+}
+// ... and its store to columns from c0, slots from r0 on.  Slots behind an expert's last row
+// are written too: up to its next multiple of 32 they are no one else's, and no one's input
+// but to columns of their own.
+__device__ __forceinline__ void store_block(const CUtensorMap* m, uint8_t* stage, uint32_t& blocks, int32_t c0,
+                                            int32_t r0) {
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    ptx::tma_store_2d(m, stage + (blocks % 2) * 2048, c0, r0);
+    ptx::bulk_commit_group();
+  }
+  ++blocks;
 }
 
 // Sums over the warp's lanes of 32 values: lane i ends with the sum of v[i].
@@ -568,7 +592,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    uint32_t acc = 0;
+    uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
+    uint32_t acc = 0, blocks = 0;
     bool ok = true;
     while (walk.take(q, &ok)) {
       const bool empty_tile = q.nkb == 0;
@@ -584,37 +609,35 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       if (C::kGated) {
         // lanes 0-7 and 16-23 hold gate values, the lanes eight further the up values of the
         // same column of H; of two tokens each of the two lanes computes one
-        const int up = (lane >> 3) & 1;
-        const int f = q.m0 + lane0 / 2 + (lane >> 4) * 8 + (lane & 7);
+        const int up = (lane >> 3) & 1, own = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll 1
         for (int c = half * 32; c < q.rows; c += 64) {
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c + up) * a.M + f;
-          const int left = f < a.M ? q.rows - c - up : 0;
+          uint16_t* out = stage_block<2>(stage, blocks) + up * 16 + own;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float z0 = __uint_as_float(z[2 * i]), z1 = __uint_as_float(z[2 * i + 1]);
             const float other = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 8);
             const float g = up ? other : z0, u = up ? z1 : other;
-            if (2 * i < left) store_bf16(out + (int64_t)(2 * i) * a.M, g * sigmoid_fast(g) * u);
+            store_bf16(out + i * 32, g * sigmoid_fast(g) * u);
           }
+          store_block(&a.mO, stage, blocks, q.m0 + lane0 / 2, q.slot0 + c);
         }
       } else if (C::kFwd1) {
-        const int f = q.m0 + lane0 + lane;
 #pragma unroll 1
         for (int c = half * 32; c < q.rows; c += 64) {
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
-          const int left = f < a.M ? q.rows - c : 0;
-          uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
+          uint16_t* out = stage_block<2>(stage, blocks) + lane;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float v = __uint_as_float(z[i]);
-            if (i < left) store_bf16(out + (int64_t)i * a.M, v * gelu_gate(v));
+            store_bf16(out + i * 32, v * gelu_gate(v));
           }
+          store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
         }
       } else if (MODE == FWD2 || MODE == DX) {
         const int f = q.m0 + lane0 + lane;
@@ -624,7 +647,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
           const int left = f < a.M ? q.rows - c : 0;
-          __half* out = reinterpret_cast<__half*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
           // the largest finite value of 32 tokens x 32 columns is put into [2^14, 2^15); what is
           // above 2^-29 of it keeps fp16's precision
           float most = 0.0f;
@@ -641,9 +663,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           }
           const uint32_t e = max(top >> 23, 15u);
           const float by = __uint_as_float((268u - e) << 23);
+          uint16_t* out = stage_block<2>(stage, blocks) + lane;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < left) out[(int64_t)i * a.M] = __float2half_rn(__uint_as_float(z[i]) * by);
+          for (int i = 0; i < 32; i += 2) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(z[i]) * by, __uint_as_float(z[i + 1]) * by);
+            out[i * 32] = __half_as_ushort(__low2half(h));
+            out[i * 32 + 32] = __half_as_ushort(__high2half(h));
+          }
+          store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
           if (c + lane < q.rows && q.m0 + lane0 < a.M)
             reinterpret_cast<uint16_t*>(a.out2)[(int64_t)(q.slot0 + c + lane) * a.scales + (q.m0 + lane0) / 32] =
                 (uint16_t)((e - 14u) << 7);
@@ -697,7 +724,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           if (live) a.part[(int64_t)mine * a.parts + (q.m0 + lane0) / 32] = s;
         }
       } else {
-        uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
         const int64_t m = (int64_t)q.m0 + lane0;
         uint8_t* base = reinterpret_cast<uint8_t*>(a.out) + (((int64_t)q.e * a.M + m) * a.N + q.n0) * 2;
 #pragma unroll 1
@@ -724,6 +750,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         }
       }
     }
+    if (C::kStaged && lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
     if (!ok && lane == 0) {
       abort_flag = 1;
       a.plan[PLAN_ERR] = (int32_t)kErrWait;
