@@ -113,7 +113,9 @@ struct GemmCfg {
   static constexpr int kBlockBytes = kAParts * kABytes + kBParts * kBBytes;  // 64 k
   static constexpr int kKps = kBlockBytes <= 32 * 1024 ? 2 : 1;              // blocks of 64 k in a stage
   static constexpr int kStageBytes = kKps * kBlockBytes;
-  static constexpr bool kStaged = kFwd1 || MODE == FWD2 || MODE == DX;
+  // Outputs by slot: on pairs staged in shared memory and stored by TMA, 32 rows at a time; on
+  // single CTAs, whose tiles often have few rows, stored from registers, real rows only.
+  static constexpr bool kStaged = PAIR == 2 && (kFwd1 || MODE == FWD2 || MODE == DX);
   static constexpr int kRing = (kDw || kStaged ? 192 : 224) * 1024;
   static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
   static constexpr int kStageOut = kDw || kStaged ? 8 * 4096 : 0;  // epilogue: two blocks of 2 KB a warp
@@ -615,15 +617,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
-          uint16_t* out = stage_block<2>(stage, blocks) + up * 16 + own;
+          const int f = q.m0 + lane0 / 2 + own, left = f < a.M ? q.rows - c - up : 0;
+          uint16_t* out = C::kStaged ? stage_block<2>(stage, blocks) + up * 16 + own
+                                     : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c + up) * a.M + f;
+          const int64_t pitch = C::kStaged ? 16 : a.M;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float z0 = __uint_as_float(z[2 * i]), z1 = __uint_as_float(z[2 * i + 1]);
             const float other = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 8);
             const float g = up ? other : z0, u = up ? z1 : other;
-            store_bf16(out + i * 32, g * sigmoid_fast(g) * u);
+            if (C::kStaged || 2 * i < left) store_bf16(out + 2 * i * pitch, g * sigmoid_fast(g) * u);
           }
-          store_block(&a.mO, stage, blocks, q.m0 + lane0 / 2, q.slot0 + c);
+          if (C::kStaged) store_block(&a.mO, stage, blocks, q.m0 + lane0 / 2, q.slot0 + c);
         }
       } else if (C::kFwd1) {
 #pragma unroll 1
@@ -631,13 +636,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
-          uint16_t* out = stage_block<2>(stage, blocks) + lane;
+          const int f = q.m0 + lane0 + lane, left = f < a.M ? q.rows - c : 0;
+          uint16_t* out = C::kStaged ? stage_block<2>(stage, blocks) + lane
+                                     : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
+          const int64_t pitch = C::kStaged ? 32 : a.M;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float v = __uint_as_float(z[i]);
-            store_bf16(out + i * 32, v * gelu_gate(v));
+            if (C::kStaged || i < left) store_bf16(out + i * pitch, v * gelu_gate(v));
           }
-          store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
+          if (C::kStaged) store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
         }
       } else if (MODE == FWD2 || MODE == DX) {
         const int f = q.m0 + lane0 + lane;
@@ -663,14 +671,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
           }
           const uint32_t e = max(top >> 23, 15u);
           const float by = __uint_as_float((268u - e) << 23);
-          uint16_t* out = stage_block<2>(stage, blocks) + lane;
+          uint16_t* out = C::kStaged ? stage_block<2>(stage, blocks) + lane
+                                     : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
+          const int64_t pitch = C::kStaged ? 32 : a.M;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const __half2 h = __floats2half2_rn(__uint_as_float(z[i]) * by, __uint_as_float(z[i + 1]) * by);
-            out[i * 32] = __half_as_ushort(__low2half(h));
-            out[i * 32 + 32] = __half_as_ushort(__high2half(h));
+            if (C::kStaged || i < left) out[i * pitch] = __half_as_ushort(__low2half(h));
+            if (C::kStaged || i + 1 < left) out[(i + 1) * pitch] = __half_as_ushort(__high2half(h));
           }
-          store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
+          if (C::kStaged) store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
           if (c + lane < q.rows && q.m0 + lane0 < a.M)
             reinterpret_cast<uint16_t*>(a.out2)[(int64_t)(q.slot0 + c + lane) * a.scales + (q.m0 + lane0) / 32] =
                 (uint16_t)((e - 14u) << 7);
