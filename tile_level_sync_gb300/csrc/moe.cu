@@ -324,7 +324,7 @@ cudaError_t launch_gemm(GemmArgs a, const Layer& L, int sms, cudaStream_t s) {
   // an upper bound: how many tiles of rows there are is only known on the device
   const int64_t tiles = (C::kDw ? (int64_t)a.E * a.n_tiles : row_tiles) * a.m_tiles;
   const int grid = PAIR * (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / PAIR));
-  return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, PAIR>, dim3(grid), kGemmThreads, C::kSmemBytes, s, a);
+  return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, PAIR>, dim3(grid), C::kThreads, C::kSmemBytes, s, a);
 }
 template <int MODE, int ACT>
 cudaError_t launch_gemm(bool pair, const GemmArgs& a, const Layer& L, int sms, cudaStream_t s) {

@@ -24,14 +24,15 @@
 //
 // One CTA (or pair) per SM.  Tiles differ in length, so they are claimed one by one from a
 // counter that the plan cleared; the claim of a tile is made when the one before it starts:
-//   warp 11    (of a pair's first CTA) claims tiles, reads their plan entries and hands them
+//   last warp  (of a pair's first CTA) claims tiles, reads their plan entries and hands them
 //              to the other warps of both CTAs through a ring in shared memory.
-//   warp 0     copies of A, warp 10 copies of B (TMA boxes; FWD1G: tile::gather4, four
+//   warp 0     copies of A, the last warp but one copies of B (TMA boxes; FWD1G: tile::gather4, four
 //              rows a copy, through the plan's row indices).  A copy has a fixed cost
 //              besides its bytes, so a stage holds two blocks of 64 k where three such
 //              stages fit, and where widths allow one box brings all of an operand.
 //   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma.
-//   warps 2-9  epilogue: two warps per TMEM lane quarter, every other 32 columns each.
+//   warps 2 .. epilogue: two (BWD1: four) warps per TMEM lane quarter, 32 (16) columns each in
+//              turn.
 // Accumulators are double-buffered where two fit in TMEM's 512 columns.
 //
 // X by slot is a copy in dispatch order (dispatch_kernel).  The gather needs none, but
@@ -63,7 +64,6 @@ namespace moe {
 enum : int { FWD1 = 0, FWD2 = 1, BWD1 = 2, DX = 3, DW1 = 4, DW2 = 5, FWD1G = 6 };
 
 constexpr uint64_t kWaitNs = 1000000000ull;
-constexpr int kGemmThreads = 384;
 constexpr int kTileSlots = 4;
 constexpr int kRowStep = 16;                 // slots up to a multiple of which a row's zeros are stored
 constexpr uint32_t kErrWait = 3u << 24;      // the pipeline-wait class of the chain kernel's error words
@@ -113,6 +113,10 @@ struct GemmCfg {
   static constexpr int kBlockBytes = kAParts * kABytes + kBParts * kBBytes;  // 64 k
   static constexpr int kKps = kBlockBytes <= 32 * 1024 ? 2 : 1;              // blocks of 64 k in a stage
   static constexpr int kStageBytes = kKps * kBlockBytes;
+  // Epilogue warps, a multiple of four.  BWD1 has no second set of accumulators to hide its
+  // epilogue behind: twice the warps.
+  static constexpr int kEpi = kBwd1 ? 16 : 8;
+  static constexpr int kThreads = (kEpi + 4) * 32;
   // Outputs by slot: on pairs staged in shared memory and stored by TMA, 32 rows at a time; on
   // single CTAs, whose tiles often have few rows, stored from registers, real rows only.
   static constexpr bool kStaged = PAIR == 2 && (kFwd1 || MODE == FWD2 || MODE == DX);
@@ -242,7 +246,7 @@ __device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine
   for (int i = 0; i < 4; ++i) {
     const int r = i * 8 + lane / 4;
     const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ (r / 2)) & 3) * 16);
-    if (r < rows && piece < pieces) *reinterpret_cast<uint4*>(out + r * pitch + piece * 16) = v;
+    if (r < rows && piece < pieces) __stcs(reinterpret_cast<uint4*>(out + r * pitch + piece * 16), v);
   }
 }
 
@@ -268,10 +272,12 @@ __device__ __forceinline__ void store_block(const CUtensorMap* m, uint8_t* stage
   ++blocks;
 }
 
-// Sums over the warp's lanes of 32 values: lane i ends with the sum of v[i].
-__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+// Sums over the warp's lanes of 16 values: lanes i and i + 16 end with the sum of v[i].
+__device__ __forceinline__ float transpose_sum(float (&v)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -283,7 +289,7 @@ __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
 }
 
 template <int MODE, int ACT, int PAIR>
-__global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_constant__ GemmArgs a) {
+__global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gemm_kernel(const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<MODE, ACT, PAIR>;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -301,12 +307,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&tfull[i], 1);
-      ptx::mbar_init(&tempty[i], 8 * PAIR);
+      ptx::mbar_init(&tempty[i], C::kEpi * PAIR);
     }
     ptx::mbar_init(&drain, 1);
     for (int i = 0; i < kTileSlots; ++i) {
       ptx::mbar_init(&tiles.full[i], 1);
-      ptx::mbar_init(&tiles.empty[i], PAIR == 2 ? 21 : 11);  // copies, MMA (first CTA), epilogue
+      ptx::mbar_init(&tiles.empty[i], PAIR == 2 ? 2 * C::kEpi + 5 : C::kEpi + 3);  // copies, MMA (first CTA), epilogue
     }
     ptx::mbar_init(&tiles.taken, 1);
     ptx::mbar_init_fence();
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
   Walk<PAIR> walk(tiles, rank);
   Tile q;
 
-  if (warp == 0 || warp == 10) {
+  if (warp == 0 || warp == C::kEpi + 2) {
     // ------------------------------------------------------------ copies
     const bool copies_a = warp == 0;
     const uint64_t pol = ptx::l2_policy_evict_normal();
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == C::kEpi + 3) {
     // ------------------------------------------------------------ claims
     if (rank == 0 && lane == 0) {
       const int32_t total = tile_total<MODE, ACT, PAIR>(a);
@@ -592,7 +598,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
-    const int quarter = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter; every other 32 columns
+    const int quarter = warp & 3;               // TMEM lane quarter
+    constexpr int cols = C::kBwd1 ? 16 : 32;    // columns at a time
+    const int first = ((warp - 2) >> 2) * cols;  // this warp's first, and from there to its next
+    constexpr int step = C::kEpi / 4 * cols;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
     uint32_t acc = 0, blocks = 0;
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         // same column of H; of two tokens each of the two lanes computes one
         const int up = (lane >> 3) & 1, own = (lane >> 4) * 8 + (lane & 7);
 #pragma unroll 1
-        for (int c = half * 32; c < q.rows; c += 64) {
+        for (int c = first; c < q.rows; c += step) {
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
@@ -632,7 +641,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         }
       } else if (C::kFwd1) {
 #pragma unroll 1
-        for (int c = half * 32; c < q.rows; c += 64) {
+        for (int c = first; c < q.rows; c += step) {
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
@@ -650,7 +659,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
       } else if (MODE == FWD2 || MODE == DX) {
         const int f = q.m0 + lane0 + lane;
 #pragma unroll 1
-        for (int c = half * 32; c < q.rows; c += 64) {
+        for (int c = first; c < q.rows; c += step) {
           uint32_t z[32];
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
@@ -690,54 +699,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1) moe_gemm_kernel(const __grid_
         const bool in = f < a.M;
         const int stored = (q.rows + kRowStep - 1) / kRowStep * kRowStep;  // zeros behind the last row
 #pragma unroll 1
-        for (int c = half * 32; c < q.rows; c += 64) {
-          const int mine = q.slot0 + c + lane;
-          const bool live = c + lane < q.rows;
+        for (int c = first; c < q.rows; c += step) {
+          const int token = lane & 15, mine = q.slot0 + c + token;
+          const bool live = c + token < q.rows;
           const int r = live ? a.plan[a.row_of + mine] : -1;
           const float w_lane = r >= 0 ? a.weights[r] : 0.0f;
-          float dots[32];
+          float dots[16];
           uint16_t* dz = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * (C::kG * (int64_t)a.M) + f;
           uint16_t* wh = reinterpret_cast<uint16_t*>(a.out2) + (int64_t)(q.slot0 + c) * a.M + f;
+          uint32_t z[16], u[16], g[16];
+          ptx::tmem_ld_32x32b_x16(d + c, z);
+          if (C::kG == 2) ptx::tmem_ld_32x32b_x16(d + C::kCols + c, u);
+          ptx::tmem_ld_32x32b_x16(d + C::kG * C::kCols + c, g);
+          ptx::tmem_ld_wait();
 #pragma unroll
-          for (int i0 = 0; i0 < 32; i0 += 16) {
-            uint32_t z[16], u[16], g[16];
-            ptx::tmem_ld_32x32b_x16(d + c + i0, z);
-            if (C::kG == 2) ptx::tmem_ld_32x32b_x16(d + C::kCols + c + i0, u);
-            ptx::tmem_ld_32x32b_x16(d + C::kG * C::kCols + c + i0, g);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int i = i0 + j;
-              const float w = __shfl_sync(0xffffffffu, w_lane, i);
-              const bool on = c + i < q.rows;
-              const float zz = __uint_as_float(z[j]), dh = __uint_as_float(g[j]), dhw = w * dh;
-              float h, vz, vu = 0.0f;
-              if (C::kG == 2) {
-                const float uu = __uint_as_float(u[j]), sg = sigmoid_fast(zz), zs = zz * sg;
-                h = zs * uu;
-                vz = dhw * uu * (sg + zs * (1.0f - sg));
-                vu = dhw * zs;
-              } else {
-                const float sg = gelu_gate(zz);
-                h = zz * sg;
-                vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
-              }
-              dots[i] = in ? dh * h : 0.0f;
-              if (in && c + i < stored) {
-                store_bf16(dz + (int64_t)i * (C::kG * (int64_t)a.M), on ? vz : 0.0f);
-                if (C::kG == 2) store_bf16(dz + (int64_t)i * (2 * (int64_t)a.M) + a.M, on ? vu : 0.0f);
-                store_bf16(wh + (int64_t)i * a.M, on ? w * h : 0.0f);
-              }
+          for (int i = 0; i < 16; ++i) {
+            const float w = __shfl_sync(0xffffffffu, w_lane, i);
+            const bool on = c + i < q.rows;
+            const float zz = __uint_as_float(z[i]), dh = __uint_as_float(g[i]), dhw = w * dh;
+            float h, vz, vu = 0.0f;
+            if (C::kG == 2) {
+              const float uu = __uint_as_float(u[i]), sg = sigmoid_fast(zz), zs = zz * sg;
+              h = zs * uu;
+              vz = dhw * uu * (sg + zs * (1.0f - sg));
+              vu = dhw * zs;
+            } else {
+              const float sg = gelu_gate(zz);
+              h = zz * sg;
+              vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
+            }
+            dots[i] = in ? dh * h : 0.0f;
+            if (in && c + i < stored) {
+              store_bf16(dz + (int64_t)i * (C::kG * (int64_t)a.M), on ? vz : 0.0f);
+              if (C::kG == 2) store_bf16(dz + (int64_t)i * (2 * (int64_t)a.M) + a.M, on ? vu : 0.0f);
+              store_bf16(wh + (int64_t)i * a.M, on ? w * h : 0.0f);
             }
           }
           const float s = transpose_sum(dots, lane);
-          if (live) a.part[(int64_t)mine * a.parts + (q.m0 + lane0) / 32] = s;
+          if (live && lane < 16) a.part[(int64_t)mine * a.parts + (q.m0 + lane0) / 32] = s;
         }
       } else {
         const int64_t m = (int64_t)q.m0 + lane0;
         uint8_t* base = reinterpret_cast<uint8_t*>(a.out) + (((int64_t)q.e * a.M + m) * a.N + q.n0) * 2;
 #pragma unroll 1
-        for (int c = half * 32; c < C::kCols; c += 64) {
+        for (int c = first; c < C::kCols; c += step) {
           uint32_t z[32], p[16];
           if (empty_tile) {
 #pragma unroll

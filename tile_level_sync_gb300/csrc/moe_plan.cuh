@@ -23,6 +23,7 @@ constexpr int kTileRows = 128;
 constexpr int kMidRows = 160;  // rows of BWD1's tiles on pairs
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kHeld = 4;  // groups of 32 ids whose ranks a warp keeps in registers
 enum : int { PLAN_ERR = 0, PLAN_TILES = 2, PLAN_PAIRS = 3, PLAN_MIDS = 4, PLAN_COUNTERS = 8, PLAN_HEADER = 16 };
 
 struct PlanArgs {
@@ -86,20 +87,31 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   ptx::pdl_launch_dependents();
   __syncthreads();
 
-  // this warp's part of the chunk: ranks within the warp, kept in slot_of for now
+  // this warp's part of the chunk: ranks within the warp, the first kHeld groups' in
+  // registers, what comes behind them in slot_of for now
   const int64_t lo = (int64_t)blockIdx.x * a.chunk, end = min(a.A, lo + a.chunk);
   const int64_t per_warp = a.chunk / kPlanWarps;
   const int64_t w0 = lo + warp * per_warp, w1 = min(end, w0 + per_warp);
   uint32_t* mine = whist + warp * E;
   int32_t* slot_of = a.plan + a.slot_of;
-  for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-    const int id = plan_id(a, i0 + lane, w1);
-    const unsigned same = __match_any_sync(0xffffffffu, id);
+  auto rank_of = [&](int id) {
+    const unsigned same = __match_any_sync(0xffffffffu, id), lower = same & ((1u << lane) - 1);
     const uint32_t seen = id >= 0 ? mine[id] : 0;
     __syncwarp();
-    if (id >= 0 && (same & ((1u << lane) - 1)) == 0) mine[id] = seen + __popc(same);
+    if (id >= 0 && lower == 0) mine[id] = seen + __popc(same);
     __syncwarp();
-    if (i0 + lane < w1) slot_of[i0 + lane] = id >= 0 ? (int32_t)(seen + __popc(same & ((1u << lane) - 1))) : -1;
+    return seen + __popc(lower);
+  };
+  int held_id[kHeld];
+  uint32_t held[kHeld];
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) held_id[h] = plan_id(a, w0 + 32 * h + lane, w1);
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (w0 + 32 * h < w1) held[h] = rank_of(held_id[h]);
+  for (int64_t i0 = w0 + 32 * kHeld; i0 < w1; i0 += 32) {
+    const uint32_t r = rank_of(plan_id(a, i0 + lane, w1));
+    if (i0 + lane < w1) slot_of[i0 + lane] = (int32_t)r;
   }
   // what other blocks hold: all of it into count, the earlier blocks' into before
   if (a.blocks > 1) {
@@ -194,13 +206,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(PlanArgs a) {
   }
   for (int64_t i = used + (int64_t)blockIdx.x * kPlanThreads + tid; i < a.S; i += (int64_t)gridDim.x * kPlanThreads)
     row_of[i] = -1;
-  for (int64_t i = w0 + lane; i < w1; i += 32) {
-    const int id = plan_id(a, i, w1);
-    if (id < 0) continue;
-    const uint32_t s = offset[id] + before[id] + mine[id] + (uint32_t)slot_of[i];
-    slot_of[i] = (int32_t)s;
-    row_of[s] = (int32_t)i;
-  }
+  auto place = [&](int64_t i, int id, uint32_t rank) {
+    const uint32_t s = id >= 0 ? offset[id] + before[id] + mine[id] + rank : 0xffffffffu;
+    slot_of[i] = (int32_t)s;  // -1: no expert
+    if (id >= 0) row_of[s] = (int32_t)i;
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (w0 + 32 * h + lane < w1) place(w0 + 32 * h + lane, held_id[h], held[h]);
+  for (int64_t i = w0 + 32 * kHeld + lane; i < w1; i += 32) place(i, plan_id(a, i, w1), (uint32_t)slot_of[i]);
 }
 
 }  // namespace moe

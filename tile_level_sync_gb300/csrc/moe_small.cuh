@@ -49,10 +49,13 @@ __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(DispatchArgs
     const int64_t from = r < 0 ? 0 : (int64_t)(r / a.k) * a.chunks, to = s * a.chunks;
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-    for (int c = lane; c < a.chunks; c += 32) a.xs[to + c] = r < 0 ? zero : a.x[from + c];
-    if (a.y)
-#pragma unroll 4
-      for (int c = lane; c < a.chunks; c += 32) a.ys[to + c] = r < 0 ? zero : a.y[from + c];
+    for (int c = lane; c < a.chunks; c += 32) {
+      const uint4 x = r < 0 ? zero : a.x[from + c];
+      uint4 y = zero;
+      if (a.y && r >= 0) y = a.y[from + c];
+      a.xs[to + c] = x;
+      if (a.y) a.ys[to + c] = y;
+    }
   }
 }
 
