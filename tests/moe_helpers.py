@@ -31,8 +31,10 @@ def layer(s, act, **more):
 
 
 def guarded(n_bytes):
-    """A device buffer of n_bytes with 4 KB of a known pattern behind it."""
-    buf = torch.full((n_bytes + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    """A device buffer of n_bytes, NaN in every type that the kernels keep there, with 4 KB of a
+    known pattern behind it."""
+    buf = torch.full((n_bytes + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    buf[n_bytes:] = 0x5A
     return buf, buf[:n_bytes]
 
 

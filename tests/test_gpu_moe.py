@@ -237,3 +237,208 @@ def test_mlp_ids(T, act, grad, how):
     else:
         ids[:] = 2
     _check_mlp(mlp_inputs(T, E, k, 96, 80, act, seed=1, ids=torch.from_numpy(ids)), act, grad)
+
+
+# ------------------------------------------------------------------ use
+
+def _bytes(t):
+    return t.contiguous().view(torch.uint8).cpu().numpy()
+
+
+@pytest.mark.parametrize("T", [5, 60, 700])
+def test_layer_forward_and_backward(T):
+    """The calls of a training step in a row: route, mlp, their gradients, on one stream of the
+    caller's; the oracle takes the router's own choice."""
+    E, k, D, N1, act = 8, 2, 136, 72, "swiglu"
+    s = mlp_inputs(T, E, k, D, N1, act, seed=4)
+    logits, bias = torch.randn(T, E), 0.1 * torch.randn(E)
+    m = layer(s, act, score="sigmoid", renorm=True, scale=2.0)
+    d = {n: v.cuda() for n, v in s.items()}
+    lo, bi = logits.cuda(), bias.cuda()
+    ids, w = torch.empty_like(d["ids"]), torch.empty_like(d["weights"])
+    work = torch.full((max(m.info.work_bytes, m.info.grad_work_bytes),), 0xFF, dtype=torch.uint8, device="cuda")
+    Y, dlo = torch.empty_like(d["X"]), torch.empty_like(lo)
+    out = {n: torch.empty_like(d[n[1:]]) for n in ("dX", "dW1t", "dW2t", "dweights")}
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    m.run(d["X"], lo, bi, d["W1t"], d["W2t"], ids, w, work, Y, stream=st)
+    m.run_grad(d["X"], lo, d["W1t"], d["W2t"], ids, w, d["dY"], work, out["dX"], out["dW1t"], out["dW2t"],
+               out["dweights"], dlo, stream=st)
+    st.synchronize()
+    assert m.check(work, stream=st) == (cs.OK, 0)
+    host = {n: f64(v) for n, v in s.items()}
+    want_ids, want_w = ref.route(f64(logits), f64(bias), k, "sigmoid", renorm=True, scale=2.0)
+    got_ids, got_w = ids.cpu().numpy(), f64(w)
+    assert np.array_equal(got_ids, want_ids) and np.allclose(got_w, want_w, rtol=ROUTE_TOL)
+    y, bound = ref.mlp(host["X"], host["W1t"], host["W2t"], got_ids, got_w, act)
+    assert_within(Y, y, bound, "Y")
+    want = ref.mlp_grad(host["X"], host["W1t"], host["W2t"], got_ids, got_w, host["dY"], act)
+    for name, (value, bound) in want.items():
+        assert_within(out[name], value, bound, name)
+    dw = f64(out["dweights"])
+    want = ref.route_grad(f64(logits), got_ids, dw, "sigmoid", True, 2.0)
+    q = np.abs(got_w) / 2.0  # the chosen scores over their sum
+    size = 2.0 * np.abs(dw).max(axis=1, keepdims=True) * q.max(axis=1, keepdims=True)
+    assert np.all(np.abs(f64(dlo) - want) <= 2 * ROUTE_TOL * size)
+
+
+@pytest.mark.parametrize("T", [2, 100, 900])
+def test_same_bytes_every_time_and_from_a_graph(T):
+    """Repeated calls, calls with few SMs, and replays of a captured graph write the same bytes."""
+    s = mlp_inputs(T, 4, 2, 192, 128, "swiglu", seed=2)
+    d = {n: v.cuda() for n, v in s.items()}
+    m = layer(s, "swiglu")
+    work = torch.empty(max(m.info.work_bytes, m.info.grad_work_bytes), dtype=torch.uint8, device="cuda")
+    Y = torch.empty_like(d["X"])
+    out = [torch.empty_like(d[n]) for n in ("X", "W1t", "W2t", "weights")]
+
+    def step(layer_, w):
+        layer_.mlp(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], w, Y)
+        layer_.mlp_grad(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], d["dY"], w, *out)
+
+    def result():
+        torch.cuda.synchronize()
+        r = [_bytes(t) for t in [Y] + out]
+        for t in [Y] + out:
+            t.fill_(float("nan"))
+        return r
+
+    step(m, work)
+    first = result()
+    for other in (m, layer(s, "swiglu", num_sms=2), layer(s, "swiglu", num_sms=1)):
+        step(other, work)
+        # one SM takes single CTAs where more would take pairs: other widths, the same sums
+        assert all(np.array_equal(a, b) for a, b in zip(first, result()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(m, work)
+    for _ in range(3):
+        work.fill_(0xFF)
+        graph.replay()
+        assert all(np.array_equal(a, b) for a, b in zip(first, result()))
+
+
+def test_calls_side_by_side():
+    """Two streams, each with buffers of its own."""
+    cases = []
+    for seed, T in ((0, 400), (1, 37)):
+        s = mlp_inputs(T, 5, 2, 200, 96, "gelu", seed=seed)
+        m = layer(s, "gelu")
+        d = {n: v.cuda() for n, v in s.items()}
+        cases.append((m, d, torch.empty(m.info.work_bytes, dtype=torch.uint8, device="cuda"), torch.empty_like(d["X"]),
+                      _bytes(run_mlp(m, s)), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for m, d, work, Y, _, st in cases:
+            m.mlp(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], work, Y, stream=st)
+    torch.cuda.synchronize()
+    for m, d, work, Y, want, st in cases:
+        assert np.array_equal(_bytes(Y), want) and m.check(work, stream=st)[0] == cs.OK
+
+
+def test_routes_from_a_graph():
+    c = dict(T=300, E=64, k=6, score="sigmoid", groups=8, group_limit=4, group_top=2, bias=True, renorm=True)
+    logits, bias = _route_case(c, True, "none")
+    m, lo, bi = _layer(c, True), logits.cuda(), bias.cuda()
+    ids = torch.empty((300, 6), dtype=torch.int32, device="cuda")
+    w, dl = torch.empty((300, 6), device="cuda"), torch.empty_like(lo)
+    plan = torch.empty(m.info.plan_bytes // 4, dtype=torch.int32, device="cuda")
+
+    def step():
+        m.route(lo, bi, ids, w)
+        m.plan(ids, plan)
+        m.route_grad(lo, ids, w, dl)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    lo.mul_(-1.0)  # replays read the tensors anew
+    graph.replay()
+    want = _oracle_route(c, -logits, bias)
+    assert np.array_equal(ids.cpu().numpy(), want[0])
+    assert np.array_equal(m.plan_views(plan)["slot_of"].cpu().numpy(), ref.plan(want[0], 64)["slot_of"])
+
+
+# ------------------------------------------------------------------ values that do not mix
+
+@pytest.mark.parametrize("T", [12, 200, 600])
+def test_a_token_of_nans_stays_alone(T):
+    s = mlp_inputs(T, 2, 1, 128, 64, "swiglu", seed=6)
+    s["weights"][:] = 1.0
+    clean = run_mlp(layer(s, "swiglu"), s)
+    s["X"][5] = float("nan")
+    s["X"][7] = float("inf")
+    Y = run_mlp(layer(s, "swiglu"), s)
+    assert bool(Y[5].isnan().all()) and not bool(Y[7].isfinite().all())
+    keep = [t for t in range(T) if t not in (5, 7)]
+    # the rows that share a scale with the two may be rounded to another fp16 (2^-11 each time),
+    # and from there to another bf16
+    assert bool(torch.isfinite(Y[keep]).all())
+    diff = (Y[keep].float() - clean[keep].float()).abs()
+    assert bool((diff <= 2.0 ** -7 * clean[keep].float().abs() + 2.0 ** -10 * clean.float().abs().max()).all())
+
+
+@pytest.mark.parametrize("T", [300, 900])
+def test_an_expert_of_nans_stays_alone(T):
+    s = mlp_inputs(T, 4, 2, 128, 64, "swiglu", seed=8)
+    m = layer(s, "swiglu")
+    clean_y, clean = run_mlp(m, s), run_mlp_grad(m, s)
+    s["W1t"][1], s["W2t"][1] = float("nan"), float("inf")
+    Y, out = run_mlp(m, s), run_mlp_grad(m, s)
+    free = (s["ids"] != 1).all(dim=1)
+    assert bool(free.any()) and bool((~free).any())
+    assert torch.equal(Y.cpu()[free], clean_y.cpu()[free]) and torch.equal(out["dX"].cpu()[free], clean["dX"].cpu()[free])
+    for e in (0, 2, 3):
+        assert torch.equal(out["dW1t"][e], clean["dW1t"][e]) and torch.equal(out["dW2t"][e], clean["dW2t"][e])
+    assert torch.equal(out["dweights"].cpu()[s["ids"] != 1], clean["dweights"].cpu()[s["ids"] != 1])
+
+
+def test_scaled_rows_keep_their_range():
+    """Outputs far apart in size, in one tile: each token's own precision."""
+    s = mlp_inputs(600, 2, 1, 128, 64, "swiglu", seed=9)
+    s["X"][::2] *= 2.0 ** -9  # SwiGLU squares it: 2^-18 beside 1
+    _check_mlp(s, "swiglu", False)
+    s["W2t"] *= 2.0 ** 60     # beyond what fp16 holds
+    _check_mlp(s, "swiglu", False)
+    s["W2t"] *= 2.0 ** -120
+    _check_mlp(s, "swiglu", False)
+
+
+def test_offsets_beyond_32_bits():
+    """Over 2^31 elements of rows by slot; the last tokens against the oracle."""
+    T, E, k, D, N1 = 140000, 8, 8, 2048, 64
+    ids = torch.arange(T * k, dtype=torch.int32).view(T, k) % E
+    s = mlp_inputs(T, E, k, D, N1, "gelu", seed=3, ids=ids)
+    m = layer(s, "gelu")
+    assert m.info.slots * D > 2 ** 31
+    Y = run_mlp(m, s)
+    last = slice(T - 40, T)
+    host = {n: f64(s[n][last] if n in ("X", "weights") else s[n]) for n in ("X", "W1t", "W2t", "weights")}
+    y, bound = ref.mlp(host["X"], host["W1t"], host["W2t"], ids[last].numpy(), host["weights"], "gelu")
+    assert_within(Y[last], y, bound, "Y")
+    first = f64(Y[:40])
+    assert np.all(np.isfinite(first))
+
+
+def test_no_tokens():
+    s = mlp_inputs(4, 3, 2, 64, 64, "gelu")
+    for n in ("X", "dY", "ids", "weights"):
+        s[n] = s[n][:0]
+    m = layer(s, "gelu")
+    out = run_mlp_grad_empty(m, s)
+    assert all(bool((out[n] == 0).all()) for n in ("dW1t", "dW2t"))
+    plan = torch.full((m.info.plan_bytes // 4,), 7, dtype=torch.int32, device="cuda")
+    m.plan(s["ids"].cuda(), plan)
+    assert bool((m.plan_views(plan)["counts"] == 0).all()) and bool((m.plan_views(plan)["offsets"] == 0).all())
+
+
+def run_mlp_grad_empty(m, s):
+    d = {n: v.cuda() for n, v in s.items()}
+    out = {n: torch.full_like(d[n[1:]], float("nan")) for n in ("dX", "dW1t", "dW2t", "dweights")}
+    work = torch.empty(max(16, m.info.grad_work_bytes), dtype=torch.uint8, device="cuda")
+    m.mlp_grad(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], d["dY"], work, out["dX"], out["dW1t"], out["dW2t"],
+               out["dweights"])
+    m.mlp(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], work, out["dX"])
+    torch.cuda.synchronize()
+    return out

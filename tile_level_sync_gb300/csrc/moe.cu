@@ -72,6 +72,12 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
   if (mlp) {
     if (d->D < 1 || d->N1 < 1) return CUSYNC_ERR_INVALID_ARG;
     if (d->D % 8 || d->N1 % 8 || d->D > (1 << 20) || d->N1 > (1 << 20)) return CUSYNC_ERR_UNSUPPORTED;
+    // the kernels count weight rows and tiles in 32 bits
+    const int64_t rows = (int64_t)d->experts * std::max(2 * d->N1, d->D);
+    const int64_t row_tiles = d->T * d->top_k / kTileRows + d->experts;
+    const int64_t tiles = std::max(row_tiles * div_up(std::max(d->N1, d->D), 64),
+                                   d->experts * div_up(2 * d->N1, 128) * div_up(d->D, 128));
+    if (rows > INT32_MAX || tiles > INT32_MAX / 2) return CUSYNC_ERR_UNSUPPORTED;
   }
   L->T = d->T;
   L->D = d->D;
