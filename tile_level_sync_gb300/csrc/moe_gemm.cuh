@@ -23,7 +23,8 @@
 // eight further hold the two factors of one h.  BWD1 has them in accumulators of their own.
 //
 // One CTA (or pair) per SM.  Tiles differ in length, so they are claimed one by one from a
-// counter that the plan cleared; the claim of a tile is made when the one before it starts:
+// counter that the plan cleared; the claim of a tile is made when the one before it starts, or
+// the one before that where tiles are short and a claim (2 us) would be waited for:
 //   last warp  (of a pair's first CTA) claims tiles, reads their plan entries and hands them
 //              to the other warps of both CTAs through a ring in shared memory.
 //   warp 0     copies of A, the last warp but one copies of B (TMA boxes; FWD1G: tile::gather4, four
@@ -193,11 +194,11 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
 }
 
 // The ring of claimed tiles.  full: one arrival by the claiming warp (each CTA has its
-// own); empty, taken (the first CTA's): arrivals by every warp that read a slot, and by the
+// own); empty, taken (the first CTA's): arrivals by every warp that read the slot, and by the
 // first copying warp alone.
 struct TileRing {
   int32_t slot[kTileSlots][8];  // a Tile; rows < 0: no more
-  uint64_t full[kTileSlots], empty[kTileSlots], taken;
+  uint64_t full[kTileSlots], empty[kTileSlots], taken[kTileSlots];
 };
 
 // One warp's way through the ring.
@@ -229,7 +230,7 @@ struct Walk {
     if (lane == 0) {
       if (rank == 0) ptx::mbar_arrive(&ring.empty[s]);
       else ptx::mbar_arrive_cluster(ptx::mapa(&ring.empty[s], 0));
-      if (first_copier) ptx::mbar_arrive(&ring.taken);
+      if (first_copier) ptx::mbar_arrive(&ring.taken[s]);
     }
     __syncwarp();
     ++n;
@@ -320,8 +321,8 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
     for (int i = 0; i < kTileSlots; ++i) {
       ptx::mbar_init(&tiles.full[i], 1);
       ptx::mbar_init(&tiles.empty[i], PAIR == 2 ? 2 * C::kEpi + 5 : C::kEpi + 3);  // copies, MMA (first CTA), epilogue
+      ptx::mbar_init(&tiles.taken[i], 1);
     }
-    ptx::mbar_init(&tiles.taken, 1);
     ptx::mbar_init_fence();
     abort_flag = 0;
     ptx::prefetch_tmap(&a.mA);
@@ -575,13 +576,17 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
     // ------------------------------------------------------------ claims
     if (rank == 0 && lane == 0) {
       const int32_t total = tile_total<MODE, ACT, PAIR>(a);
+      const uint32_t ahead = C::kDw ? 3 : a.K < 24 * 64 ? 2 : 1;
       bool ok = true;
       for (uint32_t n = 0; !abort_flag; ++n) {
         const uint32_t s = n % kTileSlots;
         if (n >= kTileSlots)
           ok = PAIR == 2 ? ptx::mbar_wait_bounded_cluster(&tiles.empty[s], ((n / kTileSlots) & 1) ^ 1, kWaitNs)
                          : ptx::mbar_wait_sleepy(&tiles.empty[s], ((n / kTileSlots) & 1) ^ 1, kWaitNs);
-        if (ok && n) ok = ptx::mbar_wait_sleepy(&tiles.taken, (n - 1) & 1, kWaitNs);
+        if (ok && n >= ahead) {
+          const uint32_t before = n - ahead;
+          ok = ptx::mbar_wait_bounded(&tiles.taken[before % kTileSlots], (before / kTileSlots) & 1, kWaitNs);
+        }
         if (!ok) break;
         int32_t t = blockIdx.x / PAIR;  // the first tile needs no claim
         if (n) t = gridDim.x / PAIR + atomicAdd(a.plan + a.counter, 1);
