@@ -155,6 +155,21 @@ def test_route_grad(c, f32, mask):
     assert np.all(np.abs(f64(dl) - want) <= 2 * ROUTE_TOL * size * s + half * np.abs(want) + 1e-37)
 
 
+@pytest.mark.parametrize("E", [64, 33])
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", False)])
+def test_route_grad_of_an_expert_given_twice(E, score, renorm):
+    c = dict(T=37, E=E, k=6, score=score, renorm=renorm)
+    logits, _ = _route_case(c, True, "none")
+    ids, _ = _oracle_route(c, logits, None)
+    ids[::2, 3], ids[::3, 5], ids[5] = ids[::2, 0], E, -1
+    dw = np.random.default_rng(1).normal(size=ids.shape).astype(np.float32)
+    dl = torch.full_like(logits, 77).cuda()
+    _layer(c, True).route_grad(logits.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), dl)
+    ids[ids == E] = -1
+    want = ref.route_grad(f64(logits), ids, dw.astype(np.float64), score, renorm, 1.0)
+    assert np.all(np.abs(f64(dl) - want) <= 4 * ROUTE_TOL * np.abs(dw).max())
+
+
 def test_route_grad_against_differences():
     c = dict(T=6, E=40, k=5, score="softmax")
     for score in ("softmax", "sigmoid"):

@@ -12,7 +12,7 @@
 // min/max; a step of the selection is then one reduction of the lanes' heads, one vote and a
 // shift in the winning lane.  route_any_kernel takes any count and grouping: experts lane,
 // lane + 32, ..., and a pass over the lane's registers at every step.  32768 tokens x 256
-// experts, 8 chosen out of 4 of 8 groups: ROUTE_FAST us against ROUTE_ANY us.
+// experts, 8 chosen out of 4 of 8 groups: 41 us against 139 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -34,14 +34,17 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return __b
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// Over groups of N neighbouring lanes (32: the warp).
+template <int N = 32>
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  for (int o = N / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
   return v;
 }
+template <int N = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  for (int o = N / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
 }
 __device__ __forceinline__ double warp_sum(double v) {
@@ -660,12 +663,159 @@ __global__ void __launch_bounds__(256) route_any_kernel(const __grid_constant__ 
   store_choice<L, SCORE>(a, t, lane, id, m, 1.0f / sum);
 }
 
+// ------------------------------------------------------------------ gradient
+
 // With q_j = s_j / sum of chosen s (renorm) the chosen experts' gradients need nothing of
 // the others, for softmax too (its denominator cancels):
 //   softmax  dl_j = scale q_j (dw_j - sum_i q_i dw_i)
 //   sigmoid  the same, times 1 - s_j
 // Without: softmax dl_e = p_e (scale dw_e [e chosen] - scale sum_j p_j dw_j), sigmoid
-// dl_j = scale dw_j s_j (1 - s_j).  All other gradients are zero.
+// dl_j = scale dw_j s_j (1 - s_j).  All other gradients are zero, so that only softmax
+// without renorm has to read the row.
+//
+// Lane j of a token's N lanes holds the j-th chosen expert.  The chosen's part of its gradient,
+// and softmax's common term scale sum_j p_j dw_j in every lane.
+template <int SCORE, int N = 32>
+__device__ __forceinline__ float chosen_grad(const RouteArgs& a, bool on, float mine, float dw, float m, float inv,
+                                             float& inner) {
+  inner = 0.0f;
+  float g = 0.0f;
+  if (a.renorm) {
+    const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
+    const float mx = warp_max<N>(ls);
+    const float ex = on ? expf(ls - mx) : 0.0f;
+    const float q = ex / warp_sum<N>(ex);
+    const float mean = warp_sum<N>(on ? q * dw : 0.0f);
+    if (on) g = a.scale * q * (dw - mean);
+    if (SCORE == 1 && on) g *= sigmoid_f(-mine);
+  } else if (SCORE == 0) {
+    const float p = on ? expf(mine - m) * inv : 0.0f;
+    inner = a.scale * warp_sum<N>(on ? p * dw : 0.0f);
+    if (on) g = a.scale * dw * p;
+  } else if (on) {
+    g = a.scale * dw * sigmoid_f(mine) * sigmoid_f(-mine);
+  }
+  return g;
+}
+
+// Lane j's chosen expert (-1: none, or switched off), its logit and the gradient of its weight.
+template <typename L>
+__device__ __forceinline__ bool load_chosen(const RouteArgs& a, int64_t t, int lane, int& id, float& mine, float& dw) {
+  id = -1;
+  dw = 0.0f;
+  if (lane < a.k) {
+    id = a.ids[t * a.k + lane];
+    if (id < 0 || id >= a.E) id = -1;
+    dw = a.weights[t * a.k + lane];
+  }
+  mine = id >= 0 ? one_logit<L>(a, t, id) : -INFINITY;
+  return mine > -INFINITY;
+}
+
+// An expert that a token was given twice gets the sum of both, from the first of the two
+// lanes, which is the one that stores (returned).  key: equal for equal experts of a token.
+template <int N>
+__device__ __forceinline__ bool first_of_equals(int lane, int key, float& g) {
+  const unsigned same = __match_any_sync(kFull, key);
+  if (__any_sync(kFull, __popc(same) > 1)) {
+    float total = 0.0f;
+    for (int j = 0; j < N; ++j) {
+      const int from = (lane & ~(N - 1)) + j;
+      const float v = __shfl_sync(kFull, g, from);
+      if ((same >> from) & 1u) total += v;
+    }
+    g = total;
+  }
+  return (same & ((1u << lane) - 1)) == 0;
+}
+
+// Gradients that are zero but for the chosen experts', rows of whole 16-byte pieces: a token
+// takes N >= k lanes, a warp 32 / N tokens; rows are zeroed, then the chosen's values stored
+// over them.  32768 tokens x 256 experts, 8 a token: 10 us, 20 us for route_grad_kernel.
+template <typename L, int SCORE, int N>
+__global__ void __launch_bounds__(256) route_grad_chosen_kernel(const __grid_constant__ RouteArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, group = lane / N;
+  const int64_t t0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * (32 / N), t = t0 + group;
+  if (t0 >= a.T) return;
+  int id = -1;
+  float mine = -INFINITY, dw = 0.0f;
+  if (t < a.T) load_chosen<L>(a, t, lane & (N - 1), id, mine, dw);
+  const bool on = mine > -INFINITY;
+  const int64_t rows = min((int64_t)(32 / N), a.T - t0);
+  uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<L*>(a.dlogits) + t0 * a.E);
+  const int pieces = (int)(rows * a.E * (int64_t)sizeof(L) / 16);
+#pragma unroll 4
+  for (int c = lane; c < pieces; c += 32) out[c] = make_uint4(0u, 0u, 0u, 0u);
+  float inner;
+  float g = chosen_grad<SCORE, N>(a, on, mine, dw, 0.0f, 0.0f, inner);
+  const bool first = first_of_equals<N>(lane, on ? id * 32 + group : -1 - lane, g);
+  __syncwarp();  // the rows are written
+  if (on && first) store_logit(reinterpret_cast<L*>(a.dlogits) + t * a.E + id, g);
+}
+
+// softmax without renorm: every expert's gradient, rows of whole 16-byte pieces, at most C of
+// them a lane.
+template <typename L, int C>
+__global__ void __launch_bounds__(256) route_grad_rows_kernel(const __grid_constant__ RouteArgs a) {
+  constexpr int W = 16 / sizeof(L);
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  const L* row = reinterpret_cast<const L*>(a.logits) + t * a.E;
+  float l[C * W];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    float v[W];
+    load_lane<W>(row, (c * 32 + lane) * W, a.E, true, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) l[c * W + i] = v[i] == v[i] ? v[i] : -INFINITY;
+  }
+  int id;
+  float mine, dw;
+  const bool on = load_chosen<L>(a, t, lane, id, mine, dw);
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < C * W; ++i) m = fmaxf(m, l[i]);
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.0f;  // every expert switched off: zeros
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < C * W; ++i) {
+    l[i] = expf(l[i] - m);
+    sum += l[i];
+  }
+  sum = warp_sum(sum);
+  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+  float inner;
+  float g = chosen_grad<0>(a, on, mine, dw, m, inv, inner);
+  L* out = reinterpret_cast<L*>(a.dlogits) + t * a.E;
+  const float common = -inner * inv;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int e0 = (c * 32 + lane) * W;
+    uint32_t p[4];
+    if constexpr (W == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = __float_as_uint(common * l[c * W + i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(common * l[c * W + 2 * i], common * l[c * W + 2 * i + 1]);
+        p[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    if (e0 < a.E) *reinterpret_cast<uint4*>(out + e0) = make_uint4(p[0], p[1], p[2], p[3]);
+  }
+  const bool first = first_of_equals<32>(lane, on ? id : -1 - lane, g);
+  __syncwarp();  // the row is written
+  if (on && first) store_logit(out + id, g + common * expf(mine - m));
+}
+
+// Any count of experts.
 template <typename L, int V, int SCORE>
 __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__ RouteArgs a) {
   ptx::pdl_wait();
@@ -675,15 +825,9 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
   if (t >= a.T) return;
   float l[V];
   load_row<L, V>(a, t, lane, l);
-  int id = -1;
-  float dw = 0.0f;
-  if (lane < a.k) {
-    id = a.ids[t * a.k + lane];
-    if (id < 0 || id >= a.E) id = -1;
-    dw = a.weights[t * a.k + lane];
-  }
-  const float mine = id >= 0 ? one_logit<L>(a, t, id) : -INFINITY;
-  const bool on = mine > -INFINITY;
+  int id;
+  float mine, dw;
+  const bool on = load_chosen<L>(a, t, lane, id, mine, dw);
   float m = 0.0f, inv = 0.0f;
   if (SCORE == 0 && !a.renorm) {
     m = -INFINITY;
@@ -696,22 +840,8 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
       if (lane + 32 * i < a.E) sum += expf(l[i] - m);
     inv = 1.0f / warp_sum(sum);
   }
-  float g = 0.0f, inner = 0.0f;  // this lane's chosen expert's gradient; softmax's common term
-  if (a.renorm) {
-    const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
-    const float mx = warp_max(ls);
-    const float ex = on ? expf(ls - mx) : 0.0f;
-    const float q = ex / warp_sum(ex);
-    const float mean = warp_sum(on ? q * dw : 0.0f);
-    if (on) g = a.scale * q * (dw - mean);
-    if (SCORE == 1 && on) g *= sigmoid_f(-mine);
-  } else if (SCORE == 0) {
-    const float p = on ? expf(mine - m) * inv : 0.0f;
-    inner = a.scale * warp_sum(on ? p * dw : 0.0f);
-    if (on) g = a.scale * dw * p;
-  } else if (on) {
-    g = a.scale * dw * sigmoid_f(mine) * sigmoid_f(-mine);
-  }
+  float inner;
+  const float g = chosen_grad<SCORE>(a, on, mine, dw, m, inv, inner);
   float d[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -719,7 +849,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
     if (SCORE == 0 && !a.renorm && l[i] != -INFINITY) d[i] = -inner * expf(l[i] - m) * inv;
   }
   for (int j = 0; j < a.k; ++j) {
-    const int e = __shfl_sync(kFull, id, j);
+    const int e = __shfl_sync(kFull, on ? id : -1, j);
     const float v = __shfl_sync(kFull, g, j);
     if (e >= 0 && (e & 31) == lane) {
 #pragma unroll
@@ -746,10 +876,28 @@ cudaError_t launch_lanes(bool scored, bool grouped, dim3 g, cudaStream_t s, cons
                  : launch(route_kernel<L, V, SCORE, false, false>, g, 256, 0, s, a, vec);
 }
 
+template <typename L, int SCORE>
+cudaError_t launch_grad_rows(const RouteArgs& a, dim3 rows, cudaStream_t s) {
+  if (SCORE == 0 && !a.renorm) {
+    const int c = (a.E * (int)sizeof(L) + 511) / 512;
+    if (c <= 1) return launch(route_grad_rows_kernel<L, 1>, rows, 256, 0, s, a);
+    if (c <= 2) return launch(route_grad_rows_kernel<L, 2>, rows, 256, 0, s, a);
+    if (c <= 4) return launch(route_grad_rows_kernel<L, 4>, rows, 256, 0, s, a);
+    return launch(route_grad_rows_kernel<L, 8>, rows, 256, 0, s, a);
+  }
+  const int n = a.k <= 4 ? 4 : a.k <= 8 ? 8 : a.k <= 16 ? 16 : 32;
+  const dim3 g((unsigned)((a.T * n + 255) / 256));
+  if (n == 4) return launch(route_grad_chosen_kernel<L, SCORE, 4>, g, 256, 0, s, a);
+  if (n == 8) return launch(route_grad_chosen_kernel<L, SCORE, 8>, g, 256, 0, s, a);
+  if (n == 16) return launch(route_grad_chosen_kernel<L, SCORE, 16>, g, 256, 0, s, a);
+  return launch(route_grad_chosen_kernel<L, SCORE, 32>, g, 256, 0, s, a);
+}
+
 template <typename L, int SCORE, bool GRAD>
 cudaError_t launch_route(const RouteArgs& a, int sms, cudaStream_t s) {
   const dim3 grid((unsigned)((a.T + 7) / 8));
   const int v = (a.E + 31) / 32;
+  if (GRAD && a.E * sizeof(L) % 16 == 0) return launch_grad_rows<L, SCORE>(a, grid, s);
   // Up to 256 experts in groups of whole lanes, a power of two of them: neighbours in a lane;
   // warps go on to further tokens, so that the biases are read once.
   if (!GRAD && v <= 8) {

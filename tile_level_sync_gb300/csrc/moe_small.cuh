@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kSmallThreads, kSmallBlocks) small_up_kernel(S
     const uint16_t* w = a.W1t + ((int64_t)e * (ACT == 1 ? 2 : 1) * a.N1 + n) * a.D;
     const uint16_t* v = w + (int64_t)a.N1 * a.D;
     float z = 0.0f, g = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = lane * 8; c < a.D; c += 256) {
       const uint4 ww = ld_stream(w + c);
       uint4 vv;
