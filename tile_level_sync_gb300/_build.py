@@ -11,13 +11,16 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-CSRC = os.path.join(PKG, "csrc")
+CSRC = os.path.join(PKG, "csrc")          # the chains
+CSRC_MOE = os.path.join(PKG, "csrc_moe")  # the expert layer
 INCLUDE = os.path.join(ROOT, "include")
+OBJECTS = os.path.join(PKG, "build")
 LIB_PATH = os.path.join(PKG, "libcusync.so")
 
-SOURCES = [os.path.join(CSRC, f) for f in ("cusync.cu", "moe.cu", "moe_route_f32.cu", "moe_route_bf16.cu")]
+SOURCES = [os.path.join(CSRC, "cusync.cu")] + [
+    os.path.join(CSRC_MOE, f) for f in ("moe.cu", "moe_route_f32.cu", "moe_route_bf16.cu")]
 DEPS = SOURCES + [
-    os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".h", ".cuh"))
+    os.path.join(d, f) for d in (CSRC, CSRC_MOE) for f in sorted(os.listdir(d)) if f.endswith((".h", ".cuh"))
 ] + [os.path.join(INCLUDE, f) for f in ("cusync.h", "cusync_moe.h")]
 
 NVCC_FLAGS = [
@@ -47,7 +50,8 @@ def build(force=False, verbose=False, extra_flags=()):
     if not force and not needs_build():
         return LIB_PATH
     nvcc = _nvcc()
-    objs = [os.path.splitext(src)[0] + ".o" for src in SOURCES]
+    os.makedirs(OBJECTS, exist_ok=True)
+    objs = [os.path.join(OBJECTS, os.path.splitext(os.path.basename(src))[0] + ".o") for src in SOURCES]
     running = []
     for src, obj in zip(SOURCES, objs):
         cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-c", "-o", obj, src]

@@ -57,7 +57,7 @@
 #include <cstdint>
 
 #include "moe_plan.cuh"
-#include "ptx.cuh"
+#include "moe_ptx.cuh"
 
 namespace cusync {
 namespace moe {

@@ -14,7 +14,7 @@
 
 #include <cstdint>
 
-#include "ptx.cuh"
+#include "moe_ptx.cuh"
 
 namespace cusync {
 namespace moe {

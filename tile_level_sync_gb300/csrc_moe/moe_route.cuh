@@ -22,7 +22,7 @@
 #include <cstdint>
 
 #include "moe_launch.h"
-#include "ptx.cuh"
+#include "moe_ptx.cuh"
 
 namespace cusync {
 namespace moe {

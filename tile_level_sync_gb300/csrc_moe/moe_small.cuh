@@ -8,7 +8,7 @@
 #include <cstdint>
 
 #include "moe_gemm.cuh"
-#include "ptx.cuh"
+#include "moe_ptx.cuh"
 
 namespace cusync {
 namespace moe {
