@@ -208,6 +208,11 @@ MLPS = [
     dict(T=900, E=4, k=2, D=320, N1=192),
     dict(T=70, E=5, k=2, D=192, N1=320),
     dict(T=300, E=2, k=2, D=640, N1=64),
+    dict(T=40, E=4, k=1, D=8, N1=8),
+    dict(T=300, E=2, k=1, D=16, N1=8),
+    dict(T=200, E=1, k=1, D=24, N1=1000),
+    dict(T=300, E=2, k=1, D=1032, N1=64),
+    dict(T=600, E=200, k=5, D=64, N1=128),
 ]
 _name = lambda c: "T{T}E{E}k{k}D{D}N{N1}".format(**c)  # noqa: E731
 
