@@ -149,11 +149,13 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, float v) {
 // 1 / (1 + e^-x); the fast exponential and division are within a few 1e-7 of it
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
+// The same to an ulp or two, where 32 bits of the result count (dweights)
+__device__ __forceinline__ float sigmoid_full(float x) { return __frcp_rn(1.0f + expf(-x)); }
+
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
-// The factor of z in GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3))
-__device__ __forceinline__ float gelu_gate(float z) {
-  return sigmoid_fast(2.0f * kGeluC * (z + 0.044715f * z * z * z));
-}
+// The argument of the sigmoid in GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3)), and that sigmoid
+__device__ __forceinline__ float gelu_arg(float z) { return 2.0f * kGeluC * (z + 0.044715f * z * z * z); }
+__device__ __forceinline__ float gelu_gate(float z) { return sigmoid_fast(gelu_arg(z)); }
 
 // One tile of a launch: `rows` tokens of expert e from slot0 on (DW: all of the expert's),
 // output columns (DW: matrix rows) from m0 on, DW: columns from n0 on; nkb blocks of 64 k.
@@ -732,12 +734,12 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
             const float zz = __uint_as_float(z[i]) * whole, dh = __uint_as_float(g[i]) * whole, dhw = w * dh;
             float h, vz, vu = 0.0f;
             if (C::kG == 2) {
-              const float uu = __uint_as_float(u[i]) * whole, sg = sigmoid_fast(zz), zs = zz * sg;
+              const float uu = __uint_as_float(u[i]) * whole, sg = sigmoid_full(zz), zs = zz * sg;
               h = zs * uu;
               vz = dhw * uu * (sg + zs * (1.0f - sg));
               vu = dhw * zs;
             } else {
-              const float sg = gelu_gate(zz);
+              const float sg = sigmoid_full(gelu_arg(zz));
               h = zz * sg;
               vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
             }
