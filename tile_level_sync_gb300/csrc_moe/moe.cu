@@ -118,7 +118,7 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     L->x = bytes(L->S * L->D * 2);
     L->h = bytes(L->S * L->N1 * 2);
     L->rows = bytes(L->S * L->D * 2);
-    L->scales = bytes(L->S * div_up(L->D, 32) * 2);
+    L->scales = bytes(L->S / 32 * div_up(L->D, 32) * 2);
     L->work_bytes = b;
     b = L->plan_bytes;
     L->parts = (int32_t)(8 * div_up(L->N1, 256));  // one for 32 columns
@@ -127,7 +127,7 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     L->gh = bytes(L->S * L->N1 * 2);
     L->gz = bytes(L->S * L->G * L->N1 * 2);
     L->grows = bytes(L->S * L->D * 2);
-    L->gscales = bytes(L->S * div_up(L->D, 32) * 2);
+    L->gscales = bytes(L->S / 32 * div_up(L->D, 32) * 2);
     L->gpart = bytes(L->S * L->parts * 4);
     L->grad_bytes = b;
   }

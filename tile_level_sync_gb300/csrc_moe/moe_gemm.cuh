@@ -41,8 +41,8 @@
 // tiles of few rows.
 //
 // O and dX per slot are sums over a token's experts in fp32 still to be made: their 16 bits
-// are fp16 with a power of two for 32 columns of 32 rows (kept for each row), an error of
-// 2^-12 beside the 2^-9 of the bf16 result, at half the bytes of fp32.
+// are fp16 with a power of two for every 32 rows x 32 columns, an error of 2^-12 beside the
+// 2^-9 of the bf16 result, at half the bytes of fp32.
 //
 // Token rows behind an expert's last one are columns of their own and are not stored.  In
 // the weight gradients K runs over slots in steps of 16: dispatch_kernel and BWD1 store
@@ -79,7 +79,7 @@ struct GemmArgs {
   int32_t* plan;
   const float* weights;
   void* out;           // H, O, dZ, dX per slot, dW1t or dW2t
-  void* out2;          // BWD1: w H; FWD2, DX: scales, bf16 [slot][scales]
+  void* out2;          // BWD1: w H; FWD2, DX: scales, bf16 [slot / 32][scales]
   float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
   int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
   int32_t T, k, E;
@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
             if (C::kStaged || i + 1 < left) out[(i + 1) * pitch] = __half_as_ushort(__high2half(h));
           }
           if (C::kStaged) store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
-          if (c + lane < q.rows && q.m0 + lane0 < a.M)
-            reinterpret_cast<uint16_t*>(a.out2)[(int64_t)(q.slot0 + c + lane) * a.scales + (q.m0 + lane0) / 32] =
+          // tiles start at multiples of 32 slots: one scale for the block
+          if (lane == 0 && q.m0 + lane0 < a.M)
+            reinterpret_cast<uint16_t*>(a.out2)[(int64_t)(q.slot0 + c) / 32 * a.scales + (q.m0 + lane0) / 32] =
                 (uint16_t)((e - 14u) << 7);
         }
       } else if (C::kBwd1) {
