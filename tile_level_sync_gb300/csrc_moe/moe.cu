@@ -249,6 +249,15 @@ bool map_output(CUtensorMap* m, const void* p, int64_t rows, int64_t width, int 
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// A weight gradient [experts][rows, cols]: boxes of 32 x 32, 64-byte swizzle.
+bool map_gradient(CUtensorMap* m, void* p, int64_t experts, int64_t rows, int64_t cols) {
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)experts};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(rows * cols) * 2};
+  cuuint32_t box[3] = {32, 32, 1}, one[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // Token rows by slot, in the four box heights.
 bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, bool wide, int blocks, int last = 128) {
   bool ok = true;
@@ -553,11 +562,9 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   GemmArgs w1 = gemm_args(L, work, weights);
   w1.M = (int32_t)H;
   w1.N = (int32_t)L.D;
-  w1.out = dW1t;
   GemmArgs w2 = gemm_args(L, work, weights);
   w2.M = (int32_t)L.D;
   w2.N = (int32_t)L.N1;
-  w2.out = dW2t;
   const bool wide = L.D % 64 == 0 && L.N1 % 64 == 0;
   p.wide = x.wide = w1.wide = w2.wide = wide;
   // a weight gradient's stage holds two blocks of 64 rows on pairs, one on single CTAs
@@ -567,7 +574,8 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if (!map_gate_up(&p.mA, W1t, L.E, L.G, L.N1, L.D, wide) || !map_weights(&p.mA2, W2t, L.E, L.D, L.N1, 64, wide, 2) ||
       !map_tokens(p.mB, gx, L.S, L.D, wide, 1, last) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1, last) ||
       !map_weights(&x.mA, W1t, L.E, H, L.D, wide ? 128 : 64, wide, 2) || !map_tokens(x.mB, gz, L.S, H, wide, 2) ||
-      !map_output(&x.mO, rows, L.S, L.D, 32) ||
+      !map_output(&x.mO, rows, L.S, L.D, 32) || !map_gradient(&w1.mO, dW1t, L.E, H, L.D) ||
+      !map_gradient(&w2.mO, dW2t, L.E, L.D, L.N1) ||
       !map_rows(&w1.mA, gz, L.S, H, kr1, wide, 2) || !map_rows(&w1.mB[0], gx, L.S, L.D, kr1, wide, 2) ||
       !map_rows(&w2.mA, gy, L.S, L.D, kr2, wide, 2) || !map_rows(&w2.mB[0], gh, L.S, L.N1, kr2, wide, 2))
     return CUSYNC_ERR_CUDA;

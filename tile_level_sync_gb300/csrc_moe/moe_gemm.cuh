@@ -75,10 +75,10 @@ struct GemmArgs {
   CUtensorMap mB[4];   // tokens, boxes of 16, 32, 64 and 128 (BWD1 on pairs: 80) rows (gather: [0],
                        // one row); DW: [0], 64 rows
   CUtensorMap mB2[4];  // BWD1: dY
-  CUtensorMap mO;      // FWD1, FWD2, DX: the output by slot, boxes of a warp's columns x 32 rows
+  CUtensorMap mO;      // the output, boxes of 32 rows x a warp's columns (BWD1: none)
   int32_t* plan;
   const float* weights;
-  void* out;           // H, O, dZ, dX per slot, dW1t or dW2t
+  void* out;           // H, O, dZ or dX per slot
   void* out2;          // BWD1: w H; FWD2, DX: scales, bf16 [slot / 32][scales]
   float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
   int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
@@ -240,43 +240,24 @@ struct Walk {
   }
 };
 
-// 32 rows x 64 bytes, staged in shared memory (16-byte pieces, swizzled so that neither
-// side conflicts) and stored eight rows to an instruction.  `mine` is this lane's row; row
-// r of the warp goes to out + r * pitch when r < rows, its 16-byte pieces below `pieces`.
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&mine)[16], uint8_t* out, int64_t pitch,
-                                           int rows, int pieces, int lane) {
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane / 2)) & 3) * 16) =
-        make_uint4(mine[4 * i], mine[4 * i + 1], mine[4 * i + 2], mine[4 * i + 3]);
-  __syncwarp();
-  const int piece = lane % 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + lane / 4;
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ (r / 2)) & 3) * 16);
-    if (r < rows && piece < pieces) __stcs(reinterpret_cast<uint4*>(out + r * pitch + piece * 16), v);
-  }
-}
-
-// A warp's two blocks of 2 KB in turn for TMA stores of 32 tokens: the block to fill, once the
-// store before the last has read it ...
-template <int N>
+// A warp's two blocks of 2 KB in turn for TMA stores: the block to fill, once the store before
+// the last has read it ...
 __device__ __forceinline__ uint16_t* stage_block(uint8_t* stage, uint32_t blocks) {
-  if ((threadIdx.x & 31) == 0) ptx::bulk_wait_group_read<N - 1>();
+  if ((threadIdx.x & 31) == 0) ptx::bulk_wait_group_read<1>();
   __syncwarp();
-  return reinterpret_cast<uint16_t*>(stage + (blocks % N) * 2048);
+  return reinterpret_cast<uint16_t*>(stage + (blocks % 2) * 2048);
 }
-// ... and its store to columns from c0, slots from r0 on.  Slots behind an expert's last row
+// ... and its store: to columns from c0, rows from r0 of matrix e on; or, without e, to columns
+// from c0, slots from r0 on.  Slots behind an expert's last row
 // are written too: up to its next multiple of 32 they are no one else's, and no one's input
 // but to columns of their own.
 __device__ __forceinline__ void store_block(const CUtensorMap* m, uint8_t* stage, uint32_t& blocks, int32_t c0,
-                                            int32_t r0) {
+                                            int32_t r0, int32_t e = -1) {
   ptx::fence_proxy_async_smem();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
-    ptx::tma_store_2d(m, stage + (blocks % 2) * 2048, c0, r0);
+    if (e < 0) ptx::tma_store_2d(m, stage + (blocks % 2) * 2048, c0, r0);
+    else ptx::tma_store_3d(m, stage + (blocks % 2) * 2048, c0, r0, e);
     ptx::bulk_commit_group();
   }
   ++blocks;
@@ -641,7 +622,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
           const int f = q.m0 + lane0 / 2 + own, left = f < a.M ? q.rows - c - up : 0;
-          uint16_t* out = C::kStaged ? stage_block<2>(stage, blocks) + up * 16 + own
+          uint16_t* out = C::kStaged ? stage_block(stage, blocks) + up * 16 + own
                                      : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c + up) * a.M + f;
           const int64_t pitch = C::kStaged ? 16 : a.M;
 #pragma unroll
@@ -660,7 +641,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
           const int f = q.m0 + lane0 + lane, left = f < a.M ? q.rows - c : 0;
-          uint16_t* out = C::kStaged ? stage_block<2>(stage, blocks) + lane
+          uint16_t* out = C::kStaged ? stage_block(stage, blocks) + lane
                                      : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
           const int64_t pitch = C::kStaged ? 32 : a.M;
 #pragma unroll
@@ -694,7 +675,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
           }
           const uint32_t e = max(top >> 23, 15u);
           const float by = __uint_as_float((268u - e) << 23);
-          uint16_t* out = C::kStaged ? stage_block<2>(stage, blocks) + lane
+          uint16_t* out = C::kStaged ? stage_block(stage, blocks) + lane
                                      : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
           const int64_t pitch = C::kStaged ? 32 : a.M;
 #pragma unroll
@@ -755,11 +736,11 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
           if (live && lane < 16) a.part[(int64_t)mine * a.parts + (q.m0 + lane0) / 32] = s;
         }
       } else {
-        const int64_t m = (int64_t)q.m0 + lane0;
-        uint8_t* base = reinterpret_cast<uint8_t*>(a.out) + (((int64_t)q.e * a.M + m) * a.N + q.n0) * 2;
+        // a lane holds 32 columns of its row: four 16-byte pieces of 64-byte rows, placed as the
+        // map's 64-byte swizzle has them; rows and columns outside the matrix are not written
 #pragma unroll 1
         for (int c = first; c < C::kCols; c += step) {
-          uint32_t z[32], p[16];
+          uint32_t z[32];
           if (empty_tile) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0;
@@ -767,9 +748,17 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
             ptx::tmem_ld_32x32b_x32(d + c, z);
             ptx::tmem_ld_wait();
           }
+          if (q.n0 + c >= a.N || q.m0 + lane0 >= a.M) continue;
+          uint8_t* row = reinterpret_cast<uint8_t*>(stage_block(stage, blocks)) + lane * 64;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = pack2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1]));
-          store_rows(stage, p, base + c * 2, (int64_t)a.N * 2, (int)(a.M - m), (a.N - q.n0 - c) / 8, lane);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              p[j] = pack2(__uint_as_float(z[8 * i + 2 * j]), __uint_as_float(z[8 * i + 2 * j + 1]));
+            *reinterpret_cast<uint4*>(row + ((i ^ (lane / 2)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+          store_block(&a.mO, stage, blocks, q.n0 + c, q.m0 + lane0, q.e);
         }
       }
       if (!empty_tile) {
@@ -781,7 +770,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
         }
       }
     }
-    if (C::kStaged && lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
+    if ((C::kDw || C::kStaged) && lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
     if (!ok && lane == 0) {
       abort_flag = 1;
       a.plan[PLAN_ERR] = (int32_t)kErrWait;
