@@ -348,18 +348,21 @@ cudaError_t launch_gemm(bool pair, const GemmArgs& a, const Layer& L, int sms, c
 
 bool use_pairs(const Layer& L, int sms) { return L.A >= kPairRows * L.E && sms >= 2; }
 
-cudaError_t launch_dispatch(const Layer& L, void* work, const void* x, void* xs, const void* y, void* ys, int sms,
-                            cudaStream_t s) {
+cudaError_t launch_dispatch(const Layer& L, void* work, const void* x, void* xs, const void* y, void* ys, cudaStream_t s) {
   DispatchArgs d = {};
   d.plan = static_cast<int32_t*>(work);
   d.x = static_cast<const uint4*>(x);
   d.xs = static_cast<uint4*>(xs);
   d.y = static_cast<const uint4*>(y);
   d.ys = static_cast<uint4*>(ys);
-  d.row_of = L.row_of;
-  d.k = L.k;
+  d.T = L.T;
+  d.slot_of = L.slot_of;
+  d.counts = L.counts;
+  d.offsets = L.offsets;
+  d.k = (int32_t)L.k;
+  d.E = (int32_t)L.E;
   d.chunks = (int32_t)(L.D / 8);
-  const int64_t blocks = std::min<int64_t>(div_up(L.S, kDispatchThreads / 32), (int64_t)sms * 8);
+  const int64_t blocks = div_up((L.T + L.E) * d.chunks, kDispatchThreads);  // 2^31 of them would be an X of 8 TB
   return launch(dispatch_kernel, dim3((unsigned)blocks), kDispatchThreads, 0, s, d);
 }
 
@@ -510,7 +513,7 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
     for (int i = 1; i < 4; ++i) a.mB[i] = a.mB[0];
     e = L.G == 2 ? launch_gemm<FWD1G, 1, 1>(a, L, sms, s) : launch_gemm<FWD1G, 0, 1>(a, L, sms, s);
   } else {
-    e = launch_dispatch(L, work, X, w + L.x, nullptr, nullptr, sms, s);
+    e = launch_dispatch(L, work, X, w + L.x, nullptr, nullptr, s);
     if (e == cudaSuccess)
       e = L.G == 2 ? launch_gemm<FWD1, 1>(pair, a, L, sms, s) : launch_gemm<FWD1, 0>(pair, a, L, sms, s);
   }
@@ -584,7 +587,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
     w2.mB[i] = w2.mB[0];
   }
   cudaError_t e = launch_plan(L, ids, work, s);
-  if (e == cudaSuccess) e = launch_dispatch(L, work, X, gx, dY, gy, sms, s);
+  if (e == cudaSuccess) e = launch_dispatch(L, work, X, gx, dY, gy, s);
   if (e == cudaSuccess)
     e = L.G == 2 ? launch_gemm<BWD1, 1>(pair, p, L, sms, s) : launch_gemm<BWD1, 0>(pair, p, L, sms, s);
   if (e == cudaSuccess) e = launch_gemm<DX, 0>(pair, x, L, sms, s);

@@ -29,32 +29,40 @@ struct DispatchArgs {
   int32_t* plan;
   const uint4 *x, *y;    // [T, chunks] of 16 bytes
   uint4 *xs, *ys;        // [slots, chunks]; y and ys may be null
-  int64_t row_of;
-  int32_t k, chunks;
+  int64_t T, slot_of, counts, offsets;  // tokens; plan words
+  int32_t k, E, chunks;
 };
 
 constexpr int kDispatchThreads = 256;
 
-// Rows of X (and dY) into slot order, a warp per slot; zeros behind an expert's last row up
-// to the next multiple of kRowStep (the weight gradients sum over them).
+// Rows of X (and dY) into slot order: a thread reads 16 bytes of a token once and writes them
+// to each of its slots.  Behind the tokens come the experts: zeros from an expert's last row up
+// to the next multiple of kRowStep (the weight gradients sum over them).  4096 tokens of
+// D = 2048 in 8 slots each: 22 us, 46 us for two tensors, at the rate of the writes; a warp
+// per slot, which reads a token once for each slot, takes 32 and 62 us.
 __global__ void __launch_bounds__(kDispatchThreads) dispatch_kernel(DispatchArgs a) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t used = (int64_t)a.plan[PLAN_TILES] * kTileRows;
-  const int64_t warps = (int64_t)gridDim.x * (kDispatchThreads / 32);
-  for (int64_t s = (int64_t)blockIdx.x * (kDispatchThreads / 32) + (threadIdx.x >> 5); s < used; s += warps) {
-    const int32_t r = a.plan[a.row_of + s];
-    if (r < 0 && a.plan[a.row_of + s / kRowStep * kRowStep] < 0) continue;
-    const int64_t from = r < 0 ? 0 : (int64_t)(r / a.k) * a.chunks, to = s * a.chunks;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int64_t i = (int64_t)blockIdx.x * kDispatchThreads + threadIdx.x;
+  const int64_t t = i / a.chunks, c = i - t * a.chunks;
+  if (t < a.T) {
+    const uint4 x = a.x[i], y = a.y ? a.y[i] : x;
+    const int32_t* slots = a.plan + a.slot_of + t * a.k;
 #pragma unroll 4
-    for (int c = lane; c < a.chunks; c += 32) {
-      const uint4 x = r < 0 ? zero : a.x[from + c];
-      uint4 y = zero;
-      if (a.y && r >= 0) y = a.y[from + c];
-      a.xs[to + c] = x;
-      if (a.y) a.ys[to + c] = y;
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t slot = slots[j];
+      if (slot < 0) continue;
+      const int64_t to = (int64_t)slot * a.chunks + c;
+      a.xs[to] = x;
+      if (a.y) a.ys[to] = y;
+    }
+  } else if (t < a.T + a.E) {
+    const int e = (int)(t - a.T);
+    const int32_t count = a.plan[a.counts + e];
+    for (int32_t n = count; n % kRowStep; ++n) {
+      const int64_t to = (a.plan[a.offsets + e] + (int64_t)n) * a.chunks + c;
+      a.xs[to] = make_uint4(0, 0, 0, 0);
+      if (a.y) a.ys[to] = make_uint4(0, 0, 0, 0);
     }
   }
 }
