@@ -568,38 +568,36 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
         for (int i = 0; i < V; ++i) key[i] = 0u;
       }
     }
-    int id = -1;
-    uint32_t last = 0u;       // 32-bit logits: the key before, for equality but for the low bits
-    float before = INFINITY;  // scores: the value before
-    float gap = INFINITY;     // the closest pair
-    float least = -INFINITY;  // the last chosen
-    for (int j = 0; j <= a.k; ++j) {
+    // lane j: the j-th chosen key and its lane; `best`: the first one left out
+    uint32_t got = 0u, best;
+    int from = 0, n = 0;
+    for (;; ++n) {
       const uint32_t head = key[0] | kLow;
-      const uint32_t best = __reduce_max_sync(kFull, head);
-      if (best == kLow) break;  // none left
-      if (scored) {
-        const float value = unordered(best);
-        gap = fminf(gap, before - value);
-        before = value;
-      } else if (sizeof(L) == 4) {
-        if (last == best) gap = -1.0f;
-        last = best;
-        before = unordered(best & ~kLow);
-      }
-      if (j == a.k) break;
-      least = before;
+      best = __reduce_max_sync(kFull, head);
+      if (best == kLow || n == a.k) break;  // none left, or enough
       const int who = __ffs(__ballot_sync(kFull, head == best)) - 1;  // equal keys: the lowest expert
       const uint32_t won = __shfl_sync(kFull, key[0], who);
-      if (lane == j) id = who * V + (int)(~won & kLow);
+      if (lane == n) {
+        got = won;
+        from = who;
+      }
       if (lane == who) {
 #pragma unroll
         for (int i = 0; i + 1 < V; ++i) key[i] = key[i + 1];
         key[V - 1] = 0u;
       }
     }
-    if ((scored || sizeof(L) == 4) && !(gap > tol) && !lost) {
-      id = order_again<L, V, SCORE, scored>(a, t, lane, keep, least - 4.0f * tol);
-      lost = id == -2;
+    int id = lane < n ? from * V + (int)(~got & kLow) : -1;
+    if (scored || sizeof(L) == 4) {
+      // a chosen key against the one after it
+      const uint32_t below = __shfl_down_sync(kFull, got, 1) | kLow, after = lane == n - 1 ? best : below;
+      const bool close = scored ? !(unordered(got | kLow) - unordered(after) > tol) : (got | kLow) == after;
+      if (__any_sync(kFull, lane < n && after != kLow && close) && !lost) {
+        const uint32_t last = __shfl_sync(kFull, got, n - 1);
+        const float least = unordered(scored ? last | kLow : last & ~kLow);
+        id = order_again<L, V, SCORE, scored>(a, t, lane, keep, least - 4.0f * tol);
+        lost = id == -2;
+      }
     }
     if (__any_sync(kFull, lost)) id = select_again<L, V, SCORE>(a, t, lane);
     store_choice<L, SCORE>(a, t, lane, id, m, inv);
