@@ -542,21 +542,23 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
       auto value = [](uint32_t k) { return k ? unordered(k & ~kLow) : -INFINITY; };
       float rank = value(b1);
       if (a.group_top == 2 && a.group_size > 1) rank += value(b2);
-      if (mine >= a.groups) rank = -INFINITY;  // lanes behind the last group
-      // the other groups' ranks, by whole groups of lanes up the warp and round; of equal
-      // ranks the lower group is the better one
-      int better = 0;
-      for (int o = lanes; o < 32; o += lanes) {
-        const int from = (lane + o) & 31;
-        const float r = __shfl_sync(kFull, rank, from);
-        better += r > rank || (r == rank && from < leader);
-      }
+      // the groups in order of rank, of equal ones the lower first; a group's lanes hold the same
       const bool real = mine < a.groups;
-      keep = real && better < a.group_limit;
+      uint32_t left = real ? ordered(rank) : 0u, best, last = 0u;
+      keep = false;
+      for (int n = 0;; ++n) {
+        best = __reduce_max_sync(kFull, left);
+        if (best == 0u || n == a.group_limit) break;
+        last = best;
+        const int who = __ffs(__ballot_sync(kFull, left == best)) - 1;
+        if (leader == (who & -lanes)) {
+          keep = true;
+          left = 0u;
+        }
+      }
       // the closest pair across the border: scores, by the bound; 32-bit logits, by equality but
       // for the low bits
-      const float low = unordered(__reduce_min_sync(kFull, keep ? ordered(rank) : 0xffffffffu));
-      const float high = unordered(__reduce_max_sync(kFull, real && !keep ? ordered(rank) : ordered(-INFINITY)));
+      const float low = unordered(last), high = best ? unordered(best) : -INFINITY;
       if ((scored || sizeof(L) == 4) && high > -INFINITY && !(scored ? low - high > 2.0f * tol : low != high)) {
         const float floor = value(a.group_top == 2 && a.group_size > 1 ? b2 : b1) - 4.0f * tol;
         const unsigned bits = groups_again<L, V, SCORE, scored>(a, t, lane, real ? floor : INFINITY);
