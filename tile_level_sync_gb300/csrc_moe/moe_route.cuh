@@ -235,32 +235,44 @@ __device__ __noinline__ int select_again(const RouteArgs& a, int64_t t, int lane
   return id;
 }
 
-// Lane j < k holds the j-th chosen expert (-1: none): its weight, and both stored.  m and
-// inv: the row's largest logit and the inverse of its sum of exponentials (softmax weights
-// that are not renormalised).
+// The sum, or the maximum, over aligned groups of n neighbouring lanes, n a power of two.
+__device__ __forceinline__ float lanes_max(float v, int n) {
+  for (int o = n >> 1; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float lanes_sum(float v, int n) {
+  for (int o = n >> 1; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// The j-th lane of n (a power of two, at least k) that share token t holds its j-th chosen
+// expert (-1: none): its weight, and both stored.  t < 0: no token.  m and inv: the row's
+// largest logit and the inverse of its sum of exponentials (softmax weights that are not
+// renormalised).
 template <typename L, int SCORE>
-__device__ __forceinline__ void store_choice(const RouteArgs& a, int64_t t, int lane, int id, float m, float inv) {
-  const bool on = lane < a.k && id >= 0;
+__device__ __forceinline__ void store_choice(const RouteArgs& a, int64_t t, int lane, int n, int id, float m,
+                                             float inv) {
+  const int j = lane & (n - 1);
+  const bool mine_to_store = t >= 0 && j < a.k, on = mine_to_store && id >= 0;
   const float mine = on ? one_logit<L>(a, t, id) : -INFINITY;  // read again, from L1
   float w;
   if (a.renorm) {
     // s_j / sum s_i: softmax's as exponentials relative to the largest chosen logit; sigmoids
     // as they are, unless one is so small (below e^-60) that only its logarithm is safe
-    float ex;
-    if (SCORE == 0 || __any_sync(kFull, on && mine < -60.0f)) {
+    const unsigned small = SCORE == 0 ? 0u : __ballot_sync(kFull, on && mine < -60.0f);
+    float ex = SCORE == 0 ? 0.0f : on ? sigmoid_f(mine) : 0.0f;
+    if (SCORE == 0 || small) {
       const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
-      const float mx = warp_max(ls);
-      ex = on ? expf(ls - mx) : 0.0f;
-    } else {
-      ex = on ? sigmoid_f(mine) : 0.0f;
+      const float mx = lanes_max(ls, n);
+      if (SCORE == 0 || (small >> (lane - j) & (0xffffffffu >> (32 - n)))) ex = on ? expf(ls - mx) : 0.0f;
     }
-    w = ex / warp_sum(ex);
+    w = ex / lanes_sum(ex, n);
   } else {
     w = SCORE == 0 ? expf(mine - m) * inv : sigmoid_f(mine);
   }
-  if (lane < a.k) {
-    a.ids[t * a.k + lane] = id;
-    a.weights[t * a.k + lane] = on ? a.scale * w : 0.0f;
+  if (mine_to_store) {
+    a.ids[t * a.k + j] = id;
+    a.weights[t * a.k + j] = on ? a.scale * w : 0.0f;
   }
 }
 
@@ -491,6 +503,10 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
   // a group's lanes, this lane's group and the group's first lane
   const int lanes = a.group_size / V > 0 ? a.group_size / V : 1, mine = lane / lanes, leader = mine * lanes;
   bias_most = warp_max(bias_most);
+  const int share = a.k > 1 ? 1 << (32 - __clz(a.k - 1)) : 1;  // lanes of a choice
+  int held = 0, their_id = -1;
+  int64_t their_t = -1;
+  float their_m = 0.0f, their_inv = 0.0f;
   load_lane<V>(reinterpret_cast<const L*>(a.logits) + t * a.E, e0, a.E, vec, next);
   for (; t < a.T; t += warps) {
     float l[V];
@@ -602,7 +618,20 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
       }
     }
     if (__any_sync(kFull, lost)) id = select_again<L, V, SCORE>(a, t, lane);
-    store_choice<L, SCORE>(a, t, lane, id, m, inv);
+    // the choices of 32 / share tokens are stored together
+    const int moved = __shfl_sync(kFull, id, lane & (share - 1));
+    if ((lane & -share) == held) {
+      their_t = t;
+      their_id = moved;
+      their_m = m;
+      their_inv = inv;
+    }
+    held += share;
+    if (held == 32 || t + warps >= a.T) {
+      store_choice<L, SCORE>(a, their_t, lane, share, their_id, their_m, their_inv);
+      held = 0;
+      their_t = -1;
+    }
   }
 }
 
@@ -660,7 +689,7 @@ __global__ void __launch_bounds__(256) route_any_kernel(const __grid_constant__ 
   int id;
   sure = pick<float, V>(a, key, lane, tol, id) && sure;
   if (scored && !sure) id = select_again<L, V, SCORE>(a, t, lane);
-  store_choice<L, SCORE>(a, t, lane, id, m, 1.0f / sum);
+  store_choice<L, SCORE>(a, t, lane, 32, id, m, 1.0f / sum);
 }
 
 // ------------------------------------------------------------------ gradient
