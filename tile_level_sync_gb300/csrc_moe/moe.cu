@@ -159,8 +159,7 @@ cudaError_t prepare_pair() {
   if (e == cudaSuccess) e = prepare_gemm<BWD1, 0, PAIR>();
   if (e == cudaSuccess) e = prepare_gemm<BWD1, 1, PAIR>();
   if (e == cudaSuccess) e = prepare_gemm<DX, 0, PAIR>();
-  if (e == cudaSuccess) e = prepare_gemm<DW1, 0, PAIR>();
-  if (e == cudaSuccess) e = prepare_gemm<DW2, 0, PAIR>();
+  if (e == cudaSuccess) e = prepare_gemm<DW, 0, PAIR>();
   return e;
 }
 
@@ -328,7 +327,7 @@ GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
 
 template <int MODE, int ACT, int PAIR>
 cudaError_t launch_gemm(GemmArgs a, const Layer& L, int sms, cudaStream_t s) {
-  static_assert(MODE <= DW2 || MODE == FWD1G, "one counter for each product of a call");
+  static_assert(MODE <= DW || MODE == FWD1G, "one counter for each product of a call");
   a.counter = PLAN_COUNTERS + (MODE == FWD1G ? FWD1 : MODE);
   using C = GemmCfg<MODE, ACT, PAIR>;
   constexpr int count = C::kTileCount;
@@ -336,8 +335,11 @@ cudaError_t launch_gemm(GemmArgs a, const Layer& L, int sms, cudaStream_t s) {
   const int64_t row_tiles = count == PLAN_PAIRS ? L.max_pairs : count == PLAN_MIDS ? L.max_mids : L.S / kTileRows;
   a.m_tiles = (int32_t)div_up(a.M, C::kFeatures);
   a.n_tiles = C::kDw ? (int32_t)div_up(a.N, C::kCols) : 1;
+  a.m_tiles2 = (int32_t)div_up(a.M2, C::kFeatures);  // DW
+  a.n_tiles2 = (int32_t)div_up(a.N2, C::kCols);
   // an upper bound: how many tiles of rows there are is only known on the device
-  const int64_t tiles = (C::kDw ? (int64_t)a.E * a.n_tiles : row_tiles) * a.m_tiles;
+  const int64_t tiles = C::kDw ? a.E * ((int64_t)a.m_tiles * a.n_tiles + (int64_t)a.m_tiles2 * a.n_tiles2)
+                               : row_tiles * a.m_tiles;
   const int grid = PAIR * (int)std::max<int64_t>(1, std::min<int64_t>(tiles, sms / PAIR));
   return launch_cluster(PAIR, moe_gemm_kernel<MODE, ACT, PAIR>, dim3(grid), C::kThreads, C::kSmemBytes, s, a);
 }
@@ -544,7 +546,8 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if (d->num_sms) sms = std::min(sms, d->num_sms);
   char* w = static_cast<char*>(work);
   const int64_t H = L.G * L.N1;
-  const bool pair = use_pairs(L, sms), pair1 = H > 128 && sms >= 2, pair2 = L.D > 128 && sms >= 2;  // rows: slots; the weights' gradients'
+  // the weights' gradients take pairs where either has more rows than one CTA's tile
+  const bool pair = use_pairs(L, sms), pair_g = std::max(H, L.D) > 128 && sms >= 2;
   void *gx = w + L.gx, *gy = w + L.gy, *gh = w + L.gh, *gz = w + L.gz;
   void* rows = w + L.grows;
   float* part = reinterpret_cast<float*>(w + L.gpart);
@@ -562,38 +565,32 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   x.out = rows;
   x.out2 = w + L.gscales;
   x.scales = (int32_t)div_up(L.D, 32);
-  GemmArgs w1 = gemm_args(L, work, weights);
-  w1.M = (int32_t)H;
-  w1.N = (int32_t)L.D;
-  GemmArgs w2 = gemm_args(L, work, weights);
-  w2.M = (int32_t)L.D;
-  w2.N = (int32_t)L.N1;
+  GemmArgs g = gemm_args(L, work, weights);  // the weights' gradients
+  g.M = (int32_t)H;
+  g.N = (int32_t)L.D;
+  g.M2 = (int32_t)L.D;
+  g.N2 = (int32_t)L.N1;
   const bool wide = L.D % 64 == 0 && L.N1 % 64 == 0;
-  p.wide = x.wide = w1.wide = w2.wide = wide;
+  p.wide = x.wide = g.wide = wide;
   // a weight gradient's stage holds two blocks of 64 rows on pairs, one on single CTAs
-  const int kr1 = wide && pair1 ? 128 : 64, kr2 = wide && pair2 ? 128 : 64;
+  const int kr = wide && pair_g ? 128 : 64;
   const int last = pair ? kMidRows / 2 : 128;  // BWD1's highest token box
   // BWD1's stage holds one block, DX's two
   if (!map_gate_up(&p.mA, W1t, L.E, L.G, L.N1, L.D, wide) || !map_weights(&p.mA2, W2t, L.E, L.D, L.N1, 64, wide, 2) ||
       !map_tokens(p.mB, gx, L.S, L.D, wide, 1, last) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1, last) ||
       !map_weights(&x.mA, W1t, L.E, H, L.D, wide ? 128 : 64, wide, 2) || !map_tokens(x.mB, gz, L.S, H, wide, 2) ||
-      !map_output(&x.mO, rows, L.S, L.D, 32) || !map_gradient(&w1.mO, dW1t, L.E, H, L.D) ||
-      !map_gradient(&w2.mO, dW2t, L.E, L.D, L.N1) ||
-      !map_rows(&w1.mA, gz, L.S, H, kr1, wide, 2) || !map_rows(&w1.mB[0], gx, L.S, L.D, kr1, wide, 2) ||
-      !map_rows(&w2.mA, gy, L.S, L.D, kr2, wide, 2) || !map_rows(&w2.mB[0], gh, L.S, L.N1, kr2, wide, 2))
+      !map_output(&x.mO, rows, L.S, L.D, 32) || !map_gradient(&g.mO, dW1t, L.E, H, L.D) ||
+      !map_gradient(&g.mO2, dW2t, L.E, L.D, L.N1) ||
+      !map_rows(&g.mA, gz, L.S, H, kr, wide, 2) || !map_rows(&g.mB[0], gx, L.S, L.D, kr, wide, 2) ||
+      !map_rows(&g.mA2, gy, L.S, L.D, kr, wide, 2) || !map_rows(&g.mB2[0], gh, L.S, L.N1, kr, wide, 2))
     return CUSYNC_ERR_CUDA;
-  for (int i = 1; i < 4; ++i) {
-    w1.mB[i] = w1.mB[0];
-    w2.mB[i] = w2.mB[0];
-  }
   cudaError_t e = launch_plan(L, ids, work, s);
   if (e == cudaSuccess) e = launch_dispatch(L, work, X, gx, dY, gy, s);
   if (e == cudaSuccess)
     e = L.G == 2 ? launch_gemm<BWD1, 1>(pair, p, L, sms, s) : launch_gemm<BWD1, 0>(pair, p, L, sms, s);
   if (e == cudaSuccess) e = launch_gemm<DX, 0>(pair, x, L, sms, s);
   if (e == cudaSuccess) e = launch_combine(L, work, rows, w + L.gscales, nullptr, dX, part, dweights, s);
-  if (e == cudaSuccess) e = launch_gemm<DW1, 0>(pair1, w1, L, sms, s);
-  if (e == cudaSuccess) e = launch_gemm<DW2, 0>(pair2, w2, L, sms, s);
+  if (e == cudaSuccess) e = launch_gemm<DW, 0>(pair_g, g, L, sms, s);
   return status_of(e);
 }
 
