@@ -240,7 +240,7 @@ struct Walk {
     q.nkb = __shfl_sync(0xffffffffu, mine, 5);
     if (lane == 0) {
       if (rank == 0) ptx::mbar_arrive(&ring.empty[s]);
-      else ptx::mbar_arrive_cluster(ptx::mapa(&ring.empty[s], 0));
+      else ptx::mbar_arrive_relaxed(ptx::mapa(&ring.empty[s], 0));
       if (first_copier) ptx::mbar_arrive(&ring.taken[s]);
     }
     __syncwarp();
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
         __syncwarp();
         if (lane == 0) {
           if (rank == 0) ptx::mbar_arrive(&tempty[buf]);
-          else ptx::mbar_arrive_cluster(ptx::mapa(&tempty[buf], 0));
+          else ptx::mbar_arrive_relaxed(ptx::mapa(&tempty[buf], 0));
         }
       }
     }
