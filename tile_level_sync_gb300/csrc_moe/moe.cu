@@ -257,6 +257,15 @@ bool map_gradient(CUtensorMap* m, void* p, int64_t experts, int64_t rows, int64_
                   CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// dZ or w H by slot, [slots][g, cols]: boxes of 16 slots x 32 columns of one of the g parts.
+bool map_hidden(CUtensorMap* m, void* p, int64_t slots, int64_t g, int64_t cols) {
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)g, (cuuint64_t)slots};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)(g * cols) * 2};
+  cuuint32_t box[3] = {32, 1, 16}, one[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // Token rows by slot, in the four box heights.
 bool map_tokens(CUtensorMap (&m)[4], const void* p, int64_t rows, int64_t cols, bool wide, int blocks, int last = 128) {
   bool ok = true;
@@ -555,8 +564,6 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   GemmArgs p = gemm_args(L, work, weights);  // hidden layer and its gradient
   p.M = (int32_t)L.N1;
   p.K = (int32_t)L.D;
-  p.out = gz;
-  p.out2 = gh;
   p.part = part;
   p.parts = L.parts;
   GemmArgs x = gemm_args(L, work, weights);  // dX per slot
@@ -577,6 +584,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   const int last = pair ? kMidRows / 2 : 128;  // BWD1's highest token box
   // BWD1's stage holds one block, DX's two
   if (!map_gate_up(&p.mA, W1t, L.E, L.G, L.N1, L.D, wide) || !map_weights(&p.mA2, W2t, L.E, L.D, L.N1, 64, wide, 2) ||
+      !map_hidden(&p.mO, gz, L.S, L.G, L.N1) || !map_hidden(&p.mO2, gh, L.S, 1, L.N1) ||
       !map_tokens(p.mB, gx, L.S, L.D, wide, 1, last) || !map_tokens(p.mB2, gy, L.S, L.D, wide, 1, last) ||
       !map_weights(&x.mA, W1t, L.E, H, L.D, wide ? 128 : 64, wide, 2) || !map_tokens(x.mB, gz, L.S, H, wide, 2) ||
       !map_output(&x.mO, rows, L.S, L.D, 32) || !map_gradient(&g.mO, dW1t, L.E, H, L.D) ||

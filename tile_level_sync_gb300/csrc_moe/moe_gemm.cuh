@@ -78,12 +78,13 @@ struct GemmArgs {
   CUtensorMap mB[4];   // tokens, boxes of 16, 32, 64 and 128 (BWD1 on pairs: 80) rows (gather: [0],
                        // one row); DW: [0], X
   CUtensorMap mB2[4];  // BWD1: dY; DW: [0], w H
-  CUtensorMap mO;      // the output, boxes of 32 rows x a warp's columns (BWD1: none); DW: dW1t
-  CUtensorMap mO2;     // DW: dW2t
+  CUtensorMap mO;      // the output, boxes of 32 rows x a warp's columns; BWD1: dZ, 16 x 32;
+                       // DW: dW1t
+  CUtensorMap mO2;     // BWD1: w H; DW: dW2t
   int32_t* plan;
   const float* weights;
-  void* out;           // H, O, dZ or dX per slot
-  void* out2;          // BWD1: w H; FWD2, DX: scales, bf16 [slot / 32][scales]
+  void* out;           // H, O or dX per slot
+  void* out2;          // FWD2, DX: scales, bf16 [slot / 32][scales]
   float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
   int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
   int32_t T, k, E;
@@ -130,12 +131,14 @@ struct GemmCfg {
   // epilogue behind: twice the warps.
   static constexpr int kEpi = kBwd1 ? 16 : 8;
   static constexpr int kThreads = (kEpi + 4) * 32;
-  // Outputs by slot: on pairs staged in shared memory and stored by TMA, 32 rows at a time; on
+  // Outputs by slot: on pairs (BWD1: always) staged in shared memory and stored by TMA, 32 (16) rows at a time; on
   // single CTAs, whose tiles often have few rows, stored from registers, real rows only.
   static constexpr bool kStaged = PAIR == 2 && (kFwd1 || MODE == FWD2 || MODE == DX);
   static constexpr int kRing = (kDw || kStaged ? 192 : 224) * 1024;
   static constexpr int kStages = kRing / kStageBytes < 8 ? kRing / kStageBytes : 8;
-  static constexpr int kStageOut = kDw || kStaged ? 8 * 4096 : 0;  // epilogue: two blocks of 2 KB a warp
+  // epilogue: two blocks of 2 KB a warp; BWD1 one of 1 KB
+  static constexpr int kWarpOut = kBwd1 ? 1024 : kDw || kStaged ? 4096 : 0;
+  static constexpr int kStageOut = kEpi * kWarpOut;
   static constexpr int kAccCols = kAParts * kCols;
   static constexpr int kAccs = 2 * kAccCols <= 512 ? 2 : 1;
   static constexpr int kTmemCols = kAccs * kAccCols <= 256 ? 256 : 512;
@@ -154,8 +157,9 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, float v) {
 // 1 / (1 + e^-x); the fast exponential and division are within a few 1e-7 of it
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
-// The same to an ulp or two, where 32 bits of the result count (dweights)
-__device__ __forceinline__ float sigmoid_full(float x) { return __frcp_rn(1.0f + expf(-x)); }
+// The same to some ulp, where 32 bits of the result count (dweights): expf within 2, the division
+// within 2
+__device__ __forceinline__ float sigmoid_full(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
 
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 // The argument of the sigmoid in GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3)), and that sigmoid
@@ -608,12 +612,24 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
     const int first = ((warp - 2) >> 2) * cols;  // this warp's first, and from there to its next
     constexpr int step = C::kEpi / 4 * cols;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * 4096;
+    uint8_t* stage = ring + C::kStages * C::kStageBytes + (warp - 2) * C::kWarpOut;
     uint32_t acc = 0, blocks = 0;
     bool ok = true;
     while (walk.take(q, &ok)) {
       const bool empty_tile = q.nkb == 0;
       const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
+      // BWD1: the weights of this warp's tokens, while the product runs: of its first 16 in lanes
+      // 0 to 15, of the next in the others, of the third in w_held[1]
+      float w_held[2] = {0.0f, 0.0f};
+      if (C::kBwd1) {
+        static_assert(!C::kBwd1 || C::kCols <= 4 * step, "a warp's tokens fit w_held");
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = first + (2 * h + lane / 16) * step + lane % 16;
+          const int r = c < q.rows ? a.plan[a.row_of + q.slot0 + c] : -1;
+          if (r >= 0) w_held[h] = a.weights[r];
+        }
+      }
       if (!empty_tile) {
         ++acc;
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
@@ -704,16 +720,10 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
         const int f = q.m0 + lane0 + lane;
         const bool in = f < a.M;
         const float whole = 1.0f + kCutPerStep * (float)((a.K + 15) / 16);
-        const int stored = (q.rows + kRowStep - 1) / kRowStep * kRowStep;  // zeros behind the last row
 #pragma unroll 1
         for (int c = first; c < q.rows; c += step) {
-          const int token = lane & 15, mine = q.slot0 + c + token;
-          const bool live = c + token < q.rows;
-          const int r = live ? a.plan[a.row_of + mine] : -1;
-          const float w_lane = r >= 0 ? a.weights[r] : 0.0f;
+          const int nth = (c - first) / step;
           float dots[16];
-          uint16_t* dz = reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * (C::kG * (int64_t)a.M) + f;
-          uint16_t* wh = reinterpret_cast<uint16_t*>(a.out2) + (int64_t)(q.slot0 + c) * a.M + f;
           uint32_t z[16], u[16], g[16];
           ptx::tmem_ld_32x32b_x16(d + c, z);
           if (C::kG == 2) ptx::tmem_ld_32x32b_x16(d + C::kCols + c, u);
@@ -721,8 +731,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float w = __shfl_sync(0xffffffffu, w_lane, i);
-            const bool on = c + i < q.rows;
+            const float w = __shfl_sync(0xffffffffu, w_held[0], nth % 2 * 16 + i);
             const float zz = __uint_as_float(z[i]) * whole, dh = __uint_as_float(g[i]) * whole, dhw = w * dh;
             float h, vz, vu = 0.0f;
             if (C::kG == 2) {
@@ -736,14 +745,51 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
               vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
             }
             dots[i] = in ? dh * h : 0.0f;
-            if (in && c + i < stored) {
-              store_bf16(dz + (int64_t)i * (C::kG * (int64_t)a.M), on ? vz : 0.0f);
-              if (C::kG == 2) store_bf16(dz + (int64_t)i * (2 * (int64_t)a.M) + a.M, on ? vu : 0.0f);
-              store_bf16(wh + (int64_t)i * a.M, on ? w * h : 0.0f);
+            // two tokens to a register
+            z[i] = __float_as_uint(vz);
+            g[i] = __float_as_uint(w * h);
+            if (C::kG == 2) u[i] = __float_as_uint(vu);
+            if (i & 1) {
+              z[i / 2] = pack2(__uint_as_float(z[i - 1]), __uint_as_float(z[i]));
+              g[i / 2] = pack2(__uint_as_float(g[i - 1]), __uint_as_float(g[i]));
+              if (C::kG == 2) u[i / 2] = pack2(__uint_as_float(u[i - 1]), __uint_as_float(u[i]));
             }
           }
+          if (c + 16 > q.rows) {  // zeros behind the last row, to the end of these kRowStep
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int left = q.rows - c - 2 * i;
+              const uint32_t kept = left <= 0 ? 0u : left == 1 ? 0xffffu : 0xffffffffu;
+              z[i] &= kept;
+              g[i] &= kept;
+              if (C::kG == 2) u[i] &= kept;
+            }
+          }
+          auto put = [&](const uint32_t (&v)[16], const CUtensorMap* m, int part) {
+            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+            uint16_t* o = reinterpret_cast<uint16_t*>(stage) + lane;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              o[64 * i] = (uint16_t)v[i];
+              o[64 * i + 32] = (uint16_t)(v[i] >> 16);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::tma_store_3d(m, stage, q.m0 + lane0, part, q.slot0 + c);
+              ptx::bulk_commit_group();
+            }
+          };
+          if (q.m0 + lane0 < a.M) {
+            put(z, &a.mO, 0);
+            if (C::kG == 2) put(u, &a.mO, 1);
+            put(g, &a.mO2, 0);
+          }
           const float s = transpose_sum(dots, lane);
-          if (live && lane < 16) a.part[(int64_t)mine * a.parts + (q.m0 + lane0) / 32] = s;
+          if (lane < 16 && c + lane < q.rows)
+            a.part[(int64_t)(q.slot0 + c + lane) * a.parts + (q.m0 + lane0) / 32] = s;
+          if (nth % 2) w_held[0] = w_held[1];
         }
       } else {
         // A lane holds 32 columns of its row: four 16-byte pieces of 64-byte rows, placed as the
@@ -785,7 +831,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
         }
       }
     }
-    if ((C::kDw || C::kStaged) && lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
+    if (C::kWarpOut && lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
     if (!ok && lane == 0) {
       abort_flag = 1;
       a.plan[PLAN_ERR] = (int32_t)kErrWait;
