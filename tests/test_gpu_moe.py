@@ -238,6 +238,30 @@ def test_mlp(c, act, grad):
     _check_mlp(mlp_inputs(act=act, seed=7, **c), act, grad)
 
 
+@pytest.mark.parametrize("D,N1", [(64, 256), (256, 64), (72, 264), (520, 40), (128, 64), (8, 8)])
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_mlp_grad_of_narrow_matrices(D, N1, act):
+    """One weight gradient has fewer rows than a CTA's tile, the other may have more."""
+    _check_mlp(mlp_inputs(act=act, seed=11, T=150, D=D, N1=N1, E=3, k=2), act, True)
+
+
+@pytest.mark.parametrize("k", [1, 2, 3, 5, 16, 17, 32])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_choices_stored_together(k, score, renorm):
+    """Tokens that share a warp's store, with logits so low that only their logarithms are safe."""
+    T, E = 5003, 40
+    rng = np.random.default_rng(k)
+    logits = torch.from_numpy(rng.normal(size=(T, E)).astype(np.float32))
+    logits[::3] -= 80.0
+    logits[5::7, 2:] = -float("inf")
+    c = dict(T=T, E=E, k=k, score=score, renorm=renorm, scale=1.5)
+    want_ids, want_w = _oracle_route(c, logits, None)
+    ids, w = _run_route(c, logits, None, True)
+    assert np.array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want_w) <= ROUTE_TOL * np.abs(want_w) + 1e-37)
+
+
 @pytest.mark.parametrize("T", [3, 90])
 @pytest.mark.parametrize("act", ["swiglu", "gelu"])
 @pytest.mark.parametrize("grad", [False, True])
