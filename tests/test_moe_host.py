@@ -203,3 +203,20 @@ def test_binding_matches_the_header():
     assert re.findall(r"(\w+);", fields) == [f for f, _ in cs.cusync_moe_desc_t._fields_]
     fields = re.search(r"typedef struct \{([^}]*)\} cusync_moe_info_t;", src, re.S).group(1)
     assert re.findall(r"(\w+);", fields) == [f for f, _ in cs.cusync_moe_info_t._fields_]
+
+
+# ------------------------------------------------------------------ the kernels' sources
+
+def _sources():
+    for folder in ("csrc", "csrc_moe"):
+        at = os.path.join(ROOT, "tile_level_sync_gb300", folder)
+        for name in sorted(os.listdir(at)):
+            yield os.path.join(folder, name), open(os.path.join(at, name)).read()
+
+
+def test_every_arrival_on_a_barrier_releases():
+    """What a thread has read (a ring's slot, an accumulator) may be overwritten once its arrival is
+    seen: only a release orders the reads before that."""
+    arrivals = [(f, m.group(0)) for f, text in _sources() for m in re.finditer(r"mbarrier\.arrive[\w.:]*\.b64", text)]
+    assert any(f.startswith("csrc_moe") or f.endswith("ptx.cuh") for f, _ in arrivals)
+    assert [a for a in arrivals if ".release." not in a[1] and "tcgen05" not in a[1]] == []

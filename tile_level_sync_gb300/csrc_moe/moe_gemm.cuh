@@ -31,7 +31,12 @@
 //              rows a copy, through the plan's row indices).  A copy has a fixed cost
 //              besides its bytes, so a stage holds two blocks of 64 k where three such
 //              stages fit, and where widths allow one box brings all of an operand.
-//   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma.
+//   warp 1     TMEM owner; lane 0 (of a pair's first CTA) issues tcgen05.mma.  In a pair's second CTA
+//              it hands the accumulators that the epilogue there has read back to the first, and
+//              the last warp the ring's slots: arrivals across the pair need a release, which waits for
+//              the thread's own stores, and these two warps have none (the weight gradients'
+//              epilogue took 5200 cycles a tile in the second CTA, 3000 in the first, when it
+//              made them itself).
 //   warps 2 .. epilogue: two (BWD1: four) warps per TMEM lane quarter, 32 (16) columns each in
 //              turn.
 // Accumulators are double-buffered where two fit in TMEM's 512 columns.
@@ -208,9 +213,9 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs& a, int32_t t) {
   return r;
 }
 
-// The ring of claimed tiles.  full: one arrival by the claiming warp (each CTA has its
-// own); empty, taken (the first CTA's): arrivals by every warp that read the slot, and by the
-// first copying warp alone.
+// The ring of claimed tiles.  full: one arrival by the claiming warp; empty: arrivals by every
+// warp of the CTA that read the slot, and in a pair's first CTA one for all of the second's; each
+// CTA has its own.  taken (the first CTA's): an arrival by the first copying warp alone.
 struct TileRing {
   int32_t slot[kTileSlots][8];  // a Tile; rows < 0: no more
   uint64_t full[kTileSlots], empty[kTileSlots], taken[kTileSlots];
@@ -220,9 +225,8 @@ struct TileRing {
 template <int PAIR>
 struct Walk {
   TileRing& ring;
-  const int rank;
   uint32_t n;
-  __device__ __forceinline__ Walk(TileRing& r, int rank_) : ring(r), rank(rank_), n(0) {}
+  __device__ __forceinline__ explicit Walk(TileRing& r) : ring(r), n(0) {}
   // The next tile, in every lane.  False at the end, and (with *ok cleared) if a wait expired.
   __device__ __forceinline__ bool take(Tile& q, bool* ok, bool first_copier = false) {
     const uint32_t s = n % kTileSlots, par = (n / kTileSlots) & 1;
@@ -243,8 +247,7 @@ struct Walk {
     q.n0 = __shfl_sync(0xffffffffu, mine, 4);
     q.nkb = __shfl_sync(0xffffffffu, mine, 5);
     if (lane == 0) {
-      if (rank == 0) ptx::mbar_arrive(&ring.empty[s]);
-      else ptx::mbar_arrive_relaxed(ptx::mapa(&ring.empty[s], 0));
+      ptx::mbar_arrive(&ring.empty[s]);
       if (first_copier) ptx::mbar_arrive(&ring.taken[s]);
     }
     __syncwarp();
@@ -310,12 +313,13 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&tfull[i], 1);
-      ptx::mbar_init(&tempty[i], C::kEpi * PAIR);
+      ptx::mbar_init(&tempty[i], C::kEpi + (PAIR == 2 && rank == 0));  // and the other CTA's warp 1
     }
     ptx::mbar_init(&drain, 1);
     for (int i = 0; i < kTileSlots; ++i) {
       ptx::mbar_init(&tiles.full[i], 1);
-      ptx::mbar_init(&tiles.empty[i], PAIR == 2 ? 2 * C::kEpi + 5 : C::kEpi + 3);  // copies, MMA (first CTA), epilogue
+      // copies, warp 1, epilogue, and the last warp: the second CTA's own, the first CTA's for those
+      ptx::mbar_init(&tiles.empty[i], C::kEpi + (PAIR == 2 ? 4 : 3));
       ptx::mbar_init(&tiles.taken[i], 1);
     }
     ptx::mbar_init_fence();
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  Walk<PAIR> walk(tiles, rank);
+  Walk<PAIR> walk(tiles);
   Tile q;
 
   if (warp == 0 || warp == C::kEpi + 2) {
@@ -567,6 +571,23 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
         if (one) commit(&drain);  // MMAs still in flight
         ptx::mbar_wait_bounded(&drain, 0, kWaitNs);
       }
+    } else {
+      // a pair's second CTA: accumulators back to the first as the epilogue here is done with them
+      uint32_t acc = 0;
+      bool ok = true;
+      while (!abort_flag && walk.take(q, &ok)) {
+        if (q.nkb == 0) continue;
+        const uint32_t buf = acc % C::kAccs, use = acc / C::kAccs;
+        ++acc;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&tempty[buf], use & 1, kWaitNs));
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(&tempty[buf], 0));
+        __syncwarp();
+      }
+      if (!ok) {
+        abort_flag = 1;
+        a.plan[PLAN_ERR] = (int32_t)kErrWait;
+      }
     }
     __syncwarp();
   } else if (warp == C::kEpi + 3) {
@@ -598,6 +619,20 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
         ptx::mbar_arrive(&tiles.full[s]);
         if (PAIR == 2) ptx::mbar_arrive_cluster(ptx::mapa(&tiles.full[s], 1));
         if (t >= total) break;
+      }
+      if (!ok) {
+        abort_flag = 1;
+        a.plan[PLAN_ERR] = (int32_t)kErrWait;
+      }
+    } else if (rank == 1) {
+      // the ring's slots back to the claiming warp as all of this CTA's warps have read them
+      bool ok = true;
+      for (uint32_t n = 0; !abort_flag && walk.take(q, &ok); ++n) {
+        const uint32_t s = n % kTileSlots;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&tiles.empty[s], (n / kTileSlots) & 1, kWaitNs));
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(&tiles.empty[s], 0));
+        __syncwarp();
       }
       if (!ok) {
         abort_flag = 1;
@@ -824,10 +859,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
       if (!empty_tile) {
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) ptx::mbar_arrive(&tempty[buf]);
-          else ptx::mbar_arrive_relaxed(ptx::mapa(&tempty[buf], 0));
-        }
+        if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
       }
     }
     if (C::kWarpOut && lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks

@@ -50,14 +50,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* s
                : "memory");
 }
 
-// Arrival on an mbarrier of another CTA of the cluster, of a thread that has written nothing for
-// whoever waits: what it read there (shared memory, TMEM) has come into registers before.
-// The release of an ordinary arrival across the cluster makes the thread wait until its stores
-// to global memory have arrived.
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // 32 lanes x 16 consecutive 32-bit columns of TMEM.
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
