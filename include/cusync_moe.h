@@ -87,8 +87,9 @@ cusync_status_t cusync_moe_info(const cusync_moe_desc_t* d, cusync_moe_info_t* o
  *   ids = the top_k largest keys, largest first; weights = scale * s[ids] (renorm: over
  *   the sum of the chosen s).
  * Equal keys, and equal ranks of groups, go to the lowest index; keys that 32 bits cannot
- * tell apart are compared in 64.  A logit of -inf or NaN is never chosen; where nothing is
- * left to choose the id is -1 and the weight 0. */
+ * tell apart are compared in 64.  A logit of -inf or NaN, or a bias of -inf or NaN, is never
+ * chosen; a bias of +inf comes before all others.  A group with fewer keys left than its rank
+ * adds up ranks last.  Where nothing is left to choose the id is -1 and the weight 0. */
 cusync_status_t cusync_moe_route(const cusync_moe_desc_t* d, const void* logits, const float* bias, int32_t* ids,
                                  float* weights, cusync_stream_t stream);
 

@@ -45,10 +45,12 @@ def route(logits, bias, top_k, kind="softmax", groups=1, group_limit=0, group_to
     for t in range(T):
         key = [(-np.inf if np.isneginf(logits[t, e]) or np.isnan(logits[t, e])
                 else s[t, e] + (0.0 if bias is None else float(bias[e]))) for e in range(E)]
+        key = [-np.inf if np.isnan(x) else x for x in key]  # a bias of NaN
         rank = []
         for g in range(groups):
             best = sorted(key[g * size:(g + 1) * size], reverse=True)[:group_top]
-            rank.append((-sum(best), g))
+            # a group without as many keys as its rank adds up is last, beside a key of +inf too
+            rank.append((np.inf if -np.inf in best else -sum(best), g))
         kept = {g for _, g in sorted(rank)[:limit]}
         order = sorted((-key[e], e) for e in range(E) if e // size in kept and key[e] > -np.inf)[:top_k]
         for j, (_, e) in enumerate(order):

@@ -486,3 +486,32 @@ def run_mlp_grad_empty(m, s):
     m.mlp(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], work, out["dX"])
     torch.cuda.synchronize()
     return out
+
+
+# ------------------------------------------------------------------ routes at the edges of their range
+
+@pytest.mark.parametrize("E,groups,group_limit", [(20, 1, 1), (64, 1, 1), (100, 1, 1), (256, 1, 1), (300, 1, 1), (64, 8, 3),
+                                                  (256, 8, 4), (160, 8, 3), (32, 4, 2), (512, 4, 2)])
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("forced", ["one", "top_k", "many"])
+def test_route_with_biases_of_infinity(E, groups, group_limit, group_top, score, forced):
+    """A bias of +inf forces its expert, one of -inf or NaN switches it off; the logits are masked too, so that
+    groups hold a forced expert and nothing else."""
+    T = 40
+    k = min(4, group_limit * E // groups)
+    rng = np.random.default_rng(E + groups + group_top)
+    logits = torch.from_numpy(rng.normal(0, 1.5, (T, E)).astype(np.float32))
+    logits[::2][torch.from_numpy(rng.random((T // 2, E)) < 0.9)] = float("-inf")
+    bias = rng.normal(0, 0.1, E).astype(np.float32)
+    off = rng.permutation(E)
+    bias[off[-2]], bias[off[-1]] = -np.inf, np.nan
+    bias[off[:{"one": 1, "top_k": k, "many": min(40, E - 2)}[forced]]] = np.inf
+    c = dict(T=T, E=E, k=k, score=score, groups=groups, group_limit=group_limit, group_top=group_top, renorm=True)
+    for top_k in {1, k}:
+        c["k"] = top_k
+        with np.errstate(invalid="ignore"):
+            want_ids, want_w = _oracle_route(c, logits, torch.from_numpy(bias))
+        ids, w = _run_route(c, logits, torch.from_numpy(bias), True)
+        assert np.array_equal(ids, want_ids)
+        assert np.all(np.abs(w - want_w) <= ROUTE_TOL * np.abs(want_w) + 1e-37)

@@ -78,6 +78,11 @@ __device__ __forceinline__ void warp_best(double& key, int& idx) {
   }
 }
 
+// The rank of a group by its two largest keys: -inf where there is no second one, also beside
+// a first of +inf (whose sum is a NaN, which the maximum drops).
+__device__ __forceinline__ float rank_of_two(float first, float second) { return fmaxf(first + second, -INFINITY); }
+__device__ __forceinline__ double rank_of_two(double first, double second) { return fmax(first + second, (double)-INFINITY); }
+
 // Keeps the keys of the group_limit best groups, sets the others to -inf.  A group's rank
 // is the sum of its group_top (1 or 2) largest keys.  Lane g ends with group g's rank.
 // Returns false if ranks that decide are closer than tol.
@@ -110,7 +115,7 @@ __device__ bool keep_groups(const RouteArgs& a, F (&key)[V], int lane, F tol) {
       }
       int j2 = 0x7fffffff;
       warp_best(b2, j2);
-      r = m1 + b2;
+      r = rank_of_two(m1, b2);
     }
     if (lane == g) rank = r;
   }
@@ -446,7 +451,7 @@ __device__ __noinline__ unsigned groups_again(const RouteArgs& a, int64_t t, int
       b2 = k, d2 = d;
     }
   }
-  const int64_t rank = ordered_64(a.group_top == 2 && a.group_size > 1 ? d1 + d2 : d1);
+  const int64_t rank = ordered_64(a.group_top == 2 && a.group_size > 1 ? rank_of_two(d1, d2) : d1);
   int better = 0;
   for (int g = 0; g < a.groups; ++g) {
     const int64_t r = __shfl_sync(kFull, rank, g);
@@ -457,13 +462,14 @@ __device__ __noinline__ unsigned groups_again(const RouteArgs& a, int64_t t, int
 
 // The chosen experts (lane j: the j-th), where 32-bit keys could not decide: the candidates
 // from `least` on, the k-th key's approximation less its error, in the kept groups (this
-// lane's among them or not).  -2 in every lane if they do not fit.
+// lane's among them or not).  -2 in every lane if they do not fit, or are not the n that there
+// have to be.
 template <typename L, int V, int SCORE, bool scored>
-__device__ __noinline__ int order_again(const RouteArgs& a, int64_t t, int lane, bool keep, float least) {
+__device__ __noinline__ int order_again(const RouteArgs& a, int64_t t, int lane, bool keep, float least, int n) {
   int e;
   double key;
-  const int total = candidates<L, V, SCORE, scored>(a, t, lane, keep ? least : INFINITY, e, key);
-  if (total > 32) return -2;
+  const int total = candidates<L, V, SCORE, scored>(a, t, lane, keep ? least : NAN, e, key);
+  if (total > 32 || total < n) return -2;
   const int64_t o = ordered_64(key);
   int better = 0;
   for (int c = 0; c < total; ++c) {
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     bias[i] = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.0f;
-    if (bias[i] > -INFINITY) bias_most = fmaxf(bias_most, fabsf(bias[i]));
+    if (fabsf(bias[i]) < INFINITY) bias_most = fmaxf(bias_most, fabsf(bias[i]));
   }
   // a group's lanes, this lane's group and the group's first lane
   const int lanes = a.group_size / V > 0 ? a.group_size / V : 1, mine = lane / lanes, leader = mine * lanes;
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
       }
       auto value = [](uint32_t k) { return k ? unordered(k & ~kLow) : -INFINITY; };
       float rank = value(b1);
-      if (a.group_top == 2 && a.group_size > 1) rank += value(b2);
+      if (a.group_top == 2 && a.group_size > 1) rank = rank_of_two(rank, value(b2));
       // the groups in order of rank, of equal ones the lower first; a group's lanes hold the same
       const bool real = mine < a.groups;
       uint32_t left = real ? ordered(rank) : 0u, best, last = 0u;
@@ -581,7 +587,7 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
       const float low = unordered(last), high = best ? unordered(best) : -INFINITY;
       if ((scored || sizeof(L) == 4) && high > -INFINITY && !(scored ? low - high > 2.0f * tol : low != high)) {
         const float floor = value(a.group_top == 2 && a.group_size > 1 ? b2 : b1) - 4.0f * tol;
-        const unsigned bits = groups_again<L, V, SCORE, scored>(a, t, lane, real ? floor : INFINITY);
+        const unsigned bits = groups_again<L, V, SCORE, scored>(a, t, lane, real ? floor : NAN);
         lost = bits == 0;
         keep = real && ((bits >> mine) & 1u);
       }
@@ -611,13 +617,13 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
     }
     int id = lane < n ? from * V + (int)(~got & kLow) : -1;
     if (scored || sizeof(L) == 4) {
-      // a chosen key against the one after it
+      // a chosen key against the one after it; one of +inf (a bias) is never far enough from it
       const uint32_t below = __shfl_down_sync(kFull, got, 1) | kLow, after = lane == n - 1 ? best : below;
       const bool close = scored ? !(unordered(got | kLow) - unordered(after) > tol) : (got | kLow) == after;
       if (__any_sync(kFull, lane < n && after != kLow && close) && !lost) {
         const uint32_t last = __shfl_sync(kFull, got, n - 1);
-        const float least = unordered(scored ? last | kLow : last & ~kLow);
-        id = order_again<L, V, SCORE, scored>(a, t, lane, keep, least - 4.0f * tol);
+        const float least = unordered(scored ? min(last | kLow, ordered(INFINITY)) : last & ~kLow);
+        id = order_again<L, V, SCORE, scored>(a, t, lane, keep, least - 4.0f * tol, n);
         lost = id == -2;
       }
     }
