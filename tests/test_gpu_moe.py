@@ -515,3 +515,40 @@ def test_route_with_biases_of_infinity(E, groups, group_limit, group_top, score,
         ids, w = _run_route(c, logits, torch.from_numpy(bias), True)
         assert np.array_equal(ids, want_ids)
         assert np.all(np.abs(w - want_w) <= ROUTE_TOL * np.abs(want_w) + 1e-37)
+
+
+# ------------------------------------------------------------------ tokens that share an expert's rows
+
+# by the tile: gathered rows, copied rows on single CTAs, pairs of CTAs
+SHARED = [dict(T=48, E=4, k=1, D=64, N1=64), dict(T=200, E=2, k=1, D=136, N1=72), dict(T=600, E=2, k=1, D=128, N1=64),
+          dict(T=500, E=2, k=2, D=328, N1=192)]
+
+
+@pytest.mark.parametrize("c", SHARED, ids=_name)
+@pytest.mark.parametrize("down", [30, 36, 45])
+@pytest.mark.parametrize("grad", [False, True])
+def test_small_tokens_beside_large_ones(c, down, grad):
+    """Every second token 2^-down of its neighbours: its outputs and gradients keep the precision
+    that they would have alone (the oracle's bound goes by each token's own values)."""
+    s = mlp_inputs(act="gelu", seed=21, **c)
+    s["X"][::2] *= 2.0 ** -down
+    if grad:
+        s["dY"][1::2] *= 2.0 ** -down
+    _check_mlp(s, "gelu", grad)
+
+
+@pytest.mark.parametrize("c", SHARED, ids=_name)
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_a_huge_token_changes_no_other(c, act):
+    """A finite token of 2^50 times the others' size: every other token's bytes stay as they are."""
+    s = mlp_inputs(act=act, seed=22, **c)
+    m = layer(s, act)
+    keep = torch.arange(c["T"]) != 5
+    y, dx = run_mlp(m, s).cpu(), run_mlp_grad(m, s)["dX"].cpu()
+    s["X"][5] *= 2.0 ** 50
+    Y = run_mlp(m, s).cpu()
+    assert torch.equal(Y[keep], y[keep]) and bool(Y[5].isfinite().all())
+    s["X"][5] *= 2.0 ** -50
+    s["dY"][5] *= 2.0 ** 50
+    dX = run_mlp_grad(m, s)["dX"].cpu()
+    assert torch.equal(dX[keep], dx[keep]) and bool(dX[5].isfinite().all())

@@ -118,7 +118,7 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     L->x = bytes(L->S * L->D * 2);
     L->h = bytes(L->S * L->N1 * 2);
     L->rows = bytes(L->S * L->D * 2);
-    L->scales = bytes(L->S / 32 * div_up(L->D, 32) * 2);
+    L->scales = bytes(L->S * 8 * div_up(L->D, 256));
     L->work_bytes = b;
     b = L->plan_bytes;
     L->parts = (int32_t)(8 * div_up(L->N1, 256));  // one for 32 columns
@@ -127,7 +127,7 @@ cusync_status_t read_desc(const cusync_moe_desc_t* d, Layer* L, bool mlp) {
     L->gh = bytes(L->S * L->N1 * 2);
     L->gz = bytes(L->S * L->G * L->N1 * 2);
     L->grows = bytes(L->S * L->D * 2);
-    L->gscales = bytes(L->S / 32 * div_up(L->D, 32) * 2);
+    L->gscales = bytes(L->S * 8 * div_up(L->D, 256));
     L->gpart = bytes(L->S * L->parts * 4);
     L->grad_bytes = b;
   }
@@ -331,6 +331,7 @@ GemmArgs gemm_args(const Layer& L, void* work, const float* weights) {
   a.T = (int32_t)L.T;
   a.k = L.k;
   a.E = L.E;
+  a.slots = (int32_t)L.S;
   return a;
 }
 
@@ -382,8 +383,8 @@ cudaError_t launch_combine(const Layer& L, void* work, const void* rows, const v
   CombineArgs c = {};
   c.plan = static_cast<int32_t*>(work);
   c.rows = static_cast<const __half*>(rows);
-  c.scale = static_cast<const uint16_t*>(scale);
-  c.scales = (int32_t)div_up(L.D, 32);
+  c.scale = static_cast<const uint8_t*>(scale);
+  c.slots = (int32_t)L.S;
   c.weights = weights;
   c.out = out;
   c.part = part;
@@ -510,8 +511,7 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   b.M = (int32_t)L.D;
   b.K = (int32_t)L.N1;
   b.out = w + L.rows;
-  b.out2 = w + L.scales;
-  b.scales = (int32_t)div_up(L.D, 32);
+  b.scale = reinterpret_cast<uint8_t*>(w + L.scales);
   const bool wide = L.D % 64 == 0 && L.N1 % 64 == 0;
   a.wide = b.wide = wide;
   if (!(L.G == 2 ? map_gated(&a.mA, W1t, L.E, L.N1, L.D, wide, 2)
@@ -570,8 +570,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   x.M = (int32_t)L.D;
   x.K = (int32_t)H;
   x.out = rows;
-  x.out2 = w + L.gscales;
-  x.scales = (int32_t)div_up(L.D, 32);
+  x.scale = reinterpret_cast<uint8_t*>(w + L.gscales);
   GemmArgs g = gemm_args(L, work, weights);  // the weights' gradients
   g.M = (int32_t)H;
   g.N = (int32_t)L.D;

@@ -10,7 +10,7 @@
 //   mode   A (M)                      B (N)                  epilogue
 //   FWD1   W1t[e] rows (G * N1)       X by slot              h = act(z), bf16
 //   FWD1G  the same                   X (gather)
-//   FWD2   W2t[e] rows (D)            H                      O, fp16 scaled by 32 columns
+//   FWD2   W2t[e] rows (D)            H                      O, fp16 scaled by slot and 32 columns
 //   BWD1   W1t[e] gate, up;           X; dY by slot          dZ and w h, bf16; sums of dH h
 //          W2t[e] along N1
 //   DX     W1t[e] along D             dZ                     dX per slot, as O
@@ -46,8 +46,10 @@
 // tiles of few rows.
 //
 // O and dX per slot are sums over a token's experts in fp32 still to be made: their 16 bits
-// are fp16 with a power of two for every 32 rows x 32 columns, an error of 2^-12 beside the
-// 2^-9 of the bf16 result, at half the bytes of fp32.
+// are fp16 with a power of two for every slot and 32 columns, at half the bytes of fp32: at most
+// 2^-11 of a value off, where it is above 2^-29 of the slot's largest of the 32, beside the 2^-8 of
+// the bf16 result.  One power for 32 slots together saves 2 us of 379 (4096 tokens), but takes the
+// bits of a token that stands beside one 2^30 times as large.
 //
 // Token rows behind an expert's last one are columns of their own and are not stored.  In
 // the weight gradients K runs over slots in steps of 16: dispatch_kernel and BWD1 store
@@ -89,14 +91,14 @@ struct GemmArgs {
   int32_t* plan;
   const float* weights;
   void* out;           // H, O or dX per slot
-  void* out2;          // FWD2, DX: scales, bf16 [slot / 32][scales]
+  uint8_t* scale;      // FWD2, DX: exponents of the slots' blocks of 32 columns (scale_at)
   float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
   int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
   int32_t T, k, E;
   int32_t M;           // output columns (DW: rows of an expert's matrix)
   int32_t N;           // DW: output columns
   int32_t K;           // reduction length (not DW)
-  int32_t m_tiles, n_tiles, parts, scales;
+  int32_t m_tiles, n_tiles, parts, slots;
   int32_t M2, N2, m_tiles2, n_tiles2;  // DW: of dW2t
   int32_t counter;     // plan word that counts this launch's claimed tiles
   // Every width is a multiple of 64: the maps see rows as [width / 64][rows][64], and one
@@ -151,6 +153,12 @@ struct GemmCfg {
   static constexpr int kFeatures = (kGated ? 64 : 128) * PAIR;  // output columns of a tile (DW: rows)
   static constexpr int kSmemBytes = kStages * kStageBytes + kStageOut + 1024;
 };
+
+// Where the exponent of a slot's block of 32 columns is: those of 256 columns beside each other,
+// as a warp of combine_kernel reads them.
+__host__ __device__ __forceinline__ int64_t scale_at(int64_t slots, int64_t slot, int block) {
+  return ((block / 8) * slots + slot) * 8 + block % 8;
+}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -720,36 +728,30 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
           ptx::tmem_ld_32x32b_x32(d + c, z);
           ptx::tmem_ld_wait();
           const int left = f < a.M ? q.rows - c : 0;
-          // the largest finite value of 32 tokens x 32 columns is put into [2^14, 2^15); what is
-          // above 2^-29 of it keeps fp16's precision
-          float most = 0.0f;
+          // a token's largest finite value of these 32 columns is put into [2^14, 2^15); what is
+          // above 2^-29 of it keeps fp16's precision.  The sum lifts a magnitude's exponent by one,
+          // which makes infinities and NaN negative and so no maximum.
+          const uint32_t magnitude = f < a.M ? 0x7fffffffu : 0u;
+          int32_t mine = 0;  // lane i: the exponent of token c + i
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (i < left) most = fmaxf(most, fabsf(__uint_as_float(z[i])));
-          uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-          if (top >= 0x7f800000u) {  // an infinity among them: without those
-            most = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < left && (z[i] & 0x7fffffffu) < 0x7f800000u) most = fmaxf(most, fabsf(__uint_as_float(z[i])));
-            top = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+          for (int i = 0; i < 32; ++i) {
+            const int32_t top = __reduce_max_sync(0xffffffffu, (int32_t)((z[i] & magnitude) + 0x00800000u));
+            const int32_t e = max(top >> 23, 16);
+            z[i] = __float_as_uint(__uint_as_float(z[i]) * __uint_as_float((uint32_t)(269 - e) << 23));
+            if (lane == i) mine = e - 15;
           }
-          const uint32_t e = max(top >> 23, 15u);
-          const float by = __uint_as_float((268u - e) << 23);
           uint16_t* out = C::kStaged ? stage_block(stage, blocks) + lane
                                      : reinterpret_cast<uint16_t*>(a.out) + (int64_t)(q.slot0 + c) * a.M + f;
           const int64_t pitch = C::kStaged ? 32 : a.M;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(z[i]) * by, __uint_as_float(z[i + 1]) * by);
+            const __half2 h = __floats2half2_rn(__uint_as_float(z[i]), __uint_as_float(z[i + 1]));
             if (C::kStaged || i < left) out[i * pitch] = __half_as_ushort(__low2half(h));
             if (C::kStaged || i + 1 < left) out[(i + 1) * pitch] = __half_as_ushort(__high2half(h));
           }
           if (C::kStaged) store_block(&a.mO, stage, blocks, q.m0 + lane0, q.slot0 + c);
-          // tiles start at multiples of 32 slots: one scale for the block
-          if (lane == 0 && q.m0 + lane0 < a.M)
-            reinterpret_cast<uint16_t*>(a.out2)[(int64_t)(q.slot0 + c) / 32 * a.scales + (q.m0 + lane0) / 32] =
-                (uint16_t)((e - 14u) << 7);
+          if (c + lane < q.rows && q.m0 + lane0 < a.M)
+            a.scale[scale_at(a.slots, q.slot0 + c + lane, (q.m0 + lane0) / 32)] = (uint8_t)mine;
         }
       } else if (C::kBwd1) {
         const int f = q.m0 + lane0 + lane;

@@ -15,14 +15,14 @@ namespace moe {
 
 struct CombineArgs {
   int32_t* plan;
-  const __half* rows;    // [slots, D], scaled by 32 rows x 32 columns
-  const uint16_t* scale; // bf16 [slots / 32, ceil(D / 32)]
+  const __half* rows;    // [slots, D], scaled by slot and 32 columns
+  const uint8_t* scale;  // exponents of those powers of two (scale_at)
   const float* weights;  // [T, k], or null: plain sums
   void* out;             // [T, D] bf16
   const float* part;     // gradient: sums of dH h, [slots][parts]; null otherwise
   float* dweights;       // [T, k]
   int64_t slot_of;
-  int32_t T, k, D, scales, parts, used;  // used: sums of a slot, of parts
+  int32_t T, k, D, slots, parts, used;  // used: sums of a slot, of parts
 };
 
 struct DispatchArgs {
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(CombineArgs a)
       const int32_t slot = slots[j];
       if (slot < 0) continue;
       const uint4 v = __ldcs(reinterpret_cast<const uint4*>(a.rows + (int64_t)slot * a.D + c));
-      const float unit = __uint_as_float((uint32_t)a.scale[(int64_t)(slot / 32) * a.scales + c / 32] << 16);
+      const float unit = __uint_as_float((uint32_t)a.scale[scale_at(a.slots, slot, c / 32)] << 23);
       const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
       const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
