@@ -552,3 +552,25 @@ def test_a_huge_token_changes_no_other(c, act):
     s["dY"][5] *= 2.0 ** 50
     dX = run_mlp_grad(m, s)["dX"].cpu()
     assert torch.equal(dX[keep], dx[keep]) and bool(dX[5].isfinite().all())
+
+
+@pytest.mark.parametrize("T", [40, 600])
+@pytest.mark.parametrize("D", [1024, 4096, 16384])
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+def test_dweights_of_exact_sums(T, D, act):
+    """Rows with a single one: the products' sums are exact, whatever their length.  What is left:
+    the sigmoid, its exponential and its division 2 steps of 2^-23 each, and half of one for each
+    addition, for its argument in GeLU (weighed by less than 0.3) and for the products with it, u
+    and dH; 5 + N1 / 32 additions of positive terms: 2^-23 (4 + 0.5 * (1 + 2 + 3 + 7)) < 11 steps."""
+    E, N1 = 2, 64
+    s = mlp_inputs(T, E, 1, D, N1, act, seed=31)
+    for n in ("W1t", "W2t"):
+        s[n] = (0.5 + 0.5 * s[n].float().abs().clamp(max=1.0)).to(torch.bfloat16)
+    rng = np.random.default_rng(T + D)
+    for n in ("X", "dY"):
+        s[n].zero_()
+        s[n][torch.arange(T), torch.from_numpy(rng.integers(0, D, T))] = 1.0
+    want = ref.mlp_grad(*(f64(s[n]) for n in ("X", "W1t", "W2t")), s["ids"].numpy(), f64(s["weights"]), f64(s["dY"]), act)
+    got = f64(run_mlp_grad(layer(s, act), s)["dweights"])
+    value = want["dweights"][0]
+    assert np.all(np.abs(got - value) <= 11 * 2.0 ** -23 * value)

@@ -106,13 +106,6 @@ struct GemmArgs {
   int32_t wide;
 };
 
-// What a 16-product step of the MMA loses of a sum on average.  Its adder cuts what lies
-// behind the accumulator's 24 bits, always towards zero, so the loss adds up over K where
-// rounding would not: measured 1.2e-8 to 1.5e-8 of the sum a step for normal products (K = 256
-// to 8192), more for products of one sign.  BWD1, whose dweights are fp32, gives the least of
-// it back: dweights at D = 2048, N1 = 1024 are 1.9e-6 off with it and 6.1e-6 without.
-constexpr float kCutPerStep = 1.3e-8f;
-
 template <int MODE, int ACT, int PAIR>
 struct GemmCfg {
   static constexpr bool kDw = MODE == DW;
@@ -754,9 +747,11 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
             a.scale[scale_at(a.slots, q.slot0 + c + lane, (q.m0 + lane0) / 32)] = (uint8_t)mine;
         }
       } else if (C::kBwd1) {
+        // The MMA's adder cuts what lies behind the accumulator's 24 bits, towards zero: normal
+        // operands lose 1.2e-8 to 1.5e-8 of a sum in each step of 16 products (K = 256 to 8192), sums
+        // that are exact nothing.  The values are taken as they are: no factor is right for both.
         const int f = q.m0 + lane0 + lane;
         const bool in = f < a.M;
-        const float whole = 1.0f + kCutPerStep * (float)((a.K + 15) / 16);
 #pragma unroll 1
         for (int c = first; c < q.rows; c += step) {
           const int nth = (c - first) / step;
@@ -769,10 +764,10 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float w = __shfl_sync(0xffffffffu, w_held[0], nth % 2 * 16 + i);
-            const float zz = __uint_as_float(z[i]) * whole, dh = __uint_as_float(g[i]) * whole, dhw = w * dh;
+            const float zz = __uint_as_float(z[i]), dh = __uint_as_float(g[i]), dhw = w * dh;
             float h, vz, vu = 0.0f;
             if (C::kG == 2) {
-              const float uu = __uint_as_float(u[i]) * whole, sg = sigmoid_full(zz), zs = zz * sg;
+              const float uu = __uint_as_float(u[i]), sg = sigmoid_full(zz), zs = zz * sg;
               h = zs * uu;
               vz = dhw * uu * (sg + zs * (1.0f - sg));
               vu = dhw * zs;
