@@ -85,11 +85,14 @@ cusync_status_t cusync_moe_info(const cusync_moe_desc_t* d, cusync_moe_info_t* o
  *   s = softmax or sigmoid of the logits; key = s + bias (bias [experts] fp32, or NULL)
  *   groups > 1: only experts of the group_limit groups with the largest rank remain
  *   ids = the top_k largest keys, largest first; weights = scale * s[ids] (renorm: over
- *   the sum of the chosen s).
+ *   the sum of the chosen s).  Scores grow with their logits: without a bias, and where ranks
+ *   are single keys, experts go by their logits alone.
  * Equal keys, and equal ranks of groups, go to the lowest index; keys that 32 bits cannot
  * tell apart are compared in 64.  A logit of -inf or NaN, or a bias of -inf or NaN, is never
- * chosen; a bias of +inf comes before all others.  A group with fewer keys left than its rank
- * adds up ranks last.  Where nothing is left to choose the id is -1 and the weight 0. */
+ * chosen; a bias of +inf comes before all others.  A logit of +inf has the score that it
+ * tends to: 1 for sigmoid; for softmax an equal share with the token's other +inf, where all
+ * other scores are 0.  A group with fewer keys left than its rank adds up ranks last.  Where
+ * nothing is left to choose the id is -1 and the weight 0. */
 cusync_status_t cusync_moe_route(const cusync_moe_desc_t* d, const void* logits, const float* bias, int32_t* ids,
                                  float* weights, cusync_stream_t stream);
 

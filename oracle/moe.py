@@ -22,20 +22,29 @@ def sigmoid(x):
     return np.exp(-np.logaddexp(0.0, -x))
 
 
+def _below(l, most):
+    """l - most, 0 where both are +inf."""
+    with np.errstate(invalid="ignore"):
+        return np.where(l == most, 0.0, l - most)
+
+
 def scores(logits, kind):
-    """fp64 scores; a logit of -inf or NaN scores 0."""
+    """fp64 scores; a logit of -inf or NaN scores 0, one of +inf what it tends to (softmax: all there
+    is, shared with other +inf)."""
     l = np.where(np.isnan(logits), -np.inf, logits)
     with np.errstate(invalid="ignore"):
         if kind == "sigmoid":
             return sigmoid(l)
         m = l.max(axis=1, keepdims=True)
-        e = np.where(np.isneginf(l), 0.0, np.exp(l - np.where(np.isneginf(m), 0.0, m)))
+        e = np.where(np.isneginf(l), 0.0, np.exp(_below(l, np.where(np.isneginf(m), 0.0, m))))
         total = e.sum(axis=1, keepdims=True)
         return np.divide(e, total, out=np.zeros_like(e), where=total > 0)
 
 
 def route(logits, bias, top_k, kind="softmax", groups=1, group_limit=0, group_top=1, renorm=False, scale=1.0):
-    """(ids, weights), by sorting python tuples: no vectorised selection to get wrong."""
+    """(ids, weights), by sorting python tuples: no vectorised selection to get wrong.  Where no bias
+    and no sum of two keys decides, experts go by their logits: scores that 64 bits round to the
+    same number grow with them all the same."""
     T, E = logits.shape
     s = scores(logits, kind)
     ids = np.full((T, top_k), -1, np.int32)
@@ -46,6 +55,8 @@ def route(logits, bias, top_k, kind="softmax", groups=1, group_limit=0, group_to
         key = [(-np.inf if np.isneginf(logits[t, e]) or np.isnan(logits[t, e])
                 else s[t, e] + (0.0 if bias is None else float(bias[e]))) for e in range(E)]
         key = [-np.inf if np.isnan(x) else x for x in key]  # a bias of NaN
+        if bias is None and (groups == 1 or group_top == 1):
+            key = [-np.inf if np.isnan(x) else x for x in logits[t].astype(np.float64)]
         rank = []
         for g in range(groups):
             best = sorted(key[g * size:(g + 1) * size], reverse=True)[:group_top]
@@ -59,7 +70,7 @@ def route(logits, bias, top_k, kind="softmax", groups=1, group_limit=0, group_to
             chosen = ids[t, :len(order)]
             l = logits[t, chosen].astype(np.float64)
             ls = l if kind == "softmax" else -np.logaddexp(0.0, -l)
-            w = np.exp(ls - ls.max())
+            w = np.exp(_below(ls, ls.max()))
             weights[t, :len(order)] = w / w.sum()
     return ids, scale * weights
 

@@ -574,3 +574,29 @@ def test_dweights_of_exact_sums(T, D, act):
     got = f64(run_mlp_grad(layer(s, act), s)["dweights"])
     value = want["dweights"][0]
     assert np.all(np.abs(got - value) <= 11 * 2.0 ** -23 * value)
+
+
+@pytest.mark.parametrize("c", ROUTES, ids=lambda c: f"T{c['T']}E{c['E']}k{c['k']}{c['score']}")
+@pytest.mark.parametrize("f32", [True, False])
+def test_route_with_logits_of_infinity(c, f32):
+    """Rows with one +inf, several, nothing else, and none; their weights and gradients."""
+    logits, bias = _route_case(c, f32, "none", seed=3)
+    rng = np.random.default_rng(c["E"])
+    T, E = logits.shape
+    logits[::4, rng.integers(0, E)] = float("inf")
+    logits[1::4][torch.from_numpy(rng.random(logits[1::4].shape) < 0.2)] = float("inf")
+    logits[1::4][torch.from_numpy(rng.random(logits[1::4].shape) < 0.2)] = float("-inf")
+    logits[2::8] = float("inf")
+    want_ids, want_w = _oracle_route(c, logits, bias)
+    ids, w = _run_route(c, logits, bias, f32)
+    assert np.array_equal(ids, want_ids)
+    assert np.all(np.abs(w - want_w) <= ROUTE_TOL * np.abs(want_w) + 1e-37)
+    dw = rng.normal(size=ids.shape).astype(np.float32)
+    dl = torch.full_like(logits, 77).cuda()
+    _layer(c, f32).route_grad(logits.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(dw).cuda(), dl)
+    renorm, scale = c.get("renorm", False), c.get("scale", 1.0)
+    want = ref.route_grad(f64(logits), ids, dw.astype(np.float64), c["score"], renorm, scale)
+    # as in test_route_grad, the scores of at most 1 left out
+    size = scale * np.abs(dw).max(axis=1, keepdims=True)
+    half = 0.0 if f32 else ref.BF16
+    assert np.all(np.abs(f64(dl) - want) <= 2 * ROUTE_TOL * size + half * np.abs(want))

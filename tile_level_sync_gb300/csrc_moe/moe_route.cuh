@@ -78,6 +78,13 @@ __device__ __forceinline__ void warp_best(double& key, int& idx) {
   }
 }
 
+// l - most for softmax's exponential; a logit of +inf is as far from the largest as what it tends
+// to, 0 from itself and from others of its kind.
+template <typename F>
+__device__ __forceinline__ F below(F l, F most) {
+  return l == most ? (F)0 : l - most;
+}
+
 // The rank of a group by its two largest keys: -inf where there is no second one, also beside
 // a first of +inf (whose sum is a NaN, which the maximum drops).
 __device__ __forceinline__ float rank_of_two(float first, float second) { return fmaxf(first + second, -INFINITY); }
@@ -222,7 +229,7 @@ __device__ __noinline__ int select_again(const RouteArgs& a, int64_t t, int lane
     sum = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (l[i] > -INFINITY) sum += exp((double)l[i] - (double)m);
+      if (l[i] > -INFINITY) sum += exp(below((double)l[i], (double)m));
     sum = warp_sum(sum);
   }
   double key[V];
@@ -230,7 +237,7 @@ __device__ __noinline__ int select_again(const RouteArgs& a, int64_t t, int lane
   for (int i = 0; i < V; ++i) {
     key[i] = -INFINITY;
     if (l[i] > -INFINITY) {
-      double k = SCORE == 0 ? exp((double)l[i] - (double)m) / sum : 1.0 / (1.0 + exp(-(double)l[i]));
+      double k = SCORE == 0 ? exp(below((double)l[i], (double)m)) / sum : 1.0 / (1.0 + exp(-(double)l[i]));
       if (a.bias) k += (double)a.bias[lane + 32 * i];
       if (k == k) key[i] = k;
     }
@@ -269,11 +276,11 @@ __device__ __forceinline__ void store_choice(const RouteArgs& a, int64_t t, int 
     if (SCORE == 0 || small) {
       const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
       const float mx = lanes_max(ls, n);
-      if (SCORE == 0 || (small >> (lane - j) & (0xffffffffu >> (32 - n)))) ex = on ? expf(ls - mx) : 0.0f;
+      if (SCORE == 0 || (small >> (lane - j) & (0xffffffffu >> (32 - n)))) ex = on ? expf(below(ls, mx)) : 0.0f;
     }
     w = ex / lanes_sum(ex, n);
   } else {
-    w = SCORE == 0 ? expf(mine - m) * inv : sigmoid_f(mine);
+    w = SCORE == 0 ? expf(below(mine, m)) * inv : sigmoid_f(mine);
   }
   if (mine_to_store) {
     a.ids[t * a.k + j] = id;
@@ -393,7 +400,7 @@ __device__ __forceinline__ int candidates(const RouteArgs& a, int64_t t, int lan
     m = warp_max(m);
     sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += l[i] > -INFINITY ? exp((double)l[i] - (double)m) : 0.0;
+    for (int i = 0; i < V; ++i) sum += l[i] > -INFINITY ? exp(below((double)l[i], (double)m)) : 0.0;
     sum = warp_sum(sum);
   }
   int total = 0, src = -1, part = 0;
@@ -401,7 +408,7 @@ __device__ __forceinline__ int candidates(const RouteArgs& a, int64_t t, int lan
   for (int i = 0; i < V; ++i) {
     float k = l[i];
     if (scored && l[i] > -INFINITY) {
-      k = SCORE == 0 ? __expf(l[i] - m) / (float)sum : sigmoid_f(l[i]);
+      k = SCORE == 0 ? __expf(below(l[i], m)) / (float)sum : sigmoid_f(l[i]);
       if (a.bias) k += a.bias[lane * V + i];
     }
     for (unsigned mask = __ballot_sync(kFull, k > -INFINITY && k >= floor); mask; mask &= mask - 1, ++total)
@@ -421,7 +428,7 @@ __device__ __forceinline__ int candidates(const RouteArgs& a, int64_t t, int lan
   if (src >= 0) {
     key = mine;
     if (scored) {
-      key = SCORE == 0 ? exp((double)mine - (double)m) / sum : 1.0 / (1.0 + exp(-(double)mine));
+      key = SCORE == 0 ? exp(below((double)mine, (double)m)) / sum : 1.0 / (1.0 + exp(-(double)mine));
       if (a.bias) key += (double)a.bias[e];
     }
   }
@@ -528,9 +535,10 @@ __global__ void __launch_bounds__(256, kRouteBlocks) route_kernel(const __grid_c
       m = warp_max(m);
       float sum = 0.0f;
       if (m > -INFINITY) {
+        const bool finite = m < INFINITY;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float ex = expf(l[i] - m);
+          const float ex = finite ? expf(l[i] - m) : l[i] == m ? 1.0f : 0.0f;
           sum += ex;
           if (scored && l[i] > -INFINITY) l[i] = ex;  // -inf stays -inf, off
         }
@@ -667,7 +675,7 @@ __global__ void __launch_bounds__(256) route_any_kernel(const __grid_constant__ 
   if (SCORE == 0 && (scored || !a.renorm)) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      key[i] = expf(l[i] - m);
+      key[i] = expf(below(l[i], m));
       if (lane + 32 * i < a.E) sum += key[i];
     }
     sum = warp_sum(sum);
@@ -722,13 +730,13 @@ __device__ __forceinline__ float chosen_grad(const RouteArgs& a, bool on, float 
   if (a.renorm) {
     const float ls = on ? (SCORE == 0 ? mine : log_sigmoid(mine)) : -INFINITY;
     const float mx = warp_max<N>(ls);
-    const float ex = on ? expf(ls - mx) : 0.0f;
+    const float ex = on ? expf(below(ls, mx)) : 0.0f;
     const float q = ex / warp_sum<N>(ex);
     const float mean = warp_sum<N>(on ? q * dw : 0.0f);
     if (on) g = a.scale * q * (dw - mean);
     if (SCORE == 1 && on) g *= sigmoid_f(-mine);
   } else if (SCORE == 0) {
-    const float p = on ? expf(mine - m) * inv : 0.0f;
+    const float p = on ? expf(below(mine, m)) * inv : 0.0f;
     inner = a.scale * warp_sum<N>(on ? p * dw : 0.0f);
     if (on) g = a.scale * dw * p;
   } else if (on) {
@@ -824,7 +832,7 @@ __global__ void __launch_bounds__(256) route_grad_rows_kernel(const __grid_const
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < C * W; ++i) {
-    l[i] = expf(l[i] - m);
+    l[i] = expf(below(l[i], m));
     sum += l[i];
   }
   sum = warp_sum(sum);
@@ -851,7 +859,7 @@ __global__ void __launch_bounds__(256) route_grad_rows_kernel(const __grid_const
   }
   const bool first = first_of_equals<32>(lane, on ? id : -1 - lane, g);
   __syncwarp();  // the row is written
-  if (on && first) store_logit(out + id, g + common * expf(mine - m));
+  if (on && first) store_logit(out + id, g + common * expf(below(mine, m)));
 }
 
 // Any count of experts.
@@ -876,7 +884,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < a.E) sum += expf(l[i] - m);
+      if (lane + 32 * i < a.E) sum += expf(below(l[i], m));
     inv = 1.0f / warp_sum(sum);
   }
   float inner;
@@ -885,7 +893,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     d[i] = 0.0f;
-    if (SCORE == 0 && !a.renorm && l[i] != -INFINITY) d[i] = -inner * expf(l[i] - m) * inv;
+    if (SCORE == 0 && !a.renorm && l[i] != -INFINITY) d[i] = -inner * expf(below(l[i], m)) * inv;
   }
   for (int j = 0; j < a.k; ++j) {
     const int e = __shfl_sync(kFull, on ? id : -1, j);
