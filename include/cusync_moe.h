@@ -62,7 +62,8 @@ typedef struct {
   int32_t renorm;      /* weights divided by the sum of the chosen scores */
   float scale;         /* factor on the weights (finite) */
   int32_t logits_f32;  /* logits and their gradient: 1 = fp32, 0 = bf16 */
-  int32_t num_sms;     /* thread blocks of the persistent kernels; 0 = one per SM */
+  int32_t num_sms;     /* SMs that the grids of persistent kernels (the products, the router, the
+                          MLP of few tokens) are made for; 0 = all */
   int32_t _pad0;
 } cusync_moe_desc_t;
 

@@ -1,5 +1,7 @@
 """GPU parity of the mixture-of-experts operators with the fp64 oracle (oracle/moe.py)."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -600,3 +602,43 @@ def test_route_with_logits_of_infinity(c, f32):
     size = scale * np.abs(dw).max(axis=1, keepdims=True)
     half = 0.0 if f32 else ref.BF16
     assert np.all(np.abs(f64(dl) - want) <= 2 * ROUTE_TOL * size + half * np.abs(want))
+
+
+def _grids(step):
+    """The grid sizes of the kernels that step() launches."""
+    class Params(ctypes.Structure):  # CUDA_KERNEL_NODE_PARAMS
+        _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                    ("smem", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                    ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+    cuda = ctypes.CDLL("libcuda.so.1")
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        step()
+    raw, n = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(0)
+    assert cuda.cuGraphGetNodes(raw, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cuda.cuGraphGetNodes(raw, nodes, ctypes.byref(n)) == 0
+    out = []
+    for node in nodes:
+        p = Params()
+        assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        out.append(p.grid[0] * p.grid[1] * p.grid[2])
+    return out
+
+
+def test_routes_on_few_sms():
+    """num_sms bounds the router's persistent kernel too; it chooses the same."""
+    T, E, k = 9000, 256, 8
+    logits = torch.randn(T, E, device="cuda")
+    found = {}
+    for sms in (0, 3, 1):
+        m = cs.Moe(cs.make_moe_desc(T=T, experts=E, top_k=k, score="sigmoid", num_sms=sms))
+        ids, w = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+        m.route(logits, None, ids, w)
+        found[sms] = ids, w, _grids(lambda: m.route(logits, None, ids, w))
+    most = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = found[0][2][0] // most  # of the persistent kernel on an SM
+    assert blocks >= 1
+    for sms in (3, 1):
+        assert found[sms][2] == [sms * blocks]
+        assert torch.equal(found[sms][0], found[0][0]) and torch.equal(found[sms][1], found[0][1])

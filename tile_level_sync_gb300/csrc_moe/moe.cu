@@ -290,6 +290,7 @@ cusync_status_t route_any(const cusync_moe_desc_t* d, const Layer& L, RouteArgs 
   int sms = 0;
   const cusync_status_t st = prepare_device(&sms);
   if (st != CUSYNC_OK) return st;
+  if (d->num_sms) sms = std::min(sms, d->num_sms);
   const bool soft = d->score == CUSYNC_MOE_SOFTMAX;
   const cudaError_t e = d->logits_f32 ? route_f32(a, soft, GRAD, sms, s) : route_bf16(a, soft, GRAD, sms, s);
   return e == cudaSuccess ? CUSYNC_OK : CUSYNC_ERR_CUDA;
