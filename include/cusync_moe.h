@@ -12,7 +12,9 @@
  *    dimension contiguous ("[out, in]"), as in cusync.h.
  *  - Calls enqueue kernels on the caller's stream, on the current device, and return; they
  *    allocate nothing, keep nothing between calls and can be recorded by stream capture (a
- *    device's first call prepares its kernels: make it before a capture).
+ *    device's first call sets the attributes that kernels need: make it before a capture; which
+ *    call it is does not matter, the driver loads other kernels at their first launch, also in
+ *    a capture).
  *    A `plan` or `work` buffer belongs to one call at a time: two calls (or two captured
  *    graphs) that may run at the same time need buffers of their own.
  *  - Results do not depend on timing: the same inputs give the same bytes.

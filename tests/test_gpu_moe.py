@@ -1,6 +1,9 @@
 """GPU parity of the mixture-of-experts operators with the fp64 oracle (oracle/moe.py)."""
 
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +14,7 @@ from oracle import moe as ref
 from moe_helpers import assert_within, f64, layer, mlp_inputs, run_mlp, run_mlp_grad
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ------------------------------------------------------------------ plan
@@ -642,3 +646,40 @@ def test_routes_on_few_sms():
     for sms in (3, 1):
         assert found[sms][2] == [sms * blocks]
         assert torch.equal(found[sms][0], found[0][0]) and torch.equal(found[sms][1], found[0][1])
+
+
+def test_a_first_call_of_any_kind_is_enough_before_a_capture():
+    """In a process of its own: one plan, then every other call for the first time inside a capture."""
+    code = """
+import torch, tile_level_sync_gb300 as cs
+T, E, k, D, N1 = 300, 8, 2, 128, 64
+bf = torch.bfloat16
+def new(*s, dt=bf): return torch.randn(s, device="cuda").to(dt)
+first = True
+for f32 in (True, False):
+    m = cs.Moe(cs.make_moe_desc(T=T, D=D, N1=N1, experts=E, top_k=k, logits_f32=f32))
+    X, dY, W1, W2 = new(T, D), new(T, D), new(E, 2 * N1, D), new(E, D, N1)
+    lo = new(T, E, dt=torch.float32 if f32 else bf)
+    ids, w = torch.zeros(T, k, dtype=torch.int32, device="cuda"), torch.ones(T, k, device="cuda")
+    work = torch.empty(max(m.info.work_bytes, m.info.grad_work_bytes), dtype=torch.uint8, device="cuda")
+    plan = torch.empty(m.info.plan_bytes // 4, dtype=torch.int32, device="cuda")
+    out = [torch.empty_like(t) for t in (X, X, W1, W2, w, lo)]
+    if first: m.plan(ids, plan)
+    first = False
+    def step():
+        m.run(X, lo, None, W1, W2, ids, w, work, out[0])
+        m.run_grad(X, lo, W1, W2, ids, w, dY, work, *out[1:])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    g.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in [ids, w] + out]
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, [ids, w] + out))
+print("same bytes")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "same bytes" in r.stdout, r.stdout + r.stderr

@@ -163,8 +163,9 @@ cudaError_t prepare_pair() {
   return e;
 }
 
-// The current device: its kernels' attributes set, the descriptor encoder found.  The first
-// call on a device does the work.
+// The current device: the attributes set of the kernels that need some, the descriptor encoder
+// found.  The first call on a device does the work.  The kernels without attributes (router,
+// copies, sums, few tokens) are loaded by their first launch.
 cusync_status_t prepare_device(int* sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return CUSYNC_ERR_CUDA;
