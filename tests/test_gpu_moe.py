@@ -683,3 +683,18 @@ print("same bytes")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0 and "same bytes" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_no_tokens_leave_no_error(grad):
+    """A call without tokens clears the error word of its buffer as any other does."""
+    m = cs.Moe(cs.make_moe_desc(T=0, D=64, N1=64, experts=3, top_k=2))
+    work = torch.full((max(m.info.work_bytes, m.info.grad_work_bytes),), 0xFF, dtype=torch.uint8, device="cuda")
+    W1t, W2t = torch.empty(3, 128, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 64, 64, dtype=torch.bfloat16, device="cuda")
+    none = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    ids, w = torch.empty(0, 2, dtype=torch.int32, device="cuda"), torch.empty(0, 2, device="cuda")
+    if grad:
+        m.mlp_grad(none, W1t, W2t, ids, w, none, work, none, torch.empty_like(W1t), torch.empty_like(W2t), w)
+    else:
+        m.mlp(none, W1t, W2t, ids, w, work, none)
+    assert m.check(work) == (cs.OK, 0)

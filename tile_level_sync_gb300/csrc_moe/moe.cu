@@ -403,6 +403,11 @@ cudaError_t launch_combine(const Layer& L, void* work, const void* rows, const v
 
 cusync_status_t status_of(cudaError_t e) { return e == cudaSuccess ? CUSYNC_OK : CUSYNC_ERR_CUDA; }
 
+// The error word of a buffer that no kernel of the call touches (no token; work may be null).
+cudaError_t clear_error(void* work, cudaStream_t s) {
+  return aligned(work) ? cudaMemsetAsync(static_cast<int32_t*>(work) + PLAN_ERR, 0, 4, s) : cudaSuccess;
+}
+
 }  // namespace
 
 extern "C" {
@@ -470,7 +475,7 @@ cusync_status_t cusync_moe_mlp(const cusync_moe_desc_t* d, const void* X, const 
   Layer L;
   cusync_status_t st = read_desc(d, &L, true);
   if (st != CUSYNC_OK) return st;
-  if (L.T == 0) return CUSYNC_OK;
+  if (L.T == 0) return status_of(clear_error(work, (cudaStream_t)stream));
   if (!aligned(X) || !aligned(W1t) || !aligned(W2t) || !aligned(ids) || !aligned(weights) || !aligned(work) ||
       !aligned(Y))
     return CUSYNC_ERR_INVALID_ARG;
@@ -547,6 +552,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
   if (L.T == 0) {  // no token: every weight gradient is zero
     cudaError_t e = cudaMemsetAsync(dW1t, 0, (size_t)L.E * L.G * L.N1 * L.D * 2, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(dW2t, 0, (size_t)L.E * L.N1 * L.D * 2, s);
+    if (e == cudaSuccess) e = clear_error(work, s);
     return status_of(e);
   }
   if (!aligned(X) || !aligned(W1t) || !aligned(W2t) || !aligned(ids) || !aligned(weights) || !aligned(dY) ||
