@@ -127,7 +127,7 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
 
 /* Synchronise `stream` and read the error word of the last call that used `buffer` (a plan
  * or work buffer): OK, or DEVICE if a device-internal wait gave up (the outputs of that
- * call are not valid).  code may be NULL. */
+ * call are not valid).  code may be NULL.  UNSUPPORTED while the stream is being captured. */
 cusync_status_t cusync_moe_check(const void* buffer, cusync_stream_t stream, uint32_t* code);
 
 #ifdef __cplusplus

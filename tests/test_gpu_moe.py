@@ -698,3 +698,20 @@ def test_no_tokens_leave_no_error(grad):
     else:
         m.mlp(none, W1t, W2t, ids, w, work, none)
     assert m.check(work) == (cs.OK, 0)
+
+
+def test_check_is_refused_in_a_capture():
+    """It waits for the stream: a refusal leaves the capture as it was."""
+    s = mlp_inputs(60, 3, 2, 64, 64, "swiglu", seed=2)
+    d = {n: v.cuda() for n, v in s.items()}
+    m = layer(s, "swiglu")
+    want = run_mlp(m, s)
+    work, Y = torch.empty(m.info.work_bytes, dtype=torch.uint8, device="cuda"), torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.mlp(d["X"], d["W1t"], d["W2t"], d["ids"], d["weights"], work, Y)
+        with pytest.raises(cs.CusyncError) as e:
+            m.check(work)
+    assert e.value.status == cs.ERR_UNSUPPORTED
+    graph.replay()
+    assert m.check(work) == (cs.OK, 0) and torch.equal(Y, want)

@@ -611,8 +611,13 @@ cusync_status_t cusync_moe_mlp_grad(const cusync_moe_desc_t* d, const void* X, c
 
 cusync_status_t cusync_moe_check(const void* buffer, cusync_stream_t stream, uint32_t* code) {
   if (!aligned(buffer)) return CUSYNC_ERR_INVALID_ARG;
+  // a wait inside a capture would end the capture
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &capture);
+  if (e == cudaErrorStreamCaptureImplicit || (e == cudaSuccess && capture != cudaStreamCaptureStatusNone))
+    return CUSYNC_ERR_UNSUPPORTED;
   uint32_t err = 0;
-  cudaError_t e = cudaMemcpyAsync(&err, buffer, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&err, buffer, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
   if (code) *code = err;
