@@ -715,3 +715,19 @@ def test_check_is_refused_in_a_capture():
     assert e.value.status == cs.ERR_UNSUPPORTED
     graph.replay()
     assert m.check(work) == (cs.OK, 0) and torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("T", [40, 600])
+def test_gelu_gradient_far_out(T):
+    """Pre-activations whose squares 32 bits do not hold: the slope there is 0 or 1."""
+    s = mlp_inputs(T, 2, 1, 64, 64, "gelu", seed=41)
+    s["X"][3] *= 2.0 ** 70
+    out = run_mlp_grad(layer(s, "gelu"), s)
+    assert all(bool(t.isfinite().all()) for t in out.values())
+    e = int(s["ids"][3, 0])
+    x, y, a, b = f64(s["X"][3]), f64(s["dY"][3]), f64(s["W1t"][e]), f64(s["W2t"][e])
+    z, w = a @ x, float(s["weights"][3, 0])
+    dz = np.where(z > 0, w * (y @ b), 0.0)
+    # dZ and dX rounded to bf16, dX to fp16 between (half a step of its largest neighbour), sums of 64
+    bound = 2 * ref.BF16 * (np.abs(dz) @ np.abs(a)) + ref.HALF * np.abs(dz @ a).max() + ref.BF16 * np.abs(dz @ a)
+    assert np.all(np.abs(f64(out["dX"][3]) - dz @ a) <= bound)

@@ -774,7 +774,9 @@ __global__ void __launch_bounds__(GemmCfg<MODE, ACT, PAIR>::kThreads, 1) moe_gem
             } else {
               const float sg = sigmoid_full(gelu_arg(zz));
               h = zz * sg;
-              vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * zz * zz));
+              // far out, where the sigmoid is 0 or 1, the square must not become an infinity
+              const float z2 = fminf(zz * zz, 1e30f);
+              vz = dhw * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * z2));
             }
             dots[i] = in ? dh * h : 0.0f;
             // two tokens to a register
