@@ -731,3 +731,82 @@ def test_gelu_gradient_far_out(T):
     # dZ and dX rounded to bf16, dX to fp16 between (half a step of its largest neighbour), sums of 64
     bound = 2 * ref.BF16 * (np.abs(dz) @ np.abs(a)) + ref.HALF * np.abs(dz @ a).max() + ref.BF16 * np.abs(dz @ a)
     assert np.all(np.abs(f64(out["dX"][3]) - dz @ a) <= bound)
+
+
+# ------------------------------------------------------------------ long sums, borders, captures
+
+@pytest.mark.parametrize("c", [dict(T=300, E=2, k=1, D=2056, N1=64), dict(T=70, E=4, k=2, D=1600, N1=840),
+                               dict(T=400, E=3, k=2, D=1536, N1=1536)], ids=_name)
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("grad", [False, True])
+def test_long_sums(c, act, grad):
+    """Widths from which tiles are claimed only one ahead, in every product."""
+    _check_mlp(mlp_inputs(act=act, seed=51, **c), act, grad)
+
+
+@pytest.mark.parametrize("act", ["swiglu", "gelu"])
+@pytest.mark.parametrize("T,E,k", [(4, 16, 8), (32, 3, 1), (16, 2, 2), (20, 40, 8), (16, 1, 1), (48, 3, 1), (127, 1, 1), (128, 1, 1)])
+def test_one_token_more(T, E, k, act):
+    """The same tokens on both sides of a border between kernels (32 assignments; 16 and 128 an
+    expert): each within its bound, and so at most two bounds apart."""
+    s = mlp_inputs(T + 1, E, k, 264, 136, act, seed=52)
+    host = {n: f64(v) for n, v in s.items()}
+    y, bound = ref.mlp(host["X"], host["W1t"], host["W2t"], s["ids"].numpy(), host["weights"], act)
+    more = run_mlp(layer(s, act), s)
+    assert_within(more, y, bound, "one token more")
+    for n in ("X", "ids", "weights"):
+        s[n] = s[n][:T].contiguous()
+    assert_within(run_mlp(layer(s, act), s), y[:T], bound[:T], "without it")
+
+
+@pytest.mark.parametrize("T", [3, 60, 700])
+def test_captured_behind_other_work(T):
+    """Calls captured behind a memset, a copy and another stream's kernels, which write what they read."""
+    s = mlp_inputs(T, 4, 2, 128, 64, "swiglu", seed=53)
+    d = {n: v.cuda() for n, v in s.items()}
+    m = layer(s, "swiglu")
+    want, grads = run_mlp(m, s), run_mlp_grad(m, s)
+    X, dY, ids, w = (torch.full_like(d[n], 0) for n in ("X", "dY", "ids", "weights"))
+    work = torch.empty(max(m.info.work_bytes, m.info.grad_work_bytes), dtype=torch.uint8, device="cuda")
+    Y, out = torch.empty_like(X), {n: torch.empty_like(grads[n]) for n in ("dX", "dW1t", "dW2t", "dweights")}
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            X.copy_(d["X"])
+            w.copy_(d["weights"] * 1.0)
+        ids.copy_(d["ids"])
+        work.zero_()
+        torch.cuda.current_stream().wait_stream(side)
+        m.mlp(X, d["W1t"], d["W2t"], ids, w, work, Y)
+        dY.copy_(d["dY"])
+        m.mlp_grad(X, d["W1t"], d["W2t"], ids, w, dY, work, *out.values())
+        X.zero_()
+
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for t in [X, dY, w, Y, *out.values()]:
+            t.fill_(float("nan"))
+        ids.fill_(-1)
+        work.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want) and all(torch.equal(out[n], grads[n]) for n in out)
+
+
+def test_gradient_offsets_beyond_32_bits():
+    """Over 2^31 elements of rows by slot; the last tokens' gradients against the oracle."""
+    T, E, k, D, N1 = 140000, 8, 8, 2048, 64
+    ids = torch.arange(T * k, dtype=torch.int32).view(T, k) % E
+    s = mlp_inputs(T, E, k, D, N1, "gelu", seed=3, ids=ids)
+    m = layer(s, "gelu")
+    assert m.info.slots * D > 2 ** 31
+    out = run_mlp_grad(m, s)
+    last = slice(T - 40, T)
+    host = {n: f64(s[n][last] if n in ("X", "weights", "dY") else s[n]) for n in ("X", "W1t", "W2t", "weights", "dY")}
+    want = ref.mlp_grad(host["X"], host["W1t"], host["W2t"], ids[last].numpy(), host["weights"], host["dY"], "gelu")
+    for name in ("dX", "dweights"):
+        assert_within(out[name][last], *want[name], name)
+    assert all(bool(out[n].isfinite().all()) for n in ("dX", "dW1t", "dW2t", "dweights"))
