@@ -56,7 +56,7 @@
 // zeros up to the step's end.
 //
 // Both weights' gradients are one launch, whose second half fills the first's tail: 12 us less
-// of 378 for 4096 tokens, 9 of 84 in the smallest gradient measured.
+// of 378 for 4096 tokens, 8 of 84 in the gradient of 333 tokens.
 //
 // Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
 #pragma once
@@ -93,7 +93,7 @@ struct GemmArgs {
   void* out;           // H, O or dX per slot
   uint8_t* scale;      // FWD2, DX: exponents of the slots' blocks of 32 columns (scale_at)
   float* part;         // BWD1: sums of dH h over 32 columns of N1, [slot][parts]
-  int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128 or 256 rows
+  int64_t counts, offsets, tiles, row_of;  // plan words; tiles: of the launch's 128, 160 or 256 rows
   int32_t T, k, E;
   int32_t M;           // output columns (DW: rows of an expert's matrix)
   int32_t N;           // DW: output columns
