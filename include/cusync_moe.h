@@ -12,12 +12,13 @@
  *    dimension contiguous ("[out, in]"), as in cusync.h.
  *  - Calls enqueue kernels on the caller's stream, on the current device, and return; they
  *    allocate nothing, keep nothing between calls and can be recorded by stream capture (a
- *    device's first call sets the attributes that kernels need: make it before a capture; which
- *    call it is does not matter, the driver loads other kernels at their first launch, also in
- *    a capture).
+ *    device's first call with tokens sets the attributes that kernels need: make it before a
+ *    capture; which call it is does not matter, CUDA loads other kernels at their first launch,
+ *    also in a capture).
  *    A `plan` or `work` buffer belongs to one call at a time: two calls (or two captured
  *    graphs) that may run at the same time need buffers of their own.
- *  - Results do not depend on timing: the same inputs give the same bytes.
+ *  - Results do not depend on timing: the same inputs give the same bytes.  Calls of different
+ *    sizes may take different kernels, whose results differ by roundings.
  *  - An id outside [0, experts) is an assignment to no expert: it adds nothing, and its
  *    gradient is zero.  The same expert may be chosen twice by a token; both count.
  *  - Sizes the kernels do not cover return CUSYNC_ERR_UNSUPPORTED; there is no fallback.
