@@ -1,5 +1,5 @@
 """Python binding of the tile-level synchronisation library (include/cusync.h,
-include/cusync_moe.h).
+include/cusync_moe.h, include/cusync_linear.h).
 
 Argument marshalling only: every function forwards to the C ABI function of the same
 name in the in-tree ``libcusync.so``; all computation runs in the library's CUDA
@@ -32,6 +32,12 @@ NOALLOC_MAX_SEMAPHORES = 16336
 MOE_SOFTMAX, MOE_SIGMOID = range(2)
 MOE_GELU, MOE_SWIGLU = range(2)
 MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_MAX_GROUPS, MOE_MAX_ASSIGNMENTS, MOE_TILE_ROWS = 1024, 32, 32, 16777216, 128
+# cusync_linear.h
+NORM_RMS, NORM_NONE = range(2)
+NORM_MAX_D = 32768
+LINEAR_NONE, LINEAR_RELU, LINEAR_GELU, LINEAR_SWIGLU = range(4)
+LINEAR_BF16, LINEAR_E4M3 = range(2)
+LINEAR_BLOCK = 32
 
 POLICY_NAMES = {"STREAM": POLICY_STREAM, "ROW": POLICY_ROW, "TILE": POLICY_TILE,
                 "STRIDED": POLICY_STRIDED_TILE, "SENTINEL": POLICY_SENTINEL, "AUTO": POLICY_AUTO}
@@ -99,7 +105,26 @@ class cusync_moe_info_t(ctypes.Structure):
                 ("counts", c_i64), ("offsets", c_i64), ("slot_of", c_i64), ("row_of", c_i64)]
 
 
+class cusync_norm_desc_t(ctypes.Structure):
+    _fields_ = [("M", c_i64), ("D", c_i64), ("kind", c_i32), ("eps", ctypes.c_float), ("num_sms", c_i32),
+                ("_pad0", c_i32)]
+
+
+class cusync_norm_info_t(ctypes.Structure):
+    _fields_ = [("grad_work_bytes", c_i64)]
+
+
+class cusync_linear_desc_t(ctypes.Structure):
+    _fields_ = [("M", c_i64), ("K", c_i64), ("N", c_i64), ("act", c_i32), ("dtype", c_i32), ("num_sms", c_i32),
+                ("_pad0", c_i32)]
+
+
+class cusync_linear_info_t(ctypes.Structure):
+    _fields_ = [("work_bytes", c_i64), ("grad_work_bytes", c_i64), ("parts", c_i64), ("blocks", c_i64)]
+
+
 _VP = ctypes.c_void_p
+_NORM, _LINEAR = ctypes.POINTER(cusync_norm_desc_t), ctypes.POINTER(cusync_linear_desc_t)
 _MOE = ctypes.POINTER(cusync_moe_desc_t)
 _SIGNATURES = {
     "cusync_status_string": (ctypes.c_char_p, [c_i32]),
@@ -142,6 +167,13 @@ _SIGNATURES = {
     "cusync_moe_mlp": (c_i32, [_MOE] + [_VP] * 8),
     "cusync_moe_mlp_grad": (c_i32, [_MOE] + [_VP] * 12),
     "cusync_moe_check": (c_i32, [_VP, _VP, ctypes.POINTER(c_u32)]),
+    "cusync_norm_info": (c_i32, [_NORM, ctypes.POINTER(cusync_norm_info_t)]),
+    "cusync_norm": (c_i32, [_NORM] + [_VP] * 8),
+    "cusync_norm_grad": (c_i32, [_NORM] + [_VP] * 8),
+    "cusync_linear_info": (c_i32, [_LINEAR, ctypes.POINTER(cusync_linear_info_t)]),
+    "cusync_linear": (c_i32, [_LINEAR] + [_VP] * 11),
+    "cusync_linear_grad": (c_i32, [_LINEAR] + [_VP] * 11),
+    "cusync_linear_check": (c_i32, [_VP, _VP, ctypes.POINTER(c_u32)]),
 }
 
 _lib = None
@@ -433,6 +465,38 @@ class Chain:
             pass
 
 
+# ---------------------------------------------------------------- layers
+
+
+def _checked(want, tensors):
+    """Device addresses of the named arguments, the tensors among them checked against
+    ``want``: name -> (type, elements), or (None, bytes) for a buffer."""
+    out, device = [], None
+    for name, t in tensors.items():
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        dtype, n = want[name]
+        if dtype is None:
+            if t.numel() * t.element_size() < n:
+                raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes: {n} are needed")
+        elif t.dtype is not dtype:
+            raise ValueError(f"{name} is {t.dtype}: {dtype} is needed")
+        elif t.numel() != n:
+            raise ValueError(f"{name} has {t.numel()} elements: {n} are needed")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+        if not t.is_cuda:
+            raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
+        out.append(t.data_ptr())
+    return out
+
+
 # ---------------------------------------------------------------- mixture of experts
 
 
@@ -482,33 +546,9 @@ class Moe:
             "plan": (None, self.info.plan_bytes), "work": (None, self.info.work_bytes),
             "grad_work": (None, self.info.grad_work_bytes),
         }
-        self._device = torch.cuda.current_device
 
     def _ptrs(self, **tensors):
-        """Device addresses of the named arguments, the tensors among them checked."""
-        out, device = [], None
-        for name, t in tensors.items():
-            if t is None or isinstance(t, int):
-                out.append(t)
-                continue
-            dtype, n = self._want[name]
-            if dtype is None:
-                if t.numel() * t.element_size() < n:
-                    raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes: {n} are needed")
-            elif t.dtype is not dtype:
-                raise ValueError(f"{name} is {t.dtype}: {dtype} is needed")
-            elif t.numel() != n:
-                raise ValueError(f"{name} has {t.numel()} elements: {n} are needed")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} is not contiguous")
-            if not t.is_cuda:
-                raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
-            if device is None:
-                device = self._device()
-            if t.get_device() != device:
-                raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
-            out.append(t.data_ptr())
-        return out
+        return _checked(self._want, tensors)
 
     def route(self, logits, bias, ids, weights, stream=None):
         p = self._ptrs(logits=logits, bias=bias, ids=ids, weights=weights)
@@ -555,4 +595,107 @@ class Moe:
         st = self._lib.cusync_moe_check(_ptr(buffer), _stream(stream), ctypes.byref(code))
         if st not in (OK, ERR_DEVICE):
             raise CusyncError(st, "cusync_moe_check")
+        return st, code.value
+
+
+# ---------------------------------------------------------------- norm and linear layers
+
+
+def make_norm_desc(M=0, D=0, kind=NORM_RMS, eps=1e-6, num_sms=0):
+    """Descriptor of a norm (cusync_norm_desc_t); kind also by name: "rms", "none"."""
+    if isinstance(kind, str):
+        kind = {"rms": NORM_RMS, "none": NORM_NONE}[kind.lower()]
+    return cusync_norm_desc_t(M=M, D=D, kind=kind, eps=eps, num_sms=num_sms)
+
+
+def cusync_norm_info(desc):
+    r = cusync_norm_info_t()
+    _check(load().cusync_norm_info(ctypes.byref(desc), ctypes.byref(r)), "cusync_norm_info")
+    return r
+
+
+def make_linear_desc(M=0, K=0, N=0, act=LINEAR_NONE, dtype=LINEAR_BF16, num_sms=0):
+    """Descriptor of a linear layer (cusync_linear_desc_t); act and dtype also by name: "none" /
+    "relu" / "gelu" / "swiglu", "bf16" / "e4m3"."""
+    if isinstance(act, str):
+        act = {"none": LINEAR_NONE, "relu": LINEAR_RELU, "gelu": LINEAR_GELU, "swiglu": LINEAR_SWIGLU}[act.lower()]
+    if isinstance(dtype, str):
+        dtype = {"bf16": LINEAR_BF16, "e4m3": LINEAR_E4M3}[dtype.lower()]
+    return cusync_linear_desc_t(M=M, K=K, N=N, act=act, dtype=dtype, num_sms=num_sms)
+
+
+def cusync_linear_info(desc):
+    r = cusync_linear_info_t()
+    _check(load().cusync_linear_info(ctypes.byref(desc), ctypes.byref(r)), "cusync_linear_info")
+    return r
+
+
+class Norm:
+    """A norm of one descriptor: its calls, on tensors and buffers of the caller.
+
+    Torch tensors are checked as Moe's are.  8-bit rows are a float8_e4m3fn tensor [M, D]
+    and float32 scales [M]; ``run_grad`` takes a buffer of ``info.grad_work_bytes``."""
+
+    def __init__(self, desc):
+        self.desc = desc
+        self.info = cusync_norm_info(desc)
+        self._d = ctypes.byref(desc)
+        self._lib = load()
+        import torch
+        bf16, n = torch.bfloat16, desc.M * desc.D
+        self._want = {k: (bf16, n) for k in ("X", "R", "S", "Y", "dY", "dS", "dX")}
+        self._want.update(w=(bf16, desc.D), dw=(bf16, desc.D), Q=(torch.float8_e4m3fn, n), Qs=(torch.float32, desc.M),
+                          work=(None, self.info.grad_work_bytes))
+
+    def run(self, X, R=None, w=None, S=None, Y=None, Q=None, Qs=None, stream=None):
+        """S = X + R, and its norm in bf16 (Y), as 8-bit rows (Q, Qs), or both."""
+        p = _checked(self._want, dict(X=X, R=R, w=w, S=S, Y=Y, Q=Q, Qs=Qs))
+        _check(self._lib.cusync_norm(self._d, *p, _stream(stream)), "cusync_norm")
+
+    def run_grad(self, S, w, dY, dS, work, dX, dw, stream=None):
+        p = _checked(self._want, dict(S=S, w=w, dY=dY, dS=dS, work=work, dX=dX, dw=dw))
+        _check(self._lib.cusync_norm_grad(self._d, *p, _stream(stream)), "cusync_norm_grad")
+
+
+class Linear:
+    """A linear layer of one descriptor: its calls, on tensors and buffers of the caller.
+
+    Torch tensors are checked as Moe's are.  8-bit rows are float8_e4m3fn with float32
+    scales, a checkpoint is Zq float8_e4m3fn [M, parts * N] and Ze uint8 [M, parts, info.blocks].
+    ``run`` takes a buffer of ``info.work_bytes``, ``run_grad`` one of ``info.grad_work_bytes``."""
+
+    def __init__(self, desc):
+        self.desc = desc
+        self.info = cusync_linear_info(desc)
+        self._d = ctypes.byref(desc)
+        self._lib = load()
+        import torch
+        bf16, f8, f32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32
+        M, K, N, H = desc.M, desc.K, desc.N, self.info.parts * desc.N
+        wide = f8 if desc.dtype == LINEAR_E4M3 else bf16
+        self._want = {
+            "X": (wide, M * K), "Xs": (f32, M), "Wt": (wide, H * K), "Ws": (f32, H), "bias": (bf16, H),
+            "R": (bf16, M * N), "Y": (bf16, M * N), "Zq": (f8, M * H), "Ze": (torch.uint8, M * self.info.parts * self.info.blocks),
+            "work": (None, self.info.work_bytes),
+        }
+        self._want_grad = dict(self._want, Wt=(bf16, H * K), dY=(bf16, M * N), dX=(bf16, M * K), dWt=(bf16, H * K),
+                               dbias=(bf16, H), work=(None, self.info.grad_work_bytes))
+
+    def run(self, X, Wt, work, Y, Xs=None, Ws=None, bias=None, R=None, Zq=None, Ze=None, stream=None):
+        """Y = act(X x W + bias) + R; Zq and Ze: the checkpoint that run_grad reads."""
+        p = _checked(self._want, dict(X=X, Xs=Xs, Wt=Wt, Ws=Ws, bias=bias, R=R, work=work, Y=Y, Zq=Zq, Ze=Ze))
+        _check(self._lib.cusync_linear(self._d, *p, _stream(stream)), "cusync_linear")
+
+    def run_grad(self, X, Wt, dY, work, dX, dWt, dbias=None, Xs=None, Zq=None, Ze=None, stream=None):
+        """The gradients that are not None, from dY, the checkpoint and X."""
+        p = _checked(self._want_grad, dict(X=X, Xs=Xs, Wt=Wt, Zq=Zq, Ze=Ze, dY=dY, work=work, dX=dX, dWt=dWt,
+                                           dbias=dbias))
+        _check(self._lib.cusync_linear_grad(self._d, *p, _stream(stream)), "cusync_linear_grad")
+
+    def check(self, buffer, stream=None):
+        """(status, code) of the last call that used a work buffer: OK or ERR_DEVICE."""
+        code = c_u32()
+        st = self._lib.cusync_linear_check(_ptr(buffer), _stream(stream), ctypes.byref(code))
+        if st not in (OK, ERR_DEVICE):
+            raise CusyncError(st, "cusync_linear_check")
         return st, code.value

@@ -13,15 +13,17 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")          # the chains
 CSRC_MOE = os.path.join(PKG, "csrc_moe")  # the expert layer
+CSRC_LINEAR = os.path.join(PKG, "csrc_linear")  # the norm and the linear layer
 INCLUDE = os.path.join(ROOT, "include")
 OBJECTS = os.path.join(PKG, "build")
 LIB_PATH = os.path.join(PKG, "libcusync.so")
 
 SOURCES = [os.path.join(CSRC, "cusync.cu")] + [
-    os.path.join(CSRC_MOE, f) for f in ("moe.cu", "moe_route_f32.cu", "moe_route_bf16.cu")]
+    os.path.join(CSRC_MOE, f) for f in ("moe.cu", "moe_route_f32.cu", "moe_route_bf16.cu")] + [
+    os.path.join(CSRC_LINEAR, f) for f in ("linear.cu", "norm.cu")]
 DEPS = SOURCES + [
-    os.path.join(d, f) for d in (CSRC, CSRC_MOE) for f in sorted(os.listdir(d)) if f.endswith((".h", ".cuh"))
-] + [os.path.join(INCLUDE, f) for f in ("cusync.h", "cusync_moe.h")]
+    os.path.join(d, f) for d in (CSRC, CSRC_MOE, CSRC_LINEAR) for f in sorted(os.listdir(d)) if f.endswith((".h", ".cuh"))
+] + [os.path.join(INCLUDE, f) for f in ("cusync.h", "cusync_moe.h", "cusync_linear.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

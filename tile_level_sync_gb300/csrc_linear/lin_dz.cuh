@@ -1,0 +1,120 @@
+// What a linear layer's backward pass does besides its products: the gradient at the
+// pre-activations, the bias's, and 8-bit rows as bf16.  Bound by memory, as the norm.
+#pragma once
+#include "lin_math.cuh"
+
+namespace cusync {
+namespace lin {
+
+struct DzArgs {
+  const uint16_t* dY;
+  const uint8_t *Zq, *Ze;
+  uint16_t* dZ;   // [M, parts * N], or NULL (act NONE)
+  float* part;    // [gridDim.y][parts * N] sums of dZ over a block's rows, or NULL
+  int32_t* err;   // the call's error word, cleared by the call's first kernel
+  int64_t M;
+  int32_t N, rows;  // rows of a block
+};
+
+constexpr int kDzCols = 256;
+
+// dZ = act'(z) dY from the checkpoint, and the sums over rows that dbias is made of (before
+// dZ's rounding).  A lane takes 8 columns, a warp every eighth row of the block's.
+template <int ACT>
+__global__ void __launch_bounds__(256) dz_kernel(const DzArgs a) {
+  constexpr int G = ACT == ACT_SWIGLU ? 2 : 1;
+  __shared__ float sums[8][kDzCols + 8];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x * kDzCols + lane * 8;
+  const int blocks = (a.N + kBlock - 1) / kBlock;
+  const int64_t r0 = (int64_t)blockIdx.y * a.rows, end = min(r0 + a.rows, a.M);
+  float acc[G][8];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[g][j] = 0.0f;
+  if (c < a.N) {
+#pragma unroll 4
+    for (int64_t r = r0 + warp; r < end; r += 8) {
+      float dy[8], z[G][8];
+      unpack8(*reinterpret_cast<const uint4*>(a.dY + r * a.N + c), dy);
+      if (ACT != ACT_NONE) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint2 q = *reinterpret_cast<const uint2*>(a.Zq + (r * G + g) * a.N + c);
+          const float e = exponent_value(a.Ze[(r * G + g) * blocks + c / kBlock]);
+          unpack_e4m3(q.x, z[g]);
+          unpack_e4m3(q.y, z[g] + 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[g][j] *= e;
+        }
+      }
+      float dz[G][8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (ACT == ACT_NONE) {
+          dz[0][j] = dy[j];
+        } else if (ACT == ACT_RELU) {
+          dz[0][j] = z[0][j] > 0.0f ? dy[j] : 0.0f;
+        } else if (ACT == ACT_GELU) {
+          const float x = z[0][j], sg = gelu_gate(x), h = x * sg;
+          // far out, where the sigmoid is 0 or 1, the square must not become an infinity
+          const float x2 = fminf(x * x, 1e30f);
+          dz[0][j] = dy[j] * (sg + h * (1.0f - sg) * 2.0f * kGeluC * (1.0f + 3.0f * 0.044715f * x2));
+        } else {
+          const float x = z[0][j], u = z[G - 1][j], sg = sigmoid_fast(x), h = x * sg;
+          dz[0][j] = dy[j] * u * (sg + h * (1.0f - sg));
+          dz[G - 1][j] = dy[j] * h;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[g][j] += dz[g][j];
+      }
+      if (ACT != ACT_NONE) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) *reinterpret_cast<uint4*>(a.dZ + (r * G + g) * a.N + c) = pack8(dz[g]);
+      }
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[warp][lane * 8 + j] = acc[g][j];
+    __syncthreads();
+    const int col = blockIdx.x * kDzCols + threadIdx.x;
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
+    if (col < a.N) a.part[((int64_t)blockIdx.y * G + g) * a.N + col] = t;
+  }
+}
+
+// 8-bit rows as bf16: one rounding of scale * q.
+__global__ void __launch_bounds__(256) rows_from_e4m3_kernel(const uint4* q, const float* scales, uint4* out, int64_t M,
+                                                             int32_t vecs /* K / 16 */) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int64_t n = M * vecs, step = (int64_t)gridDim.x * blockDim.x;
+#pragma unroll 2
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
+    const uint4 v = q[i];
+    const float s = scales[i / vecs];
+    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+    float f[2][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack_e4m3(words[k], &f[k / 2][4 * (k % 2)]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[k][j] *= s;
+      out[2 * i + k] = pack8(f[k]);
+    }
+  }
+}
+
+}  // namespace lin
+}  // namespace cusync

@@ -1,0 +1,425 @@
+// The products of a linear layer on CTA pairs: one persistent tcgen05 kernel.
+//
+//   mode   A (M: 256 rows a pair)    B (N: 256 columns a pair)      epilogue
+//   FWD    X rows                    Wt rows; SwiGLU: 128 gate rows  scales, bias, checkpoint, activation,
+//                                    in the first CTA, the 128 up    residual, bf16
+//                                    rows N further in the second
+//   DX     dZ rows                   Wt along K                      bf16
+//   DW     dZ along N (K: tokens)    X along K                       bf16
+//
+// "along": the operand is stored with its M (or N) index contiguous rather than the reduction's,
+// and the MMA reads it that way through its descriptors; nothing is transposed in memory.
+//
+// A stage holds 128 bytes x 2 of the reduction for the CTA's 128 rows of A and of B (64 KB), three
+// stages fit beside the epilogue's staging.  Roles, as in the expert layer's products: warp 0 copies A,
+// the last warp but one copies B (TMA, one box each where the widths are multiples of 128 bytes),
+// lane 0 of the first CTA's warp 1 issues the MMAs (256 x 256 x 32 bytes), the eight epilogue warps read
+// one accumulator of TMEM while the next tile runs into the other.  Tiles are equal, so a
+// pair takes tiles t = pair, pair + pairs, ...: row tiles inner within groups of `group`, so that pairs
+// at work at the same time share operands in the L2.
+//
+// Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
+#pragma once
+#include "lin_math.cuh"
+#include "../csrc_moe/moe_ptx.cuh"
+
+namespace cusync {
+namespace ptx {
+
+// As umma_bf16 and umma_bf16_pair for e4m3 operands (kind::f8f6f4): 32 k an instruction.
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, e4m3 A and B (type fields 0).
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+}  // namespace ptx
+
+namespace lin {
+
+enum : int { FWD = 0, DX = 1, DW = 2 };
+
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr uint32_t kErrWait = 3u << 24;  // the pipeline-wait class of the chain kernel's error words
+
+// What both kernels' epilogues of the forward product apply.
+struct Epilogue {
+  const float *Xs, *Ws;    // E4M3
+  const uint16_t *bias, *R;
+  uint8_t *Zq, *Ze;
+  uint16_t* out;
+  int32_t act;
+};
+
+struct GemmArgs {
+  CUtensorMap mA, mB, mO;
+  Epilogue e;
+  int32_t* err;
+  int32_t clear;            // this kernel is the call's first: it clears the error word
+  int32_t M, N, K;          // output rows, output columns (SwiGLU: of Y), reduction length
+  int32_t m_tiles, n_tiles, group;
+  int32_t wideA, wideB;     // one box brings an operand's whole share of a stage
+};
+
+constexpr int kEpiWarps = 8;
+constexpr int kGemmThreads = (kEpiWarps + 4) * 32;
+constexpr int kOperandBytes = 32 * 1024;  // a CTA's share of A, and of B, in a stage
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kStages = 3;
+constexpr int kWarpOut = 4096;            // two blocks of 32 rows x 32 columns
+constexpr int kGemmSmem = kStages * kStageBytes + kEpiWarps * kWarpOut + 1024;
+
+// 16 bytes of bf16 or fp32 values that all lanes read
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// Scales and bias of 8 columns from c on (of a part that begins at `first` of Wt's rows).
+template <bool E4M3>
+__device__ __forceinline__ void finish8(const Epilogue& e, float xs, int64_t first, int c, float* z) {
+  float f[8];
+  if (E4M3) {
+    load8(e.Ws + first + c, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] *= xs * f[j];
+  }
+  if (e.bias) {
+    load8(e.bias + first + c, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[j] += f[j];
+  }
+}
+
+// 32 columns of a row as a block of the checkpoint, `left` of them inside.
+__device__ __forceinline__ void store_checkpoint(const Epilogue& e, const float (&z)[32], int left, int64_t row, int part,
+                                                 int parts, int N, int c) {
+  float most = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < left) most = fmaxf(most, finite_abs(z[i]));
+  const uint32_t x = block_exponent(most);
+  const float inv = exponent_inverse(x);
+  const int64_t line = row * parts + part;
+  uint2* q = reinterpret_cast<uint2*>(e.Zq + line * N + c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (8 * i >= left) break;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = no_inf(z[8 * i + j]) * inv;
+    q[i] = make_uint2(pack_e4m3(v[0], v[1], v[2], v[3]), pack_e4m3(v[4], v[5], v[6], v[7]));
+  }
+  e.Ze[line * ((N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)x;
+}
+
+template <int MODE, bool E4M3, bool GATED>
+__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
+  constexpr bool kMnA = MODE == DW, kMnB = MODE != FWD;
+  constexpr int kElems = E4M3 ? 128 : 64;        // reduction elements in 128 bytes
+  constexpr int kTileN = GATED ? 128 : 256;      // output columns of a tile
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int32_t abort_flag;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&full[i], 1);
+      ptx::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&tfull[i], 1);
+      ptx::mbar_init(&tempty[i], kEpiWarps + (rank == 0));  // and the second CTA's warp 1
+    }
+    ptx::mbar_init(&drain, 1);
+    ptx::mbar_init_fence();
+    abort_flag = 0;
+    ptx::prefetch_tmap(&a.mA);
+    ptx::prefetch_tmap(&a.mB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&tmem_slot, 512);
+    ptx::tmem_relinquish_pair();
+    ptx::tc_fence_before();
+  }
+  __syncthreads();
+  ptx::cluster_sync();  // the other CTA's barriers exist
+  ptx::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+
+  const int total = a.m_tiles * a.n_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int nkb = (a.K + kElems - 1) / kElems;  // blocks of 128 bytes
+  // tile t: groups of `group` row tiles, columns outer, rows inner
+  auto tile = [&](int t, int& m0, int& n0) {
+    const int per = a.group * a.n_tiles, g = t / per, r = t - g * per;
+    const int rows = min(a.group, a.m_tiles - g * a.group);
+    const int n = r / rows;
+    m0 = (g * a.group + r - n * rows) * 256;
+    n0 = n * kTileN;
+  };
+
+  if (warp == 0 || warp == kEpiWarps + 2) {
+    // ------------------------------------------------------------ copies
+    const bool copies_a = warp == 0;
+    const uint64_t pol = ptx::l2_policy_evict_normal();
+    const bool one = ptx::elect_one();
+    const bool mn = copies_a ? kMnA : kMnB, wide = copies_a ? a.wideA : a.wideB;
+    const CUtensorMap* map = copies_a ? &a.mA : &a.mB;
+    uint8_t* base = ring + (copies_a ? 0 : kOperandBytes);
+    const uint32_t full0 = ptx::mapa(&full[0], 0);
+    uint32_t it = 0, st = 0, par = 1;
+    bool ok = true;
+    for (int t = first; t < total && ok && !abort_flag; t += step) {
+      int m0, n0;
+      tile(t, m0, n0);
+      // this CTA's first row (or column) of the operand
+      const int r0 = copies_a ? m0 + 128 * rank : GATED ? n0 + rank * a.N : n0 + 128 * rank;
+      for (int kb = 0; kb < nkb; kb += 2, ++it) {
+        ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
+        if (!ok) break;
+        const uint32_t bar = full0 + 8 * st;  // both CTAs' copies complete on the first one's barrier
+        uint8_t* dst = base + st * kStageBytes;
+        const bool half = kb + 1 == nkb;
+        if (one) {
+          if (copies_a && rank == 0) {
+            // an operand's second block is counted where a box brings it, even from outside
+            const uint32_t as = kMnA || a.wideA || !half ? kOperandBytes : kOperandBytes / 2;
+            const uint32_t bs = kMnB || a.wideB || !half ? kOperandBytes : kOperandBytes / 2;
+            ptx::mbar_arrive_expect_tx(&full[st], 2 * (as + bs));
+          }
+          if (mn) {  // chunks of 64 columns x 128 k
+            if (wide) {
+              ptx::tma_load_3d_to_leader(dst, map, bar, 0, kb * 64, r0 / 64, pol);
+            } else {
+              ptx::tma_load_2d_to_leader(dst, map, bar, r0, kb * 64, pol);
+              ptx::tma_load_2d_to_leader(dst + 16384, map, bar, r0 + 64, kb * 64, pol);
+            }
+          } else {   // blocks of 128 bytes x 128 rows
+            if (wide) {
+              ptx::tma_load_3d_to_leader(dst, map, bar, 0, r0, kb, pol);
+            } else {
+              ptx::tma_load_2d_to_leader(dst, map, bar, kb * kElems, r0, pol);
+              if (!half) ptx::tma_load_2d_to_leader(dst + 16384, map, bar, (kb + 1) * kElems, r0, pol);
+            }
+          }
+        }
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          par ^= 1;
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      *a.err = (int32_t)kErrWait;
+    }
+    __syncwarp();
+    // after an abort: wait, bounded, for the copies still in flight (all complete on the first CTA's `full`)
+    if (abort_flag && copies_a && lane == 0 && rank == 0)
+      for (uint32_t i = it > (uint32_t)kStages ? it - kStages : 0; i < it; ++i)
+        ptx::mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1, kWaitNs);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA
+    bool ok = true;
+    if (rank == 0) {
+      const uint32_t ring0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
+      const bool one = ptx::elect_one();  // the lane whose MMAs its commits cover
+      constexpr uint32_t idesc = (E4M3 ? ptx::idesc_e4m3_f32(256, 256) : ptx::idesc_bf16_f32(256, 256)) |
+                                 (kMnA ? ptx::kIdescAMn : 0) | (kMnB ? ptx::kIdescBMn : 0);
+      uint32_t st = 0, par = 0, acc = 0;
+      for (int t = first; t < total && ok && !abort_flag; t += step, ++acc) {
+        const uint32_t buf = acc & 1, use = acc >> 1;
+        ok = ptx::mbar_wait_bounded_cluster(&tempty[buf], (use & 1) ^ 1, kWaitNs) && !abort_flag;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + buf * 256;
+        for (int kb = 0; kb < nkb; kb += 2) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full[st], par, kWaitNs));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t sA = ring0 + st * kStageBytes, sB = sA + kOperandBytes;
+          const uint64_t dA = kMnA ? ptx::smem_desc_mn128(sA, 16384) : ptx::smem_desc_k128(sA);
+          const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, 16384) : ptx::smem_desc_k128(sB);
+          // 32 bytes of the reduction at a time; the last stage's steps that hold none of it are left out
+          const int steps = (a.K - kb * kElems + kElems / 4 - 1) / (kElems / 4);
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            if (s >= steps) break;
+            if (!one) continue;
+            // along the reduction: 32 bytes of a block's rows; across it: 16 rows of 128 bytes
+            const uint64_t kk = (uint64_t)(s / 4 * 16384 + s % 4 * 32) >> 4, mn = (uint64_t)(s * 2048) >> 4;
+            const uint64_t oA = kMnA ? mn : kk, oB = kMnB ? mn : kk;
+            if (E4M3) ptx::umma_e4m3_pair(d, dA + oA, dB + oB, idesc, kb || s);
+            else ptx::umma_bf16_pair(d, dA + oA, dB + oB, idesc, kb || s);
+          }
+          if (one) ptx::umma_commit_pair_multicast(&empty[st], 0x3);
+          __syncwarp();
+          if (++st == kStages) {
+            st = 0;
+            par ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (one) ptx::umma_commit_pair_multicast(&tfull[buf], 0x3);
+        __syncwarp();
+      }
+      if (!ok || abort_flag) {
+        abort_flag = 1;
+        *a.err = (int32_t)kErrWait;
+        if (one) ptx::umma_commit_pair_multicast(&drain, 0x3);  // MMAs still in flight
+        ptx::mbar_wait_bounded(&drain, 0, kWaitNs);
+      }
+    } else {
+      // the second CTA's: accumulators back to the first as the epilogue here is done with them (a
+      // release across the pair waits for the thread's own stores, and this warp has none)
+      uint32_t acc = 0;
+      for (int t = first; t < total && !abort_flag; t += step, ++acc) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&tempty[acc & 1], (acc >> 1) & 1, kWaitNs));
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(&tempty[acc & 1], 0));
+        __syncwarp();
+      }
+      if (!ok) {
+        abort_flag = 1;
+        *a.err = (int32_t)kErrWait;
+      }
+    }
+    __syncwarp();
+  } else if (warp < kEpiWarps + 2) {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    uint8_t* stage = ring + kStages * kStageBytes + (warp - 2) * kWarpOut;
+    const Epilogue& e = a.e;
+    uint32_t acc = 0, blocks = 0;
+    bool ok = true;
+    for (int t = first; t < total; t += step, ++acc) {
+      int m0, n0;
+      tile(t, m0, n0);
+      const uint32_t buf = acc & 1, use = acc >> 1;
+      const int row0 = m0 + 128 * rank + 32 * quarter, row = row0 + lane;
+      const bool in = row < a.M;
+      float xs = 1.0f;
+      if (E4M3 && in) xs = e.Xs[row];
+      ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t d = tmem + buf * 256 + lanes;
+#pragma unroll 1
+      for (int i = 0; i < kTileN / 64; ++i) {
+        const int at = half * (kTileN / 2) + 32 * i, c = n0 + at, left = a.N - c;  // columns from c on
+        if (left <= 0 || row0 >= a.M) break;
+        float z[32], u[GATED ? 32 : 1];
+        {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(d + at, v);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(v[j]);
+        }
+        if (GATED) {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(d + 128 + at, v);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) u[j % (GATED ? 32 : 1)] = __uint_as_float(v[j]);
+        }
+        if (MODE == FWD) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (j >= left) break;
+            finish8<E4M3>(e, xs, 0, c + j, z + j);
+            if (GATED) finish8<E4M3>(e, xs, a.N, c + j, u + (GATED ? j : 0));
+          }
+          if (e.Zq && in) {
+            store_checkpoint(e, z, left, row, 0, GATED ? 2 : 1, a.N, c);
+            if (GATED) store_checkpoint(e, reinterpret_cast<const float(&)[32]>(u), left, row, 1, 2, a.N, c);
+          }
+          if (GATED) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] = z[j] * sigmoid_fast(z[j]) * u[j % (GATED ? 32 : 1)];
+          } else if (e.act != ACT_NONE) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] = activate(z[j], e.act);
+          }
+          if (e.R && in) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (j >= left) break;
+              float f[8];
+              load8(e.R + (int64_t)row * a.N + c + j, f);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) z[j + k] += f[k];
+            }
+          }
+        }
+        // a lane's 32 columns: four 16-byte pieces of 64-byte rows, placed as the map's 64-byte swizzle
+        // has them; rows and columns outside the matrix are not written
+        if (lane == 0) ptx::bulk_wait_group_read<1>();
+        __syncwarp();
+        uint8_t* block = stage + (blocks & 1) * 2048;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) p[k] = pack2(z[8 * j + 2 * k], z[8 * j + 2 * k + 1]);
+          *reinterpret_cast<uint4*>(block + lane * 64 + ((j ^ (lane / 2)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::tma_store_2d(&a.mO, block, c, row0);
+          ptx::bulk_commit_group();
+        }
+        ++blocks;
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
+    }
+    if (lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      *a.err = (int32_t)kErrWait;
+    }
+    __syncwarp();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // both CTAs are done with the pair's TMEM and barriers
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace lin
+}  // namespace cusync

@@ -1,0 +1,220 @@
+// The norm and its gradient, and 8-bit rows.  Bound by memory: every tensor is read or written
+// once, in 16-byte pieces; sums are in 32 bits and of a fixed order.
+#pragma once
+#include "lin_math.cuh"
+
+namespace cusync {
+namespace lin {
+
+// Sum and maximum over a block's threads, in every thread; one call in a kernel's loop needs
+// the other of the two buffers next.
+__device__ __forceinline__ float2 block_sum_max(float sum, float most, float2* buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return make_float2(sum, most);
+  if (lane == 0) buf[threadIdx.x >> 5] = make_float2(sum, most);
+  __syncthreads();
+  const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+  sum = v.x;
+  most = v.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  return make_float2(sum, most);
+}
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return make_float2(a, b);
+  if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+  a = v.x;
+  b = v.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  return make_float2(a, b);
+}
+
+struct NormArgs {
+  const uint4 *X, *R, *w;
+  uint4 *S, *Y;
+  uint2* Q;
+  float* Qs;
+  int64_t M;
+  int32_t vecs;  // D / 8
+  int32_t rms;
+  float eps, inv_d;
+};
+
+// A block takes a row and keeps it in registers: V pieces of 8 columns a thread.  The sum of
+// squares and the largest |S w| come out of one pass, as the row's factor r = 1 / sqrt(mean + eps)
+// is common to all: max |y| = r max |S w|.
+template <int V, int T>
+__global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
+  __shared__ float2 buf[32];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int64_t base = (int64_t)blockIdx.x * a.vecs;
+  float t[V][8];
+  uint4 x[V], r[V], g[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    x[v] = r[v] = g[v] = make_uint4(0, 0, 0, 0);
+    if (i < a.vecs) {
+      x[v] = a.X[base + i];
+      if (a.R) r[v] = a.R[base + i];
+      if (a.rms) g[v] = a.w[i];
+    }
+  }
+  float sum = 0.0f, most = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    unpack8(x[v], t[v]);
+    if (a.R) {
+      float f[8];
+      unpack8(r[v], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[v][j] += f[j];
+    }
+    if (a.S && i < a.vecs) a.S[base + i] = pack8(t[v]);
+    if (a.rms) {
+      float w[8];
+      unpack8(g[v], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sum = fmaf(t[v][j], t[v][j], sum);
+        most = fmaxf(most, finite_abs(t[v][j] * w[j]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = fmaxf(most, finite_abs(t[v][j]));
+    }
+  }
+  const float2 all = block_sum_max(sum, most, buf);
+  const float f = a.rms ? 1.0f / sqrtf(all.x * a.inv_d + a.eps) : 1.0f;
+  // r is NaN or 0 where the row holds NaN or infinities: nothing finite is left, or zeros
+  const float scale = fmaxf(finite_abs(f * all.y) * (1.0f / kE4m3Max), kLeastScale);
+  const float inv = 1.0f / scale;
+  if (a.Q && threadIdx.x == 0) a.Qs[blockIdx.x] = scale;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    if (i >= a.vecs) continue;
+    if (a.rms) {
+      float w[8];
+      unpack8(g[v], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[v][j] = t[v][j] * f * w[j];
+    }
+    if (a.Y) a.Y[base + i] = pack8(t[v]);
+    if (a.Q) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[v][j] = no_inf(t[v][j]) * inv;
+      a.Q[base + i] = make_uint2(pack_e4m3(t[v][0], t[v][1], t[v][2], t[v][3]),
+                                 pack_e4m3(t[v][4], t[v][5], t[v][6], t[v][7]));
+    }
+  }
+}
+
+struct NormGradArgs {
+  const uint4 *S, *w, *dY, *dS;
+  uint4* dX;
+  float* part;  // [blocks][D] sums of dY S r over a block's rows, or NULL
+  int64_t M;
+  int32_t vecs;
+  float eps, inv_d;
+};
+
+// dX = r (g - S r^2 mean(g S)) + dS with g = w dY; a block takes rows blockIdx.x, + gridDim.x, ...
+// and keeps its columns' share of dw in registers.
+template <int V, int T, int PER_SM>
+__global__ void __launch_bounds__(T, PER_SM) norm_grad_kernel(const NormGradArgs a) {
+  __shared__ float2 buf[2][32];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  float dw[V][8];
+  uint4 wv[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    wv[v] = i < a.vecs ? a.w[i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+    const int64_t base = row * a.vecs;
+    uint4 x[V], y[V], s[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = threadIdx.x + v * blockDim.x;
+      x[v] = y[v] = s[v] = make_uint4(0, 0, 0, 0);
+      if (i < a.vecs) {
+        x[v] = a.S[base + i];
+        y[v] = a.dY[base + i];
+        if (a.dS) s[v] = a.dS[base + i];
+      }
+    }
+    float squares = 0.0f, dots = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float fx[8], fy[8], fw[8];
+      unpack8(x[v], fx);
+      unpack8(y[v], fy);
+      unpack8(wv[v], fw);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        squares = fmaf(fx[j], fx[j], squares);
+        dots = fmaf(fy[j] * fw[j], fx[j], dots);
+      }
+    }
+    const float2 all = block_sum2(squares, dots, buf[turn]);
+    const float r = 1.0f / sqrtf(all.x * a.inv_d + a.eps);
+    const float c = all.y * a.inv_d * r * r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = threadIdx.x + v * blockDim.x;
+      if (i >= a.vecs) continue;
+      float fx[8], fy[8], fw[8], fs[8];
+      unpack8(x[v], fx);
+      unpack8(y[v], fy);
+      unpack8(wv[v], fw);
+      unpack8(s[v], fs);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[v][j] = fmaf(fy[j], fx[j] * r, dw[v][j]);
+        fs[j] += r * (fy[j] * fw[j] - fx[j] * c);
+      }
+      a.dX[base + i] = pack8(fs);
+    }
+  }
+  if (a.part) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = threadIdx.x + v * blockDim.x;
+      if (i >= a.vecs) continue;
+      float4* out = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.vecs + i) * 2;
+      out[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+      out[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+    }
+  }
+}
+
+}  // namespace lin
+}  // namespace cusync

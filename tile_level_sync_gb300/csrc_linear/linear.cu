@@ -1,0 +1,401 @@
+// Host side of the linear layer in include/cusync_linear.h: argument checks, buffer layouts, TMA
+// descriptors and kernel launches.
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cstring>
+#include <mutex>
+
+#include "lin_dz.cuh"
+#include "lin_gemm.cuh"
+#include "lin_host.h"
+#include "lin_split.cuh"
+
+using namespace cusync;
+using namespace cusync::lin;
+
+namespace {
+
+constexpr int64_t kHeader = 256;     // bytes of a work buffer before its arrays; the error word first
+constexpr int64_t kDzBlocks = 1024;  // blocks of the pass over dY, about
+constexpr int64_t kDzRows = 32;      // rows of such a block at least
+constexpr int kSmemPerSm = 227 * 1024;
+
+// What a descriptor means.
+struct Layer {
+  int64_t M, K, N, G, blocks;
+  bool e4m3;
+  int64_t dz_rows, dz_parts;               // rows of a block of the pass over dY; blocks along M
+  int64_t dz, x, part, work_bytes, grad_bytes;  // gradient work, bytes
+};
+
+cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
+  if (!d || d->M < 0 || d->K < 1 || d->N < 1 || d->num_sms < 0 || d->act < CUSYNC_LINEAR_NONE ||
+      d->act > CUSYNC_LINEAR_SWIGLU || (d->dtype != CUSYNC_LINEAR_BF16 && d->dtype != CUSYNC_LINEAR_E4M3))
+    return CUSYNC_ERR_INVALID_ARG;
+  L->e4m3 = d->dtype == CUSYNC_LINEAR_E4M3;
+  // the kernels count rows, columns and tiles in 32 bits
+  if (d->N % 8 || d->K % (L->e4m3 ? 16 : 8) || d->K > (1 << 24) || d->N > (1 << 24) || d->M > (1 << 30) ||
+      div_up(d->M, 16) * div_up(std::max(d->N, d->K), 64) > INT32_MAX / 8 ||
+      div_up(2 * d->N, 64) * div_up(d->K, 64) > INT32_MAX / 8)
+    return CUSYNC_ERR_UNSUPPORTED;
+  L->M = d->M;
+  L->K = d->K;
+  L->N = d->N;
+  L->G = d->act == CUSYNC_LINEAR_SWIGLU ? 2 : 1;
+  L->blocks = div_up(d->N, kBlock);
+  const int64_t columns = div_up(L->N, kDzCols);
+  L->dz_rows = std::max(kDzRows, round_up(div_up(L->M, std::max<int64_t>(1, kDzBlocks / columns)), 8));
+  L->dz_parts = std::max<int64_t>(1, div_up(L->M, L->dz_rows));
+  int64_t b = kHeader;
+  auto bytes = [&b](int64_t n) {
+    const int64_t at = b;
+    b += round_up(n, 256);
+    return at;
+  };
+  L->work_bytes = b;
+  L->dz = bytes(d->act == CUSYNC_LINEAR_NONE ? 0 : L->M * L->G * L->N * 2);
+  L->x = bytes(L->e4m3 ? L->M * L->K * 2 : 0);
+  L->part = bytes(L->dz_parts * L->G * L->N * 4);
+  L->grad_bytes = b;
+  return CUSYNC_OK;
+}
+
+// ----------------------------------------------------------------------------- devices
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::mutex g_mu;
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];  // SMs of a prepared device, 0 = not prepared
+
+cudaError_t prepare_kernel(const void* f, int smem) {
+  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;  // loads the kernel now, not at a launch inside a capture
+  return cudaFuncGetAttributes(&fa, f);
+}
+template <int MODE, bool E4M3, bool GATED>
+cudaError_t prepare_product() {
+  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(&gemm_kernel<MODE, E4M3, GATED>), kGemmSmem);
+  if (e != cudaSuccess) return e;
+  return prepare_kernel(reinterpret_cast<const void*>(&split_kernel<MODE, E4M3, GATED>), kSmemPerSm - 1024);
+}
+
+// The current device: the attributes set of the kernels that need some, the descriptor encoder
+// found.  The first call on a device does the work.
+cusync_status_t prepare_device(int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return CUSYNC_ERR_CUDA;
+  if (int n = g_sms[dev].load(std::memory_order_acquire)) {
+    *sms = n;
+    return CUSYNC_OK;
+  }
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return CUSYNC_ERR_CUDA;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  int n = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = prepare_product<FWD, false, false>();
+  if (e == cudaSuccess) e = prepare_product<FWD, false, true>();
+  if (e == cudaSuccess) e = prepare_product<FWD, true, false>();
+  if (e == cudaSuccess) e = prepare_product<FWD, true, true>();
+  if (e == cudaSuccess) e = prepare_product<DX, false, false>();
+  if (e == cudaSuccess) e = prepare_product<DW, false, false>();
+  if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
+  g_sms[dev].store(n, std::memory_order_release);
+  *sms = n;
+  return CUSYNC_OK;
+}
+
+// A map of `bytes`-wide elements: sizes and strides (in elements, from the second dimension on) and
+// the box, innermost first; elements outside read as zero.
+template <int N>
+bool map_nd(CUtensorMap* m, const void* p, int bytes, CUtensorMapSwizzle swizzle, const int64_t (&size)[N],
+            const int64_t (&stride)[N - 1], const int (&box_size)[N]) {
+  cuuint64_t dims[N], strides[N - 1];
+  cuuint32_t box[N], one[N];
+  for (int i = 0; i < N; ++i) {
+    dims[i] = (cuuint64_t)size[i];
+    box[i] = (cuuint32_t)box_size[i];
+    one[i] = 1;
+    if (i) strides[i - 1] = (cuuint64_t)stride[i - 1] * bytes;
+  }
+  return g_encode(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N,
+                  const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An operand [rows, cols] whose columns are the reduction's: boxes of 128 bytes x box_rows; wide (columns a
+// multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of two blocks.
+bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int box_rows, int32_t* wide) {
+  const int n = 128 / bytes;
+  *wide = cols % n == 0;
+  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {cols, n}, {n, box_rows, 2})
+               : map_nd<2>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {n, box_rows});
+}
+// Gate and up rows of a gated layer's weights [2][rows, cols], 64 of each in a box.
+bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int32_t* wide) {
+  const int n = 128 / bytes;
+  *wide = cols % n == 0;
+  return *wide ? map_nd<4>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, 2, cols / n}, {cols, rows * cols, n},
+                           {n, 64, 2, 2})
+               : map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows, 2}, {cols, rows * cols}, {n, 64, 2});
+}
+// A bf16 operand [rows, cols] whose rows are the reduction's: boxes of 64 columns x 128 rows; wide (columns a
+// multiple of 64): as [chunks][rows][64], boxes of `chunks`.
+bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int chunks, int32_t* wide) {
+  *wide = cols % 64 == 0;
+  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {cols, 64}, {64, 128, chunks})
+               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {64, 128});
+}
+// An output [rows, cols]: boxes of 32 x 32 as a warp's lanes write them.
+bool map_output(CUtensorMap* m, void* p, int64_t rows, int64_t cols) {
+  return map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_64B, {cols, rows}, {cols}, {32, 32});
+}
+
+// ----------------------------------------------------------------------------- products
+
+// One product: `rows` x `cols` outputs (SwiGLU: columns of Y), reduction `depth`.  P and Q are the
+// operands of the output's rows and columns: [rows, depth] and [cols, depth] (SwiGLU: [2 * cols, depth]),
+// or, where they lie along the output, [depth, rows] and [depth, cols].
+struct Product {
+  const void *P, *Q;
+  int64_t rows, cols, depth;
+  Epilogue e;
+  int32_t* err;
+  bool clear;
+};
+
+// How a product is computed: on CTA pairs, or (cols > 0) on clusters of `splits` CTAs.
+struct Plan {
+  int cols, splits, stages;
+};
+
+template <int MODE, bool GATED>
+Plan choose(const Product& p, int sms, int elems) {
+  const int64_t pair_tiles = div_up(p.rows, 256) * div_up(p.cols, GATED ? 128 : 256);
+  if (sms >= 2 && pair_tiles >= 38) return {0, 0, 0};
+  Plan r;
+  r.cols = MODE == DW ? 64 : 16;
+  while (r.cols < 128 && r.cols < p.rows) r.cols *= 2;
+  const int stage = split_stage_bytes(r.cols);
+  // two CTAs an SM where three stages of both fit
+  const int resident = 2 * (3 * stage + 2048) <= kSmemPerSm ? 2 : 1;
+  r.stages = std::min(kMaxStages, (kSmemPerSm / resident - 2048) / stage);
+  const int64_t tiles = div_up(p.rows, r.cols) * div_up(p.cols, GATED ? 64 : 128);
+  const int64_t steps = div_up(p.depth, 2 * elems);
+  r.splits = 1;
+  while (r.splits < 8 && 2 * r.splits * tiles <= (int64_t)sms * resident && 2 * r.splits <= steps) r.splits *= 2;
+  return r;
+}
+
+template <int MODE, bool E4M3, bool GATED>
+cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
+  constexpr int bytes = E4M3 ? 1 : 2;
+  const Plan plan = choose<MODE, GATED>(p, sms, 128 / bytes);
+  if (!plan.cols) {
+    GemmArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.e = p.e;
+    a.err = p.err;
+    a.clear = p.clear;
+    a.M = (int32_t)p.rows;
+    a.N = (int32_t)p.cols;
+    a.K = (int32_t)p.depth;
+    a.m_tiles = (int32_t)div_up(p.rows, 256);
+    a.n_tiles = (int32_t)div_up(p.cols, GATED ? 128 : 256);
+    a.group = std::min(a.m_tiles, 8);
+    const bool ok = (MODE == DW ? map_along(&a.mA, p.P, p.depth, p.rows, 2, &a.wideA)
+                                : map_rows(&a.mA, p.P, bytes, p.rows, p.depth, 128, &a.wideA)) &&
+                    (MODE == FWD ? map_rows(&a.mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, 128, &a.wideB)
+                                 : map_along(&a.mB, p.Q, p.depth, p.cols, 2, &a.wideB)) &&
+                    map_output(&a.mO, p.e.out, p.rows, p.cols);
+    if (!ok) return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
+    const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
+    return launch_cluster(2, gemm_kernel<MODE, E4M3, GATED>, dim3(grid), kGemmThreads, kGemmSmem, s, a);
+  }
+  SplitArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.e = p.e;
+  a.err = p.err;
+  a.clear = p.clear;
+  a.M = (int32_t)p.rows;
+  a.N = (int32_t)p.cols;
+  a.K = (int32_t)p.depth;
+  a.cols = plan.cols;
+  a.row_tiles = (int32_t)div_up(p.rows, plan.cols);
+  a.splits = plan.splits;
+  a.stages = plan.stages;
+  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, 2, &a.wideA)
+                   : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, &a.wideA)
+                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, 128, &a.wideA)) &&
+                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, plan.cols / 64, &a.wideB)
+                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, plan.cols, &a.wideB));
+  if (!ok) return cudaErrorInvalidValue;
+  const int64_t tiles = div_up(p.cols, GATED ? 64 : 128) * a.row_tiles;
+  return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)),
+                        kSplitThreads, (size_t)plan.stages * split_stage_bytes(plan.cols) + 1024, s, a);
+}
+
+cusync_status_t capture_or_ok(cudaStream_t s) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  const cudaError_t e = cudaStreamIsCapturing(s, &capture);
+  if (e == cudaErrorStreamCaptureImplicit || (e == cudaSuccess && capture != cudaStreamCaptureStatusNone))
+    return CUSYNC_ERR_UNSUPPORTED;
+  return status_of(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+cusync_status_t cusync_linear_info(const cusync_linear_desc_t* d, cusync_linear_info_t* out) {
+  Layer L;
+  if (!out) return CUSYNC_ERR_INVALID_ARG;
+  const cusync_status_t st = read_desc(d, &L);
+  if (st != CUSYNC_OK) return st;
+  out->work_bytes = L.work_bytes;
+  out->grad_work_bytes = L.grad_bytes;
+  out->parts = L.G;
+  out->blocks = L.blocks;
+  return CUSYNC_OK;
+}
+
+cusync_status_t cusync_linear(const cusync_linear_desc_t* d, const void* X, const float* Xs, const void* Wt,
+                              const float* Ws, const void* bias, const void* R, void* work, void* Y, void* Zq,
+                              uint8_t* Ze, cusync_stream_t stream) {
+  Layer L;
+  cusync_status_t st = read_desc(d, &L);
+  if (st != CUSYNC_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!aligned(work) || !Zq != !Ze || (!L.e4m3 && (Xs || Ws))) return CUSYNC_ERR_INVALID_ARG;
+  if (L.M == 0) return status_of(cudaMemsetAsync(work, 0, 4, s));
+  if (!aligned(X) || !aligned(Wt) || !aligned(Y) || !aligned_or_null(bias) || !aligned_or_null(R) ||
+      !aligned_or_null(Zq) || !aligned_or_null(Ze) || (L.e4m3 && (!aligned(Xs) || !aligned(Ws))))
+    return CUSYNC_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = prepare_device(&sms)) != CUSYNC_OK) return st;
+  if (d->num_sms) sms = std::min(sms, d->num_sms);
+  Product p = {};
+  p.P = X;
+  p.Q = Wt;
+  p.rows = L.M;
+  p.cols = L.N;
+  p.depth = L.K;
+  p.e.Xs = Xs;
+  p.e.Ws = Ws;
+  p.e.bias = static_cast<const uint16_t*>(bias);
+  p.e.R = static_cast<const uint16_t*>(R);
+  p.e.Zq = static_cast<uint8_t*>(Zq);
+  p.e.Ze = Ze;
+  p.e.out = static_cast<uint16_t*>(Y);
+  p.e.act = d->act;
+  p.err = static_cast<int32_t*>(work);
+  p.clear = true;
+  return status_of(L.e4m3 ? (L.G == 2 ? launch_product<FWD, true, true>(p, sms, s) : launch_product<FWD, true, false>(p, sms, s))
+                          : (L.G == 2 ? launch_product<FWD, false, true>(p, sms, s)
+                                      : launch_product<FWD, false, false>(p, sms, s)));
+}
+
+cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X, const float* Xs, const void* Wt,
+                                   const void* Zq, const uint8_t* Ze, const void* dY, void* work, void* dX,
+                                   void* dWt, void* dbias, cusync_stream_t stream) {
+  Layer L;
+  cusync_status_t st = read_desc(d, &L);
+  if (st != CUSYNC_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool act = d->act != CUSYNC_LINEAR_NONE;
+  if (!aligned(work) || (!dX && !dWt && !dbias) || !aligned_or_null(dX) || !aligned_or_null(dWt) ||
+      !aligned_or_null(dbias) || (!L.e4m3 && Xs))
+    return CUSYNC_ERR_INVALID_ARG;
+  const int64_t H = L.G * L.N;
+  if (L.M == 0) {  // no token: the parameters' gradients are zero
+    cudaError_t e = cudaMemsetAsync(work, 0, 4, s);
+    if (e == cudaSuccess && dWt) e = cudaMemsetAsync(dWt, 0, (size_t)H * L.K * 2, s);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)H * 2, s);
+    return status_of(e);
+  }
+  if (!aligned(dY) || (act && (!aligned(Zq) || !aligned(Ze))) || (dX && !aligned(Wt)) ||
+      (dWt && (!aligned(X) || (L.e4m3 && !aligned(Xs)))))
+    return CUSYNC_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((st = prepare_device(&sms)) != CUSYNC_OK) return st;
+  if (d->num_sms) sms = std::min(sms, d->num_sms);
+  char* w = static_cast<char*>(work);
+  int32_t* err = static_cast<int32_t*>(work);
+  bool clear = true;
+  cudaError_t e = cudaSuccess;
+  const void* dZ = act ? w + L.dz : dY;
+  if (act || dbias) {
+    DzArgs a = {};
+    a.dY = static_cast<const uint16_t*>(dY);
+    a.Zq = static_cast<const uint8_t*>(Zq);
+    a.Ze = Ze;
+    a.dZ = reinterpret_cast<uint16_t*>(w + L.dz);
+    a.part = dbias ? reinterpret_cast<float*>(w + L.part) : nullptr;
+    a.err = err;
+    a.M = L.M;
+    a.N = (int32_t)L.N;
+    a.rows = (int32_t)L.dz_rows;
+    clear = false;
+    const dim3 grid((unsigned)div_up(L.N, kDzCols), (unsigned)L.dz_parts);
+    e = d->act == CUSYNC_LINEAR_NONE   ? launch(dz_kernel<ACT_NONE>, grid, 256, 0, s, a)
+        : d->act == CUSYNC_LINEAR_RELU ? launch(dz_kernel<ACT_RELU>, grid, 256, 0, s, a)
+        : d->act == CUSYNC_LINEAR_GELU ? launch(dz_kernel<ACT_GELU>, grid, 256, 0, s, a)
+                                       : launch(dz_kernel<ACT_SWIGLU>, grid, 256, 0, s, a);
+    if (e == cudaSuccess && dbias)
+      e = launch(column_sum_kernel, dim3((unsigned)div_up(H, 32)), 256, 0, s, (const float*)a.part, (int32_t)L.dz_parts,
+                 (int32_t)H, static_cast<uint16_t*>(dbias));
+  }
+  Product p = {};
+  p.P = dZ;
+  p.err = err;
+  if (e == cudaSuccess && dX) {
+    p.Q = Wt;
+    p.rows = L.M;
+    p.cols = L.K;
+    p.depth = H;
+    p.e.out = static_cast<uint16_t*>(dX);
+    p.clear = clear;
+    clear = false;
+    e = launch_product<DX, false, false>(p, sms, s);
+  }
+  if (e == cudaSuccess && dWt) {
+    p.Q = X;
+    if (L.e4m3) {
+      p.Q = w + L.x;
+      const int64_t pieces = L.M * (L.K / 16);
+      e = launch(rows_from_e4m3_kernel, dim3((unsigned)std::min<int64_t>(div_up(pieces, 256), (int64_t)sms * 16)), 256, 0, s,
+                 static_cast<const uint4*>(X), Xs, reinterpret_cast<uint4*>(w + L.x), L.M, (int32_t)(L.K / 16));
+    }
+    p.rows = H;
+    p.cols = L.K;
+    p.depth = L.M;
+    p.e.out = static_cast<uint16_t*>(dWt);
+    p.clear = clear;
+    if (e == cudaSuccess) e = launch_product<DW, false, false>(p, sms, s);
+  }
+  return status_of(e);
+}
+
+cusync_status_t cusync_linear_check(const void* work, cusync_stream_t stream, uint32_t* code) {
+  if (!aligned(work)) return CUSYNC_ERR_INVALID_ARG;
+  // a wait inside a capture would end the capture
+  const cusync_status_t st = capture_or_ok((cudaStream_t)stream);
+  if (st != CUSYNC_OK) return st;
+  uint32_t err = 0;
+  cudaError_t e = cudaMemcpyAsync(&err, work, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
+  if (code) *code = err;
+  return err ? CUSYNC_ERR_DEVICE : CUSYNC_OK;
+}
+
+}  // extern "C"
