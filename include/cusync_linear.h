@@ -75,7 +75,9 @@ cusync_status_t cusync_norm(const cusync_norm_desc_t* d, const void* X, const vo
 /* Gradients at S [M, D] (what cusync_norm wrote, or its X where it had no R) for dY [M, D]:
  * dX [M, D], which is R's gradient too, and dw [D] (NULL: not wanted).  dS [M, D] or NULL is the
  * gradient that reaches S along the residual path: it is added to dX, which may be dY or dS (that
- * buffer itself).  work: grad_work_bytes of scratch.  UNSUPPORTED for CUSYNC_NORM_NONE. */
+ * buffer itself).  work (not read where dw is NULL): grad_work_bytes of scratch, of which the first
+ * 256 are left as they are, so that a buffer shared with linear calls keeps their error word.
+ * UNSUPPORTED for CUSYNC_NORM_NONE. */
 cusync_status_t cusync_norm_grad(const cusync_norm_desc_t* d, const void* S, const void* w, const void* dY,
                                  const void* dS, void* work, void* dX, void* dw, cusync_stream_t stream);
 

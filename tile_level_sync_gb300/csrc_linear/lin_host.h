@@ -12,6 +12,8 @@
 namespace cusync {
 namespace lin {
 
+constexpr int64_t kHeader = 256;  // bytes of a work buffer before its arrays; a linear call's error word first
+
 using moe::launch;
 using moe::launch_cluster;
 

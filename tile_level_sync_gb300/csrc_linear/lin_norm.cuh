@@ -60,12 +60,17 @@ struct NormArgs {
   float eps, inv_d;
 };
 
+// Squares of a row's values leave fp32's range before the values do.  Where the mean of the squares
+// plus eps, v, is outside of what follows, the row is taken times this power of two instead.
+__device__ __forceinline__ bool squares_fit(float v) { return v >= 0x1p-100f && v <= 0x1p120f; }
+__device__ __forceinline__ float square_scale(float v) { return v > 1.0f ? 0x1p-70f : 0x1p70f; }
+
 // A block takes a row and keeps it in registers: V pieces of 8 columns a thread.  The sum of
 // squares and the largest |S w| come out of one pass, as the row's factor r = 1 / sqrt(mean + eps)
 // is common to all: max |y| = r max |S w|.
 template <int V, int T>
 __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
-  __shared__ float2 buf[32];
+  __shared__ float2 buf[2][32];
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int64_t base = (int64_t)blockIdx.x * a.vecs;
@@ -106,10 +111,33 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
       for (int j = 0; j < 8; ++j) most = fmaxf(most, finite_abs(t[v][j]));
     }
   }
-  const float2 all = block_sum_max(sum, most, buf);
-  const float f = a.rms ? 1.0f / sqrtf(all.x * a.inv_d + a.eps) : 1.0f;
-  // r is NaN or 0 where the row holds NaN or infinities: nothing finite is left, or zeros
-  const float scale = fmaxf(finite_abs(f * all.y) * (1.0f / kE4m3Max), kLeastScale);
+  float2 all = block_sum_max(sum, most, buf[0]);
+  float f = 1.0f;
+  if (a.rms) {
+    float v = all.x * a.inv_d + a.eps, c = 1.0f;
+    if (!squares_fit(v)) {
+      c = square_scale(v);
+      sum = most = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float w[8];
+        unpack8(g[v], w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = t[v][j] * c;
+          sum = fmaf(x, x, sum);
+          most = fmaxf(most, finite_abs(x * w[j]));
+        }
+      }
+      all = block_sum_max(sum, most, buf[1]);
+      v = all.x * a.inv_d + a.eps * c * c;
+    }
+    f = 1.0f / sqrtf(v);
+    all.y *= f;
+    f *= c;
+  }
+  // the factor is NaN or 0 where the row holds NaN or infinities: nothing finite is left, or zeros
+  const float scale = fmaxf(finite_abs(all.y) * (1.0f / kE4m3Max), kLeastScale);
   const float inv = 1.0f / scale;
   if (a.Q && threadIdx.x == 0) a.Qs[blockIdx.x] = scale;
 #pragma unroll
@@ -141,11 +169,11 @@ struct NormGradArgs {
   float eps, inv_d;
 };
 
-// dX = r (g - S r^2 mean(g S)) + dS with g = w dY; a block takes rows blockIdx.x, + gridDim.x, ...
+// dX = r (g - S r mean(g S r)) + dS with g = w dY; a block takes rows blockIdx.x, + gridDim.x, ...
 // and keeps its columns' share of dw in registers.
 template <int V, int T, int PER_SM>
 __global__ void __launch_bounds__(T, PER_SM) norm_grad_kernel(const NormGradArgs a) {
-  __shared__ float2 buf[2][32];
+  __shared__ float2 buf[4][32];
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   float dw[V][8];
@@ -184,9 +212,28 @@ __global__ void __launch_bounds__(T, PER_SM) norm_grad_kernel(const NormGradArgs
         dots = fmaf(fy[j] * fw[j], fx[j], dots);
       }
     }
-    const float2 all = block_sum2(squares, dots, buf[turn]);
-    const float r = 1.0f / sqrtf(all.x * a.inv_d + a.eps);
-    const float c = all.y * a.inv_d * r * r;
+    float2 all = block_sum2(squares, dots, buf[turn]);
+    float square = all.x * a.inv_d + a.eps, c = 1.0f;
+    if (!squares_fit(square)) {
+      c = square_scale(square);
+      squares = dots = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float fx[8], fy[8], fw[8];
+        unpack8(x[v], fx);
+        unpack8(y[v], fy);
+        unpack8(wv[v], fw);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float xc = fx[j] * c;
+          squares = fmaf(xc, xc, squares);
+          dots = fmaf(fy[j] * fw[j], xc, dots);
+        }
+      }
+      all = block_sum2(squares, dots, buf[2 + turn]);
+      square = all.x * a.inv_d + a.eps * c * c;
+    }
+    const float rc = 1.0f / sqrtf(square), mean = all.y * a.inv_d * rc, r = rc * c;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = threadIdx.x + v * blockDim.x;
@@ -198,8 +245,9 @@ __global__ void __launch_bounds__(T, PER_SM) norm_grad_kernel(const NormGradArgs
       unpack8(s[v], fs);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[v][j] = fmaf(fy[j], fx[j] * r, dw[v][j]);
-        fs[j] += r * (fy[j] * fw[j] - fx[j] * c);
+        const float xh = fx[j] * r;
+        dw[v][j] = fmaf(fy[j], xh, dw[v][j]);
+        fs[j] += r * (fy[j] * fw[j] - xh * mean);
       }
       a.dX[base + i] = pack8(fs);
     }

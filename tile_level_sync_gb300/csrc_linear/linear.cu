@@ -16,7 +16,6 @@ using namespace cusync::lin;
 
 namespace {
 
-constexpr int64_t kHeader = 256;     // bytes of a work buffer before its arrays; the error word first
 constexpr int64_t kDzBlocks = 1024;  // blocks of the pass over dY, about
 constexpr int64_t kDzRows = 32;      // rows of such a block at least
 constexpr int kSmemPerSm = 227 * 1024;
@@ -275,7 +274,7 @@ cusync_status_t cusync_linear(const cusync_linear_desc_t* d, const void* X, cons
   cusync_status_t st = read_desc(d, &L);
   if (st != CUSYNC_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  if (!aligned(work) || !Zq != !Ze || (!L.e4m3 && (Xs || Ws))) return CUSYNC_ERR_INVALID_ARG;
+  if (!aligned(work) || (L.M && !Zq != !Ze) || (!L.e4m3 && (Xs || Ws))) return CUSYNC_ERR_INVALID_ARG;
   if (L.M == 0) return status_of(cudaMemsetAsync(work, 0, 4, s));
   if (!aligned(X) || !aligned(Wt) || !aligned(Y) || !aligned_or_null(bias) || !aligned_or_null(R) ||
       !aligned_or_null(Zq) || !aligned_or_null(Ze) || (L.e4m3 && (!aligned(Xs) || !aligned(Ws))))
@@ -312,7 +311,7 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
   if (st != CUSYNC_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   const bool act = d->act != CUSYNC_LINEAR_NONE;
-  if (!aligned(work) || (!dX && !dWt && !dbias) || !aligned_or_null(dX) || !aligned_or_null(dWt) ||
+  if (!aligned(work) || (L.M && !dX && !dWt && !dbias) || !aligned_or_null(dX) || !aligned_or_null(dWt) ||
       !aligned_or_null(dbias) || (!L.e4m3 && Xs))
     return CUSYNC_ERR_INVALID_ARG;
   const int64_t H = L.G * L.N;

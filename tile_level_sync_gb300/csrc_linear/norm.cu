@@ -45,7 +45,7 @@ cusync_status_t cusync_norm_info(const cusync_norm_desc_t* d, cusync_norm_info_t
   if (!out) return CUSYNC_ERR_INVALID_ARG;
   const cusync_status_t st = read_desc(d);
   if (st != CUSYNC_OK) return st;
-  out->grad_work_bytes = round_up(std::min<int64_t>(std::max<int64_t>(d->M, 1), kGradBlocks) * d->D * 4, 256);
+  out->grad_work_bytes = kHeader + round_up(std::min<int64_t>(std::max<int64_t>(d->M, 1), kGradBlocks) * d->D * 4, 256);
   return CUSYNC_OK;
 }
 
@@ -54,8 +54,8 @@ cusync_status_t cusync_norm(const cusync_norm_desc_t* d, const void* X, const vo
   const cusync_status_t st = read_desc(d);
   if (st != CUSYNC_OK) return st;
   const bool rms = d->kind == CUSYNC_NORM_RMS;
-  if ((!S && !Y && !Q) || !Q != !Qs) return CUSYNC_ERR_INVALID_ARG;
   if (d->M == 0) return CUSYNC_OK;
+  if ((!S && !Y && !Q) || !Q != !Qs) return CUSYNC_ERR_INVALID_ARG;
   if (!aligned(X) || (rms && !aligned(w)) || !aligned_or_null(R) || !aligned_or_null(S) || !aligned_or_null(Y) ||
       !aligned_or_null(Q) || !aligned_or_null(Qs))
     return CUSYNC_ERR_INVALID_ARG;
@@ -103,7 +103,7 @@ cusync_status_t cusync_norm_grad(const cusync_norm_desc_t* d, const void* S, con
   a.dY = static_cast<const uint4*>(dY);
   a.dS = static_cast<const uint4*>(dS);
   a.dX = static_cast<uint4*>(dX);
-  a.part = dw ? static_cast<float*>(work) : nullptr;
+  a.part = dw ? reinterpret_cast<float*>(static_cast<char*>(work) + kHeader) : nullptr;
   a.M = d->M;
   a.vecs = (int32_t)(d->D / 8);
   a.eps = d->eps;
