@@ -1,19 +1,21 @@
 // The products of a linear layer on CTA pairs: one persistent tcgen05 kernel.
 //
-//   mode   A (M: 256 rows a pair)    B (N: 256 columns a pair)      epilogue
-//   FWD    X rows                    Wt rows; SwiGLU: 128 gate rows  scales, bias, checkpoint, activation,
-//                                    in the first CTA, the 128 up    residual, bf16
+//   mode   A (M: 256 rows a pair)    B (N: BN columns a pair)       epilogue
+//   FWD    X rows                    Wt rows; SwiGLU: BN / 2 gate    scales, bias, checkpoint, activation,
+//                                    rows in the first CTA, the up   residual, bf16
 //                                    rows N further in the second
-//   DX     dZ rows                   Wt along K                      bf16
-//   DW     dZ along N (K: tokens)    X along K                       bf16
+//   GRAD   dX: dZ rows               Wt along K                      bf16
+//          dWt: dZ along N           X along K (K: tokens)           bf16
 //
 // "along": the operand is stored with its M (or N) index contiguous rather than the reduction's,
-// and the MMA reads it that way through its descriptors; nothing is transposed in memory.
+// and the MMA reads it that way through its descriptors; nothing is transposed in memory.  GRAD
+// computes both products in one launch, the one with the longer reduction first, whose tail the
+// other's tiles fill; dbias's partial sums are added up by a warp that the products leave idle.
 //
-// A stage holds 128 bytes x 2 of the reduction for the CTA's 128 rows of A and of B (64 KB), three
-// stages fit beside the epilogue's staging.  Roles, as in the expert layer's products: warp 0 copies A,
+// A stage holds 128 bytes x 2 of the reduction for the CTA's 128 rows of A and BN / 2 of B (64 or 48 KB);
+// three or four fit beside the epilogue's staging.  Roles, as in the expert layer's products: warp 0 copies A,
 // the last warp but one copies B (TMA, one box each where the widths are multiples of 128 bytes),
-// lane 0 of the first CTA's warp 1 issues the MMAs (256 x 256 x 32 bytes), the eight epilogue warps read
+// lane 0 of the first CTA's warp 1 issues the MMAs (256 x BN x 32 bytes), the eight epilogue warps read
 // one accumulator of TMEM while the next tile runs into the other.  Tiles are equal, so a
 // pair takes tiles t = pair, pair + pairs, ...: row tiles inner within groups of `group`, so that pairs
 // at work at the same time share operands in the L2.
@@ -54,7 +56,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
 
 namespace lin {
 
-enum : int { FWD = 0, DX = 1, DW = 2 };
+enum : int { FWD = 0, DX = 1, DW = 2, GRAD = 3 };
 
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kErrWait = 3u << 24;  // the pipeline-wait class of the chain kernel's error words
@@ -68,23 +70,35 @@ struct Epilogue {
   int32_t act;
 };
 
-struct GemmArgs {
+// One product: output rows and columns (SwiGLU: of Y), reduction length.
+struct GemmShape {
   CUtensorMap mA, mB, mO;
-  Epilogue e;
-  int32_t* err;
-  int32_t clear;            // this kernel is the call's first: it clears the error word
-  int32_t M, N, K;          // output rows, output columns (SwiGLU: of Y), reduction length
+  int32_t M, N, K;
   int32_t m_tiles, n_tiles, group;
   int32_t wideA, wideB;     // one box brings an operand's whole share of a stage
+  int32_t along;            // GRAD: A's rows are the reduction's
+};
+struct GemmArgs {
+  GemmShape p[2];           // FWD: [0]
+  Epilogue e;               // FWD
+  const float* part;        // GRAD: dbias's partial sums [part_rows][part_cols], or NULL
+  uint16_t* sums;
+  int32_t part_rows, part_cols;
+  int32_t* err;
+  int32_t clear;            // this kernel is the call's first: it clears the error word
 };
 
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (kEpiWarps + 4) * 32;
-constexpr int kOperandBytes = 32 * 1024;  // a CTA's share of A, and of B, in a stage
-constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 3;
+constexpr int kABytes = 32 * 1024;        // a CTA's share of A in a stage
 constexpr int kWarpOut = 4096;            // two blocks of 32 rows x 32 columns
-constexpr int kGemmSmem = kStages * kStageBytes + kEpiWarps * kWarpOut + 1024;
+template <int BN>
+struct GemmCfg {
+  static constexpr int kBBytes = BN * 128;  // BN / 2 rows x 2 blocks of 128 bytes
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 192 * 1024 / kStageBytes;
+  static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpOut + 1024;
+};
 
 // 16 bytes of bf16 or fp32 values that all lanes read
 __device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
@@ -131,11 +145,13 @@ __device__ __forceinline__ void store_checkpoint(const Epilogue& e, const float 
   e.Ze[line * ((N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)x;
 }
 
-template <int MODE, bool E4M3, bool GATED>
+template <int MODE, bool E4M3, bool GATED, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
-  constexpr bool kMnA = MODE == DW, kMnB = MODE != FWD;
+  using C = GemmCfg<BN>;
+  constexpr bool kMnB = MODE != FWD;
+  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes, kBBytes = C::kBBytes;
   constexpr int kElems = E4M3 ? 128 : 64;        // reduction elements in 128 bytes
-  constexpr int kTileN = GATED ? 128 : 256;      // output columns of a tile
+  constexpr int kTileN = GATED ? BN / 2 : BN;    // output columns of a tile
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
@@ -156,11 +172,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     ptx::mbar_init(&drain, 1);
     ptx::mbar_init_fence();
     abort_flag = 0;
-    ptx::prefetch_tmap(&a.mA);
-    ptx::prefetch_tmap(&a.mB);
+    ptx::prefetch_tmap(&a.p[0].mA);
+    ptx::prefetch_tmap(&a.p[0].mB);
   }
   if (warp == 1) {
-    ptx::tmem_alloc_pair(&tmem_slot, 512);
+    ptx::tmem_alloc_pair(&tmem_slot, 2 * BN);
     ptx::tmem_relinquish_pair();
     ptx::tc_fence_before();
   }
@@ -172,15 +188,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   ptx::pdl_launch_dependents();
   if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
 
-  const int total = a.m_tiles * a.n_tiles, first = blockIdx.x / 2, step = gridDim.x / 2;
-  const int nkb = (a.K + kElems - 1) / kElems;  // blocks of 128 bytes
-  // tile t: groups of `group` row tiles, columns outer, rows inner
-  auto tile = [&](int t, int& m0, int& n0) {
-    const int per = a.group * a.n_tiles, g = t / per, r = t - g * per;
-    const int rows = min(a.group, a.m_tiles - g * a.group);
+  const int total0 = a.p[0].m_tiles * a.p[0].n_tiles;
+  const int total = total0 + (MODE == GRAD ? a.p[1].m_tiles * a.p[1].n_tiles : 0);
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  // tile t's product, and its place: groups of `group` row tiles, columns outer, rows inner
+  auto tile = [&](int t, int& m0, int& n0) -> const GemmShape& {
+    const bool second = MODE == GRAD && t >= total0;
+    const GemmShape& p = a.p[second ? 1 : 0];
+    if (second) t -= total0;
+    const int per = p.group * p.n_tiles, g = t / per, r = t - g * per;
+    const int rows = min(p.group, p.m_tiles - g * p.group);
     const int n = r / rows;
-    m0 = (g * a.group + r - n * rows) * 256;
+    m0 = (g * p.group + r - n * rows) * 256;
     n0 = n * kTileN;
+    return p;
   };
 
   if (warp == 0 || warp == kEpiWarps + 2) {
@@ -188,17 +209,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     const bool copies_a = warp == 0;
     const uint64_t pol = ptx::l2_policy_evict_normal();
     const bool one = ptx::elect_one();
-    const bool mn = copies_a ? kMnA : kMnB, wide = copies_a ? a.wideA : a.wideB;
-    const CUtensorMap* map = copies_a ? &a.mA : &a.mB;
-    uint8_t* base = ring + (copies_a ? 0 : kOperandBytes);
+    uint8_t* base = ring + (copies_a ? 0 : kABytes);
+    constexpr int kBRows = BN / 2;  // of a CTA
     const uint32_t full0 = ptx::mapa(&full[0], 0);
     uint32_t it = 0, st = 0, par = 1;
     bool ok = true;
     for (int t = first; t < total && ok && !abort_flag; t += step) {
       int m0, n0;
-      tile(t, m0, n0);
+      const GemmShape& p = tile(t, m0, n0);
+      const int nkb = (p.K + kElems - 1) / kElems;  // blocks of 128 bytes
+      const bool mn = MODE == GRAD && (!copies_a || p.along), wide = copies_a ? p.wideA : p.wideB;
+      const CUtensorMap* map = copies_a ? &p.mA : &p.mB;
       // this CTA's first row (or column) of the operand
-      const int r0 = copies_a ? m0 + 128 * rank : GATED ? n0 + rank * a.N : n0 + 128 * rank;
+      const int r0 = copies_a ? m0 + 128 * rank : GATED ? n0 + rank * p.N : n0 + kBRows * rank;
+      const int block = copies_a ? 128 * 128 : kBRows * 128;  // bytes of a block, or of a chunk of 64 columns
       for (int kb = 0; kb < nkb; kb += 2, ++it) {
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
@@ -208,8 +232,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         if (one) {
           if (copies_a && rank == 0) {
             // an operand's second block is counted where a box brings it, even from outside
-            const uint32_t as = kMnA || a.wideA || !half ? kOperandBytes : kOperandBytes / 2;
-            const uint32_t bs = kMnB || a.wideB || !half ? kOperandBytes : kOperandBytes / 2;
+            const uint32_t as = (MODE == GRAD && p.along) || p.wideA || !half ? kABytes : kABytes / 2;
+            const uint32_t bs = kMnB || p.wideB || !half ? kBBytes : kBBytes / 2;
             ptx::mbar_arrive_expect_tx(&full[st], 2 * (as + bs));
           }
           if (mn) {  // chunks of 64 columns x 128 k
@@ -217,14 +241,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
               ptx::tma_load_3d_to_leader(dst, map, bar, 0, kb * 64, r0 / 64, pol);
             } else {
               ptx::tma_load_2d_to_leader(dst, map, bar, r0, kb * 64, pol);
-              ptx::tma_load_2d_to_leader(dst + 16384, map, bar, r0 + 64, kb * 64, pol);
+              if (copies_a || kBRows > 64) ptx::tma_load_2d_to_leader(dst + 16384, map, bar, r0 + 64, kb * 64, pol);
             }
-          } else {   // blocks of 128 bytes x 128 rows
+          } else {   // blocks of 128 bytes
             if (wide) {
               ptx::tma_load_3d_to_leader(dst, map, bar, 0, r0, kb, pol);
             } else {
               ptx::tma_load_2d_to_leader(dst, map, bar, kb * kElems, r0, pol);
-              if (!half) ptx::tma_load_2d_to_leader(dst + 16384, map, bar, (kb + 1) * kElems, r0, pol);
+              if (!half) ptx::tma_load_2d_to_leader(dst + block, map, bar, (kb + 1) * kElems, r0, pol);
             }
           }
         }
@@ -251,32 +275,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     if (rank == 0) {
       const uint32_t ring0 = __shfl_sync(0xffffffffu, ptx::smem_u32(ring), 0);
       const bool one = ptx::elect_one();  // the lane whose MMAs its commits cover
-      constexpr uint32_t idesc = (E4M3 ? ptx::idesc_e4m3_f32(256, 256) : ptx::idesc_bf16_f32(256, 256)) |
-                                 (kMnA ? ptx::kIdescAMn : 0) | (kMnB ? ptx::kIdescBMn : 0);
+      constexpr uint32_t kIdesc = (E4M3 ? ptx::idesc_e4m3_f32(256, BN) : ptx::idesc_bf16_f32(256, BN)) |
+                                  (kMnB ? ptx::kIdescBMn : 0);
       uint32_t st = 0, par = 0, acc = 0;
       for (int t = first; t < total && ok && !abort_flag; t += step, ++acc) {
         const uint32_t buf = acc & 1, use = acc >> 1;
+        int m0, n0;
+        const GemmShape& p = tile(t, m0, n0);
+        const int nkb = (p.K + kElems - 1) / kElems;
+        const bool along = MODE == GRAD && p.along;
+        const uint32_t idesc = kIdesc | (along ? ptx::kIdescAMn : 0);
         ok = ptx::mbar_wait_bounded_cluster(&tempty[buf], (use & 1) ^ 1, kWaitNs) && !abort_flag;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + buf * 256;
+        const uint32_t d = tmem + buf * BN;
         for (int kb = 0; kb < nkb; kb += 2) {
           ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full[st], par, kWaitNs));
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t sA = ring0 + st * kStageBytes, sB = sA + kOperandBytes;
-          const uint64_t dA = kMnA ? ptx::smem_desc_mn128(sA, 16384) : ptx::smem_desc_k128(sA);
+          const uint32_t sA = ring0 + st * kStageBytes, sB = sA + kABytes;
+          const uint64_t dA = along ? ptx::smem_desc_mn128(sA, 16384) : ptx::smem_desc_k128(sA);
           const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, 16384) : ptx::smem_desc_k128(sB);
           // 32 bytes of the reduction at a time; the last stage's steps that hold none of it are left out
-          const int steps = (a.K - kb * kElems + kElems / 4 - 1) / (kElems / 4);
+          const int steps = (p.K - kb * kElems + kElems / 4 - 1) / (kElems / 4);
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
             if (s >= steps) break;
             if (!one) continue;
             // along the reduction: 32 bytes of a block's rows; across it: 16 rows of 128 bytes
-            const uint64_t kk = (uint64_t)(s / 4 * 16384 + s % 4 * 32) >> 4, mn = (uint64_t)(s * 2048) >> 4;
-            const uint64_t oA = kMnA ? mn : kk, oB = kMnB ? mn : kk;
+            const uint64_t mn = (uint64_t)(s * 2048) >> 4;
+            const uint64_t oA = along ? mn : (uint64_t)(s / 4 * 16384 + s % 4 * 32) >> 4;
+            const uint64_t oB = kMnB ? mn : (uint64_t)(s / 4 * (kBBytes / 2) + s % 4 * 32) >> 4;
             if (E4M3) ptx::umma_e4m3_pair(d, dA + oA, dB + oB, idesc, kb || s);
             else ptx::umma_bf16_pair(d, dA + oA, dB + oB, idesc, kb || s);
           }
@@ -323,20 +353,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     bool ok = true;
     for (int t = first; t < total; t += step, ++acc) {
       int m0, n0;
-      tile(t, m0, n0);
+      const GemmShape& p = tile(t, m0, n0);
       const uint32_t buf = acc & 1, use = acc >> 1;
       const int row0 = m0 + 128 * rank + 32 * quarter, row = row0 + lane;
-      const bool in = row < a.M;
+      const bool in = row < p.M;
       float xs = 1.0f;
       if (E4M3 && in) xs = e.Xs[row];
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
       if (!ok) break;
       ptx::tc_fence_after();
-      const uint32_t d = tmem + buf * 256 + lanes;
+      const uint32_t d = tmem + buf * BN + lanes;
 #pragma unroll 1
       for (int i = 0; i < kTileN / 64; ++i) {
-        const int at = half * (kTileN / 2) + 32 * i, c = n0 + at, left = a.N - c;  // columns from c on
-        if (left <= 0 || row0 >= a.M) break;
+        const int at = half * (kTileN / 2) + 32 * i, c = n0 + at, left = p.N - c;  // columns from c on
+        if (left <= 0 || row0 >= p.M) break;
         float z[32], u[GATED ? 32 : 1];
         {
           uint32_t v[32];
@@ -347,7 +377,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         }
         if (GATED) {
           uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(d + 128 + at, v);
+          ptx::tmem_ld_32x32b_x32(d + BN / 2 + at, v);
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 32; ++j) u[j % (GATED ? 32 : 1)] = __uint_as_float(v[j]);
@@ -357,11 +387,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           for (int j = 0; j < 32; j += 8) {
             if (j >= left) break;
             finish8<E4M3>(e, xs, 0, c + j, z + j);
-            if (GATED) finish8<E4M3>(e, xs, a.N, c + j, u + (GATED ? j : 0));
+            if (GATED) finish8<E4M3>(e, xs, p.N, c + j, u + (GATED ? j : 0));
           }
           if (e.Zq && in) {
-            store_checkpoint(e, z, left, row, 0, GATED ? 2 : 1, a.N, c);
-            if (GATED) store_checkpoint(e, reinterpret_cast<const float(&)[32]>(u), left, row, 1, 2, a.N, c);
+            store_checkpoint(e, z, left, row, 0, GATED ? 2 : 1, p.N, c);
+            if (GATED) store_checkpoint(e, reinterpret_cast<const float(&)[32]>(u), left, row, 1, 2, p.N, c);
           }
           if (GATED) {
 #pragma unroll
@@ -375,7 +405,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             for (int j = 0; j < 32; j += 8) {
               if (j >= left) break;
               float f[8];
-              load8(e.R + (int64_t)row * a.N + c + j, f);
+              load8(e.R + (int64_t)row * p.N + c + j, f);
 #pragma unroll
               for (int k = 0; k < 8; ++k) z[j + k] += f[k];
             }
@@ -396,7 +426,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          ptx::tma_store_2d(&a.mO, block, c, row0);
+          ptx::tma_store_2d(&p.mO, block, c, row0);
           ptx::bulk_commit_group();
         }
         ++blocks;
@@ -405,10 +435,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&tempty[buf]);
     }
-    if (lane == 0) ptx::bulk_wait_group_all();  // the stores still read this warp's blocks
+    if (lane == 0) ptx::bulk_wait_group_read<0>();  // the stores still read this warp's blocks
     if (!ok && lane == 0) {
       abort_flag = 1;
       *a.err = (int32_t)kErrWait;
+    }
+    __syncwarp();
+  } else if (MODE == GRAD && a.part) {
+    // ------------------------------------------------------------ dbias: 32 columns at a time, rows in order
+    for (int c = blockIdx.x * 32 + lane; c < a.part_cols; c += gridDim.x * 32) {
+      float sum = 0.0f;
+#pragma unroll 8
+      for (int r = 0; r < a.part_rows; ++r) sum += a.part[(int64_t)r * a.part_cols + c];
+      a.sums[c] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
     }
     __syncwarp();
   }
@@ -417,7 +456,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
   ptx::cluster_sync();  // both CTAs are done with the pair's TMEM and barriers
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc_pair(tmem, 512);
+    ptx::tmem_dealloc_pair(tmem, 2 * BN);
   }
 }
 

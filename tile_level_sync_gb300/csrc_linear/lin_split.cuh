@@ -22,6 +22,12 @@
 namespace cusync {
 namespace ptx {
 
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -43,18 +49,20 @@ struct SplitArgs {
   int32_t cols, row_tiles;  // MMA columns (output rows) of a tile: 16, 32, 64 or 128; tiles of them
   int32_t splits;        // CTAs of a cluster, at most the reduction's stages
   int32_t stages;        // of the ring
+  int32_t blocks;        // of 128 bytes of the reduction in a stage: 1 or 2
   int32_t wideA, wideB;
 };
 
 constexpr int kSplitThreads = 256;
-constexpr int kMaxStages = 6;
-inline int split_stage_bytes(int cols) { return kOperandBytes + cols * 256; }
+constexpr int kMaxStages = 8;
+__host__ __device__ constexpr int split_stage_bytes(int cols, int blocks) { return blocks * (128 + cols) * 128; }
 
 template <int MODE, bool E4M3, bool GATED>
 __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr bool kMnA = MODE != FWD, kMnB = MODE == DW;
   constexpr int kElems = E4M3 ? 128 : 64;
   constexpr int kFeatures = GATED ? 64 : 128;
+  constexpr bool kAhead = MODE != DW;            // A is the weights
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull, drain;
@@ -84,16 +92,28 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
 
   const int t = blockIdx.x / splits;
   const int f0 = t / a.row_tiles * kFeatures, r0 = t % a.row_tiles * a.cols;
   const int nkb = (a.K + kElems - 1) / kElems;
-  const int all = (nkb + 1) / 2;  // stages of the whole reduction; this CTA's:
+  const int blocks = a.blocks, all = (nkb + blocks - 1) / blocks;  // stages of the whole reduction; this CTA's:
   const int s0 = (int)((int64_t)all * rank / splits), s1 = (int)((int64_t)all * (rank + 1) / splits);
-  const int stage_bytes = kOperandBytes + a.cols * 256, b_bytes = a.cols * 256;
+  const int a_bytes = blocks * 128 * 128, b_bytes = blocks * a.cols * 128, stage_bytes = a_bytes + b_bytes;
+  // where a stage's block b begins, and an "along" operand's second chunk of 64 columns
+  const int b_step = a.cols * 128, chunk = blocks * 64 * 128;
+
+  // Weights are on their way into the L2 while the kernel before this one ends.
+  if (kAhead && threadIdx.x == 0) {
+    for (int s = s0; s < min(s1, s0 + a.stages); ++s) {
+      const int kb = s * blocks;
+      if (GATED && a.wideA) ptx::tma_prefetch_4d(&a.mA, 0, f0, 0, kb);
+      else if (MODE == FWD && a.wideA) ptx::tma_prefetch_3d(&a.mA, 0, f0, kb);
+      else if (MODE == DX && a.wideA) ptx::tma_prefetch_3d(&a.mA, 0, kb * 64, f0 / 64);
+    }
+  }
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
   bool ok = true;
 
   if (warp == 0 || warp == 2) {
@@ -105,13 +125,13 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     for (int s = s0; s < s1; ++s, ++it) {
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&empty[st], par, kWaitNs));
       if (!ok || abort_flag) break;
-      const int kb = 2 * s;
-      const bool half = kb + 1 == nkb;
+      const int kb = s * blocks;
+      const bool half = blocks == 2 && kb + 1 == nkb;  // the stage's second block holds nothing
       uint8_t* sA = ring + st * stage_bytes;
-      uint8_t* sB = sA + kOperandBytes;
+      uint8_t* sB = sA + a_bytes;
       uint64_t* bar = &full[st];
       if (one && copies_a) {
-        const uint32_t as = kMnA || a.wideA || !half ? kOperandBytes : kOperandBytes / 2;
+        const uint32_t as = kMnA || a.wideA || !half ? a_bytes : a_bytes / 2;
         const uint32_t bs = kMnB || a.wideB || !half ? b_bytes : b_bytes / 2;
         ptx::mbar_arrive_expect_tx(bar, as + bs);
         if (kMnA) {
@@ -119,20 +139,16 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
             ptx::tma_load_3d(sA, &a.mA, bar, 0, kb * 64, f0 / 64, pol);
           } else {
             ptx::tma_load_2d(sA, &a.mA, bar, f0, kb * 64, pol);
-            ptx::tma_load_2d(sA + 16384, &a.mA, bar, f0 + 64, kb * 64, pol);
-          }
-        } else if (GATED) {
-          if (a.wideA) {
-            ptx::tma_load_4d(sA, &a.mA, bar, 0, f0, 0, kb, pol);
-          } else {
-            ptx::tma_load_3d(sA, &a.mA, bar, kb * kElems, f0, 0, pol);
-            if (!half) ptx::tma_load_3d(sA + 16384, &a.mA, bar, (kb + 1) * kElems, f0, 0, pol);
+            ptx::tma_load_2d(sA + chunk, &a.mA, bar, f0 + 64, kb * 64, pol);
           }
         } else if (a.wideA) {
-          ptx::tma_load_3d(sA, &a.mA, bar, 0, f0, kb, pol);
+          if (GATED) ptx::tma_load_4d(sA, &a.mA, bar, 0, f0, 0, kb, pol);
+          else ptx::tma_load_3d(sA, &a.mA, bar, 0, f0, kb, pol);
         } else {
-          ptx::tma_load_2d(sA, &a.mA, bar, kb * kElems, f0, pol);
-          if (!half) ptx::tma_load_2d(sA + 16384, &a.mA, bar, (kb + 1) * kElems, f0, pol);
+          for (int b = 0; b < (half ? 1 : blocks); ++b) {
+            if (GATED) ptx::tma_load_3d(sA + b * 16384, &a.mA, bar, (kb + b) * kElems, f0, 0, pol);
+            else ptx::tma_load_2d(sA + b * 16384, &a.mA, bar, (kb + b) * kElems, f0, pol);
+          }
         }
       }
       if (one && !copies_a) {
@@ -141,13 +157,13 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
             ptx::tma_load_3d(sB, &a.mB, bar, 0, kb * 64, r0 / 64, pol);
           } else {
             ptx::tma_load_2d(sB, &a.mB, bar, r0, kb * 64, pol);
-            if (a.cols > 64) ptx::tma_load_2d(sB + 16384, &a.mB, bar, r0 + 64, kb * 64, pol);
+            if (a.cols > 64) ptx::tma_load_2d(sB + chunk, &a.mB, bar, r0 + 64, kb * 64, pol);
           }
         } else if (a.wideB) {
           ptx::tma_load_3d(sB, &a.mB, bar, 0, r0, kb, pol);
         } else {
-          ptx::tma_load_2d(sB, &a.mB, bar, kb * kElems, r0, pol);
-          if (!half) ptx::tma_load_2d(sB + b_bytes / 2, &a.mB, bar, (kb + 1) * kElems, r0, pol);
+          for (int b = 0; b < (half ? 1 : blocks); ++b)
+            ptx::tma_load_2d(sB + b * b_step, &a.mB, bar, (kb + b) * kElems, r0, pol);
         }
       }
       __syncwarp();
@@ -174,17 +190,17 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full[st], par, kWaitNs));
       if (!ok || abort_flag) break;
       ptx::tc_fence_after();
-      const uint32_t sA = ring0 + st * stage_bytes, sB = sA + kOperandBytes;
-      const uint64_t dA = kMnA ? ptx::smem_desc_mn128(sA, 16384) : ptx::smem_desc_k128(sA);
-      const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, 16384) : ptx::smem_desc_k128(sB);
-      const int steps = (a.K - 2 * s * kElems + kElems / 4 - 1) / (kElems / 4);
+      const uint32_t sA = ring0 + st * stage_bytes, sB = sA + a_bytes;
+      const uint64_t dA = kMnA ? ptx::smem_desc_mn128(sA, chunk) : ptx::smem_desc_k128(sA);
+      const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, chunk) : ptx::smem_desc_k128(sB);
+      const int steps = min(4 * blocks, (a.K - blocks * s * kElems + kElems / 4 - 1) / (kElems / 4));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (i >= steps) break;
         if (!one) continue;
         const uint64_t mn = (uint64_t)(i * 2048) >> 4;
         const uint64_t oA = kMnA ? mn : (uint64_t)(i / 4 * 16384 + i % 4 * 32) >> 4;
-        const uint64_t oB = kMnB ? mn : (uint64_t)(i / 4 * (b_bytes / 2) + i % 4 * 32) >> 4;
+        const uint64_t oB = kMnB ? mn : (uint64_t)(i / 4 * b_step + i % 4 * 32) >> 4;
         if (E4M3) ptx::umma_e4m3(tmem, dA + oA, dB + oB, idesc, s > s0 || i);
         else ptx::umma_bf16(tmem, dA + oA, dB + oB, idesc, s > s0 || i);
       }
@@ -206,6 +222,18 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   }
 
   // ------------------------------------------------------------ exchange
+  // A thread finishes the same 8 features of all its tokens: their scales and biases, while the product runs.
+  constexpr int kGroups = kFeatures / 8;
+  const Epilogue& e = a.e;
+  const int group = threadIdx.x % kGroups, c = f0 + group * 8;
+  float ws[GATED ? 2 : 1][8], bs[GATED ? 2 : 1][8];
+#pragma unroll
+  for (int g = 0; g < (GATED ? 2 : 1); ++g) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ws[g][j] = 1.0f, bs[g][j] = 0.0f;
+    if (E4M3 && c < a.N) load8(e.Ws + (int64_t)g * a.N + c, ws[g]);
+    if (MODE == FWD && e.bias && c < a.N) load8(e.bias + (int64_t)g * a.N + c, bs[g]);
+  }
   ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull, 0, 2 * kWaitNs)) && ok;
   if (!ok) {
     abort_flag = 1;
@@ -215,16 +243,15 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   // every CTA's MMAs have read its ring, which now takes [splits][cols / splits][128] sums
   __syncthreads();
   if (splits > 1) ptx::cluster_sync();
-  const int per = a.cols / splits;
+  const int per = a.cols / splits, shift = 31 - __clz(per);
   {
     const int quarter = warp & 3, m = 32 * quarter + lane, width = a.cols / 2, c0 = (warp >> 2) * width;
     const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16);
-    float* own = reinterpret_cast<float*>(ring);
+    float* own = reinterpret_cast<float*>(ring) + m;
+    float* mine = own + rank * per * 128;  // this CTA's sums, wherever they go
     auto put = [&](int n, uint32_t v) {
-      const int to = n / per;
-      float* p = own + ((rank * per + n - to * per) * 128 + m);
-      if (splits > 1) ptx::st_cluster_u32(ptx::mapa(p, to), v);
-      else *p = __uint_as_float(v);
+      if (splits > 1) ptx::st_cluster_u32(ptx::mapa(mine + (n & (per - 1)) * 128, n >> shift), v);
+      else own[n * 128] = __uint_as_float(v);
     };
     if (width >= 32) {
 #pragma unroll 1
@@ -251,18 +278,17 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   if (splits > 1) ptx::cluster_sync();
 
   // ------------------------------------------------------------ finish: 8 features of a token a thread
-  constexpr int kGroups = kFeatures / 8;
-  const Epilogue& e = a.e;
   const float* sums = reinterpret_cast<const float*>(ring);
-  for (int i = threadIdx.x; i < (per * kGroups + 31) / 32 * 32; i += kSplitThreads) {
-    const int tok = i / kGroups, c = f0 + i % kGroups * 8, row = r0 + rank * per + tok;
+#pragma unroll 2
+  for (int tok = threadIdx.x / kGroups; tok < max(per, 32 / kGroups); tok += kSplitThreads / kGroups) {
+    const int row = r0 + rank * per + tok;
     const bool in = tok < per && row < a.M && c < a.N;
     float z[8], u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = u[j] = 0.0f;
     if (in) {
       for (int s = 0; s < splits; ++s) {
-        const float* p = sums + (s * per + tok) * 128 + i % kGroups * 8;
+        const float* p = sums + (s * per + tok) * 128 + group * 8;
         float f[8];
         load8(p, f);
 #pragma unroll
@@ -277,8 +303,11 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     if (MODE == FWD) {
       if (in) {
         const float xs = E4M3 ? e.Xs[row] : 1.0f;
-        finish8<E4M3>(e, xs, 0, c, z);
-        if (GATED) finish8<E4M3>(e, xs, a.N, c, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          z[j] = E4M3 ? z[j] * (xs * ws[0][j]) + bs[0][j] : z[j] + bs[0][j];
+          if (GATED) u[j] = E4M3 ? u[j] * (xs * ws[GATED][j]) + bs[GATED][j] : u[j] + bs[GATED][j];
+        }
       }
       if (e.Zq) {  // four neighbours share a block
         auto put = [&](const float (&v)[8], int part) {

@@ -73,11 +73,19 @@ cudaError_t prepare_kernel(const void* f, int smem) {
   cudaFuncAttributes fa;  // loads the kernel now, not at a launch inside a capture
   return cudaFuncGetAttributes(&fa, f);
 }
+template <int MODE, bool E4M3, bool GATED, int BN>
+cudaError_t prepare_gemm() {
+  return prepare_kernel(reinterpret_cast<const void*>(&gemm_kernel<MODE, E4M3, GATED, BN>), GemmCfg<BN>::kSmem);
+}
 template <int MODE, bool E4M3, bool GATED>
-cudaError_t prepare_product() {
-  const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(&gemm_kernel<MODE, E4M3, GATED>), kGemmSmem);
-  if (e != cudaSuccess) return e;
+cudaError_t prepare_split() {
   return prepare_kernel(reinterpret_cast<const void*>(&split_kernel<MODE, E4M3, GATED>), kSmemPerSm - 1024);
+}
+template <bool E4M3, bool GATED>
+cudaError_t prepare_forward() {
+  cudaError_t e = prepare_gemm<FWD, E4M3, GATED, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<FWD, E4M3, GATED, 128>();
+  return e == cudaSuccess ? prepare_split<FWD, E4M3, GATED>() : e;
 }
 
 // The current device: the attributes set of the kernels that need some, the descriptor encoder
@@ -100,12 +108,14 @@ cusync_status_t prepare_device(int* sms) {
   }
   int n = 0;
   cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = prepare_product<FWD, false, false>();
-  if (e == cudaSuccess) e = prepare_product<FWD, false, true>();
-  if (e == cudaSuccess) e = prepare_product<FWD, true, false>();
-  if (e == cudaSuccess) e = prepare_product<FWD, true, true>();
-  if (e == cudaSuccess) e = prepare_product<DX, false, false>();
-  if (e == cudaSuccess) e = prepare_product<DW, false, false>();
+  if (e == cudaSuccess) e = prepare_forward<false, false>();
+  if (e == cudaSuccess) e = prepare_forward<false, true>();
+  if (e == cudaSuccess) e = prepare_forward<true, false>();
+  if (e == cudaSuccess) e = prepare_forward<true, true>();
+  if (e == cudaSuccess) e = prepare_gemm<GRAD, false, false, 256>();
+  if (e == cudaSuccess) e = prepare_gemm<GRAD, false, false, 128>();
+  if (e == cudaSuccess) e = prepare_split<DX, false, false>();
+  if (e == cudaSuccess) e = prepare_split<DW, false, false>();
   if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
   g_sms[dev].store(n, std::memory_order_release);
   *sms = n;
@@ -131,27 +141,28 @@ bool map_nd(CUtensorMap* m, const void* p, int bytes, CUtensorMapSwizzle swizzle
 }
 
 // An operand [rows, cols] whose columns are the reduction's: boxes of 128 bytes x box_rows; wide (columns a
-// multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of two blocks.
-bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int box_rows, int32_t* wide) {
+// multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of `blocks`.
+bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int box_rows, int blocks,
+              int32_t* wide) {
   const int n = 128 / bytes;
   *wide = cols % n == 0;
-  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {cols, n}, {n, box_rows, 2})
+  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {cols, n}, {n, box_rows, blocks})
                : map_nd<2>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {n, box_rows});
 }
 // Gate and up rows of a gated layer's weights [2][rows, cols], 64 of each in a box.
-bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int32_t* wide) {
+bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int blocks, int32_t* wide) {
   const int n = 128 / bytes;
   *wide = cols % n == 0;
   return *wide ? map_nd<4>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, 2, cols / n}, {cols, rows * cols, n},
-                           {n, 64, 2, 2})
+                           {n, 64, 2, blocks})
                : map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows, 2}, {cols, rows * cols}, {n, 64, 2});
 }
-// A bf16 operand [rows, cols] whose rows are the reduction's: boxes of 64 columns x 128 rows; wide (columns a
-// multiple of 64): as [chunks][rows][64], boxes of `chunks`.
-bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int chunks, int32_t* wide) {
+// A bf16 operand [rows, cols] whose rows are the reduction's: boxes of 64 columns x `box_rows` rows; wide (columns
+// a multiple of 64): as [chunks][rows][64], boxes of `chunks`.
+bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows, int chunks, int32_t* wide) {
   *wide = cols % 64 == 0;
-  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {cols, 64}, {64, 128, chunks})
-               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {64, 128});
+  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {cols, 64}, {64, box_rows, chunks})
+               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {64, box_rows});
 }
 // An output [rows, cols]: boxes of 32 x 32 as a warp's lanes write them.
 bool map_output(CUtensorMap* m, void* p, int64_t rows, int64_t cols) {
@@ -167,64 +178,51 @@ struct Product {
   const void *P, *Q;
   int64_t rows, cols, depth;
   Epilogue e;
-  int32_t* err;
-  bool clear;
 };
 
-// How a product is computed: on CTA pairs, or (cols > 0) on clusters of `splits` CTAs.
+// How products are computed: on CTA pairs with tiles of 256 x `bn` (SwiGLU: bn / 2 columns of Y), or (bn = 0) on
+// clusters of `splits` CTAs with tiles of 128 (64) columns x `cols` rows; and about how long it takes.
 struct Plan {
-  int cols, splits, stages;
+  double us;
+  int bn, cols, splits, stages, blocks;
 };
+
+Plan pair_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems, bool gated) {
+  Plan best = {1e30, 0, 0, 0, 0, 0};
+  if (sms < 2) return best;
+  for (int bn = 128; bn <= 256; bn += 128) {
+    const int64_t tiles = div_up(rows, 256) * div_up(cols, gated ? bn / 2 : bn);
+    const double us = 4.2 + (double)div_up(tiles, sms / 2) * (0.5 + (bn == 256 ? 0.30 : 0.19) * (double)div_up(depth, elems));
+    if (us < best.us) best = {us, bn, 0, 0, 0, 0};
+  }
+  return best;
+}
 
 template <int MODE, bool GATED>
-Plan choose(const Product& p, int sms, int elems) {
-  const int64_t pair_tiles = div_up(p.rows, 256) * div_up(p.cols, GATED ? 128 : 256);
-  if (sms >= 2 && pair_tiles >= 38) return {0, 0, 0};
-  Plan r;
+Plan split_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems) {
+  Plan r = {1e30, 0, 0, 0, 0, 2};
   r.cols = MODE == DW ? 64 : 16;
-  while (r.cols < 128 && r.cols < p.rows) r.cols *= 2;
-  const int stage = split_stage_bytes(r.cols);
+  while (r.cols < 128 && r.cols < rows) r.cols *= 2;
+  const int stage = split_stage_bytes(r.cols, r.blocks);
   // two CTAs an SM where three stages of both fit
   const int resident = 2 * (3 * stage + 2048) <= kSmemPerSm ? 2 : 1;
   r.stages = std::min(kMaxStages, (kSmemPerSm / resident - 2048) / stage);
-  const int64_t tiles = div_up(p.rows, r.cols) * div_up(p.cols, GATED ? 64 : 128);
-  const int64_t steps = div_up(p.depth, 2 * elems);
+  const int64_t tiles = div_up(rows, r.cols) * div_up(cols, GATED ? 64 : 128);
+  const int64_t steps = div_up(depth, r.blocks * elems);
   r.splits = 1;
   while (r.splits < 8 && 2 * r.splits * tiles <= (int64_t)sms * resident && 2 * r.splits <= steps) r.splits *= 2;
+  r.us = 6.0 + (double)div_up(tiles * r.splits, (int64_t)sms * resident) * 0.27 * (double)div_up(depth, elems * r.splits);
   return r;
 }
 
 template <int MODE, bool E4M3, bool GATED>
-cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
+cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool clear, cudaStream_t s) {
   constexpr int bytes = E4M3 ? 1 : 2;
-  const Plan plan = choose<MODE, GATED>(p, sms, 128 / bytes);
-  if (!plan.cols) {
-    GemmArgs a;
-    std::memset(&a, 0, sizeof(a));
-    a.e = p.e;
-    a.err = p.err;
-    a.clear = p.clear;
-    a.M = (int32_t)p.rows;
-    a.N = (int32_t)p.cols;
-    a.K = (int32_t)p.depth;
-    a.m_tiles = (int32_t)div_up(p.rows, 256);
-    a.n_tiles = (int32_t)div_up(p.cols, GATED ? 128 : 256);
-    a.group = std::min(a.m_tiles, 8);
-    const bool ok = (MODE == DW ? map_along(&a.mA, p.P, p.depth, p.rows, 2, &a.wideA)
-                                : map_rows(&a.mA, p.P, bytes, p.rows, p.depth, 128, &a.wideA)) &&
-                    (MODE == FWD ? map_rows(&a.mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, 128, &a.wideB)
-                                 : map_along(&a.mB, p.Q, p.depth, p.cols, 2, &a.wideB)) &&
-                    map_output(&a.mO, p.e.out, p.rows, p.cols);
-    if (!ok) return cudaErrorInvalidValue;
-    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles;
-    const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
-    return launch_cluster(2, gemm_kernel<MODE, E4M3, GATED>, dim3(grid), kGemmThreads, kGemmSmem, s, a);
-  }
   SplitArgs a;
   std::memset(&a, 0, sizeof(a));
   a.e = p.e;
-  a.err = p.err;
-  a.clear = p.clear;
+  a.err = err;
+  a.clear = clear;
   a.M = (int32_t)p.rows;
   a.N = (int32_t)p.cols;
   a.K = (int32_t)p.depth;
@@ -232,15 +230,117 @@ cudaError_t launch_product(const Product& p, int sms, cudaStream_t s) {
   a.row_tiles = (int32_t)div_up(p.rows, plan.cols);
   a.splits = plan.splits;
   a.stages = plan.stages;
-  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, 2, &a.wideA)
-                   : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, &a.wideA)
-                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, 128, &a.wideA)) &&
-                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, plan.cols / 64, &a.wideB)
-                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, plan.cols, &a.wideB));
+  a.blocks = plan.blocks;
+  const int n = plan.blocks;
+  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, 64 * n, 2, &a.wideA)
+                   : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, n, &a.wideA)
+                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, 128, n, &a.wideA)) &&
+                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, 64 * n, plan.cols / 64, &a.wideB)
+                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, plan.cols, n, &a.wideB));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = div_up(p.cols, GATED ? 64 : 128) * a.row_tiles;
-  return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)),
-                        kSplitThreads, (size_t)plan.stages * split_stage_bytes(plan.cols) + 1024, s, a);
+  return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)), kSplitThreads,
+                        (size_t)plan.stages * split_stage_bytes(plan.cols, n) + 1024, s, a);
+}
+
+// A product on pairs; along: P's rows are the reduction's (dWt).  Q's are, too, in both gradients.
+template <bool E4M3, bool GATED, int BN>
+bool fill_shape(GemmShape* g, const Product& p, bool grad, bool along) {
+  constexpr int bytes = E4M3 ? 1 : 2;
+  g->M = (int32_t)p.rows;
+  g->N = (int32_t)p.cols;
+  g->K = (int32_t)p.depth;
+  g->m_tiles = (int32_t)div_up(p.rows, 256);
+  g->n_tiles = (int32_t)div_up(p.cols, GATED ? BN / 2 : BN);
+  g->group = std::min(g->m_tiles, 8);
+  g->along = along;
+  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, 128, 2, &g->wideA)
+                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, 128, 2, &g->wideA)) &&
+         (grad ? map_along(&g->mB, p.Q, p.depth, p.cols, 128, BN / 128, &g->wideB)
+               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, BN / 2, 2, &g->wideB)) &&
+         map_output(&g->mO, p.e.out, p.rows, p.cols);
+}
+template <int MODE, bool E4M3, bool GATED, int BN>
+cudaError_t launch_gemm(const GemmArgs& a, int sms, cudaStream_t s) {
+  const int64_t tiles = (int64_t)a.p[0].m_tiles * a.p[0].n_tiles + (int64_t)a.p[1].m_tiles * a.p[1].n_tiles;
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, sms / 2);
+  return launch_cluster(2, gemm_kernel<MODE, E4M3, GATED, BN>, dim3(grid), kGemmThreads, GemmCfg<BN>::kSmem, s, a);
+}
+
+template <bool E4M3, bool GATED>
+cudaError_t forward(const Product& p, int32_t* err, int sms, cudaStream_t s) {
+  constexpr int elems = E4M3 ? 128 : 64;
+  const Plan pair = pair_plan(p.rows, p.cols, p.depth, sms, elems, GATED);
+  const Plan split = split_plan<FWD, GATED>(p.rows, p.cols, p.depth, sms, elems);
+  if (split.us <= pair.us) return launch_split<FWD, E4M3, GATED>(split, p, err, true, s);
+  GemmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.e = p.e;
+  a.err = err;
+  a.clear = true;
+  if (pair.bn == 256)
+    return fill_shape<E4M3, GATED, 256>(&a.p[0], p, false, false) ? launch_gemm<FWD, E4M3, GATED, 256>(a, sms, s)
+                                                                  : cudaErrorInvalidValue;
+  return fill_shape<E4M3, GATED, 128>(&a.p[0], p, false, false) ? launch_gemm<FWD, E4M3, GATED, 128>(a, sms, s)
+                                                                : cudaErrorInvalidValue;
+}
+
+// dX and dWt (either may be NULL), and on pairs dbias's sums.
+struct Sums {
+  const float* part;
+  uint16_t* out;
+  int64_t rows, cols;
+};
+template <int BN>
+cudaError_t pair_gradients(const Product* dx, const Product* dw, const Sums& sums, int32_t* err, bool clear, int sms,
+                           cudaStream_t s) {
+  GemmArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.err = err;
+  a.clear = clear;
+  a.part = sums.part;
+  a.sums = sums.out;
+  a.part_rows = (int32_t)sums.rows;
+  a.part_cols = (int32_t)sums.cols;
+  const bool dw_first = dw && (!dx || dw->depth > dx->depth);
+  GemmShape *gx = &a.p[dw_first ? 1 : 0], *gw = &a.p[dw_first || !dx ? 0 : 1];
+  if ((dx && !fill_shape<false, false, BN>(gx, *dx, true, false)) || (dw && !fill_shape<false, false, BN>(gw, *dw, true, true)))
+    return cudaErrorInvalidValue;
+  return launch_gemm<GRAD, false, false, BN>(a, sms, s);
+}
+cudaError_t sum_columns(const Sums& sums, cudaStream_t s) {
+  return launch(column_sum_kernel, dim3((unsigned)div_up(sums.cols, 32)), 256, 0, s, sums.part, (int32_t)sums.rows,
+                (int32_t)sums.cols, sums.out);
+}
+cudaError_t gradients(const Product* dx, const Product* dw, const Sums& sums, int32_t* err, bool clear, int sms,
+                      cudaStream_t s) {
+  Plan px = {0}, pw = {0}, sx = {0}, sw = {0};
+  if (dx) {
+    px = pair_plan(dx->rows, dx->cols, dx->depth, sms, 64, false);
+    sx = split_plan<DX, false>(dx->rows, dx->cols, dx->depth, sms, 64);
+  }
+  if (dw) {
+    pw = pair_plan(dw->rows, dw->cols, dw->depth, sms, 64, false);
+    sw = split_plan<DW, false>(dw->rows, dw->cols, dw->depth, sms, 64);
+  }
+  const bool split_x = dx && sx.us <= px.us, split_w = dw && sw.us <= pw.us;
+  const bool pairs = (dx && !split_x) || (dw && !split_w);
+  cudaError_t e = cudaSuccess;
+  if (sums.part && !pairs) e = sum_columns(sums, s);
+  if (e == cudaSuccess && split_x) {
+    e = launch_split<DX, false, false>(sx, *dx, err, clear, s);
+    clear = false;
+  }
+  if (e == cudaSuccess && split_w) {
+    e = launch_split<DW, false, false>(sw, *dw, err, clear, s);
+    clear = false;
+  }
+  if (e == cudaSuccess && pairs) {
+    const Product *x = split_x ? nullptr : dx, *w = split_w ? nullptr : dw;
+    const int bn = x && w ? std::min(px.bn, pw.bn) : x ? px.bn : pw.bn;
+    e = bn == 256 ? pair_gradients<256>(x, w, sums, err, clear, sms, s) : pair_gradients<128>(x, w, sums, err, clear, sms, s);
+  }
+  return e;
 }
 
 cusync_status_t capture_or_ok(cudaStream_t s) {
@@ -296,11 +396,9 @@ cusync_status_t cusync_linear(const cusync_linear_desc_t* d, const void* X, cons
   p.e.Ze = Ze;
   p.e.out = static_cast<uint16_t*>(Y);
   p.e.act = d->act;
-  p.err = static_cast<int32_t*>(work);
-  p.clear = true;
-  return status_of(L.e4m3 ? (L.G == 2 ? launch_product<FWD, true, true>(p, sms, s) : launch_product<FWD, true, false>(p, sms, s))
-                          : (L.G == 2 ? launch_product<FWD, false, true>(p, sms, s)
-                                      : launch_product<FWD, false, false>(p, sms, s)));
+  int32_t* err = static_cast<int32_t*>(work);
+  return status_of(L.e4m3 ? (L.G == 2 ? forward<true, true>(p, err, sms, s) : forward<true, false>(p, err, sms, s))
+                          : (L.G == 2 ? forward<false, true>(p, err, sms, s) : forward<false, false>(p, err, sms, s)));
 }
 
 cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X, const float* Xs, const void* Wt,
@@ -349,38 +447,26 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
         : d->act == CUSYNC_LINEAR_RELU ? launch(dz_kernel<ACT_RELU>, grid, 256, 0, s, a)
         : d->act == CUSYNC_LINEAR_GELU ? launch(dz_kernel<ACT_GELU>, grid, 256, 0, s, a)
                                        : launch(dz_kernel<ACT_SWIGLU>, grid, 256, 0, s, a);
-    if (e == cudaSuccess && dbias)
-      e = launch(column_sum_kernel, dim3((unsigned)div_up(H, 32)), 256, 0, s, (const float*)a.part, (int32_t)L.dz_parts,
-                 (int32_t)H, static_cast<uint16_t*>(dbias));
   }
-  Product p = {};
-  p.P = dZ;
-  p.err = err;
-  if (e == cudaSuccess && dX) {
-    p.Q = Wt;
-    p.rows = L.M;
-    p.cols = L.K;
-    p.depth = H;
-    p.e.out = static_cast<uint16_t*>(dX);
-    p.clear = clear;
-    clear = false;
-    e = launch_product<DX, false, false>(p, sms, s);
+  if (e == cudaSuccess && dWt && L.e4m3) {
+    const int64_t pieces = L.M * (L.K / 16);
+    e = launch(rows_from_e4m3_kernel, dim3((unsigned)std::min<int64_t>(div_up(pieces, 256), (int64_t)sms * 16)), 256, 0, s,
+               static_cast<const uint4*>(X), Xs, reinterpret_cast<uint4*>(w + L.x), L.M, (int32_t)(L.K / 16));
   }
-  if (e == cudaSuccess && dWt) {
-    p.Q = X;
-    if (L.e4m3) {
-      p.Q = w + L.x;
-      const int64_t pieces = L.M * (L.K / 16);
-      e = launch(rows_from_e4m3_kernel, dim3((unsigned)std::min<int64_t>(div_up(pieces, 256), (int64_t)sms * 16)), 256, 0, s,
-                 static_cast<const uint4*>(X), Xs, reinterpret_cast<uint4*>(w + L.x), L.M, (int32_t)(L.K / 16));
-    }
-    p.rows = H;
-    p.cols = L.K;
-    p.depth = L.M;
-    p.e.out = static_cast<uint16_t*>(dWt);
-    p.clear = clear;
-    if (e == cudaSuccess) e = launch_product<DW, false, false>(p, sms, s);
-  }
+  Product dx = {}, dw = {};
+  dx.P = dw.P = dZ;
+  dx.Q = Wt;
+  dx.rows = L.M;
+  dx.cols = L.K;
+  dx.depth = H;
+  dx.e.out = static_cast<uint16_t*>(dX);
+  dw.Q = L.e4m3 ? w + L.x : X;
+  dw.rows = H;
+  dw.cols = L.K;
+  dw.depth = L.M;
+  dw.e.out = static_cast<uint16_t*>(dWt);
+  const Sums sums = {dbias ? reinterpret_cast<const float*>(w + L.part) : nullptr, static_cast<uint16_t*>(dbias), L.dz_parts, H};
+  if (e == cudaSuccess) e = gradients(dX ? &dx : nullptr, dWt ? &dw : nullptr, sums, err, clear, sms, s);
   return status_of(e);
 }
 
