@@ -75,9 +75,7 @@ cusync_status_t cusync_norm(const cusync_norm_desc_t* d, const void* X, const vo
 /* Gradients at S [M, D] (what cusync_norm wrote, or its X where it had no R) for dY [M, D]:
  * dX [M, D], which is R's gradient too, and dw [D] (NULL: not wanted).  dS [M, D] or NULL is the
  * gradient that reaches S along the residual path: it is added to dX, which may be dY or dS (that
- * buffer itself).  work (not read where dw is NULL): grad_work_bytes of scratch, of which the first
- * 256 are left as they are, so that a buffer shared with linear calls keeps their error word.
- * UNSUPPORTED for CUSYNC_NORM_NONE. */
+ * buffer itself).  work: grad_work_bytes of scratch.  UNSUPPORTED for CUSYNC_NORM_NONE. */
 cusync_status_t cusync_norm_grad(const cusync_norm_desc_t* d, const void* S, const void* w, const void* dY,
                                  const void* dS, void* work, void* dX, void* dw, cusync_stream_t stream);
 
@@ -137,8 +135,8 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
                                    const void* Zq, const uint8_t* Ze, const void* dY, void* work, void* dX,
                                    void* dWt, void* dbias, cusync_stream_t stream);
 
-/* Synchronise `stream` and read the error word of the last cusync_linear or cusync_linear_grad call
- * that used `work`: OK, or DEVICE if a device-internal wait gave up (the outputs of that call
+/* Synchronise `stream` and read the error word of the last cusync_linear, cusync_linear_grad or
+ * cusync_norm_grad call that used `work`: OK, or DEVICE if a device-internal wait gave up (the outputs of that call
  * are not valid).  code may be NULL.  UNSUPPORTED while the stream is being captured. */
 cusync_status_t cusync_linear_check(const void* work, cusync_stream_t stream, uint32_t* code);
 

@@ -149,7 +149,7 @@ def test_norm_grad_in_place_and_without_dw():
         n.run_grad(d["X"], d["w"], t["dY"], t["R"], work, t[into], again)
         assert torch.equal(t[into], dX) and torch.equal(again, dw)
     t = torch.empty_like(dX)
-    n.run_grad(d["X"], d["w"], d["dY"], d["R"], None, t, None)
+    n.run_grad(d["X"], d["w"], d["dY"], d["R"], work, t, None)
     assert torch.equal(t, dX)
     few = _norm(M, D, num_sms=3)
     few.run_grad(d["X"], d["w"], d["dY"], d["R"], work, t, again)

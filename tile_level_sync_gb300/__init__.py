@@ -468,33 +468,50 @@ class Chain:
 # ---------------------------------------------------------------- layers
 
 
-def _checked(want, tensors):
-    """Device addresses of the named arguments, the tensors among them checked against
-    ``want``: name -> (type, elements), or (None, bytes) for a buffer."""
-    out, device = [], None
-    for name, t in tensors.items():
+def _refuse(name, t, dtype, n):
+    """Raise what is wrong with the tensor t, of which n elements of dtype (None: n bytes of any
+    type) on the current device are needed."""
+    if dtype is None:
+        if t.nbytes < n:
+            raise ValueError(f"{name} holds {t.nbytes} bytes: {n} are needed")
+    elif t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}: {dtype} is needed")
+    elif t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements: {n} are needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
+
+
+_device = None  # index of torch's current device
+
+
+def _checked(want, *args):
+    """Device addresses of the arguments, the tensors among them checked against ``want``: for
+    each (name, type, elements), or (name, None, bytes) for a buffer."""
+    global _device
+    if _device is None:
+        import torch
+        # the call behind torch.cuda.current_device(), whose own start a CUDA tensor has made
+        _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    out, device = [], -2
+    for (name, dtype, n), t in zip(want, args):
         if t is None or isinstance(t, int):
             out.append(t)
             continue
-        dtype, n = want[name]
-        if dtype is None:
-            if t.numel() * t.element_size() < n:
-                raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes: {n} are needed")
-        elif t.dtype is not dtype:
-            raise ValueError(f"{name} is {t.dtype}: {dtype} is needed")
-        elif t.numel() != n:
-            raise ValueError(f"{name} has {t.numel()} elements: {n} are needed")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
-        if not t.is_cuda:
-            raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
-        if device is None:
-            import torch
-            device = torch.cuda.current_device()
-        if t.get_device() != device:
-            raise ValueError(f"{name} is on {t.device}: the current CUDA device is needed")
-        out.append(t.data_ptr())
+        if (t.numel() == n if t.dtype is dtype else dtype is None and t.nbytes >= n) and t.is_contiguous():
+            at = t.get_device()
+            if at >= 0 and device == -2:
+                device = _device()
+            if at == device:
+                out.append(t.data_ptr())
+                continue
+        _refuse(name, t, dtype, n)
     return out
+
+
+def _wants(table, names):
+    return tuple((name, *table[name]) for name in names.split())
 
 
 # ---------------------------------------------------------------- mixture of experts
@@ -548,7 +565,7 @@ class Moe:
         }
 
     def _ptrs(self, **tensors):
-        return _checked(self._want, tensors)
+        return _checked([(name, *self._want[name]) for name in tensors], *tensors.values())
 
     def route(self, logits, bias, ids, weights, stream=None):
         p = self._ptrs(logits=logits, bias=bias, ids=ids, weights=weights)
@@ -643,18 +660,31 @@ class Norm:
         self._lib = load()
         import torch
         bf16, n = torch.bfloat16, desc.M * desc.D
-        self._want = {k: (bf16, n) for k in ("X", "R", "S", "Y", "dY", "dS", "dX")}
-        self._want.update(w=(bf16, desc.D), dw=(bf16, desc.D), Q=(torch.float8_e4m3fn, n), Qs=(torch.float32, desc.M),
-                          work=(None, self.info.grad_work_bytes))
+        table = {k: (bf16, n) for k in ("X", "R", "S", "Y", "dY", "dS", "dX")}
+        table.update(w=(bf16, desc.D), dw=(bf16, desc.D), Q=(torch.float8_e4m3fn, n), Qs=(torch.float32, desc.M),
+                     work=(None, self.info.grad_work_bytes))
+        self._run, self._grad = _wants(table, "X R w S Y Q Qs"), _wants(table, "S w dY dS work dX dw")
 
     def run(self, X, R=None, w=None, S=None, Y=None, Q=None, Qs=None, stream=None):
         """S = X + R, and its norm in bf16 (Y), as 8-bit rows (Q, Qs), or both."""
-        p = _checked(self._want, dict(X=X, R=R, w=w, S=S, Y=Y, Q=Q, Qs=Qs))
+        p = _checked(self._run, X, R, w, S, Y, Q, Qs)
         _check(self._lib.cusync_norm(self._d, *p, _stream(stream)), "cusync_norm")
 
     def run_grad(self, S, w, dY, dS, work, dX, dw, stream=None):
-        p = _checked(self._want, dict(S=S, w=w, dY=dY, dS=dS, work=work, dX=dX, dw=dw))
+        p = _checked(self._grad, S, w, dY, dS, work, dX, dw)
         _check(self._lib.cusync_norm_grad(self._d, *p, _stream(stream)), "cusync_norm_grad")
+
+    def check(self, buffer, stream=None):
+        """(status, code) of the last run_grad that used a work buffer: OK or ERR_DEVICE."""
+        return _work_check(buffer, stream)
+
+
+def _work_check(buffer, stream):
+    code = c_u32()
+    st = load().cusync_linear_check(_ptr(buffer), _stream(stream), ctypes.byref(code))
+    if st not in (OK, ERR_DEVICE):
+        raise CusyncError(st, "cusync_linear_check")
+    return st, code.value
 
 
 class Linear:
@@ -673,29 +703,26 @@ class Linear:
         bf16, f8, f32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32
         M, K, N, H = desc.M, desc.K, desc.N, self.info.parts * desc.N
         wide = f8 if desc.dtype == LINEAR_E4M3 else bf16
-        self._want = {
+        table = {
             "X": (wide, M * K), "Xs": (f32, M), "Wt": (wide, H * K), "Ws": (f32, H), "bias": (bf16, H),
-            "R": (bf16, M * N), "Y": (bf16, M * N), "Zq": (f8, M * H), "Ze": (torch.uint8, M * self.info.parts * self.info.blocks),
-            "work": (None, self.info.work_bytes),
+            "R": (bf16, M * N), "Y": (bf16, M * N), "Zq": (f8, M * H),
+            "Ze": (torch.uint8, M * self.info.parts * self.info.blocks), "work": (None, self.info.work_bytes),
         }
-        self._want_grad = dict(self._want, Wt=(bf16, H * K), dY=(bf16, M * N), dX=(bf16, M * K), dWt=(bf16, H * K),
-                               dbias=(bf16, H), work=(None, self.info.grad_work_bytes))
+        self._run = _wants(table, "X Xs Wt Ws bias R work Y Zq Ze")
+        table.update(Wt=(bf16, H * K), dY=(bf16, M * N), dX=(bf16, M * K), dWt=(bf16, H * K), dbias=(bf16, H),
+                     work=(None, self.info.grad_work_bytes))
+        self._grad = _wants(table, "X Xs Wt Zq Ze dY work dX dWt dbias")
 
     def run(self, X, Wt, work, Y, Xs=None, Ws=None, bias=None, R=None, Zq=None, Ze=None, stream=None):
         """Y = act(X x W + bias) + R; Zq and Ze: the checkpoint that run_grad reads."""
-        p = _checked(self._want, dict(X=X, Xs=Xs, Wt=Wt, Ws=Ws, bias=bias, R=R, work=work, Y=Y, Zq=Zq, Ze=Ze))
+        p = _checked(self._run, X, Xs, Wt, Ws, bias, R, work, Y, Zq, Ze)
         _check(self._lib.cusync_linear(self._d, *p, _stream(stream)), "cusync_linear")
 
     def run_grad(self, X, Wt, dY, work, dX, dWt, dbias=None, Xs=None, Zq=None, Ze=None, stream=None):
         """The gradients that are not None, from dY, the checkpoint and X."""
-        p = _checked(self._want_grad, dict(X=X, Xs=Xs, Wt=Wt, Zq=Zq, Ze=Ze, dY=dY, work=work, dX=dX, dWt=dWt,
-                                           dbias=dbias))
+        p = _checked(self._grad, X, Xs, Wt, Zq, Ze, dY, work, dX, dWt, dbias)
         _check(self._lib.cusync_linear_grad(self._d, *p, _stream(stream)), "cusync_linear_grad")
 
     def check(self, buffer, stream=None):
         """(status, code) of the last call that used a work buffer: OK or ERR_DEVICE."""
-        code = c_u32()
-        st = self._lib.cusync_linear_check(_ptr(buffer), _stream(stream), ctypes.byref(code))
-        if st not in (OK, ERR_DEVICE):
-            raise CusyncError(st, "cusync_linear_check")
-        return st, code.value
+        return _work_check(buffer, stream)

@@ -90,11 +90,12 @@ struct GemmArgs {
 
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (kEpiWarps + 4) * 32;
-constexpr int kABytes = 32 * 1024;        // a CTA's share of A in a stage
 constexpr int kWarpOut = 4096;            // two blocks of 32 rows x 32 columns
 template <int BN>
 struct GemmCfg {
-  static constexpr int kBBytes = BN * 128;  // BN / 2 rows x 2 blocks of 128 bytes
+  static constexpr int kBlocks = 2;                        // blocks of 128 bytes of the reduction in a stage
+  static constexpr int kABytes = kBlocks * 128 * 128;      // a CTA's share of A in a stage
+  static constexpr int kBBytes = kBlocks * BN / 2 * 128;   // and of B
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 192 * 1024 / kStageBytes;
   static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpOut + 1024;
@@ -107,19 +108,40 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
-// Scales and bias of 8 columns from c on (of a part that begins at `first` of Wt's rows).
-template <bool E4M3>
-__device__ __forceinline__ void finish8(const Epilogue& e, float xs, int64_t first, int c, float* z) {
-  float f[8];
-  if (E4M3) {
-    load8(e.Ws + first + c, f);
+// What the epilogue of 32 columns reads: lane j the scale and bias of column j of each part (from there they
+// go to all lanes by shuffles), and 32 values of its own row of the residual.  Loaded one block of columns
+// ahead: a load takes longer than a block.
+template <int G>
+struct Ahead {
+  float ws[G], bs[G];
+  uint4 r[4];
+};
+template <bool E4M3, int G>
+__device__ __forceinline__ Ahead<G> load_ahead(const Epilogue& e, int N, int c, int64_t row, bool in) {
+  Ahead<G> v;
+  const int col = c + (threadIdx.x & 31);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] *= xs * f[j];
+  for (int g = 0; g < G; ++g) {
+    v.ws[g] = E4M3 && col < N ? e.Ws[(int64_t)g * N + col] : 0.0f;
+    v.bs[g] = e.bias && col < N ? __uint_as_float((uint32_t)e.bias[(int64_t)g * N + col] << 16) : 0.0f;
+  }
+  if (e.R) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v.r[i] = in && c + 8 * i < N ? *reinterpret_cast<const uint4*>(e.R + row * N + c + 8 * i) : make_uint4(0, 0, 0, 0);
+  }
+  return v;
+}
+// z * scales + bias of 32 columns.
+template <bool E4M3>
+__device__ __forceinline__ void finish32(const Epilogue& e, float xs, float ws, float bs, float (&z)[32]) {
+  if (E4M3) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) z[j] *= xs * __shfl_sync(0xffffffffu, ws, j);
   }
   if (e.bias) {
-    load8(e.bias + first + c, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) z[j] += f[j];
+    for (int j = 0; j < 32; ++j) z[j] += __shfl_sync(0xffffffffu, bs, j);
   }
 }
 
@@ -149,7 +171,8 @@ template <int MODE, bool E4M3, bool GATED, int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<BN>;
   constexpr bool kMnB = MODE != FWD;
-  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes, kBBytes = C::kBBytes;
+  constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes, kABytes = C::kABytes, kBBytes = C::kBBytes;
+  constexpr int kBlocks = C::kBlocks, kChunk = kBlocks * 64 * 128;  // an "along" operand's 64 columns in a stage
   constexpr int kElems = E4M3 ? 128 : 64;        // reduction elements in 128 bytes
   constexpr int kTileN = GATED ? BN / 2 : BN;    // output columns of a tile
   extern __shared__ uint8_t raw[];
@@ -222,13 +245,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       const CUtensorMap* map = copies_a ? &p.mA : &p.mB;
       // this CTA's first row (or column) of the operand
       const int r0 = copies_a ? m0 + 128 * rank : GATED ? n0 + rank * p.N : n0 + kBRows * rank;
-      const int block = copies_a ? 128 * 128 : kBRows * 128;  // bytes of a block, or of a chunk of 64 columns
-      for (int kb = 0; kb < nkb; kb += 2, ++it) {
+      const int block = copies_a ? 128 * 128 : kBRows * 128;  // bytes of a block
+      for (int kb = 0; kb < nkb; kb += kBlocks, ++it) {
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
         const uint32_t bar = full0 + 8 * st;  // both CTAs' copies complete on the first one's barrier
         uint8_t* dst = base + st * kStageBytes;
-        const bool half = kb + 1 == nkb;
+        const bool half = kBlocks == 2 && kb + 1 == nkb;
         if (one) {
           if (copies_a && rank == 0) {
             // an operand's second block is counted where a box brings it, even from outside
@@ -241,14 +264,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
               ptx::tma_load_3d_to_leader(dst, map, bar, 0, kb * 64, r0 / 64, pol);
             } else {
               ptx::tma_load_2d_to_leader(dst, map, bar, r0, kb * 64, pol);
-              if (copies_a || kBRows > 64) ptx::tma_load_2d_to_leader(dst + 16384, map, bar, r0 + 64, kb * 64, pol);
+              if (copies_a || kBRows > 64) ptx::tma_load_2d_to_leader(dst + kChunk, map, bar, r0 + 64, kb * 64, pol);
             }
           } else {   // blocks of 128 bytes
             if (wide) {
               ptx::tma_load_3d_to_leader(dst, map, bar, 0, r0, kb, pol);
             } else {
               ptx::tma_load_2d_to_leader(dst, map, bar, kb * kElems, r0, pol);
-              if (!half) ptx::tma_load_2d_to_leader(dst + block, map, bar, (kb + 1) * kElems, r0, pol);
+              if (kBlocks == 2 && !half) ptx::tma_load_2d_to_leader(dst + block, map, bar, (kb + 1) * kElems, r0, pol);
             }
           }
         }
@@ -290,23 +313,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + buf * BN;
-        for (int kb = 0; kb < nkb; kb += 2) {
+        for (int kb = 0; kb < nkb; kb += kBlocks) {
           ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&full[st], par, kWaitNs));
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t sA = ring0 + st * kStageBytes, sB = sA + kABytes;
-          const uint64_t dA = along ? ptx::smem_desc_mn128(sA, 16384) : ptx::smem_desc_k128(sA);
-          const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, 16384) : ptx::smem_desc_k128(sB);
+          const uint64_t dA = along ? ptx::smem_desc_mn128(sA, kChunk) : ptx::smem_desc_k128(sA);
+          const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, kChunk) : ptx::smem_desc_k128(sB);
           // 32 bytes of the reduction at a time; the last stage's steps that hold none of it are left out
           const int steps = (p.K - kb * kElems + kElems / 4 - 1) / (kElems / 4);
 #pragma unroll
-          for (int s = 0; s < 8; ++s) {
+          for (int s = 0; s < 4 * kBlocks; ++s) {
             if (s >= steps) break;
             if (!one) continue;
             // along the reduction: 32 bytes of a block's rows; across it: 16 rows of 128 bytes
             const uint64_t mn = (uint64_t)(s * 2048) >> 4;
             const uint64_t oA = along ? mn : (uint64_t)(s / 4 * 16384 + s % 4 * 32) >> 4;
-            const uint64_t oB = kMnB ? mn : (uint64_t)(s / 4 * (kBBytes / 2) + s % 4 * 32) >> 4;
+            const uint64_t oB = kMnB ? mn : (uint64_t)(s / 4 * (kBBytes / kBlocks) + s % 4 * 32) >> 4;
             if (E4M3) ptx::umma_e4m3_pair(d, dA + oA, dB + oB, idesc, kb || s);
             else ptx::umma_bf16_pair(d, dA + oA, dB + oB, idesc, kb || s);
           }
@@ -359,6 +382,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       const bool in = row < p.M;
       float xs = 1.0f;
       if (E4M3 && in) xs = e.Xs[row];
+      constexpr int G = GATED ? 2 : 1;
+      Ahead<G> now, next;
+      if (MODE == FWD) next = load_ahead<E4M3, G>(e, p.N, n0 + half * (kTileN / 2), row, in);
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -367,7 +393,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       for (int i = 0; i < kTileN / 64; ++i) {
         const int at = half * (kTileN / 2) + 32 * i, c = n0 + at, left = p.N - c;  // columns from c on
         if (left <= 0 || row0 >= p.M) break;
-        float z[32], u[GATED ? 32 : 1];
+        if (MODE == FWD) {
+          now = next;
+          if (i + 1 < kTileN / 64) next = load_ahead<E4M3, G>(e, p.N, c + 32, row, in);
+        }
+        float z[32], u[32];
         {
           uint32_t v[32];
           ptx::tmem_ld_32x32b_x32(d + at, v);
@@ -380,34 +410,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           ptx::tmem_ld_32x32b_x32(d + BN / 2 + at, v);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) u[j % (GATED ? 32 : 1)] = __uint_as_float(v[j]);
+          for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(v[j]);
         }
         if (MODE == FWD) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (j >= left) break;
-            finish8<E4M3>(e, xs, 0, c + j, z + j);
-            if (GATED) finish8<E4M3>(e, xs, p.N, c + j, u + (GATED ? j : 0));
-          }
+          finish32<E4M3>(e, xs, now.ws[0], now.bs[0], z);
+          if (GATED) finish32<E4M3>(e, xs, now.ws[G - 1], now.bs[G - 1], u);
           if (e.Zq && in) {
             store_checkpoint(e, z, left, row, 0, GATED ? 2 : 1, p.N, c);
-            if (GATED) store_checkpoint(e, reinterpret_cast<const float(&)[32]>(u), left, row, 1, 2, p.N, c);
+            if (GATED) store_checkpoint(e, u, left, row, 1, 2, p.N, c);
           }
           if (GATED) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] = z[j] * sigmoid_fast(z[j]) * u[j % (GATED ? 32 : 1)];
+            for (int j = 0; j < 32; ++j) z[j] = z[j] * sigmoid_fast(z[j]) * u[j];
           } else if (e.act != ACT_NONE) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = activate(z[j], e.act);
           }
-          if (e.R && in) {
+          if (e.R) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (j >= left) break;
+            for (int j = 0; j < 4; ++j) {
               float f[8];
-              load8(e.R + (int64_t)row * p.N + c + j, f);
+              unpack8(now.r[j], f);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) z[j + k] += f[k];
+              for (int k = 0; k < 8; ++k) z[8 * j + k] += f[k];
             }
           }
         }

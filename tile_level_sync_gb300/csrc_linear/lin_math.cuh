@@ -10,6 +10,18 @@
 #include "../csrc/ptx.cuh"
 
 namespace cusync {
+namespace ptx {
+
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned; completes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+}  // namespace ptx
+
 namespace lin {
 
 constexpr float kE4m3Max = 448.0f;

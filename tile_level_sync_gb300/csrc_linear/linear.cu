@@ -246,7 +246,7 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
 // A product on pairs; along: P's rows are the reduction's (dWt).  Q's are, too, in both gradients.
 template <bool E4M3, bool GATED, int BN>
 bool fill_shape(GemmShape* g, const Product& p, bool grad, bool along) {
-  constexpr int bytes = E4M3 ? 1 : 2;
+  constexpr int bytes = E4M3 ? 1 : 2, n = GemmCfg<BN>::kBlocks;
   g->M = (int32_t)p.rows;
   g->N = (int32_t)p.cols;
   g->K = (int32_t)p.depth;
@@ -254,10 +254,10 @@ bool fill_shape(GemmShape* g, const Product& p, bool grad, bool along) {
   g->n_tiles = (int32_t)div_up(p.cols, GATED ? BN / 2 : BN);
   g->group = std::min(g->m_tiles, 8);
   g->along = along;
-  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, 128, 2, &g->wideA)
-                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, 128, 2, &g->wideA)) &&
-         (grad ? map_along(&g->mB, p.Q, p.depth, p.cols, 128, BN / 128, &g->wideB)
-               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, BN / 2, 2, &g->wideB)) &&
+  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, 64 * n, 2, &g->wideA)
+                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, 128, n, &g->wideA)) &&
+         (grad ? map_along(&g->mB, p.Q, p.depth, p.cols, 64 * n, BN / 128, &g->wideB)
+               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, BN / 2, n, &g->wideB)) &&
          map_output(&g->mO, p.e.out, p.rows, p.cols);
 }
 template <int MODE, bool E4M3, bool GATED, int BN>

@@ -1,4 +1,5 @@
 // Host side of the norm in include/cusync_linear.h: argument checks and kernel launches.
+#include <atomic>
 #include <cmath>
 
 #include "lin_host.h"
@@ -32,9 +33,36 @@ Shape shape(int64_t D, int full, int most) {
   return {v, (int)round_up(div_up(vecs, v), 32)};
 }
 
-int grad_blocks(const cusync_norm_desc_t* d, const Shape& s, int sms) {
-  const int per_sm = std::min(8, std::max(1, (s.v == 1 ? 2048 : 1024) / s.threads));
-  return (int)std::min<int64_t>(std::max<int64_t>(d->M, 1), std::min((int64_t)kGradBlocks, (int64_t)sms * per_sm));
+// Blocks of the gradient's kernel on an SM, and rows of a block's ring.
+struct Ring {
+  int per_sm, stages;
+};
+constexpr int kRingBytes = 208 * 1024;  // of an SM
+Ring ring(const cusync_norm_desc_t* d, const Shape& s, int tensors) {
+  const int row = (int)d->D * 2 * tensors;
+  int per_sm = std::min(8, std::max(1, 1024 / s.threads));
+  while (per_sm > 1 && 4 * row > kRingBytes / per_sm) --per_sm;
+  return {per_sm, std::min(kNormStages, std::max(1, kRingBytes / per_sm / row))};
+}
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];  // SMs of a prepared device, 0 = not prepared
+
+// The current device, the gradient's kernels set up.  The first call on a device does the work.
+cusync_status_t prepare_device(int* sms) {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return CUSYNC_ERR_CUDA;
+  if ((*sms = g_sms[dev].load(std::memory_order_acquire))) return CUSYNC_OK;
+  cudaError_t e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  const void* kernels[] = {reinterpret_cast<const void*>(&norm_grad_kernel<1, 256>),
+                           reinterpret_cast<const void*>(&norm_grad_kernel<2, 512>),
+                           reinterpret_cast<const void*>(&norm_grad_kernel<2, 1024>),
+                           reinterpret_cast<const void*>(&norm_grad_kernel<4, 1024>)};
+  for (const void* f : kernels)
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return CUSYNC_ERR_CUDA;
+  g_sms[dev].store(*sms = n, std::memory_order_release);
+  return CUSYNC_OK;
 }
 
 }  // namespace
@@ -89,13 +117,16 @@ cusync_status_t cusync_norm_grad(const cusync_norm_desc_t* d, const void* S, con
   if (d->kind != CUSYNC_NORM_RMS) return CUSYNC_ERR_UNSUPPORTED;
   cudaStream_t q = (cudaStream_t)stream;
   if (!aligned_or_null(dw)) return CUSYNC_ERR_INVALID_ARG;
-  if (d->M == 0) return status_of(dw ? cudaMemsetAsync(dw, 0, (size_t)d->D * 2, q) : cudaSuccess);
-  if (!aligned(S) || !aligned(w) || !aligned(dY) || !aligned_or_null(dS) || !aligned(dX) || (dw && !aligned(work)))
-    return CUSYNC_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return CUSYNC_ERR_CUDA;
+  if (!aligned(work)) return CUSYNC_ERR_INVALID_ARG;
+  if (d->M == 0) {
+    cudaError_t e = cudaMemsetAsync(work, 0, 4, q);
+    if (e == cudaSuccess && dw) e = cudaMemsetAsync(dw, 0, (size_t)d->D * 2, q);
+    return status_of(e);
+  }
+  if (!aligned(S) || !aligned(w) || !aligned(dY) || !aligned_or_null(dS) || !aligned(dX)) return CUSYNC_ERR_INVALID_ARG;
+  int sms = 0;
+  const cusync_status_t ready = prepare_device(&sms);
+  if (ready != CUSYNC_OK) return ready;
   if (d->num_sms) sms = std::min(sms, d->num_sms);
   NormGradArgs a = {};
   a.S = static_cast<const uint4*>(S);
@@ -104,17 +135,22 @@ cusync_status_t cusync_norm_grad(const cusync_norm_desc_t* d, const void* S, con
   a.dS = static_cast<const uint4*>(dS);
   a.dX = static_cast<uint4*>(dX);
   a.part = dw ? reinterpret_cast<float*>(static_cast<char*>(work) + kHeader) : nullptr;
+  a.err = static_cast<int32_t*>(work);
   a.M = d->M;
   a.vecs = (int32_t)(d->D / 8);
   a.eps = d->eps;
   a.inv_d = 1.0f / (float)d->D;
   const Shape s = shape(d->D, 256, 2);
-  const int blocks = grad_blocks(d, s, sms);
+  const int tensors = dS ? 3 : 2;
+  const Ring g = ring(d, s, tensors);
+  a.stages = g.stages;
+  const int blocks = (int)std::min<int64_t>(d->M, std::min<int64_t>(kGradBlocks, (int64_t)sms * g.per_sm));
   const dim3 grid((unsigned)blocks);
-  cudaError_t e = s.v == 1           ? launch(norm_grad_kernel<1, 256, 4>, grid, s.threads, 0, q, a)
-                  : s.v == 2 && s.threads <= 512 ? launch(norm_grad_kernel<2, 512, 2>, grid, s.threads, 0, q, a)
-                  : s.v == 2         ? launch(norm_grad_kernel<2, 1024, 1>, grid, s.threads, 0, q, a)
-                                     : launch(norm_grad_kernel<4, 1024, 1>, grid, s.threads, 0, q, a);
+  const size_t smem = (size_t)g.stages * tensors * d->D * 2;
+  cudaError_t e = s.v == 1                       ? launch(norm_grad_kernel<1, 256>, grid, s.threads, smem, q, a)
+                  : s.v == 2 && s.threads <= 512 ? launch(norm_grad_kernel<2, 512>, grid, s.threads, smem, q, a)
+                  : s.v == 2                     ? launch(norm_grad_kernel<2, 1024>, grid, s.threads, smem, q, a)
+                                                 : launch(norm_grad_kernel<4, 1024>, grid, s.threads, smem, q, a);
   if (e == cudaSuccess && dw)
     e = launch(column_sum_kernel, dim3((unsigned)div_up(d->D, 32)), 256, 0, q, (const float*)a.part, (int32_t)blocks,
                (int32_t)d->D, static_cast<uint16_t*>(dw));
