@@ -11,8 +11,8 @@
 // that all SMs stream weights at once.  Weights are the MMA's rows, whose number is fixed, and tokens
 // its columns, of which 16 will do.  A tile's reduction is cut into `splits` runs, one for each CTA
 // of a cluster; their fp32 sums meet in shared memory: each CTA sends every other one the columns that
-// that one finishes, and adds what it gets in the CTAs' order.  No partial sum leaves the SMs, and one
-// launch does it all.
+// that one finishes, and adds what it gets in the CTAs' order.  The sums are counted by a barrier of the CTA
+// that they go to, which waits for them alone.  No partial sum leaves the SMs, and one launch does it all.
 //
 // Roles: warp 0 copies A, warp 2 copies B, warp 1 owns TMEM and issues the MMAs; then all
 // eight warps read the accumulator, exchange and finish.  Every wait is bounded.
@@ -22,12 +22,8 @@
 namespace cusync {
 namespace ptx {
 
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -50,22 +46,26 @@ struct SplitArgs {
   int32_t splits;        // CTAs of a cluster, at most the reduction's stages
   int32_t stages;        // of the ring
   int32_t blocks;        // of 128 bytes of the reduction in a stage: 1 or 2
+  int32_t apart;         // the sums have room of their own behind the ring, else they take the ring's
   int32_t wideA, wideB;
 };
 
 constexpr int kSplitThreads = 256;
 constexpr int kMaxStages = 8;
 __host__ __device__ constexpr int split_stage_bytes(int cols, int blocks) { return blocks * (128 + cols) * 128; }
+constexpr size_t split_smem(int cols, int blocks, int stages, bool apart) {
+  const size_t ring = (size_t)stages * split_stage_bytes(cols, blocks), sums = (size_t)cols * 128 * 4;
+  return 1024 + (apart ? ring + sums : ring > sums ? ring : sums);
+}
 
 template <int MODE, bool E4M3, bool GATED>
 __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_constant__ SplitArgs a) {
   constexpr bool kMnA = MODE != FWD, kMnB = MODE == DW;
   constexpr int kElems = E4M3 ? 128 : 64;
   constexpr int kFeatures = GATED ? 64 : 128;
-  constexpr bool kAhead = MODE != DW;            // A is the weights
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull, drain;
+  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tfull, drain, came;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int32_t abort_flag;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -79,7 +79,9 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     }
     ptx::mbar_init(&tfull, 1);
     ptx::mbar_init(&drain, 1);
+    ptx::mbar_init(&came, 1);
     ptx::mbar_init_fence();
+    if (splits > 1) ptx::mbar_arrive_expect_tx(&came, a.cols * 128 * 4);
     abort_flag = 0;
     ptx::prefetch_tmap(&a.mA);
     ptx::prefetch_tmap(&a.mB);
@@ -90,6 +92,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     ptx::tc_fence_before();
   }
   __syncthreads();
+  if (splits > 1) ptx::cluster_arrive();  // this CTA's barriers exist
   ptx::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
@@ -102,15 +105,6 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   // where a stage's block b begins, and an "along" operand's second chunk of 64 columns
   const int b_step = a.cols * 128, chunk = blocks * 64 * 128;
 
-  // Weights are on their way into the L2 while the kernel before this one ends.
-  if (kAhead && threadIdx.x == 0) {
-    for (int s = s0; s < min(s1, s0 + a.stages); ++s) {
-      const int kb = s * blocks;
-      if (GATED && a.wideA) ptx::tma_prefetch_4d(&a.mA, 0, f0, 0, kb);
-      else if (MODE == FWD && a.wideA) ptx::tma_prefetch_3d(&a.mA, 0, f0, kb);
-      else if (MODE == DX && a.wideA) ptx::tma_prefetch_3d(&a.mA, 0, kb * 64, f0 / 64);
-    }
-  }
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
@@ -240,18 +234,23 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     *a.err = (int32_t)kErrWait;
   }
   ptx::tc_fence_after();
-  // every CTA's MMAs have read its ring, which now takes [splits][cols / splits][128] sums
-  __syncthreads();
-  if (splits > 1) ptx::cluster_sync();
   const int per = a.cols / splits, shift = 31 - __clz(per);
+  float* sums = reinterpret_cast<float*>(ring + (a.apart ? a.stages * stage_bytes : 0));  // [splits][per][128]
+  if (splits > 1) {
+    ptx::cluster_wait();
+    if (!a.apart) {  // every CTA's MMAs have read its ring
+      __syncthreads();
+      ptx::cluster_sync();
+    }
+  }
   {
     const int quarter = warp & 3, m = 32 * quarter + lane, width = a.cols / 2, c0 = (warp >> 2) * width;
     const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16);
-    float* own = reinterpret_cast<float*>(ring) + m;
-    float* mine = own + rank * per * 128;  // this CTA's sums, wherever they go
+    float* mine = sums + rank * per * 128 + m;  // this CTA's sums, wherever they go
     auto put = [&](int n, uint32_t v) {
-      if (splits > 1) ptx::st_cluster_u32(ptx::mapa(mine + (n & (per - 1)) * 128, n >> shift), v);
-      else own[n * 128] = __uint_as_float(v);
+      const int to = n >> shift;
+      if (splits > 1) ptx::st_async_u32(ptx::mapa(mine + (n & (per - 1)) * 128, to), v, ptx::mapa(&came, to));
+      else mine[n * 128] = __uint_as_float(v);
     };
     if (width >= 32) {
 #pragma unroll 1
@@ -275,10 +274,9 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (splits > 1) ptx::cluster_sync();
+  if (splits > 1 && !ptx::mbar_wait_bounded_cluster(&came, 0, 3 * kWaitNs)) *a.err = (int32_t)kErrWait;
 
   // ------------------------------------------------------------ finish: 8 features of a token a thread
-  const float* sums = reinterpret_cast<const float*>(ring);
 #pragma unroll 2
   for (int tok = threadIdx.x / kGroups; tok < max(per, 32 / kGroups); tok += kSplitThreads / kGroups) {
     const int row = r0 + rank * per + tok;

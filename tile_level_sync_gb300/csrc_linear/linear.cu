@@ -181,38 +181,77 @@ struct Product {
 };
 
 // How products are computed: on CTA pairs with tiles of 256 x `bn` (SwiGLU: bn / 2 columns of Y), or (bn = 0) on
-// clusters of `splits` CTAs with tiles of 128 (64) columns x `cols` rows; and about how long it takes.
+// clusters of `splits` CTAs with tiles of 128 (64) columns x `cols` rows; and about how long it takes.  The
+// times are fits to passes on one GB300 (us; bf16, no activation, weights in the L2 where they fit it):
+//   rows x cols   reduction   pairs 256   pairs 128   clusters (cols, splits)
+//   1777 x 1024        2048        13.3        10.2        15.3 (128, 1)  21.2 (64, 2)
+//   4096 x 2048        4096        42.9        51.0        91.7 (128, 1)
+//    333 x  776         512         6.8         5.2         6.3 (64, 2)    7.3 (128, 4)
+//    333 x  776        4096        21.6        13.3        11.9 (64, 2)   10.9 (128, 4)
+//    100 x 4096        2048        12.8         8.5         9.1 (64, 2)    9.5 (128, 4)
+//    100 x 4096        4096        22.9        15.3        16.5 (64, 2)   12.7 (128, 4)
 struct Plan {
   double us;
   int bn, cols, splits, stages, blocks;
+  bool apart;  // clusters: room of their own for the sums
 };
+constexpr double kBytesPerUs = 6.5e6;  // of HBM
+
+// A tile of 256 x bn with `blocks` blocks of 128 bytes of the reduction, on a pair.
+double pair_tile(int bn, int64_t blocks) { return 0.5 + (bn == 256 ? 0.30 : 0.19) * (double)blocks; }
+// n tiles that take a each, then m that take b, dealt out to `pairs` pairs in turn: the pair that ends last is
+// the first one, or the first one with a tile less of the first kind.
+double pair_time(int64_t n, double a, int64_t m, double b, int64_t pairs) {
+  const int64_t rest = n % pairs;
+  const double first = (double)div_up(n, pairs) * a + (double)(div_up(n + m, pairs) - div_up(n, pairs)) * b;
+  const double other = (double)(n / pairs) * a + (double)(div_up(n + m - rest, pairs) - n / pairs) * b;
+  return 4.2 + (rest ? std::max(first, other) : first);
+}
 
 Plan pair_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems, bool gated) {
-  Plan best = {1e30, 0, 0, 0, 0, 0};
+  Plan best = {1e30, 0, 0, 0, 0, 0, false};
   if (sms < 2) return best;
   for (int bn = 128; bn <= 256; bn += 128) {
     const int64_t tiles = div_up(rows, 256) * div_up(cols, gated ? bn / 2 : bn);
-    const double us = 4.2 + (double)div_up(tiles, sms / 2) * (0.5 + (bn == 256 ? 0.30 : 0.19) * (double)div_up(depth, elems));
-    if (us < best.us) best = {us, bn, 0, 0, 0, 0};
+    const double us = pair_time(tiles, pair_tile(bn, div_up(depth, elems)), 0, 0.0, sms / 2);
+    if (us < best.us) best = {us, bn, 0, 0, 0, 0, false};
   }
   return best;
 }
 
 template <int MODE, bool GATED>
 Plan split_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems) {
-  Plan r = {1e30, 0, 0, 0, 0, 2};
-  r.cols = MODE == DW ? 64 : 16;
-  while (r.cols < 128 && r.cols < rows) r.cols *= 2;
-  const int stage = split_stage_bytes(r.cols, r.blocks);
-  // two CTAs an SM where three stages of both fit
-  const int resident = 2 * (3 * stage + 2048) <= kSmemPerSm ? 2 : 1;
-  r.stages = std::min(kMaxStages, (kSmemPerSm / resident - 2048) / stage);
-  const int64_t tiles = div_up(rows, r.cols) * div_up(cols, GATED ? 64 : 128);
-  const int64_t steps = div_up(depth, r.blocks * elems);
-  r.splits = 1;
-  while (r.splits < 8 && 2 * r.splits * tiles <= (int64_t)sms * resident && 2 * r.splits <= steps) r.splits *= 2;
-  r.us = 6.0 + (double)div_up(tiles * r.splits, (int64_t)sms * resident) * 0.27 * (double)div_up(depth, elems * r.splits);
-  return r;
+  Plan best = {1e30, 0, 0, 0, 0, 2, false};
+  int most = 16;  // rows of a tile that covers all rows, where one does
+  while (most < 128 && most < rows) most *= 2;
+  const int64_t blocks = div_up(depth, elems);
+  for (int n = MODE == DW ? 64 : std::max(16, most / 2); n <= std::max(most, MODE == DW ? 64 : 16); n *= 2) {
+    const int stage = split_stage_bytes(n, best.blocks);
+    const int64_t tiles = div_up(rows, n) * div_up(cols, GATED ? 64 : 128);
+    for (int splits = 1; splits <= 8; splits *= 2) {
+      if (splits > 1 && splits > div_up(blocks, best.blocks)) break;
+      const int64_t ctas = tiles * splits;
+      // two CTAs an SM where there are enough and two stages of both fit; clusters of four or eight leave some
+      // SMs out (of 152: 144 and 120 take one CTA, 296 and 288 CTAs fit two an SM)
+      const int64_t alone = splits == 8 ? sms * 15 / 19 : splits == 4 ? sms * 18 / 19 : sms;
+      const int64_t both = splits == 8 ? sms * 36 / 19 : splits == 4 ? sms * 37 / 19 : 2 * sms;
+      const bool two = ctas > alone && 2 * (2 * stage + 2048) <= kSmemPerSm;
+      // an SM's CTAs share what it can load: 0.2 us a block (0.26 with 128 rows), one CTA or two
+      const double stream = (double)(div_up(ctas, sms) * div_up(blocks, splits)) * (n <= 64 ? 0.2 : 0.26);
+      // weights come at HBM's rate, a little less where SMs are left out
+      const double weights = (double)(cols * (GATED ? 2 : 1) * depth) * (64.0 / elems) * 2.0 / kBytesPerUs /
+                             std::min(1.0, 0.9 + 0.1 * (double)ctas / sms);
+      const double us = 5.2 + 0.012 * n + 0.15 * (splits - 1) + 2.0 * (double)(div_up(ctas, two ? both : alone) - 1) +
+                        std::max(stream, MODE == DW ? 0.0 : weights);
+      if (us < best.us) {
+        const int room = (two ? kSmemPerSm / 2 : kSmemPerSm) - 1024;  // static shared memory and the block's own
+        best = {us, 0, n, splits, 0, best.blocks, false};
+        best.stages = (int)std::min<int64_t>(std::min(kMaxStages, (room - 1024) / stage), div_up(div_up(blocks, best.blocks), splits));
+        best.apart = splits > 1 && split_smem(n, best.blocks, best.stages, true) <= (size_t)room;
+      }
+    }
+  }
+  return best;
 }
 
 template <int MODE, bool E4M3, bool GATED>
@@ -231,6 +270,7 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
   a.splits = plan.splits;
   a.stages = plan.stages;
   a.blocks = plan.blocks;
+  a.apart = plan.apart;
   const int n = plan.blocks;
   const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, 64 * n, 2, &a.wideA)
                    : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, n, &a.wideA)
@@ -240,7 +280,7 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = div_up(p.cols, GATED ? 64 : 128) * a.row_tiles;
   return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)), kSplitThreads,
-                        (size_t)plan.stages * split_stage_bytes(plan.cols, n) + 1024, s, a);
+                        split_smem(plan.cols, n, plan.stages, plan.apart), s, a);
 }
 
 // A product on pairs; along: P's rows are the reduction's (dWt).  Q's are, too, in both gradients.
@@ -312,6 +352,7 @@ cudaError_t sum_columns(const Sums& sums, cudaStream_t s) {
   return launch(column_sum_kernel, dim3((unsigned)div_up(sums.cols, 32)), 256, 0, s, sums.part, (int32_t)sums.rows,
                 (int32_t)sums.cols, sums.out);
 }
+// Both on pairs in one launch, or one or both on clusters: what is estimated fastest.
 cudaError_t gradients(const Product* dx, const Product* dw, const Sums& sums, int32_t* err, bool clear, int sms,
                       cudaStream_t s) {
   Plan px = {0}, pw = {0}, sx = {0}, sw = {0};
@@ -323,10 +364,24 @@ cudaError_t gradients(const Product* dx, const Product* dw, const Sums& sums, in
     pw = pair_plan(dw->rows, dw->cols, dw->depth, sms, 64, false);
     sw = split_plan<DW, false>(dw->rows, dw->cols, dw->depth, sms, 64);
   }
-  const bool split_x = dx && sx.us <= px.us, split_w = dw && sw.us <= pw.us;
-  const bool pairs = (dx && !split_x) || (dw && !split_w);
+  int bn = dx && px.us < sx.us ? px.bn : 0;  // of the launch on pairs
+  bool split_x = dx && !bn, split_w = dw && sw.us <= pw.us;
+  if (dw && !split_w) bn = bn ? std::min(bn, pw.bn) : pw.bn;
+  if (dx && dw && sms >= 2) {
+    double apart = std::min(px.us, sx.us) + std::min(pw.us, sw.us);
+    for (int n = 128; n <= 256; n += 128) {
+      const int64_t tx = div_up(dx->rows, 256) * div_up(dx->cols, n), tw = div_up(dw->rows, 256) * div_up(dw->cols, n);
+      const double ux = pair_tile(n, div_up(dx->depth, 64)), uw = pair_tile(n, div_up(dw->depth, 64));
+      const double us = ux > uw ? pair_time(tx, ux, tw, uw, sms / 2) : pair_time(tw, uw, tx, ux, sms / 2);
+      if (us < apart) {
+        apart = us;
+        bn = n;
+        split_x = split_w = false;
+      }
+    }
+  }
   cudaError_t e = cudaSuccess;
-  if (sums.part && !pairs) e = sum_columns(sums, s);
+  if (sums.part && !bn) e = sum_columns(sums, s);
   if (e == cudaSuccess && split_x) {
     e = launch_split<DX, false, false>(sx, *dx, err, clear, s);
     clear = false;
@@ -335,9 +390,8 @@ cudaError_t gradients(const Product* dx, const Product* dw, const Sums& sums, in
     e = launch_split<DW, false, false>(sw, *dw, err, clear, s);
     clear = false;
   }
-  if (e == cudaSuccess && pairs) {
+  if (e == cudaSuccess && bn) {
     const Product *x = split_x ? nullptr : dx, *w = split_w ? nullptr : dw;
-    const int bn = x && w ? std::min(px.bn, pw.bn) : x ? px.bn : pw.bn;
     e = bn == 256 ? pair_gradients<256>(x, w, sums, err, clear, sms, s) : pair_gradients<128>(x, w, sums, err, clear, sms, s);
   }
   return e;
