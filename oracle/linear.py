@@ -164,24 +164,26 @@ def checkpoint(z, parts):
     return round_to_e4m3(z / units(e, parts, z.shape[1] // parts)), e
 
 
-def rows_bf16(q, scales):
-    """8-bit rows as the backward pass reads them: q * scale in fp32, rounded to bf16."""
-    return round_to_bf16((q.astype(np.float32) * scales.astype(np.float32)[:, None]).astype(np.float64))
-
-
-def linear_grad(X, Wt, z, dY, kind):
-    """{name: (gradient, bound)}; z: what the checkpoint stands for (None for kind "none"), X in
-    bf16."""
+def linear_grad(X, Xs, Wt, z, dY, kind):
+    """{name: (gradient, bound)}; z: what the checkpoint stands for (None for kind "none").  X in bf16,
+    or the values of 8-bit rows with scales Xs: dWt is the product of the rounded dZ * Xs with them then."""
     dz, err = slope(z, dY, kind)
     err = err + 2.0 ** -24 * np.abs(dz)
-    d = dz if kind == "none" else round_to_bf16(dz)
-    slack = np.zeros_like(d) if kind == "none" else np.maximum(np.abs(round_to_bf16(dz - err) - d),
-                                                               np.abs(round_to_bf16(dz + err) - d))
+
+    def rounded(v, e, exact):
+        d = v if exact else round_to_bf16(v)
+        slack = np.zeros_like(v) if exact else np.maximum(np.abs(round_to_bf16(v - e) - d), np.abs(round_to_bf16(v + e) - d))
+        return d, slack
+    dx, sx = rounded(dz, err, kind == "none")
+    dw, sw = dx, sx
+    if Xs is not None:
+        v = dz * Xs[:, None]
+        dw, sw = rounded(v, err * Xs[:, None] + 2.0 ** -24 * np.abs(v), False)
     out = {}
-    M, H = d.shape
+    M, H = dz.shape
     for name, value, mag, loose, depth in (
-            ("dX", d @ Wt, np.abs(d) @ np.abs(Wt), slack @ np.abs(Wt), H),
-            ("dWt", d.T @ X, np.abs(d).T @ np.abs(X), slack.T @ np.abs(X), M)):
+            ("dX", dx @ Wt, np.abs(dx) @ np.abs(Wt), sx @ np.abs(Wt), H),
+            ("dWt", dw.T @ X, np.abs(dw).T @ np.abs(X), sw.T @ np.abs(X), M)):
         e = (depth / 16 + 16) * STEP * mag + loose
         out[name] = (value, e + BF16 * (np.abs(value) + e))
     b = dz.sum(axis=0)

@@ -143,5 +143,4 @@ def oracle_linear(s, act):
 
 
 def oracle_grad(s, act):
-    X = f64(s["X"]) if s["Xs"] is None else ref.rows_bf16(f64(s["X"]), s["Xs"].cpu().numpy())
-    return ref.linear_grad(X, f64(s["Wt"]), values(s, 2 if act == "swiglu" else 1), f64(s["dY"]), act)
+    return ref.linear_grad(f64(s["X"]), f64(s["Xs"]), f64(s["Wt"]), values(s, 2 if act == "swiglu" else 1), f64(s["dY"]), act)

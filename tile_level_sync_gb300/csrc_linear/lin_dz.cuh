@@ -9,28 +9,60 @@ namespace lin {
 struct DzArgs {
   const uint16_t* dY;
   const uint8_t *Zq, *Ze;
-  uint16_t* dZ;   // [M, parts * N], or NULL (act NONE)
-  float* part;    // [gridDim.y][parts * N] sums of dZ over a block's rows, or NULL
+  uint16_t* dZ;         // [M, parts * N], or NULL (dY itself is dZ, or dX is not wanted)
+  const float* Xs;      // 8-bit X, where dWt is wanted: its scales,
+  uint16_t* dZs;        // dZ times them [M, parts * N],
+  const uint4* q;       // X [M, K]
+  uint4* x;             // and its values in bf16, exactly
+  int64_t pieces;       // M * K / 16
+  float* part;    // [parts][parts of a row * N] sums of dZ over a block's rows, or NULL
   int32_t* err;   // the call's error word, cleared by the call's first kernel
   int64_t M;
   int32_t N, rows;  // rows of a block
+  int32_t col_blocks, parts;
 };
 
 constexpr int kDzCols = 256;
+constexpr int kUnpackPieces = 8;  // of 16 values a thread
 
 // dZ = act'(z) dY from the checkpoint, and the sums over rows that dbias is made of (before
 // dZ's rounding).  A lane takes 8 columns, a warp every eighth row of the block's.
+//
+// dWt of 8-bit rows X = s q is the product of s dZ with q: q is exact in bf16, so that there is one rounding,
+// s dZ's, as with X in bf16 (of dZ with s q rounded to bf16 there would be two).  The blocks behind those of dZ
+// write q in bf16.
 template <int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a) {
   constexpr int G = ACT == ACT_SWIGLU ? 2 : 1;
   __shared__ float sums[8][kDzCols + 8];
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
-  if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.err = 0;
+  if (a.err && blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * kDzCols + lane * 8;
+  const int own = blockIdx.x / a.col_blocks, col_block = blockIdx.x - own * a.col_blocks;
+  if (own >= a.parts) {
+    const int64_t b = (int64_t)blockIdx.x - (int64_t)a.parts * a.col_blocks, i0 = b * 256 * kUnpackPieces + threadIdx.x;
+    uint4 v[kUnpackPieces];
+#pragma unroll
+    for (int k = 0; k < kUnpackPieces; ++k)
+      if (i0 + k * 256 < a.pieces) v[k] = a.q[i0 + k * 256];
+#pragma unroll
+    for (int k = 0; k < kUnpackPieces; ++k) {
+      if (i0 + k * 256 >= a.pieces) break;
+      float f[2][8];
+      unpack_e4m3(v[k].x, f[0]);
+      unpack_e4m3(v[k].y, f[0] + 4);
+      unpack_e4m3(v[k].z, f[1]);
+      unpack_e4m3(v[k].w, f[1] + 4);
+      uint4* out = a.x + 2 * (i0 + k * 256);
+      out[0] = pack8(f[0]);
+      out[1] = pack8(f[1]);
+    }
+    return;
+  }
+  const int c = col_block * kDzCols + lane * 8;
   const int blocks = (a.N + kBlock - 1) / kBlock;
-  const int64_t r0 = (int64_t)blockIdx.y * a.rows, end = min(r0 + a.rows, a.M);
+  const int64_t r0 = (int64_t)own * a.rows, end = min(r0 + a.rows, a.M);
   float acc[G][8];
 #pragma unroll
   for (int g = 0; g < G; ++g)
@@ -72,9 +104,18 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a) {
 #pragma unroll
         for (int g = 0; g < G; ++g) acc[g][j] += dz[g][j];
       }
-      if (ACT != ACT_NONE) {
+      if (a.dZ) {
 #pragma unroll
         for (int g = 0; g < G; ++g) *reinterpret_cast<uint4*>(a.dZ + (r * G + g) * a.N + c) = pack8(dz[g]);
+      }
+      if (a.dZs) {
+        const float xs = a.Xs[r];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dz[g][j] *= xs;
+          *reinterpret_cast<uint4*>(a.dZs + (r * G + g) * a.N + c) = pack8(dz[g]);
+        }
       }
     }
   }
@@ -85,34 +126,11 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[warp][lane * 8 + j] = acc[g][j];
     __syncthreads();
-    const int col = blockIdx.x * kDzCols + threadIdx.x;
+    const int col = col_block * kDzCols + threadIdx.x;
     float t = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) t += sums[w][threadIdx.x];
-    if (col < a.N) a.part[((int64_t)blockIdx.y * G + g) * a.N + col] = t;
-  }
-}
-
-// 8-bit rows as bf16: one rounding of scale * q.
-__global__ void __launch_bounds__(256) rows_from_e4m3_kernel(const uint4* q, const float* scales, uint4* out, int64_t M,
-                                                             int32_t vecs /* K / 16 */) {
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  const int64_t n = M * vecs, step = (int64_t)gridDim.x * blockDim.x;
-#pragma unroll 2
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-    const uint4 v = q[i];
-    const float s = scales[i / vecs];
-    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-    float f[2][8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) unpack_e4m3(words[k], &f[k / 2][4 * (k % 2)]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[k][j] *= s;
-      out[2 * i + k] = pack8(f[k]);
-    }
+    if (col < a.N) a.part[((int64_t)own * G + g) * a.N + col] = t;
   }
 }
 

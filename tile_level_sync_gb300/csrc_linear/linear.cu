@@ -25,7 +25,7 @@ struct Layer {
   int64_t M, K, N, G, blocks;
   bool e4m3;
   int64_t dz_rows, dz_parts;               // rows of a block of the pass over dY; blocks along M
-  int64_t dz, x, part, work_bytes, grad_bytes;  // gradient work, bytes
+  int64_t dz, dzs, x, part, work_bytes, grad_bytes;  // gradient work, bytes
 };
 
 cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
@@ -33,10 +33,10 @@ cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
       d->act > CUSYNC_LINEAR_SWIGLU || (d->dtype != CUSYNC_LINEAR_BF16 && d->dtype != CUSYNC_LINEAR_E4M3))
     return CUSYNC_ERR_INVALID_ARG;
   L->e4m3 = d->dtype == CUSYNC_LINEAR_E4M3;
-  // the kernels count rows, columns and tiles in 32 bits
+  // the kernels count rows, columns, tiles and blocks in 32 bits
   if (d->N % 8 || d->K % (L->e4m3 ? 16 : 8) || d->K > (1 << 24) || d->N > (1 << 24) || d->M > (1 << 30) ||
       div_up(d->M, 16) * div_up(std::max(d->N, d->K), 64) > INT32_MAX / 8 ||
-      div_up(2 * d->N, 64) * div_up(d->K, 64) > INT32_MAX / 8)
+      div_up(2 * d->N, 64) * div_up(d->K, 64) > INT32_MAX / 8 || div_up(d->M * d->K, 1 << 15) > INT32_MAX / 2)
     return CUSYNC_ERR_UNSUPPORTED;
   L->M = d->M;
   L->K = d->K;
@@ -54,6 +54,7 @@ cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
   };
   L->work_bytes = b;
   L->dz = bytes(d->act == CUSYNC_LINEAR_NONE ? 0 : L->M * L->G * L->N * 2);
+  L->dzs = bytes(L->e4m3 ? L->M * L->G * L->N * 2 : 0);
   L->x = bytes(L->e4m3 ? L->M * L->K * 2 : 0);
   L->part = bytes(L->dz_parts * L->G * L->N * 4);
   L->grad_bytes = b;
@@ -483,32 +484,38 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
   int32_t* err = static_cast<int32_t*>(work);
   bool clear = true;
   cudaError_t e = cudaSuccess;
+  const bool scaled = L.e4m3 && dWt;
   const void* dZ = act ? w + L.dz : dY;
-  if (act || dbias) {
+  if (act || dbias || scaled) {
     DzArgs a = {};
     a.dY = static_cast<const uint16_t*>(dY);
     a.Zq = static_cast<const uint8_t*>(Zq);
     a.Ze = Ze;
-    a.dZ = reinterpret_cast<uint16_t*>(w + L.dz);
+    a.dZ = act && (dX || (dWt && !scaled)) ? reinterpret_cast<uint16_t*>(w + L.dz) : nullptr;
+    if (scaled) {
+      a.Xs = Xs;
+      a.dZs = reinterpret_cast<uint16_t*>(w + L.dzs);
+      a.q = static_cast<const uint4*>(X);
+      a.x = reinterpret_cast<uint4*>(w + L.x);
+      a.pieces = L.M * (L.K / 16);
+    }
     a.part = dbias ? reinterpret_cast<float*>(w + L.part) : nullptr;
     a.err = err;
     a.M = L.M;
     a.N = (int32_t)L.N;
     a.rows = (int32_t)L.dz_rows;
+    a.col_blocks = (int32_t)div_up(L.N, kDzCols);
+    a.parts = (int32_t)L.dz_parts;
     clear = false;
-    const dim3 grid((unsigned)div_up(L.N, kDzCols), (unsigned)L.dz_parts);
+    const dim3 grid((unsigned)(a.col_blocks * L.dz_parts + div_up(a.pieces, 256 * kUnpackPieces)));
     e = d->act == CUSYNC_LINEAR_NONE   ? launch(dz_kernel<ACT_NONE>, grid, 256, 0, s, a)
         : d->act == CUSYNC_LINEAR_RELU ? launch(dz_kernel<ACT_RELU>, grid, 256, 0, s, a)
         : d->act == CUSYNC_LINEAR_GELU ? launch(dz_kernel<ACT_GELU>, grid, 256, 0, s, a)
                                        : launch(dz_kernel<ACT_SWIGLU>, grid, 256, 0, s, a);
   }
-  if (e == cudaSuccess && dWt && L.e4m3) {
-    const int64_t pieces = L.M * (L.K / 16);
-    e = launch(rows_from_e4m3_kernel, dim3((unsigned)std::min<int64_t>(div_up(pieces, 256), (int64_t)sms * 16)), 256, 0, s,
-               static_cast<const uint4*>(X), Xs, reinterpret_cast<uint4*>(w + L.x), L.M, (int32_t)(L.K / 16));
-  }
   Product dx = {}, dw = {};
-  dx.P = dw.P = dZ;
+  dx.P = dZ;
+  dw.P = scaled ? w + L.dzs : dZ;
   dx.Q = Wt;
   dx.rows = L.M;
   dx.cols = L.K;
