@@ -15,7 +15,7 @@
 // A stage holds 128 bytes x 2 of the reduction for the CTA's 128 rows of A and BN / 2 of B (64 or 48 KB);
 // three or four fit beside the epilogue's staging.  Roles, as in the expert layer's products: warp 0 copies A,
 // the last warp but one copies B (TMA, one box each where the widths are multiples of 128 bytes),
-// lane 0 of the first CTA's warp 1 issues the MMAs (256 x BN x 32 bytes), the eight epilogue warps read
+// lane 0 of the first CTA's warp 1 issues the MMAs (256 x BN x 32 bytes), the epilogue warps read
 // one accumulator of TMEM while the next tile runs into the other.  Tiles are equal, so a
 // pair takes tiles t = pair, pair + pairs, ...: row tiles inner within groups of `group`, so that pairs
 // at work at the same time share operands in the L2.
@@ -88,17 +88,21 @@ struct GemmArgs {
   int32_t clear;            // this kernel is the call's first: it clears the error word
 };
 
-constexpr int kEpiWarps = 8;
-constexpr int kGemmThreads = (kEpiWarps + 4) * 32;
-constexpr int kWarpOut = 4096;            // two blocks of 32 rows x 32 columns
-template <int BN>
+template <int MODE, bool GATED, int BN>
 struct GemmCfg {
+  // Epilogue warps: four for a tile's 128 rows, two or four such groups side by side over its columns.  Sixteen
+  // warps hide each other's latencies (us with eight / sixteen: GeLU, bias and residual, 4096 x 1024 x 4096 38.3 /
+  // 35.3, no activation in e4m3 18.5 / 17.2); a gate's registers are too many for that, and the
+  // gradients' epilogue is too short (13.6 / 13.8 for 333 x 1000 x 776).
+  static constexpr int kEpi = MODE == FWD && !GATED ? 16 : 8;
+  static constexpr int kThreads = (kEpi + 4) * 32;
+  static constexpr int kWarpOut = 32 * 1024 / kEpi;        // blocks of 32 rows x 32 columns, 2 KB each
   static constexpr int kBlocks = 2;                        // blocks of 128 bytes of the reduction in a stage
   static constexpr int kABytes = kBlocks * 128 * 128;      // a CTA's share of A in a stage
   static constexpr int kBBytes = kBlocks * BN / 2 * 128;   // and of B
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 192 * 1024 / kStageBytes;
-  static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kWarpOut + 1024;
+  static constexpr int kSmem = kStages * kStageBytes + kEpi * kWarpOut + 1024;
 };
 
 // 16 bytes of bf16 or fp32 values that all lanes read
@@ -137,7 +141,7 @@ template <bool E4M3>
 __device__ __forceinline__ void finish32(const Epilogue& e, float xs, float ws, float bs, float (&z)[32]) {
   if (E4M3) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) z[j] *= xs * __shfl_sync(0xffffffffu, ws, j);
+    for (int j = 0; j < 32; ++j) z[j] = z[j] * xs * __shfl_sync(0xffffffffu, ws, j);
   }
   if (e.bias) {
 #pragma unroll
@@ -168,13 +172,15 @@ __device__ __forceinline__ void store_checkpoint(const Epilogue& e, const float 
 }
 
 template <int MODE, bool E4M3, bool GATED, int BN>
-__global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
-  using C = GemmCfg<BN>;
+__global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
+  using C = GemmCfg<MODE, GATED, BN>;
   constexpr bool kMnB = MODE != FWD;
   constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes, kABytes = C::kABytes, kBBytes = C::kBBytes;
   constexpr int kBlocks = C::kBlocks, kChunk = kBlocks * 64 * 128;  // an "along" operand's 64 columns in a stage
   constexpr int kElems = E4M3 ? 128 : 64;        // reduction elements in 128 bytes
   constexpr int kTileN = GATED ? BN / 2 : BN;    // output columns of a tile
+  constexpr int kEpiWarps = C::kEpi, kWarpOut = C::kWarpOut, kOuts = kWarpOut / 2048;
+  constexpr int kWarpN = kTileN / (kEpiWarps / 4);  // of an epilogue warp
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
@@ -383,20 +389,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
       float xs = 1.0f;
       if (E4M3 && in) xs = e.Xs[row];
       constexpr int G = GATED ? 2 : 1;
-      Ahead<G> now, next;
-      if (MODE == FWD) next = load_ahead<E4M3, G>(e, p.N, n0 + half * (kTileN / 2), row, in);
+      Ahead<G> now;
+      if (MODE == FWD) now = load_ahead<E4M3, G>(e, p.N, n0 + half * kWarpN, row, in);
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t d = tmem + buf * BN + lanes;
 #pragma unroll 1
-      for (int i = 0; i < kTileN / 64; ++i) {
-        const int at = half * (kTileN / 2) + 32 * i, c = n0 + at, left = p.N - c;  // columns from c on
+      for (int i = 0; i < kWarpN / 32; ++i) {
+        const int at = half * kWarpN + 32 * i, c = n0 + at, left = p.N - c;  // columns from c on
         if (left <= 0 || row0 >= p.M) break;
-        if (MODE == FWD) {
-          now = next;
-          if (i + 1 < kTileN / 64) next = load_ahead<E4M3, G>(e, p.N, c + 32, row, in);
-        }
         float z[32], u[32];
         {
           uint32_t v[32];
@@ -435,12 +437,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
               for (int k = 0; k < 8; ++k) z[8 * j + k] += f[k];
             }
           }
+          if (i + 1 < kWarpN / 32) now = load_ahead<E4M3, G>(e, p.N, c + 32, row, in);
         }
         // a lane's 32 columns: four 16-byte pieces of 64-byte rows, placed as the map's 64-byte swizzle
         // has them; rows and columns outside the matrix are not written
-        if (lane == 0) ptx::bulk_wait_group_read<1>();
+        if (lane == 0) ptx::bulk_wait_group_read<kOuts - 1>();
         __syncwarp();
-        uint8_t* block = stage + (blocks & 1) * 2048;
+        uint8_t* block = stage + (blocks % kOuts) * 2048;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint32_t p[4];

@@ -73,11 +73,26 @@ __device__ __forceinline__ uint32_t block_exponent(float most) {
 __device__ __forceinline__ float exponent_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 __device__ __forceinline__ float exponent_value(uint32_t e) { return __uint_as_float(e << 23); }
 
-// 1 / (1 + e^-x); the fast exponential and division are within a few 1e-7 of it
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// 2^x and 1 / x to 2 ulp; beyond fp32's range 0 and infinity
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
-// GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3))
-__device__ __forceinline__ float gelu_gate(float z) { return sigmoid_fast(2.0f * kGeluC * (z + 0.044715f * z * z * z)); }
+// 1 / (1 + e^-x)
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(x * -kLog2e)); }
+// GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3)); the sigmoid's argument as z (a + b z^2)
+__device__ __forceinline__ float gelu_gate(float z) {
+  constexpr float a = -2.0f * kGeluC * kLog2e, b = 0.044715f * a;
+  return rcp_fast(1.0f + exp2_fast(z * fmaf(z * z, b, a)));
+}
 
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SWIGLU = 3 };
 

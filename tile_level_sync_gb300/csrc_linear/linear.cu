@@ -76,7 +76,7 @@ cudaError_t prepare_kernel(const void* f, int smem) {
 }
 template <int MODE, bool E4M3, bool GATED, int BN>
 cudaError_t prepare_gemm() {
-  return prepare_kernel(reinterpret_cast<const void*>(&gemm_kernel<MODE, E4M3, GATED, BN>), GemmCfg<BN>::kSmem);
+  return prepare_kernel(reinterpret_cast<const void*>(&gemm_kernel<MODE, E4M3, GATED, BN>), GemmCfg<MODE, GATED, BN>::kSmem);
 }
 template <int MODE, bool E4M3, bool GATED>
 cudaError_t prepare_split() {
@@ -285,9 +285,9 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
 }
 
 // A product on pairs; along: P's rows are the reduction's (dWt).  Q's are, too, in both gradients.
-template <bool E4M3, bool GATED, int BN>
-bool fill_shape(GemmShape* g, const Product& p, bool grad, bool along) {
-  constexpr int bytes = E4M3 ? 1 : 2, n = GemmCfg<BN>::kBlocks;
+template <int MODE, bool E4M3, bool GATED, int BN>
+bool fill_shape(GemmShape* g, const Product& p, bool along) {
+  constexpr int bytes = E4M3 ? 1 : 2, n = GemmCfg<MODE, GATED, BN>::kBlocks;
   g->M = (int32_t)p.rows;
   g->N = (int32_t)p.cols;
   g->K = (int32_t)p.depth;
@@ -297,7 +297,7 @@ bool fill_shape(GemmShape* g, const Product& p, bool grad, bool along) {
   g->along = along;
   return (along ? map_along(&g->mA, p.P, p.depth, p.rows, 64 * n, 2, &g->wideA)
                 : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, 128, n, &g->wideA)) &&
-         (grad ? map_along(&g->mB, p.Q, p.depth, p.cols, 64 * n, BN / 128, &g->wideB)
+         (MODE == GRAD ? map_along(&g->mB, p.Q, p.depth, p.cols, 64 * n, BN / 128, &g->wideB)
                : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, BN / 2, n, &g->wideB)) &&
          map_output(&g->mO, p.e.out, p.rows, p.cols);
 }
@@ -305,7 +305,7 @@ template <int MODE, bool E4M3, bool GATED, int BN>
 cudaError_t launch_gemm(const GemmArgs& a, int sms, cudaStream_t s) {
   const int64_t tiles = (int64_t)a.p[0].m_tiles * a.p[0].n_tiles + (int64_t)a.p[1].m_tiles * a.p[1].n_tiles;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, sms / 2);
-  return launch_cluster(2, gemm_kernel<MODE, E4M3, GATED, BN>, dim3(grid), kGemmThreads, GemmCfg<BN>::kSmem, s, a);
+  return launch_cluster(2, gemm_kernel<MODE, E4M3, GATED, BN>, dim3(grid), GemmCfg<MODE, GATED, BN>::kThreads, GemmCfg<MODE, GATED, BN>::kSmem, s, a);
 }
 
 template <bool E4M3, bool GATED>
@@ -320,9 +320,9 @@ cudaError_t forward(const Product& p, int32_t* err, int sms, cudaStream_t s) {
   a.err = err;
   a.clear = true;
   if (pair.bn == 256)
-    return fill_shape<E4M3, GATED, 256>(&a.p[0], p, false, false) ? launch_gemm<FWD, E4M3, GATED, 256>(a, sms, s)
+    return fill_shape<FWD, E4M3, GATED, 256>(&a.p[0], p, false) ? launch_gemm<FWD, E4M3, GATED, 256>(a, sms, s)
                                                                   : cudaErrorInvalidValue;
-  return fill_shape<E4M3, GATED, 128>(&a.p[0], p, false, false) ? launch_gemm<FWD, E4M3, GATED, 128>(a, sms, s)
+  return fill_shape<FWD, E4M3, GATED, 128>(&a.p[0], p, false) ? launch_gemm<FWD, E4M3, GATED, 128>(a, sms, s)
                                                                 : cudaErrorInvalidValue;
 }
 
@@ -345,7 +345,7 @@ cudaError_t pair_gradients(const Product* dx, const Product* dw, const Sums& sum
   a.part_cols = (int32_t)sums.cols;
   const bool dw_first = dw && (!dx || dw->depth > dx->depth);
   GemmShape *gx = &a.p[dw_first ? 1 : 0], *gw = &a.p[dw_first || !dx ? 0 : 1];
-  if ((dx && !fill_shape<false, false, BN>(gx, *dx, true, false)) || (dw && !fill_shape<false, false, BN>(gw, *dw, true, true)))
+  if ((dx && !fill_shape<GRAD, false, false, BN>(gx, *dx, false)) || (dw && !fill_shape<GRAD, false, false, BN>(gw, *dw, true)))
     return cudaErrorInvalidValue;
   return launch_gemm<GRAD, false, false, BN>(a, sms, s);
 }
