@@ -77,6 +77,7 @@ struct GemmShape {
   int32_t m_tiles, n_tiles, group;
   int32_t wideA, wideB;     // one box brings an operand's whole share of a stage
   int32_t along;            // GRAD: A's rows are the reduction's
+  int32_t b_first;          // B is the first to leave the L2
 };
 struct GemmArgs {
   GemmShape p[2];           // FWD: [0]
@@ -236,7 +237,8 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
   if (warp == 0 || warp == kEpiWarps + 2) {
     // ------------------------------------------------------------ copies
     const bool copies_a = warp == 0;
-    const uint64_t pol = ptx::l2_policy_evict_normal();
+    const bool leaves = MODE == FWD && !copies_a && a.p[0].b_first;
+    const uint64_t pol = leaves ? ptx::l2_policy_evict_first() : ptx::l2_policy_evict_normal();
     const bool one = ptx::elect_one();
     uint8_t* base = ring + (copies_a ? 0 : kABytes);
     constexpr int kBRows = BN / 2;  // of a CTA

@@ -19,6 +19,7 @@ namespace {
 constexpr int64_t kDzBlocks = 1024;  // blocks of the pass over dY, about
 constexpr int64_t kDzRows = 32;      // rows of such a block at least
 constexpr int kSmemPerSm = 227 * 1024;
+constexpr int64_t kResident = 48 << 20;  // bytes of an operand that the L2 (129 MB on two dies) keeps beside what passes by
 
 // What a descriptor means.
 struct Layer {
@@ -293,7 +294,15 @@ bool fill_shape(GemmShape* g, const Product& p, bool along) {
   g->K = (int32_t)p.depth;
   g->m_tiles = (int32_t)div_up(p.rows, 256);
   g->n_tiles = (int32_t)div_up(p.cols, GATED ? BN / 2 : BN);
-  g->group = std::min(g->m_tiles, 8);
+  // Row tiles whose A stays in the L2 while the columns' B passes by: as few groups as such a share allows, and B
+  // marked to leave first where one group is all and both do not fit.  Under the power cap bytes from HBM cost
+  // MMAs (us of passes for seconds; groups of 2, 4, 8, 16 row tiles, 29 to 34 MB of A in 16: SwiGLU 4096 x 8192 x 3584 in
+  // e4m3 158, 157, 156, 153, linear 4096 x 3584 x 8192 169, 163, 160, 157, with B leaving first 149 and 154.5; both gradients
+  // of the first, 59 MB in 16 and in 28: 650, 629, 615, 618; by shares of 20, 36, 48, 64 MB 611, 610, 607, 623).
+  const int64_t a_bytes = p.rows * p.depth * bytes, b_bytes = p.cols * (GATED ? 2 : 1) * p.depth * bytes;
+  const int64_t groups = std::min<int64_t>(std::max<int64_t>(1, div_up(a_bytes, kResident)), g->m_tiles);
+  g->group = (int32_t)div_up(g->m_tiles, groups);
+  g->b_first = MODE == FWD && groups == 1 && a_bytes + b_bytes > 3 * kResident / 2;
   g->along = along;
   return (along ? map_along(&g->mA, p.P, p.depth, p.rows, 64 * n, 2, &g->wideA)
                 : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, 128, n, &g->wideA)) &&
