@@ -99,7 +99,7 @@ def test_norm_of_odd_rows():
         assert abs(sc[r] - x[r][ok].float().abs().max() / 448) <= 2.0 ** -22 * sc[r]
 
 
-@pytest.mark.parametrize("M,D", NORMS + [(2000, 1000), (700, 8200), (330, 16392)])
+@pytest.mark.parametrize("M,D", NORMS + [(2000, 1000), (700, 8200), (330, 16392), (330, 32768)])
 @pytest.mark.parametrize("residual", [True, False])
 def test_norm_grad(M, D, residual):
     s = norm_inputs(M, D, residual)
@@ -204,6 +204,25 @@ def test_linear(M, K, N, act, dtype):
     assert_checkpoint(got["Zq"], got["Ze"], z, dz, m.info.parts, "Z")
     # without the checkpoint, the same Y
     assert torch.equal(run_linear(m, s)["Y"], got["Y"])
+
+
+@pytest.mark.parametrize("M,K,N", [(33, 16384, 136), (1, 16400, 1032), (600, 16400, 2056)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_linear_long_sums(M, K, N, dtype):
+    """Sums of whole numbers that 24 bits hold come out exactly, whatever the order; others within the bound."""
+    g = torch.Generator().manual_seed(M)
+    s = linear_inputs(M, K, N, "none", dtype, bias=False, residual=False)
+    m = layer(M, K, N, "none", dtype)
+    Y, bound, _, _ = oracle_linear(s, "none")
+    assert_within(run_linear(m, s)["Y"], Y, bound, "Y")
+    x, w = torch.randint(-8, 9, (M, K), generator=g).float(), torch.randint(-8, 9, (N, K), generator=g).float()
+    w[:, 128:] *= torch.rand(N, 1, generator=g) < 0.5
+    s["X"], s["Wt"] = (t.to(F8 if dtype == "e4m3" else BF) for t in (x, w))
+    if dtype == "e4m3":
+        s["Xs"], s["Ws"] = torch.ones(M), torch.full((N,), 2.0 ** -4)
+        w = w * 2.0 ** -4
+    want = (x.double() @ w.double().t()).numpy()
+    assert np.array_equal(f64(run_linear(m, s)["Y"]), round_to_bf16(want))
 
 
 @pytest.mark.parametrize("M,K,N", [(5, 1000, 776), (1281, 520, 2056)])
@@ -487,6 +506,60 @@ def test_calls_side_by_side():
     for i in (0, 1):
         assert all(torch.equal(blocks[i][1][k].view(torch.uint8), wants[i][k].view(torch.uint8)) for k in OUTS)
         assert blocks[i][0]["up"].check(blocks[i][1]["work"])[0] == cs.OK
+
+
+@pytest.mark.parametrize("M", [40, 1300])
+def test_one_graph_after_another_with_one_buffer(M):
+    """Two captured passes that share a work buffer, replayed in order on one stream; a capture behind other work."""
+    K, N = 1000, 776
+    s = [linear_inputs(M, K, N, "gelu", "bf16", seed=i, grad=True) for i in (1, 2)]
+    m = layer(M, K, N, "gelu")
+    want = [run_linear_grad(m, x) for x in s]
+    work = torch.empty(m.info.grad_work_bytes, dtype=torch.uint8, device="cuda")
+    d = [cuda(x) for x in s]
+    out = [{k: torch.zeros_like(v) for k, v in w.items()} for w in want]
+    graphs = []
+    for x, o in zip(d, out):
+        g = torch.cuda.CUDAGraph()
+        torch.cuda._sleep(1000000)
+        with torch.cuda.graph(g):
+            m.run_grad(x["X"], x["Wt"], x["dY"], work, o["dX"], o["dWt"], o["dbias"], Zq=x["Zq"], Ze=x["Ze"])
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(out, want):
+        assert all(torch.equal(o[k], w[k]) for k in w)
+    assert m.check(work)[0] == cs.OK
+
+
+def test_calls_beside_other_kernels_of_the_library():
+    """A layer of experts on one stream and linear layers on another, which share the SMs' tensor memory."""
+    from moe_helpers import layer as experts, mlp_inputs
+    x = mlp_inputs(700, 8, 2, 1024, 512, "swiglu")
+    moe, dx = experts(x, "swiglu"), {k: v.cuda() for k, v in x.items()}
+    mwork, Y = torch.empty(moe.info.work_bytes, dtype=torch.uint8, device="cuda"), torch.empty_like(dx["X"])
+    moe.mlp(dx["X"], dx["W1t"], dx["W2t"], dx["ids"], dx["weights"], mwork, Y)
+    want = Y.clone()
+    layers = []
+    for M, K, N in ((20, 1024, 1032), (1300, 520, 2056), (200, 4096, 264)):
+        s = linear_inputs(M, K, N, "swiglu")
+        m = layer(M, K, N, "swiglu")
+        layers.append((m, cuda(s), torch.empty(m.info.work_bytes, dtype=torch.uint8, device="cuda"),
+                       torch.empty(M, N, dtype=BF, device="cuda"), run_linear(m, s)["Y"]))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        with torch.cuda.stream(a):
+            moe.mlp(dx["X"], dx["W1t"], dx["W2t"], dx["ids"], dx["weights"], mwork, Y)
+        with torch.cuda.stream(b):
+            for m, d, work, y, _ in layers:
+                m.run(d["X"], d["Wt"], work, y, bias=d["bias"], R=d["R"])
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and moe.check(mwork)[0] == cs.OK
+    for m, d, work, y, w in layers:
+        assert torch.equal(y, w) and m.check(work)[0] == cs.OK
 
 
 def test_no_rows():

@@ -34,8 +34,9 @@ cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
       d->act > CUSYNC_LINEAR_SWIGLU || (d->dtype != CUSYNC_LINEAR_BF16 && d->dtype != CUSYNC_LINEAR_E4M3))
     return CUSYNC_ERR_INVALID_ARG;
   L->e4m3 = d->dtype == CUSYNC_LINEAR_E4M3;
-  // the kernels count rows, columns, tiles and blocks in 32 bits
+  // the kernels count rows, columns, tiles and blocks in 32 bits; a tensor map's strides are below 2^40 bytes
   if (d->N % 8 || d->K % (L->e4m3 ? 16 : 8) || d->K > (1 << 24) || d->N > (1 << 24) || d->M > (1 << 30) ||
+      d->K * d->N >= (int64_t)1 << 38 ||
       div_up(d->M, 16) * div_up(std::max(d->N, d->K), 64) > INT32_MAX / 8 ||
       div_up(2 * d->N, 64) * div_up(d->K, 64) > INT32_MAX / 8 || div_up(d->M * d->K, 1 << 15) > INT32_MAX / 2)
     return CUSYNC_ERR_UNSUPPORTED;
