@@ -129,9 +129,9 @@ cusync_status_t cusync_linear(const cusync_linear_desc_t* d, const void* X, cons
  * [parts*N, K] and dbias [parts*N] in bf16; each NULL where it is not wanted, at least one
  * is.  Zq and Ze: the checkpoint (NULL for act NONE).  Wt [parts*N, K] is always bf16 (needed
  * for dX).  X (needed for dWt): bf16, or E4M3: 8-bit rows with Xs.  The gradient at the
- * pre-activations is rounded to bf16 before the products that read it (for dWt of 8-bit rows:
- * that gradient times the row's scale); dbias is summed before that rounding.  work:
- * grad_work_bytes of scratch. */
+ * pre-activations is rounded to bf16 before the products that read it (with dWt of 8-bit rows:
+ * times the fraction of the row's scale, a factor of at most 2); dbias is summed before that
+ * rounding.  work: grad_work_bytes of scratch. */
 cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X, const float* Xs, const void* Wt,
                                    const void* Zq, const uint8_t* Ze, const void* dY, void* work, void* dX,
                                    void* dWt, void* dbias, cusync_stream_t stream);

@@ -166,24 +166,28 @@ def checkpoint(z, parts):
 
 def linear_grad(X, Xs, Wt, z, dY, kind):
     """{name: (gradient, bound)}; z: what the checkpoint stands for (None for kind "none").  X in bf16,
-    or the values of 8-bit rows with scales Xs: dWt is the product of the rounded dZ * Xs with them then."""
+    or the values of 8-bit rows with scales Xs = f * 2^e, f in [1, 2): dZ is rounded times f then,
+    for dWt, and with an activation for dX, too."""
     dz, err = slope(z, dY, kind)
     err = err + 2.0 ** -24 * np.abs(dz)
 
-    def rounded(v, e, exact):
-        d = v if exact else round_to_bf16(v)
-        slack = np.zeros_like(v) if exact else np.maximum(np.abs(round_to_bf16(v - e) - d), np.abs(round_to_bf16(v + e) - d))
-        return d, slack
-    dx, sx = rounded(dz, err, kind == "none")
-    dw, sw = dx, sx
+    def rounded(f, exact):
+        v, e = dz * f, err * f + (0 if np.isscalar(f) else 2.0 ** -24 * np.abs(dz * f))
+        if exact:
+            return v, np.zeros_like(v)
+        d = round_to_bf16(v)
+        return d, np.maximum(np.abs(round_to_bf16(v - e) - d), np.abs(round_to_bf16(v + e) - d))
+    f, x = 1.0, X
     if Xs is not None:
-        v = dz * Xs[:, None]
-        dw, sw = rounded(v, err * Xs[:, None] + 2.0 ** -24 * np.abs(v), False)
+        fraction, exponent = np.frexp(Xs)
+        f, x = 2 * fraction[:, None], X * np.ldexp(1.0, exponent - 1)[:, None]
+    dw, sw = rounded(f, kind == "none" and Xs is None)
+    dx, sx = (dw / f, sw / f) if kind != "none" else rounded(1.0, True)
     out = {}
     M, H = dz.shape
     for name, value, mag, loose, depth in (
             ("dX", dx @ Wt, np.abs(dx) @ np.abs(Wt), sx @ np.abs(Wt), H),
-            ("dWt", dw.T @ X, np.abs(dw).T @ np.abs(X), sw.T @ np.abs(X), M)):
+            ("dWt", dw.T @ x, np.abs(dw).T @ np.abs(x), sw.T @ np.abs(x), M)):
         e = (depth / 16 + 16) * STEP * mag + loose
         out[name] = (value, e + BF16 * (np.abs(value) + e))
     b = dz.sum(axis=0)

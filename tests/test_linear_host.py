@@ -77,7 +77,7 @@ def test_oracle_linear_grad_is_the_difference_quotient(act):
         got, bound = ref.linear_grad(X, None, Wt, None if act == "none" else z, dY, act)[name]
         assert np.all(bound >= 0) and np.allclose(got, want, atol=0.2, rtol=0.02), name
         # rows of 8 bits: the same for their values
-        Xs = 2.0 ** np.arange(-2, 2)
+        Xs = np.array([0.3, 1.0, 1.7, 5.0])
         again, _ = ref.linear_grad(X / Xs[:, None], Xs, Wt, None if act == "none" else z, dY, act)[name]
         assert np.allclose(again, want, atol=0.2, rtol=0.02), name
 
@@ -145,8 +145,8 @@ def test_sizes():
     assert cs.cusync_norm_info(cs.make_norm_desc(**NORM)).grad_work_bytes >= 64 * 4 * 10
     i = cs.cusync_linear_info(cs.make_linear_desc(M=10, K=64, N=104, act="swiglu", dtype="e4m3"))
     assert (i.parts, i.blocks) == (2, 4)
-    # dZ, dZ times X's scales, X in bf16 and the bias's partial sums
-    assert i.work_bytes >= 4 and i.grad_work_bytes >= i.work_bytes + 2 * 10 * 208 * 2 + 10 * 64 * 2 + 208 * 4
+    # dZ, X in bf16 and the bias's partial sums
+    assert i.work_bytes >= 4 and i.grad_work_bytes >= i.work_bytes + 10 * 208 * 2 + 10 * 64 * 2 + 208 * 4
     small = cs.cusync_linear_info(cs.make_linear_desc(M=10, K=64, N=104))
     assert small.parts == 1 and small.grad_work_bytes < i.grad_work_bytes
 

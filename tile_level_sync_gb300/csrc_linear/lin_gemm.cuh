@@ -81,7 +81,7 @@ struct GemmShape {
 };
 struct GemmArgs {
   GemmShape p[2];           // FWD: [0]
-  Epilogue e;               // FWD
+  Epilogue e;               // FWD; GRAD: Xs, by the fractions of which dX's rows are divided, or NULL
   const float* part;        // GRAD: dbias's partial sums [part_rows][part_cols], or NULL
   uint16_t* sums;
   int32_t part_rows, part_cols;
@@ -390,6 +390,8 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
       const bool in = row < p.M;
       float xs = 1.0f;
       if (E4M3 && in) xs = e.Xs[row];
+      const bool divide = MODE == GRAD && e.Xs && !p.along;
+      if (divide && in) xs = 1.0f / scale_fraction(e.Xs[row]);
       constexpr int G = GATED ? 2 : 1;
       Ahead<G> now;
       if (MODE == FWD) now = load_ahead<E4M3, G>(e, p.N, n0 + half * kWarpN, row, in);
@@ -440,6 +442,10 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
             }
           }
           if (i + 1 < kWarpN / 32) now = load_ahead<E4M3, G>(e, p.N, c + 32, row, in);
+        }
+        if (divide) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] *= xs;
         }
         // a lane's 32 columns: four 16-byte pieces of 64-byte rows, placed as the map's 64-byte swizzle
         // has them; rows and columns outside the matrix are not written

@@ -86,6 +86,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+// A row's scale as f * 2^e with f in [1, 2): f, and 2^e.
+__device__ __forceinline__ float scale_fraction(float s) {
+  return __uint_as_float((__float_as_uint(s) & 0x007fffffu) | 0x3f800000u);
+}
+__device__ __forceinline__ float scale_power(float s) { return __uint_as_float(__float_as_uint(s) & 0x7f800000u); }
+
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(x * -kLog2e)); }
 // GeLU_tanh(z) = z sigmoid(2 c (z + 0.044715 z^3)); the sigmoid's argument as z (a + b z^2)

@@ -337,6 +337,11 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
       }
     }
     if (!in) continue;
+    if (MODE == DX && e.Xs) {  // the rows of its operand came times the fractions of X's scales
+      const float f = 1.0f / scale_fraction(e.Xs[row]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] *= f;
+    }
     const int64_t at = (int64_t)row * a.N + c;
     if (MODE == FWD && e.R) {
       float f[8];

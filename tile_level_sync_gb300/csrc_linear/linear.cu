@@ -26,7 +26,7 @@ struct Layer {
   int64_t M, K, N, G, blocks;
   bool e4m3;
   int64_t dz_rows, dz_parts;               // rows of a block of the pass over dY; blocks along M
-  int64_t dz, dzs, x, part, work_bytes, grad_bytes;  // gradient work, bytes
+  int64_t dz, x, part, work_bytes, grad_bytes;  // gradient work, bytes
 };
 
 cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
@@ -55,8 +55,7 @@ cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
     return at;
   };
   L->work_bytes = b;
-  L->dz = bytes(d->act == CUSYNC_LINEAR_NONE ? 0 : L->M * L->G * L->N * 2);
-  L->dzs = bytes(L->e4m3 ? L->M * L->G * L->N * 2 : 0);
+  L->dz = bytes(d->act == CUSYNC_LINEAR_NONE && !L->e4m3 ? 0 : L->M * L->G * L->N * 2);
   L->x = bytes(L->e4m3 ? L->M * L->K * 2 : 0);
   L->part = bytes(L->dz_parts * L->G * L->N * 4);
   L->grad_bytes = b;
@@ -353,6 +352,7 @@ cudaError_t pair_gradients(const Product* dx, const Product* dw, const Sums& sum
   a.sums = sums.out;
   a.part_rows = (int32_t)sums.rows;
   a.part_cols = (int32_t)sums.cols;
+  if (dx) a.e.Xs = dx->e.Xs;
   const bool dw_first = dw && (!dx || dw->depth > dx->depth);
   GemmShape *gx = &a.p[dw_first ? 1 : 0], *gw = &a.p[dw_first || !dx ? 0 : 1];
   if ((dx && !fill_shape<GRAD, false, false, BN>(gx, *dx, false)) || (dw && !fill_shape<GRAD, false, false, BN>(gw, *dw, true)))
@@ -494,6 +494,7 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
   int32_t* err = static_cast<int32_t*>(work);
   bool clear = true;
   cudaError_t e = cudaSuccess;
+  // 8-bit X: dWt's operand is dZ times the fractions of its scales, and dX's the same but where dY itself will do
   const bool scaled = L.e4m3 && dWt;
   const void* dZ = act ? w + L.dz : dY;
   if (act || dbias || scaled) {
@@ -501,13 +502,13 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
     a.dY = static_cast<const uint16_t*>(dY);
     a.Zq = static_cast<const uint8_t*>(Zq);
     a.Ze = Ze;
-    a.dZ = act && (dX || (dWt && !scaled)) ? reinterpret_cast<uint16_t*>(w + L.dz) : nullptr;
+    a.dZ = scaled || (act && (dX || dWt)) ? reinterpret_cast<uint16_t*>(w + L.dz) : nullptr;
     if (scaled) {
       a.Xs = Xs;
-      a.dZs = reinterpret_cast<uint16_t*>(w + L.dzs);
       a.q = static_cast<const uint4*>(X);
       a.x = reinterpret_cast<uint4*>(w + L.x);
       a.pieces = L.M * (L.K / 16);
+      a.row_pieces = (int32_t)(L.K / 16);
     }
     a.part = dbias ? reinterpret_cast<float*>(w + L.part) : nullptr;
     a.err = err;
@@ -525,7 +526,8 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
   }
   Product dx = {}, dw = {};
   dx.P = dZ;
-  dw.P = scaled ? w + L.dzs : dZ;
+  dx.e.Xs = scaled && act ? Xs : nullptr;
+  dw.P = scaled ? w + L.dz : dZ;
   dx.Q = Wt;
   dx.rows = L.M;
   dx.cols = L.K;
