@@ -20,7 +20,7 @@ def _norm(M, D, kind="rms", **more):
     return cs.Norm(cs.make_norm_desc(M=M, D=D, kind=kind, eps=EPS, **more))
 
 
-NORMS = [(1, 8), (3, 1000), (300, 136), (5, 2048), (2, 2056), (4, 4104), (3, 8192), (3, 8200), (2, 16392), (2, 32768), (5000, 64)]
+NORMS = [(1, 8), (3, 1000), (300, 136), (5, 2048), (2, 2056), (4, 4104), (3, 8192), (3, 8200), (2, 16392), (2, 32768), (5000, 64), (7, 256), (9, 1024), (9, 1032), (2100, 256), (2051, 1000)]
 
 
 @pytest.mark.parametrize("M,D", NORMS)
@@ -99,7 +99,8 @@ def test_norm_of_odd_rows():
         assert abs(sc[r] - x[r][ok].float().abs().max() / 448) <= 2.0 ** -22 * sc[r]
 
 
-@pytest.mark.parametrize("M,D", NORMS + [(2000, 1000), (700, 8200), (330, 16392), (330, 32768)])
+@pytest.mark.parametrize("M,D", NORMS + [(2000, 1000), (700, 8200), (330, 16392), (330, 32768), (3000, 8), (9000, 256), (3000, 1024), (2500, 1032),
+                                         (1300, 4096), (400, 12288), (400, 20480), (200, 1024)])
 @pytest.mark.parametrize("residual", [True, False])
 def test_norm_grad(M, D, residual):
     s = norm_inputs(M, D, residual)

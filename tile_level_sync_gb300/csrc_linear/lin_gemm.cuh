@@ -481,8 +481,13 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
     // ------------------------------------------------------------ dbias: 32 columns at a time, rows in order
     for (int c = blockIdx.x * 32 + lane; c < a.part_cols; c += gridDim.x * 32) {
       float sum = 0.0f;
-#pragma unroll 8
-      for (int r = 0; r < a.part_rows; ++r) sum += a.part[(int64_t)r * a.part_cols + c];
+      for (int r = 0; r < a.part_rows; r += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = r + k < a.part_rows ? a.part[(int64_t)(r + k) * a.part_cols + c] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum += v[k];
+      }
       a.sums[c] = __bfloat16_as_ushort(__float2bfloat16_rn(sum));
     }
     __syncwarp();

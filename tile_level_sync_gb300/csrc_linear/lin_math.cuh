@@ -117,13 +117,19 @@ static __global__ void __launch_bounds__(256) column_sum_kernel(const float* par
   const int c = blockIdx.x * 32 + piece * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < cols) {
-#pragma unroll 4
-    for (int r = group; r < rows; r += 32) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)r * cols + c);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+    for (int r0 = group; r0 < rows; r0 += 32 * 8) {  // eight loads at a time, whatever is left
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = r0 + 32 * k < rows ? *reinterpret_cast<const float4*>(part + (int64_t)(r0 + 32 * k) * cols + c)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s.x += v[k].x;
+        s.y += v[k].y;
+        s.z += v[k].z;
+        s.w += v[k].w;
+      }
     }
   }
   sums[group][piece] = s;

@@ -1,53 +1,56 @@
 // The norm and its gradient, and 8-bit rows.  Bound by memory: every tensor is read or written
 // once, in 16-byte pieces; sums are in 32 bits and of a fixed order.
+//
+// A row of at most kWarpVecs pieces of 8 columns is a warp's, a longer one a block's; each thread keeps up to four
+// pieces of it in registers.  (A block for each row of 256 columns took 17.4 us where warps take 5.9, 16384 rows of the
+// norm with residual and 8 bits out; the gradient of such rows 21.5 and 13.0, of 4096 rows of 1024 20.4 and 10.5.)
 #pragma once
 #include "lin_math.cuh"
 
 namespace cusync {
 namespace lin {
 
-// Sum and maximum over a block's threads, in every thread; one call in a kernel's loop needs
-// the other of the two buffers next.
-__device__ __forceinline__ float2 block_sum_max(float sum, float most, float2* buf) {
+constexpr int kWarpVecs = 128;  // 1024 columns
+constexpr int kRowWarps = 8;    // of a block whose warps take rows
+
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  }
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return make_float2(sum, most);
-  if (lane == 0) buf[threadIdx.x >> 5] = make_float2(sum, most);
-  __syncthreads();
-  const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
-  sum = v.x;
-  most = v.y;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  }
-  return make_float2(sum, most);
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
-__device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf) {
+__device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  if (warps == 1) return make_float2(a, b);
-  if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
-  a = v.x;
-  b = v.y;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  return make_float2(a, b);
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
+// The sum of a, and the sum or maximum of b, over the threads that share a row, in each of them.
+struct WarpRow {
+  static constexpr bool kBlock = false;
+  __device__ __forceinline__ void sync() const { __syncwarp(); }
+  template <bool MAX>
+  __device__ __forceinline__ float2 reduce(float a, float b, int) const {
+    return make_float2(warp_sum(a), MAX ? warp_max(b) : warp_sum(b));
+  }
+};
+struct BlockRow {
+  static constexpr bool kBlock = true;
+  __device__ __forceinline__ void sync() const { __syncthreads(); }
+  float2 (*buf)[32];  // one call needs another buffer than the one before it
+  template <bool MAX>
+  __device__ __forceinline__ float2 reduce(float a, float b, int turn) const {
+    const float2 w = WarpRow().reduce<MAX>(a, b, 0);
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) buf[turn][threadIdx.x >> 5] = w;
+    __syncthreads();
+    const float2 v = lane < warps ? buf[turn][lane] : make_float2(0.0f, 0.0f);
+    return WarpRow().reduce<MAX>(v.x, v.y, 0);
+  }
+};
+
+// Squares of a row's values leave fp32's range before the values do.  Where the mean of the squares
+// plus eps, v, is outside of what follows, the row is taken times this power of two instead.
+__device__ __forceinline__ bool squares_fit(float v) { return v >= 0x1p-100f && v <= 0x1p120f; }
+__device__ __forceinline__ float square_scale(float v) { return v > 1.0f ? 0x1p-70f : 0x1p70f; }
 
 struct NormArgs {
   const uint4 *X, *R, *w;
@@ -60,25 +63,16 @@ struct NormArgs {
   float eps, inv_d;
 };
 
-// Squares of a row's values leave fp32's range before the values do.  Where the mean of the squares
-// plus eps, v, is outside of what follows, the row is taken times this power of two instead.
-__device__ __forceinline__ bool squares_fit(float v) { return v >= 0x1p-100f && v <= 0x1p120f; }
-__device__ __forceinline__ float square_scale(float v) { return v > 1.0f ? 0x1p-70f : 0x1p70f; }
-
-// A block takes a row and keeps it in registers: V pieces of 8 columns a thread.  The sum of
-// squares and the largest |S w| come out of one pass, as the row's factor r = 1 / sqrt(mean + eps)
-// is common to all: max |y| = r max |S w|.
-template <int V, int T>
-__global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
-  __shared__ float2 buf[2][32];
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  const int64_t base = (int64_t)blockIdx.x * a.vecs;
+// One row by the threads i0, i0 + step, ...: V pieces each.  The sum of squares and the largest |S w| come
+// out of one pass, as the row's factor r = 1 / sqrt(mean + eps) is common to all: max |y| = r max |S w|.
+template <int V, typename Row>
+__device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int i0, int step, const Row& threads) {
+  const int64_t base = row * a.vecs;
   float t[V][8];
   uint4 x[V], r[V], g[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = threadIdx.x + v * blockDim.x;
+    const int i = i0 + v * step;
     x[v] = r[v] = g[v] = make_uint4(0, 0, 0, 0);
     if (i < a.vecs) {
       x[v] = a.X[base + i];
@@ -89,7 +83,7 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
   float sum = 0.0f, most = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = threadIdx.x + v * blockDim.x;
+    const int i = i0 + v * step;
     unpack8(x[v], t[v]);
     if (a.R) {
       float f[8];
@@ -111,7 +105,7 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
       for (int j = 0; j < 8; ++j) most = fmaxf(most, finite_abs(t[v][j]));
     }
   }
-  float2 all = block_sum_max(sum, most, buf[0]);
+  float2 all = threads.template reduce<true>(sum, most, 0);
   float f = 1.0f;
   if (a.rms) {
     float square = all.x * a.inv_d + a.eps, c = 1.0f;
@@ -124,12 +118,12 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
         unpack8(g[v], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float x = t[v][j] * c;
-          sum = fmaf(x, x, sum);
-          most = fmaxf(most, finite_abs(x * w[j]));
+          const float xc = t[v][j] * c;
+          sum = fmaf(xc, xc, sum);
+          most = fmaxf(most, finite_abs(xc * w[j]));
         }
       }
-      all = block_sum_max(sum, most, buf[1]);
+      all = threads.template reduce<true>(sum, most, 1);
       square = all.x * a.inv_d + a.eps * c * c;
     }
     f = 1.0f / sqrtf(square);
@@ -139,10 +133,10 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
   // the factor is NaN or 0 where the row holds NaN or infinities: nothing finite is left, or zeros
   const float scale = fmaxf(finite_abs(all.y) * (1.0f / kE4m3Max), kLeastScale);
   const float inv = 1.0f / scale;
-  if (a.Q && threadIdx.x == 0) a.Qs[blockIdx.x] = scale;
+  if (a.Q && i0 == 0) a.Qs[row] = scale;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = threadIdx.x + v * blockDim.x;
+    const int i = i0 + v * step;
     if (i >= a.vecs) continue;
     if (a.rms) {
       float w[8];
@@ -160,6 +154,21 @@ __global__ void __launch_bounds__(T) norm_kernel(const NormArgs a) {
   }
 }
 
+template <int V, int T>
+__global__ void __launch_bounds__(T) norm_block_kernel(const NormArgs a) {
+  __shared__ float2 buf[2][32];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  norm_row<V>(a, blockIdx.x, threadIdx.x, blockDim.x, BlockRow{buf});
+}
+template <int V>
+__global__ void __launch_bounds__(kRowWarps * 32) norm_warp_kernel(const NormArgs a) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int64_t row = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  if (row < a.M) norm_row<V>(a, row, threadIdx.x & 31, 32, WarpRow());
+}
+
 struct NormGradArgs {
   const uint4 *S, *w, *dY, *dS;
   uint4* dX;
@@ -167,7 +176,7 @@ struct NormGradArgs {
   int32_t* err;
   int64_t M;
   int32_t vecs;
-  int32_t stages;  // rows of the ring
+  int32_t stages;  // rows of a ring
   float eps, inv_d;
 };
 
@@ -175,40 +184,34 @@ constexpr int kNormStages = 8;
 constexpr uint64_t kNormWaitNs = 1000000000ull;
 constexpr uint32_t kNormErrWait = 3u << 24;
 
-// dX = r (g - S r mean(g S r)) + dS with g = w dY; a block takes rows blockIdx.x, + gridDim.x, ...
-// and keeps its columns' share of dw in registers.  A row's tensors come by bulk copies into a ring of
-// `stages` rows, so that the next rows are under way while this one waits for its sums: the same
-// kernel with rows loaded into registers reached 4230 GB/s where this one reaches 6090 (8192 x 8192, dS added).
-template <int V, int T>
-__global__ void __launch_bounds__(T, 1) norm_grad_kernel(const NormGradArgs a) {
-  extern __shared__ __align__(128) uint4 rows[];
-  __shared__ float2 buf[4][32];
-  __shared__ uint64_t full[kNormStages];
-  const int tensors = a.dS ? 3 : 2, stages = a.stages;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
-    ptx::mbar_init_fence();
-  }
-  __syncthreads();
-  ptx::pdl_wait();
-  ptx::pdl_launch_dependents();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+// dX = r (g - S r mean(g S r)) + dS with g = w dY.  A warp or a block takes rows first, first + stride, ... and keeps
+// its columns' share of dw in registers.  A row's tensors come by bulk copies into a ring of `stages` rows, so that the
+// next rows are under way while this one waits for its sums: with rows loaded into registers alone 8192 x 8192 (dS
+// added) took 127 us, with the ring 82 (6.5 TB/s).  Where the ring holds three rows or fewer, a row's place is refilled as
+// soon as it is read, at the price of a barrier (2000 x 12288: 39.0 us, 43.2 with the row after it).  Four pieces a
+// thread, rows above 16384 columns, leave dS out of the ring, which would hold one row with it (2000 x 20480: 120 us,
+// 131 with it).
+template <int V, typename Row>
+__device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, int64_t first, int64_t stride, int i0, int step,
+                                               const Row& threads, uint4* ring, uint64_t* full, float (&dw)[V][8]) {
+  const int stages = a.stages;
   const uint32_t bytes = (uint32_t)a.vecs * 16;
+  constexpr bool kDirect = V == 4 && Row::kBlock;  // dS
+  const int tensors = a.dS && !kDirect ? 3 : 2;
   auto fetch = [&](int64_t row, int st) {  // one thread
     if (row >= a.M) return;
-    uint4* to = rows + (int64_t)st * tensors * a.vecs;
+    uint4* to = ring + (int64_t)st * tensors * a.vecs;
     ptx::mbar_arrive_expect_tx(&full[st], tensors * bytes);
     ptx::bulk_load(to, a.S + row * a.vecs, bytes, &full[st]);
     ptx::bulk_load(to + a.vecs, a.dY + row * a.vecs, bytes, &full[st]);
-    if (a.dS) ptx::bulk_load(to + 2 * a.vecs, a.dS + row * a.vecs, bytes, &full[st]);
+    if (a.dS && !kDirect) ptx::bulk_load(to + 2 * a.vecs, a.dS + row * a.vecs, bytes, &full[st]);
   };
-  if (threadIdx.x == 0)
-    for (int i = 0; i < stages; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
-  float dw[V][8];
+  if (i0 == 0)
+    for (int i = 0; i < stages; ++i) fetch(first + i * stride, i);
   uint4 wv[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int i = threadIdx.x + v * blockDim.x;
+    const int i = i0 + v * step;
     wv[v] = i < a.vecs ? a.w[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[v][j] = 0.0f;
@@ -216,19 +219,27 @@ __global__ void __launch_bounds__(T, 1) norm_grad_kernel(const NormGradArgs a) {
   int turn = 0, st = 0;
   uint32_t par = 0;
   bool ok = true;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, turn ^= 1) {
+  for (int64_t row = first; row < a.M; row += stride, turn ^= 1) {
+    uint4 s[kDirect ? V : 1];
+    if (kDirect) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int i = i0 + v * step;
+        s[kDirect ? v : 0] = a.dS && i < a.vecs ? a.dS[row * a.vecs + i] : make_uint4(0, 0, 0, 0);
+      }
+    }
     // after a wait that gave up: on with what is there
     if (ok && !ptx::mbar_wait_bounded(&full[st], par, kNormWaitNs)) {
       ok = false;
       *a.err = (int32_t)kNormErrWait;
     }
-    const uint4 *x = rows + (int64_t)st * tensors * a.vecs, *y = x + a.vecs, *s = y + a.vecs;
+    const uint4 *x = ring + (int64_t)st * tensors * a.vecs, *y = x + a.vecs;
     float squares = 0.0f, dots = 0.0f;
     auto sums = [&](float c) {
       squares = dots = 0.0f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int i = threadIdx.x + v * blockDim.x;
+        const int i = i0 + v * step;
         if (i >= a.vecs) continue;
         float fx[8], fy[8], fw[8];
         unpack8(x[i], fx);
@@ -243,29 +254,26 @@ __global__ void __launch_bounds__(T, 1) norm_grad_kernel(const NormGradArgs a) {
       }
     };
     sums(1.0f);
-    float2 all = block_sum2(squares, dots, buf[turn]);
-    // behind that barrier every thread is done with the row before: its place takes the row `stages` further
-    if (threadIdx.x == 0 && stages > 1 && row >= gridDim.x) {
-      const int before = st ? st - 1 : stages - 1;
-      fetch(row + (int64_t)(stages - 1) * gridDim.x, before);
-    }
+    float2 all = threads.template reduce<false>(squares, dots, turn);
+    // behind these sums every thread is done with the row before: its place takes the row `stages` further
+    if (i0 == 0 && stages > 3 && row != first) fetch(row + (stages - 1) * stride, st ? st - 1 : stages - 1);
     float square = all.x * a.inv_d + a.eps, c = 1.0f;
     if (!squares_fit(square)) {
       c = square_scale(square);
       sums(c);
-      all = block_sum2(squares, dots, buf[2 + turn]);
+      all = threads.template reduce<false>(squares, dots, 2 + turn);
       square = all.x * a.inv_d + a.eps * c * c;
     }
     const float rc = 1.0f / sqrtf(square), mean = all.y * a.inv_d * rc, r = rc * c;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int i = threadIdx.x + v * blockDim.x;
+      const int i = i0 + v * step;
       if (i >= a.vecs) continue;
       float fx[8], fy[8], fw[8], fs[8];
       unpack8(x[i], fx);
       unpack8(y[i], fy);
       unpack8(wv[v], fw);
-      unpack8(a.dS ? s[i] : make_uint4(0, 0, 0, 0), fs);
+      unpack8(kDirect ? s[kDirect ? v : 0] : a.dS ? y[a.vecs + i] : make_uint4(0, 0, 0, 0), fs);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xh = fx[j] * r;
@@ -274,24 +282,77 @@ __global__ void __launch_bounds__(T, 1) norm_grad_kernel(const NormGradArgs a) {
       }
       a.dX[row * a.vecs + i] = pack8(fs);
     }
-    if (stages == 1) {
-      __syncthreads();
-      if (threadIdx.x == 0) fetch(row + gridDim.x, 0);
+    if (stages <= 3) {
+      threads.sync();
+      if (i0 == 0) fetch(row + stages * stride, st);
     }
     if (++st == stages) {
       st = 0;
       par ^= 1;
     }
   }
-  if (a.part) {
+}
+
+template <int V, int T, int PER_SM>
+__global__ void __launch_bounds__(T, PER_SM) norm_grad_block_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(128) uint4 rows[];
+  __shared__ float2 buf[4][32];
+  __shared__ uint64_t full[kNormStages];
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) ptx::mbar_init(&full[i], 1);
+    ptx::mbar_init_fence();
+  }
+  __syncthreads();
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  float dw[V][8];
+  norm_grad_rows<V>(a, blockIdx.x, gridDim.x, threadIdx.x, blockDim.x, BlockRow{buf}, rows, full, dw);
+  if (!a.part) return;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = threadIdx.x + v * blockDim.x;
-      if (i >= a.vecs) continue;
-      float4* out = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.vecs + i) * 2;
-      out[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
-      out[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
-    }
+  for (int v = 0; v < V; ++v) {
+    const int i = threadIdx.x + v * blockDim.x;
+    if (i >= a.vecs) continue;
+    float4* out = reinterpret_cast<float4*>(a.part) + ((int64_t)blockIdx.x * a.vecs + i) * 2;
+    out[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+    out[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+  }
+}
+
+// Each warp has a ring of its own; the warps' shares of dw are added in their order.
+template <int V>
+__global__ void __launch_bounds__(kRowWarps * 32) norm_grad_warp_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(128) uint4 rows[];
+  __shared__ uint64_t full[kRowWarps][kNormStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    for (int i = 0; i < a.stages; ++i) ptx::mbar_init(&full[warp][i], 1);
+    ptx::mbar_init_fence();
+  }
+  __syncthreads();
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+  float dw[V][8];
+  norm_grad_rows<V>(a, (int64_t)blockIdx.x * kRowWarps + warp, (int64_t)gridDim.x * kRowWarps, lane, 32, WarpRow(),
+                    rows + (int64_t)warp * a.stages * (a.dS ? 3 : 2) * a.vecs, full[warp], dw);
+  if (!a.part) return;
+  __syncthreads();  // the rings take [warps][D] sums
+  float* sums = reinterpret_cast<float*>(rows);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = lane + v * 32;
+    if (i >= a.vecs) continue;
+    float4* out = reinterpret_cast<float4*>(sums) + (warp * a.vecs + i) * 2;
+    out[0] = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+    out[1] = make_float4(dw[v][4], dw[v][5], dw[v][6], dw[v][7]);
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 8 * a.vecs; c += kRowWarps * 32) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) s += sums[w * 8 * a.vecs + c];
+    a.part[(int64_t)blockIdx.x * 8 * a.vecs + c] = s;
   }
 }
 
