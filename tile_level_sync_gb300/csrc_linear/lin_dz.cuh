@@ -15,6 +15,7 @@ struct DzArgs {
   uint4* x;             // and in bf16, times the powers of two in Xs
   int64_t pieces;       // M * K / 16
   int32_t row_pieces;   // K / 16
+  int64_t x_pitch, dz_pitch;  // columns from a row of x, of dZ to the next
   float* part;    // [parts][parts of a row * N] sums of dZ over a block's rows, or NULL
   int32_t* err;   // the call's error word, cleared by the call's first kernel
   int64_t M;
@@ -52,14 +53,15 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const DzArgs a) {
     for (int k = 0; k < kUnpackPieces; ++k) {
       if (i0 + k * 256 >= a.pieces) break;
       float f[2][8];
-      const float power = scale_power(a.Xs[(i0 + k * 256) / a.row_pieces]);
+      const int64_t i = i0 + k * 256, row = i / a.row_pieces;
+      const float power = scale_power(a.Xs[row]);
       unpack_e4m3(v[k].x, f[0]);
       unpack_e4m3(v[k].y, f[0] + 4);
       unpack_e4m3(v[k].z, f[1]);
       unpack_e4m3(v[k].w, f[1] + 4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[0][j] *= power, f[1][j] *= power;
-      uint4* out = a.x + 2 * (i0 + k * 256);
+      uint4* out = a.x + (row * a.x_pitch + (i - row * a.row_pieces) * 16) / 8;
       out[0] = pack8(f[0]);
       out[1] = pack8(f[1]);
     }
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const DzArgs a) {
         for (int g = 0; g < G; ++g) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) dz[g][j] *= f;
-          *reinterpret_cast<uint4*>(a.dZ + (r * G + g) * a.N + c) = pack8(dz[g]);
+          *reinterpret_cast<uint4*>(a.dZ + r * a.dz_pitch + g * a.N + c) = pack8(dz[g]);
         }
       }
     }

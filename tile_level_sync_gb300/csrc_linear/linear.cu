@@ -24,6 +24,7 @@ constexpr int64_t kResident = 48 << 20;  // bytes of an operand that the L2 (129
 // What a descriptor means.
 struct Layer {
   int64_t M, K, N, G, blocks;
+  int64_t dz_pitch, x_pitch;               // of the gradient's own operands: rows begin with a line of 128 bytes
   bool e4m3;
   int64_t dz_rows, dz_parts;               // rows of a block of the pass over dY; blocks along M
   int64_t dz, x, part, work_bytes, grad_bytes;  // gradient work, bytes
@@ -45,6 +46,8 @@ cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
   L->N = d->N;
   L->G = d->act == CUSYNC_LINEAR_SWIGLU ? 2 : 1;
   L->blocks = div_up(d->N, kBlock);
+  L->dz_pitch = round_up(L->G * L->N, 64);
+  L->x_pitch = round_up(L->K, 64);
   const int64_t columns = div_up(L->N, kDzCols);
   L->dz_rows = std::max(kDzRows, round_up(div_up(L->M, std::max<int64_t>(1, kDzBlocks / columns)), 8));
   L->dz_parts = std::max<int64_t>(1, div_up(L->M, L->dz_rows));
@@ -55,8 +58,8 @@ cusync_status_t read_desc(const cusync_linear_desc_t* d, Layer* L) {
     return at;
   };
   L->work_bytes = b;
-  L->dz = bytes(d->act == CUSYNC_LINEAR_NONE && !L->e4m3 ? 0 : L->M * L->G * L->N * 2);
-  L->x = bytes(L->e4m3 ? L->M * L->K * 2 : 0);
+  L->dz = bytes(d->act == CUSYNC_LINEAR_NONE && !L->e4m3 ? 0 : L->M * L->dz_pitch * 2);
+  L->x = bytes(L->e4m3 ? L->M * L->x_pitch * 2 : 0);
   L->part = bytes(L->dz_parts * L->G * L->N * 4);
   L->grad_bytes = b;
   return CUSYNC_OK;
@@ -125,7 +128,9 @@ cusync_status_t prepare_device(int* sms) {
 }
 
 // A map of `bytes`-wide elements: sizes and strides (in elements, from the second dimension on) and
-// the box, innermost first; elements outside read as zero.
+// the box, innermost first; elements outside read as zero.  Rows that begin inside a line of 128 bytes make a box's row
+// two of them, of which the L2 should not fetch four (4096 x K x 4096 in e4m3, us with lines fetched by twos / alone: K
+// 8048 129 / 118, 8032 102 / 95; 8064, a multiple of 128, 84 / 84).
 template <int N>
 bool map_nd(CUtensorMap* m, const void* p, int bytes, CUtensorMapSwizzle swizzle, const int64_t (&size)[N],
             const int64_t (&stride)[N - 1], const int (&box_size)[N]) {
@@ -139,17 +144,18 @@ bool map_nd(CUtensorMap* m, const void* p, int bytes, CUtensorMapSwizzle swizzle
   }
   return g_encode(m, bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N,
                   const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  stride[0] * bytes % 128 ? CU_TENSOR_MAP_L2_PROMOTION_NONE : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// An operand [rows, cols] whose columns are the reduction's: boxes of 128 bytes x box_rows; wide (columns a
-// multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of `blocks`.
-bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int box_rows, int blocks,
+// An operand [rows, cols], rows `pitch` elements apart, whose columns are the reduction's: boxes of 128 bytes x
+// box_rows; wide (columns a multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of `blocks`.
+bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int64_t pitch, int box_rows, int blocks,
               int32_t* wide) {
   const int n = 128 / bytes;
   *wide = cols % n == 0;
-  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {cols, n}, {n, box_rows, blocks})
-               : map_nd<2>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {n, box_rows});
+  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {pitch, n}, {n, box_rows, blocks})
+               : map_nd<2>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {pitch}, {n, box_rows});
 }
 // Gate and up rows of a gated layer's weights [2][rows, cols], 64 of each in a box.
 bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int blocks, int32_t* wide) {
@@ -161,10 +167,11 @@ bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t c
 }
 // A bf16 operand [rows, cols] whose rows are the reduction's: boxes of 64 columns x `box_rows` rows; wide (columns
 // a multiple of 64): as [chunks][rows][64], boxes of `chunks`.
-bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows, int chunks, int32_t* wide) {
+bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows, int chunks,
+               int32_t* wide) {
   *wide = cols % 64 == 0;
-  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {cols, 64}, {64, box_rows, chunks})
-               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {cols}, {64, box_rows});
+  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {pitch, 64}, {64, box_rows, chunks})
+               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {pitch}, {64, box_rows});
 }
 // An output [rows, cols]: boxes of 32 x 32 as a warp's lanes write them.
 bool map_output(CUtensorMap* m, void* p, int64_t rows, int64_t cols) {
@@ -175,10 +182,11 @@ bool map_output(CUtensorMap* m, void* p, int64_t rows, int64_t cols) {
 
 // One product: `rows` x `cols` outputs (SwiGLU: columns of Y), reduction `depth`.  P and Q are the
 // operands of the output's rows and columns: [rows, depth] and [cols, depth] (SwiGLU: [2 * cols, depth]),
-// or, where they lie along the output, [depth, rows] and [depth, cols].
+// or, where they lie along the output, [depth, rows] and [depth, cols]; their rows are p_pitch and q_pitch elements
+// apart.
 struct Product {
   const void *P, *Q;
-  int64_t rows, cols, depth;
+  int64_t rows, cols, depth, p_pitch, q_pitch;
   Epilogue e;
 };
 
@@ -274,11 +282,11 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
   a.blocks = plan.blocks;
   a.apart = plan.apart;
   const int n = plan.blocks;
-  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, 64 * n, 2, &a.wideA)
+  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, p.q_pitch, 64 * n, 2, &a.wideA)
                    : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, n, &a.wideA)
-                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, 128, n, &a.wideA)) &&
-                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, 64 * n, plan.cols / 64, &a.wideB)
-                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, plan.cols, n, &a.wideB));
+                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, p.q_pitch, 128, n, &a.wideA)) &&
+                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, p.p_pitch, 64 * n, plan.cols / 64, &a.wideB)
+                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, p.p_pitch, plan.cols, n, &a.wideB));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = div_up(p.cols, GATED ? 64 : 128) * a.row_tiles;
   return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)), kSplitThreads,
@@ -304,10 +312,10 @@ bool fill_shape(GemmShape* g, const Product& p, bool along) {
   g->group = (int32_t)div_up(g->m_tiles, groups);
   g->b_first = MODE == FWD && groups == 1 && a_bytes + b_bytes > 3 * kResident / 2;
   g->along = along;
-  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, 64 * n, 2, &g->wideA)
-                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, 128, n, &g->wideA)) &&
-         (MODE == GRAD ? map_along(&g->mB, p.Q, p.depth, p.cols, 64 * n, BN / 128, &g->wideB)
-               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, BN / 2, n, &g->wideB)) &&
+  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, p.p_pitch, 64 * n, 2, &g->wideA)
+                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, p.p_pitch, 128, n, &g->wideA)) &&
+         (MODE == GRAD ? map_along(&g->mB, p.Q, p.depth, p.cols, p.q_pitch, 64 * n, BN / 128, &g->wideB)
+               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, p.q_pitch, BN / 2, n, &g->wideB)) &&
          map_output(&g->mO, p.e.out, p.rows, p.cols);
 }
 template <int MODE, bool E4M3, bool GATED, int BN>
@@ -452,7 +460,7 @@ cusync_status_t cusync_linear(const cusync_linear_desc_t* d, const void* X, cons
   p.Q = Wt;
   p.rows = L.M;
   p.cols = L.N;
-  p.depth = L.K;
+  p.depth = p.p_pitch = p.q_pitch = L.K;
   p.e.Xs = Xs;
   p.e.Ws = Ws;
   p.e.bias = static_cast<const uint16_t*>(bias);
@@ -509,11 +517,13 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
       a.x = reinterpret_cast<uint4*>(w + L.x);
       a.pieces = L.M * (L.K / 16);
       a.row_pieces = (int32_t)(L.K / 16);
+      a.x_pitch = L.x_pitch;
     }
     a.part = dbias ? reinterpret_cast<float*>(w + L.part) : nullptr;
     a.err = err;
     a.M = L.M;
     a.N = (int32_t)L.N;
+    a.dz_pitch = L.dz_pitch;
     a.rows = (int32_t)L.dz_rows;
     a.col_blocks = (int32_t)div_up(L.N, kDzCols);
     a.parts = (int32_t)L.dz_parts;
@@ -528,7 +538,11 @@ cusync_status_t cusync_linear_grad(const cusync_linear_desc_t* d, const void* X,
   dx.P = dZ;
   dx.e.Xs = scaled && act ? Xs : nullptr;
   dw.P = scaled ? w + L.dz : dZ;
+  dw.p_pitch = scaled || act ? L.dz_pitch : L.N;
+  dw.q_pitch = L.e4m3 ? L.x_pitch : L.K;
+  dx.p_pitch = act ? L.dz_pitch : L.N;
   dx.Q = Wt;
+  dx.q_pitch = L.K;
   dx.rows = L.M;
   dx.cols = L.K;
   dx.depth = H;
