@@ -14,7 +14,7 @@
 //
 // A stage holds 128 bytes x 2 of the reduction for the CTA's 128 rows of A and BN / 2 of B (64 or 48 KB);
 // three or four fit beside the epilogue's staging.  Roles, as in the expert layer's products: warp 0 copies A,
-// the last warp but one copies B (TMA, one box each where the widths are multiples of 128 bytes),
+// warp kEpi + 2 copies B (TMA, one box each where the widths are multiples of 128 bytes),
 // lane 0 of the first CTA's warp 1 issues the MMAs (256 x BN x 32 bytes), the epilogue warps read
 // one accumulator of TMEM while the next tile runs into the other.  Tiles are equal, so a
 // pair takes tiles t = pair, pair + pairs, ...: row tiles inner within groups of `group`, so that pairs
@@ -77,10 +77,12 @@ struct GemmShape {
   int32_t m_tiles, n_tiles, group;
   int32_t wideA, wideB;     // one box brings an operand's whole share of a stage
   int32_t along;            // GRAD: A's rows are the reduction's
+  int32_t a_rows;           // of a CTA that are copied: 128, or fewer where there are fewer, a multiple of 8
   int32_t b_first;          // B is the first to leave the L2
 };
 struct GemmArgs {
   GemmShape p[2];           // FWD: [0]
+  CUtensorMap mR;           // FWD: the residual, as mO
   Epilogue e;               // FWD; GRAD: Xs, by the fractions of which dX's rows are divided, or NULL
   const float* part;        // GRAD: dbias's partial sums [part_rows][part_cols], or NULL
   uint16_t* sums;
@@ -96,7 +98,7 @@ struct GemmCfg {
   // 35.3, no activation in e4m3 18.5 / 17.2); a gate's registers are too many for that, and the
   // gradients' epilogue is too short (13.6 / 13.8 for 333 x 1000 x 776).
   static constexpr int kEpi = MODE == FWD && !GATED ? 16 : 8;
-  static constexpr int kThreads = (kEpi + 4) * 32;
+  static constexpr int kThreads = (kEpi + (MODE == GRAD ? 4 : 3)) * 32;  // GRAD: one for dbias's sums
   static constexpr int kWarpOut = 32 * 1024 / kEpi;        // blocks of 32 rows x 32 columns, 2 KB each
   static constexpr int kBlocks = 2;                        // blocks of 128 bytes of the reduction in a stage
   static constexpr int kABytes = kBlocks * 128 * 128;      // a CTA's share of A in a stage
@@ -113,27 +115,21 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
   f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
 }
 
-// What the epilogue of 32 columns reads: lane j the scale and bias of column j of each part (from there they
-// go to all lanes by shuffles), and 32 values of its own row of the residual.  Loaded one block of columns
-// ahead: a load takes longer than a block.
+// What the epilogue of 32 columns needs of them: lane j the scale and bias of column j of each part, which go to
+// all lanes by shuffles (read by all lanes 16 bytes at a time a block took longer: 8 against 9.6 us, SwiGLU of 1777 x
+// 512 x 1024 in e4m3).  Loaded one block of columns ahead, as a load takes longer than a block.
 template <int G>
 struct Ahead {
   float ws[G], bs[G];
-  uint4 r[4];
 };
 template <bool E4M3, int G>
-__device__ __forceinline__ Ahead<G> load_ahead(const Epilogue& e, int N, int c, int64_t row, bool in) {
+__device__ __forceinline__ Ahead<G> load_ahead(const Epilogue& e, int N, int c) {
   Ahead<G> v;
   const int col = c + (threadIdx.x & 31);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     v.ws[g] = E4M3 && col < N ? e.Ws[(int64_t)g * N + col] : 0.0f;
     v.bs[g] = e.bias && col < N ? __uint_as_float((uint32_t)e.bias[(int64_t)g * N + col] << 16) : 0.0f;
-  }
-  if (e.R) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      v.r[i] = in && c + 8 * i < N ? *reinterpret_cast<const uint4*>(e.R + row * N + c + 8 * i) : make_uint4(0, 0, 0, 0);
   }
   return v;
 }
@@ -172,6 +168,14 @@ __device__ __forceinline__ void store_checkpoint(const Epilogue& e, const float 
   e.Ze[line * ((N + kBlock - 1) / kBlock) + c / kBlock] = (uint8_t)x;
 }
 
+// Where a CTA's `span` rows (or columns) of `total` begin that nominally begin at `at`: moved back by a multiple of
+// `unit`, so that fewer than `unit` of them lie outside.  The copy engine takes about 8 ns for a row of 128 bytes
+// outside of a tensor where it takes 1 for one inside (48 and 128 rows x 384 x 7168 took 11.1 and 12.0 us, 256 rows
+// 6.1).  What lies before `at` is another CTA's and not stored here.
+__device__ __forceinline__ int span_start(int at, int total, int span, int unit) {
+  return min(at, max(0, (total + unit - 1) / unit * unit - span));
+}
+
 template <int MODE, bool E4M3, bool GATED, int BN>
 __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
   using C = GemmCfg<MODE, GATED, BN>;
@@ -182,9 +186,11 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
   constexpr int kTileN = GATED ? BN / 2 : BN;    // output columns of a tile
   constexpr int kEpiWarps = C::kEpi, kWarpOut = C::kWarpOut, kOuts = kWarpOut / 2048;
   constexpr int kWarpN = kTileN / (kEpiWarps / 4);  // of an epilogue warp
+  constexpr int kBRows = BN / 2;                     // a CTA's share of B
+  constexpr int kUnitB = kMnB ? 64 : 32;             // by which B's share may begin elsewhere: chunks, the epilogue's columns
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain, came[C::kEpi];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int32_t abort_flag;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -199,6 +205,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
       ptx::mbar_init(&tfull[i], 1);
       ptx::mbar_init(&tempty[i], kEpiWarps + (rank == 0));  // and the second CTA's warp 1
     }
+    for (int i = 0; i < C::kEpi; ++i) ptx::mbar_init(&came[i], 1);
     ptx::mbar_init(&drain, 1);
     ptx::mbar_init_fence();
     abort_flag = 0;
@@ -241,7 +248,6 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
     const uint64_t pol = leaves ? ptx::l2_policy_evict_first() : ptx::l2_policy_evict_normal();
     const bool one = ptx::elect_one();
     uint8_t* base = ring + (copies_a ? 0 : kABytes);
-    constexpr int kBRows = BN / 2;  // of a CTA
     const uint32_t full0 = ptx::mapa(&full[0], 0);
     uint32_t it = 0, st = 0, par = 1;
     bool ok = true;
@@ -252,8 +258,15 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
       const bool mn = MODE == GRAD && (!copies_a || p.along), wide = copies_a ? p.wideA : p.wideB;
       const CUtensorMap* map = copies_a ? &p.mA : &p.mB;
       // this CTA's first row (or column) of the operand
-      const int r0 = copies_a ? m0 + 128 * rank : GATED ? n0 + rank * p.N : n0 + kBRows * rank;
-      const int block = copies_a ? 128 * 128 : kBRows * 128;  // bytes of a block
+      const int r0 = copies_a ? span_start(m0 + 128 * rank, p.M, 128, mn ? 64 : 32)
+                     : GATED  ? span_start(n0, p.N, kBRows, kUnitB) + rank * p.N
+                              : span_start(n0 + kBRows * rank, p.N, kBRows, kUnitB);
+      const int block = (copies_a ? p.a_rows : kBRows) * 128;  // bytes of a block
+      const uint32_t a_bytes = 2 * p.a_rows * 128;
+      // the second CTA's share, where none of it is inside, is not copied: what stands there counts for outputs that no
+      // one stores
+      const int both_a = m0 + 128 < p.M ? 2 : 1, both_b = GATED || n0 + kBRows < p.N ? 2 : 1;
+      const bool skip = rank == 1 && (copies_a ? both_a : both_b) == 1;
       for (int kb = 0; kb < nkb; kb += kBlocks, ++it) {
         ok = ptx::mbar_wait_bounded(&empty[st], par, kWaitNs);
         if (!ok) break;
@@ -263,11 +276,12 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
         if (one) {
           if (copies_a && rank == 0) {
             // an operand's second block is counted where a box brings it, even from outside
-            const uint32_t as = (MODE == GRAD && p.along) || p.wideA || !half ? kABytes : kABytes / 2;
+            const uint32_t as = (MODE == GRAD && p.along) || p.wideA || !half ? a_bytes : a_bytes / 2;
             const uint32_t bs = kMnB || p.wideB || !half ? kBBytes : kBBytes / 2;
-            ptx::mbar_arrive_expect_tx(&full[st], 2 * (as + bs));
+            ptx::mbar_arrive_expect_tx(&full[st], both_a * as + both_b * bs);
           }
-          if (mn) {  // chunks of 64 columns x 128 k
+          if (skip) {
+          } else if (mn) {  // chunks of 64 columns x 128 k
             if (wide) {
               ptx::tma_load_3d_to_leader(dst, map, bar, 0, kb * 64, r0 / 64, pol);
             } else {
@@ -315,6 +329,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
         const GemmShape& p = tile(t, m0, n0);
         const int nkb = (p.K + kElems - 1) / kElems;
         const bool along = MODE == GRAD && p.along;
+        const int a_block = p.a_rows * 128;
         const uint32_t idesc = kIdesc | (along ? ptx::kIdescAMn : 0);
         ok = ptx::mbar_wait_bounded_cluster(&tempty[buf], (use & 1) ^ 1, kWaitNs) && !abort_flag;
         ok = __all_sync(0xffffffffu, ok);
@@ -336,7 +351,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
             if (!one) continue;
             // along the reduction: 32 bytes of a block's rows; across it: 16 rows of 128 bytes
             const uint64_t mn = (uint64_t)(s * 2048) >> 4;
-            const uint64_t oA = along ? mn : (uint64_t)(s / 4 * 16384 + s % 4 * 32) >> 4;
+            const uint64_t oA = along ? mn : (uint64_t)(s / 4 * a_block + s % 4 * 32) >> 4;
             const uint64_t oB = kMnB ? mn : (uint64_t)(s / 4 * (kBBytes / kBlocks) + s % 4 * 32) >> 4;
             if (E4M3) ptx::umma_e4m3_pair(d, dA + oA, dB + oB, idesc, kb || s);
             else ptx::umma_bf16_pair(d, dA + oA, dB + oB, idesc, kb || s);
@@ -380,29 +395,45 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     uint8_t* stage = ring + kStages * kStageBytes + (warp - 2) * kWarpOut;
     const Epilogue& e = a.e;
-    uint32_t acc = 0, blocks = 0;
+    uint32_t acc = 0, blocks = 0, loads = 0;
     bool ok = true;
-    for (int t = first; t < total; t += step, ++acc) {
+    for (int t = first; t < total && ok; t += step, ++acc) {
       int m0, n0;
       const GemmShape& p = tile(t, m0, n0);
       const uint32_t buf = acc & 1, use = acc >> 1;
-      const int row0 = m0 + 128 * rank + 32 * quarter, row = row0 + lane;
-      const bool in = row < p.M;
+      const int row0 = span_start(m0 + 128 * rank, p.M, 128, MODE == GRAD && p.along ? 64 : 32) + 32 * quarter, row = row0 + lane;
+      const bool rows = row0 >= m0 + 128 * rank && row0 < p.M;  // of this CTA's own
+      const bool in = rows && row < p.M;
+      // this warp's first output column, and the first of its blocks of 32 from there on that is the tile's own
+      const int own = GATED ? n0 : n0 + half * kWarpN / kBRows * kBRows;  // of the share of B that they come from
+      const int c0 = span_start(own, p.N, kBRows, kUnitB) + (GATED ? half * kWarpN : half * kWarpN % kBRows);
+      const int i0 = rows ? max(0, own - c0) / 32 : kWarpN / 32;
       float xs = 1.0f;
       if (E4M3 && in) xs = e.Xs[row];
       const bool divide = MODE == GRAD && e.Xs && !p.along;
       if (divide && in) xs = 1.0f / scale_fraction(e.Xs[row]);
       constexpr int G = GATED ? 2 : 1;
       Ahead<G> now;
-      if (MODE == FWD) now = load_ahead<E4M3, G>(e, p.N, n0 + half * kWarpN, row, in);
+      if (MODE == FWD) now = load_ahead<E4M3, G>(e, p.N, c0 + 32 * i0);
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleepy(&tfull[buf], use & 1, kWaitNs) && !abort_flag);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint32_t d = tmem + buf * BN + lanes;
 #pragma unroll 1
-      for (int i = 0; i < kWarpN / 32; ++i) {
-        const int at = half * kWarpN + 32 * i, c = n0 + at, left = p.N - c;  // columns from c on
-        if (left <= 0 || row0 >= p.M) break;
+      for (int i = i0; i < kWarpN / 32; ++i) {
+        const int at = half * kWarpN + 32 * i, c = c0 + 32 * i, left = p.N - c;  // columns from c on
+        if (left <= 0) break;
+        // this block of the staging, free once the store before the last (the last, with one block) has read it; the
+        // residual's 32 x 32 come into it first
+        uint8_t* block = stage + (blocks % kOuts) * 2048;
+        if (lane == 0) {
+          ptx::bulk_wait_group_read<kOuts - 1>();
+          if (MODE == FWD && e.R) {
+            ptx::mbar_arrive_expect_tx(&came[warp - 2], 2048);
+            ptx::tma_load_2d(block, &a.mR, &came[warp - 2], c, row0, ptx::l2_policy_evict_first());
+          }
+        }
+        __syncwarp();
         float z[32], u[32];
         {
           uint32_t v[32];
@@ -432,32 +463,32 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
 #pragma unroll
             for (int j = 0; j < 32; ++j) z[j] = activate(z[j], e.act);
           }
-          if (e.R) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float f[8];
-              unpack8(now.r[j], f);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) z[8 * j + k] += f[k];
-            }
-          }
-          if (i + 1 < kWarpN / 32) now = load_ahead<E4M3, G>(e, p.N, c + 32, row, in);
+          if (i + 1 < kWarpN / 32) now = load_ahead<E4M3, G>(e, p.N, c + 32);
         }
         if (divide) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) z[j] *= xs;
         }
-        // a lane's 32 columns: four 16-byte pieces of 64-byte rows, placed as the map's 64-byte swizzle
+        // a lane's 32 columns: four 16-byte pieces of 64-byte rows, placed as the maps' 64-byte swizzle
         // has them; rows and columns outside the matrix are not written
-        if (lane == 0) ptx::bulk_wait_group_read<kOuts - 1>();
-        __syncwarp();
-        uint8_t* block = stage + (blocks % kOuts) * 2048;
+        if (MODE == FWD && e.R) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&came[warp - 2], loads & 1, kWaitNs));
+          ++loads;
+          if (!ok) break;
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t p[4];
+          uint4* piece = reinterpret_cast<uint4*>(block + lane * 64 + ((j ^ (lane / 2)) & 3) * 16);
+          if (MODE == FWD && e.R) {
+            float f[8];
+            unpack8(*piece, f);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) p[k] = pack2(z[8 * j + 2 * k], z[8 * j + 2 * k + 1]);
-          *reinterpret_cast<uint4*>(block + lane * 64 + ((j ^ (lane / 2)) & 3) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+            for (int k = 0; k < 8; ++k) z[8 * j + k] += f[k];
+          }
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = pack2(z[8 * j + 2 * k], z[8 * j + 2 * k + 1]);
+          *piece = make_uint4(v[0], v[1], v[2], v[3]);
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -467,6 +498,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
         }
         ++blocks;
       }
+      if (!ok) break;
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&tempty[buf]);

@@ -42,6 +42,7 @@ struct SplitArgs {
   int32_t* err;
   int32_t clear;
   int32_t M, N, K;       // output rows, output columns (SwiGLU: of Y), reduction length
+  int32_t b_rows;           // rows of B that are copied: cols, or fewer where there are fewer, a multiple of 8
   int32_t cols, row_tiles;  // MMA columns (output rows) of a tile: 16, 32, 64 or 128; tiles of them
   int32_t splits;        // CTAs of a cluster, at most the reduction's stages
   int32_t stages;        // of the ring
@@ -97,13 +98,15 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
 
   const int t = blockIdx.x / splits;
-  const int f0 = t / a.row_tiles * kFeatures, r0 = t % a.row_tiles * a.cols;
+  const int f_first = t / a.row_tiles * kFeatures, r_first = t % a.row_tiles * a.cols;
+  const int f0 = span_start(f_first, a.N, kFeatures, kMnA ? 64 : 32), r0 = span_start(r_first, a.M, a.cols, kMnB ? 64 : 1);
   const int nkb = (a.K + kElems - 1) / kElems;
   const int blocks = a.blocks, all = (nkb + blocks - 1) / blocks;  // stages of the whole reduction; this CTA's:
   const int s0 = (int)((int64_t)all * rank / splits), s1 = (int)((int64_t)all * (rank + 1) / splits);
-  const int a_bytes = blocks * 128 * 128, b_bytes = blocks * a.cols * 128, stage_bytes = a_bytes + b_bytes;
+  const int a_bytes = blocks * 128 * 128, b_bytes = blocks * a.b_rows * 128;
+  const int stage_bytes = split_stage_bytes(a.cols, blocks);
   // where a stage's block b begins, and an "along" operand's second chunk of 64 columns
-  const int b_step = a.cols * 128, chunk = blocks * 64 * 128;
+  const int b_step = a.b_rows * 128, chunk = blocks * 64 * 128;
 
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
 #pragma unroll 2
   for (int tok = threadIdx.x / kGroups; tok < max(per, 32 / kGroups); tok += kSplitThreads / kGroups) {
     const int row = r0 + rank * per + tok;
-    const bool in = tok < per && row < a.M && c < a.N;
+    const bool in = tok < per && row >= r_first && row < a.M && c >= f_first && c < a.N;
     float z[8], u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) z[j] = u[j] = 0.0f;

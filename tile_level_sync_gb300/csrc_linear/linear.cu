@@ -277,6 +277,7 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
   a.K = (int32_t)p.depth;
   a.cols = plan.cols;
   a.row_tiles = (int32_t)div_up(p.rows, plan.cols);
+  a.b_rows = MODE == DW ? plan.cols : (int32_t)std::min<int64_t>(plan.cols, round_up(p.rows, 8));
   a.splits = plan.splits;
   a.stages = plan.stages;
   a.blocks = plan.blocks;
@@ -286,7 +287,7 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
                    : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, n, &a.wideA)
                                 : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, p.q_pitch, 128, n, &a.wideA)) &&
                   (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, p.p_pitch, 64 * n, plan.cols / 64, &a.wideB)
-                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, p.p_pitch, plan.cols, n, &a.wideB));
+                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, p.p_pitch, a.b_rows, n, &a.wideB));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = div_up(p.cols, GATED ? 64 : 128) * a.row_tiles;
   return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)), kSplitThreads,
@@ -312,8 +313,9 @@ bool fill_shape(GemmShape* g, const Product& p, bool along) {
   g->group = (int32_t)div_up(g->m_tiles, groups);
   g->b_first = MODE == FWD && groups == 1 && a_bytes + b_bytes > 3 * kResident / 2;
   g->along = along;
+  g->a_rows = along ? 128 : (int32_t)std::min<int64_t>(128, round_up(p.rows, 8));
   return (along ? map_along(&g->mA, p.P, p.depth, p.rows, p.p_pitch, 64 * n, 2, &g->wideA)
-                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, p.p_pitch, 128, n, &g->wideA)) &&
+                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, p.p_pitch, g->a_rows, n, &g->wideA)) &&
          (MODE == GRAD ? map_along(&g->mB, p.Q, p.depth, p.cols, p.q_pitch, 64 * n, BN / 128, &g->wideB)
                : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, p.q_pitch, BN / 2, n, &g->wideB)) &&
          map_output(&g->mO, p.e.out, p.rows, p.cols);
@@ -336,6 +338,7 @@ cudaError_t forward(const Product& p, int32_t* err, int sms, cudaStream_t s) {
   a.e = p.e;
   a.err = err;
   a.clear = true;
+  if (p.e.R && !map_output(&a.mR, const_cast<uint16_t*>(p.e.R), p.rows, p.cols)) return cudaErrorInvalidValue;
   if (pair.bn == 256)
     return fill_shape<FWD, E4M3, GATED, 256>(&a.p[0], p, false) ? launch_gemm<FWD, E4M3, GATED, 256>(a, sms, s)
                                                                   : cudaErrorInvalidValue;
