@@ -14,6 +14,11 @@
 // that one finishes, and adds what it gets in the CTAs' order.  The sums are counted by a barrier of the CTA
 // that they go to, which waits for them alone.  No partial sum leaves the SMs, and one launch does it all.
 //
+// What bounds it: HBM while the weights come (59 MB of one token's layer 3584 -> 8192 in 8 us of 12.7, and the same of 48
+// tokens' 8192 -> 3584 with SwiGLU in e4m3 of 13.9: traced from the first copy to the last MMA), and 5 us around: the end
+// of the kernel before, the first bytes' latency, exchange and finish.  Copying the weights' first stages to the L2
+// before the kernel before has ended gained nothing (13.7 us without, 13.9 with, 15.0 with all stages).
+//
 // Roles: warp 0 copies A, warp 2 copies B, warp 1 owns TMEM and issues the MMAs; then all
 // eight warps read the accumulator, exchange and finish.  Every wait is bounded.
 #pragma once

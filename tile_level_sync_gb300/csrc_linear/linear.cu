@@ -194,12 +194,13 @@ struct Product {
 // clusters of `splits` CTAs with tiles of 128 (64) columns x `cols` rows; and about how long it takes.  The
 // times are fits to passes on one GB300 (us; bf16, no activation, weights in the L2 where they fit it):
 //   rows x cols   reduction   pairs 256   pairs 128   clusters (cols, splits)
-//   1777 x 1024        2048        13.3        10.2        15.3 (128, 1)  21.2 (64, 2)
-//   4096 x 2048        4096        42.9        51.0        91.7 (128, 1)
-//    333 x  776         512         6.8         5.2         6.3 (64, 2)    7.3 (128, 4)
-//    333 x  776        4096        21.6        13.3        11.9 (64, 2)   10.9 (128, 4)
-//    100 x 4096        2048        12.8         8.5         9.1 (64, 2)    9.5 (128, 4)
-//    100 x 4096        4096        22.9        15.3        16.5 (64, 2)   12.7 (128, 4)
+//   1777 x 1024        2048        13.7        10.5        14.6 (128, 1)  21.6 (64, 2)
+//   4096 x 2048        4096        43.3        51.9        89.4 (128, 1)
+//    333 x  776         512         7.5         5.6         5.7 (64, 2)    7.0 (128, 4)
+//    333 x  776        4096        22.2        13.6        11.9 (64, 2)   11.1 (128, 4)
+//    100 x 4096        2048        13.2         8.7         9.0 (64, 2)    9.3 (128, 4)
+//    100 x 4096        4096        22.6        15.0        16.5 (64, 2)   12.7 (128, 4)
+//     16 x 4096        4096        21.7        14.1        11.0 (16, 2)    8.7 (16, 4)
 struct Plan {
   double us;
   int bn, cols, splits, stages, blocks;
