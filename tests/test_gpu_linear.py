@@ -188,7 +188,8 @@ def test_norm_gradient_against_differences():
 # few tiles (clusters that divide the reduction), then many (pairs); ragged in every dimension
 SMALL = [(1, 64, 128), (1, 1000, 776), (2, 8, 8), (16, 4096, 264), (17, 136, 200), (33, 520, 328), (64, 2048, 1024),
          (100, 1000, 776), (129, 256, 128), (333, 1000, 776)]
-PAIRS = [(1030, 72, 2312), (2048, 256, 1536), (1281, 520, 2056)]
+PAIRS = [(1030, 72, 2312), (2048, 256, 1536), (1281, 520, 2056), (48, 384, 6992), (129, 384, 6992), (20000, 64, 8), (20000, 16, 40),
+         (300, 64, 20008)]
 
 
 @pytest.mark.parametrize("M,K,N", SMALL + PAIRS)
@@ -294,7 +295,8 @@ def test_checkpoint_of_odd_blocks():
 # ------------------------------------------------------------------ linear: gradients
 
 @pytest.mark.parametrize("M,K,N", [(1, 64, 128), (3, 1000, 776), (17, 136, 200), (100, 264, 520), (333, 1000, 776),
-                                   (1030, 264, 520), (700, 1544, 1032), (1300, 2056, 2056), (2050, 2048, 1024)])
+                                   (1030, 264, 520), (700, 1544, 1032), (1300, 2056, 2056), (2050, 2048, 1024),
+                                   (20000, 64, 8), (20000, 16, 40), (130, 64, 8200), (5000, 136, 72)])
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "swiglu"])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_linear_grad(M, K, N, act, dtype):

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
         if (!ok) break;
         const uint32_t bar = full0 + 8 * st;  // both CTAs' copies complete on the first one's barrier
         uint8_t* dst = base + st * kStageBytes;
-        const bool half = kBlocks == 2 && kb + 1 == nkb;
+        const bool half = kb + 1 == nkb;  // the second block holds nothing
         if (one) {
           if (copies_a && rank == 0) {
             // an operand's second block is counted where a box brings it, even from outside
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(GemmCfg<MODE, GATED, BN>::kThreads, 1) gemm_ke
               ptx::tma_load_3d_to_leader(dst, map, bar, 0, r0, kb, pol);
             } else {
               ptx::tma_load_2d_to_leader(dst, map, bar, kb * kElems, r0, pol);
-              if (kBlocks == 2 && !half) ptx::tma_load_2d_to_leader(dst + block, map, bar, (kb + 1) * kElems, r0, pol);
+              if (!half) ptx::tma_load_2d_to_leader(dst + block, map, bar, (kb + 1) * kElems, r0, pol);
             }
           }
         }

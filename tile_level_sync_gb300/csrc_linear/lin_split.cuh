@@ -51,16 +51,16 @@ struct SplitArgs {
   int32_t cols, row_tiles;  // MMA columns (output rows) of a tile: 16, 32, 64 or 128; tiles of them
   int32_t splits;        // CTAs of a cluster, at most the reduction's stages
   int32_t stages;        // of the ring
-  int32_t blocks;        // of 128 bytes of the reduction in a stage: 1 or 2
   int32_t apart;         // the sums have room of their own behind the ring, else they take the ring's
   int32_t wideA, wideB;
 };
 
 constexpr int kSplitThreads = 256;
 constexpr int kMaxStages = 8;
-__host__ __device__ constexpr int split_stage_bytes(int cols, int blocks) { return blocks * (128 + cols) * 128; }
-constexpr size_t split_smem(int cols, int blocks, int stages, bool apart) {
-  const size_t ring = (size_t)stages * split_stage_bytes(cols, blocks), sums = (size_t)cols * 128 * 4;
+// A stage holds two blocks of 128 bytes of the reduction.
+__host__ __device__ constexpr int split_stage_bytes(int cols) { return 2 * (128 + cols) * 128; }
+constexpr size_t split_smem(int cols, int stages, bool apart) {
+  const size_t ring = (size_t)stages * split_stage_bytes(cols), sums = (size_t)cols * 128 * 4;
   return 1024 + (apart ? ring + sums : ring > sums ? ring : sums);
 }
 
@@ -106,12 +106,11 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
   const int f_first = t / a.row_tiles * kFeatures, r_first = t % a.row_tiles * a.cols;
   const int f0 = span_start(f_first, a.N, kFeatures, kMnA ? 64 : 32), r0 = span_start(r_first, a.M, a.cols, kMnB ? 64 : 1);
   const int nkb = (a.K + kElems - 1) / kElems;
-  const int blocks = a.blocks, all = (nkb + blocks - 1) / blocks;  // stages of the whole reduction; this CTA's:
+  const int all = (nkb + 1) / 2;  // stages of the whole reduction; this CTA's:
   const int s0 = (int)((int64_t)all * rank / splits), s1 = (int)((int64_t)all * (rank + 1) / splits);
-  const int a_bytes = blocks * 128 * 128, b_bytes = blocks * a.b_rows * 128;
-  const int stage_bytes = split_stage_bytes(a.cols, blocks);
+  const int a_bytes = 2 * 128 * 128, b_bytes = 2 * a.b_rows * 128, stage_bytes = split_stage_bytes(a.cols);
   // where a stage's block b begins, and an "along" operand's second chunk of 64 columns
-  const int b_step = a.b_rows * 128, chunk = blocks * 64 * 128;
+  const int b_step = a.b_rows * 128, chunk = 2 * 64 * 128;
 
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
@@ -127,8 +126,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
     for (int s = s0; s < s1; ++s, ++it) {
       ok = __all_sync(0xffffffffu, ptx::mbar_wait_bounded(&empty[st], par, kWaitNs));
       if (!ok || abort_flag) break;
-      const int kb = s * blocks;
-      const bool half = blocks == 2 && kb + 1 == nkb;  // the stage's second block holds nothing
+      const int kb = 2 * s;
+      const bool half = kb + 1 == nkb;  // the stage's second block holds nothing
       uint8_t* sA = ring + st * stage_bytes;
       uint8_t* sB = sA + a_bytes;
       uint64_t* bar = &full[st];
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
           if (GATED) ptx::tma_load_4d(sA, &a.mA, bar, 0, f0, 0, kb, pol);
           else ptx::tma_load_3d(sA, &a.mA, bar, 0, f0, kb, pol);
         } else {
-          for (int b = 0; b < (half ? 1 : blocks); ++b) {
+          for (int b = 0; b < (half ? 1 : 2); ++b) {
             if (GATED) ptx::tma_load_3d(sA + b * 16384, &a.mA, bar, (kb + b) * kElems, f0, 0, pol);
             else ptx::tma_load_2d(sA + b * 16384, &a.mA, bar, (kb + b) * kElems, f0, pol);
           }
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
         } else if (a.wideB) {
           ptx::tma_load_3d(sB, &a.mB, bar, 0, r0, kb, pol);
         } else {
-          for (int b = 0; b < (half ? 1 : blocks); ++b)
+          for (int b = 0; b < (half ? 1 : 2); ++b)
             ptx::tma_load_2d(sB + b * b_step, &a.mB, bar, (kb + b) * kElems, r0, pol);
         }
       }
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
       const uint32_t sA = ring0 + st * stage_bytes, sB = sA + a_bytes;
       const uint64_t dA = kMnA ? ptx::smem_desc_mn128(sA, chunk) : ptx::smem_desc_k128(sA);
       const uint64_t dB = kMnB ? ptx::smem_desc_mn128(sB, chunk) : ptx::smem_desc_k128(sB);
-      const int steps = min(4 * blocks, (a.K - blocks * s * kElems + kElems / 4 - 1) / (kElems / 4));
+      const int steps = (a.K - 2 * s * kElems + kElems / 4 - 1) / (kElems / 4);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (i >= steps) break;

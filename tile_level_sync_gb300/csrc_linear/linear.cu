@@ -149,29 +149,29 @@ bool map_nd(CUtensorMap* m, const void* p, int bytes, CUtensorMapSwizzle swizzle
 }
 
 // An operand [rows, cols], rows `pitch` elements apart, whose columns are the reduction's: boxes of 128 bytes x
-// box_rows; wide (columns a multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of `blocks`.
-bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int64_t pitch, int box_rows, int blocks,
+// box_rows; wide (columns a multiple of 128 bytes): as [blocks][rows][128 bytes], boxes of two.
+bool map_rows(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int64_t pitch, int box_rows,
               int32_t* wide) {
   const int n = 128 / bytes;
   *wide = cols % n == 0;
-  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {pitch, n}, {n, box_rows, blocks})
+  return *wide ? map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, cols / n}, {pitch, n}, {n, box_rows, 2})
                : map_nd<2>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {pitch}, {n, box_rows});
 }
 // Gate and up rows of a gated layer's weights [2][rows, cols], 64 of each in a box.
-bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int blocks, int32_t* wide) {
+bool map_gated(CUtensorMap* m, const void* p, int bytes, int64_t rows, int64_t cols, int32_t* wide) {
   const int n = 128 / bytes;
   *wide = cols % n == 0;
   return *wide ? map_nd<4>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {n, rows, 2, cols / n}, {cols, rows * cols, n},
-                           {n, 64, 2, blocks})
+                           {n, 64, 2, 2})
                : map_nd<3>(m, p, bytes, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows, 2}, {cols, rows * cols}, {n, 64, 2});
 }
-// A bf16 operand [rows, cols] whose rows are the reduction's: boxes of 64 columns x `box_rows` rows; wide (columns
+// A bf16 operand [rows, cols] whose rows are the reduction's: boxes of 64 columns x 128 rows; wide (columns
 // a multiple of 64): as [chunks][rows][64], boxes of `chunks`.
-bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch, int box_rows, int chunks,
+bool map_along(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t pitch, int chunks,
                int32_t* wide) {
   *wide = cols % 64 == 0;
-  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {pitch, 64}, {64, box_rows, chunks})
-               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {pitch}, {64, box_rows});
+  return *wide ? map_nd<3>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {64, rows, cols / 64}, {pitch, 64}, {64, 128, chunks})
+               : map_nd<2>(m, p, 2, CU_TENSOR_MAP_SWIZZLE_128B, {cols, rows}, {pitch}, {64, 128});
 }
 // An output [rows, cols]: boxes of 32 x 32 as a warp's lanes write them.
 bool map_output(CUtensorMap* m, void* p, int64_t rows, int64_t cols) {
@@ -203,7 +203,7 @@ struct Product {
 //     16 x 4096        4096        21.7        14.1        11.0 (16, 2)    8.7 (16, 4)
 struct Plan {
   double us;
-  int bn, cols, splits, stages, blocks;
+  int bn, cols, splits, stages;
   bool apart;  // clusters: room of their own for the sums
 };
 constexpr double kBytesPerUs = 6.5e6;  // of HBM
@@ -220,27 +220,27 @@ double pair_time(int64_t n, double a, int64_t m, double b, int64_t pairs) {
 }
 
 Plan pair_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems, bool gated) {
-  Plan best = {1e30, 0, 0, 0, 0, 0, false};
+  Plan best = {1e30, 0, 0, 0, 0, false};
   if (sms < 2) return best;
   for (int bn = 128; bn <= 256; bn += 128) {
     const int64_t tiles = div_up(rows, 256) * div_up(cols, gated ? bn / 2 : bn);
     const double us = pair_time(tiles, pair_tile(bn, div_up(depth, elems)), 0, 0.0, sms / 2);
-    if (us < best.us) best = {us, bn, 0, 0, 0, 0, false};
+    if (us < best.us) best = {us, bn, 0, 0, 0, false};
   }
   return best;
 }
 
 template <int MODE, bool GATED>
 Plan split_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems) {
-  Plan best = {1e30, 0, 0, 0, 0, 2, false};
+  Plan best = {1e30, 0, 0, 0, 0, false};
   int most = 16;  // rows of a tile that covers all rows, where one does
   while (most < 128 && most < rows) most *= 2;
   const int64_t blocks = div_up(depth, elems);
   for (int n = MODE == DW ? 64 : std::max(16, most / 2); n <= std::max(most, MODE == DW ? 64 : 16); n *= 2) {
-    const int stage = split_stage_bytes(n, best.blocks);
+    const int stage = split_stage_bytes(n);
     const int64_t tiles = div_up(rows, n) * div_up(cols, GATED ? 64 : 128);
     for (int splits = 1; splits <= 8; splits *= 2) {
-      if (splits > 1 && splits > div_up(blocks, best.blocks)) break;
+      if (splits > 1 && splits > div_up(blocks, 2)) break;
       const int64_t ctas = tiles * splits;
       // two CTAs an SM where there are enough and two stages of both fit; clusters of four or eight leave some
       // SMs out (of 152: 144 and 120 take one CTA, 296 and 288 CTAs fit two an SM)
@@ -256,9 +256,9 @@ Plan split_plan(int64_t rows, int64_t cols, int64_t depth, int sms, int elems) {
                         std::max(stream, MODE == DW ? 0.0 : weights);
       if (us < best.us) {
         const int room = (two ? kSmemPerSm / 2 : kSmemPerSm) - 1024;  // static shared memory and the block's own
-        best = {us, 0, n, splits, 0, best.blocks, false};
-        best.stages = (int)std::min<int64_t>(std::min(kMaxStages, (room - 1024) / stage), div_up(div_up(blocks, best.blocks), splits));
-        best.apart = splits > 1 && split_smem(n, best.blocks, best.stages, true) <= (size_t)room;
+        best = {us, 0, n, splits, 0, false};
+        best.stages = (int)std::min<int64_t>(std::min(kMaxStages, (room - 1024) / stage), div_up(div_up(blocks, 2), splits));
+        best.apart = splits > 1 && split_smem(n, best.stages, true) <= (size_t)room;
       }
     }
   }
@@ -281,24 +281,22 @@ cudaError_t launch_split(const Plan& plan, const Product& p, int32_t* err, bool 
   a.b_rows = MODE == DW ? plan.cols : (int32_t)std::min<int64_t>(plan.cols, round_up(p.rows, 8));
   a.splits = plan.splits;
   a.stages = plan.stages;
-  a.blocks = plan.blocks;
   a.apart = plan.apart;
-  const int n = plan.blocks;
-  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, p.q_pitch, 64 * n, 2, &a.wideA)
-                   : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, n, &a.wideA)
-                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, p.q_pitch, 128, n, &a.wideA)) &&
-                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, p.p_pitch, 64 * n, plan.cols / 64, &a.wideB)
-                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, p.p_pitch, a.b_rows, n, &a.wideB));
+  const bool ok = (MODE != FWD  ? map_along(&a.mA, p.Q, p.depth, p.cols, p.q_pitch, 2, &a.wideA)
+                   : GATED      ? map_gated(&a.mA, p.Q, bytes, p.cols, p.depth, &a.wideA)
+                                : map_rows(&a.mA, p.Q, bytes, p.cols, p.depth, p.q_pitch, 128, &a.wideA)) &&
+                  (MODE == DW ? map_along(&a.mB, p.P, p.depth, p.rows, p.p_pitch, plan.cols / 64, &a.wideB)
+                              : map_rows(&a.mB, p.P, bytes, p.rows, p.depth, p.p_pitch, a.b_rows, &a.wideB));
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = div_up(p.cols, GATED ? 64 : 128) * a.row_tiles;
   return launch_cluster(plan.splits, split_kernel<MODE, E4M3, GATED>, dim3((unsigned)(tiles * plan.splits)), kSplitThreads,
-                        split_smem(plan.cols, n, plan.stages, plan.apart), s, a);
+                        split_smem(plan.cols, plan.stages, plan.apart), s, a);
 }
 
 // A product on pairs; along: P's rows are the reduction's (dWt).  Q's are, too, in both gradients.
 template <int MODE, bool E4M3, bool GATED, int BN>
 bool fill_shape(GemmShape* g, const Product& p, bool along) {
-  constexpr int bytes = E4M3 ? 1 : 2, n = GemmCfg<MODE, GATED, BN>::kBlocks;
+  constexpr int bytes = E4M3 ? 1 : 2;
   g->M = (int32_t)p.rows;
   g->N = (int32_t)p.cols;
   g->K = (int32_t)p.depth;
@@ -315,10 +313,10 @@ bool fill_shape(GemmShape* g, const Product& p, bool along) {
   g->b_first = MODE == FWD && groups == 1 && a_bytes + b_bytes > 3 * kResident / 2;
   g->along = along;
   g->a_rows = along ? 128 : (int32_t)std::min<int64_t>(128, round_up(p.rows, 8));
-  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, p.p_pitch, 64 * n, 2, &g->wideA)
-                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, p.p_pitch, g->a_rows, n, &g->wideA)) &&
-         (MODE == GRAD ? map_along(&g->mB, p.Q, p.depth, p.cols, p.q_pitch, 64 * n, BN / 128, &g->wideB)
-               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, p.q_pitch, BN / 2, n, &g->wideB)) &&
+  return (along ? map_along(&g->mA, p.P, p.depth, p.rows, p.p_pitch, 2, &g->wideA)
+                : map_rows(&g->mA, p.P, bytes, p.rows, p.depth, p.p_pitch, g->a_rows, &g->wideA)) &&
+         (MODE == GRAD ? map_along(&g->mB, p.Q, p.depth, p.cols, p.q_pitch, BN / 128, &g->wideB)
+               : map_rows(&g->mB, p.Q, bytes, GATED ? 2 * p.cols : p.cols, p.depth, p.q_pitch, BN / 2, &g->wideB)) &&
          map_output(&g->mO, p.e.out, p.rows, p.cols);
 }
 template <int MODE, bool E4M3, bool GATED, int BN>
