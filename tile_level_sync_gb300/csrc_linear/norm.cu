@@ -39,9 +39,10 @@ Shape shape(int64_t M, int64_t D, int most, int64_t rows) {
   return {v, (int)round_up(div_up(vecs, v), 32), false};
 }
 
-// Rows of up to 1024 columns from which warps take them (us, blocks / warps, 1000 columns: norm 333 rows 1.9 / 2.6, 1000 2.6 /
-// 2.7, 4096 6.3 / 5.9; gradient 32 rows 3.5 / 4.7, 333 5.5 / 4.9, 1000 9.0 / 5.5).
-constexpr int64_t kNormWarpRows = 2048, kGradWarpRows = 256;
+// Rows of up to 1024 columns from which warps take them (us, blocks / warps: norm 650 rows of 256 1.8 / 1.7, of 1000 1.9 / 2.4;
+// 1000 rows of 256 1.9 / 1.7, of 512 2.0 / 1.9, of 1000 2.7 / 2.4 and with residual and 8 bits 2.6 / 2.7; 1777 rows of 1000
+// 3.2 / 2.9; gradient of rows of 1000, 32 rows 3.5 / 4.7, 333 5.5 / 4.9, 1000 9.0 / 5.5).
+constexpr int64_t kNormWarpRows = 1000, kGradWarpRows = 256;
 
 // The gradient's blocks on an SM, and rows of a ring (a block's, or each of its warps').
 struct Ring {
