@@ -14,7 +14,7 @@
  *    caller.  Activations, weights and parameters are bf16; weights have the reduction
  *    dimension contiguous ("[out, in]"), as in cusync.h.
  *  - 8-bit rows: q [rows, cols] e4m3 and scales [rows] fp32; row r stands for
- *    scales[r] * q[r].
+ *    scales[r] * q[r] (a scale below 2^-126 in magnitude may count as 0).
  *  - 8-bit checkpoint of pre-activations z [M, parts, N] (parts: 2 for SwiGLU, gate then up,
  *    else 1): Zq [M, parts, N] e4m3 and Ze [M, parts, ceil(N / 32)] one byte for each 32
  *    columns (the last block may be shorter): z ~ Zq * 2^(Ze - 127), the smallest such power by

@@ -120,7 +120,7 @@ def pre(X, Xs, Wt, Ws, bias):
     z, mag = X @ Wt.T, np.abs(X) @ np.abs(Wt).T
     if Xs is not None:
         scale = Xs[:, None] * Ws[None, :]
-        z, mag = z * scale, mag * scale
+        z, mag = z * scale, mag * np.abs(scale)
     err = (X.shape[1] / 16 + 16) * STEP * mag
     if bias is not None:
         z = z + bias
@@ -166,7 +166,7 @@ def checkpoint(z, parts):
 
 def linear_grad(X, Xs, Wt, z, dY, kind):
     """{name: (gradient, bound)}; z: what the checkpoint stands for (None for kind "none").  X in bf16,
-    or the values of 8-bit rows with scales Xs = f * 2^e, f in [1, 2): dZ is rounded times f then,
+    or the values of 8-bit rows with scales Xs = f * +-2^e, f in [1, 2): dZ is rounded times f then,
     for dWt, and with an activation for dX, too."""
     dz, err = slope(z, dY, kind)
     err = err + 2.0 ** -24 * np.abs(dz)
@@ -180,7 +180,7 @@ def linear_grad(X, Xs, Wt, z, dY, kind):
     f, x = 1.0, X
     if Xs is not None:
         fraction, exponent = np.frexp(Xs)
-        f, x = 2 * fraction[:, None], X * np.ldexp(1.0, exponent - 1)[:, None]
+        f, x = 2 * np.abs(fraction[:, None]), X * np.copysign(np.ldexp(1.0, exponent - 1), Xs)[:, None]
     dw, sw = rounded(f, kind == "none" and Xs is None)
     dx, sx = (dw / f, sw / f) if kind != "none" else rounded(1.0, True)
     out = {}

@@ -277,6 +277,20 @@ def test_odd_values_stay_in_their_rows(M, K, N, act):
         assert np.array_equal(y, np.maximum(want, 0) + f64(s["R"][0]) if act == "relu" else want)
 
 
+@pytest.mark.parametrize("M,K,N", [(5, 1008, 776), (1281, 528, 2056)])
+@pytest.mark.parametrize("xs,ws", [(2.0 ** 118, 1.0), (-2.0 ** 118, 1.0), (2.0 ** -118, 2.0 ** 100), (1.0, -1.0)])
+@pytest.mark.parametrize("act", ["none", "relu"])
+def test_scales_far_out_and_negative(M, K, N, xs, ws, act):
+    """Rows and weights whose values, and whose products' sums, bf16 holds: what lies between stays within 32 bits, too."""
+    s = linear_inputs(M, K, N, act, "e4m3", bias=False, residual=False)
+    s["Xs"], s["Ws"] = s["Xs"] * xs, s["Ws"] * ws
+    m = layer(M, K, N, act, "e4m3")
+    got = run_linear(m, s, checkpoint=True)
+    Y, bound, z, dz = oracle_linear(s, act)
+    assert_within(got["Y"], Y, bound, "Y")
+    assert_checkpoint(got["Zq"], got["Ze"], z, dz, 1, "Z")
+
+
 def test_checkpoint_of_odd_blocks():
     """Pre-activations of one large value beside small ones, and of zeros: through a bias on zero inputs."""
     M, K, N = 3, 64, 72
@@ -306,6 +320,22 @@ def test_linear_grad(M, K, N, act, dtype):
     got = run_linear_grad(layer(M, K, N, act, dtype), s)
     for name, (value, bound) in oracle_grad(s, act).items():
         assert_within(got[name], value, bound, name)
+
+
+@pytest.mark.parametrize("M,K,N", [(17, 144, 200), (1300, 1040, 1032)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_linear_grad_of_negative_scales(M, K, N, act):
+    s = linear_inputs(M, K, N, act, "e4m3", grad=True)
+    s["Xs"][1::2] *= -1
+    m = layer(M, K, N, act, "e4m3")
+    got = run_linear_grad(m, s)
+    for name, (value, bound) in oracle_grad(s, act).items():
+        assert_within(got[name], value, bound, name)
+    # a row that stands for NaN: dX and dbias do not see it, dWt is NaN
+    s["Xs"][2] = float("nan")
+    odd = run_linear_grad(m, s)
+    assert torch.isnan(odd["dWt"].float()).all()
+    assert torch.equal(odd["dbias"], got["dbias"]) and torch.isfinite(odd["dX"].float()).all()
 
 
 @pytest.mark.parametrize("want", [("dX",), ("dWt",), ("dbias",), ("dX", "dWt"), ("dX", "dbias")])

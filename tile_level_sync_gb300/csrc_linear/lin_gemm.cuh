@@ -138,12 +138,13 @@ __device__ __forceinline__ Ahead<G> load_ahead(const Epilogue& e, int N, int c) 
   }
   return v;
 }
-// z * scales + bias of 32 columns.
+// z * scales + bias of 32 columns.  The weights' scale first: that of a row of large values would take z, a sum of
+// products of up to 448 each, out of 32 bits before it.
 template <bool E4M3>
 __device__ __forceinline__ void finish32(const Epilogue& e, float xs, float ws, float bs, float (&z)[32]) {
   if (E4M3) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) z[j] = z[j] * xs * __shfl_sync(0xffffffffu, ws, j);
+    for (int j = 0; j < 32; ++j) z[j] = z[j] * __shfl_sync(0xffffffffu, ws, j) * xs;
   }
   if (e.bias) {
 #pragma unroll

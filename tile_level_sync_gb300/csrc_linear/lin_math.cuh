@@ -86,11 +86,13 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
-// A row's scale as f * 2^e with f in [1, 2): f, and 2^e.
+// A row's scale as f * +-2^e with f in [1, 2): f, and +-2^e (infinities and NaN whole; below 2^-126: 0).
 __device__ __forceinline__ float scale_fraction(float s) {
   return __uint_as_float((__float_as_uint(s) & 0x007fffffu) | 0x3f800000u);
 }
-__device__ __forceinline__ float scale_power(float s) { return __uint_as_float(__float_as_uint(s) & 0x7f800000u); }
+__device__ __forceinline__ float scale_power(float s) {
+  return fabsf(s) <= kFloatMax ? __uint_as_float(__float_as_uint(s) & 0xff800000u) : s;
+}
 
 // 1 / (1 + e^-x)
 __device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.0f + exp2_fast(x * -kLog2e)); }

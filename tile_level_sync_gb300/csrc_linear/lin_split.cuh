@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_const
         const float xs = E4M3 ? e.Xs[row] : 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          z[j] = E4M3 ? z[j] * (xs * ws[0][j]) + bs[0][j] : z[j] + bs[0][j];
-          if (GATED) u[j] = E4M3 ? u[j] * (xs * ws[GATED][j]) + bs[GATED][j] : u[j] + bs[GATED][j];
+          z[j] = E4M3 ? z[j] * ws[0][j] * xs + bs[0][j] : z[j] + bs[0][j];
+          if (GATED) u[j] = E4M3 ? u[j] * ws[GATED][j] * xs + bs[GATED][j] : u[j] + bs[GATED][j];
         }
       }
       if (e.Zq) {  // four neighbours share a block
