@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -24,3 +25,17 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True)
+def collect_between_gpu_tests(request):
+    """The garbage collector runs between GPU tests, not in them: a graph of an earlier test that it destroys during a
+    capture ends the capture.  (An exception that a test keeps holds the test's frame, which holds the exception and
+    the test's graphs: such rings wait for the collector.)"""
+    if "gpu" not in request.keywords:
+        yield
+        return
+    gc.disable()
+    yield
+    gc.enable()
+    gc.collect(0)
