@@ -3,6 +3,8 @@ binding."""
 
 import os
 import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -221,3 +223,57 @@ def test_binding_checks_tensors():
         m.run(4096, 4096, 4096, 4096, stream=0)  # without scales
     with pytest.raises(KeyError):
         cs.make_linear_desc(**LINEAR, act="tanh")
+
+
+PLANNER = r"""
+#include <cstdio>
+#include "lin_plan.h"
+using namespace cusync::lin;
+int bad = 0, seen = 0;
+template <int MODE, bool GATED>
+void look(int64_t rows, int64_t cols, int64_t depth, int sms, int elems) {
+  const Plan s = split_plan<MODE, GATED>(rows, cols, depth, sms, elems), p = pair_plan(rows, cols, depth, sms, elems, GATED);
+  const bool pow2 = (s.cols & (s.cols - 1)) == 0 && (s.splits & (s.splits - 1)) == 0;
+  const int64_t stages = (div_up(depth, elems) + 1) / 2;
+  // nothing takes less than its start and end; a CTA has a stage of the reduction at least
+  const bool ok = s.us >= 5.2 && s.us < 1e12 && pow2 && s.cols >= (MODE == DW ? 64 : 16) && s.cols <= 128 && s.splits >= 1 &&
+                  s.splits <= 8 && s.splits <= stages && s.stages >= 1 && s.stages <= kMaxStages && s.stages * s.splits <= stages + s.splits - 1 &&
+                  split_smem(s.cols, s.stages, s.apart) <= (size_t)kSmemPerSm - 1024 &&
+                  (sms < 2 ? p.us == 1e30 && !p.bn : p.us >= 4.2 && p.us < 1e12 && (p.bn == 128 || p.bn == 256));
+  ++seen;
+  if (!ok) ++bad, std::printf("mode %d gated %d %lld x %lld x %lld on %d: %g us, %d, %d, %d\n", MODE, GATED, (long long)rows,
+                              (long long)cols, (long long)depth, sms, s.us, s.cols, s.splits, s.stages);
+}
+int main() {
+  const int64_t sizes[] = {1, 8, 20, 64, 72, 100, 333, 776, 1000, 1281, 2056, 9000};
+  for (int sms : {1, 2, 3, 4, 5, 6, 7, 8, 37, 151, 152})
+    for (int64_t rows : sizes)
+      for (int64_t cols : sizes)
+        for (int64_t depth : sizes) {
+          look<FWD, false>(rows, cols, depth, sms, 64);
+          look<FWD, false>(rows, cols, depth, sms, 128);
+          look<FWD, true>(rows, cols, depth, sms, 64);
+          look<FWD, true>(rows, cols, depth, sms, 128);
+          look<DX, false>(rows, cols, depth, sms, 64);
+          look<DW, false>(rows, cols, depth, sms, 64);
+        }
+  std::printf("%d plans, %d bad\n", seen, bad);
+  return bad != 0;
+}
+"""
+
+
+def test_plans_on_any_number_of_sms(tmp_path):
+    """The plans of all kinds of products are sound from one SM on; a division by zero traps, whatever the host makes of one."""
+    gxx = shutil.which("g++")
+    if not gxx:
+        pytest.skip("no host compiler")
+    src = tmp_path / "plans.cpp"
+    src.write_text(PLANNER)
+    build = subprocess.run([gxx, "-std=c++17", "-O1", "-fsanitize=integer-divide-by-zero", "-fsanitize-undefined-trap-on-error",
+                            "-I" + os.path.join(ROOT, "tile_level_sync_gb300", "csrc_linear"), str(src), "-o", str(tmp_path / "plans")],
+                           capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    r = subprocess.run([str(tmp_path / "plans")], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, (r.returncode, r.stdout[-2000:])
+    assert int(r.stdout.split()[0]) > 100000

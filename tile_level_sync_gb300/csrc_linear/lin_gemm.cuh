@@ -28,6 +28,7 @@
 // Every wait is bounded; an expired one raises the error word and ends the CTA's roles.
 #pragma once
 #include "lin_math.cuh"
+#include "lin_plan.h"
 #include "../csrc_moe/moe_ptx.cuh"
 
 namespace cusync {
@@ -60,8 +61,6 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
 }  // namespace ptx
 
 namespace lin {
-
-enum : int { FWD = 0, DX = 1, DW = 2, GRAD = 3 };
 
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint32_t kErrWait = 3u << 24;  // the pipeline-wait class of the chain kernel's error words

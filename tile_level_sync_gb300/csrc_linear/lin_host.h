@@ -8,6 +8,7 @@
 
 #include "../../include/cusync_linear.h"
 #include "../csrc_moe/moe_launch.h"
+#include "lin_plan.h"
 
 namespace cusync {
 namespace lin {
@@ -17,7 +18,6 @@ constexpr int64_t kHeader = 256;  // bytes of a work buffer before its arrays; a
 using moe::launch;
 using moe::launch_cluster;
 
-inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return div_up(a, b) * b; }
 inline bool aligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned_or_null(const void* p) { return !p || aligned(p); }

@@ -23,6 +23,7 @@
 // eight warps read the accumulator, exchange and finish.  Every wait is bounded.
 #pragma once
 #include "lin_gemm.cuh"
+#include "lin_plan.h"
 
 namespace cusync {
 namespace ptx {
@@ -56,13 +57,6 @@ struct SplitArgs {
 };
 
 constexpr int kSplitThreads = 256;
-constexpr int kMaxStages = 8;
-// A stage holds two blocks of 128 bytes of the reduction.
-__host__ __device__ constexpr int split_stage_bytes(int cols) { return 2 * (128 + cols) * 128; }
-constexpr size_t split_smem(int cols, int stages, bool apart) {
-  const size_t ring = (size_t)stages * split_stage_bytes(cols), sums = (size_t)cols * 128 * 4;
-  return 1024 + (apart ? ring + sums : ring > sums ? ring : sums);
-}
 
 template <int MODE, bool E4M3, bool GATED>
 __global__ void __launch_bounds__(kSplitThreads) split_kernel(const __grid_constant__ SplitArgs a) {
