@@ -138,6 +138,36 @@ def test_norm_of_rows_whose_squares_leave_32_bits(size):
     assert_within(dw.t, value, bound + 2.0 ** -18 * np.abs(f64(s["dY"])).sum(axis=0), "dw")
 
 
+def _norm_and_gradient_of(M, D, X, dY):
+    """Y, 8-bit rows and gradients without eps, within the bounds of rows whose squares fit."""
+    s = dict(norm_inputs(M, D, False), X=X, dY=dY)
+    d, n = cuda(s), cs.Norm(cs.make_norm_desc(M=M, D=D, eps=0.0))
+    Y, Q, Qs, dX, dw = Out((M, D), BF), Out((M, D), F8), Out((M,), F32), Out((M, D), BF), Out((D,), BF)
+    n.run(d["X"], None, d["w"], Y=Y.t, Q=Q.t, Qs=Qs.t)
+    S, y = ref.norm(f64(s["X"]), None, f64(s["w"]), 0.0)
+    err = ref.norm_bound(S, y)
+    assert_within(Y.t, y, 2.0 ** -8 * np.abs(y) + 1.01 * err, "Y")
+    assert_rows8(Q.t, Qs.t, y, err, "Q")
+    work = Out((n.info.grad_work_bytes,), torch.uint8)
+    n.run_grad(d["X"], d["w"], d["dY"], None, work.t, dX.t, dw.t)
+    want = ref.norm_grad(f64(s["X"]), f64(s["w"]), f64(s["dY"]), None, 0.0)
+    value, bound = want["dX"]
+    assert_within(dX.t, value, bound + 2.0 ** -133, "dX")  # the type's smallest step, of which half is a rounding
+    assert_within(dw.t, *want["dw"], "dw")
+    assert all(o.intact() for o in (Y, Q, Qs, dX, dw, work))
+
+
+ENDS = [(5, 264), (1100, 264), (5, 1024), (1100, 1024), (3, 4104), (3, 8200), (3, 32768)]
+
+
+@pytest.mark.parametrize("M,D", ENDS)
+def test_norm_of_rows_of_the_largest_values(M, D):
+    g = torch.Generator().manual_seed(4 + M + D)
+    sign = torch.randint(0, 2, (M, D), generator=g).double() * 2 - 1
+    X = (sign * torch.finfo(BF).max * (1 - 2.0 ** -3 * torch.randint(0, 5, (M, D), generator=g))).to(BF)
+    _norm_and_gradient_of(M, D, X, norm_inputs(M, D, False)["dY"])
+
+
 def test_norm_grad_in_place_and_without_dw():
     M, D = 700, 1032
     d = cuda(norm_inputs(M, D))

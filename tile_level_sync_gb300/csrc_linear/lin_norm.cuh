@@ -48,9 +48,10 @@ struct BlockRow {
 };
 
 // Squares of a row's values leave fp32's range before the values do.  Where the mean of the squares
-// plus eps, v, is outside of what follows, the row is taken times this power of two instead.
+// plus eps, v, is outside of what follows, the row is taken times this power of two instead: 2^15 squares of values
+// below 2^128 then add up to less than 2^111, and a square of 2^-133 alone among as many columns has a mean of 2^-121.
 __device__ __forceinline__ bool squares_fit(float v) { return v >= 0x1p-100f && v <= 0x1p120f; }
-__device__ __forceinline__ float square_scale(float v) { return v > 1.0f ? 0x1p-70f : 0x1p70f; }
+__device__ __forceinline__ float square_scale(float v) { return v > 1.0f ? 0x1p-80f : 0x1p80f; }
 
 struct NormArgs {
   const uint4 *X, *R, *w;
