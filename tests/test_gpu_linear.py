@@ -168,6 +168,17 @@ def test_norm_of_rows_of_the_largest_values(M, D):
     _norm_and_gradient_of(M, D, X, norm_inputs(M, D, False)["dY"])
 
 
+@pytest.mark.parametrize("M,D", ENDS)
+def test_norm_of_rows_of_the_smallest_values(M, D):
+    """Whole multiples of 2^-133, whose rows' factors are beyond 32 bits, and one row with a single such value."""
+    g = torch.Generator().manual_seed(4 + M + D)
+    X = torch.randint(-7, 8, (M, D), generator=g).double()
+    X[:, 0] = 1
+    X[1, 1:] = 0
+    dY = norm_inputs(M, D, False)["dY"].float() * 2.0 ** -24  # the gradients are divided by the rows' size
+    _norm_and_gradient_of(M, D, (X * 2.0 ** -133).to(BF), dY.to(BF))
+
+
 def test_norm_grad_in_place_and_without_dw():
     M, D = 700, 1032
     d = cuda(norm_inputs(M, D))
