@@ -179,6 +179,39 @@ def test_norm_of_rows_of_the_smallest_values(M, D):
     _norm_and_gradient_of(M, D, (X * 2.0 ** -133).to(BF), dY.to(BF))
 
 
+@pytest.mark.parametrize("M,D", [(5, 264), (1100, 264), (3, 2056), (3, 8200), (2, 20480)])
+@pytest.mark.parametrize("size,weight", [(2.0 ** 59, 2.0 ** 70), (2.0 ** -45, 2.0 ** -110), (2.0 ** 100, 2.0 ** 100),
+                                         (2.0 ** -100, 2.0 ** -100), (2.0 ** 40, 2.0 ** -60)])
+def test_norm_row_scales_of_far_out_weights(M, D, size, weight):
+    """A row's scale is of its y, whose factors' product S w may lie outside of 32 bits where y does not."""
+    s = norm_inputs(M, D, False)
+    s["X"] = (torch.randn(M, D, generator=torch.Generator().manual_seed(11)) * size).to(BF)
+    s["w"] = (s["w"].float() * weight).to(BF)
+    d = cuda(s)
+    Y, Q, Qs = Out((M, D), BF), Out((M, D), F8), Out((M,), F32)
+    cs.Norm(cs.make_norm_desc(M=M, D=D, eps=0.0)).run(d["X"], None, d["w"], Y=Y.t, Q=Q.t, Qs=Qs.t)
+    S, y = ref.norm(f64(s["X"]), None, f64(s["w"]), 0.0)
+    err = ref.norm_bound(S, y)
+    assert_within(Y.t, y, 2.0 ** -8 * np.abs(y) + 1.01 * err, "Y")
+    assert_rows8(Q.t, Qs.t, y, err, "Q")
+
+
+@pytest.mark.parametrize("M,D", [(3, 264), (1100, 264), (3, 8200)])
+@pytest.mark.parametrize("size,odd", [(1.0, 100.0), (2.0 ** -7, 0.5)])  # S w beyond 32 bits, and S w / rms alone
+def test_norm_values_beyond_32_bits_do_not_count_for_a_scale(M, D, size, odd):
+    s = norm_inputs(M, D, False)
+    s["X"] = (torch.randn(M, D, generator=torch.Generator().manual_seed(12)) * size).to(BF)
+    s["X"][:, 7], s["w"][7] = odd, torch.finfo(BF).max
+    d = cuda(s)
+    Y, Q, Qs = Out((M, D), BF), Out((M, D), F8), Out((M,), F32)
+    _norm(M, D).run(d["X"], None, d["w"], Y=Y.t, Q=Q.t, Qs=Qs.t)
+    S, y = ref.norm(f64(s["X"]), None, f64(s["w"]), EPS)
+    assert (y[:, 7] > 2.0 * 2.0 ** 128).all()
+    assert torch.isinf(Y.t[:, 7].float()).all() and torch.isnan(Q.t[:, 7].float()).all()
+    keep = np.arange(D) != 7
+    assert_rows8(Q.t.float()[:, torch.from_numpy(keep).cuda()], Qs.t, y[:, keep], ref.norm_bound(S, y)[:, keep], "Q")
+
+
 def test_norm_grad_in_place_and_without_dw():
     M, D = 700, 1032
     d = cuda(norm_inputs(M, D))

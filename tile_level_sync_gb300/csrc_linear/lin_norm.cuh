@@ -68,8 +68,9 @@ struct NormArgs {
   float eps, inv_d;
 };
 
-// y of a row whose squares do not fit, in t's place (S on entry); returns the largest finite |y|.  A call of its own, with t
-// in memory, so that the kernels keep their registers: in line it cost 8192 x 8192 73.5 us where this takes 68.7.
+// y of a row whose squares, or whose products S w, do not fit, in t's place (S on entry); returns the largest finite |y|.  A
+// call of its own, with t in memory, so that the kernels keep their registers: in line it cost 8192 x 8192 71 us and more
+// where this takes 68.7.
 template <int V, typename Row>
 __device__ __noinline__ float norm_odd_row(float* t, const uint4* weights, int vecs, int i0, int step, float square, float eps,
                                            float inv_d, const Row& threads) {
@@ -98,7 +99,8 @@ __device__ __noinline__ float norm_odd_row(float* t, const uint4* weights, int v
 }
 
 // One row by the threads i0, i0 + step, ...: V pieces each.  The sum of squares and the largest |S w| come
-// out of one pass, as the row's factor r = 1 / sqrt(mean + eps) is common to all: max |y| = r max |S w|.
+// out of one pass, as the row's factor r = 1 / sqrt(mean + eps) is common to all: max |y| = r max |S w|, where that
+// product is neither too large for 32 bits nor so small that it has fewer (a maximum of 0 may be such a one).
 template <int V, typename Row>
 __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int i0, int step, const Row& threads) {
   const int64_t base = row * a.vecs;
@@ -132,7 +134,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int i0,
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         sum = fmaf(t[v][j], t[v][j], sum);
-        most = fmaxf(most, finite_abs(t[v][j] * w[j]));
+        most = fmaxf(most, fabsf(t[v][j] * w[j]));  // passes a NaN by, keeps infinities
       }
     } else {
 #pragma unroll
@@ -144,7 +146,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int i0,
   if (a.rms) {
     const float square = all.x * a.inv_d + a.eps;
     f = 1.0f / sqrtf(square);
-    if (!squares_fit(square)) {
+    if (!squares_fit(square) || (a.Q && !(all.y >= 0x1p-100f && all.y <= kFloatMax && all.y * f <= kFloatMax))) {
       float y[V * 8];
 #pragma unroll
       for (int i = 0; i < 8 * V; ++i) y[i] = t[i / 8][i % 8];
