@@ -20,7 +20,7 @@
  *    columns (the last block may be shorter): z ~ Zq * 2^(Ze - 127), the smallest such power by
  *    which the block's finite values fit into +-448, at least 2^-126.
  *  - Values that are infinite or NaN become NaN in 8 bits (e4m3 has no infinity) and do not count
- *    for a scale.
+ *    for a scale.  The gradient at a pre-activation whose checkpoint is NaN is NaN, ReLU's too.
  *  - Calls enqueue kernels on the caller's stream, on the current device, and return; they
  *    allocate nothing, keep nothing between calls and can be recorded by stream capture (a
  *    device's first call sets the attributes that kernels need: make it before a capture).

@@ -100,7 +100,7 @@ def slope(z, dY, kind):
     if kind == "none":
         return dY, np.zeros_like(dY)
     if kind == "relu":
-        return dY * (z > 0), np.zeros_like(dY)
+        return np.where(np.isnan(z), np.nan, dY * (z > 0)), np.zeros_like(dY)
     if kind == "gelu":
         t = np.tanh(_C * (z + 0.044715 * z ** 3))
         inner = _C * (1 + 3 * 0.044715 * z ** 2)

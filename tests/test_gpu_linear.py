@@ -466,6 +466,24 @@ def test_slopes_far_out(act):
         assert_within(got["dX"], d @ f64(s["Wt"]), 2.0 ** -7 * (np.abs(d) @ np.abs(f64(s["Wt"]))), "dX")
 
 
+@pytest.mark.parametrize("act", ["relu", "gelu", "swiglu"])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_gradient_of_preactivations_that_are_not_finite(act, dtype):
+    """NaN, what a checkpoint holds of infinities and NaN, reaches the gradients that it is part of, and no other byte."""
+    M, K, N = 70, 64, 72
+    s = linear_inputs(M, K, N, act, dtype, grad=True)
+    m = layer(M, K, N, act, dtype)
+    clean = run_linear_grad(m, s)
+    s["Zq"].view(torch.uint8)[33, 5] = 0x7F
+    odd = run_linear_grad(m, s)
+    assert torch.isnan(odd["dX"][33].float()).all() and torch.isnan(odd["dWt"][5].float()).all() and torch.isnan(odd["dbias"][5])
+    rows, cols = torch.arange(M) != 33, torch.ones(m.info.parts * N, dtype=torch.bool)
+    cols[5::N] = False  # SwiGLU: the up column beside the gate's
+    assert torch.equal(odd["dX"][rows.cuda()], clean["dX"][rows.cuda()])
+    for k in ("dWt", "dbias"):
+        assert torch.equal(odd[k][cols.cuda()], clean[k][cols.cuda()]), k
+
+
 def test_linear_gradient_against_differences():
     """dX along a direction, against differences of the forward pass on the device."""
     M, K, N, h = 32, 128, 192, 2.0 ** -4

@@ -84,6 +84,17 @@ def test_oracle_linear_grad_is_the_difference_quotient(act):
         assert np.allclose(again, want, atol=0.2, rtol=0.02), name
 
 
+def test_oracle_slopes_of_nan_are_nan():
+    z, dY = np.array([[np.nan, 2.0, -2.0, 1.0, 1.0, 1.0]]), np.full((1, 6), 3.0)
+    for act in ("relu", "gelu"):
+        dz = ref.slope(z, dY, act)[0]
+        assert np.isnan(dz[0, 0]) and np.isfinite(dz[0, 1:]).all()
+    assert ref.slope(z, dY, "relu")[0][0, 1:].tolist() == [3.0, 0.0, 3.0, 3.0, 3.0]
+    with np.errstate(invalid="ignore"):
+        gated = ref.slope(z, dY[:, :3], "swiglu")[0]
+    assert np.isnan(gated).tolist() == [[True, False, False, True, False, False]]
+
+
 # ------------------------------------------------------------------ header and binding
 
 def _header():

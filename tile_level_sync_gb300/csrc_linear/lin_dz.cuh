@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(256, 3) dz_kernel(const DzArgs a) {
         if (ACT == ACT_NONE) {
           dz[0][j] = dy[j];
         } else if (ACT == ACT_RELU) {
-          dz[0][j] = z[0][j] > 0.0f ? dy[j] : 0.0f;
+          // NaN, which a checkpoint holds of infinities too, stays NaN, as it does in the other slopes
+          dz[0][j] = z[0][j] <= 0.0f ? 0.0f : fmaf(z[0][j], 0.0f, dy[j]);
         } else if (ACT == ACT_GELU) {
           const float x = z[0][j], sg = gelu_gate(x), h = x * sg;
           // far out, where the sigmoid is 0 or 1, the square must not become an infinity
