@@ -230,8 +230,9 @@ __device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, int64_t fi
   const uint32_t bytes = (uint32_t)a.vecs * 16;
   constexpr bool kDirect = V == 4 && Row::kBlock;  // dS
   const int tensors = a.dS && !kDirect ? 3 : 2;
+  bool ok = true;
   auto fetch = [&](int64_t row, int st) {  // one thread
-    if (row >= a.M) return;
+    if (row >= a.M || !ok) return;
     uint4* to = ring + (int64_t)st * tensors * a.vecs;
     ptx::mbar_arrive_expect_tx(&full[st], tensors * bytes);
     ptx::bulk_load(to, a.S + row * a.vecs, bytes, &full[st]);
@@ -250,7 +251,6 @@ __device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, int64_t fi
   }
   int turn = 0, st = 0;
   uint32_t par = 0;
-  bool ok = true;
   for (int64_t row = first; row < a.M; row += stride, turn ^= 1) {
     uint4 s[kDirect ? V : 1];
     if (kDirect) {
@@ -260,10 +260,17 @@ __device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, int64_t fi
         s[kDirect ? v : 0] = a.dS && i < a.vecs ? a.dS[row * a.vecs + i] : make_uint4(0, 0, 0, 0);
       }
     }
-    // after a wait that gave up: on with what is there
+    // after a wait that gave up: on with what is there.  The thread that copies asks for no more rows and waits, with a limit
+    // again, for those that it has asked for: no block ends with copies into its memory under way.
     if (ok && !ptx::mbar_wait_bounded(&full[st], par, kNormWaitNs)) {
       ok = false;
       *a.err = (int32_t)kNormErrWait;
+      const int asked = stages > 3 && row != first ? stages - 1 : stages;  // the row before's place is free
+      if (i0 == 0)
+        for (int i = 0, at = st; i < asked && row + i * stride < a.M; ++i) {
+          ptx::mbar_wait_bounded(&full[at], at < st ? par ^ 1 : par, kNormWaitNs);
+          if (++at == stages) at = 0;
+        }
     }
     const uint4 *x = ring + (int64_t)st * tensors * a.vecs, *y = x + a.vecs;
     float squares = 0.0f, dots = 0.0f;
