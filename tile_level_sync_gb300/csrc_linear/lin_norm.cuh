@@ -294,7 +294,9 @@ __device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, int64_t fi
     };
     sums(1.0f);
     float2 all = threads.template reduce<false>(squares, dots, turn);
-    // behind these sums every thread is done with the row before: its place takes the row `stages` further
+    // behind these sums every thread is done with the row before: its place takes the row `stages` further.  A block's
+    // sums meet at a barrier; a warp's shuffles order no memory.
+    if (!Row::kBlock) threads.sync();
     if (i0 == 0 && stages > 3 && row != first) fetch(row + (stages - 1) * stride, st ? st - 1 : stages - 1);
     float square = all.x * a.inv_d + a.eps, c = 1.0f;
     if (!squares_fit(square)) {
