@@ -22,8 +22,10 @@
  *  - Values that are infinite or NaN become NaN in 8 bits (e4m3 has no infinity) and do not count
  *    for a scale.  The gradient at a pre-activation whose checkpoint is NaN is NaN, ReLU's too.
  *  - Calls enqueue kernels on the caller's stream, on the current device, and return; they
- *    allocate nothing, keep nothing between calls and can be recorded by stream capture (a
- *    device's first call sets the attributes that kernels need: make it before a capture).
+ *    allocate nothing, keep nothing between calls and can be recorded by stream capture.  A
+ *    device's first cusync_norm_grad with rows, and its first cusync_linear or cusync_linear_grad
+ *    with rows, sets the attributes of the kernels of the norms and of the linear layers; that, and CUDA's
+ *    loading of a kernel at its first launch, may also happen in a capture, at the host's time.
  *    A `work` buffer belongs to one call at a time: two calls (or two captured graphs) that may
  *    run at the same time need buffers of their own.
  *  - Results do not depend on timing: the same inputs give the same bytes.  Calls of different

@@ -1,5 +1,9 @@
 """GPU parity of the norm and linear layers with the fp64 oracle (oracle/linear.py)."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -12,6 +16,7 @@ from oracle.bf16 import round_to_bf16
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-5
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 # ------------------------------------------------------------------ norm
@@ -661,6 +666,60 @@ def test_one_graph_after_another_with_one_buffer(M):
     for o, w in zip(out, want):
         assert all(torch.equal(o[k], w[k]) for k in w)
     assert m.check(work)[0] == cs.OK
+
+
+FRESH = r"""
+import sys, torch
+import tile_level_sync_gb300 as cs
+first = sys.argv[1]
+bf, f8 = torch.bfloat16, torch.float8_e4m3fn
+new = lambda dtype, *shape: torch.ones(shape, dtype=torch.float32, device="cuda").to(dtype)
+M = 3
+n = cs.Norm(cs.make_norm_desc(M=M, D=64))
+if first == "norm": n.run(new(bf, M, 64), None, new(bf, 64), Y=new(bf, M, 64))
+if first == "linear":
+    m = cs.Linear(cs.make_linear_desc(M=M, K=64, N=64))
+    m.run(new(bf, M, 64), new(bf, 64, 64), new(torch.uint8, m.info.work_bytes), new(bf, M, 64))
+for M, D in ((5, 264), (1100, 264), (5, 12288), (5, 20480)):
+    n = cs.Norm(cs.make_norm_desc(M=M, D=D))
+    x, w, y, dx, dw, work = new(bf, M, D), new(bf, D), new(bf, M, D), new(bf, M, D), new(bf, D), new(torch.uint8, n.info.grad_work_bytes)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        n.run(x, None, w, Y=y)
+        n.run_grad(x, w, y, None, work, dx, dw)
+    g.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (y, dx, dw)]
+    n.run(x, None, w, Y=y)
+    n.run_grad(x, w, y, None, work, dx, dw)
+    assert all(torch.equal(a, b) for a, b in zip(got, (y, dx, dw)))
+for M, K, N, act in ((20, 256, 264, "gelu"), (1300, 528, 2056, "swiglu"), (2048, 1024, 2048, "relu")):
+    m = cs.Linear(cs.make_linear_desc(M=M, K=K, N=N, act=act))
+    G = m.info.parts
+    x, W, dy, y = new(bf, M, K), new(bf, G * N, K), new(bf, M, N), new(bf, M, N)
+    Zq, Ze = new(f8, M, G * N), new(torch.uint8, M, G, m.info.blocks)
+    dx, dW, db, work = new(bf, M, K), new(bf, G * N, K), new(bf, G * N), new(torch.uint8, m.info.grad_work_bytes)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.run(x, W, work, y, Zq=Zq, Ze=Ze)
+        m.run_grad(x, W, dy, work, dx, dW, db, Zq=Zq, Ze=Ze)
+    g.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in (y, dx, dW, db)]
+    m.run(x, W, work, y, Zq=Zq, Ze=Ze)
+    m.run_grad(x, W, dy, work, dx, dW, db, Zq=Zq, Ze=Ze)
+    assert all(torch.equal(a, b) for a, b in zip(got, (y, dx, dW, db)))
+print("same bytes")
+"""
+
+
+@pytest.mark.parametrize("first", ["none", "norm", "linear"])
+def test_captures_in_a_fresh_process(first):
+    """Captures of calls whose kernels no call has launched before them, and whose attributes another call has set, or none."""
+    r = subprocess.run([sys.executable, "-c", FRESH, first], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0 and "same bytes" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
 
 
 def test_calls_beside_other_kernels_of_the_library():

@@ -75,7 +75,7 @@ std::atomic<int> g_sms[kMaxDevices];  // SMs of a prepared device, 0 = not prepa
 cudaError_t prepare_kernel(const void* f, int smem) {
   cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;  // loads the kernel now, not at a launch inside a capture
+  cudaFuncAttributes fa;  // loads the kernel now, not at its first launch
   return cudaFuncGetAttributes(&fa, f);
 }
 template <int MODE, bool E4M3, bool GATED, int BN>
