@@ -503,7 +503,8 @@ cusync_status_t cusync_band_rows(const cusync_chain_desc_t* d, int32_t band, int
 cusync_status_t cusync_chain_trace(cusync_chain_t chain, cusync_stream_t stream, cusync_trace_rec_t* out,
                                    int32_t max, int32_t* n_out);
 
-/* Release the chain's device state.  NULL is accepted. */
+/* Release the chain's device state.  NULL is accepted.  Allowed while a stream is being captured; runs of the
+ * chain that a graph has recorded, or that the capture has, need the chain alive for as long as they are replayed. */
 cusync_status_t cusync_destroy_chain(cusync_chain_t chain);
 
 #ifdef __cplusplus

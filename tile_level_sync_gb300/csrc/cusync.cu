@@ -1559,10 +1559,15 @@ cusync_status_t cusync_chain_trace(cusync_chain_t ch, cusync_stream_t stream, cu
 cusync_status_t cusync_destroy_chain(cusync_chain_t ch) {
   if (!ch) return CUSYNC_OK;
   cudaError_t e = cudaSuccess;
+  // A garbage collector may get here while some stream is being captured.  The frees would end that capture, unless this
+  // thread's capture mode lets them pass.
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
   if (ch->trace) cudaFree(ch->trace);
   if (ch->split_ws) cudaFree(ch->split_ws);
   if (ch->band_ev) cudaEventDestroy(ch->band_ev);
   if (ch->state) e = cudaFree(ch->state);
+  if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
   delete ch;
   return e == cudaSuccess ? CUSYNC_OK : CUSYNC_ERR_CUDA;
 }
