@@ -27,15 +27,16 @@ def pytest_collection_modifyitems(config, items):
             item.add_marker(skip)
 
 
+def pytest_collection_finish(session):
+    gc.collect()
+    gc.freeze()  # what is there stays: collections between tests look at what tests make
+
+
 @pytest.fixture(autouse=True)
 def collect_between_gpu_tests(request):
-    """The garbage collector runs between GPU tests, not in them: a graph of an earlier test that it destroys during a
-    capture ends the capture.  (An exception that a test keeps holds the test's frame, which holds the exception and
-    the test's graphs: such rings wait for the collector.)"""
-    if "gpu" not in request.keywords:
-        yield
-        return
-    gc.disable()
+    """GPU tests start without what earlier ones left for the garbage collector: a graph that it destroys during a capture
+    ends the capture.  (An exception that a test keeps holds the test's frame, which holds the exception and the test's
+    graphs: such rings wait for the collector.)  In them it runs as it does in a user's program."""
+    if "gpu" in request.keywords:
+        gc.collect()
     yield
-    gc.enable()
-    gc.collect(0)

@@ -1,13 +1,43 @@
-"""Python's garbage collector beside captures: a chain that it destroys in a capture does not end that capture."""
+"""Python's garbage collector beside captures: GPU tests run with it on and start without what earlier ones left, and a chain
+that it destroys in a capture does not end that capture."""
 
+import gc
 import os
 import subprocess
 import sys
+import weakref
 
 import pytest
+import torch
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LEFT = []
+
+
+class _Ring:
+    def __init__(self):
+        self.self = self
+        self.graph = torch.cuda.CUDAGraph()
+
+
+def test_collector_is_on():
+    assert gc.isenabled()
+
+
+@pytest.mark.parametrize("generation", [0, 1, 2])
+def test_ring_left_behind(generation):
+    """A graph that only the collector can free, in each of its generations; looked for by the test after this one."""
+    LEFT.append(weakref.ref(_Ring()))
+    for g in range(generation):
+        keep = LEFT[-1]()
+        gc.collect(g)
+        del keep
+
+
+def test_ring_is_gone():
+    assert len(LEFT) == 3 and all(r() is None for r in LEFT)
+
 
 CAPTURE = r"""
 import gc, os, sys, torch
