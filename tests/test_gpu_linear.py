@@ -10,7 +10,7 @@ import torch
 
 import tile_level_sync_gb300 as cs
 from linear_helpers import (BF, F8, F32, Out, assert_checkpoint, assert_rows8, assert_within, cuda, f64, finish, layer,
-                            linear_inputs, norm_inputs, oracle_grad, oracle_linear, run_linear, run_linear_grad)
+                            linear_inputs, norm_inputs, oracle_grad, oracle_linear, run_linear, run_linear_grad, values)
 from oracle import linear as ref
 from oracle.bf16 import round_to_bf16
 
@@ -262,6 +262,49 @@ def test_norm_gradient_against_differences():
     assert abs(along - seen) <= slack and slack < 20 * abs(h) * M * D
 
 
+ROUNDINGS = 6.0  # sums of independent errors e_i exceed 6 sqrt(sum e_i^2) with a probability of 3e-8 at most (Hoeffding)
+
+
+def test_norm_gradient_along_itself_and_along_the_rows():
+    """The gradient's products with two directions against the forward pass's differences: its own signs, along which every
+    part of it counts, and the rows S, along which y does not change and the term of the mean does all.  Wrong gradients
+    have to be found out by the same bounds."""
+    M, D, h, eps = 4, 256, 2.0 ** -5, 1e-5
+    g = torch.Generator().manual_seed(1)
+    s = norm_inputs(M, D, False, seed=3)
+    s["X"] = torch.randn(M, D, generator=g).to(BF)
+    s["w"] = torch.exp(torch.randn(D, generator=g)).to(BF)
+    # the sign of S w in dY makes the mean of g S large
+    s["dY"] = (torch.sign(s["X"].float() * s["w"].float()) * torch.randn(M, D, generator=g).abs()).to(BF)
+    n = _norm(M, D)
+    dX, dw = torch.empty(M, D, dtype=BF, device="cuda"), torch.empty(D, dtype=BF, device="cuda")
+    work = torch.empty(n.info.grad_work_bytes, dtype=torch.uint8, device="cuda")
+    d = cuda(s)
+    n.run_grad(d["X"], d["w"], d["dY"], None, work, dX, dw)
+    S, w, dY = f64(s["X"]), f64(s["w"]), f64(s["dY"])
+    exact = ref.norm_grad(S, w, dY, None, eps)["dX"][0]
+    r = 1 / np.sqrt((S * S).mean(axis=1, keepdims=True) + eps)
+    wrong = {"zero": 0 * exact, "negated": -exact, "twice": 2 * exact, "without w": r * (dY - S * r * (dY * S * r).mean(axis=1, keepdims=True)),
+             "without the mean": r * w * dY}
+    found = set()
+    for step in (np.sign(exact), S):
+        ends = []
+        for sign in (1, -1):
+            x = torch.from_numpy(S + sign * h * step).to(BF)
+            y = torch.empty(M, D, dtype=BF, device="cuda")
+            n.run(x.cuda(), None, d["w"], Y=y)
+            ends.append((f64(x), f64(y)))
+        (xa, ya), (xb, yb) = ends
+        seen = ((ya - yb) * dY).sum()
+        # y's roundings, 2^-8 of the value each; the difference's own distance from the first derivative
+        noise = ROUNDINGS * 2.0 ** -8 * np.sqrt((ya ** 2 * dY ** 2).sum() + (yb ** 2 * dY ** 2).sum())
+        curve = abs(((ref.norm(xa, None, w, eps)[1] - ref.norm(xb, None, w, eps)[1]) * dY).sum() - (exact * (xa - xb)).sum())
+        own = ROUNDINGS * 2.0 ** -8 * np.sqrt((exact ** 2 * (xa - xb) ** 2).sum())  # dX's roundings
+        assert abs((f64(dX) * (xa - xb)).sum() - seen) <= noise + curve + own
+        found |= {k for k, v in wrong.items() if abs((v * (xa - xb)).sum() - seen) > noise + curve + own}
+    assert found == set(wrong)
+
+
 # ------------------------------------------------------------------ linear: forward
 
 # few tiles (clusters that divide the reduction), then many (pairs); ragged in every dimension
@@ -508,6 +551,50 @@ def test_linear_gradient_against_differences():
         along, seen = dX * (xa - xb), (ya - yb) * f64(s["dY"])
         # the checkpoint's 2^-4 of a slope, at random over M N terms; a missing factor or part is far above
         assert abs(along.sum() - seen.sum()) <= 0.1 * np.sqrt((seen ** 2).sum() * 9 + (along ** 2).sum() * 9), act
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "swiglu"])
+def test_linear_gradient_along_its_parts(act):
+    """dX's products with the signs of its parts (of the gate and the up projection, or the whole and what the slope takes
+    away), against differences of the forward pass on the device, bounded by the roundings and by what 64 bits give for the
+    checkpoint's and the difference's share.
+    A gradient that lacks a part, a factor or the slope has to be found out by the same bounds."""
+    M, K, N, h = 32, 128, 192, 2.0 ** -6
+    s = linear_inputs(M, K, N, act, residual=False, seed=5)
+    m = layer(M, K, N, act)
+    fwd = run_linear(m, s, checkpoint=True)
+    s["Zq"], s["Ze"] = fwd["Zq"].cpu(), fwd["Ze"].cpu()
+    dX = f64(run_linear_grad(m, s)["dX"])
+    X, Wt, dY, bias = f64(s["X"]), f64(s["Wt"]), f64(s["dY"]), f64(s["bias"])
+    z = X @ Wt.T + bias
+    dz, kept = ref.slope(z, dY, act)[0], ref.slope(values(s, m.info.parts), dY, act)[0]
+    exact = dz @ Wt
+    cut = [slice(0, N), slice(N, 2 * N)][:m.info.parts]
+    parts = [dz[:, c] @ Wt[c] for c in cut]
+    wrong = {"zero": 0 * exact, "negated": -exact, "twice": 2 * exact}
+    if act == "swiglu":
+        wrong.update({"without gate": parts[1], "without up": parts[0], "parts exchanged": dz[:, cut[0]] @ Wt[cut[1]] + dz[:, cut[1]] @ Wt[cut[0]]})
+    else:
+        wrong["slope of one"] = dY @ Wt
+        parts.append(exact - dY @ Wt)
+    found = set()
+    for part in parts:
+        step = np.sign(part)
+        ends = []
+        for sign in (1, -1):
+            t = dict(s, X=torch.from_numpy(X + sign * h * step).to(BF))
+            ends.append((f64(t["X"]), f64(run_linear(m, t)["Y"])))
+        (xa, ya), (xb, yb) = ends
+        seen = ((ya - yb) * dY).sum()
+        noise = ROUNDINGS * 2.0 ** -8 * np.sqrt((ya ** 2 * dY ** 2).sum() + (yb ** 2 * dY ** 2).sum())
+        curve = abs(((ref.act(xa @ Wt.T + bias, act) - ref.act(xb @ Wt.T + bias, act)) * dY).sum() - (exact * (xa - xb)).sum())
+        # the checkpoint's share; dZ's roundings and dX's
+        kept_share = abs(((kept - dz) @ Wt * (xa - xb)).sum())
+        own = ROUNDINGS * 2.0 ** -8 * np.sqrt(((kept * ((xa - xb) @ Wt.T)) ** 2).sum() + ((kept @ Wt * (xa - xb)) ** 2).sum())
+        slack = noise + curve + kept_share + own
+        assert abs((dX * (xa - xb)).sum() - seen) <= slack
+        found |= {k for k, v in wrong.items() if abs((v * (xa - xb)).sum() - seen) > slack}
+    assert found == set(wrong)
 
 
 # ------------------------------------------------------------------ together
