@@ -29,7 +29,12 @@
  *    A `work` buffer belongs to one call at a time: two calls (or two captured graphs) that may
  *    run at the same time need buffers of their own.
  *  - Results do not depend on timing: the same inputs give the same bytes.  Calls of different
- *    sizes may take different kernels, whose results differ by roundings.
+ *    sizes, with another num_sms or for other outputs (dX without dWt, dbias alone) may take different
+ *    kernels, whose results differ by roundings.
+ *  - cusync_norm holds for all finite S and w, and any finite eps that is not negative.  Elsewhere these
+ *    intermediate results are in 32 bits, whatever the result's own range: w * dY and w * dY * S in
+ *    cusync_norm_grad, dY * up in the gradient of SwiGLU, e4m3 sums times a Ws beyond 2^+-80.  Sigmoids
+ *    below 2^-126 (gates below -87.3) count as 0.
  *  - Outputs may not overlap inputs or one another, except where a function says so.
  *  - Sizes the kernels do not cover return CUSYNC_ERR_UNSUPPORTED; there is no fallback.
  */
@@ -56,7 +61,7 @@ typedef struct {
   int64_t D;       /* columns: a multiple of 8, at most CUSYNC_NORM_MAX_D */
   int32_t kind;    /* cusync_norm_kind_t */
   float eps;       /* finite, not negative */
-  int32_t num_sms; /* SMs that the gradient's grid is made for; 0 = all */
+  int32_t num_sms; /* SMs that the gradient's grid is made for; 0 = all.  cusync_norm takes all that are free */
   int32_t _pad0;
 } cusync_norm_desc_t;
 
@@ -105,7 +110,9 @@ typedef struct {
   int64_t N;       /* columns of Y: a multiple of 8 */
   int32_t act;     /* cusync_linear_act_t */
   int32_t dtype;   /* cusync_linear_dtype_t */
-  int32_t num_sms; /* SMs that grids of persistent kernels are made for; 0 = all */
+  int32_t num_sms; /* SMs that grids of persistent kernels are made for; 0 = all.  It does not keep others free:
+                      products of few tiles and the gradients at the pre-activations take a block for
+                      each piece of work, on all SMs */
   int32_t _pad0;
 } cusync_linear_desc_t;
 

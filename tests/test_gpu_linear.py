@@ -376,6 +376,21 @@ def test_linear_on_few_sms(num_sms, M, K, N):
     assert_within(run_linear(layer(M, K, N, "swiglu", num_sms=num_sms), s)["Y"], Y, bound, "Y")
 
 
+@pytest.mark.parametrize("num_sms", [1, 2, 3])
+@pytest.mark.parametrize("M,K,N", [(100, 1024, 776), (333, 1008, 776)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_linear_and_gradient_on_few_sms(num_sms, M, K, N, dtype):
+    """Reductions long enough for clusters of eight, of which one SM holds none."""
+    s = linear_inputs(M, K, N, "gelu", dtype)
+    Y, bound, _, _ = oracle_linear(s, "gelu")
+    m = layer(M, K, N, "gelu", dtype, num_sms=num_sms)
+    assert_within(run_linear(m, s)["Y"], Y, bound, "Y")
+    s = linear_inputs(M, K, N, "gelu", dtype, grad=True)
+    got = run_linear_grad(m, s)
+    for name, (value, bound) in oracle_grad(s, "gelu").items():
+        assert_within(got[name], value, bound, name)
+
+
 @pytest.mark.parametrize("M,K,N", [(70, 1000, 776), (1281, 520, 2056)])
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "swiglu"])
 def test_odd_values_stay_in_their_rows(M, K, N, act):

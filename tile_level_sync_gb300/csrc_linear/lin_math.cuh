@@ -73,7 +73,9 @@ __device__ __forceinline__ uint32_t block_exponent(float most) {
 __device__ __forceinline__ float exponent_inverse(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 __device__ __forceinline__ float exponent_value(uint32_t e) { return __uint_as_float(e << 23); }
 
-// 2^x and 1 / x to 2 ulp; beyond fp32's range 0 and infinity
+// 2^x and 1 / x to 2 ulp, one instruction each (the full functions cost the forward epilogue 41.6 us instead of 39.4,
+// 4096 x 1024 x 4096 with GeLU); 0 below 2^-126, so that a gate below -87.3 counts as 0 where its silu is -1e-36 or nearer
+// to 0, and infinity above fp32's range
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
