@@ -31,8 +31,8 @@
  *  - Results do not depend on timing: the same inputs give the same bytes.  Calls of different
  *    sizes, with another num_sms or for other outputs (dX without dWt, dbias alone) may take different
  *    kernels, whose results differ by roundings.
- *  - cusync_norm holds for all finite S and w, and any finite eps that is not negative.  Elsewhere these
- *    intermediate results are in 32 bits, whatever the result's own range: w * dY and w * dY * S in
+ *  - cusync_norm holds for all finite S and w, and any finite eps that is not negative (elements that
+ *    pass below 2^-126 on the way, beside much larger ones, lose bits).  Elsewhere these intermediate results are in 32 bits, whatever the result's own range: w * dY and w * dY * S in
  *    cusync_norm_grad, dY * up in the gradient of SwiGLU, e4m3 sums times a Ws beyond 2^+-80.  Sigmoids
  *    below 2^-126 (gates below -87.3) count as 0.
  *  - Outputs may not overlap inputs or one another, except where a function says so.

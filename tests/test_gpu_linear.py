@@ -143,19 +143,19 @@ def test_norm_of_rows_whose_squares_leave_32_bits(size):
     assert_within(dw.t, value, bound + 2.0 ** -18 * np.abs(f64(s["dY"])).sum(axis=0), "dw")
 
 
-def _norm_and_gradient_of(M, D, X, dY):
-    """Y, 8-bit rows and gradients without eps, within the bounds of rows whose squares fit."""
+def _norm_and_gradient_of(M, D, X, dY, eps=0.0):
+    """Y, 8-bit rows and gradients within the bounds of rows whose squares fit."""
     s = dict(norm_inputs(M, D, False), X=X, dY=dY)
-    d, n = cuda(s), cs.Norm(cs.make_norm_desc(M=M, D=D, eps=0.0))
+    d, n = cuda(s), cs.Norm(cs.make_norm_desc(M=M, D=D, eps=eps))
     Y, Q, Qs, dX, dw = Out((M, D), BF), Out((M, D), F8), Out((M,), F32), Out((M, D), BF), Out((D,), BF)
     n.run(d["X"], None, d["w"], Y=Y.t, Q=Q.t, Qs=Qs.t)
-    S, y = ref.norm(f64(s["X"]), None, f64(s["w"]), 0.0)
+    S, y = ref.norm(f64(s["X"]), None, f64(s["w"]), eps)
     err = ref.norm_bound(S, y)
     assert_within(Y.t, y, 2.0 ** -8 * np.abs(y) + 1.01 * err, "Y")
     assert_rows8(Q.t, Qs.t, y, err, "Q")
     work = Out((n.info.grad_work_bytes,), torch.uint8)
     n.run_grad(d["X"], d["w"], d["dY"], None, work.t, dX.t, dw.t)
-    want = ref.norm_grad(f64(s["X"]), f64(s["w"]), f64(s["dY"]), None, 0.0)
+    want = ref.norm_grad(f64(s["X"]), f64(s["w"]), f64(s["dY"]), None, eps)
     value, bound = want["dX"]
     assert_within(dX.t, value, bound + 2.0 ** -133, "dX")  # the type's smallest step, of which half is a rounding
     assert_within(dw.t, *want["dw"], "dw")
@@ -182,6 +182,16 @@ def test_norm_of_rows_of_the_smallest_values(M, D):
     X[1, 1:] = 0
     dY = norm_inputs(M, D, False)["dY"].float() * 2.0 ** -24  # the gradients are divided by the rows' size
     _norm_and_gradient_of(M, D, (X * 2.0 ** -133).to(BF), dY.to(BF))
+
+
+@pytest.mark.parametrize("M,D", [(5, 264), (1100, 264), (3, 8200), (2, 20480)])
+@pytest.mark.parametrize("eps", [2.0 ** 127, 2.0 ** 110, 2.0 ** -120, 2.0 ** -140])
+def test_norm_of_far_out_eps(M, D, eps):
+    """eps beside rows of ordinary values, and beside rows whose squares are about as large as it is."""
+    g = torch.Generator().manual_seed(6 + M + D)
+    X = torch.randn(M, D, generator=g).double()
+    X[1] *= 2.0 ** round(np.log2(eps) / 2)
+    _norm_and_gradient_of(M, D, X.to(BF), norm_inputs(M, D, False)["dY"], eps)
 
 
 @pytest.mark.parametrize("M,D", [(5, 264), (1100, 264), (3, 2056), (3, 8200), (2, 20480)])
