@@ -211,6 +211,24 @@ def test_norm_row_scales_of_far_out_weights(M, D, size, weight):
     assert_rows8(Q.t, Qs.t, y, err, "Q")
 
 
+@pytest.mark.parametrize("M,D", [(5, 264), (1100, 264), (3, 8200)])
+@pytest.mark.parametrize("size,weight,eps", [(2.0 ** -78, 2.0 ** -78, 2.0 ** -20), (2.0 ** -78, 2.0 ** -78, 2.0 ** -98),
+                                             (2.0 ** -70, 2.0 ** -70, 2.0 ** -98), (2.0 ** -60, 2.0 ** -60, 2.0 ** -98),
+                                             (2.0 ** -60, 2.0 ** -60, 2.0 ** -60)])
+def test_norm_row_scales_of_products_near_zero(M, D, size, weight, eps):
+    """max |S w| is 0 in 32 bits, or has few of them; max |y| / 448 is above and below the least scale."""
+    s = norm_inputs(M, D, False)
+    s["X"] = (torch.randn(M, D, generator=torch.Generator().manual_seed(13)) * size).to(BF)
+    s["w"] = (s["w"].float() * weight).to(BF)
+    s["X"][1] = 0
+    d = cuda(s)
+    Q, Qs = Out((M, D), F8), Out((M,), F32)
+    cs.Norm(cs.make_norm_desc(M=M, D=D, eps=eps)).run(d["X"], None, d["w"], Q=Q.t, Qs=Qs.t)
+    S, y = ref.norm(f64(s["X"]), None, f64(s["w"]), eps)
+    assert_rows8(Q.t, Qs.t, y, ref.norm_bound(S, y) + 2.0 ** -149, "Q")  # y's own step there
+    assert Qs.t[1] == 2.0 ** -126 and (Q.t[1].float() == 0).all()
+
+
 @pytest.mark.parametrize("M,D", [(3, 264), (1100, 264), (3, 8200)])
 @pytest.mark.parametrize("size,odd", [(1.0, 100.0), (2.0 ** -7, 0.5)])  # S w beyond 32 bits, and S w / rms alone
 def test_norm_values_beyond_32_bits_do_not_count_for_a_scale(M, D, size, odd):

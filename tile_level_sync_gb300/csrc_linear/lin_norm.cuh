@@ -55,6 +55,13 @@ __device__ __forceinline__ bool squares_fit(float v) { return v >= 0x1p-100f && 
 // them for rows below 2^-128.
 __device__ __forceinline__ float square_scale(float v) { return v > 1.0f ? 0x1p-40f : 0x1p40f; }
 
+// Whether a row's max |y| is r times `most`, its max |S w| in 32 bits: where neither is infinite and the product has all of
+// its bits, or where it is 0, below 2^-149, and y so small that the least scale is the row's (rows of zeros: 8192 x 8192 of
+// them took 143 us as odd rows, and 48 so).
+__device__ __forceinline__ bool product_fits(float most, float r) {
+  return most <= kFloatMax && most * r <= kFloatMax && (most >= kLeastScale || (most == 0.0f && r <= 0x1p32f));
+}
+
 constexpr uint32_t kOnes = 0x3f803f80u;  // two bf16 ones
 
 struct NormArgs {
@@ -99,8 +106,7 @@ __device__ __noinline__ float norm_odd_row(float* t, const uint4* weights, int v
 }
 
 // One row by the threads i0, i0 + step, ...: V pieces each.  The sum of squares and the largest |S w| come
-// out of one pass, as the row's factor r = 1 / sqrt(mean + eps) is common to all: max |y| = r max |S w|, where that
-// product is neither too large for 32 bits nor so small that it has fewer (a maximum of 0 may be such a one).
+// out of one pass, as the row's factor r = 1 / sqrt(mean + eps) is common to all: max |y| = r max |S w|.
 template <int V, typename Row>
 __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int i0, int step, const Row& threads) {
   const int64_t base = row * a.vecs;
@@ -146,7 +152,7 @@ __device__ __forceinline__ void norm_row(const NormArgs& a, int64_t row, int i0,
   if (a.rms) {
     const float square = all.x * a.inv_d + a.eps;
     f = 1.0f / sqrtf(square);
-    if (!squares_fit(square) || (a.Q && !(all.y >= 0x1p-100f && all.y <= kFloatMax && all.y * f <= kFloatMax))) {
+    if (!squares_fit(square) || (a.Q && !product_fits(all.y, f))) {
       float y[V * 8];
 #pragma unroll
       for (int i = 0; i < 8 * V; ++i) y[i] = t[i / 8][i % 8];
