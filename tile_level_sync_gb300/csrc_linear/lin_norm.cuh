@@ -227,8 +227,8 @@ constexpr uint32_t kNormErrWait = 3u << 24;
 // next rows are under way while this one waits for its sums: with rows loaded into registers alone 8192 x 8192 (dS
 // added) took 127 us, with the ring 82 (6.5 TB/s).  Where the ring holds three rows or fewer, a row's place is refilled as
 // soon as it is read, at the price of a barrier (2000 x 12288: 39.0 us, 43.2 with the row after it).  Four pieces a
-// thread, rows above 16384 columns, leave dS out of the ring, which would hold one row with it (2000 x 20480: 120 us,
-// 131 with it).
+// thread, rows above 16384 columns, leave dS out of the ring, which would hold one row with it (2000 x 20480: 131 us
+// with it and 120 without; 112 now).
 template <int V, typename Row>
 __device__ __forceinline__ void norm_grad_rows(const NormGradArgs& a, int64_t first, int64_t stride, int i0, int step,
                                                const Row& threads, uint4* ring, uint64_t* full, float (&dw)[V][8]) {
